@@ -556,6 +556,138 @@ MLAQ_API int64_t mla_q_uproj_w_scale_group(const mla_q_shape *shape);
  * when no CUDA device is usable. */
 MLAQ_API size_t mla_q_uproj_workspace_size(const mla_q_shape *shape, int which);
 
+/* ---- Rotary positions with several axes ---------------------------------
+ * (an addition of this library: the pages only know one position per token).
+ *
+ *   T, H          tokens and heads of the tensor
+ *   Dn, Dr        channels of a head: Dn passed through, then Dr rotated (even)
+ *   axes          position axes (1 .. 16), e.g. 3 for time, height and width
+ *   cs_rows/width rows and columns (row pitch) of the cos/sin tables, as in
+ *                 mla_q_shape; a position of any axis is a table row
+ *   in_t, in_h    strides of the input's tokens and heads, in elements (the
+ *                 channels of a head are contiguous; a stride of 0 reads one
+ *                 row for all tokens or heads)
+ *   out_t, out_h  strides of the output; its rows must not overlap
+ *   T * H, cs_rows and cs_width are at most INT32_MAX. */
+typedef struct {
+    int64_t T;
+    int32_t H;
+    int32_t Dn;
+    int32_t Dr;
+    int32_t axes;
+    int64_t cs_rows;
+    int64_t cs_width;
+    int64_t in_t, in_h, out_t, out_h;
+    int64_t reserved; /* set to 0 */
+} mla_rope_axes_shape;
+
+/* mode of mla_rope_axes */
+enum { MLA_ROPE_APPLY = 0, MLA_ROPE_INVERSE = 1, MLA_ROPE_INVERSE_SUM = 2 };
+
+/*
+ * Rotation pair i (rope channels i and i + Dr/2 of a head, i < Dr/2) of token
+ * t is turned by the table row p = pos[pair_axis[i]][t]; rope channel j reads
+ * column j, as in mla_q_uproj_fwd:
+ *   MLA_ROPE_APPLY        out_i        = x_i cos[p][i] - x_{i+Dr/2} sin[p][i]
+ *                         out_{i+Dr/2} = x_{i+Dr/2} cos[p][i+Dr/2] + x_i sin[p][i+Dr/2]
+ *   MLA_ROPE_INVERSE      the Jacobian transpose of it (the gradient):
+ *                         out_i        = g_i cos[p][i] + g_{i+Dr/2} sin[p][i+Dr/2]
+ *                         out_{i+Dr/2} = g_{i+Dr/2} cos[p][i+Dr/2] - g_i sin[p][i]
+ *   MLA_ROPE_INVERSE_SUM  the same of the sum of all heads' gradients, the
+ *                         gradient of a tensor that the heads share: out holds
+ *                         one head (out_h is unused). The order of the float32
+ *                         sum is fixed.
+ * The Dn pass-through channels are copied (summed). Arithmetic in float32,
+ * one rounding to dtype.
+ *   dtype      MLA_IN_F32 or MLA_IN_BF16: the type of in and out
+ *   pos        [axes, T] int32, dense
+ *   pair_axis  [Dr/2] bytes in HOST memory, each < axes; read before the call
+ *              returns
+ *   A position outside [0, cs_rows) is reported as MLA_ERR_POS_RANGE in
+ *   *dev_status; the outputs of its pairs are unspecified.
+ * Requires Dr <= 256, Dn + Dr <= 8192 (else MLA_ERR_UNSUPPORTED). Any element
+ * alignment and strides; 16-byte aligned rows whose Dn and Dr/2 are multiples
+ * of 16 bytes move by 16-byte accesses. out may overlap no input, by the byte
+ * range from its first to its last element.
+ */
+MLAQ_API int mla_rope_axes(const mla_rope_axes_shape *shape, int dtype, int mode, const void *in,
+                           const float *cos_tab, const float *sin_tab, const int32_t *pos,
+                           const uint8_t *pair_axis, void *out, int *dev_status, void *stream);
+
+/*
+ * The cos/sin rows of every token for positions with several axes:
+ * cos_out[t][j] = cos_tab[pos[pair_axis[j mod Dr/2]][t]][j], sin_out alike,
+ * both [T, Dr] fp32, dense, 16-byte aligned. With them as the tables, T rows
+ * and no positions (pos = NULL), mla_q_uproj_fwd, the backward calls and
+ * mla_kv_uproj_fwd rotate by several axes. H, Dn and the strides of the
+ * shape are unused (H > 0). Entries of positions outside the table are
+ * unspecified (reported as above).
+ */
+MLAQ_API int mla_rope_axes_table(const mla_rope_axes_shape *shape, const float *cos_tab, const float *sin_tab,
+                                 const int32_t *pos, const uint8_t *pair_axis, float *cos_out, float *sin_out,
+                                 int *dev_status, void *stream);
+
+/* ---- AdamW over many tensors --------------------------------------------
+ * One optimizer step for the parameters that the backward calls (or any
+ * other) give gradients of, in one launch (an addition of this library). For
+ * every element, in float32, t = step:
+ *   g  = grad * grad_scale,       p  = p * (1 - lr weight_decay)
+ *   m' = m beta1 + g (1 - beta1), v' = v beta2 + (g (1 - beta2)) g
+ *   p' = p - (m' / (sqrt(v') (1 - beta2^t)^-1/2 + eps)) lr / (1 - beta1^t)
+ * A tensor's buffers, all DEVICE memory of the caller:
+ *   param           [n] float32 or bf16 (one type in a plan), in and out
+ *   grad            [n] float32 or bf16 (one type in a plan)
+ *   exp_avg, exp_avg_sq         state_bits 32: m and v, [n] float32
+ *                               state_bits 8: E4M3 codes of m and of sqrt(v),
+ *                               [n] bytes; decoded as code * 2^(scale - 127)
+ *   exp_avg_scales, exp_avg_sq_scales   state_bits 8: [ceil(n/32)] E8M0 bytes
+ *                               (mxfp8_quantize_rows' rule over 32 consecutive
+ *                               elements; all-zero codes and scales are a
+ *                               fresh state); state_bits 32: NULL
+ *   master          [n] float32 or NULL: the parameter in full precision;
+ *                   param then only receives its rounded copy
+ * The step uses m' and v' before they are rounded to 8 bits; a root above
+ * zero never rounds to code 0. A 32-element block that holds a NaN or an
+ * infinity keeps scale 0xFF and NaN codes. Pointers need their type's
+ * alignment; tensors that start on 16 bytes (codes: 8) move by wide accesses. */
+typedef struct {
+    void *param;
+    const void *grad;
+    void *exp_avg;
+    void *exp_avg_sq;
+    uint8_t *exp_avg_scales;
+    uint8_t *exp_avg_sq_scales;
+    float *master;
+    int64_t n;
+} mla_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;       /* t, counted from 1 */
+    int32_t stochastic; /* 1: E4M3 codes, and bf16 parameters without a master, are rounded up with the
+                           probability of their fraction, from `seed`; 0: to nearest even */
+    uint32_t seed;      /* another one each step */
+} mla_adamw_args;
+
+/*
+ * A plan lists the tensors of a step. mla_adamw_plan_build checks them
+ * (MLA_ERR_ALIAS when a written buffer overlaps any other) and writes the plan
+ * to HOST memory, mla_adamw_plan_bytes(tensors, count) bytes (0: invalid
+ * arguments); the caller keeps it and a copy of it in device memory (16-byte
+ * aligned) for as long as the buffers stay where they are.
+ * mla_adamw_step enqueues one step. grad_scale: one device float32 that
+ * multiplies every gradient (loss scale, clipping), or NULL for 1. The
+ * launch reads the device copy only; a plan may be used on any stream, one
+ * step at a time. The random bits of an element depend on the seed and on
+ * its place: its index plus the sizes of the tensors before its own, each
+ * rounded up to a multiple of 64.
+ */
+MLAQ_API size_t mla_adamw_plan_bytes(const mla_adamw_tensor *tensors, int64_t count);
+MLAQ_API int mla_adamw_plan_build(const mla_adamw_tensor *tensors, int64_t count, int param_dtype, int grad_dtype,
+                                  int state_bits, void *plan, size_t plan_size);
+MLAQ_API int mla_adamw_step(const void *plan_host, const void *plan_device, const mla_adamw_args *args,
+                            const float *grad_scale, void *stream);
+
 /* Static, human-readable name of a status code. */
 MLAQ_API const char *mla_status_string(int status);
 

@@ -603,3 +603,11 @@ def kv_fwd(c_kv, W, k_pe, cos, sin, H, Dn, Dv, Dr, pos=None, o_key=None, o_value
     _call(lib().mla_kv_uproj_fwd, "mla_kv_uproj_fwd", ctypes.byref(s), _ptr(c_kv), _ptr(W), _ptr(k_pe),
           _ptr(cos), _ptr(sin), _ptr(pos), _ptr(o_key), _ptr(o_value), _ptr(status), _stream(dev, stream))
     return o_key, o_value
+
+
+from .rotary import RopeAxesShape, rope_axes, rope_axes_table, rope_sections  # noqa: E402
+
+__all__ += ["RopeAxesShape", "rope_axes", "rope_axes_table", "rope_sections"]
+from .optim import AdamW, AdamwPlan, adamw_plan, adamw_step  # noqa: E402
+
+__all__ += ["AdamW", "AdamwPlan", "adamw_plan", "adamw_step"]

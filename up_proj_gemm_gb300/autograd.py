@@ -23,6 +23,10 @@ the scales (in the out_mode's layout) and an ``anchor``, a 0-d float tensor
 that carries the graph. The consumer hands back the bf16 gradient of the
 query with ``query.backward(dq)``; that runs this layer's backward, like
 ``q.backward(dq)`` on the bf16 face.
+
+``rope_axes(x, cos, sin, pos, axes, Dr, heads=None)`` rotates by positions
+with several axes; with ``heads`` one shared head becomes that many, and its
+gradient is the inverse rotation of the heads' sum.
 """
 from __future__ import annotations
 
@@ -31,8 +35,9 @@ from dataclasses import dataclass
 import torch
 
 from . import bwd_dgrad, bwd_wgrad, fwd
+from . import rope_axes as _rope_axes
 
-__all__ = ["QUpProj", "q_up_proj", "Mxfp8Query", "q_up_proj_mxfp8"]
+__all__ = ["QUpProj", "q_up_proj", "Mxfp8Query", "q_up_proj_mxfp8", "RopeAxes", "rope_axes"]
 
 
 def _layer_backward(ctx, dq):
@@ -134,3 +139,28 @@ def q_up_proj_mxfp8(x, W, cos, sin, H, Dn, Dr, bias=None, pos=None, out_mode="mx
     box = _GradBox()
     codes, scales, anchor = _QUpProjMxfp8.apply(x, W, bias, cos, sin, pos, H, Dn, Dr, out_mode, box)
     return Mxfp8Query(codes, scales, anchor, box)
+
+
+class RopeAxes(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, cos, sin, pos, axes, Dr, heads):
+        ctx.save_for_backward(cos, sin, pos)
+        ctx.axes, ctx.Dr, ctx.shared = axes, Dr, heads is not None
+        return _rope_axes(x if heads is None else x.expand(-1, heads, -1), cos, sin, pos, axes, Dr)
+
+    @staticmethod
+    def backward(ctx, g):
+        cos, sin, pos = ctx.saved_tensors
+        if g.shape[2] > 1 and g.stride(2) != 1:
+            g = g.contiguous()
+        dx = _rope_axes(g, cos, sin, pos, ctx.axes, ctx.Dr, inverse=True, sum_heads=ctx.shared)
+        return dx, None, None, None, None, None, None
+
+
+def rope_axes(x, cos, sin, pos, axes, Dr, heads=None):
+    """x [T, H, D] with the last Dr channels of every head rotated by several
+    axes, differentiable in x. heads: x holds one head [T, 1, D] that this
+    many heads share; the result is [T, heads, D]."""
+    if heads is not None and x.shape[1] != 1:
+        raise ValueError(f"a shared head is [T, 1, D], got {list(x.shape)}")
+    return RopeAxes.apply(x, cos, sin, pos, axes, Dr, heads)

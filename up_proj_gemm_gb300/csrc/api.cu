@@ -12,6 +12,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "checks.h"
 #include "internal.h"
 #include "mx.cuh"
 
@@ -120,38 +121,6 @@ int make_tmap_chunks(void* tmap_out, const void* base, uint64_t rows, uint64_t c
 }
 
 namespace {
-
-struct Range {
-    uintptr_t lo = 0, hi = 0;  // [lo, hi); empty when lo == hi
-};
-
-Range rng(const void* p, int64_t bytes) {
-    Range r;
-    if (p && bytes > 0) {
-        r.lo = reinterpret_cast<uintptr_t>(p);
-        r.hi = r.lo + (uintptr_t)bytes;
-    }
-    return r;
-}
-
-bool overlap(const Range& a, const Range& b) {
-    return a.lo != a.hi && b.lo != b.hi && a.lo < b.hi && b.lo < a.hi;
-}
-
-template <size_t NO, size_t NI>
-bool any_alias(const Range (&outs)[NO], const Range (&ins)[NI]) {
-    for (size_t i = 0; i < NO; ++i) {
-        for (size_t j = 0; j < NI; ++j)
-            if (overlap(outs[i], ins[j])) return true;
-        for (size_t j = i + 1; j < NO; ++j)
-            if (overlap(outs[i], outs[j])) return true;
-    }
-    return false;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-constexpr int64_t kI32Max = 0x7fffffffLL;
 
 // Checks shared by every mla_q_uproj_* call. On success fills D and N.
 int check_shape(const mla_q_shape* s, int* D, int64_t* N) {

@@ -1,0 +1,114 @@
+"""Rotary positions with several axes: argument marshalling for
+``mla_rope_axes`` and ``mla_rope_axes_table`` (declared in ``include/mlaq.h``).
+
+Pair i of a head (rope channels i and i + Dr/2) of token t is turned by row
+``pos[axes[i], t]`` of the cos/sin tables, so the time, height and width of an
+image or video token each turn their own pairs. ``axes`` is a sequence of
+Dr/2 axis numbers; ``rope_sections((16, 8, 8))`` gives the one for contiguous
+sections.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _call, _need, _ptr, _SIGS, _status, _stream, lib
+
+__all__ = ["RopeAxesShape", "rope_sections", "rope_axes", "rope_axes_table"]
+
+
+class RopeAxesShape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int32), ("Dn", ctypes.c_int32), ("Dr", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("cs_rows", ctypes.c_int64), ("cs_width", ctypes.c_int64),
+                ("in_t", ctypes.c_int64), ("in_h", ctypes.c_int64), ("out_t", ctypes.c_int64),
+                ("out_h", ctypes.c_int64), ("reserved", ctypes.c_int64)]
+
+
+_vp, _int = ctypes.c_void_p, ctypes.c_int
+_SIGS.update({
+    "mla_rope_axes": (_int, [ctypes.POINTER(RopeAxesShape), _int, _int, _vp, _vp, _vp, _vp, ctypes.c_char_p, _vp,
+                             _vp, _vp]),
+    "mla_rope_axes_table": (_int, [ctypes.POINTER(RopeAxesShape), _vp, _vp, _vp, ctypes.c_char_p, _vp, _vp, _vp,
+                                   _vp]),
+})
+
+
+def rope_sections(sections) -> bytes:
+    """The axis of every pair when axis a turns the next sections[a] pairs."""
+    return bytes(a for a, n in enumerate(sections) for _ in range(n))
+
+
+def _axes_args(cos, sin, pos, axes, Dr, T, dev):
+    """Check the tables, the positions [A, T] and the Dr/2 pairs' axes; the axes as bytes."""
+    _need(cos, "cos", torch.float32, dev, ndim=2)
+    _need(sin, "sin", torch.float32, dev, shape=cos.shape)
+    _need(pos, "pos", torch.int32, dev, ndim=2, shape=(pos.shape[0], T) if pos.dim() == 2 else None)
+    if len(axes) != Dr // 2:
+        raise ValueError(f"axes must name the axis of each of the {Dr // 2} pairs, got {len(axes)}")
+    return bytes(axes)
+
+
+def rope_axes(x, cos, sin, pos, axes, Dr, inverse=False, sum_heads=False, out=None, status=None, stream=None):
+    """x [T, H, D] (bf16 or float32, any token and head strides, contiguous
+    channels) with the last Dr channels of every head rotated; the others are
+    copied.
+
+    pos: int32 [A, T]; axes: the axis of each of the Dr/2 pairs. ``inverse``
+    applies the Jacobian transpose (the gradient), ``sum_heads`` (with
+    inverse) the transpose of the heads' sum, [T, 1, D]: the gradient of a key
+    part that all heads share. ``out`` may be a strided view."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
+    if not x.is_cuda or x.dim() != 3 or (x.shape[2] > 1 and x.stride(2) != 1):
+        raise ValueError("x must be a 3-D CUDA tensor [T, H, D] with unit inner stride")
+    if sum_heads and not inverse:
+        raise ValueError("sum_heads sums gradients: it needs inverse=True")
+    T, H, D = x.shape
+    if not 0 < Dr <= D:
+        raise ValueError(f"Dr must be in 1..{D}, got {Dr}")
+    dev = x.device
+    axes = _axes_args(cos, sin, pos, axes, Dr, T, dev)
+    _status(status, dev)
+    Ho = 1 if sum_heads else H
+    if out is None:
+        out = torch.empty((T, Ho, D), dtype=x.dtype, device=dev)
+        out_t, out_h = Ho * D, D
+    else:
+        if not isinstance(out, torch.Tensor) or out.dtype != x.dtype:
+            raise TypeError(f"out must be a {x.dtype} tensor")
+        if tuple(out.shape) != (T, Ho, D):
+            raise ValueError(f"out must be {[T, Ho, D]}, got {list(out.shape)}")
+        if not out.is_cuda or out.device != dev or (D > 1 and out.stride(2) != 1):
+            raise ValueError(f"out must be on {dev} with unit inner stride")
+        out_t, out_h = out.stride(0), out.stride(1)
+    s = RopeAxesShape(T, H, D - Dr, Dr, pos.shape[0], cos.shape[0], cos.shape[1], x.stride(0) if T > 1 else 0,
+                      x.stride(1) if H > 1 else 0, out_t if T > 1 else 0, out_h if Ho > 1 else 0, 0)
+    _call(lib().mla_rope_axes, "mla_rope_axes", ctypes.byref(s), 0 if x.dtype == torch.float32 else 1,
+          (2 if sum_heads else 1) if inverse else 0, _ptr(x), _ptr(cos), _ptr(sin), _ptr(pos), axes, _ptr(out),
+          _ptr(status), _stream(dev, stream))
+    return out
+
+
+def rope_axes_table(cos, sin, pos, axes, Dr, cos_out=None, sin_out=None, status=None, stream=None):
+    """(cos, sin) float32 [T, Dr] of every token for positions with several
+    axes: the tables to give fwd, bwd_dgrad, bwd_wgrad, bwd_mxfp8 and kv_fwd
+    (with pos=None), which then rotate by several axes."""
+    if not isinstance(pos, torch.Tensor) or pos.dim() != 2:
+        raise ValueError("pos must be an int32 tensor [A, T]")
+    dev = pos.device
+    T = pos.shape[1]
+    axes = _axes_args(cos, sin, pos, axes, Dr, T, dev)
+    _status(status, dev)
+    if cos_out is None:
+        cos_out = torch.empty((T, Dr), dtype=torch.float32, device=dev)
+    if sin_out is None:
+        sin_out = torch.empty((T, Dr), dtype=torch.float32, device=dev)
+    _need(cos_out, "cos_out", torch.float32, dev, shape=(T, Dr))
+    _need(sin_out, "sin_out", torch.float32, dev, shape=(T, Dr))
+    s = RopeAxesShape(T, 1, 0, Dr, pos.shape[0], cos.shape[0], cos.shape[1], 0, 0, 0, 0, 0)
+    _call(lib().mla_rope_axes_table, "mla_rope_axes_table", ctypes.byref(s), _ptr(cos), _ptr(sin), _ptr(pos), axes,
+          _ptr(cos_out), _ptr(sin_out), _ptr(status), _stream(dev, stream))
+    return cos_out, sin_out
