@@ -688,6 +688,54 @@ MLAQ_API int mla_adamw_plan_build(const mla_adamw_tensor *tensors, int64_t count
 MLAQ_API int mla_adamw_step(const void *plan_host, const void *plan_device, const mla_adamw_args *args,
                             const float *grad_scale, void *stream);
 
+/* ---- Gated feed-forward block -------------------------------------------
+ * The layer's other projections, next to the query up-projection (an addition
+ * of this library). T tokens, K channels, F hidden channels:
+ *   forward   [g | u] = x w_gate_up^T,  h = act(g) u,  y = h w_down^T
+ *   backward  dh = dy w_down,  dg = dh u act'(g),  du = dh act(g)
+ *             dx = [dg | du] w_gate_up,  dw_gate_up = [dg | du]^T x,
+ *             dw_down = dy^T h
+ *   x [T, K] bf16, row pitch ld_x elements (0: dense); w_gate_up [2F, K] bf16,
+ *   the F gate rows, then the F up rows; w_down [K, F] bf16.
+ *   act   MLA_ACT_SILU       g / (1 + exp(-g))
+ *         MLA_ACT_GELU       g (1 + erf(g / sqrt 2)) / 2
+ *         MLA_ACT_GELU_TANH  g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2
+ * Sums are float32; g, u, h, [dg | du] and the results are rounded to bf16
+ * once each (h from the float32 g and u, [dg | du] from the given bf16 ones).
+ * Requires K, F and ld_x multiples of 8 and 16-byte aligned pointers (else
+ * MLA_ERR_ALIGNMENT); outputs may overlap nothing. dev_status receives
+ * MLA_ERR_TIMEOUT when a pipeline wait gave up. */
+enum { MLA_ACT_SILU = 0, MLA_ACT_GELU = 1, MLA_ACT_GELU_TANH = 2 };
+
+typedef struct {
+    int64_t T;
+    int64_t K;
+    int64_t F;
+    int64_t ld_x;
+    int32_t act;
+    int32_t reserved; /* set to 0 */
+} mla_ffn_shape;
+
+/*
+ * Forward. h [T, F] bf16 is always written (the second product reads it);
+ * gate_up [T, 2F] bf16 (g, then u) is written when not NULL: the backward
+ * needs both. T = 0 is a no-op.
+ */
+MLAQ_API int mla_gated_ffn_fwd(const mla_ffn_shape *shape, const void *x, const void *w_gate_up, const void *w_down,
+                               void *gate_up, void *h, void *y, int *dev_status, void *stream);
+
+/*
+ * Backward from dy [T, K] bf16, the forward's inputs and its gate_up and h.
+ * dx [T, K], dw_gate_up [2F, K], dw_down [K, F] (bf16) are each optional
+ * (NULL: not computed; at least one is required). dgate_up [T, 2F] bf16
+ * receives [dg | du]; dx and dw_gate_up need it, w_down and gate_up. dx needs
+ * w_gate_up, dw_gate_up needs x, dw_down needs h; others may be NULL. T = 0
+ * writes dw_gate_up = 0 and dw_down = 0.
+ */
+MLAQ_API int mla_gated_ffn_bwd(const mla_ffn_shape *shape, const void *dy, const void *x, const void *w_gate_up,
+                               const void *w_down, const void *gate_up, const void *h, void *dgate_up, void *dx,
+                               void *dw_gate_up, void *dw_down, int *dev_status, void *stream);
+
 /* Static, human-readable name of a status code. */
 MLAQ_API const char *mla_status_string(int status);
 

@@ -611,3 +611,6 @@ __all__ += ["RopeAxesShape", "rope_axes", "rope_axes_table", "rope_sections"]
 from .optim import AdamW, AdamwPlan, adamw_plan, adamw_step  # noqa: E402
 
 __all__ += ["AdamW", "AdamwPlan", "adamw_plan", "adamw_step"]
+from .ffn import ACTIVATIONS, FfnShape, gated_ffn_bwd, gated_ffn_fwd  # noqa: E402
+
+__all__ += ["ACTIVATIONS", "FfnShape", "gated_ffn_bwd", "gated_ffn_fwd"]

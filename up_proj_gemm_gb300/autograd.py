@@ -27,6 +27,9 @@ query with ``query.backward(dq)``; that runs this layer's backward, like
 ``rope_axes(x, cos, sin, pos, axes, Dr, heads=None)`` rotates by positions
 with several axes; with ``heads`` one shared head becomes that many, and its
 gradient is the inverse rotation of the heads' sum.
+
+``gated_ffn(x, w_gate_up, w_down, act)`` is the gated feed-forward block; it
+keeps x, the gate and up products and the hidden activations for its backward.
 """
 from __future__ import annotations
 
@@ -35,9 +38,11 @@ from dataclasses import dataclass
 import torch
 
 from . import bwd_dgrad, bwd_wgrad, fwd
+from . import gated_ffn_bwd, gated_ffn_fwd
 from . import rope_axes as _rope_axes
 
-__all__ = ["QUpProj", "q_up_proj", "Mxfp8Query", "q_up_proj_mxfp8", "RopeAxes", "rope_axes"]
+__all__ = ["QUpProj", "q_up_proj", "Mxfp8Query", "q_up_proj_mxfp8", "RopeAxes", "rope_axes", "GatedFfn",
+           "gated_ffn"]
 
 
 def _layer_backward(ctx, dq):
@@ -164,3 +169,27 @@ def rope_axes(x, cos, sin, pos, axes, Dr, heads=None):
     if heads is not None and x.shape[1] != 1:
         raise ValueError(f"a shared head is [T, 1, D], got {list(x.shape)}")
     return RopeAxes.apply(x, cos, sin, pos, axes, Dr, heads)
+
+
+class GatedFfn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_gate_up, w_down, act):
+        ctx.act = act
+        if not any(ctx.needs_input_grad):
+            return gated_ffn_fwd(x, w_gate_up, w_down, act=act)
+        y, gate_up, h = gated_ffn_fwd(x, w_gate_up, w_down, act=act, save=True)
+        ctx.save_for_backward(x, w_gate_up, w_down, gate_up, h)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w_gate_up, w_down, gate_up, h = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        return (*gated_ffn_bwd(dy.contiguous(), x, w_gate_up, w_down, gate_up, h, act=ctx.act, dx=need[0],
+                               dw_gate_up=need[1], dw_down=need[2]), None)
+
+
+def gated_ffn(x, w_gate_up, w_down, act="silu"):
+    """(act(g) * u) w_down^T with [g | u] = x w_gate_up^T as bf16 [T, K],
+    differentiable in x, w_gate_up and w_down."""
+    return GatedFfn.apply(x, w_gate_up, w_down, act)

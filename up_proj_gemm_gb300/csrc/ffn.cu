@@ -1,0 +1,563 @@
+// Gated feed-forward block, forward and backward (T tokens, K channels, F
+// hidden channels, all bf16 with float32 accumulation):
+//   forward   [g | u] = x Wgu^T   (Wgu [2F, K]: F gate rows, then F up rows)
+//             h = act(g) u,  y = h Wd^T                       (Wd [K, F])
+//   backward  dh = dy Wd,  dg = dh u act'(g),  du = dh act(g)
+//             dx = [dg | du] Wgu,  dWgu = [dg | du]^T x,  dWd = dy^T h
+// Six products on one GEMM kernel: both projections, the activation and the
+// product are one launch (a tile holds the same 128 hidden channels of gate
+// and up), and so are dh and the activation's gradient.
+//
+// The GEMM: a cluster of two CTAs computes a 256 x 256 tile with
+// tcgen05.mma.cta_group::2 (M = 256: each CTA accumulates its 128 rows over
+// all 256 columns in its own TMEM; each stages its 128 rows of A and its half
+// of B, so an operand byte is fetched once per pair). 64-element K steps,
+// operands by TMA into a ring of 32 KB stages per CTA, two accumulators of
+// 256 TMEM columns, so a tile's epilogue runs under the next one's products.
+// Operands come K-major (rows contiguous along the reduction) or MN-major
+// (the reduction runs over rows): no transposed copy is made.
+// Warps: 0 producer, 1 MMA issuer (of the pair's even CTA), 2-9 epilogue.
+// Bound by the tensor cores when T is in the thousands.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <mutex>
+
+#include "checks.h"
+#include "internal.h"
+#include "mx.cuh"
+#include "ptx.cuh"
+
+namespace mlaq {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kStages = 6;
+constexpr int kBK = 64;
+constexpr uint32_t kHalfBytes = 128u * 128u;       // 128 rows (or columns) of one K step, one operand
+constexpr uint32_t kStageBytes = 2u * kHalfBytes;  // A and B of one CTA
+constexpr uint32_t kChunkBytes = 64u * 128u;       // MN-major: 64 columns of 64 K rows
+constexpr uint32_t kTmemCols = 512;
+constexpr size_t kSmem = 1024 + kStages * kStageBytes + 256;
+
+enum Epilogue { kStore = 0, kGate = 1, kGateGrad = 2 };
+
+struct GemmParams {
+    int M, N;                 // of the result; kGate: N = F (a tile holds 128 of them)
+    int k_tiles, m_tiles, n_tiles;
+    int F, act;
+    uint16_t* out;            // kStore [M, N], kGate h [M, F], kGateGrad [M, 2F]
+    uint16_t* gate_up_out;    // kGate: [M, 2F] or null
+    const uint16_t* gate_up;  // kGateGrad: [M, 2F]
+    int* status;
+};
+
+// ------------------------------------------------------- two-CTA primitives
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of the even CTA's copy of a shared-memory location.
+__device__ __forceinline__ uint32_t map_to_leader(uint32_t addr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(0));
+    return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int32_t c0, int32_t c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on the same barrier of both CTAs once the MMAs issued so far are done.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// ------------------------------------------------------------- activations
+// act(g) and its derivative; sigmoid through exp and a fast division (a few
+// ulp of float32, far below the bf16 results).
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+
+template <bool GRAD>
+__device__ __forceinline__ void activate(int act, float g, float& a, float& da) {
+    if (act == MLA_ACT_SILU) {
+        const float s = sigmoid(g);
+        a = g * s;
+        if constexpr (GRAD) da = s * (1.f + g * (1.f - s));
+    } else if (act == MLA_ACT_GELU) {
+        const float c = 0.5f * erfcf(-0.70710678f * g);
+        a = g * c;
+        if constexpr (GRAD) da = c + g * 0.39894228f * __expf(-0.5f * g * g);
+    } else {  // 0.5 g (1 + tanh(z)) = g sigmoid(2 z), z = sqrt(2/pi) (g + 0.044715 g^3)
+        const float k = 1.59576912f;  // 2 sqrt(2/pi)
+        const float s = sigmoid(k * (g + 0.044715f * g * g * g));
+        a = g * s;
+        if constexpr (GRAD) da = s + g * s * (1.f - s) * k * (1.f + 0.134145f * g * g);
+    }
+}
+
+__device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16lo_to_f32(u[i]);
+        v[2 * i + 1] = bf16hi_to_f32(u[i]);
+    }
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
+    st_global_v4(p, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// Tiles in groups of 8 row tiles, columns inside a group: the tiles that run
+// at the same time span about as many rows of A as of B, which L2 holds.
+constexpr int kGroupM = 8;
+__device__ __forceinline__ void tile_at(const GemmParams& p, int tile, int& mt, int& nt) {
+    const int per = kGroupM * p.n_tiles;
+    const int g = tile / per, r = tile - g * per;
+    const int rows = p.m_tiles - g * kGroupM < kGroupM ? p.m_tiles - g * kGroupM : kGroupM;
+    nt = r / rows;
+    mt = g * kGroupM + (r - nt * rows);
+}
+
+template <int EPI>
+__device__ __forceinline__ void epilogue_rows(const GemmParams& p, uint32_t tacc, int64_t row, int n0, int half) {
+    const bool valid = row < p.M;
+    if constexpr (EPI == kGate) {
+        // columns 0-127 of the accumulator are gates, 128-255 the same channels' up products
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+            const int col = half * 64 + c;
+            uint32_t rg[32], ru[32];
+            __syncwarp();
+            tmem_ld32(tacc + col, rg);
+            tmem_ld32(tacc + 128 + col, ru);
+            tmem_ld_wait();
+            const int f = n0 + col;
+            if (!valid) continue;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                if (f + i >= p.F) break;
+                float g[8], u[8], h[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float a, unused;
+                    g[j] = __uint_as_float(rg[i + j]);
+                    u[j] = __uint_as_float(ru[i + j]);
+                    activate<false>(p.act, g[j], a, unused);
+                    h[j] = a * u[j];
+                }
+                store8(p.out + row * p.F + f + i, h);
+                if (p.gate_up_out) {
+                    store8(p.gate_up_out + row * 2 * p.F + f + i, g);
+                    store8(p.gate_up_out + row * 2 * p.F + p.F + f + i, u);
+                }
+            }
+        }
+    } else {
+        for (int c = 0; c < 128; c += 32) {
+            const int col = half * 128 + c;
+            uint32_t r[32];
+            __syncwarp();
+            tmem_ld32(tacc + col, r);
+            tmem_ld_wait();
+            if (!valid) continue;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                const int n = n0 + col + i;
+                if (n >= p.N) break;
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[i + j]);
+                if constexpr (EPI == kStore) {
+                    store8(p.out + row * p.N + n, v);
+                } else {
+                    const uint16_t* gu = p.gate_up + row * 2 * p.F + n;
+                    float g[8], u[8], dg[8], du[8];
+                    unpack8(__ldg(reinterpret_cast<const uint4*>(gu)), g);
+                    unpack8(__ldg(reinterpret_cast<const uint4*>(gu + p.F)), u);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float a, da;
+                        activate<true>(p.act, g[j], a, da);
+                        dg[j] = v[j] * u[j] * da;
+                        du[j] = v[j] * a;
+                    }
+                    store8(p.out + row * 2 * p.F + n, dg);
+                    store8(p.out + row * 2 * p.F + p.F + n, du);
+                }
+            }
+        }
+    }
+}
+
+// AMN / BMN: the operand is MN-major (its reduction runs over rows).
+template <bool AMN, bool BMN, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    ffn_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const GemmParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t bars = base + kStages * kStageBytes;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (kStages + s); };
+    auto tfull = [&](int b) { return bars + 8u * (2 * kStages + b); };
+    auto tempty = [&](int b) { return bars + 8u * (2 * kStages + 2 + b); };
+    const uint32_t drain = bars + 8u * (2 * kStages + 4);
+    uint8_t* tail = smem_raw + (bars - raw) + 8u * (2 * kStages + 5);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(tail);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int tiles = p.m_tiles * p.n_tiles;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull(b), 1);
+            mbar_init(tempty(b), 16);  // 8 epilogue warps of each CTA
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32((const void*)tmem_slot), kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0, issued = 0, par = 0;
+            bool ok = true;
+            for (int tile = pair; ok && tile < tiles; tile += pairs) {
+                int mt, nt;
+                tile_at(p, tile, mt, nt);
+                const int a0 = mt * 256 + rank * 128;
+                // kGate: the even CTA brings the tile's 128 gate rows, the odd one its up rows
+                const int b0 = EPI == kGate ? rank * p.F + nt * 128 : nt * 256 + rank * 128;
+                for (int kt = 0; kt < p.k_tiles; ++kt) {
+                    if (!mbar_wait(empty(s), ph ^ 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sa = base + s * kStageBytes, sb = sa + kHalfBytes;
+                    const uint32_t bar = map_to_leader(full(s));
+                    if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * kStageBytes);
+                    if constexpr (AMN) {
+                        tma_load_2d_pair(sa, &tmA, a0, kt * kBK, bar);
+                        tma_load_2d_pair(sa + kChunkBytes, &tmA, a0 + 64, kt * kBK, bar);
+                    } else {
+                        tma_load_2d_pair(sa, &tmA, kt * kBK, a0, bar);
+                    }
+                    if constexpr (BMN) {
+                        tma_load_2d_pair(sb, &tmB, b0, kt * kBK, bar);
+                        tma_load_2d_pair(sb + kChunkBytes, &tmB, b0 + 64, kt * kBK, bar);
+                    } else {
+                        tma_load_2d_pair(sb, &tmB, kt * kBK, b0, bar);
+                    }
+                    issued |= 1u << s;
+                    par = (par & ~(1u << s)) | (ph << s);
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!ok && rank == 0)  // copies in flight (both CTAs') land before the pair leaves
+                for (int q = 0; q < kStages; ++q)
+                    if (issued & (1u << q)) mbar_wait(full(q), (par >> q) & 1u, nullptr, 200000000ull);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- MMA issuer
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = idesc_bf16(256, 256, AMN, BMN);
+            int s = 0, local = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int tile = pair; ok && tile < tiles; tile += pairs, ++local) {
+                const int b = local & 1;
+                if (!mbar_wait(tempty(b), (((uint32_t)local >> 1) & 1u) ^ 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int kt = 0; kt < p.k_tiles; ++kt) {
+                    if (!mbar_wait(full(s), ph, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = base + s * kStageBytes, sb = sa + kHalfBytes;
+#pragma unroll
+                    for (int j = 0; j < kBK / 16; ++j) {
+                        const uint64_t ad = AMN ? desc_mnmajor_sw128(sa + 2048u * j, kChunkBytes)
+                                                : desc_kmajor_sw128(sa + 32u * j);
+                        const uint64_t bd = BMN ? desc_mnmajor_sw128(sb + 2048u * j, kChunkBytes)
+                                                : desc_kmajor_sw128(sb + 32u * j);
+                        mma_bf16_pair(tmem + 256u * b, ad, bd, idesc, (kt | j) != 0);
+                    }
+                    mma_commit_pair(empty(s));
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (ok) mma_commit_pair(tfull(b));
+            }
+            if (!ok) {
+                mma_commit_pair(drain);
+                mbar_wait(drain, 0, nullptr, 200000000ull);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        int local = 0;
+        for (int tile = pair; tile < tiles; tile += pairs, ++local) {
+            const int b = local & 1;
+            int mt, nt;
+            tile_at(p, tile, mt, nt);
+            bool ok = mbar_wait(tfull(b), ((uint32_t)local >> 1) & 1u, abort_flag);
+            if (__any_sync(0xffffffffu, !ok)) break;
+            tc_fence_after();
+            epilogue_rows<EPI>(p, tmem + ((uint32_t)(quad * 32) << 16) + 256u * b,
+                               (int64_t)mt * 256 + rank * 128 + quad * 32 + lane, nt * (EPI == kGate ? 128 : 256), half);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(map_to_leader(tempty(b)));
+        }
+    }
+
+    // --------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) record_status(p.status, MLA_ERR_TIMEOUT);
+    cluster_sync();  // no CTA leaves while its pair may still signal it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+// Pairs that can be resident at once (some GPCs may hold an odd number of SMs).
+template <bool AMN, bool BMN, int EPI>
+int prepare_gemm(int num_sms, int device, int* pairs) {
+    static std::mutex mu;
+    static int cache[64];
+    std::lock_guard<std::mutex> lock(mu);
+    if (cache[device] == 0) {
+        auto k = ffn_gemm_kernel<AMN, BMN, EPI>;
+        if (cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+            return MLA_ERR_CUDA;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)num_sms & ~1u);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = 2;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, (const void*)k, &cfg) != cudaSuccess || n < 1) return MLA_ERR_CUDA;
+        cache[device] = n;
+    }
+    *pairs = cache[device];
+    return MLA_OK;
+}
+
+struct Operand {
+    const void* p;
+    int64_t rows, cols, ld;  // as stored, ld in elements
+};
+
+// C = A B^T over `red` elements. A is [M, red] (or [red, M] when AMN), B is
+// [N, red] (or [red, N]); kGate's B holds the gate rows, then the up rows.
+template <bool AMN, bool BMN, int EPI>
+int gemm(const Operand& a, const Operand& b, GemmParams p, int64_t red, const DeviceInfo& di, cudaStream_t stream) {
+    p.m_tiles = (p.M + 255) / 256;
+    p.n_tiles = EPI == kGate ? (p.N + 127) / 128 : (p.N + 255) / 256;
+    p.k_tiles = (int)((red + kBK - 1) / kBK);
+    alignas(64) CUtensorMap ta, tb;
+    int st = make_tmap_2d(&ta, a.p, 1, (uint64_t)a.cols, (uint64_t)a.rows, (uint64_t)a.ld * 2, 64, AMN ? kBK : 128, true);
+    if (st == MLA_OK)
+        st = make_tmap_2d(&tb, b.p, 1, (uint64_t)b.cols, (uint64_t)b.rows, (uint64_t)b.ld * 2, 64, BMN ? kBK : 128, true);
+    if (st != MLA_OK) return st;
+    int pairs = 0;
+    st = prepare_gemm<AMN, BMN, EPI>(di.num_sms, di.device, &pairs);
+    if (st != MLA_OK) return st;
+    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+    if (tiles > kI32Max / 2) return MLA_ERR_UNSUPPORTED;
+    if (tiles < pairs) pairs = (int)tiles;
+    ffn_gemm_kernel<AMN, BMN, EPI><<<2 * pairs, kThreads, kSmem, stream>>>(ta, tb, p);
+    return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int check_ffn(const mla_ffn_shape* s) {
+    if (!s) return MLA_ERR_INVALID_ARG;
+    if (s->T < 0 || s->K <= 0 || s->F <= 0 || s->ld_x < 0 || s->reserved != 0) return MLA_ERR_INVALID_ARG;
+    if (s->act < MLA_ACT_SILU || s->act > MLA_ACT_GELU_TANH) return MLA_ERR_INVALID_ARG;
+    if (s->T > kI32Max - 512 || s->K > kI32Max / 2 - 512 || s->F > kI32Max / 2 - 512) return MLA_ERR_INVALID_ARG;
+    if (s->ld_x != 0 && (s->ld_x < s->K || s->ld_x > ((int64_t)1 << 36))) return MLA_ERR_INVALID_ARG;
+    if (s->K % 8 || s->F % 8 || s->ld_x % 8) return MLA_ERR_ALIGNMENT;
+    return MLA_OK;
+}
+
+}  // namespace
+}  // namespace mlaq
+
+using namespace mlaq;
+
+extern "C" {
+
+MLAQ_API int mla_gated_ffn_fwd(const mla_ffn_shape* shape, const void* x, const void* w_gate_up, const void* w_down,
+                               void* gate_up, void* h, void* y, int* dev_status, void* stream) {
+    int st = check_ffn(shape);
+    if (st != MLA_OK) return st;
+    const mla_ffn_shape& s = *shape;
+    if (s.T > 0 && (!x || !w_gate_up || !w_down || !h || !y)) return MLA_ERR_INVALID_ARG;
+    for (const void* q : {x, w_gate_up, w_down, (const void*)gate_up, (const void*)h, (const void*)y})
+        if (!aligned(q, 16)) return MLA_ERR_ALIGNMENT;
+    if (!aligned(dev_status, 4)) return MLA_ERR_ALIGNMENT;
+    const int64_t ld = s.ld_x ? s.ld_x : s.K;
+    const Range outs[] = {rng(gate_up, s.T * s.F * 4), rng(h, s.T * s.F * 2), rng(y, s.T * s.K * 2), rng(dev_status, 4)};
+    const Range ins[] = {rng(x, s.T ? ((s.T - 1) * ld + s.K) * 2 : 0), rng(w_gate_up, s.F * s.K * 4),
+                         rng(w_down, s.F * s.K * 2)};
+    if (any_alias(outs, ins)) return MLA_ERR_ALIAS;
+    if (s.T == 0) return MLA_OK;
+    DeviceInfo di;
+    st = current_device_info(&di);
+    if (st != MLA_OK) return st;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    GemmParams p{};
+    p.F = (int)s.F;
+    p.act = s.act;
+    p.status = dev_status;
+    p.M = (int)s.T;
+    p.N = (int)s.F;
+    p.out = static_cast<uint16_t*>(h);
+    p.gate_up_out = static_cast<uint16_t*>(gate_up);
+    st = gemm<false, false, kGate>({x, s.T, s.K, ld}, {w_gate_up, 2 * s.F, s.K, s.K}, p, s.K, di, cs);
+    if (st != MLA_OK) return st;
+    p.N = (int)s.K;
+    p.out = static_cast<uint16_t*>(y);
+    return gemm<false, false, kStore>({h, s.T, s.F, s.F}, {w_down, s.K, s.F, s.F}, p, s.F, di, cs);
+}
+
+MLAQ_API int mla_gated_ffn_bwd(const mla_ffn_shape* shape, const void* dy, const void* x, const void* w_gate_up,
+                               const void* w_down, const void* gate_up, const void* h, void* dgate_up, void* dx,
+                               void* dw_gate_up, void* dw_down, int* dev_status, void* stream) {
+    int st = check_ffn(shape);
+    if (st != MLA_OK) return st;
+    const mla_ffn_shape& s = *shape;
+    const bool hidden = dx || dw_gate_up;  // the gradients that go through the activation
+    if (!dx && !dw_gate_up && !dw_down) return MLA_ERR_INVALID_ARG;
+    if (s.T > 0) {
+        if (!dy || (hidden && (!w_down || !gate_up || !dgate_up)) || (dx && !w_gate_up) || (dw_gate_up && !x) ||
+            (dw_down && !h))
+            return MLA_ERR_INVALID_ARG;
+    }
+    for (const void* q : {dy, x, w_gate_up, w_down, gate_up, h, (const void*)dgate_up, (const void*)dx,
+                          (const void*)dw_gate_up, (const void*)dw_down})
+        if (!aligned(q, 16)) return MLA_ERR_ALIGNMENT;
+    if (!aligned(dev_status, 4)) return MLA_ERR_ALIGNMENT;
+    const int64_t ld = s.ld_x ? s.ld_x : s.K;
+    const Range outs[] = {rng(dgate_up, s.T * s.F * 4), rng(dx, s.T * s.K * 2), rng(dw_gate_up, s.F * s.K * 4),
+                          rng(dw_down, s.F * s.K * 2), rng(dev_status, 4)};
+    const Range ins[] = {rng(dy, s.T * s.K * 2), rng(x, s.T ? ((s.T - 1) * ld + s.K) * 2 : 0),
+                         rng(w_gate_up, s.F * s.K * 4), rng(w_down, s.F * s.K * 2), rng(gate_up, s.T * s.F * 4),
+                         rng(h, s.T * s.F * 2)};
+    if (any_alias(outs, ins)) return MLA_ERR_ALIAS;
+    DeviceInfo di;
+    st = current_device_info(&di);
+    if (st != MLA_OK) return st;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (s.T == 0) {  // empty sums: the weights' gradients are zero
+        if (dw_gate_up && cudaMemsetAsync(dw_gate_up, 0, (size_t)(s.F * s.K * 4), cs) != cudaSuccess) return MLA_ERR_CUDA;
+        if (dw_down && cudaMemsetAsync(dw_down, 0, (size_t)(s.F * s.K * 2), cs) != cudaSuccess) return MLA_ERR_CUDA;
+        return MLA_OK;
+    }
+    GemmParams p{};
+    p.F = (int)s.F;
+    p.act = s.act;
+    p.status = dev_status;
+    if (hidden) {
+        p.M = (int)s.T;
+        p.N = (int)s.F;
+        p.out = static_cast<uint16_t*>(dgate_up);
+        p.gate_up = static_cast<const uint16_t*>(gate_up);
+        st = gemm<false, true, kGateGrad>({dy, s.T, s.K, s.K}, {w_down, s.K, s.F, s.F}, p, s.K, di, cs);
+        if (st != MLA_OK) return st;
+    }
+    if (dx) {
+        p.M = (int)s.T;
+        p.N = (int)s.K;
+        p.out = static_cast<uint16_t*>(dx);
+        st = gemm<false, true, kStore>({dgate_up, s.T, 2 * s.F, 2 * s.F}, {w_gate_up, 2 * s.F, s.K, s.K}, p, 2 * s.F, di,
+                                       cs);
+        if (st != MLA_OK) return st;
+    }
+    if (dw_gate_up) {
+        p.M = (int)(2 * s.F);
+        p.N = (int)s.K;
+        p.out = static_cast<uint16_t*>(dw_gate_up);
+        st = gemm<true, true, kStore>({dgate_up, s.T, 2 * s.F, 2 * s.F}, {x, s.T, s.K, ld}, p, s.T, di, cs);
+        if (st != MLA_OK) return st;
+    }
+    if (dw_down) {
+        p.M = (int)s.K;
+        p.N = (int)s.F;
+        p.out = static_cast<uint16_t*>(dw_down);
+        st = gemm<true, true, kStore>({dy, s.T, s.K, s.K}, {h, s.T, s.F, s.F}, p, s.T, di, cs);
+        if (st != MLA_OK) return st;
+    }
+    return MLA_OK;
+}
+
+}  // extern "C"
