@@ -147,8 +147,9 @@ def _ptr(t):
 
 
 def _stream(device, stream):
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
+    if stream is None:  # the handle alone: building a Stream object costs 2 us a call
+        index = device.index
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -158,7 +159,7 @@ def _need(t, name, dtype, device=None, ndim=None, shape=None, numel=None, min_nu
     size first, then device and layout."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")

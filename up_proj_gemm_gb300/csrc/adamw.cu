@@ -135,57 +135,150 @@ __device__ __forceinline__ void store_n(E* p, int n, const float (&v)[N]) {
     }
 }
 
-// The moments and the parameter of one element; r: the root of v'.
-template <bool EXACT_ROOT>
-__device__ __forceinline__ void update(const StepParams& q, float g, float& p, float& m, float& v, float& r) {
-    p = __fmul_rn(p, q.decay);
-    m = __fadd_rn(__fmul_rn(m, q.b1), __fmul_rn(g, q.ob1));
-    v = __fadd_rn(__fmul_rn(v, q.b2), __fmul_rn(__fmul_rn(g, q.ob2), g));
-    // the stored root is rounded once; one that only feeds the step may be off by an ulp
-    if constexpr (EXACT_ROOT) r = __fsqrt_rn(v);
-    else asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
-    p = __fsub_rn(p, __fmul_rn(__fdividef(m, __fadd_rn(__fmul_rn(r, q.root), q.eps)), q.size));
+// Two float32 values in one register pair: the packed instructions round
+// each half as the scalar ones do, at half the issue slots.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// A product that stays rounded where it feeds an addition: the compiler
+// contracts the packed forms into one rounding.
+__device__ __forceinline__ f32x2 mul2_rounded(f32x2 a, f32x2 b) {
+    float a0, a1, b0, b1;
+    unpack2(a, a0, a1);
+    unpack2(b, b0, b1);
+    return pack2(__fmul_rn(a0, b0), __fmul_rn(a1, b1));
+}
+__device__ __forceinline__ f32x2 both(float v) { return pack2(v, v); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
-// bf16 parameters rounded up or down at random, by the low 16 bits.
-__device__ __forceinline__ float bf16_random(float p, uint32_t mixed) {
-    const uint32_t bits = __float_as_uint(p);
-    if ((bits & 0x7F800000u) == 0x7F800000u) return p;
-    return __uint_as_float((bits + ((mixed * 0x3C6EF373u) >> 16)) & 0xFFFF0000u);
+// Roots of two values >= 0 (or NaN), within an ulp: a reciprocal root y of 2
+// ulp, r = v y, and one Heron correction r + (v - r^2) y / 2, whose residual
+// is exact by fused arithmetic. Values below 2^-126 count as 2^-126 for y
+// (their root then comes out at most as large as it is, and a zero's is 0);
+// an infinite v, of gradients above 10^19, counts as the largest float32.
+__device__ __forceinline__ f32x2 root2(f32x2 v) {
+    float v0, v1, y0, y1;
+    unpack2(v, v0, v1);
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(v0) : "f"(3.402823466e38f));
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(v1) : "f"(3.402823466e38f));
+    y0 = max_nan(v0, 1.17549435e-38f);
+    y1 = max_nan(v1, 1.17549435e-38f);
+    asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(y0));
+    asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(y1));
+    v = pack2(v0, v1);
+    const f32x2 y = pack2(y0, y1), r = mul2(v, y);
+    const f32x2 left = fma2(mul2(r, both(-1.f)), r, v);
+    return fma2(left, mul2(y, both(0.5f)), r);
+}
+// The moments and the parameters of two elements; v is v' on return, r its
+// root.
+__device__ __forceinline__ void update2(const StepParams& q, f32x2 g, f32x2& p, f32x2& m, f32x2& v, f32x2& r) {
+    p = mul2(p, both(q.decay));
+    m = add2(mul2_rounded(m, both(q.b1)), mul2_rounded(g, both(q.ob1)));
+    v = add2(mul2_rounded(v, both(q.b2)), mul2_rounded(mul2(g, both(q.ob2)), g));
+    r = root2(v);
+    float d0, d1;
+    unpack2(fma2(r, both(q.root), both(q.eps)), d0, d1);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d0));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d1));
+    p = fma2(mul2(m, pack2(d0, d1)), both(-q.size), p);
 }
 
-// N elements of a tensor from idx on, moments in float32.
+// N elements at once (an odd one is paired with itself).
+template <int N>
+__device__ __forceinline__ void update(const StepParams& q, float gs, const float (&g)[N], float (&p)[N], float (&m)[N],
+                                       float (&v)[N], float (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const int j = i + 1 < N ? i + 1 : i;
+        f32x2 pp = pack2(p[i], p[j]), mm = pack2(m[i], m[j]), vv = pack2(v[i], v[j]), rr;
+        update2(q, mul2(pack2(g[i], g[j]), both(gs)), pp, mm, vv, rr);
+        unpack2(pp, p[i], p[j]);
+        unpack2(mm, m[i], m[j]);
+        unpack2(vv, v[i], v[j]);
+        unpack2(rr, r[i], r[j]);
+    }
+}
+
+// The bits of a bf16 parameter rounded up or down at random, in the upper
+// half of the word (a NaN's bits must not carry into the sign).
+__device__ __forceinline__ uint32_t bf16_random(float p, uint32_t mixed) {
+    const uint32_t up = (mixed * 0x3C6EF373u) >> 16;
+    return __float_as_uint(p) + (p == p ? up : 0u);
+}
+
+// N parameters of a bf16 tensor rounded at random and stored.
+template <int N, bool VEC>
+__device__ __forceinline__ void store_random(uint16_t* p, int n, const float (&v)[N], const uint32_t (&mixed)[N]) {
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<uint2*>(p + i) =
+                make_uint2(__byte_perm(bf16_random(v[i], mixed[i]), bf16_random(v[i + 1], mixed[i + 1]), 0x7632),
+                           __byte_perm(bf16_random(v[i + 2], mixed[i + 2]), bf16_random(v[i + 3], mixed[i + 3]), 0x7632));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) p[i] = (uint16_t)(bf16_random(v[i], mixed[i]) >> 16);
+    }
+}
+
+// N elements of a tensor from idx on (n of them exist), moments in float32.
 template <int N, bool VEC, typename P, typename G>
-__device__ __forceinline__ void step_f32(const StepParams& q, const PlanTensor& T, float gs, int64_t idx, int n) {
-    P* param = static_cast<P*>(T.t.param) + idx;
-    float* em = static_cast<float*>(T.t.exp_avg) + idx;
-    float* ev = static_cast<float*>(T.t.exp_avg_sq) + idx;
-    float* ma = T.t.master ? T.t.master + idx : nullptr;
+struct GroupF32 {
     float g[N], p[N], m[N], v[N];
-    load_n<N, VEC>(static_cast<const G*>(T.t.grad) + idx, n, g);
-    load_n<N, VEC>(em, n, m);
-    load_n<N, VEC>(ev, n, v);
-    if (ma) load_n<N, VEC>(ma, n, p);
-    else load_n<N, VEC>(param, n, p);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float r;
-        update<false>(q, __fmul_rn(g[i], gs), p[i], m[i], v[i], r);
+
+    __device__ __forceinline__ void load(const PlanTensor& T, int64_t idx, int n) {
+        load_n<N, VEC>(static_cast<const G*>(T.t.grad) + idx, n, g);
+        load_n<N, VEC>(static_cast<const float*>(T.t.exp_avg) + idx, n, m);
+        load_n<N, VEC>(static_cast<const float*>(T.t.exp_avg_sq) + idx, n, v);
+        if (T.t.master) load_n<N, VEC>(T.t.master + idx, n, p);
+        else load_n<N, VEC>(static_cast<const P*>(T.t.param) + idx, n, p);
     }
-    store_n<N, VEC>(em, n, m);
-    store_n<N, VEC>(ev, n, v);
-    if (ma) store_n<N, VEC>(ma, n, p);
-    else if (sizeof(P) == 2 && q.stochastic) {
+    __device__ __forceinline__ void step(const StepParams& q, const PlanTensor& T, float gs, int64_t idx, int n) {
+        float r[N];
+        update<N>(q, gs, g, p, m, v, r);
+        store_n<N, VEC>(static_cast<float*>(T.t.exp_avg) + idx, n, m);
+        store_n<N, VEC>(static_cast<float*>(T.t.exp_avg_sq) + idx, n, v);
+        P* param = static_cast<P*>(T.t.param) + idx;
+        if (T.t.master) store_n<N, VEC>(T.t.master + idx, n, p);
+        if constexpr (sizeof(P) == 2) {
+            if (!T.t.master && q.stochastic) {
+                uint32_t mixed[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) p[i] = bf16_random(p[i], mix32((uint32_t)(T.place + idx + i), q.seed));
+                for (int i = 0; i < N; ++i) mixed[i] = mix32((uint32_t)(T.place + idx + i), q.seed);
+                store_random<N, VEC>(param, n, p, mixed);
+                return;
+            }
+        }
+        store_n<N, VEC>(param, n, p);
     }
-    store_n<N, VEC>(param, n, p);
-}
+};
 
 template <typename P, typename G>
 __global__ void __launch_bounds__(kThreads) adamw_f32_kernel(const StepParams q) {
     const PlanChunk c = q.chunks[blockIdx.x];
-    const PlanTensor& T = q.tensors[c.tensor];
+    const PlanTensor T = q.tensors[c.tensor];
     const float gs = q.grad_scale ? __ldg(q.grad_scale) : 1.f;
     const int64_t base = (int64_t)c.number * kChunk;
     const int64_t left = T.t.n - base;
@@ -197,50 +290,88 @@ __global__ void __launch_bounds__(kThreads) adamw_f32_kernel(const StepParams q)
                          (reinterpret_cast<uintptr_t>(T.t.grad) * (4 / sizeof(G)));
     const bool vec = (at & 15) == 0;
     const int whole = vec ? n & ~3 : 0;
-    for (int i = threadIdx.x * 4; i < whole; i += kThreads * 4) step_f32<4, true, P, G>(q, T, gs, base + i, 4);
-    for (int i = whole + threadIdx.x; i < n; i += kThreads) step_f32<1, false, P, G>(q, T, gs, base + i, 1);
-}
-
-// 8 code bytes at 16 random bits each: E4M3 of v * 2^-e, rounded up where
-// the 20-bit fraction below its 3 mantissa bits is above rnd * 2^-16. Values
-// below the smallest normal, 2^-6, are moved into its octave, where the
-// step is the same; adding upwards keeps "fraction above rnd" exact.
-__device__ __forceinline__ uint32_t e4m3_random(float v, float scale, uint32_t rnd) {
-    const float s = fabsf(v) * scale;
-    const bool sub = s < 0.015625f;
-    const float t = sub ? __fadd_ru(s, 0.015625f) : s;
-    const uint32_t code = ((__float_as_uint(t) + 0xFFFFFu - (rnd << 4)) >> 20) - (sub ? 968u : 960u);
-    return code | ((__float_as_uint(v) >> 24) & 0x80u);
-}
-
-// 8 of a block's 32 values (the other 24 in three neighbouring lanes).
-template <bool ROOT>
-__device__ __forceinline__ uint32_t encode8(const StepParams& q, const float (&v)[8], const uint32_t (&mixed)[8],
-                                            uint32_t (&codes)[2]) {
-    float am = 0.f;
+    for (int i = threadIdx.x * 4; i < whole; i += kThreads * 8) {  // two groups in flight
+        const int j = i + kThreads * 4;
+        GroupF32<4, true, P, G> a, b;
+        a.load(T, base + i, 4);
+        if (j < whole) b.load(T, base + j, 4);
+        a.step(q, T, gs, base + i, 4);
+        if (j < whole) b.step(q, T, gs, base + j, 4);
+    }
+    for (int i = whole + threadIdx.x; i < n; i += 4 * kThreads) {  // the rest one by one, four in flight
+        GroupF32<1, false, P, G> a[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) am = amax_nan(am, v[i]);
+        for (int u = 0; u < 4; ++u)
+            if (i + u * kThreads < n) a[u].load(T, base + i + u * kThreads, 1);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (i + u * kThreads < n) a[u].step(q, T, gs, base + i + u * kThreads, 1);
+    }
+}
+
+constexpr int kLeastExponent = -120;  // 2^(e-6) is a normal float32 from here on
+
+// E4M3 codes of 8 values * 2^-e, each rounded up where the 20-bit fraction
+// below its 3 mantissa bits is above rnd * 2^-16 (rnd: the upper 16 random
+// bits, or the lower for ROOT). On the float32 bits of |v| that is one
+// integer addition: bits + (0xFFFFF - rnd * 16) carries into bit 20 exactly
+// then, and bits 20.. less (e + 120) * 8 are the code. Values below the
+// smallest normal, 2^(e-6), are moved into its octave, where the step is the
+// same, and 8 codes back; adding upwards keeps "fraction above rnd" exact. That
+// form is the larger one below 2^(e-6) and the smaller one above it, so the
+// maximum of both picks the right one.
+template <bool ROOT>
+__device__ __forceinline__ void codes_random(const float (&v)[8], int e, const uint32_t (&mixed)[8],
+                                             uint32_t (&codes)[2]) {
+    const float least = __uint_as_float((uint32_t)(e + 121) << 23);  // 2^(e-6), e >= kLeastExponent
+    const int base = -((e + 120) * 8 << 20);
+    uint32_t top[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float a = ROOT ? v[i] : fabsf(v[i]);
+        const int up = (int)(((ROOT ? mixed[i] << 4 : mixed[i] >> 12) & 0xFFFF0u) ^ 0xFFFFFu);
+        int bits = __viaddmax_s32(__float_as_int(__fadd_ru(a, least)), -(8 << 20), __float_as_int(a)) + up + base;
+        if constexpr (ROOT) {  // a root above zero keeps a code above zero (its bits are at least 2^20 then)
+            bits = max(bits, min(__float_as_int(a), 1 << 20));
+            top[i] = (uint32_t)bits << 4;
+        } else {
+            top[i] = (((uint32_t)bits << 4) & 0x7FFFFFFFu) | (__float_as_uint(v[i]) & 0x80000000u);
+        }
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w)  // the top bytes of four words
+        codes[w] = __byte_perm(__byte_perm(top[4 * w], top[4 * w + 1], 0x0073),
+                               __byte_perm(top[4 * w + 2], top[4 * w + 3], 0x0073), 0x5410);
+}
+
+// The largest of three magnitudes, NaN when one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// 8 of a block's 32 values (the other 24 in three neighbouring lanes); v may
+// be scaled on return.
+template <bool ROOT>
+__device__ __forceinline__ uint32_t encode8(const StepParams& q, float (&v)[8], const uint32_t (&mixed)[8],
+                                            uint32_t (&codes)[2]) {
+    float am = max3_nan(max3_nan(v[0], v[1], v[2]), max3_nan(v[3], v[4], v[5]), amax_nan(fabsf(v[6]), v[7]));
     am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, 1));
     am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, 2));
     const uint32_t bits = __float_as_uint(am);
-    uint32_t sf;
-    if (!q.stochastic || bits >= 0x7F800000u) {
-        sf = quantize8_block_scale(v, bits, codes);
-    } else {
+    if (q.stochastic && bits < 0x7F800000u) {
         const int e = e8m0_exponent_f32(am);
-        const float scale = exp2_neg(e);
+        int left = e;  // what the codes still have to be scaled by
+        if (e < kLeastExponent) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            uint32_t c = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t x = mixed[4 * w + j];
-                c |= e4m3_random(v[4 * w + j], scale, ROOT ? x & 0xFFFFu : x >> 16) << (8 * j);
-            }
-            codes[w] = c;
+            for (int i = 0; i < 8; ++i) v[i] *= exp2_neg(e);
+            left = 0;
         }
-        sf = (uint32_t)(e + 127);
+        codes_random<ROOT>(v, left, mixed, codes);
+        return (uint32_t)(e + 127);
     }
+    const uint32_t sf = quantize8_block_scale(v, bits, codes);
     if constexpr (ROOT) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -264,20 +395,6 @@ __device__ __forceinline__ void e4m3x2_to_f32(uint32_t two, float& a, float& b) 
 }
 
 template <bool VEC>
-__device__ __forceinline__ void load_codes(const uint8_t* p, int n, uint32_t (&c)[2]) {
-    if constexpr (VEC) {
-        const uint2 w = *reinterpret_cast<const uint2*>(p);
-        c[0] = w.x;
-        c[1] = w.y;
-    } else {
-        c[0] = c[1] = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) c[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
-    }
-}
-
-template <bool VEC>
 __device__ __forceinline__ void store_codes(uint8_t* p, int n, const uint32_t (&c)[2]) {
     if constexpr (VEC) {
         *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[1]);
@@ -297,60 +414,141 @@ __device__ __forceinline__ void decode8(const uint32_t (&c)[2], float scale, flo
     }
 }
 
-// 8 elements of a tensor from idx on (n of them exist), moments in MXFP8.
-// All lanes of a warp take part (the block scales are shared by shuffles).
-template <bool VEC, typename P, typename G>
-__device__ __forceinline__ void step_mx(const StepParams& q, const PlanTensor& T, float gs, int64_t idx, int n) {
-    P* param = static_cast<P*>(T.t.param) + idx;
-    uint8_t* em = static_cast<uint8_t*>(T.t.exp_avg) + idx;
-    uint8_t* ev = static_cast<uint8_t*>(T.t.exp_avg_sq) + idx;
-    float* ma = T.t.master ? T.t.master + idx : nullptr;
-    float g[8], p[8], m[8], r[8];
-    uint32_t cm[2], cv[2], mixed[8];
-    uint32_t sm = 0, sv = 0;
-    if (VEC || n > 0) {
-        sm = T.t.exp_avg_scales[idx >> 5];
-        sv = T.t.exp_avg_sq_scales[idx >> 5];
-    }
-    load_n<8, VEC>(static_cast<const G*>(T.t.grad) + idx, n, g);
-    load_codes<VEC>(em, n, cm);
-    load_codes<VEC>(ev, n, cv);
-    if (ma) load_n<8, VEC>(ma, n, p);
-    else load_n<8, VEC>(param, n, p);
-    decode8(cm, e8m0_value(sm), m);
-    decode8(cv, e8m0_value(sv), r);
-    const uint32_t place = (uint32_t)(T.place + idx);
+// Words of memory at p: NW of them, or the n bytes that exist.
+template <int NW, bool VEC>
+__device__ __forceinline__ void load_words(const void* p, int n, uint32_t (&w)[NW]) {
+    if constexpr (VEC) {
+        if constexpr (NW == 2) {
+            const uint2 v = *static_cast<const uint2*>(p);
+            w[0] = v.x;
+            w[1] = v.y;
+        } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float v = __fmul_rn(r[i], r[i]);
-        update<true>(q, __fmul_rn(g[i], gs), p[i], m[i], v, r[i]);
-        mixed[i] = q.stochastic ? mix32(place + i, q.seed) : 0;
-    }
-    // the partial group of a tensor's end: elements past it count for nothing in the block's scale
-    if constexpr (!VEC) {
+            for (int i = 0; i < NW; i += 4) {
+                const uint4 v = static_cast<const uint4*>(p)[i / 4];
+                w[i] = v.x;
+                w[i + 1] = v.y;
+                w[i + 2] = v.z;
+                w[i + 3] = v.w;
+            }
+        }
+    } else if constexpr (NW == 8) {  // float32
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = i < n ? static_cast<const uint32_t*>(p)[i] : 0u;
+    } else if constexpr (NW == 4) {  // bf16
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = 2 * i < n ? static_cast<const uint16_t*>(p)[2 * i] : 0u;
+            if (2 * i + 1 < n) w[i] |= (uint32_t)static_cast<const uint16_t*>(p)[2 * i + 1] << 16;
+        }
+    } else {  // codes
+        w[0] = w[1] = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i >= n) m[i] = r[i] = 0.f;
+            if (i < n) w[i / 4] |= (uint32_t)static_cast<const uint8_t*>(p)[i] << (8 * (i % 4));
     }
-    sm = encode8<false>(q, m, mixed, cm);
-    sv = encode8<true>(q, r, mixed, cv);
-    if (!VEC && n <= 0) return;
-    store_codes<VEC>(em, n, cm);
-    store_codes<VEC>(ev, n, cv);
-    if ((idx & 31) == 0) {
-        T.t.exp_avg_scales[idx >> 5] = (uint8_t)sm;
-        T.t.exp_avg_sq_scales[idx >> 5] = (uint8_t)sv;
-    }
-    if (ma) store_n<8, VEC>(ma, n, p);
-    else if (sizeof(P) == 2 && q.stochastic) {
+}
+
+template <int NW>
+__device__ __forceinline__ void to_float(const uint32_t (&w)[NW], float (&v)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = bf16_random(p[i], mixed[i]);
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (NW == 8) v[i] = __uint_as_float(w[i]);
+        else v[i] = i & 1 ? bf16hi_to_f32(w[i / 2]) : bf16lo_to_f32(w[i / 2]);
     }
-    store_n<8, VEC>(param, n, p);
+}
+
+// 8 elements of a tensor from idx on (n of them exist), moments in MXFP8, as
+// they lie in memory. All lanes of a warp step together (the block scales
+// are shared by shuffles). MASTER: the parameter is read from its master.
+template <bool MASTER, typename P, typename G>
+struct GroupMx {
+    uint32_t g[2 * sizeof(G)], p[MASTER ? 8 : 2 * sizeof(P)], cm[2], cv[2], sm, sv;
+
+    template <bool VEC>
+    __device__ __forceinline__ void load(const PlanTensor& T, int64_t idx, int n) {
+        sm = sv = 0;
+        if (VEC || n > 0) {
+            sm = T.t.exp_avg_scales[idx >> 5];
+            sv = T.t.exp_avg_sq_scales[idx >> 5];
+        }
+        load_words<2 * sizeof(G), VEC>(static_cast<const G*>(T.t.grad) + idx, n, g);
+        load_words<2, VEC>(static_cast<const uint8_t*>(T.t.exp_avg) + idx, n, cm);
+        load_words<2, VEC>(static_cast<const uint8_t*>(T.t.exp_avg_sq) + idx, n, cv);
+        if constexpr (MASTER) load_words<8, VEC>(T.t.master + idx, n, p);
+        else load_words<2 * sizeof(P), VEC>(static_cast<const P*>(T.t.param) + idx, n, p);
+    }
+
+    template <bool VEC>
+    __device__ __forceinline__ void step(const StepParams& q, const PlanTensor& T, float gs, int64_t idx, int n) {
+        float gf[8], pf[8], m[8], v[8], r[8];
+        uint32_t mixed[8];
+        to_float(g, gf);
+        to_float(p, pf);
+        decode8(cm, e8m0_value(sm), m);
+        decode8(cv, e8m0_value(sv), r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(r[i], r[i]);
+        update<8>(q, gs, gf, pf, m, v, r);
+        const uint32_t place = (uint32_t)(T.place + idx);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mixed[i] = q.stochastic ? mix32(place + i, q.seed) : 0;
+        // the partial group of a tensor's end: elements past it count for nothing in the block's scale
+        if constexpr (!VEC) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i >= n) m[i] = r[i] = 0.f;
+        }
+        const uint32_t em = encode8<false>(q, m, mixed, cm);
+        const uint32_t ev = encode8<true>(q, r, mixed, cv);
+        if (!VEC && n <= 0) return;
+        store_codes<VEC>(static_cast<uint8_t*>(T.t.exp_avg) + idx, n, cm);
+        store_codes<VEC>(static_cast<uint8_t*>(T.t.exp_avg_sq) + idx, n, cv);
+        if ((idx & 31) == 0) {
+            T.t.exp_avg_scales[idx >> 5] = (uint8_t)em;
+            T.t.exp_avg_sq_scales[idx >> 5] = (uint8_t)ev;
+        }
+        P* param = static_cast<P*>(T.t.param) + idx;
+        if constexpr (MASTER) store_n<8, VEC>(T.t.master + idx, n, pf);
+        if constexpr (sizeof(P) == 2 && !MASTER) {
+            if (q.stochastic) {
+                store_random<8, VEC>(param, n, pf, mixed);
+                return;
+            }
+        }
+        store_n<8, VEC>(param, n, pf);
+    }
+};
+
+// Whole warps walk the chunk 256 elements at a time; a warp whose 256 elements
+// all exist takes the wide path, where the next group's loads are in flight
+// while this one is computed.
+template <bool MASTER, typename P, typename G>
+__device__ __forceinline__ void walk_mx(const StepParams& q, const PlanTensor& T, float gs, int64_t base, int n, bool vec) {
+    const int lane8 = (int)(threadIdx.x & 31) * 8;
+    int i = threadIdx.x * 8;
+    GroupMx<MASTER, P, G> cur, next;
+    if (vec && i - lane8 + 256 <= n) {
+        cur.template load<true>(T, base + i, 8);
+        for (;;) {
+            const int j = i + kThreads * 8;
+            const bool more = j - lane8 + 256 <= n;
+            if (more) next.template load<true>(T, base + j, 8);
+            cur.template step<true>(q, T, gs, base + i, 8);
+            i = j;
+            if (!more) break;
+            cur = next;
+        }
+    }
+    for (; i - lane8 < n; i += kThreads * 8) {
+        const int k = n - i < 0 ? 0 : (n - i > 8 ? 8 : n - i);
+        cur.template load<false>(T, base + i, k);
+        cur.template step<false>(q, T, gs, base + i, k);
+    }
 }
 
 template <typename P, typename G>
-__global__ void __launch_bounds__(kThreads) adamw_mx_kernel(const StepParams q) {
+__global__ void __launch_bounds__(kThreads, 4) adamw_mx_kernel(const StepParams q) {
     const PlanChunk c = q.chunks[blockIdx.x];
     const PlanTensor& T = q.tensors[c.tensor];
     const float gs = q.grad_scale ? __ldg(q.grad_scale) : 1.f;
@@ -361,13 +559,8 @@ __global__ void __launch_bounds__(kThreads) adamw_mx_kernel(const StepParams q) 
                          reinterpret_cast<uintptr_t>(T.t.grad) | (reinterpret_cast<uintptr_t>(T.t.exp_avg) * 2) |
                          (reinterpret_cast<uintptr_t>(T.t.exp_avg_sq) * 2);
     const bool vec = (at & 15) == 0;
-    // whole warps walk the chunk 256 elements at a time; a warp whose 256
-    // elements all exist takes the wide path
-    for (int i = threadIdx.x * 8; i - (int)(threadIdx.x & 31) * 8 < n; i += kThreads * 8) {
-        const int w0 = i - (int)(threadIdx.x & 31) * 8;
-        if (vec && w0 + 256 <= n) step_mx<true, P, G>(q, T, gs, base + i, 8);
-        else step_mx<false, P, G>(q, T, gs, base + i, n - i < 0 ? 0 : (n - i > 8 ? 8 : n - i));
-    }
+    if (T.t.master) walk_mx<true, P, G>(q, T, gs, base, n, vec);
+    else walk_mx<false, P, G>(q, T, gs, base, n, vec);
 }
 
 template <typename P, typename G>

@@ -25,7 +25,11 @@ namespace mlaq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;        // rows in flight per thread
+constexpr int kUnroll = 2;        // rows in flight per thread (two vectors each)
+constexpr int kRowBlocks = 4;     // resident blocks per SM: with kUnroll, 64 KB of loads in flight
+constexpr int kRunRows = 8;       // rows per thread at most
+constexpr int kFill = 4;          // table entries in flight per thread
+constexpr int kTableBytes = 16384;  // the gathered entries of a block's tokens at most
 constexpr int kMaxPairs = 128;    // Dr <= 256
 constexpr int64_t kMaxD = 8192;   // the sum kernel's shared sums: at most 32 KB
 
@@ -46,237 +50,266 @@ struct RopeParams {
     uint8_t axis[kMaxPairs];
 };
 
-template <typename E>
-struct Elem;
-template <>
-struct Elem<float> {
-    static __device__ float up(float v) { return v; }
-    static __device__ float down(float v) { return v; }
-};
-template <>
-struct Elem<uint16_t> {
-    static __device__ float up(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-    static __device__ uint16_t down(float v) { return (uint16_t)pack_bf16x2(v, 0.f); }
-};
-
-// VE elements at p (16 bytes together when VE > 1) as float32.
+// VE elements in 32-bit registers as they lie in memory (16 bytes when VE > 1).
 template <typename E, int VE>
-__device__ __forceinline__ void load_vec(const E* p, float (&v)[VE]) {
-    if constexpr (VE == 1) {
-        v[0] = Elem<E>::up(*p);
-    } else {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (VE == 4) {
-                v[i] = __uint_as_float(u[i]);
-            } else {
-                v[2 * i] = bf16lo_to_f32(u[i]);
-                v[2 * i + 1] = bf16hi_to_f32(u[i]);
-            }
+struct Raw {
+    uint32_t u[VE == 1 ? 1 : 4];
+
+    __device__ __forceinline__ void load(const E* p) {
+        if constexpr (VE == 1) {
+            if constexpr (sizeof(E) == 2) u[0] = __ldg(p);
+            else u[0] = __float_as_uint(__ldg(p));
+        } else {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+            u[0] = w.x;
+            u[1] = w.y;
+            u[2] = w.z;
+            u[3] = w.w;
         }
     }
-}
-
-template <typename E, int VE>
-__device__ __forceinline__ void store_vec(E* p, const float (&v)[VE]) {
-    if constexpr (VE == 1) {
-        *p = Elem<E>::down(v[0]);
-    } else if constexpr (VE == 4) {
-        st_global_v4(p, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-    } else {
-        st_global_v4(p, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                     pack_bf16x2(v[6], v[7]));
+    __device__ __forceinline__ void store(E* p) const {
+        if constexpr (VE == 1) {
+            if constexpr (sizeof(E) == 2) *p = (uint16_t)u[0];
+            else *p = __uint_as_float(u[0]);
+        } else {
+            st_global_v4(p, u[0], u[1], u[2], u[3]);
+        }
     }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(E) == 4) return __uint_as_float(u[i]);
+        else return i & 1 ? bf16hi_to_f32(u[i / 2]) : bf16lo_to_f32(u[i / 2]);
+    }
+    __device__ __forceinline__ void set(const float (&v)[VE]) {
+        if constexpr (sizeof(E) == 4) {
+#pragma unroll
+            for (int i = 0; i < VE; ++i) u[i] = __float_as_uint(v[i]);
+        } else if constexpr (VE == 1) {
+            u[0] = pack_bf16x2(v[0], 0.f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        }
+    }
+};
+
+// The position of token t on the axis of rope channel j (j < Dr).
+__device__ __forceinline__ int64_t position(const RopeParams& p, int j, int64_t t) {
+    const int half = p.Dr / 2;
+    return __ldg(p.pos + p.axis[j < half ? j : j - half] * p.T + t);
+}
+__device__ __forceinline__ bool in_table(const RopeParams& p, int64_t row) { return row >= 0 && row < p.cs_rows; }
+
+// The same, checked: -1 and a report when it lies outside the table.
+__device__ __forceinline__ int64_t table_row(const RopeParams& p, int j, int64_t t) {
+    const int64_t row = position(p, j, t);
+    if (in_table(p, row)) return row;
+    record_status(p.status, MLA_ERR_POS_RANGE);
+    return -1;
 }
 
-// The table entries of the VE pairs from i0 on, for token t: c0/s0 of the
-// low channels, c1/s1 of the high ones. A position outside the table is
-// reported and its entries are 0.
+// VE floats of shared memory (by 16 bytes when VE > 1).
 template <int VE>
-struct Turn {
-    float c0[VE], s0[VE], c1[VE], s1[VE];
-
-    __device__ __forceinline__ void load(const RopeParams& p, int i0, bool one_axis, int64_t t) {
-        const int h = p.Dr / 2;
-        if (VE > 1 && one_axis && p.cs_vec) {  // the pairs share an axis, so a row: read it by float4
-            const int64_t row = __ldg(p.pos + p.axis[i0] * p.T + t);
-            const bool ok = row >= 0 && row < p.cs_rows;
-            if (!ok) record_status(p.status, MLA_ERR_POS_RANGE);
-            const int64_t at = (ok ? row : 0) * p.cs_width + i0;
+__device__ __forceinline__ void from_table(const float* q, float (&v)[VE]) {
+    if constexpr (VE == 1) {
+        v[0] = *q;
+    } else {
 #pragma unroll
-            for (int k = 0; k + 4 <= VE; k += 4) {
-                four(p.cos_tab + at + k, ok, c0 + k);
-                four(p.sin_tab + at + k, ok, s0 + k);
-                four(p.cos_tab + at + h + k, ok, c1 + k);
-                four(p.sin_tab + at + h + k, ok, s1 + k);
-            }
-            return;
-        }
-#pragma unroll
-        for (int k = 0; k < VE; ++k) {
-            const int64_t row = __ldg(p.pos + p.axis[i0 + k] * p.T + t);
-            const bool ok = row >= 0 && row < p.cs_rows;
-            if (!ok) record_status(p.status, MLA_ERR_POS_RANGE);
-            const int64_t at = (ok ? row : 0) * p.cs_width + i0 + k;
-            c0[k] = ok ? __ldg(p.cos_tab + at) : 0.f;
-            s0[k] = ok ? __ldg(p.sin_tab + at) : 0.f;
-            c1[k] = ok ? __ldg(p.cos_tab + at + h) : 0.f;
-            s1[k] = ok ? __ldg(p.sin_tab + at + h) : 0.f;
+        for (int k = 0; k < VE; k += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(q + k);
+            v[k] = f.x;
+            v[k + 1] = f.y;
+            v[k + 2] = f.z;
+            v[k + 3] = f.w;
         }
     }
-
-    __device__ __forceinline__ void turn(bool inverse, float (&a)[VE], float (&b)[VE]) const {
-#pragma unroll
-        for (int k = 0; k < VE; ++k) {
-            const float x = a[k], y = b[k];
-            a[k] = inverse ? x * c0[k] + y * s1[k] : x * c0[k] - y * s0[k];
-            b[k] = inverse ? y * c1[k] - x * s0[k] : y * c1[k] + x * s1[k];
-        }
-    }
-
-private:
-    static __device__ __forceinline__ void four(const float* q, bool ok, float* d) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(q));
-        d[0] = ok ? f.x : 0.f;
-        d[1] = ok ? f.y : 0.f;
-        d[2] = ok ? f.z : 0.f;
-        d[3] = ok ? f.w : 0.f;
-    }
-};
-
-template <int VE>
-__device__ __forceinline__ bool same_axis(const RopeParams& p, int i0) {
-    bool same = true;
-#pragma unroll
-    for (int k = 1; k < VE; ++k) same &= p.axis[i0 + k] == p.axis[i0];
-    return same;
 }
 
-// apply and inverse. A thread owns one slot of a (token, head) row, two
-// vectors of VE elements: a pair vector (channels i.. and i+h..), or two
-// vectors of the pass-through channels. It walks the rows of its block, four
-// in flight, and reloads the table entries only when the token changes.
+// apply and inverse. A block takes a run of (token, head) rows. It gathers
+// the cos/sin entries of the run's tokens into shared memory once (a thread
+// that kept its own in registers had room for too few loads in flight: 1.7
+// against 5.x TB/s); a thread then owns one slot of a row, two vectors of VE
+// elements: a pair vector (channels i.. and i+h..), or two vectors of the
+// pass-through channels, and walks the rows, kUnroll in flight. The first
+// rows are on their way while the table is gathered.
 template <typename E, int VE>
-__global__ void __launch_bounds__(kThreads) rope_axes_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kRowBlocks) rope_axes_kernel(const __grid_constant__ RopeParams p) {
+    extern __shared__ float4 table4[];  // [token of the run][cos Dr | sin Dr]
+    float* table = reinterpret_cast<float*>(table4);
     const int half = p.Dr / 2;
     const int n_pair = half / VE, n_copy = p.Dn / VE;
     const int n_copy2 = (n_copy + 1) / 2;
     const int slots = n_copy2 + n_pair;
-    const int lanes = kThreads / slots > 0 ? kThreads / slots : 1;  // rows walked side by side
-    const int lane = threadIdx.x / slots;
-    if (lane >= lanes && slots <= kThreads) return;
+    const bool narrow = slots <= kThreads;
+    const int lanes = narrow ? kThreads / slots : 1;  // rows walked side by side
+    const int lane = narrow ? (int)threadIdx.x / slots : 0;
     const int64_t r_begin = (int64_t)blockIdx.x * p.rows_per_block;
     const int64_t r_end = r_begin + p.rows_per_block < p.rows ? r_begin + p.rows_per_block : p.rows;
+    const int t_first = (int)((uint32_t)r_begin / (uint32_t)p.H);
+    const int toks = (int)((uint32_t)(r_end - 1) / (uint32_t)p.H) - t_first + 1;
     const E* in = static_cast<const E*>(p.in);
     E* out = static_cast<E*>(p.out);
-    for (int s = slots <= kThreads ? (int)threadIdx.x - lane * slots : (int)threadIdx.x; s < slots; s += kThreads) {
+    bool filled = false;
+    const int rounds = narrow ? 1 : (slots + kThreads - 1) / kThreads;
+    for (int k0 = 0; k0 < rounds; ++k0) {
+        // threads without a slot only help to fill the table
+        const int s = (int)threadIdx.x - lane * slots + k0 * kThreads;
+        const bool works = s < slots && lane < lanes;
         const bool pair = s >= n_copy2;
         const int i0 = pair ? (s - n_copy2) * VE : 0;
         const int ca = pair ? p.Dn + i0 : s * VE;
         const int cb = pair ? ca + half : (s + n_copy2) * VE;
-        const bool two = pair || s + n_copy2 < n_copy;
-        const bool one_axis = pair && same_axis<VE>(p, i0);
-        int64_t cur = -1;
-        Turn<VE> tab;
-        const int64_t first = r_begin + (slots <= kThreads ? lane : 0);
-        for (int64_t r = first; r < r_end; r += (int64_t)lanes * kUnroll) {
-            float a[kUnroll][VE], b[kUnroll][VE];
-            int64_t t[kUnroll], h[kUnroll];
+        const bool two = works && (pair || s + n_copy2 < n_copy);
+        int64_t r = works ? r_begin + lane : r_end;
+        do {
+            Raw<E, VE> a[kUnroll], b[kUnroll];
+            int t[kUnroll], h[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 const int64_t ru = r + (int64_t)u * lanes;
                 if (ru >= r_end) continue;
-                t[u] = (uint32_t)ru / (uint32_t)p.H;
-                h[u] = (uint32_t)ru - (uint32_t)t[u] * (uint32_t)p.H;
+                t[u] = (int)((uint32_t)ru / (uint32_t)p.H);
+                h[u] = (int)((uint32_t)ru - (uint32_t)t[u] * (uint32_t)p.H);
                 const E* x = in + t[u] * p.in_t + h[u] * p.in_h;
-                load_vec<E, VE>(x + ca, a[u]);
-                if (two) load_vec<E, VE>(x + cb, b[u]);
+                a[u].load(x + ca);
+                if (two) b[u].load(x + cb);
+            }
+            if (!filled) {
+                const int n = toks * p.Dr;
+                for (int i0f = threadIdx.x; i0f < n; i0f += kFill * kThreads) {
+                    int64_t row[kFill];
+                    float cv[kFill], sv[kFill];
+#pragma unroll
+                    for (int q = 0; q < kFill; ++q) {
+                        const int i = i0f + q * kThreads, tt = i / p.Dr;
+                        row[q] = i < n ? position(p, i - tt * p.Dr, t_first + tt) : 0;
+                    }
+#pragma unroll
+                    for (int q = 0; q < kFill; ++q) {
+                        const int i = i0f + q * kThreads, j = i % p.Dr;
+                        const bool ok = i < n && in_table(p, row[q]);
+                        cv[q] = ok ? __ldg(p.cos_tab + row[q] * p.cs_width + j) : 0.f;
+                        sv[q] = ok ? __ldg(p.sin_tab + row[q] * p.cs_width + j) : 0.f;
+                    }
+#pragma unroll
+                    for (int q = 0; q < kFill; ++q) {
+                        const int i = i0f + q * kThreads, tt = i / p.Dr, j = i - tt * p.Dr;
+                        if (i >= n) break;
+                        if (!in_table(p, row[q])) record_status(p.status, MLA_ERR_POS_RANGE);
+                        table[tt * 2 * p.Dr + j] = cv[q];
+                        table[tt * 2 * p.Dr + p.Dr + j] = sv[q];
+                    }
+                }
+                __syncthreads();
+                filled = true;
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 if (r + (int64_t)u * lanes >= r_end) continue;
                 if (pair) {
-                    if (t[u] != cur) {
-                        cur = t[u];
-                        tab.load(p, i0, one_axis, cur);
+                    const float* c = table + (t[u] - t_first) * 2 * p.Dr + i0;
+                    float c0[VE], s0[VE], c1[VE], s1[VE], x[VE], y[VE];
+                    from_table<VE>(c, c0);
+                    from_table<VE>(c + half, c1);
+                    from_table<VE>(c + p.Dr, s0);
+                    from_table<VE>(c + p.Dr + half, s1);
+#pragma unroll
+                    for (int k = 0; k < VE; ++k) {
+                        const float v = a[u].get(k), w = b[u].get(k);
+                        x[k] = p.inverse ? v * c0[k] + w * s1[k] : v * c0[k] - w * s0[k];
+                        y[k] = p.inverse ? w * c1[k] - v * s0[k] : w * c1[k] + v * s1[k];
                     }
-                    tab.turn(p.inverse != 0, a[u], b[u]);
+                    a[u].set(x);
+                    b[u].set(y);
                 }
                 E* o = out + t[u] * p.out_t + h[u] * p.out_h;
-                store_vec<E, VE>(o + ca, a[u]);
-                if (two) store_vec<E, VE>(o + cb, b[u]);
+                a[u].store(o + ca);
+                if (two) b[u].store(o + cb);
             }
-        }
+            r += (int64_t)lanes * kUnroll;
+        } while (r < r_end);
     }
 }
 
-// The sum over heads, turned. A block takes `toks` tokens at a time; a
-// thread adds one vector of VE channels over every hl-th head in float32,
-// the partial sums meet in shared memory and are added in lane order, so the
-// result does not depend on scheduling.
+// The sum over heads, turned. A block takes the tokens whose rows fit side by
+// side; a thread adds one vector of VE channels over every hl-th head in
+// float32, the partial sums meet in shared memory and are added in lane
+// order, so the result does not depend on scheduling. The table entries are
+// fetched before the heads are summed.
 template <typename E, int VE>
 __global__ void __launch_bounds__(kThreads) rope_sum_kernel(const __grid_constant__ RopeParams p) {
     extern __shared__ float part[];  // [lanes][D]
+    constexpr int kHeads = 4;        // heads in flight per thread
     const int D = p.Dn + p.Dr, half = p.Dr / 2;
     const int slots = D / VE;
-    const int lanes = kThreads / slots > 0 ? kThreads / slots : 1;
+    const bool narrow = slots <= kThreads;
+    const int lanes = narrow ? kThreads / slots : 1;
     const int hl = p.H < lanes ? p.H : lanes;  // threads over the heads of one token
     const int toks = lanes / hl;               // tokens side by side
-    const int lane = slots <= kThreads ? (int)threadIdx.x / slots : 0;
+    const int lane = narrow ? (int)threadIdx.x / slots : 0;
     const E* in = static_cast<const E*>(p.in);
     E* out = static_cast<E*>(p.out);
-    for (int64_t t0 = (int64_t)blockIdx.x * toks; t0 < p.T; t0 += (int64_t)gridDim.x * toks) {
-        const int tl = lane / hl, h0 = lane - tl * hl;
-        if (tl < toks && t0 + tl < p.T) {
-            const E* x = in + (t0 + tl) * p.in_t;
-            for (int s = slots <= kThreads ? (int)threadIdx.x - lane * slots : (int)threadIdx.x; s < slots;
-                 s += kThreads) {
-                float acc[VE];
+    const int64_t t0 = (int64_t)blockIdx.x * toks;
+    const int per = p.Dn + half;  // outputs of a token: pass-through channels, then pairs
+    const int total = (int)(p.T - t0 < toks ? p.T - t0 : toks) * per;
+
+    float c0 = 0.f, s0 = 0.f, c1 = 0.f, s1 = 0.f;
+    auto fetch = [&](int i) {
+        const int tt = i / per, j = i - tt * per - p.Dn;
+        if (i >= total || j < 0) return;
+        const int64_t row = table_row(p, j, t0 + tt);
+        const float* cr = p.cos_tab + (row < 0 ? 0 : row) * p.cs_width + j;
+        const float* sr = p.sin_tab + (row < 0 ? 0 : row) * p.cs_width + j;
+        c0 = __ldg(cr);
+        c1 = __ldg(cr + half);
+        s0 = __ldg(sr);
+        s1 = __ldg(sr + half);
+    };
+    fetch(threadIdx.x);
+    const int tl = lane / hl, h0 = lane - tl * hl;
+    if (tl < toks && t0 + tl < p.T) {
+        const E* x = in + (t0 + tl) * p.in_t;
+        for (int s = narrow ? (int)threadIdx.x - lane * slots : (int)threadIdx.x; s < slots; s += narrow ? slots : kThreads) {
+            float acc[VE];
 #pragma unroll
-                for (int k = 0; k < VE; ++k) acc[k] = 0.f;
-                for (int h = h0; h < p.H; h += hl * kUnroll) {
-                    float v[kUnroll][VE];
+            for (int k = 0; k < VE; ++k) acc[k] = 0.f;
+            for (int h = h0; h < p.H; h += hl * kHeads) {
+                Raw<E, VE> v[kHeads];
 #pragma unroll
-                    for (int u = 0; u < kUnroll; ++u)
-                        if (h + u * hl < p.H) load_vec<E, VE>(x + (int64_t)(h + u * hl) * p.in_h + s * VE, v[u]);
+                for (int u = 0; u < kHeads; ++u)
+                    if (h + u * hl < p.H) v[u].load(x + (int64_t)(h + u * hl) * p.in_h + s * VE);
 #pragma unroll
-                    for (int u = 0; u < kUnroll; ++u)
-                        if (h + u * hl < p.H)
+                for (int u = 0; u < kHeads; ++u)
+                    if (h + u * hl < p.H)
 #pragma unroll
-                            for (int k = 0; k < VE; ++k) acc[k] += v[u][k];
-                }
-#pragma unroll
-                for (int k = 0; k < VE; ++k) part[(int64_t)lane * D + s * VE + k] = acc[k];
+                        for (int k = 0; k < VE; ++k) acc[k] += v[u].get(k);
             }
+#pragma unroll
+            for (int k = 0; k < VE; ++k) part[lane * D + s * VE + k] = acc[k];
         }
-        __syncthreads();
-        const int per = p.Dn + half;  // outputs of a token: pass-through channels, then pairs
-        for (int i = threadIdx.x; i < toks * per; i += kThreads) {
-            const int tt = i / per, c = i - tt * per;
-            const int64_t t = t0 + tt;
-            if (t >= p.T) continue;
-            const float* q = part + (int64_t)tt * hl * D + c;
-            float a = 0.f, b = 0.f;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < total; i += kThreads) {
+        const int tt = i / per, c = i - tt * per;
+        const float* q = part + tt * hl * D + c;
+        float a = 0.f, b = 0.f;
+        if (i >= kThreads) fetch(i);
+        E* o = out + (t0 + tt) * p.out_t + c;
+        Raw<E, 1> ra, rb;
+        if (c >= p.Dn) {
+#pragma unroll 8
             for (int l = 0; l < hl; ++l) {
                 a += q[l * D];
-                if (c >= p.Dn) b += q[l * D + half];
+                b += q[l * D + half];
             }
-            E* o = out + t * p.out_t + c;
-            if (c >= p.Dn) {
-                Turn<1> tab;
-                tab.load(p, c - p.Dn, false, t);
-                float av[1] = {a}, bv[1] = {b};
-                tab.turn(true, av, bv);
-                store_vec<E, 1>(o, av);
-                store_vec<E, 1>(o + half, bv);
-            } else {
-                const float av[1] = {a};
-                store_vec<E, 1>(o, av);
-            }
+            ra.set({a * c0 + b * s1});
+            rb.set({b * c1 - a * s0});
+            rb.store(o + half);
+        } else {
+#pragma unroll 8
+            for (int l = 0; l < hl; ++l) a += q[l * D];
+            ra.set({a});
         }
-        __syncthreads();
+        ra.store(o);
     }
 }
 
@@ -291,28 +324,24 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_const
     for (int64_t it = (int64_t)blockIdx.x * kThreads + threadIdx.x; it < items; it += (int64_t)gridDim.x * kThreads) {
         const int64_t t = it / quads;
         const int c = (int)(it - t * quads) * (p.cs_vec ? 4 : 1);
-        const int i = c < half ? c : c - half;
         const int n = p.cs_vec ? 4 : 1;
+        const int i = c < half ? c : c - half;
         bool same = true;
         for (int k = 1; k < n; ++k) same &= p.axis[i + k] == p.axis[i];
         if (n == 4 && same) {
-            const int64_t row = __ldg(p.pos + p.axis[i] * p.T + t);
-            const bool ok = row >= 0 && row < p.cs_rows;
-            if (!ok) record_status(p.status, MLA_ERR_POS_RANGE);
+            const int64_t row = table_row(p, c, t);
             const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int64_t at = (ok ? row : 0) * p.cs_width + c;
+            const int64_t at = (row < 0 ? 0 : row) * p.cs_width + c;
             const float4 cv = __ldg(reinterpret_cast<const float4*>(p.cos_tab + at));
             const float4 sv = __ldg(reinterpret_cast<const float4*>(p.sin_tab + at));
-            *reinterpret_cast<float4*>(cos_out + t * p.Dr + c) = ok ? cv : z;
-            *reinterpret_cast<float4*>(sin_out + t * p.Dr + c) = ok ? sv : z;
+            *reinterpret_cast<float4*>(cos_out + t * p.Dr + c) = row < 0 ? z : cv;
+            *reinterpret_cast<float4*>(sin_out + t * p.Dr + c) = row < 0 ? z : sv;
         } else {
             for (int k = 0; k < n; ++k) {
-                const int64_t row = __ldg(p.pos + p.axis[i + k] * p.T + t);
-                const bool ok = row >= 0 && row < p.cs_rows;
-                if (!ok) record_status(p.status, MLA_ERR_POS_RANGE);
-                const int64_t at = (ok ? row : 0) * p.cs_width + c + k;
-                cos_out[t * p.Dr + c + k] = ok ? __ldg(p.cos_tab + at) : 0.f;
-                sin_out[t * p.Dr + c + k] = ok ? __ldg(p.sin_tab + at) : 0.f;
+                const int64_t row = table_row(p, c + k, t);
+                const int64_t at = (row < 0 ? 0 : row) * p.cs_width + c + k;
+                cos_out[t * p.Dr + c + k] = row < 0 ? 0.f : __ldg(p.cos_tab + at);
+                sin_out[t * p.Dr + c + k] = row < 0 ? 0.f : __ldg(p.sin_tab + at);
             }
         }
     }
@@ -324,18 +353,21 @@ int launch_rows(RopeParams p, bool sum, int num_sms, cudaStream_t stream) {
         const int D = p.Dn + p.Dr, slots = D / VE;
         const int lanes = kThreads / slots > 0 ? kThreads / slots : 1;
         const int toks = lanes / (p.H < lanes ? p.H : lanes);
-        int64_t grid = (p.T + toks - 1) / toks;
-        if (grid > (int64_t)num_sms * 8) grid = (int64_t)num_sms * 8;
+        const int64_t grid = (p.T + toks - 1) / toks;
         rope_sum_kernel<E, VE><<<(unsigned)grid, kThreads, (size_t)lanes * D * sizeof(float), stream>>>(p);
     } else {
         const int slots = (p.Dn / VE + 1) / 2 + p.Dr / 2 / VE;
         const int lanes = kThreads / slots > 0 ? kThreads / slots : 1;
-        // enough rows per block to reuse table entries, fewer when the grid would not fill the SMs
-        int64_t per = p.rows / ((int64_t)lanes * num_sms * 8);
-        per = per < 1 ? 1 : (per > 2 * kUnroll ? 2 * kUnroll : per);
-        p.rows_per_block = (int)(per * lanes);
-        const int64_t grid = (p.rows + p.rows_per_block - 1) / p.rows_per_block;
-        rope_axes_kernel<E, VE><<<(unsigned)grid, kThreads, 0, stream>>>(p);
+        // up to kRunRows rows per thread, fewer when the grid would not fill the SMs or the table its room
+        const int64_t tok_rows = kTableBytes / (8 * p.Dr);  // tokens whose entries fit
+        int64_t per = p.rows / ((int64_t)lanes * num_sms * kRowBlocks);
+        per = per < 1 ? 1 : (per > kRunRows ? kRunRows : per);
+        int64_t run = per * lanes;
+        if ((run + p.H - 2) / p.H + 1 > tok_rows) run = (tok_rows - 1) * p.H;
+        p.rows_per_block = (int)run;
+        const int64_t grid = (p.rows + run - 1) / run;
+        const int64_t most = (run + p.H - 2) / p.H + 1;  // tokens that a run may touch
+        rope_axes_kernel<E, VE><<<(unsigned)grid, kThreads, (size_t)(most * 8 * p.Dr), stream>>>(p);
     }
     return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

@@ -43,7 +43,9 @@ def _axes_args(cos, sin, pos, axes, Dr, T, dev):
     """Check the tables, the positions [A, T] and the Dr/2 pairs' axes; the axes as bytes."""
     _need(cos, "cos", torch.float32, dev, ndim=2)
     _need(sin, "sin", torch.float32, dev, shape=cos.shape)
-    _need(pos, "pos", torch.int32, dev, ndim=2, shape=(pos.shape[0], T) if pos.dim() == 2 else None)
+    _need(pos, "pos", torch.int32, dev, ndim=2)
+    if pos.shape[1] != T:
+        raise ValueError(f"pos must be [axes, {T}], got {list(pos.shape)}")
     if len(axes) != Dr // 2:
         raise ValueError(f"axes must name the axis of each of the {Dr // 2} pairs, got {len(axes)}")
     return bytes(axes)
