@@ -201,3 +201,57 @@ def test_gradients_against_differences(cuda_device, act):
         lo = loss(*[t - eps * d if j == i else t for j, t in enumerate(wide)])
         got = (leaf.grad.to(f64) * d).sum()
         assert abs(float(got - (hi - lo) / (2 * eps))) <= 2.0 ** -6 * float(leaf.grad.to(f64).norm() * d.norm())
+
+
+# few tokens: padded counts around 16s, reductions split over 1, 2, 4 and 8 CTAs, ragged channel tiles and splits
+FEW = [(1, 2048, 8), (1, 1032, 2000), (3, 520, 72), (8, 264, 10008), (16, 2056, 136), (17, 640, 328), (31, 1544, 64),
+       (48, 72, 3000), (64, 1000, 1000), (80, 2048, 200), (96, 136, 136), (100, 1288, 520), (112, 64, 1032),
+       (128, 776, 264)]
+
+
+@pytest.mark.parametrize("T,K,F", FEW)
+def test_few_tokens(cuda_device, T, K, F):
+    x, wgu, wd, dy = make(T, K, F, pitch=24 if T % 2 else 0, seed=T + K)
+    st = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    y, gu, h = mlaq.gated_ffn_fwd(x, wgu, wd, save=True, status=st)
+    check_forward(x, wgu, wd, "silu", y, gu, h)
+    dgu = torch.empty((T, 2 * F), dtype=bf16, device=cuda_device)
+    dx, dwgu, dwd = mlaq.gated_ffn_bwd(dy, x, wgu, wd, gu, h, dgate_up=dgu, status=st)
+    mlaq.check_status(st)
+    dh, e = product(dy, wd.t())
+    g, u = gu.to(f64).split(F, 1)
+    a, da = act64(g, "silu")
+    check(dgu[:, :F], dh * u * da, e * (u * da).abs() + 64 * U * (dh * u).abs() * (1 + g.abs()), "dg")
+    check(dgu[:, F:], dh * a, e * a.abs() + 64 * U * (dh * a).abs() + 32 * U * (dh * g).abs() * 1e-3, "du")
+    check(dx, *product(dgu, wgu.t()), "dx")
+    check(dwgu, *product(dgu.t(), x.t()), "dw_gate_up")
+    check(dwd, *product(dy.t(), h.t()), "dw_down")
+
+
+def test_few_tokens_back_to_back(cuda_device):
+    """Calls that reuse the same scratch and outputs, one behind the other: each product waits for the one it reads."""
+    T, K, F = 4, 1024, 2048
+    sets = [make(T, K, F, seed=i) for i in range(4)]
+    want = [mlaq.gated_ffn_fwd(x, wgu, wd) for x, wgu, wd, _ in sets]
+    torch.cuda.synchronize()
+    h = torch.empty((T, F), dtype=bf16, device=cuda_device)
+    ys = [torch.empty((T, K), dtype=bf16, device=cuda_device) for _ in range(40)]
+    for i, y in enumerate(ys):
+        x, wgu, wd, _ = sets[i % 4]
+        mlaq.gated_ffn_fwd(x, wgu, wd, y=y, h=h)
+    for i, y in enumerate(ys):
+        assert torch.equal(y, want[i % 4])
+
+
+def test_few_tokens_in_a_graph(cuda_device):
+    x, wgu, wd, _ = make(5, 512, 1024)
+    y = mlaq.gated_ffn_fwd(x, wgu, wd)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = mlaq.gated_ffn_fwd(x, wgu, wd)
+    x.copy_(torch.roll(x, 1, 0))
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, torch.roll(y, 1, 0))

@@ -412,6 +412,268 @@ int prepare_gemm(int num_sms, int device, int* pairs) {
     return MLA_OK;
 }
 
+// ------------------------------------------------------------ few tokens
+// With few tokens a product reads its weights once and does little else: the
+// bound is HBM. The operands change places, 128 weight rows are the M of a
+// tcgen05.mma and all T tokens (padded to N, a multiple of 16) its N, so the
+// weights stream through every SM's ring of TMA stages and are padded by
+// nothing. The reduction is split over a cluster of S CTAs (S so that all SMs
+// stream); their float32 sums meet in distributed shared memory and are added
+// in rank order, so results do not depend on scheduling. A product that follows
+// another (y after h) starts under it: it fills its ring with weights first and
+// waits for the other grid only before it reads the tokens.
+// kGate: 64 gate rows and the same channels' 64 up rows make the 128.
+// Warps: 0 producer, 1 MMA issuer, 2-5 read TMEM; all six add and store.
+constexpr int kNarrowThreads = 192;
+constexpr int kNarrowMax = 128;                       // tokens
+constexpr uint32_t kNarrowABytes = 128u * 128u;       // 128 weight rows of one K step
+constexpr size_t kNarrowRing = 108 * 1024;            // two CTAs fit an SM
+
+struct NarrowParams {
+    int T, N, R;              // tokens, padded tokens, weight rows (kGate: channels)
+    int k_tiles, stages, splits;
+    uint32_t stage_bytes, tmem_cols;
+    int after;                // the tokens come from the grid before this one
+    int F, act;
+    uint16_t* out;
+    uint16_t* gate_up_out;
+    const uint16_t* gate_up;
+    int* status;
+};
+
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, int rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+__device__ __forceinline__ void load4(const uint16_t* p, float (&v)[4]) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+    v[0] = bf16lo_to_f32(w.x);
+    v[1] = bf16hi_to_f32(w.x);
+    v[2] = bf16lo_to_f32(w.y);
+    v[3] = bf16hi_to_f32(w.y);
+}
+
+template <bool AMN, int EPI>
+__global__ void __launch_bounds__(kNarrowThreads)
+    ffn_narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const NarrowParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t bars = base + p.stages * p.stage_bytes;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (p.stages + s); };
+    const uint32_t done = bars + 16u * p.stages, drain = done + 8u;
+    uint8_t* tail = smem_raw + (done - raw) + 16u;
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(tail);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = p.splits > 1 ? (int)cluster_rank() : 0;
+    const int tile = blockIdx.x / p.splits;
+    const int kb = (int)((int64_t)p.k_tiles * rank / p.splits);
+    const int steps = (int)((int64_t)p.k_tiles * (rank + 1) / p.splits) - kb;
+    const int r0 = tile * (EPI == kGate ? 64 : 128);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        mbar_init(done, 1);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32((const void*)tmem_slot), p.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            const uint64_t weights_once = l2_evict_first_policy();
+            auto load_a = [&](int i, int s) {
+                const uint32_t sa = base + s * p.stage_bytes;
+                const int k = (kb + i) * kBK;
+                if constexpr (EPI == kGate) {
+                    tma_load_2d_hint(sa, &tmA, k, r0, full(s), weights_once);
+                    tma_load_2d_hint(sa + kNarrowABytes / 2, &tmA, k, p.F + r0, full(s), weights_once);
+                } else if constexpr (AMN) {
+                    tma_load_2d_hint(sa, &tmA, r0, k, full(s), weights_once);
+                    tma_load_2d_hint(sa + kChunkBytes, &tmA, r0 + 64, k, full(s), weights_once);
+                } else {
+                    tma_load_2d_hint(sa, &tmA, k, r0, full(s), weights_once);
+                }
+            };
+            auto load_b = [&](int i, int s) {
+                tma_load_2d(base + s * p.stage_bytes + kNarrowABytes, &tmB, (kb + i) * kBK, 0, full(s));
+            };
+            const int ahead = steps < p.stages ? steps : p.stages;
+            for (int i = 0; i < ahead; ++i) {
+                mbar_arrive_expect_tx(full(i), p.stage_bytes);
+                load_a(i, i);
+            }
+            if (p.after) asm volatile("griddepcontrol.wait;" ::: "memory");
+            for (int i = 0; i < ahead; ++i) load_b(i, i);
+            bool ok = true;
+            int s = 0;
+            uint32_t ph = 0;  // of the stage's first refill
+            int i = ahead;
+            for (; i < steps; ++i) {
+                if (!mbar_wait(empty(s), ph, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(full(s), p.stage_bytes);
+                load_a(i, s);
+                load_b(i, s);
+                if (++s == p.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (!ok)  // copies in flight land before the CTA leaves: the last fill of each stage is one of
+                for (int j = i > p.stages ? i - p.stages : 0; j < i; ++j)
+                    mbar_wait(full(j % p.stages), (uint32_t)(j / p.stages) & 1u, nullptr, 200000000ull);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16(128, (uint32_t)p.N, AMN, 0);
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int i = 0; i < steps; ++i) {
+                if (!mbar_wait(full(s), ph, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sa = base + s * p.stage_bytes, sb = sa + kNarrowABytes;
+#pragma unroll
+                for (int j = 0; j < kBK / 16; ++j)
+                    mma_bf16(tmem, AMN ? desc_mnmajor_sw128(sa + 2048u * j, kChunkBytes) : desc_kmajor_sw128(sa + 32u * j),
+                             desc_kmajor_sw128(sb + 32u * j), idesc, (i | j) != 0);
+                mma_commit(empty(s));
+                if (++s == p.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            mma_commit(ok ? done : drain);
+            if (!ok) mbar_wait(drain, 0, nullptr, 200000000ull);
+        }
+        __syncwarp();
+    } else {
+        // partial sums to shared memory (the ring is free once every MMA is done): [token][128 rows]
+        const bool ok = mbar_wait(done, 0, abort_flag);
+        if (!__any_sync(0xffffffffu, !ok)) {
+            tc_fence_after();
+            const int quad = warp & 3;
+            const uint32_t dst = base + 4u * (quad * 32 + lane);
+            for (int c = 0; c < p.N; c += 16) {
+                uint32_t v[16];
+                __syncwarp();
+                tmem_ld16(tmem + ((uint32_t)(quad * 32) << 16) + c, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 512u * (c + i)), "r"(v[i]) : "memory");
+            }
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    if (p.splits > 1) cluster_sync();
+
+    // this CTA adds and finishes its share of the tokens
+    const int t_begin = p.T * rank / p.splits, t_end = p.T * (rank + 1) / p.splits;
+    constexpr int kQuads = EPI == kGate ? 16 : 32;
+    const bool failed = *abort_flag != 0;
+    for (int i = threadIdx.x; i < (t_end - t_begin) * kQuads && !failed; i += kNarrowThreads) {
+        const int t = t_begin + i / kQuads, q = i % kQuads, r = r0 + 4 * q;
+        if (r >= p.R) continue;
+        const uint32_t at = base + 512u * t + 16u * q;
+        float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < p.splits; ++s) {
+            const uint32_t from = p.splits > 1 ? map_to_rank(at, s) : at;
+            const float4 v = ld_cluster_v4(from);
+            a[0] += v.x;
+            a[1] += v.y;
+            a[2] += v.z;
+            a[3] += v.w;
+            if constexpr (EPI == kGate) {
+                const float4 w = ld_cluster_v4(from + 256u);
+                b[0] += w.x;
+                b[1] += w.y;
+                b[2] += w.z;
+                b[3] += w.w;
+            }
+        }
+        if constexpr (EPI == kGate) {
+            float h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float act, unused;
+                activate<false>(p.act, a[j], act, unused);
+                h[j] = act * b[j];
+            }
+            store4(p.out + (int64_t)t * p.F + r, h);
+            if (p.gate_up_out) {
+                store4(p.gate_up_out + (int64_t)t * 2 * p.F + r, a);
+                store4(p.gate_up_out + (int64_t)t * 2 * p.F + p.F + r, b);
+            }
+        } else if constexpr (EPI == kGateGrad) {
+            float g[4], u[4], dg[4], du[4];
+            load4(p.gate_up + (int64_t)t * 2 * p.F + r, g);
+            load4(p.gate_up + (int64_t)t * 2 * p.F + p.F + r, u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float act, dact;
+                activate<true>(p.act, g[j], act, dact);
+                dg[j] = a[j] * u[j] * dact;
+                du[j] = a[j] * act;
+            }
+            store4(p.out + (int64_t)t * 2 * p.F + r, dg);
+            store4(p.out + (int64_t)t * 2 * p.F + p.F + r, du);
+        } else {
+            store4(p.out + (int64_t)t * p.R + r, a);
+        }
+    }
+
+    // --------------------------------------------------------------- teardown
+    if (threadIdx.x == 0 && failed) record_status(p.status, MLA_ERR_TIMEOUT);
+    if (p.splits > 1) cluster_sync();  // the others have read this CTA's sums
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, p.tmem_cols);
+    }
+}
+
 struct Operand {
     const void* p;
     int64_t rows, cols, ld;  // as stored, ld in elements
@@ -437,6 +699,59 @@ int gemm(const Operand& a, const Operand& b, GemmParams p, int64_t red, const De
     if (tiles < pairs) pairs = (int)tiles;
     ffn_gemm_kernel<AMN, BMN, EPI><<<2 * pairs, kThreads, kSmem, stream>>>(ta, tb, p);
     return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+// The same product for few tokens (see ffn_narrow_kernel): w is [R, red] (or
+// [red, R] when AMN), tokens [T, red]. after: the tokens are the output of the
+// launch before this one.
+template <bool AMN, int EPI>
+int narrow(const Operand& w, const Operand& tokens, const GemmParams& g, int64_t red, bool after, const DeviceInfo& di,
+           cudaStream_t stream) {
+    NarrowParams p{};
+    p.T = g.M;
+    p.N = (g.M + 15) / 16 * 16;
+    p.R = g.N;
+    p.F = g.F;
+    p.act = g.act;
+    p.out = g.out;
+    p.gate_up_out = g.gate_up_out;
+    p.gate_up = g.gate_up;
+    p.status = g.status;
+    p.after = after;
+    p.k_tiles = (int)((red + kBK - 1) / kBK);
+    p.stage_bytes = kNarrowABytes + 128u * p.N;
+    p.stages = (int)(kNarrowRing / p.stage_bytes);
+    p.tmem_cols = 32;
+    while ((int)p.tmem_cols < p.N) p.tmem_cols *= 2;
+    const int tiles = EPI == kGate ? (p.R + 63) / 64 : (p.R + 127) / 128;
+    p.splits = 1;
+    while (p.splits < 8 && tiles * p.splits < di.num_sms && p.k_tiles >= 4 * p.splits) p.splits *= 2;
+    alignas(64) CUtensorMap ta, tb;
+    const uint32_t box_rows = AMN ? kBK : (EPI == kGate ? 64 : 128);
+    int st = make_tmap_2d(&ta, w.p, 1, (uint64_t)w.cols, (uint64_t)w.rows, (uint64_t)w.ld * 2, 64, box_rows, true);
+    if (st == MLA_OK)
+        st = make_tmap_2d(&tb, tokens.p, 1, (uint64_t)tokens.cols, (uint64_t)tokens.rows, (uint64_t)tokens.ld * 2, 64,
+                          (uint32_t)p.N, true);
+    if (st != MLA_OK) return st;
+    const auto kernel = ffn_narrow_kernel<AMN, EPI>;
+    const size_t smem = 1024 + kNarrowRing + 512;
+    if (cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return MLA_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(tiles * p.splits));
+    cfg.blockDim = dim3(kNarrowThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)p.splits;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = after ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, ta, tb, p) != cudaSuccess) return MLA_ERR_CUDA;
+    return MLA_OK;
 }
 
 int check_ffn(const mla_ffn_shape* s) {
@@ -483,10 +798,13 @@ MLAQ_API int mla_gated_ffn_fwd(const mla_ffn_shape* shape, const void* x, const 
     p.N = (int)s.F;
     p.out = static_cast<uint16_t*>(h);
     p.gate_up_out = static_cast<uint16_t*>(gate_up);
-    st = gemm<false, false, kGate>({x, s.T, s.K, ld}, {w_gate_up, 2 * s.F, s.K, s.K}, p, s.K, di, cs);
+    const bool few = s.T <= kNarrowMax;
+    st = few ? narrow<false, kGate>({w_gate_up, 2 * s.F, s.K, s.K}, {x, s.T, s.K, ld}, p, s.K, false, di, cs)
+             : gemm<false, false, kGate>({x, s.T, s.K, ld}, {w_gate_up, 2 * s.F, s.K, s.K}, p, s.K, di, cs);
     if (st != MLA_OK) return st;
     p.N = (int)s.K;
     p.out = static_cast<uint16_t*>(y);
+    if (few) return narrow<false, kStore>({w_down, s.K, s.F, s.F}, {h, s.T, s.F, s.F}, p, s.F, true, di, cs);
     return gemm<false, false, kStore>({h, s.T, s.F, s.F}, {w_down, s.K, s.F, s.F}, p, s.F, di, cs);
 }
 
@@ -527,20 +845,23 @@ MLAQ_API int mla_gated_ffn_bwd(const mla_ffn_shape* shape, const void* dy, const
     p.F = (int)s.F;
     p.act = s.act;
     p.status = dev_status;
+    const bool few = s.T <= kNarrowMax;
     if (hidden) {
         p.M = (int)s.T;
         p.N = (int)s.F;
         p.out = static_cast<uint16_t*>(dgate_up);
         p.gate_up = static_cast<const uint16_t*>(gate_up);
-        st = gemm<false, true, kGateGrad>({dy, s.T, s.K, s.K}, {w_down, s.K, s.F, s.F}, p, s.K, di, cs);
+        if (few) st = narrow<true, kGateGrad>({w_down, s.K, s.F, s.F}, {dy, s.T, s.K, s.K}, p, s.K, false, di, cs);
+        else st = gemm<false, true, kGateGrad>({dy, s.T, s.K, s.K}, {w_down, s.K, s.F, s.F}, p, s.K, di, cs);
         if (st != MLA_OK) return st;
     }
     if (dx) {
         p.M = (int)s.T;
         p.N = (int)s.K;
         p.out = static_cast<uint16_t*>(dx);
-        st = gemm<false, true, kStore>({dgate_up, s.T, 2 * s.F, 2 * s.F}, {w_gate_up, 2 * s.F, s.K, s.K}, p, 2 * s.F, di,
-                                       cs);
+        const Operand w{w_gate_up, 2 * s.F, s.K, s.K}, d{dgate_up, s.T, 2 * s.F, 2 * s.F};
+        st = few ? narrow<true, kStore>(w, d, p, 2 * s.F, true, di, cs)
+                 : gemm<false, true, kStore>(d, w, p, 2 * s.F, di, cs);
         if (st != MLA_OK) return st;
     }
     if (dw_gate_up) {
