@@ -73,7 +73,7 @@ int make_tmap_2d(void* tmap_out, const void* base, int dtype, uint64_t inner, ui
 }
 
 int make_tmap_3d(void* tmap_out, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
-                 uint64_t stride2, uint32_t b0, uint32_t b1, uint32_t b2) {
+                 uint64_t stride2, uint32_t b0, uint32_t b1, uint32_t b2, bool swizzle64) {
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     std::call_once(once, [] {
@@ -91,7 +91,7 @@ int make_tmap_3d(void* tmap_out, const void* base, uint64_t d0, uint64_t d1, uin
     const cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = encode(reinterpret_cast<CUtensorMap*>(tmap_out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? MLA_OK : MLA_ERR_CUDA;
 }

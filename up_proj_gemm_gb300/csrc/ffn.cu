@@ -33,19 +33,35 @@ namespace mlaq {
 namespace {
 
 constexpr int kThreads = 320;
-constexpr int kStages = 6;
 constexpr int kBK = 64;
 constexpr uint32_t kHalfBytes = 128u * 128u;       // 128 rows (or columns) of one K step, one operand
 constexpr uint32_t kStageBytes = 2u * kHalfBytes;  // A and B of one CTA
 constexpr uint32_t kChunkBytes = 64u * 128u;       // MN-major: 64 columns of 64 K rows
 constexpr uint32_t kTmemCols = 512;
-constexpr size_t kSmem = 1024 + kStages * kStageBytes + 256;
+constexpr uint32_t kSlotBytes = 32u * 64u;         // 32 rows x 32 columns of a result, 64-byte swizzle
+constexpr int kEpiWarps = 8;
+constexpr int kSplitSteps = 12;                     // K steps that adding up a split reduction costs
+constexpr int kMaxSplits = 4;                      // clusters of 8 CTAs
 
 enum Epilogue { kStore = 0, kGate = 1, kGateGrad = 2 };
+
+// Ring stages and each epilogue warp's slots: results leave by TMA from a slot
+// (a lane writing its own row of the result instead took 32 cache lines per
+// instruction: 25 against 9 us for one tile of kGateGrad), and kGateGrad's gate
+// and up products arrive in three pairs of slots, two pairs ahead.
+template <int EPI>
+struct Smem {
+    static constexpr int kStages = EPI == kGateGrad ? 4 : 5;
+    static constexpr int kSlots = EPI == kGateGrad ? 6 : 4;
+    static constexpr uint32_t kRing = kStages * kStageBytes;
+    static constexpr size_t kBytes = 1024 + kRing + (size_t)kEpiWarps * kSlots * kSlotBytes + 512;
+};
 
 struct GemmParams {
     int M, N;                 // of the result; kGate: N = F (a tile holds 128 of them)
     int k_tiles, m_tiles, n_tiles;
+    int splits;               // parts of the reduction, each a pair of the cluster
+    int after;                // an operand comes from the grid before this one
     int F, act;
     uint16_t* out;            // kStore [M, N], kGate h [M, F], kGateGrad [M, 2F]
     uint16_t* gate_up_out;    // kGate: [M, 2F] or null
@@ -62,11 +78,28 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The address of the even CTA's copy of a shared-memory location.
-__device__ __forceinline__ uint32_t map_to_leader(uint32_t addr) {
+// The address of another CTA's copy of a shared-memory location.
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, int rank) {
     uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(0));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
+}
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+// A grid that may start under the one before it: let the next one do the same,
+// and wait until the one before is complete.
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_3d(const void* tmap, int32_t c0, int32_t c1, int32_t c2, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(tmap),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(src)
+                 : "memory");
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -95,11 +128,11 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, u
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// Arrive on the same barrier of both CTAs once the MMAs issued so far are done.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+// Arrive on the same barrier of both CTAs (mask: their cluster ranks) once the MMAs issued so far are done.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint32_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
+        "h"((uint16_t)mask)
         : "memory");
 }
 
@@ -149,98 +182,239 @@ __device__ __forceinline__ void tile_at(const GemmParams& p, int tile, int& mt, 
     mt = g * kGroupM + (r - nt * rows);
 }
 
+// One epilogue warp: rows row0 .. row0 + 31 of the tile, lane = row. Its chunks
+// of 32 columns come from TMEM, or (splits > 1) as the sum of the pairs' partial
+// sums in distributed shared memory.
 template <int EPI>
-__device__ __forceinline__ void epilogue_rows(const GemmParams& p, uint32_t tacc, int64_t row, int n0, int half) {
-    const bool valid = row < p.M;
-    if constexpr (EPI == kGate) {
-        // columns 0-127 of the accumulator are gates, 128-255 the same channels' up products
+struct Epi {
+    const GemmParams& p;
+    const CUtensorMap* tmO;   // kStore [M, N], kGate h [M, F]; kGateGrad: {F, 2, T} view of [dg | du]
+    const CUtensorMap* tmG;   // kGate, kGateGrad: {F, 2, T} view of the gate and up products
+    uint32_t slots, bars;     // this warp's slots; kGateGrad: a barrier per pair of them
+    uint32_t sums;            // splits > 1: this CTA's partial sums, float4 [column / 4][128 rows]
+    int lane, quad, half, prank, srank;
+    int used = 0;             // slots (kGateGrad: chunks) this warp has used so far
+    int asked = 0;            // kGateGrad: chunks whose loads are under way
+    volatile int* abort_flag;
+
+    // chunks of this warp: of the tile's 8 (kGate: 4 of gates with their 4 of up products)
+    static constexpr int kChunks = EPI == kGate ? 4 : 8;
+    __device__ __forceinline__ int chunk(int i) const { return srank + p.splits * (half + 2 * i); }
+
+    __device__ __forceinline__ void values(uint32_t tacc, int col, uint32_t (&v)[32]) const {
+        if (p.splits == 1) {
+            tmem_ld32(tacc + col, v);
+            return;
+        }
+        float a[32];
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-            const int col = half * 64 + c;
-            uint32_t rg[32], ru[32];
-            __syncwarp();
-            tmem_ld32(tacc + col, rg);
-            tmem_ld32(tacc + 128 + col, ru);
-            tmem_ld_wait();
-            const int f = n0 + col;
-            if (!valid) continue;
+        for (int i = 0; i < 32; ++i) a[i] = 0.f;
+        const uint32_t at = sums + 16u * ((col / 4) * 128 + quad * 32 + lane);
+        for (int s = 0; s < p.splits; ++s) {
+            const uint32_t from = map_to_rank(at, 2 * s + prank);
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-                if (f + i >= p.F) break;
-                float g[8], u[8], h[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float a, unused;
-                    g[j] = __uint_as_float(rg[i + j]);
-                    u[j] = __uint_as_float(ru[i + j]);
-                    activate<false>(p.act, g[j], a, unused);
-                    h[j] = a * u[j];
-                }
-                store8(p.out + row * p.F + f + i, h);
-                if (p.gate_up_out) {
-                    store8(p.gate_up_out + row * 2 * p.F + f + i, g);
-                    store8(p.gate_up_out + row * 2 * p.F + p.F + f + i, u);
-                }
+            for (int i = 0; i < 8; ++i) {
+                const float4 f = ld_cluster_v4(from + 2048u * i);
+                a[4 * i] += f.x;
+                a[4 * i + 1] += f.y;
+                a[4 * i + 2] += f.z;
+                a[4 * i + 3] += f.w;
             }
         }
-    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(a[i]);
+    }
+
+    // Splits > 1: this warp's part of the accumulator, for the other CTAs to add.
+    __device__ __forceinline__ void share(uint32_t tacc) const {
         for (int c = 0; c < 128; c += 32) {
-            const int col = half * 128 + c;
-            uint32_t r[32];
+            uint32_t v[32];
             __syncwarp();
-            tmem_ld32(tacc + col, r);
+            tmem_ld32(tacc + half * 128 + c, v);
             tmem_ld_wait();
-            if (!valid) continue;
+            const uint32_t at = sums + 16u * ((half * 32 + c / 4) * 128 + quad * 32 + lane);
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-                const int n = n0 + col + i;
-                if (n >= p.N) break;
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[i + j]);
-                if constexpr (EPI == kStore) {
-                    store8(p.out + row * p.N + n, v);
-                } else {
-                    const uint16_t* gu = p.gate_up + row * 2 * p.F + n;
-                    float g[8], u[8], dg[8], du[8];
-                    unpack8(__ldg(reinterpret_cast<const uint4*>(gu)), g);
-                    unpack8(__ldg(reinterpret_cast<const uint4*>(gu + p.F)), u);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float a, da;
-                        activate<true>(p.act, g[j], a, da);
-                        dg[j] = v[j] * u[j] * da;
-                        du[j] = v[j] * a;
-                    }
-                    store8(p.out + row * 2 * p.F + n, dg);
-                    store8(p.out + row * 2 * p.F + p.F + n, du);
-                }
-            }
+            for (int i = 0; i < 8; ++i) sts_v4(at + 2048u * i, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         }
     }
-}
 
-// AMN / BMN: the operand is MN-major (its reduction runs over rows).
+    // 16 bytes (8 columns) of this lane's row inside a slot
+    __device__ __forceinline__ uint32_t piece(uint32_t slot, int k) const {
+        return slot + 64u * lane + 16u * (k ^ ((lane >> 1) & 3));
+    }
+    __device__ __forceinline__ void write(uint32_t slot, const float (&v)[32]) const {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            sts_v4(piece(slot, k), pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                   pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+    }
+    // Write a chunk to the next slot of the ring, which its last store has left.
+    __device__ __forceinline__ uint32_t put(const float (&v)[32]) {
+        const uint32_t slot = slots + kSlotBytes * (used++ % Smem<EPI>::kSlots);
+        if (lane == 0) bulk_wait_group_read<Smem<EPI>::kSlots - 1>();
+        __syncwarp();
+        write(slot, v);
+        fence_proxy_async_smem();
+        __syncwarp();
+        return slot;
+    }
+
+    // kGateGrad: fetch chunk i's gate and up products into the pair of slots of
+    // the chunk three before it, whose stores must have been read: all but the
+    // newest one's, since no more than two chunks are asked for ahead.
+    __device__ __forceinline__ void ask(int n0, int64_t row0, int i) {
+        const int f = n0 + 32 * chunk(i), pair = asked % 3;
+        if (lane == 0) {
+            bulk_wait_group_read<1>();  // one group per chunk
+            const uint32_t slot = slots + kSlotBytes * (2 * pair), bar = bars + 8u * pair;
+            mbar_arrive_expect_tx(bar, 2 * kSlotBytes);
+            tma_load_3d(slot, tmG, f, 0, (int32_t)row0, bar);
+            tma_load_3d(slot + kSlotBytes, tmG, f, 1, (int32_t)row0, bar);
+        }
+        ++asked;
+    }
+    __device__ __forceinline__ bool has(int n0, int64_t row0, int i) const {
+        return chunk(i) < kChunks && n0 + 32 * chunk(i) < p.N && row0 < p.M;
+    }
+
+    // Before the tile's accumulator is ready.
+    __device__ __forceinline__ void ahead(int n0, int64_t row0) {
+        if constexpr (EPI == kGateGrad)
+            for (int i = 0; i < 2; ++i)
+                if (has(n0, row0, i)) ask(n0, row0, i);
+    }
+
+    __device__ __forceinline__ bool tile(uint32_t tacc, int n0, int64_t row0) {
+        for (int i = 0; chunk(i) < kChunks; ++i) {
+            const int c = chunk(i), n = n0 + 32 * c;
+            if (!has(n0, row0, i)) break;  // this and the later chunks lie outside the result
+            uint32_t r[32];
+            float v[32];
+            if constexpr (EPI == kGate) {
+                uint32_t ru[32];
+                float u[32];
+                __syncwarp();
+                values(tacc, 32 * c, r);
+                values(tacc, 128 + 32 * c, ru);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    v[j] = __uint_as_float(r[j]);
+                    u[j] = __uint_as_float(ru[j]);
+                }
+                if (p.gate_up_out) {
+                    const uint32_t sg = put(v);
+                    if (lane == 0) {
+                        tma_store_3d(tmG, n, 0, (int32_t)row0, sg);
+                        bulk_commit_group();
+                    }
+                    const uint32_t su = put(u);
+                    if (lane == 0) {
+                        tma_store_3d(tmG, n, 1, (int32_t)row0, su);
+                        bulk_commit_group();
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    float a, unused;
+                    activate<false>(p.act, v[j], a, unused);
+                    v[j] = a * u[j];
+                }
+                const uint32_t sh = put(v);
+                if (lane == 0) {
+                    tma_store_2d(tmO, n, (int32_t)row0, sh);
+                    bulk_commit_group();
+                }
+            } else if constexpr (EPI == kStore) {
+                __syncwarp();
+                values(tacc, 32 * c, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                const uint32_t s = put(v);
+                if (lane == 0) {
+                    tma_store_2d(tmO, n, (int32_t)row0, s);
+                    bulk_commit_group();
+                }
+            } else {
+                __syncwarp();
+                values(tacc, 32 * c, r);
+                tmem_ld_wait();
+                const int pair = used % 3;
+                const bool ok = mbar_wait(bars + 8u * pair, (uint32_t)(used / 3) & 1u, abort_flag);
+                if (__any_sync(0xffffffffu, !ok)) return false;
+                ++used;
+                const uint32_t slot = slots + kSlotBytes * (2 * pair);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float g[8], u[8], dg[8], du[8];
+                    unpack8(lds_v4(piece(slot, k)), g);
+                    unpack8(lds_v4(piece(slot + kSlotBytes, k)), u);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float d = __uint_as_float(r[8 * k + j]);
+                        float a, da;
+                        activate<true>(p.act, g[j], a, da);
+                        dg[j] = d * u[j] * da;
+                        du[j] = d * a;
+                    }
+                    sts_v4(piece(slot, k), pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3]),
+                           pack_bf16x2(dg[4], dg[5]), pack_bf16x2(dg[6], dg[7]));
+                    sts_v4(piece(slot + kSlotBytes, k), pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3]),
+                           pack_bf16x2(du[4], du[5]), pack_bf16x2(du[6], du[7]));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(tmO, n, 0, (int32_t)row0, slot);
+                    tma_store_3d(tmO, n, 1, (int32_t)row0, slot + kSlotBytes);
+                    bulk_commit_group();
+                }
+                if (has(n0, row0, i + 2)) ask(n0, row0, i + 2);
+            }
+        }
+        return true;
+    }
+
+    // Every load has landed and every store has been read when the warp leaves.
+    __device__ __forceinline__ void finish() {
+        if constexpr (EPI == kGateGrad)
+            for (; used < asked; ++used) mbar_wait(bars + 8u * (used % 3), (uint32_t)(used / 3) & 1u, nullptr, 200000000ull);
+        if (lane == 0) bulk_wait_group_all();
+        __syncwarp();
+    }
+};
+
+// AMN / BMN: the operand is MN-major (its reduction runs over rows). A cluster
+// holds `splits` pairs; with one, pairs walk the tiles, with more, a cluster
+// has one tile and each pair a part of its reduction.
 template <bool AMN, bool BMN, int EPI>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmG,
                     const GemmParams p) {
+    constexpr int kStages = Smem<EPI>::kStages, kSlots = Smem<EPI>::kSlots;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    const uint32_t bars = base + kStages * kStageBytes;
+    const uint32_t staging = base + Smem<EPI>::kRing;
+    const uint32_t bars = staging + kEpiWarps * kSlots * kSlotBytes;
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (kStages + s); };
     auto tfull = [&](int b) { return bars + 8u * (2 * kStages + b); };
     auto tempty = [&](int b) { return bars + 8u * (2 * kStages + 2 + b); };
     const uint32_t drain = bars + 8u * (2 * kStages + 4);
-    uint8_t* tail = smem_raw + (bars - raw) + 8u * (2 * kStages + 5);
+    const uint32_t loads = drain + 8u;  // kGateGrad: 3 per epilogue warp
+    uint8_t* tail = smem_raw + (loads - raw) + 8u * 3 * kEpiWarps;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(tail);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int crank = (int)cluster_rank();
+    const int prank = crank & 1, leader = crank & ~1, srank = crank >> 1;
+    const int cluster = blockIdx.x / (2 * p.splits), clusters = gridDim.x / (2 * p.splits);
     const int tiles = p.m_tiles * p.n_tiles;
+    const int kb = (int)((int64_t)p.k_tiles * srank / p.splits);
+    const int ke = (int)((int64_t)p.k_tiles * (srank + 1) / p.splits);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -249,9 +423,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull(b), 1);
-            mbar_init(tempty(b), 16);  // 8 epilogue warps of each CTA
+            mbar_init(tempty(b), 2 * kEpiWarps);  // of both CTAs
         }
         mbar_init(drain, 1);
+        for (int i = 0; i < 3 * kEpiWarps; ++i) mbar_init(loads + 8u * i, 1);
         *abort_flag = 0;
         fence_mbarrier_init();
     }
@@ -265,6 +440,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    grid_launch_next();
+
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    Epi<EPI> epi{p,
+                 &tmO,
+                 &tmG,
+                 staging + (uint32_t)(warp - 2) * kSlots * kSlotBytes,
+                 loads + 24u * (warp - 2),
+                 base,
+                 lane,
+                 quad,
+                 half,
+                 prank,
+                 srank,
+                 0,
+                 0,
+                 abort_flag};
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -272,20 +464,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int s = 0;
             uint32_t ph = 0, issued = 0, par = 0;
             bool ok = true;
-            for (int tile = pair; ok && tile < tiles; tile += pairs) {
+            if (p.after) grid_wait_previous();
+            for (int tile = cluster; ok && tile < tiles; tile += clusters) {
                 int mt, nt;
                 tile_at(p, tile, mt, nt);
-                const int a0 = mt * 256 + rank * 128;
+                const int a0 = mt * 256 + prank * 128;
                 // kGate: the even CTA brings the tile's 128 gate rows, the odd one its up rows
-                const int b0 = EPI == kGate ? rank * p.F + nt * 128 : nt * 256 + rank * 128;
-                for (int kt = 0; kt < p.k_tiles; ++kt) {
+                const int b0 = EPI == kGate ? prank * p.F + nt * 128 : nt * 256 + prank * 128;
+                for (int kt = kb; kt < ke; ++kt) {
                     if (!mbar_wait(empty(s), ph ^ 1u, abort_flag)) {
                         ok = false;
                         break;
                     }
                     const uint32_t sa = base + s * kStageBytes, sb = sa + kHalfBytes;
-                    const uint32_t bar = map_to_leader(full(s));
-                    if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * kStageBytes);
+                    const uint32_t bar = map_to_rank(full(s), leader);
+                    if (prank == 0) mbar_arrive_expect_tx(full(s), 2 * kStageBytes);
                     if constexpr (AMN) {
                         tma_load_2d_pair(sa, &tmA, a0, kt * kBK, bar);
                         tma_load_2d_pair(sa + kChunkBytes, &tmA, a0 + 64, kt * kBK, bar);
@@ -306,26 +499,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!ok && rank == 0)  // copies in flight (both CTAs') land before the pair leaves
+            if (!ok && prank == 0)  // copies in flight (both CTAs') land before the pair leaves
                 for (int q = 0; q < kStages; ++q)
                     if (issued & (1u << q)) mbar_wait(full(q), (par >> q) & 1u, nullptr, 200000000ull);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer
-        if (lane == 0 && rank == 0) {
+        if (lane == 0 && prank == 0) {
             const uint32_t idesc = idesc_bf16(256, 256, AMN, BMN);
+            const uint32_t both = 3u << leader;
             int s = 0, local = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int tile = pair; ok && tile < tiles; tile += pairs, ++local) {
+            for (int tile = cluster; ok && tile < tiles; tile += clusters, ++local) {
                 const int b = local & 1;
                 if (!mbar_wait(tempty(b), (((uint32_t)local >> 1) & 1u) ^ 1u, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                for (int kt = 0; kt < p.k_tiles; ++kt) {
+                for (int kt = kb; kt < ke; ++kt) {
                     if (!mbar_wait(full(s), ph, abort_flag)) {
                         ok = false;
                         break;
@@ -338,78 +532,97 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                                 : desc_kmajor_sw128(sa + 32u * j);
                         const uint64_t bd = BMN ? desc_mnmajor_sw128(sb + 2048u * j, kChunkBytes)
                                                 : desc_kmajor_sw128(sb + 32u * j);
-                        mma_bf16_pair(tmem + 256u * b, ad, bd, idesc, (kt | j) != 0);
+                        mma_bf16_pair(tmem + 256u * b, ad, bd, idesc, kt != kb || j != 0);
                     }
-                    mma_commit_pair(empty(s));
+                    mma_commit_pair(empty(s), both);
                     if (++s == kStages) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
-                if (ok) mma_commit_pair(tfull(b));
+                if (ok) mma_commit_pair(tfull(b), both);
             }
             if (!ok) {
-                mma_commit_pair(drain);
+                mma_commit_pair(drain, both);
                 mbar_wait(drain, 0, nullptr, 200000000ull);
             }
         }
         __syncwarp();
     } else {
         // ------------------------------------------------------------ epilogue
-        const int quad = warp & 3, half = (warp - 2) >> 2;
         int local = 0;
-        for (int tile = pair; tile < tiles; tile += pairs, ++local) {
+        for (int tile = cluster; tile < tiles; tile += clusters, ++local) {
             const int b = local & 1;
             int mt, nt;
             tile_at(p, tile, mt, nt);
-            bool ok = mbar_wait(tfull(b), ((uint32_t)local >> 1) & 1u, abort_flag);
+            const int n0 = nt * (EPI == kGate ? 128 : 256);
+            const int64_t row0 = (int64_t)mt * 256 + prank * 128 + quad * 32;
+            epi.ahead(n0, row0);
+            const bool ok = mbar_wait(tfull(b), ((uint32_t)local >> 1) & 1u, abort_flag);
             if (__any_sync(0xffffffffu, !ok)) break;
             tc_fence_after();
-            epilogue_rows<EPI>(p, tmem + ((uint32_t)(quad * 32) << 16) + 256u * b,
-                               (int64_t)mt * 256 + rank * 128 + quad * 32 + lane, nt * (EPI == kGate ? 128 : 256), half);
+            const uint32_t tacc = tmem + ((uint32_t)(quad * 32) << 16) + 256u * b;
+            if (p.splits > 1) epi.share(tacc);  // the ring is free: this was the cluster's only tile
+            else if (!epi.tile(tacc, n0, row0)) break;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_cluster(map_to_leader(tempty(b)));
+            if (lane == 0) arrive_cluster(map_to_rank(tempty(b), leader));
         }
     }
+
+    if (p.splits > 1) {
+        __syncthreads();
+        cluster_sync();  // every pair's partial sums are in place
+        if (warp >= 2 && *abort_flag == 0) {
+            int mt, nt;
+            tile_at(p, cluster, mt, nt);
+            epi.tile(0, nt * (EPI == kGate ? 128 : 256), (int64_t)mt * 256 + prank * 128 + quad * 32);
+        }
+    }
+    if (warp >= 2) epi.finish();
 
     // --------------------------------------------------------------- teardown
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) record_status(p.status, MLA_ERR_TIMEOUT);
-    cluster_sync();  // no CTA leaves while its pair may still signal it
+    cluster_sync();  // no CTA leaves while another may still signal it or read its sums
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, kTmemCols);
     }
 }
 
-// Pairs that can be resident at once (some GPCs may hold an odd number of SMs).
+// Clusters of `splits` pairs that can be resident at once (a GPC may hold a
+// number of SMs that clusters do not divide).
 template <bool AMN, bool BMN, int EPI>
-int prepare_gemm(int num_sms, int device, int* pairs) {
+int resident_clusters(const DeviceInfo& di, int splits, int* out) {
     static std::mutex mu;
-    static int cache[64];
+    static int cache[64][kMaxSplits + 1];
     std::lock_guard<std::mutex> lock(mu);
-    if (cache[device] == 0) {
-        auto k = ffn_gemm_kernel<AMN, BMN, EPI>;
-        if (cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+    int& n = cache[di.device][splits];
+    if (n == 0) {
+        const auto k = (const void*)ffn_gemm_kernel<AMN, BMN, EPI>;
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<EPI>::kBytes) != cudaSuccess)
             return MLA_ERR_CUDA;
         cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)num_sms & ~1u);
+        cfg.gridDim = dim3((unsigned)(di.num_sms / (2 * splits) * 2 * splits));
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmem;
+        cfg.dynamicSmemBytes = Smem<EPI>::kBytes;
         cudaLaunchAttribute at{};
         at.id = cudaLaunchAttributeClusterDimension;
-        at.val.clusterDim.x = 2;
+        at.val.clusterDim.x = 2u * splits;
         at.val.clusterDim.y = at.val.clusterDim.z = 1;
         cfg.attrs = &at;
         cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, (const void*)k, &cfg) != cudaSuccess || n < 1) return MLA_ERR_CUDA;
-        cache[device] = n;
+        int got = 0;
+        if (cudaOccupancyMaxActiveClusters(&got, k, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            got = 0;
+        }
+        n = got > 0 ? got : -1;
     }
-    *pairs = cache[device];
-    return MLA_OK;
+    *out = n;
+    return n > 0 || splits > 1 ? MLA_OK : MLA_ERR_CUDA;
 }
 
 // ------------------------------------------------------------ few tokens
@@ -441,19 +654,6 @@ struct NarrowParams {
     int* status;
 };
 
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, int rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
 __device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
@@ -508,7 +708,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_launch_next();
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -535,7 +735,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
                 mbar_arrive_expect_tx(full(i), p.stage_bytes);
                 load_a(i, i);
             }
-            if (p.after) asm volatile("griddepcontrol.wait;" ::: "memory");
+            if (p.after) grid_wait_previous();
             for (int i = 0; i < ahead; ++i) load_b(i, i);
             bool ok = true;
             int s = 0;
@@ -682,23 +882,57 @@ struct Operand {
 // C = A B^T over `red` elements. A is [M, red] (or [red, M] when AMN), B is
 // [N, red] (or [red, N]); kGate's B holds the gate rows, then the up rows.
 template <bool AMN, bool BMN, int EPI>
-int gemm(const Operand& a, const Operand& b, GemmParams p, int64_t red, const DeviceInfo& di, cudaStream_t stream) {
+int gemm(const Operand& a, const Operand& b, GemmParams p, int64_t red, bool after, const DeviceInfo& di,
+         cudaStream_t stream) {
     p.m_tiles = (p.M + 255) / 256;
     p.n_tiles = EPI == kGate ? (p.N + 127) / 128 : (p.N + 255) / 256;
     p.k_tiles = (int)((red + kBK - 1) / kBK);
-    alignas(64) CUtensorMap ta, tb;
+    p.after = after;
+    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+    if (tiles > kI32Max / 8) return MLA_ERR_UNSUPPORTED;
+    // Split the reduction when the tiles leave pairs idle: in K steps, a pair's
+    // time is its share of them plus what the exchange of the sums costs.
+    int clusters = 0;
+    int64_t best = 0;
+    for (int s = 1; s <= kMaxSplits; ++s) {
+        int n = 0;
+        const int st = resident_clusters<AMN, BMN, EPI>(di, s, &n);
+        if (st != MLA_OK) return st;
+        if (s > 1 && (tiles > n || p.k_tiles < 4 * s)) continue;
+        const int64_t cost = s == 1 ? (tiles + n - 1) / n * p.k_tiles : (p.k_tiles + s - 1) / s + kSplitSteps;
+        if (s == 1 || cost < best) {
+            best = cost;
+            p.splits = s;
+            clusters = tiles < n ? (int)tiles : n;
+        }
+    }
+    alignas(64) CUtensorMap ta, tb, to, tg;
     int st = make_tmap_2d(&ta, a.p, 1, (uint64_t)a.cols, (uint64_t)a.rows, (uint64_t)a.ld * 2, 64, AMN ? kBK : 128, true);
     if (st == MLA_OK)
         st = make_tmap_2d(&tb, b.p, 1, (uint64_t)b.cols, (uint64_t)b.rows, (uint64_t)b.ld * 2, 64, BMN ? kBK : 128, true);
+    const uint64_t F = (uint64_t)p.F, T = (uint64_t)p.M;
+    if (st == MLA_OK)
+        st = EPI == kGateGrad ? make_tmap_3d(&to, p.out, F, 2, T, 2 * F, 4 * F, 32, 1, 32, true)
+                              : make_tmap_2d(&to, p.out, 1, (uint64_t)p.N, T, (uint64_t)p.N * 2, 32, 32, false, true);
+    const void* gu = EPI == kGateGrad ? p.gate_up : p.gate_up_out;
+    if (st == MLA_OK && EPI != kStore && gu) st = make_tmap_3d(&tg, gu, F, 2, T, 2 * F, 4 * F, 32, 1, 32, true);
+    else tg = to;
     if (st != MLA_OK) return st;
-    int pairs = 0;
-    st = prepare_gemm<AMN, BMN, EPI>(di.num_sms, di.device, &pairs);
-    if (st != MLA_OK) return st;
-    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
-    if (tiles > kI32Max / 2) return MLA_ERR_UNSUPPORTED;
-    if (tiles < pairs) pairs = (int)tiles;
-    ffn_gemm_kernel<AMN, BMN, EPI><<<2 * pairs, kThreads, kSmem, stream>>>(ta, tb, p);
-    return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(2 * p.splits * clusters));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Smem<EPI>::kBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2u * p.splits;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = after ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<AMN, BMN, EPI>, ta, tb, to, tg, p) == cudaSuccess ? MLA_OK
+                                                                                                      : MLA_ERR_CUDA;
 }
 
 // The same product for few tokens (see ffn_narrow_kernel): w is [R, red] (or
@@ -800,12 +1034,12 @@ MLAQ_API int mla_gated_ffn_fwd(const mla_ffn_shape* shape, const void* x, const 
     p.gate_up_out = static_cast<uint16_t*>(gate_up);
     const bool few = s.T <= kNarrowMax;
     st = few ? narrow<false, kGate>({w_gate_up, 2 * s.F, s.K, s.K}, {x, s.T, s.K, ld}, p, s.K, false, di, cs)
-             : gemm<false, false, kGate>({x, s.T, s.K, ld}, {w_gate_up, 2 * s.F, s.K, s.K}, p, s.K, di, cs);
+             : gemm<false, false, kGate>({x, s.T, s.K, ld}, {w_gate_up, 2 * s.F, s.K, s.K}, p, s.K, false, di, cs);
     if (st != MLA_OK) return st;
     p.N = (int)s.K;
     p.out = static_cast<uint16_t*>(y);
     if (few) return narrow<false, kStore>({w_down, s.K, s.F, s.F}, {h, s.T, s.F, s.F}, p, s.F, true, di, cs);
-    return gemm<false, false, kStore>({h, s.T, s.F, s.F}, {w_down, s.K, s.F, s.F}, p, s.F, di, cs);
+    return gemm<false, false, kStore>({h, s.T, s.F, s.F}, {w_down, s.K, s.F, s.F}, p, s.F, true, di, cs);
 }
 
 MLAQ_API int mla_gated_ffn_bwd(const mla_ffn_shape* shape, const void* dy, const void* x, const void* w_gate_up,
@@ -852,7 +1086,7 @@ MLAQ_API int mla_gated_ffn_bwd(const mla_ffn_shape* shape, const void* dy, const
         p.out = static_cast<uint16_t*>(dgate_up);
         p.gate_up = static_cast<const uint16_t*>(gate_up);
         if (few) st = narrow<true, kGateGrad>({w_down, s.K, s.F, s.F}, {dy, s.T, s.K, s.K}, p, s.K, false, di, cs);
-        else st = gemm<false, true, kGateGrad>({dy, s.T, s.K, s.K}, {w_down, s.K, s.F, s.F}, p, s.K, di, cs);
+        else st = gemm<false, true, kGateGrad>({dy, s.T, s.K, s.K}, {w_down, s.K, s.F, s.F}, p, s.K, false, di, cs);
         if (st != MLA_OK) return st;
     }
     if (dx) {
@@ -861,21 +1095,21 @@ MLAQ_API int mla_gated_ffn_bwd(const mla_ffn_shape* shape, const void* dy, const
         p.out = static_cast<uint16_t*>(dx);
         const Operand w{w_gate_up, 2 * s.F, s.K, s.K}, d{dgate_up, s.T, 2 * s.F, 2 * s.F};
         st = few ? narrow<true, kStore>(w, d, p, 2 * s.F, true, di, cs)
-                 : gemm<false, true, kStore>(d, w, p, 2 * s.F, di, cs);
+                 : gemm<false, true, kStore>(d, w, p, 2 * s.F, true, di, cs);
         if (st != MLA_OK) return st;
     }
     if (dw_gate_up) {
         p.M = (int)(2 * s.F);
         p.N = (int)s.K;
         p.out = static_cast<uint16_t*>(dw_gate_up);
-        st = gemm<true, true, kStore>({dgate_up, s.T, 2 * s.F, 2 * s.F}, {x, s.T, s.K, ld}, p, s.T, di, cs);
+        st = gemm<true, true, kStore>({dgate_up, s.T, 2 * s.F, 2 * s.F}, {x, s.T, s.K, ld}, p, s.T, true, di, cs);
         if (st != MLA_OK) return st;
     }
     if (dw_down) {
         p.M = (int)s.K;
         p.N = (int)s.F;
         p.out = static_cast<uint16_t*>(dw_down);
-        st = gemm<true, true, kStore>({dy, s.T, s.K, s.K}, {h, s.T, s.F, s.F}, p, s.T, di, cs);
+        st = gemm<true, true, kStore>({dy, s.T, s.K, s.K}, {h, s.T, s.F, s.F}, p, s.T, hidden, di, cs);
         if (st != MLA_OK) return st;
     }
     return MLA_OK;

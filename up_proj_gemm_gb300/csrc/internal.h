@@ -33,10 +33,11 @@ int make_tmap_2d(void* tmap_out /* CUtensorMap, 64 B aligned */, const void* bas
 int make_tmap_chunks(void* tmap_out, const void* base, uint64_t rows, uint64_t cols,
                      uint32_t box_rows, uint32_t box_chunks);
 
-// General 3-D bf16 map, 128-byte swizzle: dims {d0 (contiguous), d1, d2},
-// byte strides of d1 and d2, box {b0, b1, b2} (b0 * 2 bytes == 128).
+// General 3-D bf16 map, 128-byte swizzle (64-byte swizzle when swizzle64):
+// dims {d0 (contiguous), d1, d2}, byte strides of d1 and d2, box {b0, b1, b2}
+// (b0 * 2 bytes == the swizzle's span).
 int make_tmap_3d(void* tmap_out, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
-                 uint64_t stride2, uint32_t b0, uint32_t b1, uint32_t b2);
+                 uint64_t stride2, uint32_t b0, uint32_t b1, uint32_t b2, bool swizzle64 = false);
 
 // ------------------------------------------------------------- launchers
 // All launchers assume arguments were validated by the API layer.
