@@ -75,8 +75,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 // The address of another CTA's copy of a shared-memory location.
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, int rank) {
@@ -193,7 +196,7 @@ struct Epi {
     uint32_t slots, bars;     // this warp's slots; kGateGrad: a barrier per pair of them
     uint32_t sums;            // splits > 1: this CTA's partial sums, float4 [column / 4][128 rows]
     int lane, quad, half, prank, srank;
-    int used = 0;             // slots (kGateGrad: chunks) this warp has used so far
+    int used = 0;             // pairs of slots this warp has used so far
     int asked = 0;            // kGateGrad: chunks whose loads are under way
     volatile int* abort_flag;
 
@@ -201,28 +204,45 @@ struct Epi {
     static constexpr int kChunks = EPI == kGate ? 4 : 8;
     __device__ __forceinline__ int chunk(int i) const { return srank + p.splits * (half + 2 * i); }
 
-    __device__ __forceinline__ void values(uint32_t tacc, int col, uint32_t (&v)[32]) const {
-        if (p.splits == 1) {
-            tmem_ld32(tacc + col, v);
-            return;
-        }
-        float a[32];
+    template <int S>
+    __device__ __forceinline__ void add_up(uint32_t at, uint32_t (&v)[32]) const {
+        uint32_t from[S];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) a[i] = 0.f;
-        const uint32_t at = sums + 16u * ((col / 4) * 128 + quad * 32 + lane);
-        for (int s = 0; s < p.splits; ++s) {
-            const uint32_t from = map_to_rank(at, 2 * s + prank);
+        for (int s = 0; s < S; ++s) from[s] = map_to_rank(at, 2 * s + prank);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 f = ld_cluster_v4(from + 2048u * i);
-                a[4 * i] += f.x;
-                a[4 * i + 1] += f.y;
-                a[4 * i + 2] += f.z;
-                a[4 * i + 3] += f.w;
+        for (int i = 0; i < 8; i += 2) {  // 2 S loads in flight
+            float4 f[S][2];
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) f[s][k] = ld_cluster_v4(from[s] + 2048u * (i + k));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float4 a = f[0][k];
+#pragma unroll
+                for (int s = 1; s < S; ++s) {
+                    a.x += f[s][k].x;
+                    a.y += f[s][k].y;
+                    a.z += f[s][k].z;
+                    a.w += f[s][k].w;
+                }
+                v[4 * (i + k)] = __float_as_uint(a.x);
+                v[4 * (i + k) + 1] = __float_as_uint(a.y);
+                v[4 * (i + k) + 2] = __float_as_uint(a.z);
+                v[4 * (i + k) + 3] = __float_as_uint(a.w);
             }
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(a[i]);
+    }
+
+    // The 32 columns from col on of this lane's row (TMEM: complete after tmem_ld_wait).
+    __device__ __forceinline__ void values(uint32_t tacc, int col, uint32_t (&v)[32]) const {
+        const uint32_t at = sums + 16u * ((col / 4) * 128 + quad * 32 + lane);
+        switch (p.splits) {
+            case 1: tmem_ld32(tacc + col, v); break;
+            case 2: add_up<2>(at, v); break;
+            case 3: add_up<3>(at, v); break;
+            default: add_up<kMaxSplits>(at, v); break;
+        }
     }
 
     // Splits > 1: this warp's part of the accumulator, for the other CTAs to add.
@@ -248,15 +268,16 @@ struct Epi {
             sts_v4(piece(slot, k), pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
                    pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
     }
-    // Write a chunk to the next slot of the ring, which its last store has left.
-    __device__ __forceinline__ uint32_t put(const float (&v)[32]) {
-        const uint32_t slot = slots + kSlotBytes * (used++ % Smem<EPI>::kSlots);
-        if (lane == 0) bulk_wait_group_read<Smem<EPI>::kSlots - 1>();
-        __syncwarp();
-        write(slot, v);
+    // The slots written by the warp are ready for a TMA store by lane 0.
+    __device__ __forceinline__ void written() const {
         fence_proxy_async_smem();
         __syncwarp();
-        return slot;
+    }
+    // All but the newest N groups of stores have been read.
+    template <int N>
+    __device__ __forceinline__ void stores_read() const {
+        if (lane == 0) bulk_wait_group_read<N>();
+        __syncwarp();
     }
 
     // kGateGrad: fetch chunk i's gate and up products into the pair of slots of
@@ -297,22 +318,15 @@ struct Epi {
                 values(tacc, 32 * c, r);
                 values(tacc, 128 + 32 * c, ru);
                 tmem_ld_wait();
+                stores_read<0>();  // one group per chunk, in the same three slots
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     v[j] = __uint_as_float(r[j]);
                     u[j] = __uint_as_float(ru[j]);
                 }
                 if (p.gate_up_out) {
-                    const uint32_t sg = put(v);
-                    if (lane == 0) {
-                        tma_store_3d(tmG, n, 0, (int32_t)row0, sg);
-                        bulk_commit_group();
-                    }
-                    const uint32_t su = put(u);
-                    if (lane == 0) {
-                        tma_store_3d(tmG, n, 1, (int32_t)row0, su);
-                        bulk_commit_group();
-                    }
+                    write(slots, v);
+                    write(slots + kSlotBytes, u);
                 }
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
@@ -320,22 +334,42 @@ struct Epi {
                     activate<false>(p.act, v[j], a, unused);
                     v[j] = a * u[j];
                 }
-                const uint32_t sh = put(v);
+                write(slots + 2 * kSlotBytes, v);
+                written();
                 if (lane == 0) {
-                    tma_store_2d(tmO, n, (int32_t)row0, sh);
+                    if (p.gate_up_out) {
+                        tma_store_3d(tmG, n, 0, (int32_t)row0, slots);
+                        tma_store_3d(tmG, n, 1, (int32_t)row0, slots + kSlotBytes);
+                    }
+                    tma_store_2d(tmO, n, (int32_t)row0, slots + 2 * kSlotBytes);
                     bulk_commit_group();
                 }
             } else if constexpr (EPI == kStore) {
+                // two chunks at a time, in the two pairs of slots in turn
+                const bool two = has(n0, row0, i + 1);
+                const int c2 = chunk(i + 1);
+                uint32_t r2[32];
                 __syncwarp();
                 values(tacc, 32 * c, r);
+                if (two) values(tacc, 32 * c2, r2);
                 tmem_ld_wait();
+                const uint32_t slot = slots + 2 * kSlotBytes * (used++ & 1);
+                stores_read<1>();
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-                const uint32_t s = put(v);
+                write(slot, v);
+                if (two) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r2[j]);
+                    write(slot + kSlotBytes, v);
+                }
+                written();
                 if (lane == 0) {
-                    tma_store_2d(tmO, n, (int32_t)row0, s);
+                    tma_store_2d(tmO, n, (int32_t)row0, slot);
+                    if (two) tma_store_2d(tmO, n0 + 32 * c2, (int32_t)row0, slot + kSlotBytes);
                     bulk_commit_group();
                 }
+                ++i;
             } else {
                 __syncwarp();
                 values(tacc, 32 * c, r);
@@ -363,8 +397,7 @@ struct Epi {
                     sts_v4(piece(slot + kSlotBytes, k), pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3]),
                            pack_bf16x2(du[4], du[5]), pack_bf16x2(du[6], du[7]));
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
+                written();
                 if (lane == 0) {
                     tma_store_3d(tmO, n, 0, (int32_t)row0, slot);
                     tma_store_3d(tmO, n, 1, (int32_t)row0, slot + kSlotBytes);
@@ -430,16 +463,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         fence_mbarrier_init();
     }
-    if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&tmA);
-        tma_prefetch_desc(&tmB);
-    }
+    // First cluster barrier: the barriers exist (all that the producers need).
+    // Second: the TMEM of both CTAs does; it is allocated while the first loads
+    // are on their way.
+    __syncwarp();
+    cluster_arrive();
     if (warp == 1) tmem_alloc_pair(smem_u32((const void*)tmem_slot), kTmemCols);
+    cluster_wait();
     tc_fence_before();
-    __syncthreads();
-    cluster_sync();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    cluster_arrive();
     grid_launch_next();
 
     const int quad = warp & 3, half = (warp - 2) >> 2;
@@ -504,7 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (issued & (1u << q)) mbar_wait(full(q), (par >> q) & 1u, nullptr, 200000000ull);
         }
         __syncwarp();
+        cluster_wait();
     } else if (warp == 1) {
+        cluster_wait();
+        tc_fence_after();
+        const uint32_t tmem = *tmem_slot;
         // ---------------------------------------------------------- MMA issuer
         if (lane == 0 && prank == 0) {
             const uint32_t idesc = idesc_bf16(256, 256, AMN, BMN);
@@ -549,6 +585,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
+        cluster_wait();
+        tc_fence_after();
+        const uint32_t tmem = *tmem_slot;
         // ------------------------------------------------------------ epilogue
         int local = 0;
         for (int tile = cluster; tile < tiles; tile += clusters, ++local) {
@@ -588,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();  // no CTA leaves while another may still signal it or read its sums
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, kTmemCols);
+        tmem_dealloc_pair(*tmem_slot, kTmemCols);
     }
 }
 
@@ -686,6 +725,26 @@ __global__ void __launch_bounds__(kNarrowThreads)
     const int steps = (int)((int64_t)p.k_tiles * (rank + 1) / p.splits) - kb;
     const int r0 = tile * (EPI == kGate ? 64 : 128);
 
+    const uint64_t weights_once = l2_evict_first_policy();
+    auto load_a = [&](int i, int s) {
+        const uint32_t sa = base + s * p.stage_bytes;
+        const int k = (kb + i) * kBK;
+        mbar_arrive_expect_tx(full(s), p.stage_bytes);
+        if constexpr (EPI == kGate) {
+            tma_load_2d_hint(sa, &tmA, k, r0, full(s), weights_once);
+            tma_load_2d_hint(sa + kNarrowABytes / 2, &tmA, k, p.F + r0, full(s), weights_once);
+        } else if constexpr (AMN) {
+            tma_load_2d_hint(sa, &tmA, r0, k, full(s), weights_once);
+            tma_load_2d_hint(sa + kChunkBytes, &tmA, r0 + 64, k, full(s), weights_once);
+        } else {
+            tma_load_2d_hint(sa, &tmA, k, r0, full(s), weights_once);
+        }
+    };
+    auto load_b = [&](int i, int s) {
+        tma_load_2d(base + s * p.stage_bytes + kNarrowABytes, &tmB, (kb + i) * kBK, 0, full(s));
+    };
+    const int ahead = steps < p.stages ? steps : p.stages;
+
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(full(s), 1);
@@ -695,11 +754,9 @@ __global__ void __launch_bounds__(kNarrowThreads)
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbarrier_init();
+        for (int i = 0; i < ahead; ++i) load_a(i, i);  // under the rest of the setup
     }
-    if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&tmA);
-        tma_prefetch_desc(&tmB);
-    }
+    __syncwarp();
     if (warp == 1) {
         tmem_alloc(smem_u32((const void*)tmem_slot), p.tmem_cols);
         tmem_relinquish();
@@ -713,28 +770,6 @@ __global__ void __launch_bounds__(kNarrowThreads)
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
-            const uint64_t weights_once = l2_evict_first_policy();
-            auto load_a = [&](int i, int s) {
-                const uint32_t sa = base + s * p.stage_bytes;
-                const int k = (kb + i) * kBK;
-                if constexpr (EPI == kGate) {
-                    tma_load_2d_hint(sa, &tmA, k, r0, full(s), weights_once);
-                    tma_load_2d_hint(sa + kNarrowABytes / 2, &tmA, k, p.F + r0, full(s), weights_once);
-                } else if constexpr (AMN) {
-                    tma_load_2d_hint(sa, &tmA, r0, k, full(s), weights_once);
-                    tma_load_2d_hint(sa + kChunkBytes, &tmA, r0 + 64, k, full(s), weights_once);
-                } else {
-                    tma_load_2d_hint(sa, &tmA, k, r0, full(s), weights_once);
-                }
-            };
-            auto load_b = [&](int i, int s) {
-                tma_load_2d(base + s * p.stage_bytes + kNarrowABytes, &tmB, (kb + i) * kBK, 0, full(s));
-            };
-            const int ahead = steps < p.stages ? steps : p.stages;
-            for (int i = 0; i < ahead; ++i) {
-                mbar_arrive_expect_tx(full(i), p.stage_bytes);
-                load_a(i, i);
-            }
             if (p.after) grid_wait_previous();
             for (int i = 0; i < ahead; ++i) load_b(i, i);
             bool ok = true;
@@ -746,7 +781,6 @@ __global__ void __launch_bounds__(kNarrowThreads)
                     ok = false;
                     break;
                 }
-                mbar_arrive_expect_tx(full(s), p.stage_bytes);
                 load_a(i, s);
                 load_b(i, s);
                 if (++s == p.stages) {
