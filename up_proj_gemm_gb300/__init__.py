@@ -105,6 +105,8 @@ _SIGS = {
 def lib() -> ctypes.CDLL:
     """The loaded libmlaq.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(library_path):

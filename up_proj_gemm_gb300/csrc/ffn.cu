@@ -21,6 +21,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 
@@ -1003,8 +1004,13 @@ int narrow(const Operand& w, const Operand& tokens, const GemmParams& g, int64_t
     if (st != MLA_OK) return st;
     const auto kernel = ffn_narrow_kernel<AMN, EPI>;
     const size_t smem = 1024 + kNarrowRing + 512;
-    if (cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return MLA_ERR_CUDA;
+    static std::atomic<uint64_t> allowed{0};  // devices whose kernel has its shared-memory limit set
+    const uint64_t bit = 1ull << di.device;
+    if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+        if (cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+            return MLA_ERR_CUDA;
+        allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(tiles * p.splits));
     cfg.blockDim = dim3(kNarrowThreads);

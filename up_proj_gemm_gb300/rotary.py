@@ -39,16 +39,39 @@ def rope_sections(sections) -> bytes:
     return bytes(a for a, n in enumerate(sections) for _ in range(n))
 
 
-def _axes_args(cos, sin, pos, axes, Dr, T, dev):
-    """Check the tables, the positions [A, T] and the Dr/2 pairs' axes; the axes as bytes."""
-    _need(cos, "cos", torch.float32, dev, ndim=2)
-    _need(sin, "sin", torch.float32, dev, shape=cos.shape)
-    _need(pos, "pos", torch.int32, dev, ndim=2)
+_bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _refuse_tables(cos, sin, pos, axes, Dr, T, dev):
+    """Name what is wrong with the tables, the positions [A, T] or the Dr/2 pairs' axes."""
+    _need(cos, "cos", _f32, dev, ndim=2)
+    _need(sin, "sin", _f32, dev, shape=cos.shape)
+    _need(pos, "pos", _i32, dev, ndim=2)
     if pos.shape[1] != T:
         raise ValueError(f"pos must be [axes, {T}], got {list(pos.shape)}")
-    if len(axes) != Dr // 2:
-        raise ValueError(f"axes must name the axis of each of the {Dr // 2} pairs, got {len(axes)}")
-    return bytes(axes)
+    raise ValueError(f"axes must name the axis of each of the {Dr // 2} pairs, got {len(axes)}")
+
+
+def _tables_ok(cos, sin, pos, axes, Dr, T, dev):
+    """The checks of _refuse_tables in one expression: a call's checks cost as much as its launch."""
+    return (isinstance(cos, torch.Tensor) and isinstance(sin, torch.Tensor) and isinstance(pos, torch.Tensor)
+            and cos.dtype is _f32 and sin.dtype is _f32 and pos.dtype is _i32 and cos.dim() == 2
+            and sin.shape == cos.shape and pos.dim() == 2 and pos.shape[1] == T and len(axes) == Dr // 2
+            and cos.is_cuda and sin.is_cuda and pos.is_cuda
+            and cos.device == dev and sin.device == dev and pos.device == dev
+            and cos.is_contiguous() and sin.is_contiguous() and pos.is_contiguous())
+
+
+def _refuse_x(x, Dr, inverse, sum_heads):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dtype not in (_bf16, _f32):
+        raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
+    if not x.is_cuda or x.dim() != 3 or (x.shape[2] > 1 and x.stride(2) != 1):
+        raise ValueError("x must be a 3-D CUDA tensor [T, H, D] with unit inner stride")
+    if sum_heads and not inverse:
+        raise ValueError("sum_heads sums gradients: it needs inverse=True")
+    raise ValueError(f"Dr must be in 1..{x.shape[2]}, got {Dr}")
 
 
 def rope_axes(x, cos, sin, pos, axes, Dr, inverse=False, sum_heads=False, out=None, status=None, stream=None):
@@ -60,37 +83,34 @@ def rope_axes(x, cos, sin, pos, axes, Dr, inverse=False, sum_heads=False, out=No
     applies the Jacobian transpose (the gradient), ``sum_heads`` (with
     inverse) the transpose of the heads' sum, [T, 1, D]: the gradient of a key
     part that all heads share. ``out`` may be a strided view."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    if x.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
-    if not x.is_cuda or x.dim() != 3 or (x.shape[2] > 1 and x.stride(2) != 1):
-        raise ValueError("x must be a 3-D CUDA tensor [T, H, D] with unit inner stride")
-    if sum_heads and not inverse:
-        raise ValueError("sum_heads sums gradients: it needs inverse=True")
+    if not (isinstance(x, torch.Tensor) and (x.dtype is _bf16 or x.dtype is _f32) and x.is_cuda and x.dim() == 3
+            and (x.shape[2] <= 1 or x.stride(2) == 1) and (inverse or not sum_heads) and 0 < Dr <= x.shape[2]):
+        _refuse_x(x, Dr, inverse, sum_heads)
     T, H, D = x.shape
-    if not 0 < Dr <= D:
-        raise ValueError(f"Dr must be in 1..{D}, got {Dr}")
+    in_t, in_h, _ = x.stride()
     dev = x.device
-    axes = _axes_args(cos, sin, pos, axes, Dr, T, dev)
-    _status(status, dev)
+    if not _tables_ok(cos, sin, pos, axes, Dr, T, dev):
+        _refuse_tables(cos, sin, pos, axes, Dr, T, dev)
+    if status is not None:
+        _status(status, dev)
     Ho = 1 if sum_heads else H
     if out is None:
         out = torch.empty((T, Ho, D), dtype=x.dtype, device=dev)
         out_t, out_h = Ho * D, D
     else:
-        if not isinstance(out, torch.Tensor) or out.dtype != x.dtype:
+        if not isinstance(out, torch.Tensor) or out.dtype is not x.dtype:
             raise TypeError(f"out must be a {x.dtype} tensor")
         if tuple(out.shape) != (T, Ho, D):
             raise ValueError(f"out must be {[T, Ho, D]}, got {list(out.shape)}")
         if not out.is_cuda or out.device != dev or (D > 1 and out.stride(2) != 1):
             raise ValueError(f"out must be on {dev} with unit inner stride")
         out_t, out_h = out.stride(0), out.stride(1)
-    s = RopeAxesShape(T, H, D - Dr, Dr, pos.shape[0], cos.shape[0], cos.shape[1], x.stride(0) if T > 1 else 0,
-                      x.stride(1) if H > 1 else 0, out_t if T > 1 else 0, out_h if Ho > 1 else 0, 0)
-    _call(lib().mla_rope_axes, "mla_rope_axes", ctypes.byref(s), 0 if x.dtype == torch.float32 else 1,
-          (2 if sum_heads else 1) if inverse else 0, _ptr(x), _ptr(cos), _ptr(sin), _ptr(pos), axes, _ptr(out),
-          _ptr(status), _stream(dev, stream))
+    rows, width = cos.shape
+    s = RopeAxesShape(T, H, D - Dr, Dr, pos.shape[0], rows, width, in_t if T > 1 else 0, in_h if H > 1 else 0,
+                      out_t if T > 1 else 0, out_h if Ho > 1 else 0, 0)
+    _call(lib().mla_rope_axes, "mla_rope_axes", ctypes.byref(s), 0 if x.dtype is _f32 else 1,
+          (2 if sum_heads else 1) if inverse else 0, x.data_ptr(), cos.data_ptr(), sin.data_ptr(), pos.data_ptr(),
+          bytes(axes), out.data_ptr(), _ptr(status), _stream(dev, stream))
     return out
 
 
@@ -101,16 +121,21 @@ def rope_axes_table(cos, sin, pos, axes, Dr, cos_out=None, sin_out=None, status=
     if not isinstance(pos, torch.Tensor) or pos.dim() != 2:
         raise ValueError("pos must be an int32 tensor [A, T]")
     dev = pos.device
-    T = pos.shape[1]
-    axes = _axes_args(cos, sin, pos, axes, Dr, T, dev)
-    _status(status, dev)
+    A, T = pos.shape
+    if not _tables_ok(cos, sin, pos, axes, Dr, T, dev):
+        _refuse_tables(cos, sin, pos, axes, Dr, T, dev)
+    if status is not None:
+        _status(status, dev)
     if cos_out is None:
-        cos_out = torch.empty((T, Dr), dtype=torch.float32, device=dev)
+        cos_out = torch.empty((T, Dr), dtype=_f32, device=dev)
+    else:
+        _need(cos_out, "cos_out", _f32, dev, shape=(T, Dr))
     if sin_out is None:
-        sin_out = torch.empty((T, Dr), dtype=torch.float32, device=dev)
-    _need(cos_out, "cos_out", torch.float32, dev, shape=(T, Dr))
-    _need(sin_out, "sin_out", torch.float32, dev, shape=(T, Dr))
-    s = RopeAxesShape(T, 1, 0, Dr, pos.shape[0], cos.shape[0], cos.shape[1], 0, 0, 0, 0, 0)
-    _call(lib().mla_rope_axes_table, "mla_rope_axes_table", ctypes.byref(s), _ptr(cos), _ptr(sin), _ptr(pos), axes,
-          _ptr(cos_out), _ptr(sin_out), _ptr(status), _stream(dev, stream))
+        sin_out = torch.empty((T, Dr), dtype=_f32, device=dev)
+    else:
+        _need(sin_out, "sin_out", _f32, dev, shape=(T, Dr))
+    rows, width = cos.shape
+    s = RopeAxesShape(T, 1, 0, Dr, A, rows, width, 0, 0, 0, 0, 0)
+    _call(lib().mla_rope_axes_table, "mla_rope_axes_table", ctypes.byref(s), cos.data_ptr(), sin.data_ptr(),
+          pos.data_ptr(), bytes(axes), cos_out.data_ptr(), sin_out.data_ptr(), _ptr(status), _stream(dev, stream))
     return cos_out, sin_out
