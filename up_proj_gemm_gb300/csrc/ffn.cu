@@ -76,7 +76,21 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ int cluster_id() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+    return (int)r;
+}
+__device__ __forceinline__ int cluster_count() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(r));
+    return (int)r;
+}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// without a release (360 cycles): for warps that wrote nothing another CTA reads
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
     cluster_arrive();
@@ -141,26 +155,52 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint32_t mask) {
 }
 
 // ------------------------------------------------------------- activations
-// act(g) and its derivative; sigmoid through exp and a fast division (a few
-// ulp of float32, far below the bf16 results).
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// act(g) and its derivative. The sigmoid is 1 / (1 + 2^(-z log2 e)) by the
+// hardware's exponential and reciprocal (a few ulp of float32, far below the
+// bf16 results; 2^x overflows to infinity, whose reciprocal is 0). The
+// activation is a template argument: an epilogue is bound by its instructions.
+__device__ __forceinline__ float sigmoid(float z) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
 
-template <bool GRAD>
-__device__ __forceinline__ void activate(int act, float g, float& a, float& da) {
-    if (act == MLA_ACT_SILU) {
+template <int ACT>
+__device__ __forceinline__ float activate(float g) {
+    if constexpr (ACT == MLA_ACT_SILU) return g * sigmoid(g);
+    else if constexpr (ACT == MLA_ACT_GELU) return g * (0.5f * erfcf(-0.70710678f * g));
+    // 0.5 g (1 + tanh(z)) = g sigmoid(2 z), z = sqrt(2/pi) (g + 0.044715 g^3)
+    else return g * sigmoid(g * fmaf(0.0713548162f, g * g, 1.59576912f));
+}
+
+template <int ACT>
+__device__ __forceinline__ void activate_grad(float g, float& a, float& da) {
+    if constexpr (ACT == MLA_ACT_SILU) {
         const float s = sigmoid(g);
         a = g * s;
-        if constexpr (GRAD) da = s * (1.f + g * (1.f - s));
-    } else if (act == MLA_ACT_GELU) {
+        da = fmaf(a, 1.f - s, s);
+    } else if constexpr (ACT == MLA_ACT_GELU) {
         const float c = 0.5f * erfcf(-0.70710678f * g);
         a = g * c;
-        if constexpr (GRAD) da = c + g * 0.39894228f * __expf(-0.5f * g * g);
-    } else {  // 0.5 g (1 + tanh(z)) = g sigmoid(2 z), z = sqrt(2/pi) (g + 0.044715 g^3)
-        const float k = 1.59576912f;  // 2 sqrt(2/pi)
-        const float s = sigmoid(k * (g + 0.044715f * g * g * g));
+        da = fmaf(g * 0.39894228f, __expf(-0.5f * g * g), c);
+    } else {
+        const float g2 = g * g, s = sigmoid(g * fmaf(0.0713548162f, g2, 1.59576912f));
         a = g * s;
-        if constexpr (GRAD) da = s + g * s * (1.f - s) * k * (1.f + 0.134145f * g * g);
+        da = fmaf(a * (1.f - s), fmaf(0.214064449f, g2, 1.59576912f), s);
     }
+}
+
+// f with the activation as a compile-time constant.
+template <int ACT>
+struct ActTag {
+    static constexpr int value = ACT;
+};
+template <typename Fn>
+__device__ __forceinline__ void with_act(int act, Fn&& f) {
+    if (act == MLA_ACT_SILU) f(ActTag<MLA_ACT_SILU>{});
+    else if (act == MLA_ACT_GELU) f(ActTag<MLA_ACT_GELU>{});
+    else f(ActTag<MLA_ACT_GELU_TANH>{});
 }
 
 __device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
@@ -170,9 +210,6 @@ __device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
         v[2 * i] = bf16lo_to_f32(u[i]);
         v[2 * i + 1] = bf16hi_to_f32(u[i]);
     }
-}
-__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
-    st_global_v4(p, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
 // Tiles in groups of 8 row tiles, columns inside a group: the tiles that run
@@ -329,12 +366,10 @@ struct Epi {
                     write(slots, v);
                     write(slots + kSlotBytes, u);
                 }
+                with_act(p.act, [&](auto act) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    float a, unused;
-                    activate<false>(p.act, v[j], a, unused);
-                    v[j] = a * u[j];
-                }
+                    for (int j = 0; j < 32; ++j) v[j] = activate<decltype(act)::value>(v[j]) * u[j];
+                });
                 write(slots + 2 * kSlotBytes, v);
                 written();
                 if (lane == 0) {
@@ -380,24 +415,26 @@ struct Epi {
                 if (__any_sync(0xffffffffu, !ok)) return false;
                 ++used;
                 const uint32_t slot = slots + kSlotBytes * (2 * pair);
+                with_act(p.act, [&](auto act) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float g[8], u[8], dg[8], du[8];
-                    unpack8(lds_v4(piece(slot, k)), g);
-                    unpack8(lds_v4(piece(slot + kSlotBytes, k)), u);
+                    for (int k = 0; k < 4; ++k) {
+                        float g[8], u[8];
+                        unpack8(lds_v4(piece(slot, k)), g);
+                        unpack8(lds_v4(piece(slot + kSlotBytes, k)), u);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float d = __uint_as_float(r[8 * k + j]);
-                        float a, da;
-                        activate<true>(p.act, g[j], a, da);
-                        dg[j] = d * u[j] * da;
-                        du[j] = d * a;
+                        for (int j = 0; j < 8; ++j) {
+                            const float d = __uint_as_float(r[8 * k + j]);
+                            float a, da;
+                            activate_grad<decltype(act)::value>(g[j], a, da);
+                            g[j] = d * u[j] * da;
+                            u[j] = d * a;
+                        }
+                        sts_v4(piece(slot, k), pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]),
+                               pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7]));
+                        sts_v4(piece(slot + kSlotBytes, k), pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]),
+                               pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
                     }
-                    sts_v4(piece(slot, k), pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3]),
-                           pack_bf16x2(dg[4], dg[5]), pack_bf16x2(dg[6], dg[7]));
-                    sts_v4(piece(slot + kSlotBytes, k), pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3]),
-                           pack_bf16x2(du[4], du[5]), pack_bf16x2(du[6], du[7]));
-                }
+                });
                 written();
                 if (lane == 0) {
                     tma_store_3d(tmO, n, 0, (int32_t)row0, slot);
@@ -414,7 +451,7 @@ struct Epi {
     __device__ __forceinline__ void finish() {
         if constexpr (EPI == kGateGrad)
             for (; used < asked; ++used) mbar_wait(bars + 8u * (used % 3), (uint32_t)(used / 3) & 1u, nullptr, 200000000ull);
-        if (lane == 0) bulk_wait_group_all();
+        if (lane == 0) bulk_wait_group_read<0>();
         __syncwarp();
     }
 };
@@ -445,35 +482,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int crank = (int)cluster_rank();
     const int prank = crank & 1, leader = crank & ~1, srank = crank >> 1;
-    const int cluster = blockIdx.x / (2 * p.splits), clusters = gridDim.x / (2 * p.splits);
+    const int cluster = cluster_id(), clusters = cluster_count();
     const int tiles = p.m_tiles * p.n_tiles;
-    const int kb = (int)((int64_t)p.k_tiles * srank / p.splits);
-    const int ke = (int)((int64_t)p.k_tiles * (srank + 1) / p.splits);
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
+    // The setup runs once per tile when there are few: the lanes of a warp
+    // write the barriers together, nothing is divided, nothing released that
+    // nobody reads (2,000 cycles before the first load became 500).
+    if (warp == 0) {
+        for (int i = lane; i < 2 * kStages + 5 + 3 * kEpiWarps; i += 32) {
+            const bool te = i == 2 * kStages + 2 || i == 2 * kStages + 3;  // tempty: the epilogue warps of both CTAs
+            mbar_init(bars + 8u * i, te ? 2 * kEpiWarps : 1);
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(tfull(b), 1);
-            mbar_init(tempty(b), 2 * kEpiWarps);  // of both CTAs
-        }
-        mbar_init(drain, 1);
-        for (int i = 0; i < 3 * kEpiWarps; ++i) mbar_init(loads + 8u * i, 1);
-        *abort_flag = 0;
+        if (lane == 0) *abort_flag = 0;
         fence_mbarrier_init();
+    } else if (warp == 2 && lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmO);
+        if (EPI != kStore) tma_prefetch_desc(&tmG);
     }
     // First cluster barrier: the barriers exist (all that the producers need).
     // Second: the TMEM of both CTAs does; it is allocated while the first loads
     // are on their way.
     __syncwarp();
-    cluster_arrive();
-    if (warp == 1) tmem_alloc_pair(smem_u32((const void*)tmem_slot), kTmemCols);
-    cluster_wait();
-    tc_fence_before();
-    cluster_arrive();
+    cluster_arrive_relaxed();
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32((const void*)tmem_slot), kTmemCols);
+        tc_fence_before();
+        cluster_wait();
+        cluster_arrive();
+    } else {
+        cluster_wait();
+        cluster_arrive_relaxed();
+    }
     grid_launch_next();
+    int kb = 0, ke = p.k_tiles;
+    if (p.splits > 1) {
+        kb = p.k_tiles * srank / p.splits;
+        ke = p.k_tiles * (srank + 1) / p.splits;
+    }
 
     const int quad = warp & 3, half = (warp - 2) >> 2;
     Epi<EPI> epi{p,
@@ -721,9 +768,9 @@ __global__ void __launch_bounds__(kNarrowThreads)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = p.splits > 1 ? (int)cluster_rank() : 0;
-    const int tile = blockIdx.x / p.splits;
-    const int kb = (int)((int64_t)p.k_tiles * rank / p.splits);
-    const int steps = (int)((int64_t)p.k_tiles * (rank + 1) / p.splits) - kb;
+    const int tile = cluster_id();
+    const int kb = p.splits > 1 ? p.k_tiles * rank / p.splits : 0;
+    const int steps = (p.splits > 1 ? p.k_tiles * (rank + 1) / p.splits : p.k_tiles) - kb;
     const int r0 = tile * (EPI == kGate ? 64 : 128);
 
     const uint64_t weights_once = l2_evict_first_policy();
@@ -842,6 +889,11 @@ __global__ void __launch_bounds__(kNarrowThreads)
         }
     }
     __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, p.tmem_cols);
+    }
     if (p.splits > 1) cluster_sync();
 
     // this CTA adds and finishes its share of the tokens
@@ -870,12 +922,10 @@ __global__ void __launch_bounds__(kNarrowThreads)
         }
         if constexpr (EPI == kGate) {
             float h[4];
+            with_act(p.act, [&](auto act) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float act, unused;
-                activate<false>(p.act, a[j], act, unused);
-                h[j] = act * b[j];
-            }
+                for (int j = 0; j < 4; ++j) h[j] = activate<decltype(act)::value>(a[j]) * b[j];
+            });
             store4(p.out + (int64_t)t * p.F + r, h);
             if (p.gate_up_out) {
                 store4(p.gate_up_out + (int64_t)t * 2 * p.F + r, a);
@@ -885,13 +935,15 @@ __global__ void __launch_bounds__(kNarrowThreads)
             float g[4], u[4], dg[4], du[4];
             load4(p.gate_up + (int64_t)t * 2 * p.F + r, g);
             load4(p.gate_up + (int64_t)t * 2 * p.F + p.F + r, u);
+            with_act(p.act, [&](auto act) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float act, dact;
-                activate<true>(p.act, g[j], act, dact);
-                dg[j] = a[j] * u[j] * dact;
-                du[j] = a[j] * act;
-            }
+                for (int j = 0; j < 4; ++j) {
+                    float v, dv;
+                    activate_grad<decltype(act)::value>(g[j], v, dv);
+                    dg[j] = a[j] * u[j] * dv;
+                    du[j] = a[j] * v;
+                }
+            });
             store4(p.out + (int64_t)t * 2 * p.F + r, dg);
             store4(p.out + (int64_t)t * 2 * p.F + p.F + r, du);
         } else {
@@ -901,11 +953,9 @@ __global__ void __launch_bounds__(kNarrowThreads)
 
     // --------------------------------------------------------------- teardown
     if (threadIdx.x == 0 && failed) record_status(p.status, MLA_ERR_TIMEOUT);
-    if (p.splits > 1) cluster_sync();  // the others have read this CTA's sums
-    else __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, p.tmem_cols);
+    if (p.splits > 1) {  // the others have read this CTA's sums
+        cluster_arrive_relaxed();
+        cluster_wait();
     }
 }
 
