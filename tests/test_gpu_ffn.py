@@ -255,3 +255,52 @@ def test_few_tokens_in_a_graph(cuda_device):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, torch.roll(y, 1, 0))
+
+
+# many tokens: 256 x 256 tiles and their edges, reductions whole and split over 2, 3 and 4 pairs, tiles in several waves
+MANY = [(1025, 264, 392), (1030, 1288, 520), (1100, 2056, 264), (1281, 136, 4104), (1111, 72, 5000), (2049, 520, 264),
+        (1300, 1096, 1032), (5000, 8, 72), (3001, 136, 328)]
+
+
+@pytest.mark.parametrize("T,K,F", MANY)
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_many_tokens(cuda_device, T, K, F, act):
+    x, wgu, wd, dy = make(T, K, F, pitch=8, seed=T + K)
+    st = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    y, gu, h = mlaq.gated_ffn_fwd(x, wgu, wd, act=act, save=True, status=st)
+    check_forward(x, wgu, wd, act, y, gu, h)
+    assert torch.equal(mlaq.gated_ffn_fwd(x, wgu, wd, act=act), y)
+    dgu = torch.empty((T, 2 * F), dtype=bf16, device=cuda_device)
+    dx, dwgu, dwd = mlaq.gated_ffn_bwd(dy, x, wgu, wd, gu, h, act=act, dgate_up=dgu, status=st)
+    mlaq.check_status(st)
+    dh, e = product(dy, wd.t())
+    g, u = gu.to(f64).split(F, 1)
+    a, da = act64(g, act)
+    check(dgu[:, :F], dh * u * da, e * (u * da).abs() + 64 * U * (dh * u).abs() * (1 + g.abs()), "dg")
+    check(dgu[:, F:], dh * a, e * a.abs() + 64 * U * (dh * a).abs() + 32 * U * (dh * g).abs() * 1e-3, "du")
+    check(dx, *product(dgu, wgu.t()), "dx")
+    check(dwgu, *product(dgu.t(), x.t()), "dw_gate_up")
+    check(dwd, *product(dy.t(), h.t()), "dw_down")
+
+
+def test_many_tokens_parts_and_guards(cuda_device):
+    """Each gradient alone gives the bits of all together, between guard rows that stay."""
+    T, K, F = 1111, 328, 520
+    x, wgu, wd, dy = make(T, K, F)
+
+    def guarded(rows, cols):
+        b = torch.full((rows + 2, cols), 7.0, dtype=bf16, device=cuda_device)
+        return b, b[1:-1]
+
+    bufs = [guarded(T, K), guarded(T, 2 * F), guarded(T, F), guarded(T, K), guarded(2 * F, K), guarded(K, F),
+            guarded(T, 2 * F)]
+    (_, y), (_, gu), (_, h), (_, dx), (_, dwgu), (_, dwd), (_, dgu) = bufs
+    mlaq.gated_ffn_fwd(x, wgu, wd, save=True, y=y, gate_up=gu, h=h)
+    mlaq.gated_ffn_bwd(dy, x, wgu, wd, gu, h, dx=dx, dw_gate_up=dwgu, dw_down=dwd, dgate_up=dgu)
+    check_forward(x, wgu, wd, "silu", y, gu, h)
+    for b, _ in bufs:
+        assert (b[0] == 7.0).all() and (b[-1] == 7.0).all()
+    a = mlaq.gated_ffn_bwd(dy, None, wgu, wd, gu, None, dw_gate_up=False, dw_down=False)
+    b = mlaq.gated_ffn_bwd(dy, x, None, wd, gu, None, dx=False, dw_down=False)
+    c = mlaq.gated_ffn_bwd(dy, None, None, None, None, h, dx=False, dw_gate_up=False)
+    assert torch.equal(a[0], dx) and torch.equal(b[1], dwgu) and torch.equal(c[2], dwd)

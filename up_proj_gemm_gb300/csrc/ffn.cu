@@ -58,13 +58,20 @@ struct Smem {
     static constexpr size_t kBytes = 1024 + kRing + (size_t)kEpiWarps * kSlots * kSlotBytes + 512;
 };
 
+// A result and its tiles; kGate: N = F (a tile holds 128 of them).
+struct Result {
+    int M, N, m_tiles, n_tiles;
+};
+
 struct GemmParams {
-    int M, N;                 // of the result; kGate: N = F (a tile holds 128 of them)
-    int k_tiles, m_tiles, n_tiles;
+    // Both weight gradients are one launch: their tiles (over the same T) fill
+    // the last wave together. One result otherwise, and no tiles in the second.
+    Result r[2];
+    int tiles0, tiles;        // of the first result, of both
+    int k_tiles;
     int splits;               // parts of the reduction, each a pair of the cluster
     int after;                // an operand comes from the grid before this one
     int F, act;
-    uint16_t* out;            // kStore [M, N], kGate h [M, F], kGateGrad [M, 2F]
     uint16_t* gate_up_out;    // kGate: [M, 2F] or null
     const uint16_t* gate_up;  // kGateGrad: [M, 2F]
     int* status;
@@ -212,15 +219,19 @@ __device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
     }
 }
 
-// Tiles in groups of 8 row tiles, columns inside a group: the tiles that run
+// Which result a tile is of, and where. Tiles in groups of 8 row tiles, columns inside a group: the tiles that run
 // at the same time span about as many rows of A as of B, which L2 holds.
 constexpr int kGroupM = 8;
-__device__ __forceinline__ void tile_at(const GemmParams& p, int tile, int& mt, int& nt) {
-    const int per = kGroupM * p.n_tiles;
+__device__ __forceinline__ int tile_at(const GemmParams& p, int tile, int& mt, int& nt) {
+    const int job = tile >= p.tiles0;
+    tile -= job ? p.tiles0 : 0;
+    const int m_tiles = job ? p.r[1].m_tiles : p.r[0].m_tiles;
+    const int per = kGroupM * (job ? p.r[1].n_tiles : p.r[0].n_tiles);
     const int g = tile / per, r = tile - g * per;
-    const int rows = p.m_tiles - g * kGroupM < kGroupM ? p.m_tiles - g * kGroupM : kGroupM;
+    const int rows = m_tiles - g * kGroupM < kGroupM ? m_tiles - g * kGroupM : kGroupM;
     nt = r / rows;
     mt = g * kGroupM + (r - nt * rows);
+    return job;
 }
 
 // One epilogue warp: rows row0 .. row0 + 31 of the tile, lane = row. Its chunks
@@ -237,6 +248,7 @@ struct Epi {
     int used = 0;             // pairs of slots this warp has used so far
     int asked = 0;            // kGateGrad: chunks whose loads are under way
     volatile int* abort_flag;
+    int M = 0, N = 0;         // of the tile's result
 
     // chunks of this warp: of the tile's 8 (kGate: 4 of gates with their 4 of up products)
     static constexpr int kChunks = EPI == kGate ? 4 : 8;
@@ -333,7 +345,7 @@ struct Epi {
         ++asked;
     }
     __device__ __forceinline__ bool has(int n0, int64_t row0, int i) const {
-        return chunk(i) < kChunks && n0 + 32 * chunk(i) < p.N && row0 < p.M;
+        return chunk(i) < kChunks && n0 + 32 * chunk(i) < N && row0 < M;
     }
 
     // Before the tile's accumulator is ready.
@@ -463,7 +475,8 @@ template <bool AMN, bool BMN, int EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmG,
-                    const GemmParams p) {
+                    const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
+                    const __grid_constant__ CUtensorMap tmO1, const GemmParams p) {
     constexpr int kStages = Smem<EPI>::kStages, kSlots = Smem<EPI>::kSlots;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -483,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int crank = (int)cluster_rank();
     const int prank = crank & 1, leader = crank & ~1, srank = crank >> 1;
     const int cluster = cluster_id(), clusters = cluster_count();
-    const int tiles = p.m_tiles * p.n_tiles;
+    const int tiles = p.tiles;
 
     // The setup runs once per tile when there are few: the lanes of a warp
     // write the barriers together, nothing is divided, nothing released that
@@ -499,7 +512,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
         tma_prefetch_desc(&tmO);
-        if (EPI != kStore) tma_prefetch_desc(&tmG);
     }
     // First cluster barrier: the barriers exist (all that the producers need).
     // Second: the TMEM of both CTAs does; it is allocated while the first loads
@@ -547,7 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (p.after) grid_wait_previous();
             for (int tile = cluster; ok && tile < tiles; tile += clusters) {
                 int mt, nt;
-                tile_at(p, tile, mt, nt);
+                const int job = tile_at(p, tile, mt, nt);
+                const CUtensorMap *mapA = AMN && job ? &tmA1 : &tmA, *mapB = AMN && job ? &tmB1 : &tmB;
                 const int a0 = mt * 256 + prank * 128;
                 // kGate: the even CTA brings the tile's 128 gate rows, the odd one its up rows
                 const int b0 = EPI == kGate ? prank * p.F + nt * 128 : nt * 256 + prank * 128;
@@ -560,16 +573,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t bar = map_to_rank(full(s), leader);
                     if (prank == 0) mbar_arrive_expect_tx(full(s), 2 * kStageBytes);
                     if constexpr (AMN) {
-                        tma_load_2d_pair(sa, &tmA, a0, kt * kBK, bar);
-                        tma_load_2d_pair(sa + kChunkBytes, &tmA, a0 + 64, kt * kBK, bar);
+                        tma_load_2d_pair(sa, mapA, a0, kt * kBK, bar);
+                        tma_load_2d_pair(sa + kChunkBytes, mapA, a0 + 64, kt * kBK, bar);
                     } else {
-                        tma_load_2d_pair(sa, &tmA, kt * kBK, a0, bar);
+                        tma_load_2d_pair(sa, mapA, kt * kBK, a0, bar);
                     }
                     if constexpr (BMN) {
-                        tma_load_2d_pair(sb, &tmB, b0, kt * kBK, bar);
-                        tma_load_2d_pair(sb + kChunkBytes, &tmB, b0 + 64, kt * kBK, bar);
+                        tma_load_2d_pair(sb, mapB, b0, kt * kBK, bar);
+                        tma_load_2d_pair(sb + kChunkBytes, mapB, b0 + 64, kt * kBK, bar);
                     } else {
-                        tma_load_2d_pair(sb, &tmB, kt * kBK, b0, bar);
+                        tma_load_2d_pair(sb, mapB, kt * kBK, b0, bar);
                     }
                     issued |= 1u << s;
                     par = (par & ~(1u << s)) | (ph << s);
@@ -641,7 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int tile = cluster; tile < tiles; tile += clusters, ++local) {
             const int b = local & 1;
             int mt, nt;
-            tile_at(p, tile, mt, nt);
+            const int job = tile_at(p, tile, mt, nt);
+            epi.M = job ? p.r[1].M : p.r[0].M;
+            epi.N = job ? p.r[1].N : p.r[0].N;
+            if (AMN) epi.tmO = job ? &tmO1 : &tmO;
             const int n0 = nt * (EPI == kGate ? 128 : 256);
             const int64_t row0 = (int64_t)mt * 256 + prank * 128 + quad * 32;
             epi.ahead(n0, row0);
@@ -730,7 +746,8 @@ constexpr uint32_t kNarrowABytes = 128u * 128u;       // 128 weight rows of one 
 constexpr size_t kNarrowRing = 108 * 1024;            // two CTAs fit an SM
 
 struct NarrowParams {
-    int T, N, R;              // tokens, padded tokens, weight rows (kGate: channels)
+    int T, N, R;              // tokens, tokens of a tile (a multiple of 16), weight rows (kGate: channels)
+    int token_tiles;
     int k_tiles, stages, splits;
     uint32_t stage_bytes, tmem_cols;
     int after;                // the tokens come from the grid before this one
@@ -768,12 +785,13 @@ __global__ void __launch_bounds__(kNarrowThreads)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = p.splits > 1 ? (int)cluster_rank() : 0;
-    const int tile = cluster_id();
+    const int tile = cluster_id() / p.token_tiles, t0 = (cluster_id() - tile * p.token_tiles) * p.N;
     const int kb = p.splits > 1 ? p.k_tiles * rank / p.splits : 0;
     const int steps = (p.splits > 1 ? p.k_tiles * (rank + 1) / p.splits : p.k_tiles) - kb;
     const int r0 = tile * (EPI == kGate ? 64 : 128);
 
-    const uint64_t weights_once = l2_evict_first_policy();
+    // weights that one token tile reads are gone after it
+    const uint64_t weights_once = p.token_tiles == 1 ? l2_evict_first_policy() : l2_evict_last_policy();
     auto load_a = [&](int i, int s) {
         const uint32_t sa = base + s * p.stage_bytes;
         const int k = (kb + i) * kBK;
@@ -789,7 +807,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
         }
     };
     auto load_b = [&](int i, int s) {
-        tma_load_2d(base + s * p.stage_bytes + kNarrowABytes, &tmB, (kb + i) * kBK, 0, full(s));
+        tma_load_2d(base + s * p.stage_bytes + kNarrowABytes, &tmB, (kb + i) * kBK, t0, full(s));
     };
     const int ahead = steps < p.stages ? steps : p.stages;
 
@@ -897,13 +915,14 @@ __global__ void __launch_bounds__(kNarrowThreads)
     if (p.splits > 1) cluster_sync();
 
     // this CTA adds and finishes its share of the tokens
-    const int t_begin = p.T * rank / p.splits, t_end = p.T * (rank + 1) / p.splits;
+    const int n_tok = p.T - t0 < p.N ? p.T - t0 : p.N;
+    const int t_begin = n_tok * rank / p.splits, t_end = n_tok * (rank + 1) / p.splits;
     constexpr int kQuads = EPI == kGate ? 16 : 32;
     const bool failed = *abort_flag != 0;
     for (int i = threadIdx.x; i < (t_end - t_begin) * kQuads && !failed; i += kNarrowThreads) {
-        const int t = t_begin + i / kQuads, q = i % kQuads, r = r0 + 4 * q;
+        const int tl = t_begin + i / kQuads, t = t0 + tl, q = i % kQuads, r = r0 + 4 * q;
         if (r >= p.R) continue;
-        const uint32_t at = base + 512u * t + 16u * q;
+        const uint32_t at = base + 512u * tl + 16u * q;
         float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
         for (int s = 0; s < p.splits; ++s) {
             const uint32_t from = p.splits > 1 ? map_to_rank(at, s) : at;
@@ -966,15 +985,35 @@ struct Operand {
 
 // C = A B^T over `red` elements. A is [M, red] (or [red, M] when AMN), B is
 // [N, red] (or [red, N]); kGate's B holds the gate rows, then the up rows.
+struct Product {
+    Operand a, b;
+    int64_t M, N;
+    void* out;
+};
+
+int64_t pair_tiles(int64_t M, int64_t N) { return ((M + 255) / 256) * ((N + 255) / 256); }
+
+// One product, or (AMN) two over the same reduction. `beside`: tiles of a
+// product that could have been in the launch and is not; it counts where the
+// split is chosen, so a gradient's bits do not depend on which others are asked
+// for.
 template <bool AMN, bool BMN, int EPI>
-int gemm(const Operand& a, const Operand& b, GemmParams p, int64_t red, bool after, const DeviceInfo& di,
-         cudaStream_t stream) {
-    p.m_tiles = (p.M + 255) / 256;
-    p.n_tiles = EPI == kGate ? (p.N + 127) / 128 : (p.N + 255) / 256;
+int gemm(const Product* jobs, int count, GemmParams p, int64_t red, bool after, const DeviceInfo& di,
+         cudaStream_t stream, int64_t beside = 0) {
+    int64_t tiles = 0;
+    for (int j = 0; j < count; ++j) {
+        Result& r = p.r[j];
+        r.M = (int)jobs[j].M;
+        r.N = (int)jobs[j].N;
+        r.m_tiles = (r.M + 255) / 256;
+        r.n_tiles = EPI == kGate ? (r.N + 127) / 128 : (r.N + 255) / 256;
+        tiles += (int64_t)r.m_tiles * r.n_tiles;
+        if (j == 0) p.tiles0 = (int)tiles;
+    }
+    if (tiles > kI32Max / 8) return MLA_ERR_UNSUPPORTED;
+    p.tiles = (int)tiles;
     p.k_tiles = (int)((red + kBK - 1) / kBK);
     p.after = after;
-    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
-    if (tiles > kI32Max / 8) return MLA_ERR_UNSUPPORTED;
     // Split the reduction when the tiles leave pairs idle: in K steps, a pair's
     // time is its share of them plus what the exchange of the sums costs.
     int clusters = 0;
@@ -983,26 +1022,35 @@ int gemm(const Operand& a, const Operand& b, GemmParams p, int64_t red, bool aft
         int n = 0;
         const int st = resident_clusters<AMN, BMN, EPI>(di, s, &n);
         if (st != MLA_OK) return st;
-        if (s > 1 && (tiles > n || p.k_tiles < 4 * s)) continue;
-        const int64_t cost = s == 1 ? (tiles + n - 1) / n * p.k_tiles : (p.k_tiles + s - 1) / s + kSplitSteps;
+        const int64_t all = tiles + beside;
+        if (s > 1 && (all > n || p.k_tiles < 4 * s)) continue;
+        const int64_t cost = s == 1 ? (all + n - 1) / n * p.k_tiles : (p.k_tiles + s - 1) / s + kSplitSteps;
         if (s == 1 || cost < best) {
             best = cost;
             p.splits = s;
             clusters = tiles < n ? (int)tiles : n;
         }
     }
-    alignas(64) CUtensorMap ta, tb, to, tg;
-    int st = make_tmap_2d(&ta, a.p, 1, (uint64_t)a.cols, (uint64_t)a.rows, (uint64_t)a.ld * 2, 64, AMN ? kBK : 128, true);
-    if (st == MLA_OK)
-        st = make_tmap_2d(&tb, b.p, 1, (uint64_t)b.cols, (uint64_t)b.rows, (uint64_t)b.ld * 2, 64, BMN ? kBK : 128, true);
-    const uint64_t F = (uint64_t)p.F, T = (uint64_t)p.M;
-    if (st == MLA_OK)
-        st = EPI == kGateGrad ? make_tmap_3d(&to, p.out, F, 2, T, 2 * F, 4 * F, 32, 1, 32, true)
-                              : make_tmap_2d(&to, p.out, 1, (uint64_t)p.N, T, (uint64_t)p.N * 2, 32, 32, false, true);
+    alignas(64) CUtensorMap ta[2]{}, tb[2]{}, to[2]{}, tg{};
+    const uint64_t F = (uint64_t)p.F, T = (uint64_t)jobs[0].M;
+    for (int j = 0; j < count; ++j) {
+        const Operand &a = jobs[j].a, &b = jobs[j].b;
+        const uint64_t M = (uint64_t)jobs[j].M, N = (uint64_t)jobs[j].N;
+        int st = make_tmap_2d(&ta[j], a.p, 1, (uint64_t)a.cols, (uint64_t)a.rows, (uint64_t)a.ld * 2, 64,
+                              AMN ? kBK : 128, true);
+        if (st == MLA_OK)
+            st = make_tmap_2d(&tb[j], b.p, 1, (uint64_t)b.cols, (uint64_t)b.rows, (uint64_t)b.ld * 2, 64,
+                              BMN ? kBK : 128, true);
+        if (st == MLA_OK)
+            st = EPI == kGateGrad ? make_tmap_3d(&to[j], jobs[j].out, F, 2, T, 2 * F, 4 * F, 32, 1, 32, true)
+                                  : make_tmap_2d(&to[j], jobs[j].out, 1, N, M, N * 2, 32, 32, false, true);
+        if (st != MLA_OK) return st;
+    }
     const void* gu = EPI == kGateGrad ? p.gate_up : p.gate_up_out;
-    if (st == MLA_OK && EPI != kStore && gu) st = make_tmap_3d(&tg, gu, F, 2, T, 2 * F, 4 * F, 32, 1, 32, true);
-    else tg = to;
-    if (st != MLA_OK) return st;
+    if (EPI != kStore && gu) {
+        const int st = make_tmap_3d(&tg, gu, F, 2, T, 2 * F, 4 * F, 32, 1, 32, true);
+        if (st != MLA_OK) return st;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(2 * p.splits * clusters));
     cfg.blockDim = dim3(kThreads);
@@ -1016,23 +1064,39 @@ int gemm(const Operand& a, const Operand& b, GemmParams p, int64_t red, bool aft
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = after ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<AMN, BMN, EPI>, ta, tb, to, tg, p) == cudaSuccess ? MLA_OK
-                                                                                                      : MLA_ERR_CUDA;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<AMN, BMN, EPI>, ta[0], tb[0], to[0], tg, ta[1],
+                                             tb[1], to[1], p);
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+// Whether a product of T tokens and `rows` weight rows (kGate: channels) takes
+// the few-token kernel. Up to 128 tokens the bound is reading the weights; up
+// to 1024 it serves as a kernel of smaller tiles while they fill half the SMs
+// at most (T = 256, K = 1024, F = 2048: forward 19.0 against 20.6 us, backward
+// 29.0 against 36.9; T = 777, K = 1536, F = 4096, over twice that many tiles:
+// backward 83.5 against 69.1). Beyond 1024 the pairs' larger tiles win even
+// where they are few (T = 4000, K = 256, F = 512: 12.9 against 15.6).
+template <int EPI>
+bool few_tokens(int64_t T, int64_t rows, const DeviceInfo& di) {
+    if (T <= kNarrowMax) return true;
+    const int64_t tiles = EPI == kGate ? (rows + 63) / 64 : (rows + 127) / 128;
+    return T <= 1024 && 2 * tiles * ((T + kNarrowMax - 1) / kNarrowMax) <= di.num_sms;
 }
 
 // The same product for few tokens (see ffn_narrow_kernel): w is [R, red] (or
 // [red, R] when AMN), tokens [T, red]. after: the tokens are the output of the
 // launch before this one.
 template <bool AMN, int EPI>
-int narrow(const Operand& w, const Operand& tokens, const GemmParams& g, int64_t red, bool after, const DeviceInfo& di,
-           cudaStream_t stream) {
+int narrow(const Product& job, const GemmParams& g, int64_t red, bool after, const DeviceInfo& di, cudaStream_t stream) {
+    const Operand &w = job.b, &tokens = job.a;
     NarrowParams p{};
-    p.T = g.M;
-    p.N = (g.M + 15) / 16 * 16;
-    p.R = g.N;
+    p.T = (int)job.M;
+    p.token_tiles = (p.T + kNarrowMax - 1) / kNarrowMax;
+    p.N = ((p.T + p.token_tiles - 1) / p.token_tiles + 15) / 16 * 16;
+    p.R = (int)job.N;
     p.F = g.F;
     p.act = g.act;
-    p.out = g.out;
+    p.out = static_cast<uint16_t*>(job.out);
     p.gate_up_out = g.gate_up_out;
     p.gate_up = g.gate_up;
     p.status = g.status;
@@ -1044,7 +1108,9 @@ int narrow(const Operand& w, const Operand& tokens, const GemmParams& g, int64_t
     while ((int)p.tmem_cols < p.N) p.tmem_cols *= 2;
     const int tiles = EPI == kGate ? (p.R + 63) / 64 : (p.R + 127) / 128;
     p.splits = 1;
-    while (p.splits < 8 && tiles * p.splits < di.num_sms && p.k_tiles >= 4 * p.splits) p.splits *= 2;
+    const int64_t ctas = (int64_t)tiles * p.token_tiles;
+    if (ctas > kI32Max / 8) return MLA_ERR_UNSUPPORTED;
+    while (p.splits < 8 && ctas * p.splits < di.num_sms && p.k_tiles >= 4 * p.splits) p.splits *= 2;
     alignas(64) CUtensorMap ta, tb;
     const uint32_t box_rows = AMN ? kBK : (EPI == kGate ? 64 : 128);
     int st = make_tmap_2d(&ta, w.p, 1, (uint64_t)w.cols, (uint64_t)w.rows, (uint64_t)w.ld * 2, 64, box_rows, true);
@@ -1062,7 +1128,7 @@ int narrow(const Operand& w, const Operand& tokens, const GemmParams& g, int64_t
         allowed.fetch_or(bit, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(tiles * p.splits));
+    cfg.gridDim = dim3((unsigned)(ctas * p.splits));
     cfg.blockDim = dim3(kNarrowThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -1118,18 +1184,14 @@ MLAQ_API int mla_gated_ffn_fwd(const mla_ffn_shape* shape, const void* x, const 
     p.F = (int)s.F;
     p.act = s.act;
     p.status = dev_status;
-    p.M = (int)s.T;
-    p.N = (int)s.F;
-    p.out = static_cast<uint16_t*>(h);
     p.gate_up_out = static_cast<uint16_t*>(gate_up);
-    const bool few = s.T <= kNarrowMax;
-    st = few ? narrow<false, kGate>({w_gate_up, 2 * s.F, s.K, s.K}, {x, s.T, s.K, ld}, p, s.K, false, di, cs)
-             : gemm<false, false, kGate>({x, s.T, s.K, ld}, {w_gate_up, 2 * s.F, s.K, s.K}, p, s.K, false, di, cs);
+    const Product up{{x, s.T, s.K, ld}, {w_gate_up, 2 * s.F, s.K, s.K}, s.T, s.F, h};
+    const Product down{{h, s.T, s.F, s.F}, {w_down, s.K, s.F, s.F}, s.T, s.K, y};
+    st = few_tokens<kGate>(s.T, s.F, di) ? narrow<false, kGate>(up, p, s.K, false, di, cs)
+                       : gemm<false, false, kGate>(&up, 1, p, s.K, false, di, cs);
     if (st != MLA_OK) return st;
-    p.N = (int)s.K;
-    p.out = static_cast<uint16_t*>(y);
-    if (few) return narrow<false, kStore>({w_down, s.K, s.F, s.F}, {h, s.T, s.F, s.F}, p, s.F, true, di, cs);
-    return gemm<false, false, kStore>({h, s.T, s.F, s.F}, {w_down, s.K, s.F, s.F}, p, s.F, true, di, cs);
+    return few_tokens<kStore>(s.T, s.K, di) ? narrow<false, kStore>(down, p, s.F, true, di, cs)
+                         : gemm<false, false, kStore>(&down, 1, p, s.F, true, di, cs);
 }
 
 MLAQ_API int mla_gated_ffn_bwd(const mla_ffn_shape* shape, const void* dy, const void* x, const void* w_gate_up,
@@ -1169,39 +1231,26 @@ MLAQ_API int mla_gated_ffn_bwd(const mla_ffn_shape* shape, const void* dy, const
     p.F = (int)s.F;
     p.act = s.act;
     p.status = dev_status;
-    const bool few = s.T <= kNarrowMax;
+    p.gate_up = static_cast<const uint16_t*>(gate_up);
+    const Operand oy{dy, s.T, s.K, s.K}, og{dgate_up, s.T, 2 * s.F, 2 * s.F};
     if (hidden) {
-        p.M = (int)s.T;
-        p.N = (int)s.F;
-        p.out = static_cast<uint16_t*>(dgate_up);
-        p.gate_up = static_cast<const uint16_t*>(gate_up);
-        if (few) st = narrow<true, kGateGrad>({w_down, s.K, s.F, s.F}, {dy, s.T, s.K, s.K}, p, s.K, false, di, cs);
-        else st = gemm<false, true, kGateGrad>({dy, s.T, s.K, s.K}, {w_down, s.K, s.F, s.F}, p, s.K, false, di, cs);
+        const Product q{oy, {w_down, s.K, s.F, s.F}, s.T, s.F, dgate_up};
+        st = few_tokens<kGateGrad>(s.T, s.F, di) ? narrow<true, kGateGrad>(q, p, s.K, false, di, cs)
+                           : gemm<false, true, kGateGrad>(&q, 1, p, s.K, false, di, cs);
         if (st != MLA_OK) return st;
     }
     if (dx) {
-        p.M = (int)s.T;
-        p.N = (int)s.K;
-        p.out = static_cast<uint16_t*>(dx);
-        const Operand w{w_gate_up, 2 * s.F, s.K, s.K}, d{dgate_up, s.T, 2 * s.F, 2 * s.F};
-        st = few ? narrow<true, kStore>(w, d, p, 2 * s.F, true, di, cs)
-                 : gemm<false, true, kStore>(d, w, p, 2 * s.F, true, di, cs);
+        const Product q{og, {w_gate_up, 2 * s.F, s.K, s.K}, s.T, s.K, dx};
+        st = few_tokens<kStore>(s.T, s.K, di) ? narrow<true, kStore>(q, p, 2 * s.F, true, di, cs)
+                           : gemm<false, true, kStore>(&q, 1, p, 2 * s.F, true, di, cs);
         if (st != MLA_OK) return st;
     }
-    if (dw_gate_up) {
-        p.M = (int)(2 * s.F);
-        p.N = (int)s.K;
-        p.out = static_cast<uint16_t*>(dw_gate_up);
-        st = gemm<true, true, kStore>({dgate_up, s.T, 2 * s.F, 2 * s.F}, {x, s.T, s.K, ld}, p, s.T, true, di, cs);
-        if (st != MLA_OK) return st;
-    }
-    if (dw_down) {
-        p.M = (int)s.K;
-        p.N = (int)s.F;
-        p.out = static_cast<uint16_t*>(dw_down);
-        st = gemm<true, true, kStore>({dy, s.T, s.K, s.K}, {h, s.T, s.F, s.F}, p, s.T, hidden, di, cs);
-        if (st != MLA_OK) return st;
-    }
+    Product dw[2];
+    int count = 0;
+    if (dw_gate_up) dw[count++] = {og, {x, s.T, s.K, ld}, 2 * s.F, s.K, dw_gate_up};
+    if (dw_down) dw[count++] = {oy, {h, s.T, s.F, s.F}, s.K, s.F, dw_down};
+    const int64_t beside = (dw_gate_up ? 0 : pair_tiles(2 * s.F, s.K)) + (dw_down ? 0 : pair_tiles(s.K, s.F));
+    if (count) return gemm<true, true, kStore>(dw, count, p, s.T, hidden, di, cs, beside);
     return MLA_OK;
 }
 
