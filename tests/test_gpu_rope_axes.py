@@ -204,3 +204,32 @@ def test_gradients(cuda_device):
         d[t, :, c] = 0.5
         diff = float(loss(x[:, :1].expand(-1, 3, -1).to(f64) + d) - loss(x[:, :1].expand(-1, 3, -1).to(f64) - d))
         assert abs(float(shared.grad[t, 0, c]) - diff) <= 8 * 2.0 ** -24 * 100
+
+
+# more heads and rows than are resident at once: the path that gathers a block's table entries, its scalar and its wide
+# form, runs of many tokens, and runs cut short by the table's room
+ROWS = [(2100, 64, 16, 32, 3, 0), (1700, 33, 7, 6, 2, 1), (300, 20, 600, 250, 3, 3), (200, 130, 128, 256, 3, 0),
+        (12000, 17, 0, 32, 4, 0), (1111, 50, 40, 48, 3, 8)]
+
+
+@pytest.mark.parametrize("T,H,Dn,Dr,A,pad", ROWS)
+@pytest.mark.parametrize("dtype", [bf16, f32])
+@pytest.mark.parametrize("mode", ["apply", "inverse", "sum"])
+def test_many_rows(cuda_device, T, H, Dn, Dr, A, pad, dtype, mode):
+    x, cos, sin, pos, axes = make(T, H, Dn, Dr, A, dtype, seed=T, pad=pad)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    out = mlaq.rope_axes(x, cos, sin, pos, axes, Dr, inverse=mode != "apply", sum_heads=mode == "sum", status=status)
+    mlaq.check_status(status)
+    check(out, *reference(x, cos, sin, pos, axes, Dr, mode))
+
+
+def test_many_rows_report_a_bad_position(cuda_device):
+    x, cos, sin, pos, axes = make(2100, 64, 16, 32, 2, bf16)
+    axes = [0, 1] * 8
+    ref, e = reference(x, cos, sin, pos, axes, 32, "apply")
+    pos[1, 1500] = 97
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    out = mlaq.rope_axes(x, cos, sin, pos, axes, 32, status=status)
+    assert int(status) == mlaq.STATUS["MLA_ERR_POS_RANGE"]
+    ok = torch.arange(2100, device=cuda_device) != 1500
+    check(out[ok], ref[ok], e[ok])
