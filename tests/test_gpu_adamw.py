@@ -280,3 +280,28 @@ def test_graph_replay(cuda_device):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(s[k][0], w) for k, w in zip("pmv", want))
+
+
+def test_random_rounding_keeps_nans_and_infinities(cuda_device):
+    """A NaN or an infinite parameter stays one when it is rounded at random, whatever its bits and neighbours."""
+    p = torch.ones(64, dtype=bf16, device=cuda_device)
+    p[3], p[17], p[40] = float("nan"), float("inf"), -float("inf")
+    p.view(torch.int16)[50] = -1  # a NaN with every bit set
+    s = [torch.zeros(64, device=cuda_device) for _ in range(2)]
+    plan = mlaq.adamw_plan([p], [torch.ones(64, dtype=bf16, device=cuda_device)], [s[0]], [s[1]])
+    mlaq.adamw_step(plan, 1, seed=7, lr=1e-3, weight_decay=0.0)
+    bad = torch.zeros(64, dtype=torch.bool, device=cuda_device)
+    bad[[3, 50]] = True
+    assert torch.equal(torch.isnan(p), bad) and p[17] == float("inf") and p[40] == -float("inf")
+    rest = torch.ones(64, dtype=torch.bool, device=cuda_device)
+    rest[[3, 17, 40, 50]] = False
+    assert ((p[rest].double() - 0.999).abs() <= 2.0 ** -8).all()
+
+
+def test_gradients_beyond_the_range_of_their_square(cuda_device):
+    """v' overflows: it counts as the largest float32, and the parameters stay finite."""
+    p, m, v = torch.ones(8, device=cuda_device), torch.zeros(8, device=cuda_device), torch.zeros(8, device=cuda_device)
+    g = torch.full((8,), 1e30, device=cuda_device)
+    g[1] = 1.0
+    mlaq.adamw_step(mlaq.adamw_plan([p], [g], [m], [v]), 1, lr=1e-3, betas=(0.9, 0.95), weight_decay=0.0)
+    assert torch.isfinite(p).all() and torch.isinf(v[0]) and torch.isfinite(v[1])

@@ -221,15 +221,29 @@ __device__ __forceinline__ void update(const StepParams& q, float gs, const floa
 }
 
 // The bits of a bf16 parameter rounded up or down at random, in the upper
-// half of the word (a NaN's bits must not carry into the sign).
+// half of the word.
 __device__ __forceinline__ uint32_t bf16_random(float p, uint32_t mixed) {
-    const uint32_t up = (mixed * 0x3C6EF373u) >> 16;
-    return __float_as_uint(p) + (p == p ? up : 0u);
+    return __float_as_uint(p) + ((mixed * 0x3C6EF373u) >> 16);
+}
+
+// The largest of three magnitudes, NaN when one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // N parameters of a bf16 tensor rounded at random and stored.
 template <int N, bool VEC>
 __device__ __forceinline__ void store_random(uint16_t* p, int n, const float (&v)[N], const uint32_t (&mixed)[N]) {
+    // the addition would carry a NaN's bits into its sign: a group that holds one is rounded to nearest
+    float am = fabsf(v[0]);
+#pragma unroll
+    for (int i = 1; i < N; i += 2) am = max3_nan(am, v[i], v[i + 1 < N ? i + 1 : i]);
+    if (am != am) {
+        store_n<N, VEC>(p, n, v);
+        return;
+    }
     if constexpr (VEC) {
 #pragma unroll
         for (int i = 0; i < N; i += 4)
@@ -342,13 +356,6 @@ __device__ __forceinline__ void codes_random(const float (&v)[8], int e, const u
     for (int w = 0; w < 2; ++w)  // the top bytes of four words
         codes[w] = __byte_perm(__byte_perm(top[4 * w], top[4 * w + 1], 0x0073),
                                __byte_perm(top[4 * w + 2], top[4 * w + 3], 0x0073), 0x5410);
-}
-
-// The largest of three magnitudes, NaN when one of them is.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-    float r;
-    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
 }
 
 // 8 of a block's 32 values (the other 24 in three neighbouring lanes); v may
