@@ -146,8 +146,10 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) rope_axes_kernel(const _
     const int64_t r_end = r_begin + p.rows_per_block < p.rows ? r_begin + p.rows_per_block : p.rows;
     const int t_first = (int)((uint32_t)r_begin / (uint32_t)p.H);
     const int toks = (int)((uint32_t)(r_end - 1) / (uint32_t)p.H) - t_first + 1;
-    const E* in = static_cast<const E*>(p.in);
-    E* out = static_cast<E*>(p.out);
+    const int h_first = (int)((uint32_t)r_begin - (uint32_t)t_first * (uint32_t)p.H);
+    const int step_t = lanes / p.H, step_h = lanes - step_t * p.H;
+    const E* in = static_cast<const E*>(p.in) + t_first * p.in_t;
+    E* out = static_cast<E*>(p.out) + t_first * p.out_t;
     bool filled = false;
     const int rounds = narrow ? 1 : (slots + kThreads - 1) / kThreads;
     for (int k0 = 0; k0 < rounds; ++k0) {
@@ -159,16 +161,23 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) rope_axes_kernel(const _
         const int ca = pair ? p.Dn + i0 : s * VE;
         const int cb = pair ? ca + half : (s + n_copy2) * VE;
         const bool two = works && (pair || s + n_copy2 < n_copy);
-        int64_t r = works ? r_begin + lane : r_end;
+        // the lane's next row, in tokens of the run and heads, and how far it moves
+        int left = works ? ((int)(r_end - r_begin) - lane + lanes - 1) / lanes : 0;  // rows of this lane
+        int tn = (h_first + lane) / p.H, hn = h_first + lane - tn * p.H;
         do {
             Raw<E, VE> a[kUnroll], b[kUnroll];
             int t[kUnroll], h[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int64_t ru = r + (int64_t)u * lanes;
-                if (ru >= r_end) continue;
-                t[u] = (int)((uint32_t)ru / (uint32_t)p.H);
-                h[u] = (int)((uint32_t)ru - (uint32_t)t[u] * (uint32_t)p.H);
+                t[u] = tn;
+                h[u] = hn;
+                tn += step_t;
+                hn += step_h;
+                if (hn >= p.H) {
+                    hn -= p.H;
+                    ++tn;
+                }
+                if (u >= left) continue;
                 const E* x = in + t[u] * p.in_t + h[u] * p.in_h;
                 a[u].load(x + ca);
                 if (two) b[u].load(x + cb);
@@ -204,9 +213,9 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) rope_axes_kernel(const _
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                if (r + (int64_t)u * lanes >= r_end) continue;
+                if (u >= left) continue;
                 if (pair) {
-                    const float* c = table + (t[u] - t_first) * 2 * p.Dr + i0;
+                    const float* c = table + t[u] * 2 * p.Dr + i0;
                     float c0[VE], s0[VE], c1[VE], s1[VE], x[VE], y[VE];
                     from_table<VE>(c, c0);
                     from_table<VE>(c + half, c1);
@@ -225,8 +234,8 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) rope_axes_kernel(const _
                 a[u].store(o + ca);
                 if (two) b[u].store(o + cb);
             }
-            r += (int64_t)lanes * kUnroll;
-        } while (r < r_end);
+            left -= kUnroll;
+        } while (left > 0);
     }
 }
 
@@ -287,15 +296,16 @@ __global__ void __launch_bounds__(kThreads) rope_few_kernel(const __grid_constan
 // largest power of two that fits the warp beside the slots; the rest of the
 // warp takes other tokens. (A block per token with sums in shared memory waited
 // for itself: [8190, 8, 128] bf16 18.1 us.)
-constexpr int kSumHeads = 4;  // heads in flight per lane
+constexpr int kSumThreads = 128;
+constexpr int kSumHeads = 4;  // heads in flight per lane (5 blocks per SM; 8 with 2 heads lost a third at D = 192)
 
 template <typename E, int VE>
-__global__ void __launch_bounds__(kThreads) rope_sum_kernel(const __grid_constant__ RopeParams p, int hl, int per_warp) {
+__global__ void __launch_bounds__(kSumThreads, 5) rope_sum_kernel(const __grid_constant__ RopeParams p, int hl, int per_warp) {
     const int half = p.Dr / 2;
     const int n_copy = p.Dn / VE, n_copy2 = (n_copy + 1) / 2;
     const int slots = n_copy2 + half / VE;
     const int lane = threadIdx.x & 31;
-    const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+    const int64_t warp = ((int64_t)blockIdx.x * kSumThreads + threadIdx.x) >> 5;
     const int width = slots < 32 ? slots : 32;            // lanes side by side over the slots
     const int tw = lane / (width * hl);                   // token of the warp
     const int h0 = (lane - tw * width * hl) / width;      // first head of the lane
@@ -405,8 +415,8 @@ int launch_rows(RopeParams p, bool sum, int num_sms, cudaStream_t stream) {
         while (2 * hl * width <= 32 && hl < p.H) hl *= 2;
         const int per_warp = 32 / (width * hl);
         const int64_t warps = (p.T + per_warp - 1) / per_warp;
-        const int64_t grid = (warps * 32 + kThreads - 1) / kThreads;
-        rope_sum_kernel<E, VE><<<(unsigned)grid, kThreads, 0, stream>>>(p, hl, per_warp);
+        const int64_t grid = (warps * 32 + kSumThreads - 1) / kSumThreads;
+        rope_sum_kernel<E, VE><<<(unsigned)grid, kSumThreads, 0, stream>>>(p, hl, per_warp);
     } else if (p.H <= kFewHeads || p.rows * ((p.Dn / VE + 1) / 2 + p.Dr / 2 / VE) <= (int64_t)num_sms * 2048) {
         const int slots = (p.Dn / VE + 1) / 2 + p.Dr / 2 / VE;
         const int64_t grid = (p.rows * slots + kThreads - 1) / kThreads;
