@@ -14,6 +14,7 @@ wgrad, plus the bias gradient.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 import os
 import threading
@@ -54,6 +55,7 @@ class MlaError(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
+_calls = None  # the compiled calls of the layer operators, once the library is loaded (None: not built)
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 class KvShape(ctypes.Structure):
@@ -104,7 +106,7 @@ _SIGS = {
 
 def lib() -> ctypes.CDLL:
     """The loaded libmlaq.so (raises if it has not been built)."""
-    global _lib
+    global _lib, _calls
     if _lib is not None:
         return _lib
     with _lock:
@@ -118,6 +120,11 @@ def lib() -> ctypes.CDLL:
                 f = getattr(l, name)
                 f.restype = res
                 f.argtypes = args
+            try:
+                _calls = importlib.import_module("._calls", __name__)
+                _calls.load(library_path)
+            except ImportError:
+                _calls = None
             _lib = l
     return _lib
 

@@ -2,7 +2,10 @@
 
 Each CUDA translation unit under ``csrc/`` is compiled in parallel into
 ``_build/*.o`` and linked into ``libmlaq.so`` next to this file. Only
-symbols marked MLAQ_API in ``include/mlaq.h`` are exported.
+symbols marked MLAQ_API in ``include/mlaq.h`` are exported. ``csrc/calls.cpp``
+becomes ``_calls.so`` (g++, torch's headers): the layer operators' calls
+without the interpreter in between. It adds speed and nothing else: where it
+cannot be built, the ctypes binding serves those calls too.
 """
 from __future__ import annotations
 
@@ -11,12 +14,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmlaq.so")
+CALLS = os.path.join(HERE, "_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -33,7 +38,7 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
-        os.path.join(CSRC, "*.h")) + [os.path.join(ROOT, "include", "mlaq.h"), __file__]
+        os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cpp")) + [os.path.join(ROOT, "include", "mlaq.h"), __file__]
 
 
 def up_to_date() -> bool:
@@ -41,6 +46,27 @@ def up_to_date() -> bool:
         return False
     t = os.path.getmtime(LIB)
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _build_calls() -> None:
+    """Compile _calls.so against the installed torch; report a failure and go on without it."""
+    import torch
+    t = os.path.dirname(torch.__file__)
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           "-I", os.path.join(t, "include"), "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           os.path.join(CSRC, "calls.cpp"), "-o", tmp, "-L", os.path.join(t, "lib"), "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode == 0:
+        os.replace(tmp, CALLS)
+    else:
+        if os.path.exists(CALLS):
+            os.remove(CALLS)  # built for another source
+        print(f"calls.cpp was not built; the ctypes binding serves its calls:\n{r.stderr[-2000:]}")
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -61,7 +87,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        calls = ex.submit(_build_calls)
         results = list(ex.map(compile_one, _sources()))
+        calls.result()
     if verbose:
         for _, log in results:
             print(log)

@@ -10,6 +10,8 @@ import ctypes
 
 import torch
 
+import up_proj_gemm_gb300 as _pkg
+
 from . import _call, _need, _ptr, _SIGS, _status, _stream, lib
 
 __all__ = ["FfnShape", "ACTIVATIONS", "gated_ffn_fwd", "gated_ffn_bwd"]
@@ -60,10 +62,15 @@ def gated_ffn_fwd(x, w_gate_up, w_down, act="silu", save=False, gate_up=None, h=
     rows, then F up rows), w_down [K, F] bf16; act "silu", "gelu" or
     "gelu_tanh". save=True returns (y, gate_up [T, 2F], h [T, F]), what
     gated_ffn_bwd needs. h is also the scratch of the second product."""
+    a = _act(act)
+    c = _pkg._calls
+    if c is not None and gate_up is None and h is None and y is None and status is None and stream is None:
+        r = c.ffn_fwd(x, w_gate_up, w_down, a, save)
+        if r is not None:
+            return r
     ld = _rows(x, "x")
     T, K = x.shape
     dev = x.device
-    a = _act(act)
     _need(w_down, "w_down", _bf16, dev, ndim=2)
     F = w_down.shape[1]
     _need(w_down, "w_down", _bf16, dev, shape=(K, F))
@@ -97,12 +104,18 @@ def gated_ffn_bwd(dy, x, w_gate_up, w_down, gate_up, h, act="silu", dx=True, dw_
     needs may be None: w_gate_up without dx, x without dw_gate_up, h without
     dw_down, w_down and gate_up without both dx and dw_gate_up. ``dgate_up``
     [T, 2F], the gradient of gate_up, is allocated unless passed."""
+    a = _act(act)
+    c = _pkg._calls
+    if (c is not None and dx is True and dw_gate_up is True and dw_down is True and dgate_up is None and status is None
+            and stream is None):
+        r = c.ffn_bwd(dy, x, w_gate_up, w_down, gate_up, h, a)
+        if r is not None:
+            return r
     if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
         raise ValueError("dy must be a bf16 CUDA matrix [T, K]")
     T, K = dy.shape
     dev = dy.device
     _need(dy, "dy", _bf16, ndim=2)
-    a = _act(act)
     want_dx, want_gu, want_d = (t is not None and t is not False for t in (dx, dw_gate_up, dw_down))
     if not (want_dx or want_gu or want_d):
         raise ValueError("no gradient is requested")

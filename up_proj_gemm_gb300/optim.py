@@ -11,6 +11,8 @@ import ctypes
 
 import torch
 
+import up_proj_gemm_gb300 as _pkg
+
 from . import _call, _need, _ptr, _SIGS, _stream, lib
 
 __all__ = ["AdamwPlan", "adamw_plan", "adamw_step", "AdamW"]
@@ -43,6 +45,7 @@ class AdamwPlan:
         self.host_ptr, self.device_ptr = ctypes.addressof(host), device_copy.data_ptr()
         self.stream = torch.cuda.current_stream(device)  # the one the copy was made on
         self.copied = self.stream.record_event()
+        self.where = (self.host_ptr, self.device_ptr, -1 if device.index is None else device.index, self.stream.cuda_stream)
 
     def ready_on(self, stream):
         """Let `stream` use the device copy: after the copying stream, and held until it is done. (A capture starts
@@ -110,6 +113,10 @@ def adamw_step(plan, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, 
     to nearest."""
     if not isinstance(plan, AdamwPlan):
         raise TypeError("plan must come from adamw_plan")
+    c = _pkg._calls
+    if c is not None and stream is None and c.adamw_step(*plan.where, step, lr, betas[0], betas[1], eps, weight_decay,
+                                                         grad_scale, seed):
+        return
     if grad_scale is not None:
         _need(grad_scale, "grad_scale", torch.float32, plan.device, numel=1)
     if stream is None:

@@ -13,6 +13,8 @@ import ctypes
 
 import torch
 
+import up_proj_gemm_gb300 as _pkg
+
 from . import _call, _need, _ptr, _SIGS, _status, _stream, lib
 
 __all__ = ["RopeAxesShape", "rope_sections", "rope_axes", "rope_axes_table"]
@@ -83,6 +85,11 @@ def rope_axes(x, cos, sin, pos, axes, Dr, inverse=False, sum_heads=False, out=No
     applies the Jacobian transpose (the gradient), ``sum_heads`` (with
     inverse) the transpose of the heads' sum, [T, 1, D]: the gradient of a key
     part that all heads share. ``out`` may be a strided view."""
+    c = _pkg._calls
+    if c is not None and out is None and status is None and stream is None and (inverse or not sum_heads):
+        out = c.rope_axes(x, cos, sin, pos, bytes(axes), Dr, (2 if sum_heads else 1) if inverse else 0)
+        if out is not None:
+            return out
     if not (isinstance(x, torch.Tensor) and (x.dtype is _bf16 or x.dtype is _f32) and x.is_cuda and x.dim() == 3
             and (x.shape[2] <= 1 or x.stride(2) == 1) and (inverse or not sum_heads) and 0 < Dr <= x.shape[2]):
         _refuse_x(x, Dr, inverse, sum_heads)
@@ -118,6 +125,11 @@ def rope_axes_table(cos, sin, pos, axes, Dr, cos_out=None, sin_out=None, status=
     """(cos, sin) float32 [T, Dr] of every token for positions with several
     axes: the tables to give fwd, bwd_dgrad, bwd_wgrad, bwd_mxfp8 and kv_fwd
     (with pos=None), which then rotate by several axes."""
+    c = _pkg._calls
+    if c is not None and cos_out is None and sin_out is None and status is None and stream is None:
+        r = c.rope_axes_table(cos, sin, pos, bytes(axes), Dr)
+        if r is not None:
+            return r
     if not isinstance(pos, torch.Tensor) or pos.dim() != 2:
         raise ValueError("pos must be an int32 tensor [A, T]")
     dev = pos.device
