@@ -142,8 +142,10 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, int32_t c0, int32
                  "r"(c0), "r"(c1), "r"(c2), "r"(src)
                  : "memory");
 }
+// Relaxed: the arrival says that TMEM was read (ordered by the tcgen05 fence);
+// a release would wait for the warp's stores to shared memory.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int32_t c0, int32_t c1, uint32_t bar) {
     asm volatile(
@@ -397,7 +399,10 @@ struct Epi {
                 if (has(n0, row0, i)) ask(n0, row0, i);
     }
 
-    __device__ __forceinline__ bool tile(uint32_t tacc, int n0, int64_t row0) {
+    // The tile's chunks; `release` is called once its last TMEM read is done.
+    template <typename Release>
+    __device__ __forceinline__ bool tile(uint32_t tacc, int n0, int64_t row0, Release&& release) {
+        if (!has(n0, row0, 0)) release();
         for (int i = 0; chunk(i) < kChunks; ++i) {
             const int c = chunk(i), n = n0 + kWidth * c;
             if (!has(n0, row0, i)) break;  // this and the later chunks lie outside the result
@@ -410,6 +415,7 @@ struct Epi {
                 values(tacc, 32 * c, r);
                 values(tacc, 128 + 32 * c, ru);
                 tmem_ld_wait();
+                if (!has(n0, row0, i + 1)) release();
                 stores_read<0>();  // one group per chunk, in the same three slots
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
@@ -441,6 +447,7 @@ struct Epi {
                 values(tacc, 64 * c, r);
                 values(tacc, 64 * c + 32, r2);
                 tmem_ld_wait();
+                if (!has(n0, row0, i + 1)) release();
                 const uint32_t slot = slots + 2 * kSlotBytes * (used++ & 1);
                 stores_read<1>();
                 const uint32_t row = slot + 128u * lane;
@@ -461,6 +468,7 @@ struct Epi {
                 __syncwarp();
                 values(tacc, 32 * c, r);
                 tmem_ld_wait();
+                if (!has(n0, row0, i + 1)) release();
                 const int pair = used % 3;
                 const bool ok = mbar_wait(bars + 8u * pair, (uint32_t)(used / 3) & 1u, abort_flag);
                 if (__any_sync(0xffffffffu, !ok)) return false;
@@ -701,11 +709,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (__any_sync(0xffffffffu, !ok)) break;
             tc_fence_after();
             const uint32_t tacc = tmem + ((uint32_t)(quad * 32) << 16) + 256u * b;
-            if (p.splits > 1) epi.share(tacc);  // the ring is free: this was the cluster's only tile
-            else if (!epi.tile(tacc, n0, row0)) break;
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(map_to_rank(tempty(b), leader));
+            if (p.splits > 1) {
+                epi.share(tacc);  // the ring is free: this was the cluster's only tile
+                tc_fence_before();
+                continue;
+            }
+            const bool done = epi.tile(tacc, n0, row0, [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(map_to_rank(tempty(b), leader));
+            });
+            if (!done) break;
         }
     }
 
@@ -715,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp >= 2 && *abort_flag == 0) {
             int mt, nt;
             tile_at(p, cluster, mt, nt);
-            epi.tile(0, nt * (EPI == kGate ? 128 : 256), (int64_t)mt * 256 + prank * 128 + quad * 32);
+            epi.tile(0, nt * (EPI == kGate ? 128 : 256), (int64_t)mt * 256 + prank * 128 + quad * 32, [] {});
         }
     }
     if (warp >= 2) epi.finish();
