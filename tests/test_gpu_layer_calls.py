@@ -123,3 +123,40 @@ def test_current_stream_is_used(cuda_device, face):
         out = mlaq.rope_axes(q, d["cos"], d["sin"], d["pos"], d["axes"], 16)
     side.synchronize()
     assert torch.equal(out, want)
+
+
+def test_overlapped_launches_keep_the_order(cuda_device):
+    """Launches start under the ones before them; what they read and write stays in order: parameters are stepped and
+    used by the next product, its output rotated, buffers reused, many times in a row and in a graph."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(2)
+    T, K, F = 6, 256, 512
+    w = [torch.randn(s, generator=g).to(dev) * s[-1] ** -0.5 for s in ((2 * F, K), (K, F))]
+    x = torch.randn((T, K), generator=g).to(bf16).to(dev)
+    cos, sin = torch.randn((64, 32), generator=g).to(dev), torch.randn((64, 32), generator=g).to(dev)
+    pos = torch.randint(0, 64, (3, T), generator=g).to(i32).to(dev)
+    axes = [i % 3 for i in range(16)]
+
+    def chain(sync):
+        p = [t.to(bf16) for t in w]
+        grad = [torch.full_like(t, 1e-2) for t in p]
+        m, v = ([torch.zeros(t.shape, device=dev) for t in p] for _ in range(2))
+        plan = mlaq.adamw_plan(p, grad, m, v)
+        h, y = torch.empty((T, F), dtype=bf16, device=dev), torch.empty((T, K), dtype=bf16, device=dev)
+        z, outs = x.clone(), []
+        wait = torch.cuda.synchronize if sync else (lambda: None)
+        for step in range(1, 31):
+            mlaq.adamw_step(plan, step, lr=1e-2, weight_decay=0.0)
+            wait()
+            mlaq.gated_ffn_fwd(z, p[0], p[1], y=y, h=h)
+            wait()
+            mlaq.rope_axes(y.view(T, 8, 32), cos, sin, pos, axes, 32, out=z.view(T, 8, 32))
+            wait()
+            z = z.float().clamp(-2, 2).to(bf16) if step % 7 == 0 else z
+            outs.append(mlaq.rope_axes(z.view(T, 8, 32), cos, sin, pos, axes, 32, inverse=True, sum_heads=True))
+            wait()
+        return outs + [z] + p
+
+    want, got = chain(True), chain(False)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a.nan_to_num(), b.nan_to_num()) for a, b in zip(want, got))

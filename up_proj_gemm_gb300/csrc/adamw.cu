@@ -30,6 +30,7 @@
 
 #include "checks.h"
 #include "internal.h"
+#include "launch.cuh"
 #include "mx.cuh"
 #include "ptx.cuh"
 
@@ -297,6 +298,8 @@ struct GroupF32 {
 
 template <typename P, typename G>
 __global__ void __launch_bounds__(kThreads) adamw_f32_kernel(const StepParams q) {
+    grid_launch_next();
+    grid_wait_previous();
     const PlanChunk c = q.chunks[blockIdx.x];
     const PlanTensor T = q.tensors[c.tensor];
     const float gs = q.grad_scale ? __ldg(q.grad_scale) : 1.f;
@@ -562,6 +565,8 @@ __device__ __forceinline__ void walk_mx(const StepParams& q, const PlanTensor& T
 
 template <typename P, typename G>
 __global__ void __launch_bounds__(kThreads, 4) adamw_mx_kernel(const StepParams q) {
+    grid_launch_next();
+    grid_wait_previous();
     const PlanChunk c = q.chunks[blockIdx.x];
     const PlanTensor& T = q.tensors[c.tensor];
     const float gs = q.grad_scale ? __ldg(q.grad_scale) : 1.f;
@@ -578,9 +583,8 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_mx_kernel(const StepParams 
 
 template <typename P, typename G>
 int launch(const PlanHeader& h, const StepParams& q, cudaStream_t stream) {
-    if (h.bits == 32) adamw_f32_kernel<P, G><<<(unsigned)h.chunks, kThreads, 0, stream>>>(q);
-    else adamw_mx_kernel<P, G><<<(unsigned)h.chunks, kThreads, 0, stream>>>(q);
-    return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+    return launch_overlapped(h.bits == 32 ? adamw_f32_kernel<P, G> : adamw_mx_kernel<P, G>, (unsigned)h.chunks, kThreads, 0,
+                             0, stream, q);
 }
 
 // The number of chunks and (out) their size; -1: invalid sizes.

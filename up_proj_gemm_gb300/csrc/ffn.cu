@@ -27,6 +27,7 @@
 
 #include "checks.h"
 #include "internal.h"
+#include "launch.cuh"
 #include "mx.cuh"
 #include "ptx.cuh"
 
@@ -133,10 +134,6 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
                  : "memory");
     return v;
 }
-// A grid that may start under the one before it: let the next one do the same,
-// and wait until the one before is complete.
-__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void tma_store_3d(const void* tmap, int32_t c0, int32_t c1, int32_t c2, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(tmap),
                  "r"(c0), "r"(c1), "r"(c2), "r"(src)
@@ -574,6 +571,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_wait();
         cluster_arrive_relaxed();
     }
+    // The first product of a call waits here, and lets the next one start only
+    // then: that one may read its weights before it waits itself. (In the others
+    // the producer waits; nothing else reads what the grid before writes.)
+    if (!p.after) grid_wait_previous();
     grid_launch_next();
     int kb = 0, ke = p.k_tiles;
     if (p.splits > 1) {
@@ -861,6 +862,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
     };
     const int ahead = steps < p.stages ? steps : p.stages;
 
+    if (!p.after) grid_wait_previous();  // before grid_launch_next(): see ffn_gemm_kernel
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(full(s), 1);
@@ -1106,22 +1108,8 @@ int gemm(const Product* jobs, int count, GemmParams p, int64_t red, bool after, 
         const int st = make_tmap_3d(&tg, gu, F, 2, T, 2 * F, 4 * F, 32, 1, 32, true);
         if (st != MLA_OK) return st;
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(2 * p.splits * clusters));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Smem<EPI>::kBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[2]{};
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2u * p.splits;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = after ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<AMN, BMN, EPI>, ta[0], tb[0], to[0], tg, ta[1],
-                                             tb[1], to[1], p);
-    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+    return launch_overlapped(ffn_gemm_kernel<AMN, BMN, EPI>, (unsigned)(2 * p.splits * clusters), kThreads,
+                             Smem<EPI>::kBytes, 2u * p.splits, stream, ta[0], tb[0], to[0], tg, ta[1], tb[1], to[1], p);
 }
 
 // Whether a product of T tokens and `rows` weight rows (kGate: channels) takes
@@ -1182,21 +1170,8 @@ int narrow(const Product& job, const GemmParams& g, int64_t red, bool after, con
             return MLA_ERR_CUDA;
         allowed.fetch_or(bit, std::memory_order_relaxed);
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(ctas * p.splits));
-    cfg.blockDim = dim3(kNarrowThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[2]{};
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)p.splits;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = after ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, ta, tb, p) != cudaSuccess) return MLA_ERR_CUDA;
-    return MLA_OK;
+    return launch_overlapped(kernel, (unsigned)(ctas * p.splits), kNarrowThreads, smem, (unsigned)p.splits, stream, ta, tb,
+                             p);
 }
 
 int check_ffn(const mla_ffn_shape* s) {

@@ -18,6 +18,7 @@
 
 #include "checks.h"
 #include "internal.h"
+#include "launch.cuh"
 #include "mx.cuh"
 #include "ptx.cuh"
 
@@ -134,6 +135,8 @@ __device__ __forceinline__ void from_table(const float* q, float (&v)[VE]) {
 template <typename E, int VE>
 __global__ void __launch_bounds__(kThreads, kRowBlocks) rope_axes_kernel(const __grid_constant__ RopeParams p) {
     extern __shared__ float4 table4[];  // [token of the run][cos Dr | sin Dr]
+    grid_launch_next();
+    grid_wait_previous();
     float* table = reinterpret_cast<float*>(table4);
     const int half = p.Dr / 2;
     const int n_pair = half / VE, n_copy = p.Dn / VE;
@@ -248,6 +251,8 @@ constexpr int kFewHeads = 16;
 
 template <typename E, int VE>
 __global__ void __launch_bounds__(kThreads) rope_few_kernel(const __grid_constant__ RopeParams p) {
+    grid_launch_next();
+    grid_wait_previous();
     const int half = p.Dr / 2;
     const int n_copy = p.Dn / VE, n_copy2 = (n_copy + 1) / 2;
     const uint32_t slots = n_copy2 + half / VE;
@@ -301,6 +306,8 @@ constexpr int kSumHeads = 4;  // heads in flight per lane (5 blocks per SM; 8 wi
 
 template <typename E, int VE>
 __global__ void __launch_bounds__(kSumThreads, 5) rope_sum_kernel(const __grid_constant__ RopeParams p, int hl, int per_warp) {
+    grid_launch_next();
+    grid_wait_previous();
     const int half = p.Dr / 2;
     const int n_copy = p.Dn / VE, n_copy2 = (n_copy + 1) / 2;
     const int slots = n_copy2 + half / VE;
@@ -377,6 +384,8 @@ __global__ void __launch_bounds__(kSumThreads, 5) rope_sum_kernel(const __grid_c
 __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_constant__ RopeParams p,
                                                               float* __restrict__ cos_out,
                                                               float* __restrict__ sin_out) {
+    grid_launch_next();
+    grid_wait_previous();
     const int half = p.Dr / 2;
     const int quads = p.cs_vec ? p.Dr / 4 : p.Dr;
     const int64_t items = p.T * quads;
@@ -416,12 +425,12 @@ int launch_rows(RopeParams p, bool sum, int num_sms, cudaStream_t stream) {
         const int per_warp = 32 / (width * hl);
         const int64_t warps = (p.T + per_warp - 1) / per_warp;
         const int64_t grid = (warps * 32 + kSumThreads - 1) / kSumThreads;
-        rope_sum_kernel<E, VE><<<(unsigned)grid, kSumThreads, 0, stream>>>(p, hl, per_warp);
+        return launch_overlapped(rope_sum_kernel<E, VE>, (unsigned)grid, kSumThreads, 0, 0, stream, p, hl, per_warp);
     } else if (p.H <= kFewHeads || p.rows * ((p.Dn / VE + 1) / 2 + p.Dr / 2 / VE) <= (int64_t)num_sms * 2048) {
         const int slots = (p.Dn / VE + 1) / 2 + p.Dr / 2 / VE;
         const int64_t grid = (p.rows * slots + kThreads - 1) / kThreads;
         if (grid > kI32Max) return MLA_ERR_UNSUPPORTED;
-        rope_few_kernel<E, VE><<<(unsigned)grid, kThreads, 0, stream>>>(p);
+        return launch_overlapped(rope_few_kernel<E, VE>, (unsigned)grid, kThreads, 0, 0, stream, p);
     } else {
         const int slots = (p.Dn / VE + 1) / 2 + p.Dr / 2 / VE;
         const int lanes = kThreads / slots > 0 ? kThreads / slots : 1;
@@ -434,9 +443,8 @@ int launch_rows(RopeParams p, bool sum, int num_sms, cudaStream_t stream) {
         p.rows_per_block = (int)run;
         const int64_t grid = (p.rows + run - 1) / run;
         const int64_t most = (run + p.H - 2) / p.H + 1;  // tokens that a run may touch
-        rope_axes_kernel<E, VE><<<(unsigned)grid, kThreads, (size_t)(most * 8 * p.Dr), stream>>>(p);
+        return launch_overlapped(rope_axes_kernel<E, VE>, (unsigned)grid, kThreads, (size_t)(most * 8 * p.Dr), 0, stream, p);
     }
-    return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 // The checks that the entry points share; fills the parameters.
@@ -553,8 +561,8 @@ MLAQ_API int mla_rope_axes_table(const mla_rope_axes_shape* shape, const float* 
     const int64_t items = s.T * (p.cs_vec ? s.Dr / 4 : s.Dr);
     int64_t grid = (items + kThreads - 1) / kThreads;
     if (grid > (int64_t)di.num_sms * 8) grid = (int64_t)di.num_sms * 8;
-    rope_table_kernel<<<(unsigned)grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p, cos_out, sin_out);
-    return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+    return launch_overlapped(rope_table_kernel, (unsigned)grid, kThreads, 0, 0, static_cast<cudaStream_t>(stream), p,
+                             cos_out, sin_out);
 }
 
 }  // extern "C"
