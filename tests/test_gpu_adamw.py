@@ -305,3 +305,28 @@ def test_gradients_beyond_the_range_of_their_square(cuda_device):
     g[1] = 1.0
     mlaq.adamw_step(mlaq.adamw_plan([p], [g], [m], [v]), 1, lr=1e-3, betas=(0.9, 0.95), weight_decay=0.0)
     assert torch.isfinite(p).all() and torch.isinf(v[0]) and torch.isfinite(v[1])
+
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_many_elements(cuda_device, bits):
+    """Above 100 million elements a block may take more of them: the same results as in steps over fewer at a time."""
+    sizes = [60_000_000, 40_000_000, 8191, 8193, 16383, 16384, 16385, 24577, 5]
+
+    def run(some):
+        p = [torch.linspace(-1, 1, n, device=cuda_device) for n in some]
+        g = [t * 0.5 for t in p]
+        kind, at, scales = (f32, 0.0, {}) if bits == 32 else (u8, 0, dict(
+            zip(("exp_avg_scales", "exp_avg_sq_scales"),
+                ([torch.zeros(-(-n // 32), dtype=u8, device=cuda_device) for n in some] for _ in range(2)))))
+        m, v = ([torch.full((n,), at, dtype=kind, device=cuda_device) for n in some] for _ in range(2))
+        plan = mlaq.adamw_plan(p, g, m, v, **scales)
+        for step in (1, 2):
+            mlaq.adamw_step(plan, step, lr=0.25, betas=(0.5, 0.75), weight_decay=0.0)
+        return [p, m, v] + list(scales.values())
+
+    whole, parts = run(sizes), [run(sizes[:1]), run(sizes[1:2]), run(sizes[2:])]
+    for k, got in enumerate(whole):
+        assert all(torch.equal(a, b) for a, b in zip(got, parts[0][k] + parts[1][k] + parts[2][k]))
+    moved = whole[0][0] - torch.linspace(-1, 1, sizes[0], device=cuda_device)
+    assert (moved[:29_000_000] > 0.2).all() and (moved[31_000_000:] < -0.2).all()

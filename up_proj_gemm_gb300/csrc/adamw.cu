@@ -19,7 +19,10 @@
 // multiplicative mix of the seed and the element's place, so a step is
 // reproducible; 16 bits each for m, v and p.
 //
-// Bound by HBM: one pass, every operand read and written once.
+// One pass, every operand read and written once. With float32 moments HBM is
+// the bound: 100 M elements at 6.86 TB/s, a plain copy's rate. With MXFP8 moments
+// an element is 10 bytes and 67 instructions: 5.18 TB/s (300 M elements in
+// 586 us), issue slots 78% taken.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -38,11 +41,14 @@ namespace mlaq {
 namespace {
 
 constexpr int kThreads = 256;
-// Elements per block: 4 rounds of 8 per thread, halved until there are as many
-// blocks as are resident at once (5 on each of 152 SMs): 100,000 elements in 10
-// tensors 6.5 -> 3.1 us with MXFP8 moments, 4.6 -> 2.5 with float32 ones; twice
-// as many blocks lost again (3 M elements in 40 tensors: 15.3 against 17.2).
-constexpr int kChunkMost = 8192, kChunkLeast = 1024;
+// Elements per block: with MXFP8 moments 8 rounds of 8 per thread where that
+// leaves at least 8 blocks for each that is resident at once (5 on each of 152
+// SMs; 300 M elements: 654 -> 634 us against 4 rounds; 20 M elements, 1.6 blocks
+// for each: 50 -> 53; float32 moments of 100 M: 408 -> 414). Else 4, halved until there are as many blocks as are resident:
+// 100,000 elements in 10 tensors 6.5 -> 3.1 us with MXFP8 moments, 4.6 -> 2.5
+// with float32 ones; twice as many blocks lost again (3 M elements in 40 tensors:
+// 15.3 against 17.2).
+constexpr int kChunkMost = 16384, kChunkLeast = 1024;
 constexpr int64_t kChunkBlocks = 760;
 
 struct PlanTensor {
@@ -76,12 +82,18 @@ struct StepParams {
     int chunk;  // elements per block
 };
 
-// 32 mixed bits of a place: the upper and lower halves serve m and v.
-__device__ __forceinline__ uint32_t mix32(uint32_t place, uint32_t seed) {
+// The complement of 32 mixed bits of a place: its upper and lower halves serve
+// m and v. (What is added to a magnitude is the complement of a random number.)
+__device__ __forceinline__ uint32_t mix_not(uint32_t place, uint32_t seed) {
     uint32_t x = place * 0x9E3779B1u + seed;
     x = (x ^ (x >> 15)) * 0x6A09E667u;
     x = (x ^ (x >> 13)) * 0xBB67AE85u;
-    return x ^ (x >> 16);
+    return ~(x ^ (x >> 16));
+}
+// The upper halves of another mix of two of them (their complements times a
+// constant): the parameters' bits.
+__device__ __forceinline__ uint32_t mix_param(uint32_t lo, uint32_t hi) {
+    return __byte_perm(~lo * 0x3C6EF373u, ~hi * 0x3C6EF373u, 0x7632);
 }
 
 template <typename E>
@@ -227,10 +239,12 @@ __device__ __forceinline__ void update(const StepParams& q, float gs, const floa
     }
 }
 
-// The bits of a bf16 parameter rounded up or down at random, in the upper
-// half of the word.
-__device__ __forceinline__ uint32_t bf16_random(float p, uint32_t mixed) {
-    return __float_as_uint(p) + ((mixed * 0x3C6EF373u) >> 16);
+// Two values rounded to bf16, up or down at random by 16 bits each (lo: the
+// lower halves of the result and of the bits); NaNs and infinities stay.
+__device__ __forceinline__ uint32_t bf16x2_random(float lo, float hi, uint32_t mixed) {
+    uint32_t r;
+    asm("cvt.rs.bf16x2.f32 %0, %1, %2, %3;" : "=r"(r) : "f"(hi), "f"(lo), "r"(mixed));
+    return r;
 }
 
 // The largest of three magnitudes, NaN when one of them is.
@@ -243,24 +257,22 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 // N parameters of a bf16 tensor rounded at random and stored.
 template <int N, bool VEC>
 __device__ __forceinline__ void store_random(uint16_t* p, int n, const float (&v)[N], const uint32_t (&mixed)[N]) {
-    // the addition would carry a NaN's bits into its sign: a group that holds one is rounded to nearest
-    float am = fabsf(v[0]);
-#pragma unroll
-    for (int i = 1; i < N; i += 2) am = max3_nan(am, v[i], v[i + 1 < N ? i + 1 : i]);
-    if (am != am) {
-        store_n<N, VEC>(p, n, v);
-        return;
-    }
-    if constexpr (VEC) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4)
-            *reinterpret_cast<uint2*>(p + i) =
-                make_uint2(__byte_perm(bf16_random(v[i], mixed[i]), bf16_random(v[i + 1], mixed[i + 1]), 0x7632),
-                           __byte_perm(bf16_random(v[i + 2], mixed[i + 2]), bf16_random(v[i + 3], mixed[i + 3]), 0x7632));
+    if constexpr (N == 1) {
+        if (n) p[0] = (uint16_t)bf16x2_random(v[0], v[0], mix_param(mixed[0], mixed[0]));
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (i < n) p[i] = (uint16_t)(bf16_random(v[i], mixed[i]) >> 16);
+        for (int i = 0; i < N; i += 4) {
+            const uint32_t a = bf16x2_random(v[i], v[i + 1], mix_param(mixed[i], mixed[i + 1]));
+            const uint32_t b = bf16x2_random(v[i + 2], v[i + 3], mix_param(mixed[i + 2], mixed[i + 3]));
+            if constexpr (VEC) {
+                *reinterpret_cast<uint2*>(p + i) = make_uint2(a, b);
+            } else {
+                if (i < n) p[i] = (uint16_t)a;
+                if (i + 1 < n) p[i + 1] = (uint16_t)(a >> 16);
+                if (i + 2 < n) p[i + 2] = (uint16_t)b;
+                if (i + 3 < n) p[i + 3] = (uint16_t)(b >> 16);
+            }
+        }
     }
 }
 
@@ -285,9 +297,10 @@ struct GroupF32 {
         if (T.t.master) store_n<N, VEC>(T.t.master + idx, n, p);
         if constexpr (sizeof(P) == 2) {
             if (!T.t.master && q.stochastic) {
+                const uint32_t place = (uint32_t)(T.place + idx);
                 uint32_t mixed[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) mixed[i] = mix32((uint32_t)(T.place + idx + i), q.seed);
+                for (int i = 0; i < N; ++i) mixed[i] = mix_not(place + i, q.seed);
                 store_random<N, VEC>(param, n, p, mixed);
                 return;
             }
@@ -335,36 +348,46 @@ __global__ void __launch_bounds__(kThreads) adamw_f32_kernel(const StepParams q)
 constexpr int kLeastExponent = -120;  // 2^(e-6) is a normal float32 from here on
 
 // E4M3 codes of 8 values * 2^-e, each rounded up where the 20-bit fraction
-// below its 3 mantissa bits is above rnd * 2^-16 (rnd: the upper 16 random
-// bits, or the lower for ROOT). On the float32 bits of |v| that is one
-// integer addition: bits + (0xFFFFF - rnd * 16) carries into bit 20 exactly
-// then, and bits 20.. less (e + 120) * 8 are the code. Values below the
-// smallest normal, 2^(e-6), are moved into its octave, where the step is the
-// same, and 8 codes back; adding upwards keeps "fraction above rnd" exact. That
-// form is the larger one below 2^(e-6) and the smaller one above it, so the
-// maximum of both picks the right one.
-template <bool ROOT>
+// below its 3 mantissa bits carries when a random 16-bit number * 16 + 15 is
+// added: with the probability of the fraction, to 2^-16, and never for a
+// fraction of zero. Bits 20.. of the float32 less (e + 120) * 8 are then the
+// code. All of it is one multiply-add: 16 * bits (the sign falls out at the
+// top) + the word of the random number, 15 * 16 below it and the exponent's
+// difference in its top byte, where the code then stands.
+//
+// Values below the smallest normal, 2^(e-6), are moved into its octave, where
+// the step is the same, and 8 codes back; adding upwards keeps the fraction
+// exact. That form is the larger one below 2^(e-6) and the smaller one above
+// it, so the maximum of both picks the right one. LOW: there may be such
+// values; a root above zero then keeps a code above zero.
+template <bool ROOT, bool LOW>
 __device__ __forceinline__ void codes_random(const float (&v)[8], int e, const uint32_t (&mixed)[8],
                                              uint32_t (&codes)[2]) {
     const float least = __uint_as_float((uint32_t)(e + 121) << 23);  // 2^(e-6), e >= kLeastExponent
-    const int base = -((e + 120) * 8 << 20);
+    const uint32_t ends = ((uint32_t)(-(e + 120) * 8) << 24) | 0xF0u;
     uint32_t top[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float a = ROOT ? v[i] : fabsf(v[i]);
-        const int up = (int)(((ROOT ? mixed[i] << 4 : mixed[i] >> 12) & 0xFFFF0u) ^ 0xFFFFFu);
-        int bits = __viaddmax_s32(__float_as_int(__fadd_ru(a, least)), -(8 << 20), __float_as_int(a)) + up + base;
-        if constexpr (ROOT) {  // a root above zero keeps a code above zero (its bits are at least 2^20 then)
-            bits = max(bits, min(__float_as_int(a), 1 << 20));
-            top[i] = (uint32_t)bits << 4;
-        } else {
-            top[i] = (((uint32_t)bits << 4) & 0x7FFFFFFFu) | (__float_as_uint(v[i]) & 0x80000000u);
+        uint32_t bits = __float_as_uint(v[i]);
+        if constexpr (LOW) {
+            const float a = fabsf(v[i]);
+            bits = (uint32_t)__viaddmax_s32(__float_as_int(__fadd_ru(a, least)), -(8 << 20), __float_as_int(a));
         }
+        top[i] = bits * 16u + __byte_perm(ends, mixed[i], ROOT ? 0x3540 : 0x3760);
+        if constexpr (!ROOT) top[i] |= __float_as_uint(v[i]) & 0x80000000u;
+        else if (LOW && v[i] > 0.f) top[i] = max(top[i], 1u << 24);
     }
 #pragma unroll
     for (int w = 0; w < 2; ++w)  // the top bytes of four words
         codes[w] = __byte_perm(__byte_perm(top[4 * w], top[4 * w + 1], 0x0073),
                                __byte_perm(top[4 * w + 2], top[4 * w + 3], 0x0073), 0x5410);
+}
+
+// The smallest of three magnitudes.
+__device__ __forceinline__ float min3_abs(float a, float b, float c) {
+    float r;
+    asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // 8 of a block's 32 values (the other 24 in three neighbouring lanes); v may
@@ -384,7 +407,9 @@ __device__ __forceinline__ uint32_t encode8(const StepParams& q, float (&v)[8], 
             for (int i = 0; i < 8; ++i) v[i] *= exp2_neg(e);
             left = 0;
         }
-        codes_random<ROOT>(v, left, mixed, codes);
+        const float lo = min3_abs(min3_abs(v[0], v[1], v[2]), min3_abs(v[3], v[4], v[5]), fminf(fabsf(v[6]), fabsf(v[7])));
+        if (lo < __uint_as_float((uint32_t)(left + 121) << 23)) codes_random<ROOT, true>(v, left, mixed, codes);
+        else codes_random<ROOT, false>(v, left, mixed, codes);
         return (uint32_t)(e + 127);
     }
     const uint32_t sf = quantize8_block_scale(v, bits, codes);
@@ -508,7 +533,7 @@ struct GroupMx {
         update<8>(q, gs, gf, pf, m, v, r);
         const uint32_t place = (uint32_t)(T.place + idx);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mixed[i] = q.stochastic ? mix32(place + i, q.seed) : 0;
+        for (int i = 0; i < 8; ++i) mixed[i] = q.stochastic ? mix_not(place + i, q.seed) : 0;
         // the partial group of a tensor's end: elements past it count for nothing in the block's scale
         if constexpr (!VEC) {
 #pragma unroll
@@ -538,16 +563,18 @@ struct GroupMx {
 
 // Whole warps walk the chunk 256 elements at a time; a warp whose 256 elements
 // all exist takes the wide path, where the next group's loads are in flight
-// while this one is computed.
+// while this one is computed. (Fetching the group after it into L2 as well cost
+// more issue slots than it saved waiting: 300 M elements 586 -> 633 us.)
 template <bool MASTER, typename P, typename G>
 __device__ __forceinline__ void walk_mx(const StepParams& q, const PlanTensor& T, float gs, int64_t base, int n, bool vec) {
     const int lane8 = (int)(threadIdx.x & 31) * 8;
     int i = threadIdx.x * 8;
     GroupMx<MASTER, P, G> cur, next;
     if (vec && i - lane8 + 256 <= n) {
+        const int step = kThreads * 8;
         cur.template load<true>(T, base + i, 8);
         for (;;) {
-            const int j = i + kThreads * 8;
+            const int j = i + step;
             const bool more = j - lane8 + 256 <= n;
             if (more) next.template load<true>(T, base + j, 8);
             cur.template step<true>(q, T, gs, base + i, 8);
@@ -587,15 +614,17 @@ int launch(const PlanHeader& h, const StepParams& q, cudaStream_t stream) {
                              0, stream, q);
 }
 
-// The number of chunks and (out) their size; -1: invalid sizes.
-int64_t count_chunks(const mla_adamw_tensor* t, int64_t count, int* size) {
-    int64_t chunks = 0;
-    for (*size = kChunkMost;; *size /= 2) {
+// The number of chunks and (out) their size; -1: invalid sizes. Never more of
+// them with 8 bits than with 32.
+int64_t count_chunks(const mla_adamw_tensor* t, int64_t count, int bits, int* size) {
+    int64_t chunks = 0, total = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (t[i].n < 0 || t[i].n > ((int64_t)1 << 40)) return -1;
+        total = std::min(total + t[i].n, (int64_t)1 << 60);
+    }
+    for (*size = bits == 8 && total / kChunkMost >= 8 * kChunkBlocks ? kChunkMost : kChunkMost / 2;; *size /= 2) {
         chunks = 0;
-        for (int64_t i = 0; i < count; ++i) {
-            if (t[i].n < 0 || t[i].n > ((int64_t)1 << 40)) return -1;
-            chunks += (t[i].n + *size - 1) / *size;
-        }
+        for (int64_t i = 0; i < count; ++i) chunks += (t[i].n + *size - 1) / *size;
         if (chunks >= kChunkBlocks || *size <= kChunkLeast) break;
     }
     return count <= kI32Max && chunks <= kI32Max ? chunks : -1;
@@ -628,7 +657,7 @@ extern "C" {
 MLAQ_API size_t mla_adamw_plan_bytes(const mla_adamw_tensor* tensors, int64_t count) {
     if (!tensors || count <= 0 || count > kI32Max) return 0;
     int chunk;
-    const int64_t chunks = count_chunks(tensors, count, &chunk);
+    const int64_t chunks = count_chunks(tensors, count, 32, &chunk);
     return chunks < 0 ? 0 : (size_t)plan_bytes(count, chunks);
 }
 
@@ -639,7 +668,7 @@ MLAQ_API int mla_adamw_plan_build(const mla_adamw_tensor* tensors, int64_t count
         (grad_dtype != MLA_IN_F32 && grad_dtype != MLA_IN_BF16) || (state_bits != 32 && state_bits != 8))
         return MLA_ERR_INVALID_ARG;
     int chunk;
-    const int64_t chunks = count_chunks(tensors, count, &chunk);
+    const int64_t chunks = count_chunks(tensors, count, state_bits, &chunk);
     if (chunks < 0) return MLA_ERR_INVALID_ARG;
     if (plan_size < (size_t)plan_bytes(count, chunks)) return MLA_ERR_WORKSPACE;
     const int64_t ps = param_dtype == MLA_IN_F32 ? 4 : 2, gs = grad_dtype == MLA_IN_F32 ? 4 : 2;
