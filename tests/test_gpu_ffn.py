@@ -304,3 +304,29 @@ def test_many_tokens_parts_and_guards(cuda_device):
     b = mlaq.gated_ffn_bwd(dy, x, None, wd, gu, None, dx=False, dw_down=False)
     c = mlaq.gated_ffn_bwd(dy, None, None, None, None, h, dx=False, dw_gate_up=False)
     assert torch.equal(a[0], dx) and torch.equal(b[1], dwgu) and torch.equal(c[2], dwd)
+
+
+@pytest.mark.parametrize("T,K,F", [(1100, 512, 1024), (300, 2048, 512), (90, 512, 1024), (7, 264, 2048), (5000, 1024, 2048), (2000, 2000, 264)])
+def test_weight_gradients_run_beside_dx(cuda_device, T, K, F):
+    """The weights' gradients start before dx is finished: dx is whole for whoever comes after, call after call, and
+    every bit is the one that a call for it alone gives."""
+    g = torch.Generator().manual_seed(4)
+    x, dy = ((torch.randn((T, K), generator=g)).to(torch.bfloat16).to(cuda_device) for _ in range(2))
+    wgu, wd = (torch.randn(s, generator=g).mul(s[-1] ** -0.5).to(torch.bfloat16).to(cuda_device)
+               for s in ((2 * F, K), (K, F)))
+    y, gu, h = mlaq.gated_ffn_fwd(x, wgu, wd, save=True)
+    alone = [mlaq.gated_ffn_bwd(dy, x, wgu, wd, gu, h, dx=i == 0, dw_gate_up=i == 1, dw_down=i == 2)[i] for i in range(3)]
+    torch.cuda.synchronize()
+    out = [torch.empty_like(t) for t in alone]
+    kept = []
+    for _ in range(8):
+        for t in out:
+            t.fill_(float("nan"))
+        mlaq.gated_ffn_bwd(dy, x, wgu, wd, gu, h, dx=out[0], dw_gate_up=out[1], dw_down=out[2])
+        kept.append([t.clone() for t in out])
+    # and read by a kernel that itself starts under the last one: dx as the next call's dy
+    got = mlaq.gated_ffn_bwd(out[0], x, wgu, wd, gu, h)
+    torch.cuda.synchronize()
+    want = mlaq.gated_ffn_bwd(alone[0], x, wgu, wd, gu, h)
+    assert all(torch.equal(a, b) for k in kept for a, b in zip(k, alone))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -43,6 +43,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSlotBytes = 32u * 64u;         // 32 rows x 32 columns of a result, 64-byte swizzle (kStore: two, as one)
 constexpr int kEpiWarps = 8;
 constexpr int kSplitSteps = 12;                     // K steps that adding up a split reduction costs
+constexpr int kTileSteps = 4;                      // K steps that a tile costs beside its own
 constexpr int kMaxSplits = 4;                      // clusters of 8 CTAs
 
 enum Epilogue { kStore = 0, kGate = 1, kGateGrad = 2 };
@@ -59,6 +60,13 @@ struct Smem {
     static constexpr size_t kBytes = 1024 + kRing + (size_t)kEpiWarps * kSlots * kSlotBytes + 512;
 };
 
+// How a product stands to the grid before it on the stream: the first of a call
+// waits for it; one with an operand from it waits before its loads; and one that
+// needs nothing of it, but of the grid before that (the weight gradients after
+// dx), runs in the SMs it leaves idle and waits at its own end, so that whoever
+// waits for this grid has waited for both.
+enum After { kFirst = 0, kAfter = 1, kBeside = 2 };
+
 // A result and its tiles; kGate: N = F (a tile holds 128 of them).
 struct Result {
     int M, N, m_tiles, n_tiles;
@@ -71,7 +79,9 @@ struct GemmParams {
     int tiles0, tiles;        // of the first result, of both
     int k_tiles;
     int splits;               // parts of the reduction, each a pair of the cluster
-    int after;                // an operand comes from the grid before this one
+    int after;                // kFirst, kAfter or kBeside
+    int late;                 // the next grid runs beside this one: it starts after this one's wait
+    int early, head;          // the first `early` clusters share `head` tiles before all share the rest
     int F, act;
     uint16_t* gate_up_out;    // kGate: [M, 2F] or null
     const uint16_t* gate_up;  // kGateGrad: [M, 2F]
@@ -540,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int crank = (int)cluster_rank();
     const int prank = crank & 1, leader = crank & ~1, srank = crank >> 1;
     const int cluster = cluster_id(), clusters = cluster_count();
-    const int tiles = p.tiles;
+    const int tiles = p.tiles, first = cluster < p.early ? cluster : p.head + cluster;
 
     // The setup runs once per tile when there are few: the lanes of a warp
     // write the barriers together, nothing is divided, nothing released that
@@ -573,9 +583,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // The first product of a call waits here, and lets the next one start only
     // then: that one may read its weights before it waits itself. (In the others
-    // the producer waits; nothing else reads what the grid before writes.)
-    if (!p.after) grid_wait_previous();
-    grid_launch_next();
+    // the producer waits; nothing else reads what the grid before writes. With a
+    // grid to come that does not wait for this one, it lets that one start, too.)
+    if (p.after == kFirst) grid_wait_previous();
+    if (!p.late) grid_launch_next();
     int kb = 0, ke = p.k_tiles;
     if (p.splits > 1) {
         kb = p.k_tiles * srank / p.splits;
@@ -604,8 +615,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             int s = 0;
             uint32_t ph = 0, issued = 0, par = 0;
             bool ok = true;
-            if (p.after) grid_wait_previous();
-            for (int tile = cluster; ok && tile < tiles; tile += clusters) {
+            if (p.after == kAfter) grid_wait_previous();
+            if (p.late) grid_launch_next();
+            for (int tile = first; ok && tile < tiles; tile += tile < p.head ? p.early : clusters) {
                 int mt, nt;
                 const int job = tile_at(p, tile, mt, nt);
                 const CUtensorMap *mapA = AMN && job ? &tmA1 : &tmA, *mapB = AMN && job ? &tmB1 : &tmB;
@@ -658,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int s = 0, local = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int tile = cluster; ok && tile < tiles; tile += clusters, ++local) {
+            for (int tile = first; ok && tile < tiles; tile += tile < p.head ? p.early : clusters, ++local) {
                 const int b = local & 1;
                 if (!mbar_wait(tempty(b), (((uint32_t)local >> 1) & 1u) ^ 1u, abort_flag)) {
                     ok = false;
@@ -696,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tmem = *tmem_slot;
         // ------------------------------------------------------------ epilogue
         int local = 0;
-        for (int tile = cluster; tile < tiles; tile += clusters, ++local) {
+        for (int tile = first; tile < tiles; tile += tile < p.head ? p.early : clusters, ++local) {
             const int b = local & 1;
             int mt, nt;
             const int job = tile_at(p, tile, mt, nt);
@@ -744,6 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc_pair(*tmem_slot, kTmemCols);
     }
+    if (p.after == kBeside) grid_wait_previous();
 }
 
 // Clusters of `splits` pairs that can be resident at once (a GPC may hold a
@@ -801,7 +814,8 @@ struct NarrowParams {
     int token_tiles;
     int k_tiles, stages, splits;
     uint32_t stage_bytes, tmem_cols;
-    int after;                // the tokens come from the grid before this one
+    int after;                // kFirst or kAfter: the tokens come from the grid before this one
+    int late;                 // as in GemmParams
     int F, act;
     uint16_t* out;
     uint16_t* gate_up_out;
@@ -862,7 +876,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
     };
     const int ahead = steps < p.stages ? steps : p.stages;
 
-    if (!p.after) grid_wait_previous();  // before grid_launch_next(): see ffn_gemm_kernel
+    if (p.after == kFirst) grid_wait_previous();  // before grid_launch_next(): see ffn_gemm_kernel
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(full(s), 1);
@@ -883,12 +897,13 @@ __global__ void __launch_bounds__(kNarrowThreads)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    grid_launch_next();
+    if (!p.late) grid_launch_next();
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
-            if (p.after) grid_wait_previous();
+            if (p.after == kAfter) grid_wait_previous();
+            if (p.late) grid_launch_next();
             for (int i = 0; i < ahead; ++i) load_b(i, i);
             bool ok = true;
             int s = 0;
@@ -1049,13 +1064,42 @@ struct Product {
 
 int64_t pair_tiles(int64_t M, int64_t N) { return ((M + 255) / 256) * ((N + 255) / 256); }
 
+// The pairs that a grid leaves idle in its last wave, and for how many K steps.
+struct Idle {
+    int64_t pairs = 0, steps = 0;
+};
+
+// How many tiles each of the idle pairs takes before the others come, so that
+// all end soonest. cost: K steps of a tile.
+int64_t tiles_ahead(int64_t tiles, int64_t clusters, const Idle& idle, int64_t cost) {
+    int64_t best = 0, best_end = INT64_MAX;
+    for (int64_t n = 0; n * idle.pairs <= tiles && n * cost <= idle.steps + 2 * cost; ++n) {
+        const int64_t shared = tiles - n * idle.pairs, each = shared / clusters, more = shared % clusters;
+        const int64_t first = (n + each + (more > 0)) * cost - idle.steps;
+        const int64_t others = (each + (more > idle.pairs)) * cost;
+        const int64_t end = first > others ? first : others;
+        if (end < best_end) {
+            best_end = end;
+            best = n;
+        }
+        if (idle.pairs == 0) break;
+    }
+    return best;
+}
+
 // One product, or (AMN) two over the same reduction. `beside`: tiles of a
 // product that could have been in the launch and is not; it counts where the
 // split is chosen, so a gradient's bits do not depend on which others are asked
-// for.
+// for. leaves (out): the next grid runs beside this one; idle: what the grid
+// before left (kBeside). Blocks start in their order, so the first ones get the
+// idle pairs and take tiles before the others come (both gradients' calls against
+// equal shares after dx: T = 777, K = 1536, F = 4096, 28 pairs idle for 76 steps,
+// 67.1 -> 59.0 us; T = 3000, K = 2048, F = 8192 402 -> 360; T = 4096, K = 4096,
+// F = 14336 1593 -> 1522; T = 8192, K = 1024, F = 2816, no time for one, 184-191
+// either way).
 template <bool AMN, bool BMN, int EPI>
-int gemm(const Product* jobs, int count, GemmParams p, int64_t red, bool after, const DeviceInfo& di,
-         cudaStream_t stream, int64_t beside = 0) {
+int gemm(const Product* jobs, int count, GemmParams p, int64_t red, After after, const DeviceInfo& di,
+         cudaStream_t stream, int64_t beside = 0, Idle* leaves = nullptr, const Idle* idle = nullptr) {
     int64_t tiles = 0;
     for (int j = 0; j < count; ++j) {
         Result& r = p.r[j];
@@ -1073,11 +1117,12 @@ int gemm(const Product* jobs, int count, GemmParams p, int64_t red, bool after, 
     // Split the reduction when the tiles leave pairs idle: in K steps, a pair's
     // time is its share of them plus what the exchange of the sums costs.
     int clusters = 0;
-    int64_t best = 0;
+    int64_t best = 0, pairs = 0;
     for (int s = 1; s <= kMaxSplits; ++s) {
         int n = 0;
         const int st = resident_clusters<AMN, BMN, EPI>(di, s, &n);
         if (st != MLA_OK) return st;
+        if (s == 1) pairs = n;
         const int64_t all = tiles + beside;
         if (s > 1 && (all > n || p.k_tiles < 4 * s)) continue;
         const int64_t cost = s == 1 ? (all + n - 1) / n * p.k_tiles : (p.k_tiles + s - 1) / s + kSplitSteps;
@@ -1086,6 +1131,17 @@ int gemm(const Product* jobs, int count, GemmParams p, int64_t red, bool after, 
             p.splits = s;
             clusters = tiles < n ? (int)tiles : n;
         }
+    }
+    if (leaves) {
+        p.late = 1;
+        const int64_t last = tiles * p.splits % pairs;
+        leaves->pairs = last ? pairs - last : 0;
+        leaves->steps = p.splits > 1 ? p.k_tiles / p.splits + kSplitSteps : p.k_tiles;
+    }
+    if (idle && p.splits == 1 && idle->pairs < clusters) {
+        const int64_t ahead = tiles_ahead(tiles, clusters, *idle, p.k_tiles + kTileSteps);
+        p.early = ahead ? (int)idle->pairs : 0;
+        p.head = (int)(ahead * idle->pairs);
     }
     alignas(64) CUtensorMap ta[2]{}, tb[2]{}, to[2]{}, tg{};
     const uint64_t F = (uint64_t)p.F, T = (uint64_t)jobs[0].M;
@@ -1130,7 +1186,8 @@ bool few_tokens(int64_t T, int64_t rows, const DeviceInfo& di) {
 // [red, R] when AMN), tokens [T, red]. after: the tokens are the output of the
 // launch before this one.
 template <bool AMN, int EPI>
-int narrow(const Product& job, const GemmParams& g, int64_t red, bool after, const DeviceInfo& di, cudaStream_t stream) {
+int narrow(const Product& job, const GemmParams& g, int64_t red, After after, const DeviceInfo& di, cudaStream_t stream,
+           bool late = false) {
     const Operand &w = job.b, &tokens = job.a;
     NarrowParams p{};
     p.T = (int)job.M;
@@ -1144,6 +1201,7 @@ int narrow(const Product& job, const GemmParams& g, int64_t red, bool after, con
     p.gate_up = g.gate_up;
     p.status = g.status;
     p.after = after;
+    p.late = late;
     p.k_tiles = (int)((red + kBK - 1) / kBK);
     p.stage_bytes = kNarrowABytes + 128u * p.N;
     p.stages = (int)(kNarrowRing / p.stage_bytes);
@@ -1217,11 +1275,11 @@ MLAQ_API int mla_gated_ffn_fwd(const mla_ffn_shape* shape, const void* x, const 
     p.gate_up_out = static_cast<uint16_t*>(gate_up);
     const Product up{{x, s.T, s.K, ld}, {w_gate_up, 2 * s.F, s.K, s.K}, s.T, s.F, h};
     const Product down{{h, s.T, s.F, s.F}, {w_down, s.K, s.F, s.F}, s.T, s.K, y};
-    st = few_tokens<kGate>(s.T, s.F, di) ? narrow<false, kGate>(up, p, s.K, false, di, cs)
-                       : gemm<false, false, kGate>(&up, 1, p, s.K, false, di, cs);
+    st = few_tokens<kGate>(s.T, s.F, di) ? narrow<false, kGate>(up, p, s.K, kFirst, di, cs)
+                       : gemm<false, false, kGate>(&up, 1, p, s.K, kFirst, di, cs);
     if (st != MLA_OK) return st;
-    return few_tokens<kStore>(s.T, s.K, di) ? narrow<false, kStore>(down, p, s.F, true, di, cs)
-                         : gemm<false, false, kStore>(&down, 1, p, s.F, true, di, cs);
+    return few_tokens<kStore>(s.T, s.K, di) ? narrow<false, kStore>(down, p, s.F, kAfter, di, cs)
+                         : gemm<false, false, kStore>(&down, 1, p, s.F, kAfter, di, cs);
 }
 
 MLAQ_API int mla_gated_ffn_bwd(const mla_ffn_shape* shape, const void* dy, const void* x, const void* w_gate_up,
@@ -1265,14 +1323,17 @@ MLAQ_API int mla_gated_ffn_bwd(const mla_ffn_shape* shape, const void* dy, const
     const Operand oy{dy, s.T, s.K, s.K}, og{dgate_up, s.T, 2 * s.F, 2 * s.F};
     if (hidden) {
         const Product q{oy, {w_down, s.K, s.F, s.F}, s.T, s.F, dgate_up};
-        st = few_tokens<kGateGrad>(s.T, s.F, di) ? narrow<true, kGateGrad>(q, p, s.K, false, di, cs)
-                           : gemm<false, true, kGateGrad>(&q, 1, p, s.K, false, di, cs);
+        st = few_tokens<kGateGrad>(s.T, s.F, di) ? narrow<true, kGateGrad>(q, p, s.K, kFirst, di, cs)
+                           : gemm<false, true, kGateGrad>(&q, 1, p, s.K, kFirst, di, cs);
         if (st != MLA_OK) return st;
     }
+    Idle idle;
+    const bool dw_beside = dx && (dw_gate_up || dw_down);
     if (dx) {
         const Product q{og, {w_gate_up, 2 * s.F, s.K, s.K}, s.T, s.K, dx};
-        st = few_tokens<kStore>(s.T, s.K, di) ? narrow<true, kStore>(q, p, 2 * s.F, true, di, cs)
-                           : gemm<false, true, kStore>(&q, 1, p, 2 * s.F, true, di, cs);
+        st = few_tokens<kStore>(s.T, s.K, di)
+                 ? narrow<true, kStore>(q, p, 2 * s.F, kAfter, di, cs, dw_beside)
+                 : gemm<false, true, kStore>(&q, 1, p, 2 * s.F, kAfter, di, cs, 0, dw_beside ? &idle : nullptr);
         if (st != MLA_OK) return st;
     }
     Product dw[2];
@@ -1280,7 +1341,9 @@ MLAQ_API int mla_gated_ffn_bwd(const mla_ffn_shape* shape, const void* dy, const
     if (dw_gate_up) dw[count++] = {og, {x, s.T, s.K, ld}, 2 * s.F, s.K, dw_gate_up};
     if (dw_down) dw[count++] = {oy, {h, s.T, s.F, s.F}, s.K, s.F, dw_down};
     const int64_t beside = (dw_gate_up ? 0 : pair_tiles(2 * s.F, s.K)) + (dw_down ? 0 : pair_tiles(s.K, s.F));
-    if (count) return gemm<true, true, kStore>(dw, count, p, s.T, hidden, di, cs, beside);
+    if (count)
+        return gemm<true, true, kStore>(dw, count, p, s.T, dw_beside ? kBeside : hidden ? kAfter : kFirst, di, cs, beside,
+                                        nullptr, dw_beside ? &idle : nullptr);
     return MLA_OK;
 }
 

@@ -4,7 +4,8 @@
 // touches global memory, unless the thread's accesses are ordered behind one
 // that did, and grid_launch_next() to let the grid after it do the same. A grid
 // that reads something before its wait (a later product of a feed-forward
-// call, its weights) relies on the grid before it to have waited first.
+// call, its weights) relies on the grid before it to have waited first; one that
+// needs nothing of the grid before it may wait at its end instead.
 #pragma once
 #include <cuda_runtime.h>
 
