@@ -233,3 +233,20 @@ def test_many_rows_report_a_bad_position(cuda_device):
     assert int(status) == mlaq.STATUS["MLA_ERR_POS_RANGE"]
     ok = torch.arange(2100, device=cuda_device) != 1500
     check(out[ok], ref[ok], e[ok])
+
+
+@pytest.mark.parametrize("T,Dr", [(16387, 64), (25001, 256), (5003, 30), (50001, 30), (90001, 64)])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_table_of_many_tokens(cuda_device, T, Dr, mixed):
+    """Several tokens per thread, axes in runs or mixed inside four columns; positions outside the table give zero."""
+    _, cos, sin, pos, axes = make(T, 1, 0, Dr, 3, f32, rows=301)
+    if not mixed:
+        axes = sorted(axes)
+    pos[1, 7], pos[2, T - 1] = -1, 301
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    c, s = mlaq.rope_axes_table(cos, sin, pos, axes, Dr, status=status)
+    assert int(status) == mlaq.STATUS["MLA_ERR_POS_RANGE"]
+    rows = pos.long()[torch.tensor(axes * 2, device=cuda_device)].t()
+    inside = (rows >= 0) & (rows < 301)
+    rows, cols = rows.clamp(0, 300), torch.arange(Dr, device=cuda_device)[None]
+    assert torch.equal(c, cos[rows, cols] * inside) and torch.equal(s, sin[rows, cols] * inside)
