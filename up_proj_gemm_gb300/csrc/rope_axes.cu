@@ -100,14 +100,6 @@ __device__ __forceinline__ int64_t position(const RopeParams& p, int j, int64_t 
 }
 __device__ __forceinline__ bool in_table(const RopeParams& p, int64_t row) { return row >= 0 && row < p.cs_rows; }
 
-// The same, checked: -1 and a report when it lies outside the table.
-__device__ __forceinline__ int64_t table_row(const RopeParams& p, int j, int64_t t) {
-    const int64_t row = position(p, j, t);
-    if (in_table(p, row)) return row;
-    record_status(p.status, MLA_ERR_POS_RANGE);
-    return -1;
-}
-
 // VE floats of shared memory (by 16 bytes when VE > 1).
 template <int VE>
 __device__ __forceinline__ void from_table(const float* q, float (&v)[VE]) {
@@ -301,11 +293,13 @@ __global__ void __launch_bounds__(kThreads) rope_few_kernel(const __grid_constan
 // largest power of two that fits the warp beside the slots; the rest of the
 // warp takes other tokens. (A block per token with sums in shared memory waited
 // for itself: [8190, 8, 128] bf16 18.1 us.)
-constexpr int kSumThreads = 128;
-constexpr int kSumHeads = 4;  // heads in flight per lane (5 blocks per SM; 8 with 2 heads lost a third at D = 192)
+// [4096, 128, 64] of 192 channels' rows, bf16: 15.8 us, 4.4 TB/s (blocks of 128
+// 15.9; positions read pair by pair 16.9; [300, 100, 64] 3.7, 3.9, 4.5).
+constexpr int kSumThreads = 64;
+constexpr int kSumHeads = 4;  // heads in flight per lane (20 warps per SM; 32 with 2 heads lost a third at D = 192)
 
 template <typename E, int VE>
-__global__ void __launch_bounds__(kSumThreads, 5) rope_sum_kernel(const __grid_constant__ RopeParams p, int hl, int per_warp) {
+__global__ void __launch_bounds__(kSumThreads, 10) rope_sum_kernel(const __grid_constant__ RopeParams p, int hl, int per_warp) {
     grid_launch_next();
     grid_wait_previous();
     const int half = p.Dr / 2;
@@ -350,6 +344,11 @@ __global__ void __launch_bounds__(kSumThreads, 5) rope_sum_kernel(const __grid_c
                 }
             }
         }
+        // the positions all at once, and under the shuffles; then all the table's entries
+        const bool turns = mine && pair && h0 == 0;
+        int row[VE];
+#pragma unroll
+        for (int k = 0; k < VE; ++k) row[k] = turns ? (int)position(p, i0 + k, t) : 0;
         __syncwarp();
         for (int d = hl / 2; d >= 1; d /= 2)
 #pragma unroll
@@ -359,14 +358,24 @@ __global__ void __launch_bounds__(kSumThreads, 5) rope_sum_kernel(const __grid_c
             }
         if (!mine || h0 != 0) continue;
         if (pair) {
+            float c0[VE], c1[VE], n0[VE], n1[VE];
+            bool ok = true;
 #pragma unroll
             for (int k = 0; k < VE; ++k) {
-                const int64_t row = table_row(p, i0 + k, t);
-                const float* cr = p.cos_tab + (row < 0 ? 0 : row) * p.cs_width + i0 + k;
-                const float* sr = p.sin_tab + (row < 0 ? 0 : row) * p.cs_width + i0 + k;
+                const bool in = in_table(p, row[k]);
+                ok &= in;
+                const int64_t at = (in ? row[k] : 0) * p.cs_width + i0 + k;
+                c0[k] = __ldg(p.cos_tab + at);
+                c1[k] = __ldg(p.cos_tab + at + half);
+                n0[k] = __ldg(p.sin_tab + at);
+                n1[k] = __ldg(p.sin_tab + at + half);
+            }
+            if (!ok) record_status(p.status, MLA_ERR_POS_RANGE);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) {
                 const float u = a[k], w = b[k];
-                a[k] = u * __ldg(cr) + w * __ldg(sr + half);
-                b[k] = w * __ldg(cr + half) - u * __ldg(sr);
+                a[k] = u * c0[k] + w * n1[k];
+                b[k] = w * c1[k] - u * n0[k];
             }
         }
         Raw<E, VE> ra, rb;
