@@ -330,3 +330,24 @@ def test_weight_gradients_run_beside_dx(cuda_device, T, K, F):
     want = mlaq.gated_ffn_bwd(alone[0], x, wgu, wd, gu, h)
     assert all(torch.equal(a, b) for k in kept for a, b in zip(k, alone))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T,K,F", [(1290, 2568, 1664), (1290, 3328, 2600), (1290, 2568, 3328)])
+def test_last_wave_split(cuda_device, T, K, F):
+    """A few tiles more than full waves of the gate and up, the down or dh product: these tiles' reductions are split, in
+    a grid beside the others', and the bits are the same call after call."""
+    x, wgu, wd, dy = make(T, K, F, seed=8)
+    y, gu, h = mlaq.gated_ffn_fwd(x, wgu, wd, save=True)
+    check_forward(x, wgu, wd, "silu", y, gu, h)
+    dgu = torch.empty((T, 2 * F), dtype=bf16, device=cuda_device)
+    grads = mlaq.gated_ffn_bwd(dy, x, wgu, wd, gu, h, dgate_up=dgu)
+    dh, e = product(dy, wd.t())
+    g, u = gu.to(f64).split(F, 1)
+    a, da = act64(g, "silu")
+    check(dgu[:, :F], dh * u * da, e * (u * da).abs() + 64 * U * (dh * u).abs() * (1 + g.abs()), "dg")
+    check(dgu[:, F:], dh * a, e * a.abs() + 64 * U * (dh * a).abs() + 32 * U * (dh * g).abs() * 1e-3, "du")
+    check(grads[0], *product(dgu, wgu.t()), "dx")
+    for _ in range(4):
+        assert torch.equal(mlaq.gated_ffn_fwd(x, wgu, wd), y)
+        again = mlaq.gated_ffn_bwd(dy, x, wgu, wd, gu, h)
+        assert all(torch.equal(b, c) for b, c in zip(grads, again))

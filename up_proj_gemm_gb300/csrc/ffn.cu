@@ -43,6 +43,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSlotBytes = 32u * 64u;         // 32 rows x 32 columns of a result, 64-byte swizzle (kStore: two, as one)
 constexpr int kEpiWarps = 8;
 constexpr int kSplitSteps = 12;                     // K steps that adding up a split reduction costs
+constexpr int kTailSteps = 16;                     // K steps that a grid for the last tiles costs
 constexpr int kTileSteps = 4;                      // K steps that a tile costs beside its own
 constexpr int kMaxSplits = 4;                      // clusters of 8 CTAs
 
@@ -81,7 +82,7 @@ struct GemmParams {
     int splits;               // parts of the reduction, each a pair of the cluster
     int after;                // kFirst, kAfter or kBeside
     int late;                 // the next grid runs beside this one: it starts after this one's wait
-    int early, head;          // the first `early` clusters share `head` tiles before all share the rest
+    int early, head;          // the first `early` clusters share `head` tiles before all share the rest (0: not in this grid)
     int F, act;
     uint16_t* gate_up_out;    // kGate: [M, 2F] or null
     const uint16_t* gate_up;  // kGateGrad: [M, 2F]
@@ -741,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_sync();  // every pair's partial sums are in place
         if (warp >= 2 && *abort_flag == 0) {
             int mt, nt;
-            tile_at(p, cluster, mt, nt);
+            tile_at(p, first, mt, nt);
             epi.tile(0, nt * (EPI == kGate ? 128 : 256), (int64_t)mt * 256 + prank * 128 + quad * 32, [] {});
         }
     }
@@ -1099,7 +1100,7 @@ int64_t tiles_ahead(int64_t tiles, int64_t clusters, const Idle& idle, int64_t c
 // either way).
 template <bool AMN, bool BMN, int EPI>
 int gemm(const Product* jobs, int count, GemmParams p, int64_t red, After after, const DeviceInfo& di,
-         cudaStream_t stream, int64_t beside = 0, Idle* leaves = nullptr, const Idle* idle = nullptr) {
+         cudaStream_t stream, int64_t beside = 0, Idle* leaves = nullptr, const Idle* idle = nullptr, bool tail = false) {
     int64_t tiles = 0;
     for (int j = 0; j < count; ++j) {
         Result& r = p.r[j];
@@ -1115,15 +1116,29 @@ int gemm(const Product* jobs, int count, GemmParams p, int64_t red, After after,
     p.k_tiles = (int)((red + kBK - 1) / kBK);
     p.after = after;
     // Split the reduction when the tiles leave pairs idle: in K steps, a pair's
-    // time is its share of them plus what the exchange of the sums costs.
-    int clusters = 0;
-    int64_t best = 0, pairs = 0;
+    // time is its share of them plus what the exchange of the sums costs. With
+    // `tail`, the tiles of a last wave that is nearly empty are split too, in a
+    // grid of their own beside the others (forward, T = 1100, K = F = 4096 103 ->
+    // 93 us; T = 256, K = 4096, F = 11008 75.8 -> 72.5; T = 512, K = 2048, F =
+    // 10240, whose 32 steps are too few for it, 63 -> 65). Not for dx: there the
+    // weights' gradients fill the idle pairs.
+    int clusters = 0, tail_splits = 0;
+    int64_t best = 0, pairs = 0, last = 0;
     for (int s = 1; s <= kMaxSplits; ++s) {
         int n = 0;
         const int st = resident_clusters<AMN, BMN, EPI>(di, s, &n);
         if (st != MLA_OK) return st;
-        if (s == 1) pairs = n;
         const int64_t all = tiles + beside;
+        if (s == 1) {
+            pairs = n;
+            last = all % n;
+        } else if (tail && all > pairs && last && last <= n && p.k_tiles >= 4 * s) {
+            const int64_t cost = (p.k_tiles + s - 1) / s + kSplitSteps + kTailSteps;
+            if (cost < (tail_splits ? best : (int64_t)p.k_tiles)) {
+                best = cost;
+                tail_splits = s;
+            }
+        }
         if (s > 1 && (all > n || p.k_tiles < 4 * s)) continue;
         const int64_t cost = s == 1 ? (all + n - 1) / n * p.k_tiles : (p.k_tiles + s - 1) / s + kSplitSteps;
         if (s == 1 || cost < best) {
@@ -1134,7 +1149,7 @@ int gemm(const Product* jobs, int count, GemmParams p, int64_t red, After after,
     }
     if (leaves) {
         p.late = 1;
-        const int64_t last = tiles * p.splits % pairs;
+        last = tiles * p.splits % pairs;
         leaves->pairs = last ? pairs - last : 0;
         leaves->steps = p.splits > 1 ? p.k_tiles / p.splits + kSplitSteps : p.k_tiles;
     }
@@ -1164,8 +1179,19 @@ int gemm(const Product* jobs, int count, GemmParams p, int64_t red, After after,
         const int st = make_tmap_3d(&tg, gu, F, 2, T, 2 * F, 4 * F, 32, 1, 32, true);
         if (st != MLA_OK) return st;
     }
-    return launch_overlapped(ffn_gemm_kernel<AMN, BMN, EPI>, (unsigned)(2 * p.splits * clusters), kThreads,
-                             Smem<EPI>::kBytes, 2u * p.splits, stream, ta[0], tb[0], to[0], tg, ta[1], tb[1], to[1], p);
+    auto launch = [&](const GemmParams& q, int64_t n) {
+        return launch_overlapped(ffn_gemm_kernel<AMN, BMN, EPI>, (unsigned)(2 * q.splits * n), kThreads,
+                                 Smem<EPI>::kBytes, 2u * q.splits, stream, ta[0], tb[0], to[0], tg, ta[1], tb[1], to[1],
+                                 q);
+    };
+    if (!tail_splits) return launch(p, clusters);
+    GemmParams whole = p, rest = p;
+    whole.tiles = rest.head = (int)(tiles - last);
+    whole.late = 1;
+    rest.splits = tail_splits;
+    rest.after = kBeside;
+    const int st = launch(whole, clusters);
+    return st == MLA_OK ? launch(rest, last) : st;
 }
 
 // Whether a product of T tokens and `rows` weight rows (kGate: channels) takes
@@ -1276,10 +1302,10 @@ MLAQ_API int mla_gated_ffn_fwd(const mla_ffn_shape* shape, const void* x, const 
     const Product up{{x, s.T, s.K, ld}, {w_gate_up, 2 * s.F, s.K, s.K}, s.T, s.F, h};
     const Product down{{h, s.T, s.F, s.F}, {w_down, s.K, s.F, s.F}, s.T, s.K, y};
     st = few_tokens<kGate>(s.T, s.F, di) ? narrow<false, kGate>(up, p, s.K, kFirst, di, cs)
-                       : gemm<false, false, kGate>(&up, 1, p, s.K, kFirst, di, cs);
+                       : gemm<false, false, kGate>(&up, 1, p, s.K, kFirst, di, cs, 0, nullptr, nullptr, true);
     if (st != MLA_OK) return st;
     return few_tokens<kStore>(s.T, s.K, di) ? narrow<false, kStore>(down, p, s.F, kAfter, di, cs)
-                         : gemm<false, false, kStore>(&down, 1, p, s.F, kAfter, di, cs);
+                         : gemm<false, false, kStore>(&down, 1, p, s.F, kAfter, di, cs, 0, nullptr, nullptr, true);
 }
 
 MLAQ_API int mla_gated_ffn_bwd(const mla_ffn_shape* shape, const void* dy, const void* x, const void* w_gate_up,
@@ -1324,7 +1350,7 @@ MLAQ_API int mla_gated_ffn_bwd(const mla_ffn_shape* shape, const void* dy, const
     if (hidden) {
         const Product q{oy, {w_down, s.K, s.F, s.F}, s.T, s.F, dgate_up};
         st = few_tokens<kGateGrad>(s.T, s.F, di) ? narrow<true, kGateGrad>(q, p, s.K, kFirst, di, cs)
-                           : gemm<false, true, kGateGrad>(&q, 1, p, s.K, kFirst, di, cs);
+                           : gemm<false, true, kGateGrad>(&q, 1, p, s.K, kFirst, di, cs, 0, nullptr, nullptr, true);
         if (st != MLA_OK) return st;
     }
     Idle idle;
