@@ -1196,16 +1196,17 @@ int gemm(const Product* jobs, int count, GemmParams p, int64_t red, After after,
 
 // Whether a product of T tokens and `rows` weight rows (kGate: channels) takes
 // the few-token kernel. Up to 128 tokens the bound is reading the weights; up
-// to 1024 it serves as a kernel of smaller tiles while they fill half the SMs
-// at most (T = 256, K = 1024, F = 2048: forward 19.0 against 20.6 us, backward
-// 29.0 against 36.9; T = 777, K = 1536, F = 4096, over twice that many tiles:
-// backward 83.5 against 69.1). Beyond 1024 the pairs' larger tiles win even
-// where they are few (T = 4000, K = 256, F = 512: 12.9 against 15.6).
+// to three of its token tiles it serves as a kernel of smaller tiles while they
+// fill half the SMs at most (T = 260, K = 1024, F = 2048: forward 16.8 against
+// 18.7 us, backward 24.9 against 28.0; T = 384, K = 2048, F = 800: 17.6 and 18.3,
+// 25.5 and 30.4; with all SMs full T = 200, K = 2048, F = 5632 backward 61.1
+// against 58.4). Beyond, the pairs' larger tiles win even where they are few (T =
+// 512, K = 2048, F = 512: 16.9 against 20.1, 22.1 against 24.2).
 template <int EPI>
 bool few_tokens(int64_t T, int64_t rows, const DeviceInfo& di) {
     if (T <= kNarrowMax) return true;
     const int64_t tiles = EPI == kGate ? (rows + 63) / 64 : (rows + 127) / 128;
-    return T <= 1024 && 2 * tiles * ((T + kNarrowMax - 1) / kNarrowMax) <= di.num_sms;
+    return T <= 3 * kNarrowMax && 2 * tiles * ((T + kNarrowMax - 1) / kNarrowMax) <= di.num_sms;
 }
 
 // The same product for few tokens (see ffn_narrow_kernel): w is [R, red] (or
