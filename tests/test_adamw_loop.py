@@ -1,0 +1,93 @@
+"""The optimizer's bookkeeping between steps without a GPU: tensors that report themselves as CUDA tensors, steps that
+are listed instead of launched, plans read back from their host copy."""
+import contextlib
+import ctypes
+import struct
+
+import pytest
+import torch
+
+import up_proj_gemm_gb300 as mlaq
+from up_proj_gemm_gb300 import _build, optim
+
+bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+HEADER, ENTRY = 48, 72  # bytes of a plan's header and of a tensor's entry: seven addresses, the size, the first place
+
+
+class FakeStream:
+    cuda_stream = 0
+
+    def record_event(self):
+        return None
+
+    def wait_event(self, event):
+        return None
+
+
+@pytest.fixture
+def steps(monkeypatch):
+    """The plans' entries of every step: (param, grad, exp_avg, exp_avg_sq, their scales, master, n)."""
+    _build.build()
+    mlaq.lib()
+    log, real = [], optim._call
+
+    def call(fn, what, *args):
+        if what != "mla_adamw_step":
+            return real(fn, what, *args)
+        host = args[0]
+        count = struct.unpack("q", ctypes.string_at(host + 8, 8))[0]
+        log.append([struct.unpack("7Qq", ctypes.string_at(host + HEADER + i * ENTRY, 64)) for i in range(count)])
+
+    monkeypatch.setattr(mlaq, "_calls", None)
+    monkeypatch.setattr(optim, "_call", call)
+    monkeypatch.setattr(optim, "_stream", lambda device, stream: None)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: FakeStream())
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    return log
+
+
+def made(n=2, bits=32, masters=False, dtype=f32):
+    params = [torch.nn.Parameter(torch.ones(40 + i, dtype=dtype)) for i in range(n)]
+    for p in params:
+        p.grad = torch.ones_like(p)
+    return params, mlaq.AdamW(params, 1e-3, state_bits=bits, masters=masters)
+
+
+def addresses(opt, grads):
+    lists = (opt.params, grads, opt.exp_avg, opt.exp_avg_sq, opt.exp_avg_scales, opt.exp_avg_sq_scales, opt.masters)
+    return [tuple(0 if v is None else v[i].data_ptr() for v in lists) + (opt.params[i].numel(),)
+            for i in range(len(opt.params))]
+
+
+@pytest.mark.parametrize("bits,masters", [(32, False), (32, True), (8, False)])
+def test_a_step_uses_the_buffers_of_its_time(steps, bits, masters):
+    """Whatever moved since the last step: a parameter, a gradient, a moment, a scale, a master."""
+    params, opt = made(bits=bits, masters=masters)
+    grads = [p.grad for p in params]
+    moves = [lambda: setattr(params[1], "data", params[1].data.clone()),
+             lambda: grads.__setitem__(0, grads[0].clone())]
+    for v in (opt.exp_avg, opt.exp_avg_sq, opt.exp_avg_scales, opt.exp_avg_sq_scales, opt.masters):
+        if v is not None:
+            moves.append(lambda v=v: v.__setitem__(1, v[1].clone()))
+    opt.step(grads)
+    for i, move in enumerate(moves):
+        move()
+        opt.step(grads)
+        assert steps[-1] == addresses(opt, grads), i
+    assert len(steps) == 1 + len(moves)
+
+
+def test_buffers_that_change_their_type_or_layout_are_checked_again(steps):
+    """The same address as another type, size or order is no plan's any more."""
+    params, opt = made(n=1)
+    buffer = torch.ones(80)
+    opt.step([buffer[:40]])
+    with pytest.raises(ValueError):  # 40 elements, two apart
+        opt.step([buffer[::2]])
+    opt.step([buffer.view(bf16)[:40]])  # the same start, now bf16
+    assert struct.unpack("4i", ctypes.string_at(opt._plan.host_ptr + 32, 16))[1] == 1
+    with pytest.raises(ValueError):
+        opt.step([buffer[:39]])
+    opt.step([buffer[:40]])
+    assert len(steps) == 3

@@ -156,19 +156,22 @@ class AdamW:
         self.exp_avg_scales = scales() if state_bits == 8 else None
         self.exp_avg_sq_scales = scales() if state_bits == 8 else None
         self.masters = [p.detach().float().clone() for p in self.params] if masters else None
-        self._plan, self._grads = None, None
+        self._plan, self._places = None, None
 
     def step(self, grads=None, grad_scale=None, stream=None):
         """One step; every parameter needs a gradient."""
         grads = [p.grad for p in self.params] if grads is None else list(grads)
         if any(g is None for g in grads):
             raise ValueError("a parameter has no gradient")
-        at = [g.data_ptr() for g in grads]
-        if self._plan is None or at != self._grads:
+        places = [None if v is None else [(t.data_ptr(), t.numel(), t.dtype, t.is_contiguous()) for t in v]
+                  for v in (self.params, grads, self.exp_avg, self.exp_avg_sq, self.exp_avg_scales,
+                            self.exp_avg_sq_scales, self.masters)]
+        if self._plan is None or places != self._places:
+            self._plan = None  # also when the new one is refused
             self._plan = adamw_plan([p.detach() for p in self.params], grads, self.exp_avg, self.exp_avg_sq,
                                     masters=self.masters, exp_avg_scales=self.exp_avg_scales,
                                     exp_avg_sq_scales=self.exp_avg_sq_scales)
-            self._grads = at
+            self._places = places
         self.steps += 1
         seed = None if self.seed is None else (self.seed + self.steps * 0x9E3779B1) & 0xFFFFFFFF
         adamw_step(self._plan, self.steps, self.lr, self.betas, self.eps, self.weight_decay, grad_scale, seed, stream)
