@@ -162,6 +162,25 @@ def _stream(device, stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream=None, scratch=False):
+    """A tensor that a call on `stream` (None: the current one) writes. Work on
+    another stream than the current one gets memory of that stream: memory of
+    the current one may still be in use there, and what the binding drops at
+    return (scratch) would be handed out again under the work that uses it.
+    What the caller keeps may then be read on the current stream, until it is
+    dropped."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if not scratch:
+        t.record_stream(current)
+    return t
+
+
 def _need(t, name, dtype, device=None, ndim=None, shape=None, numel=None, min_numel=None):
     """Check a tensor argument. The C ABI receives bare pointers, so every
     extent a kernel reads or writes is checked here: type, dtype, rank and

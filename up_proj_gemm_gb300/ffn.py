@@ -12,7 +12,7 @@ import torch
 
 import up_proj_gemm_gb300 as _pkg
 
-from . import _call, _need, _ptr, _SIGS, _status, _stream, lib
+from . import _call, _empty, _need, _ptr, _SIGS, _status, _stream, lib
 
 __all__ = ["FfnShape", "ACTIVATIONS", "gated_ffn_fwd", "gated_ffn_bwd"]
 
@@ -77,17 +77,17 @@ def gated_ffn_fwd(x, w_gate_up, w_down, act="silu", save=False, gate_up=None, h=
     _need(w_gate_up, "w_gate_up", _bf16, dev, shape=(2 * F, K))
     _status(status, dev)
     if y is None:
-        y = torch.empty((T, K), dtype=_bf16, device=dev)
+        y = _empty((T, K), _bf16, dev, stream)
     else:
         _need(y, "y", _bf16, dev, shape=(T, K))
     if h is None:
-        h = torch.empty((T, F), dtype=_bf16, device=dev)
+        h = _empty((T, F), _bf16, dev, stream, scratch=not save)
     else:
         _need(h, "h", _bf16, dev, shape=(T, F))
     if gate_up is not None:
         _need(gate_up, "gate_up", _bf16, dev, shape=(T, 2 * F))
     elif save:
-        gate_up = torch.empty((T, 2 * F), dtype=_bf16, device=dev)
+        gate_up = _empty((T, 2 * F), _bf16, dev, stream)
     s = FfnShape(T, K, F, ld, a, 0)
     _call(lib().mla_gated_ffn_fwd, "mla_gated_ffn_fwd", ctypes.byref(s), _ptr(x), _ptr(w_gate_up), _ptr(w_down),
           _ptr(gate_up), _ptr(h), _ptr(y), _ptr(status), _stream(dev, stream))
@@ -138,7 +138,7 @@ def gated_ffn_bwd(dy, x, w_gate_up, w_down, gate_up, h, act="silu", dx=True, dw_
     _status(status, dev)
     if hidden:
         if dgate_up is None:
-            dgate_up = torch.empty((T, 2 * F), dtype=_bf16, device=dev)
+            dgate_up = _empty((T, 2 * F), _bf16, dev, stream, scratch=True)
         else:
             _need(dgate_up, "dgate_up", _bf16, dev, shape=(T, 2 * F))
     outs = []
@@ -147,7 +147,7 @@ def gated_ffn_bwd(dy, x, w_gate_up, w_down, gate_up, h, act="silu", dx=True, dw_
         if not want:
             t = None
         elif t is True:
-            t = torch.empty(shape, dtype=_bf16, device=dev)
+            t = _empty(shape, _bf16, dev, stream)
         else:
             _need(t, name, _bf16, dev, shape=shape)
         outs.append(t)

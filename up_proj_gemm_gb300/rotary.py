@@ -15,7 +15,7 @@ import torch
 
 import up_proj_gemm_gb300 as _pkg
 
-from . import _call, _need, _ptr, _SIGS, _status, _stream, lib
+from . import _call, _empty, _need, _ptr, _SIGS, _status, _stream, lib
 
 __all__ = ["RopeAxesShape", "rope_sections", "rope_axes", "rope_axes_table"]
 
@@ -102,7 +102,7 @@ def rope_axes(x, cos, sin, pos, axes, Dr, inverse=False, sum_heads=False, out=No
         _status(status, dev)
     Ho = 1 if sum_heads else H
     if out is None:
-        out = torch.empty((T, Ho, D), dtype=x.dtype, device=dev)
+        out = _empty((T, Ho, D), x.dtype, dev, stream)
         out_t, out_h = Ho * D, D
     else:
         if not isinstance(out, torch.Tensor) or out.dtype is not x.dtype:
@@ -139,11 +139,11 @@ def rope_axes_table(cos, sin, pos, axes, Dr, cos_out=None, sin_out=None, status=
     if status is not None:
         _status(status, dev)
     if cos_out is None:
-        cos_out = torch.empty((T, Dr), dtype=_f32, device=dev)
+        cos_out = _empty((T, Dr), _f32, dev, stream)
     else:
         _need(cos_out, "cos_out", _f32, dev, shape=(T, Dr))
     if sin_out is None:
-        sin_out = torch.empty((T, Dr), dtype=_f32, device=dev)
+        sin_out = _empty((T, Dr), _f32, dev, stream)
     else:
         _need(sin_out, "sin_out", _f32, dev, shape=(T, Dr))
     rows, width = cos.shape
