@@ -121,10 +121,12 @@ PyObject* rope_axes_table(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// x's row pitch when it is a bf16 matrix of contiguous rows like [T, K], else -1.
+// x's row pitch when it is a bf16 matrix of contiguous rows like [T, K] that do not overlap, else -1. (A pitch of 0,
+// one row for all tokens, would say dense to the library.)
 int64_t row_pitch(const at::Tensor* x, int64_t T, int64_t K) {
     if (x->scalar_type() != at::kBFloat16 || x->dim() != 2 || !shaped(*x, T, K) || (K > 1 && x->stride(1) != 1)) return -1;
-    return T > 1 ? x->stride(0) : K;
+    if (T <= 1) return K;
+    return x->stride(0) >= K ? x->stride(0) : -1;
 }
 
 // ffn_fwd(x, w_gate_up, w_down, act, save)

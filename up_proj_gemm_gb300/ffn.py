@@ -45,6 +45,8 @@ def _rows(t, name, dev=None, T=None, K=None):
     rows, cols = t.shape
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit inner stride")
+    if rows > 1 and t.stride(0) < cols:  # a row for all tokens, too: pitch 0 would say dense
+        raise ValueError(f"{name} must have rows that do not overlap, got a pitch of {t.stride(0)} for {cols} elements")
     return t.stride(0) if rows > 1 else cols
 
 
@@ -58,7 +60,7 @@ def gated_ffn_fwd(x, w_gate_up, w_down, act="silu", save=False, gate_up=None, h=
                   stream=None):
     """y [T, K] bf16 = (act(g) * u) w_down^T with [g | u] = x w_gate_up^T.
 
-    x [T, K] bf16 (rows may have a pitch), w_gate_up [2F, K] bf16 (F gate
+    x [T, K] bf16 (rows may have a pitch of K or more), w_gate_up [2F, K] bf16 (F gate
     rows, then F up rows), w_down [K, F] bf16; act "silu", "gelu" or
     "gelu_tanh". save=True returns (y, gate_up [T, 2F], h [T, F]), what
     gated_ffn_bwd needs. h is also the scratch of the second product."""
