@@ -257,7 +257,7 @@ def rope_table_pack(cos, sin, Dr, out=None, stream=None):
     _need(sin, "sin", torch.float32, dev, shape=cos.shape)
     rows, width = cos.shape
     if out is None:
-        out = torch.empty((Dr // 2, rows, 4), dtype=torch.float32, device=dev)
+        out = _empty((Dr // 2, rows, 4), torch.float32, dev, stream)
     _need(out, "out", torch.float32, dev, numel=rows * (Dr // 2) * 4)
     _call(lib().mla_rope_table_pack, "mla_rope_table_pack", int(rows), int(width), int(Dr), _ptr(cos), _ptr(sin),
           _ptr(out), _stream(dev, stream))
@@ -315,10 +315,10 @@ def fwd(x, W, cos, sin, H, Dn, Dr, bias=None, pos=None, weight_mode="bf16", out_
         sshape = (T, H, nb)
     q_dtype = torch.uint8 if om else torch.bfloat16
     if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=q_dtype, device=dev)
+        q_out = _empty((T, H, D), q_dtype, dev, stream)
     _need(q_out, "q_out", q_dtype, dev, numel=T * N)
     if om and q_scales is None:
-        q_scales = torch.empty(sshape, dtype=torch.uint8, device=dev)
+        q_scales = _empty(sshape, torch.uint8, dev, stream)
     if om:
         _need(q_scales, "q_scales", torch.uint8, dev, numel=math.prod(sshape))
     s = _shape(T, K, H, Dn, Dr, cos)
@@ -357,14 +357,14 @@ def bwd_dgrad(dq, W, cos, sin, H, Dn, Dr, pos=None, dx=None, status=None, stream
     _tables(cos, sin, dev, T, pos)
     _status(status, dev)
     if dx is None:
-        dx = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+        dx = _empty((T, K), torch.bfloat16, dev, stream)
     _need(dx, "dx", torch.bfloat16, dev, numel=T * K)
     _rope_buf(dq_pre_rope, T, H, Dr, dev)
     s = _shape(T, K, H, Dn, Dr, cos)
     with torch.cuda.device(dev):
         need = int(lib().mla_q_uproj_workspace_size(ctypes.byref(s), 1))
     if workspace is None and need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = _empty((need,), torch.uint8, dev, stream, scratch=True)
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8, dev, ndim=1)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -390,10 +390,10 @@ def bwd_wgrad(dq, x, cos, sin, H, Dn, Dr, pos=None, dW=None, db=True, status=Non
     _tables(cos, sin, dev, T, pos)
     _status(status, dev)
     if dW is None:
-        dW = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+        dW = _empty((N, K), torch.bfloat16, dev, stream)
     _need(dW, "dW", torch.bfloat16, dev, numel=N * K)
     if db is True:
-        db = torch.empty((N,), dtype=torch.bfloat16, device=dev)
+        db = _empty((N,), torch.bfloat16, dev, stream)
     elif db is False:
         db = None
     if db is not None:
@@ -480,7 +480,7 @@ def bwd_mxfp8(dq, W, x, cos, sin, H, Dn, Dr, pos=None, dx=True, dW=True, db=True
     outs = {}
     for name, t, shape in (("dx", dx, (T, K)), ("dW", dW, (N, K)), ("db", db, (N,))):
         if t is True:
-            t = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            t = _empty(shape, torch.bfloat16, dev, stream)
         elif t is False:
             t = None
         if t is not None:
@@ -490,7 +490,7 @@ def bwd_mxfp8(dq, W, x, cos, sin, H, Dn, Dr, pos=None, dx=True, dW=True, db=True
     s = _shape(T, K, H, Dn, Dr, cos)
     need = int(lib().mla_q_uproj_workspace_size(ctypes.byref(s), 3))
     if workspace is None and need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = _empty((need,), torch.uint8, dev, stream, scratch=True)
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8, dev, ndim=1)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -531,19 +531,19 @@ def mxfp8_quantize_rows(inp, codes=None, scales=None, stream=None, group=None):
     ld_in = int(inp.stride(0)) if R > 1 else int(C)
     dev = inp.device
     if codes is None:
-        codes = torch.empty((R, C), dtype=torch.uint8, device=dev)
+        codes = _empty((R, C), torch.uint8, dev, stream)
     _need(codes, "codes", torch.uint8, dev, numel=R * C)
     dt = 0 if inp.dtype == torch.float32 else 1
     if group is not None:
         n = int(lib().mxfp8_grouped_scale_bytes(R, (C + 31) // 32, int(group)))
         if scales is None:
-            scales = torch.empty((n,), dtype=torch.uint8, device=dev)
+            scales = _empty((n,), torch.uint8, dev, stream)
         _need(scales, "scales", torch.uint8, dev, numel=n)
         _call(lib().mxfp8_quantize_rows_tiled, "mxfp8_quantize_rows_tiled", R, C, dt, _ptr(inp), ld_in,
               _ptr(codes), _ptr(scales), int(group), _stream(dev, stream))
         return codes, scales
     if scales is None:
-        scales = torch.empty((R, (C + 31) // 32), dtype=torch.uint8, device=dev)
+        scales = _empty((R, (C + 31) // 32), torch.uint8, dev, stream)
     _need(scales, "scales", torch.uint8, dev, numel=R * ((C + 31) // 32))
     _call(lib().mxfp8_quantize_rows, "mxfp8_quantize_rows", R, C, dt, _ptr(inp), ld_in, _ptr(codes),
           _ptr(scales), _stream(dev, stream))
@@ -564,19 +564,19 @@ def mxfp8_quantize_cols(inp, codes=None, scales=None, stream=None, group=None):
     ld_in = int(inp.stride(0)) if R > 1 else int(C)
     dev = inp.device
     if codes is None:
-        codes = torch.empty((C, R), dtype=torch.uint8, device=dev)
+        codes = _empty((C, R), torch.uint8, dev, stream)
     _need(codes, "codes", torch.uint8, dev, numel=R * C)
     dt = 0 if inp.dtype == torch.float32 else 1
     if group is not None:
         n = int(lib().mxfp8_grouped_scale_bytes(C, (R + 31) // 32, int(group)))
         if scales is None:
-            scales = torch.empty((n,), dtype=torch.uint8, device=dev)
+            scales = _empty((n,), torch.uint8, dev, stream)
         _need(scales, "scales", torch.uint8, dev, numel=n)
         _call(lib().mxfp8_quantize_cols_tiled, "mxfp8_quantize_cols_tiled", R, C, dt, _ptr(inp), ld_in,
               _ptr(codes), _ptr(scales), int(group), _stream(dev, stream))
         return codes, scales
     if scales is None:
-        scales = torch.empty((C, (R + 31) // 32), dtype=torch.uint8, device=dev)
+        scales = _empty((C, (R + 31) // 32), torch.uint8, dev, stream)
     _need(scales, "scales", torch.uint8, dev, numel=C * ((R + 31) // 32))
     _call(lib().mxfp8_quantize_cols, "mxfp8_quantize_cols", R, C, dt, _ptr(inp), ld_in, _ptr(codes),
           _ptr(scales), _stream(dev, stream))
@@ -594,7 +594,7 @@ def mxfp8_swizzle_scales(scales, out=None, stream=None, group=128):
     rows, cols = scales.shape
     n = int(lib().mxfp8_grouped_scale_bytes(rows, cols, group))
     if out is None:
-        out = torch.empty((n,), dtype=torch.uint8, device=scales.device)
+        out = _empty((n,), torch.uint8, scales.device, stream)
     _need(out, "out", torch.uint8, scales.device, numel=n)
     ld = int(scales.stride(0)) if rows > 1 else int(cols)
     if group == 128:
@@ -623,9 +623,9 @@ def kv_fwd(c_kv, W, k_pe, cos, sin, H, Dn, Dv, Dr, pos=None, o_key=None, o_value
     _tables(cos, sin, dev, T, pos)
     _status(status, dev)
     if o_key is None:
-        o_key = torch.empty((T, H, Dn + Dr), dtype=torch.bfloat16, device=dev)
+        o_key = _empty((T, H, Dn + Dr), torch.bfloat16, dev, stream)
     if o_value is None:
-        o_value = torch.empty((T, H, Dv), dtype=torch.bfloat16, device=dev)
+        o_value = _empty((T, H, Dv), torch.bfloat16, dev, stream)
     _need(o_key, "o_key", torch.bfloat16, dev, numel=T * H * (Dn + Dr))
     _need(o_value, "o_value", torch.bfloat16, dev, numel=T * H * Dv)
     s = KvShape(T=T, K=K, H=H, Dn=Dn, Dv=Dv, Dr=Dr, cs_rows=cos.shape[0], cs_width=cos.shape[1])
