@@ -3,6 +3,7 @@ are listed instead of launched, plans read back from their host copy."""
 import contextlib
 import ctypes
 import struct
+import weakref
 
 import pytest
 import torch
@@ -91,3 +92,35 @@ def test_buffers_that_change_their_type_or_layout_are_checked_again(steps):
         opt.step([buffer[:39]])
     opt.step([buffer[:40]])
     assert len(steps) == 3
+
+
+def test_gradients_are_not_held(steps):
+    """A dropped gradient is gone, and one at the same place needs no new plan."""
+    params, opt = made()
+    opt.step()
+    plan, refs = opt._plan, [weakref.ref(p.grad) for p in params]
+    for p in params:
+        p.grad = None
+    assert all(r() is None for r in refs)
+    buffers = [torch.ones(p.numel()) for p in params]
+    opt.step([b.view(-1) for b in buffers])
+    assert opt._plan is not plan
+    plan = opt._plan
+    opt.step([b.view(-1) for b in buffers])  # other tensors, the same buffers
+    assert opt._plan is plan and steps[-1] == addresses(opt, buffers)
+
+
+def test_a_side_stream_keeps_what_it_reads(steps, monkeypatch):
+    """Gradients that another stream still reads are recorded on it; on the current one nothing is."""
+    class Side(FakeStream):
+        cuda_stream = 7
+
+    kept = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: kept.append((t.data_ptr(), s.cuda_stream)))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    params, opt = made()
+    opt.step()
+    opt.step(stream=FakeStream())
+    assert not kept
+    opt.step(stream=Side())
+    assert {(p.grad.data_ptr(), 7) for p in params} <= set(kept)

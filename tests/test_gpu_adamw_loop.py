@@ -37,3 +37,16 @@ def test_replaced_state_is_stepped(cuda_device, name):
     getattr(opt, name)[0] = fresh
     opt.step()
     assert torch.equal(left, kept) and not torch.equal(fresh, kept)
+
+
+def test_gradients_are_not_kept(cuda_device):
+    """With p.grad = None after a step, the gradients' memory is free: only parameters, moments and a plan remain."""
+    n = 1 << 22
+    p = torch.nn.Parameter(torch.ones(n, device=cuda_device))
+    opt = mlaq.AdamW([p], lr=1e-3)
+    before = torch.cuda.memory_allocated(cuda_device)
+    for _ in range(3):
+        p.grad = torch.ones_like(p)
+        opt.step()
+        p.grad = None
+        assert torch.cuda.memory_allocated(cuda_device) - before < n  # the gradient is 4 n bytes

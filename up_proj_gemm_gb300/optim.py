@@ -38,7 +38,8 @@ _FLOATS = {torch.float32: 0, torch.bfloat16: 1}
 
 
 class AdamwPlan:
-    """The tensors of a step (held here), their plan on the host and its device copy."""
+    """The tensors of a step (held here: parameters, gradients, moments, scales, masters), their plan on the host and
+    its device copy."""
 
     def __init__(self, tensors, host, device_copy, device):
         self.tensors, self.host, self.device_copy, self.device = tensors, host, device_copy, device
@@ -46,6 +47,10 @@ class AdamwPlan:
         self.stream = torch.cuda.current_stream(device)  # the one the copy was made on
         self.copied = self.stream.record_event()
         self.where = (self.host_ptr, self.device_ptr, -1 if device.index is None else device.index, self.stream.cuda_stream)
+
+    def release_gradients(self):
+        """Hold the gradients no longer: whoever takes a step keeps them until it has run."""
+        self.tensors[1] = None
 
     def ready_on(self, stream):
         """Let `stream` use the device copy: after the copying stream, and held until it is done. (A capture starts
@@ -171,9 +176,14 @@ class AdamW:
             self._plan = adamw_plan([p.detach() for p in self.params], grads, self.exp_avg, self.exp_avg_sq,
                                     masters=self.masters, exp_avg_scales=self.exp_avg_scales,
                                     exp_avg_sq_scales=self.exp_avg_sq_scales)
+            self._plan.release_gradients()
             self._places = places
         self.steps += 1
         seed = None if self.seed is None else (self.seed + self.steps * 0x9E3779B1) & 0xFFFFFFFF
         adamw_step(self._plan, self.steps, self.lr, self.betas, self.eps, self.weight_decay, grad_scale, seed, stream)
+        if stream is not None and grads:
+            if stream.cuda_stream != torch.cuda.current_stream(grads[0].device).cuda_stream:
+                for g in grads:  # dropped on the current stream, they stay until this one has read them
+                    g.record_stream(stream)
         for p in self.params:  # autograd sees that they were written
             torch.autograd.graph.increment_version(p)
