@@ -124,3 +124,19 @@ def test_a_side_stream_keeps_what_it_reads(steps, monkeypatch):
     assert not kept
     opt.step(stream=Side())
     assert {(p.grad.data_ptr(), 7) for p in params} <= set(kept)
+
+
+def test_compiled_comparison():
+    """The compiled list of places differs when the Python one does, and only then."""
+    _build.build()
+    mlaq.lib()
+    if mlaq._calls is None:
+        pytest.skip("calls.cpp was not built here")
+    f = mlaq._calls.adamw_places
+    a, b, c = torch.zeros(40), torch.zeros(40), torch.zeros(6, 6)
+    assert f([a, b], None, [c]) == f([a.view(-1), b.detach()], None, [c[:]])
+    same = [([a], [b]), ([a, b], []), ([a], None, [b]), ([b], [a]), ([a], [b[:39]]), ([a], [b.view(torch.int32)]),
+            ([a], [b.view(bf16)[:40]]), ([c], [b]), ([c.t()], [b]), ([a], [b], None)]
+    assert len({f(*v) for v in same}) == len(same)
+    assert f([a, None]) is None and f((a,)) is None and f([a.to_sparse()]) is None
+    assert f([torch.zeros(0)], []) != f([], [torch.zeros(0)])

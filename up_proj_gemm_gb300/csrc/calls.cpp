@@ -16,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <vector>
 
 #include "mlaq.h"
 
@@ -224,6 +225,31 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// adamw_places(list or None, ...): the address, size, type and layout of every tensor of the lists, as bytes that are
+// equal when all of these are. None when something else is listed.
+PyObject* adamw_places(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    std::vector<int64_t> v;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        if (a[i] == Py_None) {
+            v.push_back(-1);
+            continue;
+        }
+        if (!PyList_Check(a[i])) Py_RETURN_NONE;
+        const Py_ssize_t count = PyList_GET_SIZE(a[i]);
+        v.push_back(count);
+        for (Py_ssize_t k = 0; k < count; ++k) {
+            const at::Tensor* t = tensor(PyList_GET_ITEM(a[i], k));
+            if (!t || t->layout() != at::kStrided) Py_RETURN_NONE;
+            v.push_back((int64_t)reinterpret_cast<uintptr_t>(t->data_ptr()));
+            v.push_back(t->numel());
+            v.push_back((int64_t)t->scalar_type() * 2 + t->is_contiguous());
+        }
+    }
+    return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(v.data()), (Py_ssize_t)(v.size() * sizeof(int64_t)));
+    END_HANDLE_TH_ERRORS
+}
+
 PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
 }
@@ -235,6 +261,7 @@ PyMethodDef methods[] = {
     {"ffn_fwd", fast(ffn_fwd), METH_FASTCALL, nullptr},
     {"ffn_bwd", fast(ffn_bwd), METH_FASTCALL, nullptr},
     {"adamw_step", fast(adamw_step), METH_FASTCALL, nullptr},
+    {"adamw_places", fast(adamw_places), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

