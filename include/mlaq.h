@@ -665,7 +665,8 @@ typedef struct {
     double lr, beta1, beta2, eps, weight_decay;
     int64_t step;       /* t, counted from 1 */
     int32_t stochastic; /* 1: E4M3 codes, and bf16 parameters without a master, are rounded up with the
-                           probability of their fraction, from `seed`; 0: to nearest even */
+                           probability of their fraction, from `seed`; 0: to nearest even (8-bit moments then
+                           stay where a step moves them by less than half a code) */
     uint32_t seed;      /* another one each step */
 } mla_adamw_args;
 

@@ -140,3 +140,12 @@ def test_compiled_comparison():
     assert len({f(*v) for v in same}) == len(same)
     assert f([a, None]) is None and f((a,)) is None and f([a.to_sparse()]) is None
     assert f([torch.zeros(0)], []) != f([], [torch.zeros(0)])
+
+
+def test_default_seed():
+    """8-bit moments are rounded at random unless it is asked for otherwise."""
+    p = [torch.ones(4)]
+    assert mlaq.AdamW(p, 1e-3, state_bits=8).seed is not None
+    assert mlaq.AdamW(p, 1e-3, state_bits=8, seed=None).seed is None
+    assert mlaq.AdamW(p, 1e-3, state_bits=8, seed=5).seed == 5
+    assert mlaq.AdamW(p, 1e-3).seed is None

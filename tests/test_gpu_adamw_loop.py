@@ -1,11 +1,14 @@
 """AdamW as a training loop uses it."""
+import numpy as np
 import pytest
 import torch
 
+import oracle
 import up_proj_gemm_gb300 as mlaq
 
 pytestmark = pytest.mark.gpu
 bf16 = torch.bfloat16
+E4M3 = np.array([oracle.e4m3_decode(c) for c in range(256)])
 
 
 def test_a_moved_parameter_is_stepped(cuda_device):
@@ -50,3 +53,26 @@ def test_gradients_are_not_kept(cuda_device):
         opt.step()
         p.grad = None
         assert torch.cuda.memory_allocated(cuda_device) - before < n  # the gradient is 4 n bytes
+
+
+def decoded(codes, scales):
+    e = np.repeat(scales.cpu().numpy().astype(np.int64) - 127, 32)[:codes.numel()]
+    return E4M3[codes.cpu().numpy()] * np.exp2(e.astype(np.float64))
+
+
+def test_default_rounding_of_8_bit_moments_trains(cuda_device):
+    """Gradients of unit variance, default arguments: the corrected root of v is 1. Rounding at random leaves a root's
+    mean where it is and adds its variance to v: a step moves v by a thousandth, so the root stands f of a code step
+    (2^-3 to 2^-4 of it) away from a code with f about 0.0005 / 0.09, which adds f 0.09^2 to v each step and 5% of v
+    over the 1000 steps of the average. To nearest, v would stay where it is."""
+    n = 16384
+    g = torch.Generator(device=cuda_device).manual_seed(3)
+    p = torch.zeros(n, device=cuda_device)
+    grad = torch.zeros(n, device=cuda_device)
+    opt = mlaq.AdamW([p], lr=1e-3, state_bits=8)
+    for t in range(1, 601):
+        grad.normal_(generator=g)
+        opt.step([grad])
+        if t in (50, 200, 600):
+            v = np.square(decoded(opt.exp_avg_sq[0], opt.exp_avg_sq_scales[0])).mean() / (1 - 0.999 ** t)
+            assert abs(v ** 0.5 - 1) <= 0.06, (t, v ** 0.5)

@@ -115,7 +115,8 @@ def adamw_step(plan, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, 
     grad_scale: a float32 CUDA tensor of one element that multiplies every
     gradient. seed: an int, another one each step, rounds the 8-bit moments
     (and bf16 parameters without masters) up or down at random; None rounds
-    to nearest."""
+    to nearest, which holds 8-bit moments still where a step moves them by less
+    than half a code."""
     if not isinstance(plan, AdamwPlan):
         raise TypeError("plan must come from adamw_plan")
     c = _pkg._calls
@@ -144,21 +145,30 @@ def _places(*lists):
     return places
 
 
+_BY_STATE = object()  # the default seed: at random where the moments need it
+
+
 class AdamW:
     """AdamW for a list of parameters, one launch per step.
 
     ``state_bits`` 32 keeps float32 moments, 8 MXFP8 ones. ``masters`` keeps
     float32 copies of bf16 parameters. ``seed`` (an int) rounds at random as
-    in ``adamw_step``, from a seed that changes with the step. ``step()``
+    in ``adamw_step``, from a seed that changes with the step; None rounds to
+    nearest. Left out, it is 0 with MXFP8 moments and None with float32 ones:
+    a step moves a moment by less than half a step of its 8-bit code, and
+    rounded to nearest it would stay where it is (gradients of unit variance,
+    beta2 = 0.999: the root of v 0.86 of its value after 50 steps, 0.54 after
+    300). ``step()``
     takes the gradients from ``grads`` or the parameters' ``.grad``; the plan
     is rebuilt when a gradient's buffer is another one than at the last step."""
 
     def __init__(self, params, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=32, masters=False,
-                 seed=None):
+                 seed=_BY_STATE):
         if state_bits not in (32, 8):
             raise ValueError(f"state_bits must be 32 or 8, got {state_bits}")
         self.params = [p for p in params]
-        self.lr, self.betas, self.eps, self.weight_decay, self.seed = lr, betas, eps, weight_decay, seed
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.seed = (0 if state_bits == 8 else None) if seed is _BY_STATE else seed
         self.steps = 0
         dtype = torch.uint8 if state_bits == 8 else torch.float32
 
