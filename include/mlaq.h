@@ -667,7 +667,8 @@ typedef struct {
     int32_t stochastic; /* 1: E4M3 codes, and bf16 parameters without a master, are rounded up with the
                            probability of their fraction, from `seed`; 0: to nearest even (8-bit moments then
                            stay where a step moves them by less than half a code) */
-    uint32_t seed;      /* another one each step */
+    uint32_t seed;      /* another one each step, mixed well: seeds k * 0x9E3779B1 apart give place i the bits
+                           of place i + k */
 } mla_adamw_args;
 
 /*

@@ -149,3 +149,20 @@ def test_default_seed():
     assert mlaq.AdamW(p, 1e-3, state_bits=8, seed=None).seed is None
     assert mlaq.AdamW(p, 1e-3, state_bits=8, seed=5).seed == 5
     assert mlaq.AdamW(p, 1e-3).seed is None
+
+
+@pytest.mark.parametrize("seed", [0, 1, 11, 2**31, 2**32 - 1, 2**40 + 7, -3])
+def test_seeds_of_neighbouring_steps(steps, monkeypatch, seed):
+    """The kernel mixes place * 0x9E3779B1 + seed in 32 bits: two seeds a multiple k of that factor apart give place i the
+    bits of place i + k. Between a step and any of the four after it that shift is above 64, and no seed repeats. (Of
+    8000 pairs with random shifts one in 4000 draws would hold one below it.)"""
+    seeds = []
+    monkeypatch.setattr(optim, "adamw_step", lambda plan, step, *a: seeds.append(a[5]))
+    opt = mlaq.AdamW([torch.ones(4)], 1e-3, state_bits=8, seed=seed)
+    for _ in range(2000):
+        opt.step([torch.ones(4)])
+    assert len(set(seeds)) == 2000 and all(0 <= s < 2**32 for s in seeds)
+    inverse = pow(0x9E3779B1, -1, 2**32)
+    for apart in (1, 2, 3, 4):
+        shifts = [(b - a) * inverse % 2**32 for a, b in zip(seeds, seeds[apart:])]
+        assert min(min(s, 2**32 - s) for s in shifts) > 64

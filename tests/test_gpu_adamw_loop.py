@@ -76,3 +76,26 @@ def test_default_rounding_of_8_bit_moments_trains(cuda_device):
         if t in (50, 200, 600):
             v = np.square(decoded(opt.exp_avg_sq[0], opt.exp_avg_sq_scales[0])).mean() / (1 - 0.999 ** t)
             assert abs(v ** 0.5 - 1) <= 0.06, (t, v ** 0.5)
+
+
+def test_random_bits_of_consecutive_steps(cuda_device):
+    """Equal values between two codes, the same before each step: whether place i is rounded up at one step says nothing
+    of place i + lag at the next, within 6 standard errors."""
+    n = 1 << 18
+    p, grad = torch.zeros(n, device=cuda_device), torch.zeros(n, device=cuda_device)
+    opt = mlaq.AdamW([p], lr=0.0, betas=(0.9, 0.95), weight_decay=0.0, state_bits=8, seed=11)
+    m, ms = mlaq.mxfp8_quantize_rows(torch.full((n // 32, 32), 0.875, device=cuda_device))
+    v, vs = mlaq.mxfp8_quantize_rows(torch.full((n // 32, 32), 1.0, device=cuda_device))
+    ups = []
+    for _ in range(3):
+        for to, t in ((opt.exp_avg, m), (opt.exp_avg_scales, ms), (opt.exp_avg_sq, v), (opt.exp_avg_sq_scales, vs)):
+            to[0].copy_(t.reshape(-1))
+        opt.step([grad])
+        ups.append([t.double() - t.double().mean() for t in (opt.exp_avg[0], opt.exp_avg_sq[0])])
+    for a, b in zip(ups, ups[1:]):
+        for s, t in zip(a, b):
+            assert float(s.var()) > 0
+            for lag in (0, 1, 2, 3, 8, 32, 64):
+                bound = 6 * float(s.std() * t.std()) / n ** 0.5
+                assert abs(float((s[:n - lag] * t[lag:]).mean())) <= bound, lag
+                assert abs(float((s[lag:] * t[:n - lag]).mean())) <= bound, -lag

@@ -145,6 +145,16 @@ def _places(*lists):
     return places
 
 
+def _step_seed(seed, step):
+    """The kernel's seed of a step. It adds the seed to a multiple of the element's place, so seeds a small multiple of
+    that factor apart give the same bits a few places on: seed and step are mixed beyond sums of multiples (each
+    operation is a bijection of 32 bits: no two steps share a seed)."""
+    x = (seed + step * 0x3C6EF373) & 0xFFFFFFFF
+    x = ((x ^ (x >> 16)) * 0x6A09E667) & 0xFFFFFFFF
+    x = ((x ^ (x >> 13)) * 0xBB67AE85) & 0xFFFFFFFF
+    return x ^ (x >> 16)
+
+
 _BY_STATE = object()  # the default seed: at random where the moments need it
 
 
@@ -199,7 +209,7 @@ class AdamW:
             self._plan.release_gradients()
             self._places = places
         self.steps += 1
-        seed = None if self.seed is None else (self.seed + self.steps * 0x9E3779B1) & 0xFFFFFFFF
+        seed = None if self.seed is None else _step_seed(self.seed, self.steps)
         adamw_step(self._plan, self.steps, self.lr, self.betas, self.eps, self.weight_decay, grad_scale, seed, stream)
         if stream is not None and grads:
             if stream.cuda_stream != torch.cuda.current_stream(grads[0].device).cuda_stream:
