@@ -166,3 +166,16 @@ def test_seeds_of_neighbouring_steps(steps, monkeypatch, seed):
     for apart in (1, 2, 3, 4):
         shifts = [(b - a) * inverse % 2**32 for a, b in zip(seeds, seeds[apart:])]
         assert min(min(s, 2**32 - s) for s in shifts) > 64
+
+
+def test_a_refused_step_does_not_count(steps):
+    """The bias correction goes by the steps that were taken."""
+    params, opt = made()
+    opt.step()
+    with pytest.raises(ValueError):
+        opt.step(grad_scale=torch.zeros(2))
+    with pytest.raises(ValueError):
+        opt.step([p.grad[1:] for p in params])
+    assert opt.steps == 1 and len(steps) == 1
+    opt.step()
+    assert opt.steps == 2

@@ -208,9 +208,10 @@ class AdamW:
                                     exp_avg_sq_scales=self.exp_avg_sq_scales)
             self._plan.release_gradients()
             self._places = places
-        self.steps += 1
-        seed = None if self.seed is None else _step_seed(self.seed, self.steps)
-        adamw_step(self._plan, self.steps, self.lr, self.betas, self.eps, self.weight_decay, grad_scale, seed, stream)
+        step = self.steps + 1
+        seed = None if self.seed is None else _step_seed(self.seed, step)
+        adamw_step(self._plan, step, self.lr, self.betas, self.eps, self.weight_decay, grad_scale, seed, stream)
+        self.steps = step
         if stream is not None and grads:
             if stream.cuda_stream != torch.cuda.current_stream(grads[0].device).cuda_stream:
                 for g in grads:  # dropped on the current stream, they stay until this one has read them
