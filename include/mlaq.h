@@ -680,7 +680,9 @@ typedef struct {
  * mla_adamw_step enqueues one step. grad_scale: one device float32 that
  * multiplies every gradient (loss scale, clipping), or NULL for 1. The
  * launch reads the device copy only; a plan may be used on any stream, one
- * step at a time. The random bits of an element depend on the seed and on
+ * step at a time. The args are constants of the launch: a captured step
+ * replays with the step number, learning rate and seed of its capture, and
+ * reads the device copy at each replay. The random bits of an element depend on the seed and on
  * its place: its index plus the sizes of the tensors before its own, each
  * rounded up to a multiple of 64.
  */

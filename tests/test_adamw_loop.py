@@ -179,3 +179,20 @@ def test_a_refused_step_does_not_count(steps):
     assert opt.steps == 1 and len(steps) == 1
     opt.step()
     assert opt.steps == 2
+
+
+def test_a_captured_step_keeps_its_plan(steps, monkeypatch):
+    """What a graph's replays read stays when later steps use other buffers."""
+    params, opt = made()
+    opt.step()
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    opt.step()
+    refs = [weakref.ref(opt._plan.device_copy)] + [weakref.ref(p.grad) for p in params]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    for _ in range(3):
+        for p in params:
+            p.grad = p.grad.clone()
+        opt.step()
+        refs.append(weakref.ref(opt._plan.device_copy))
+    assert [r() is not None for r in refs] == [True] * 3 + [False] * 2 + [True]

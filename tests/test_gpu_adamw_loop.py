@@ -99,3 +99,24 @@ def test_random_bits_of_consecutive_steps(cuda_device):
                 bound = 6 * float(s.std() * t.std()) / n ** 0.5
                 assert abs(float((s[:n - lag] * t[lag:]).mean())) <= bound, lag
                 assert abs(float((s[lag:] * t[:n - lag]).mean())) <= bound, -lag
+
+
+def test_a_captured_step_outlives_other_gradients(cuda_device):
+    """A graph of a step replays on its own buffers after eager steps on other gradients."""
+    n = 3000
+    p = torch.nn.Parameter(torch.ones(n, device=cuda_device))
+    opt = mlaq.AdamW([p], lr=0.125, betas=(0.0, 0.0), weight_decay=0.0)  # a step is lr times the gradient's sign
+    p.grad = torch.ones_like(p)
+    opt.step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step()
+    p.grad = -torch.ones_like(p)
+    opt.step()
+    p.grad = None
+    junk = [torch.full((1 << 16,), 255, dtype=torch.uint8, device=cuda_device) for _ in range(8)]
+    junk += [torch.full((n,), float("nan"), device=cuda_device) for _ in range(8)]
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert ((p.detach().double() - (1 - 0.125 * 3)).abs() <= 100 * 2.0 ** -24).all()

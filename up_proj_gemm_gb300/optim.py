@@ -116,7 +116,11 @@ def adamw_step(plan, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, 
     gradient. seed: an int, another one each step, rounds the 8-bit moments
     (and bf16 parameters without masters) up or down at random; None rounds
     to nearest, which holds 8-bit moments still where a step moves them by less
-    than half a code."""
+    than half a code.
+
+    step, lr, betas, eps, weight_decay and seed are constants of the launch: a
+    CUDA graph replays the step with those of its capture, and needs the plan
+    as long as it lives."""
     if not isinstance(plan, AdamwPlan):
         raise TypeError("plan must come from adamw_plan")
     c = _pkg._calls
@@ -193,6 +197,7 @@ class AdamW:
         self.exp_avg_sq_scales = scales() if state_bits == 8 else None
         self.masters = [p.detach().float().clone() for p in self.params] if masters else None
         self._plan, self._places = None, None
+        self._captured = []  # what the steps inside captured graphs read
 
     def step(self, grads=None, grad_scale=None, stream=None):
         """One step; every parameter needs a gradient."""
@@ -212,6 +217,8 @@ class AdamW:
         seed = None if self.seed is None else _step_seed(self.seed, step)
         adamw_step(self._plan, step, self.lr, self.betas, self.eps, self.weight_decay, grad_scale, seed, stream)
         self.steps = step
+        if torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
+            self._captured.append((self._plan, grads))
         if stream is not None and grads:
             if stream.cuda_stream != torch.cuda.current_stream(grads[0].device).cuda_stream:
                 for g in grads:  # dropped on the current stream, they stay until this one has read them
