@@ -156,9 +156,18 @@ def _ptr(t):
 
 
 def _stream(device, stream):
+    """The handle of the stream to launch on. The library launches on the
+    current device; a default stream's handle is 0 on each, so tensors of
+    another device would be given to the wrong one's kernels."""
+    current = torch.cuda.current_device()
+    index = current if device.index is None else device.index
+    if index != current:
+        raise ValueError(f"the tensors are on cuda:{index}, the current device is cuda:{current}: "
+                         f"call inside torch.cuda.device({index})")
     if stream is None:  # the handle alone: building a Stream object costs 2 us a call
-        index = device.index
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index))
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(index))
+    if stream.device_index != index:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
     return ctypes.c_void_p(stream.cuda_stream)
 
 

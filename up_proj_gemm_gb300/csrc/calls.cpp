@@ -4,12 +4,13 @@
 // (a rotation of one token 15 us, here 4).
 //
 // Every function takes the usual call only: arguments of the documented types
-// and shapes, outputs to allocate, the current stream, no status word. For
-// anything else, and whenever the library refuses, it returns None, and the
-// Python face handles the call (or names what is wrong with it).
+// and shapes on the current device, outputs to allocate, the current stream, no
+// status word. For anything else, and whenever the library refuses, it returns
+// None, and the Python face handles the call (or names what is wrong with it).
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
 #include <torch/csrc/Exceptions.h>
@@ -54,6 +55,9 @@ bool dense(const at::Tensor* t, at::ScalarType type, int64_t dim, const at::Tens
 }
 bool shaped(const at::Tensor& t, int64_t rows, int64_t cols) { return t.size(0) == rows && t.size(1) == cols; }
 
+// The library launches on the current device.
+bool here(const at::Tensor& t) { return t.device().index() == c10::cuda::current_device(); }
+
 void* stream_of(const at::Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }
 
 // The tables, positions and axes of a rotary call.
@@ -71,7 +75,7 @@ PyObject* rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t Dr = PyLong_AsLongLong(a[5]);
     const int mode = (int)PyLong_AsLong(a[6]);
     if (PyErr_Occurred()) return nullptr;
-    if (!x || !x->is_cuda() || x->dim() != 3 || !rotary_args(cos, sin, pos, a[4], Dr, x)) Py_RETURN_NONE;
+    if (!x || !x->is_cuda() || !here(*x) || x->dim() != 3 || !rotary_args(cos, sin, pos, a[4], Dr, x)) Py_RETURN_NONE;
     const bool bf = x->scalar_type() == at::kBFloat16;
     const int64_t T = x->size(0), H = x->size(1), D = x->size(2), Ho = mode == MLA_ROPE_INVERSE_SUM ? 1 : H;
     if ((!bf && x->scalar_type() != at::kFloat) || (D > 1 && x->stride(2) != 1) || Dr > D || pos->size(1) != T ||
@@ -106,7 +110,8 @@ PyObject* rope_axes_table(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor *cos = tensor(a[0]), *sin = tensor(a[1]), *pos = tensor(a[2]);
     const int64_t Dr = PyLong_AsLongLong(a[4]);
     if (PyErr_Occurred()) return nullptr;
-    if (!rotary_args(cos, sin, pos, a[3], Dr, nullptr) || Dr > INT32_MAX || pos->size(0) > INT32_MAX) Py_RETURN_NONE;
+    if (!rotary_args(cos, sin, pos, a[3], Dr, nullptr) || !here(*cos) || Dr > INT32_MAX || pos->size(0) > INT32_MAX)
+        Py_RETURN_NONE;
     const int64_t T = pos->size(1);
     at::Tensor c = at::empty({T, Dr}, cos->options()), s = at::empty({T, Dr}, cos->options());
     const mla_rope_axes_shape shape{T, 1, 0, (int32_t)Dr, (int32_t)pos->size(0), cos->size(0), cos->size(1), 0, 0, 0, 0, 0};
@@ -137,7 +142,7 @@ PyObject* ffn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor *x = tensor(a[0]), *wgu = tensor(a[1]), *wd = tensor(a[2]);
     const int act = (int)PyLong_AsLong(a[3]), save = PyObject_IsTrue(a[4]);
     if (PyErr_Occurred()) return nullptr;
-    if (!x || !x->is_cuda() || x->dim() != 2 || !dense(wd, at::kBFloat16, 2, x) || !dense(wgu, at::kBFloat16, 2, x))
+    if (!x || !x->is_cuda() || !here(*x) || x->dim() != 2 || !dense(wd, at::kBFloat16, 2, x) || !dense(wgu, at::kBFloat16, 2, x))
         Py_RETURN_NONE;
     const int64_t T = x->size(0), K = x->size(1), F = wd->size(1), ld = row_pitch(x, T, K);
     if (ld < 0 || wd->size(0) != K || !shaped(*wgu, 2 * F, K)) Py_RETURN_NONE;
@@ -166,7 +171,7 @@ PyObject* ffn_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      *h = tensor(a[5]);
     const int act = (int)PyLong_AsLong(a[6]);
     if (PyErr_Occurred()) return nullptr;
-    if (!dense(dy, at::kBFloat16, 2, nullptr) || !x || x->device() != dy->device() || !dense(wgu, at::kBFloat16, 2, dy) ||
+    if (!dense(dy, at::kBFloat16, 2, nullptr) || !here(*dy) || !x || x->device() != dy->device() || !dense(wgu, at::kBFloat16, 2, dy) ||
         !dense(wd, at::kBFloat16, 2, dy) || !dense(gu, at::kBFloat16, 2, dy) || !dense(h, at::kBFloat16, 2, dy))
         Py_RETURN_NONE;
     const int64_t T = dy->size(0), K = dy->size(1), F = wd->size(1), ld = row_pitch(x, T, K);
@@ -216,7 +221,7 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
         q.seed = (uint32_t)PyLong_AsUnsignedLongMask(a[11]);
     }
     if (PyErr_Occurred()) return nullptr;
-    if (index < 0) Py_RETURN_NONE;
+    if (index < 0 || index != c10::cuda::current_device()) Py_RETURN_NONE;
     void* stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream();
     if (reinterpret_cast<uintptr_t>(stream) != on) Py_RETURN_NONE;
     if (adamw_step_fn(reinterpret_cast<const void*>(host), reinterpret_cast<const void*>(dev), &q, scale, stream) != MLA_OK)
