@@ -10,6 +10,7 @@ sections.
 from __future__ import annotations
 
 import ctypes
+import operator
 
 import torch
 
@@ -41,24 +42,33 @@ def rope_sections(sections) -> bytes:
     return bytes(a for a, n in enumerate(sections) for _ in range(n))
 
 
+def _axes(axes, Dr):
+    """The pairs' axes as one byte each: from bytes, or a sequence of Dr/2 integers (an integer alone or an array's
+    memory would be other bytes)."""
+    if type(axes) is not bytes:
+        axes = bytes(axes if type(axes) in (list, tuple) else [operator.index(a) for a in axes])
+    if len(axes) != Dr // 2:
+        raise ValueError(f"axes must name the axis of each of the {Dr // 2} pairs, got {len(axes)}")
+    return axes
+
+
 _bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _refuse_tables(cos, sin, pos, axes, Dr, T, dev):
-    """Name what is wrong with the tables, the positions [A, T] or the Dr/2 pairs' axes."""
+def _refuse_tables(cos, sin, pos, T, dev):
+    """Name what is wrong with the tables or the positions [A, T]."""
     _need(cos, "cos", _f32, dev, ndim=2)
     _need(sin, "sin", _f32, dev, shape=cos.shape)
     _need(pos, "pos", _i32, dev, ndim=2)
     if pos.shape[1] != T:
         raise ValueError(f"pos must be [axes, {T}], got {list(pos.shape)}")
-    raise ValueError(f"axes must name the axis of each of the {Dr // 2} pairs, got {len(axes)}")
 
 
-def _tables_ok(cos, sin, pos, axes, Dr, T, dev):
+def _tables_ok(cos, sin, pos, T, dev):
     """The checks of _refuse_tables in one expression: a call's checks cost as much as its launch."""
     return (isinstance(cos, torch.Tensor) and isinstance(sin, torch.Tensor) and isinstance(pos, torch.Tensor)
             and cos.dtype is _f32 and sin.dtype is _f32 and pos.dtype is _i32 and cos.dim() == 2
-            and sin.shape == cos.shape and pos.dim() == 2 and pos.shape[1] == T and len(axes) == Dr // 2
+            and sin.shape == cos.shape and pos.dim() == 2 and pos.shape[1] == T
             and cos.is_cuda and sin.is_cuda and pos.is_cuda
             and cos.device == dev and sin.device == dev and pos.device == dev
             and cos.is_contiguous() and sin.is_contiguous() and pos.is_contiguous())
@@ -81,13 +91,15 @@ def rope_axes(x, cos, sin, pos, axes, Dr, inverse=False, sum_heads=False, out=No
     channels) with the last Dr channels of every head rotated; the others are
     copied.
 
-    pos: int32 [A, T]; axes: the axis of each of the Dr/2 pairs. ``inverse``
-    applies the Jacobian transpose (the gradient), ``sum_heads`` (with
-    inverse) the transpose of the heads' sum, [T, 1, D]: the gradient of a key
-    part that all heads share. ``out`` may be a strided view."""
+    pos: int32 [A, T]; axes: the axis of each of the Dr/2 pairs, as bytes or a
+    sequence of integers. ``inverse`` applies the Jacobian transpose (the
+    gradient), ``sum_heads`` (with inverse) the transpose of the heads' sum,
+    [T, 1, D]: the gradient of a key part that all heads share. ``out`` may be
+    a strided view."""
+    axes = _axes(axes, Dr)
     c = _pkg._calls
     if c is not None and out is None and status is None and stream is None and (inverse or not sum_heads):
-        out = c.rope_axes(x, cos, sin, pos, bytes(axes), Dr, (2 if sum_heads else 1) if inverse else 0)
+        out = c.rope_axes(x, cos, sin, pos, axes, Dr, (2 if sum_heads else 1) if inverse else 0)
         if out is not None:
             return out
     if not (isinstance(x, torch.Tensor) and (x.dtype is _bf16 or x.dtype is _f32) and x.is_cuda and x.dim() == 3
@@ -96,8 +108,8 @@ def rope_axes(x, cos, sin, pos, axes, Dr, inverse=False, sum_heads=False, out=No
     T, H, D = x.shape
     in_t, in_h, _ = x.stride()
     dev = x.device
-    if not _tables_ok(cos, sin, pos, axes, Dr, T, dev):
-        _refuse_tables(cos, sin, pos, axes, Dr, T, dev)
+    if not _tables_ok(cos, sin, pos, T, dev):
+        _refuse_tables(cos, sin, pos, T, dev)
     if status is not None:
         _status(status, dev)
     Ho = 1 if sum_heads else H
@@ -117,7 +129,7 @@ def rope_axes(x, cos, sin, pos, axes, Dr, inverse=False, sum_heads=False, out=No
                       out_t if T > 1 else 0, out_h if Ho > 1 else 0, 0)
     _call(lib().mla_rope_axes, "mla_rope_axes", ctypes.byref(s), 0 if x.dtype is _f32 else 1,
           (2 if sum_heads else 1) if inverse else 0, x.data_ptr(), cos.data_ptr(), sin.data_ptr(), pos.data_ptr(),
-          bytes(axes), out.data_ptr(), _ptr(status), _stream(dev, stream))
+          axes, out.data_ptr(), _ptr(status), _stream(dev, stream))
     return out
 
 
@@ -125,17 +137,18 @@ def rope_axes_table(cos, sin, pos, axes, Dr, cos_out=None, sin_out=None, status=
     """(cos, sin) float32 [T, Dr] of every token for positions with several
     axes: the tables to give fwd, bwd_dgrad, bwd_wgrad, bwd_mxfp8 and kv_fwd
     (with pos=None), which then rotate by several axes."""
+    axes = _axes(axes, Dr)
     c = _pkg._calls
     if c is not None and cos_out is None and sin_out is None and status is None and stream is None:
-        r = c.rope_axes_table(cos, sin, pos, bytes(axes), Dr)
+        r = c.rope_axes_table(cos, sin, pos, axes, Dr)
         if r is not None:
             return r
     if not isinstance(pos, torch.Tensor) or pos.dim() != 2:
         raise ValueError("pos must be an int32 tensor [A, T]")
     dev = pos.device
     A, T = pos.shape
-    if not _tables_ok(cos, sin, pos, axes, Dr, T, dev):
-        _refuse_tables(cos, sin, pos, axes, Dr, T, dev)
+    if not _tables_ok(cos, sin, pos, T, dev):
+        _refuse_tables(cos, sin, pos, T, dev)
     if status is not None:
         _status(status, dev)
     if cos_out is None:
@@ -149,5 +162,5 @@ def rope_axes_table(cos, sin, pos, axes, Dr, cos_out=None, sin_out=None, status=
     rows, width = cos.shape
     s = RopeAxesShape(T, 1, 0, Dr, A, rows, width, 0, 0, 0, 0, 0)
     _call(lib().mla_rope_axes_table, "mla_rope_axes_table", ctypes.byref(s), cos.data_ptr(), sin.data_ptr(),
-          pos.data_ptr(), bytes(axes), cos_out.data_ptr(), sin_out.data_ptr(), _ptr(status), _stream(dev, stream))
+          pos.data_ptr(), axes, cos_out.data_ptr(), sin_out.data_ptr(), _ptr(status), _stream(dev, stream))
     return cos_out, sin_out
