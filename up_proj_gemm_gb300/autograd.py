@@ -40,6 +40,7 @@ import torch
 from . import bwd_dgrad, bwd_wgrad, fwd
 from . import gated_ffn_bwd, gated_ffn_fwd
 from . import rope_axes as _rope_axes
+from .rotary import _axes
 
 __all__ = ["QUpProj", "q_up_proj", "Mxfp8Query", "q_up_proj_mxfp8", "RopeAxes", "rope_axes", "GatedFfn",
            "gated_ffn"]
@@ -168,7 +169,8 @@ def rope_axes(x, cos, sin, pos, axes, Dr, heads=None):
     many heads share; the result is [T, heads, D]."""
     if heads is not None and x.shape[1] != 1:
         raise ValueError(f"a shared head is [T, 1, D], got {list(x.shape)}")
-    return RopeAxes.apply(x, cos, sin, pos, axes, Dr, heads)
+    # as bytes: a list that changes until the backward would turn the gradient otherwise
+    return RopeAxes.apply(x, cos, sin, pos, _axes(axes, Dr), Dr, heads)
 
 
 class GatedFfn(torch.autograd.Function):
