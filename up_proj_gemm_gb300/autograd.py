@@ -194,4 +194,6 @@ class GatedFfn(torch.autograd.Function):
 def gated_ffn(x, w_gate_up, w_down, act="silu"):
     """(act(g) * u) w_down^T with [g | u] = x w_gate_up^T as bf16 [T, K],
     differentiable in x, w_gate_up and w_down."""
+    if not torch.is_grad_enabled():  # nothing to keep for a backward; a Function sees the inputs' flags only
+        return gated_ffn_fwd(x, w_gate_up, w_down, act=act)
     return GatedFfn.apply(x, w_gate_up, w_down, act)
