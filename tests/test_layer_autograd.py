@@ -43,3 +43,33 @@ def test_nothing_is_saved_without_a_gradient(ffn):
     assert ffn == [("fwd", False)] * 3
     assert autograd.gated_ffn(x.detach(), wgu.detach(), wd).requires_grad  # one gradient is enough
     assert ffn[3:] == [("fwd", True)]
+
+
+def test_a_gradient_off_the_16_byte_grid(ffn):
+    """The gradient of one part of a concatenation is a slice: contiguous, but anywhere. It reaches the call aligned."""
+    x, wgu, wd = tensors()
+    y = autograd.gated_ffn(x, wgu, wd)
+    out = torch.cat([torch.zeros(3, dtype=bf16), y.flatten()])
+    g = torch.arange(out.numel()).to(bf16)
+    out.backward(g)
+    what, aligned, dy = ffn[-1]
+    assert what == "bwd" and aligned and torch.equal(dy.flatten(), g[3:])
+
+
+def test_a_query_gradient_off_the_16_byte_grid(monkeypatch):
+    """The same for the projection's query."""
+    seen = []
+
+    def dgrad(dq, W, *a, **kw):
+        seen.append(dq.is_contiguous() and dq.data_ptr() % 16 == 0)
+        return torch.ones((3, K), dtype=bf16)
+
+    monkeypatch.setattr(autograd, "fwd", lambda x, W, *a, **kw: torch.ones((3, 2, 4), dtype=bf16))
+    monkeypatch.setattr(autograd, "bwd_dgrad", dgrad)
+    monkeypatch.setattr(autograd, "bwd_wgrad", lambda dq, *a, **kw: (seen.append(dq.data_ptr() % 16 == 0) or
+                                                                     torch.ones((8, K), dtype=bf16), None))
+    x, W = torch.ones((3, K), dtype=bf16, requires_grad=True), torch.ones((8, K), dtype=bf16, requires_grad=True)
+    q = autograd.q_up_proj(x, W, torch.ones(3, 4), torch.ones(3, 4), 2, 0, 4)
+    out = torch.cat([torch.zeros(1, dtype=bf16), q.flatten()])
+    out.backward(torch.ones_like(out))
+    assert seen == [True, True]

@@ -46,13 +46,20 @@ __all__ = ["QUpProj", "q_up_proj", "Mxfp8Query", "q_up_proj_mxfp8", "RopeAxes", 
            "gated_ffn"]
 
 
+def _dense(g):
+    """An upstream gradient as the kernels take it: contiguous, on 16 bytes. (A part of a concatenation's gradient is a
+    slice that may start anywhere.)"""
+    g = g.contiguous()
+    return g.clone() if g.data_ptr() % 16 else g
+
+
 def _layer_backward(ctx, dq):
     """dx, dW, db of the layer for the upstream gradient dq [T, H, D] bf16,
     only those autograd asks for."""
     x, W, cos, sin, pos = ctx.saved_tensors
     H, Dn, Dr = ctx.shape
     need_x, need_w, need_b = ctx.needs_input_grad[0], ctx.needs_input_grad[1], ctx.needs_input_grad[2]
-    dq = dq.contiguous()
+    dq = _dense(dq)
     dx = dW = db = None
     rope = None
     if need_x:
@@ -187,7 +194,7 @@ class GatedFfn(torch.autograd.Function):
     def backward(ctx, dy):
         x, w_gate_up, w_down, gate_up, h = ctx.saved_tensors
         need = ctx.needs_input_grad
-        return (*gated_ffn_bwd(dy.contiguous(), x, w_gate_up, w_down, gate_up, h, act=ctx.act, dx=need[0],
+        return (*gated_ffn_bwd(_dense(dy), x, w_gate_up, w_down, gate_up, h, act=ctx.act, dx=need[0],
                                dw_gate_up=need[1], dw_down=need[2]), None)
 
 
