@@ -73,3 +73,30 @@ def test_a_query_gradient_off_the_16_byte_grid(monkeypatch):
     out = torch.cat([torch.zeros(1, dtype=bf16), q.flatten()])
     out.backward(torch.ones_like(out))
     assert seen == [True, True]
+
+
+def test_second_derivatives_are_refused(ffn, monkeypatch):
+    """The backward is not differentiable itself: a penalty on a gradient raises instead of counting for nothing."""
+    monkeypatch.setattr(autograd, "_rope_axes", lambda x, *a, **kw: x * 1.0)
+    monkeypatch.setattr(autograd, "fwd", lambda x, W, *a, **kw: torch.ones((3, 2, 4), dtype=bf16))
+    monkeypatch.setattr(autograd, "bwd_dgrad", lambda dq, W, *a, **kw: torch.ones((3, K), dtype=bf16))
+    monkeypatch.setattr(autograd, "bwd_wgrad", lambda dq, *a, **kw: (torch.ones((8, K), dtype=bf16), None))
+    t = torch.ones(3, 4)
+
+    def rope():
+        x = torch.ones(3, 2, 4, requires_grad=True)
+        return x, autograd.rope_axes(x, t, t, torch.zeros(1, 3, dtype=torch.int32), [0, 0], 4)
+
+    def block():
+        x, wgu, wd = tensors()
+        return x, autograd.gated_ffn(x, wgu, wd)
+
+    def query():
+        x, W = (torch.ones(s, dtype=bf16, requires_grad=True) for s in ((3, K), (8, K)))
+        return x, autograd.q_up_proj(x, W, t, t, 2, 0, 4)
+
+    for make in (rope, block, query):
+        x, y = make()
+        (g,) = torch.autograd.grad((y.float() ** 2).sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            (y.float().sum() + (g.float() ** 2).sum()).backward()

@@ -36,6 +36,7 @@ from __future__ import annotations
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import bwd_dgrad, bwd_wgrad, fwd
 from . import gated_ffn_bwd, gated_ffn_fwd
@@ -82,6 +83,7 @@ class QUpProj(torch.autograd.Function):
         return q
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq):
         dx, dW, db = _layer_backward(ctx, dq)
         return dx, dW, db, None, None, None, None, None, None
@@ -112,6 +114,7 @@ class _QUpProjMxfp8(torch.autograd.Function):
         return codes, scales, anchor
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_codes, g_scales, g_anchor):
         dq = ctx.box.dq
         if dq is None:
@@ -162,6 +165,7 @@ class RopeAxes(torch.autograd.Function):
         return _rope_axes(x if heads is None else x.expand(-1, heads, -1), cos, sin, pos, axes, Dr)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         cos, sin, pos = ctx.saved_tensors
         if g.shape[2] > 1 and g.stride(2) != 1:
@@ -191,6 +195,7 @@ class GatedFfn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, w_gate_up, w_down, gate_up, h = ctx.saved_tensors
         need = ctx.needs_input_grad
