@@ -648,7 +648,8 @@ MLAQ_API int mla_rope_axes_table(const mla_rope_axes_shape *shape, const float *
  *                   param then only receives its rounded copy
  * The step uses m' and v' before they are rounded to 8 bits; a root above
  * zero never rounds to code 0. A 32-element block that holds a NaN or an
- * infinity keeps scale 0xFF and NaN codes. Pointers need their type's
+ * infinity keeps scale 0xFF and NaN codes. Where v' overflows float32 the
+ * quotient is 0; with 8 bits its root is kept as the largest float32's. Pointers need their type's
  * alignment; tensors that start on 16 bytes (codes: 8) move by wide accesses. */
 typedef struct {
     void *param;

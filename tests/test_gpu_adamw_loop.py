@@ -120,3 +120,19 @@ def test_a_captured_step_outlives_other_gradients(cuda_device):
         graph.replay()
     torch.cuda.synchronize()
     assert ((p.detach().double() - (1 - 0.125 * 3)).abs() <= 100 * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_an_overflowing_second_moment_stops_its_element(cuda_device, bits):
+    """v' is infinite in float32: its root is, the quotient is zero and the parameter stays, as the formula says; the
+    others step on. (The 8-bit root itself is kept as the largest float32's, in a block of its own here.)"""
+    n = 64
+    p = torch.ones(n, device=cuda_device)
+    g = torch.ones(n, device=cuda_device)
+    g[:32] = torch.tensor([1e30, -1e25], device=cuda_device).repeat(16)
+    opt = mlaq.AdamW([p], lr=0.25, betas=(0.9, 0.95), weight_decay=0.0, state_bits=bits)
+    opt.step([g])
+    assert (p[:32] == 1.0).all()
+    assert ((p[32:].double() - 0.75).abs() <= 20 * 2.0 ** -24).all()
+    if bits == 8:
+        assert 255 not in opt.exp_avg_sq_scales[0].tolist()

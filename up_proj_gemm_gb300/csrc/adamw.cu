@@ -21,8 +21,8 @@
 //
 // One pass, every operand read and written once. With float32 moments HBM is
 // the bound: 100 M elements at 6.86 TB/s, a plain copy's rate. With MXFP8 moments
-// an element is 10 bytes and 67 instructions: 5.18 TB/s (300 M elements in
-// 586 us), issue slots 78% taken.
+// an element is 10 bytes and 67 instructions: 5.13 TB/s (300 M elements in
+// 592 us), issue slots 78% taken.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -193,8 +193,9 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
 // Roots of two values >= 0 (or NaN), within an ulp: a reciprocal root y of 2
 // ulp, r = v y, and one Heron correction r + (v - r^2) y / 2, whose residual
 // is exact by fused arithmetic. Values below 2^-126 count as 2^-126 for y
-// (their root then comes out at most as large as it is, and a zero's is 0);
-// an infinite v, of gradients above 10^19, counts as the largest float32.
+// (their root then comes out at most as large as it is, and a zero's is 0); an
+// infinite one, of gradients above 10^19, counts as the largest float32 up to
+// the residual, which then makes the root infinite (and the quotient 0).
 __device__ __forceinline__ f32x2 root2(f32x2 v) {
     float v0, v1, y0, y1;
     unpack2(v, v0, v1);
@@ -204,8 +205,7 @@ __device__ __forceinline__ f32x2 root2(f32x2 v) {
     y1 = max_nan(v1, 1.17549435e-38f);
     asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(y0));
     asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(y1));
-    v = pack2(v0, v1);
-    const f32x2 y = pack2(y0, y1), r = mul2(v, y);
+    const f32x2 y = pack2(y0, y1), r = mul2(pack2(v0, v1), y);
     const f32x2 left = fma2(mul2(r, both(-1.f)), r, v);
     return fma2(left, mul2(y, both(0.5f)), r);
 }
@@ -390,6 +390,8 @@ __device__ __forceinline__ float min3_abs(float a, float b, float c) {
     return r;
 }
 
+constexpr float kLargestRoot = 1.8446743e19f;  // of the largest float32
+
 // 8 of a block's 32 values (the other 24 in three neighbouring lanes); v may
 // be scaled on return.
 template <bool ROOT>
@@ -398,7 +400,7 @@ __device__ __forceinline__ uint32_t encode8(const StepParams& q, float (&v)[8], 
     float am = max3_nan(max3_nan(v[0], v[1], v[2]), max3_nan(v[3], v[4], v[5]), amax_nan(fabsf(v[6]), v[7]));
     am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, 1));
     am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, 2));
-    const uint32_t bits = __float_as_uint(am);
+    uint32_t bits = __float_as_uint(am);
     if (q.stochastic && bits < 0x7F800000u) {
         const int e = e8m0_exponent_f32(am);
         int left = e;  // what the codes still have to be scaled by
@@ -411,6 +413,11 @@ __device__ __forceinline__ uint32_t encode8(const StepParams& q, float (&v)[8], 
         if (lo < __uint_as_float((uint32_t)(left + 121) << 23)) codes_random<ROOT, true>(v, left, mixed, codes);
         else codes_random<ROOT, false>(v, left, mixed, codes);
         return (uint32_t)(e + 127);
+    }
+    if (ROOT && bits == 0x7F800000u) {  // an infinite root is kept as that of the largest float32
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fminf(v[i], kLargestRoot);
+        bits = __float_as_uint(kLargestRoot);
     }
     const uint32_t sf = quantize8_block_scale(v, bits, codes);
     if constexpr (ROOT) {
