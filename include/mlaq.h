@@ -67,7 +67,8 @@ enum {
     MLA_ERR_CUDA = 6,        /* a CUDA runtime/driver call failed (no device, launch error) */
     MLA_ERR_TIMEOUT = 7,     /* device only: a pipeline wait gave up; outputs are unspecified */
     MLA_ERR_POS_RANGE = 8,   /* a position outside [0, cs_rows); device-side for pos arrays */
-    MLA_ERR_WORKSPACE = 9    /* workspace pointer/size smaller than the size query returned */
+    MLA_ERR_WORKSPACE = 9,   /* workspace pointer/size smaller than the size query returned */
+    MLA_ERR_MEMORY = 10      /* host memory for a call's checks could not be allocated */
 };
 
 /* weight_mode */
@@ -674,7 +675,8 @@ typedef struct {
 
 /*
  * A plan lists the tensors of a step. mla_adamw_plan_build checks them
- * (MLA_ERR_ALIAS when a written buffer overlaps any other) and writes the plan
+ * (MLA_ERR_ALIAS when a written buffer overlaps any other; MLA_ERR_MEMORY when
+ * the 168 bytes per tensor that this takes cannot be had) and writes the plan
  * to HOST memory, mla_adamw_plan_bytes(tensors, count) bytes (0: invalid
  * arguments); the caller keeps it and a copy of it in device memory (16-byte
  * aligned) for as long as the buffers stay where they are.

@@ -35,7 +35,7 @@ library_path = os.path.join(_HERE, "libmlaq.so")
 STATUS = {
     "MLA_OK": 0, "MLA_ERR_INVALID_ARG": 1, "MLA_ERR_ROPE_WIDTH": 2, "MLA_ERR_ALIGNMENT": 3,
     "MLA_ERR_ALIAS": 4, "MLA_ERR_UNSUPPORTED": 5, "MLA_ERR_CUDA": 6, "MLA_ERR_TIMEOUT": 7,
-    "MLA_ERR_POS_RANGE": 8, "MLA_ERR_WORKSPACE": 9,
+    "MLA_ERR_POS_RANGE": 8, "MLA_ERR_WORKSPACE": 9, "MLA_ERR_MEMORY": 10,
 }
 WEIGHT_MODES = {"bf16": 0, "mxfp8": 1, "mxfp8_tiled": 2}
 OUT_MODES = {"bf16": 0, "mxfp8": 1, "mxfp8_bhsd": 2, "mxfp8_bhsd_swizzled": 3}

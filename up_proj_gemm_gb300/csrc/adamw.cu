@@ -29,6 +29,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <new>
 #include <vector>
 
 #include "checks.h"
@@ -654,6 +655,32 @@ bool spans_alias(std::vector<Span>& spans) {
     return false;
 }
 
+// The same for a plan's tensors, ps, gs and ss bytes for each element of a
+// parameter, a gradient and a moment. No exception leaves it.
+int written_overlap(const mla_adamw_tensor* tensors, int64_t count, int64_t ps, int64_t gs, int64_t ss) {
+    try {
+        std::vector<Span> spans;
+        spans.reserve((size_t)count * 7);
+        auto add = [&spans](const void* p, int64_t bytes, bool out) {
+            const Range r = rng(p, bytes);
+            if (r.lo != r.hi) spans.push_back({r.lo, r.hi, out});
+        };
+        for (int64_t i = 0; i < count; ++i) {
+            const mla_adamw_tensor& t = tensors[i];
+            add(t.grad, t.n * gs, false);
+            add(t.param, t.n * ps, true);
+            add(t.exp_avg, t.n * ss, true);
+            add(t.exp_avg_sq, t.n * ss, true);
+            add(t.exp_avg_scales, (t.n + 31) / 32, true);
+            add(t.exp_avg_sq_scales, (t.n + 31) / 32, true);
+            add(t.master, t.n * 4, true);
+        }
+        return spans_alias(spans) ? MLA_ERR_ALIAS : MLA_OK;
+    } catch (const std::bad_alloc&) {
+        return MLA_ERR_MEMORY;
+    }
+}
+
 }  // namespace
 }  // namespace mlaq
 
@@ -693,22 +720,8 @@ MLAQ_API int mla_adamw_plan_build(const mla_adamw_tensor* tensors, int64_t count
             !aligned(t.master, 4))
             return MLA_ERR_ALIGNMENT;
     }
-    std::vector<Span> spans;
-    auto add = [&spans](const void* p, int64_t bytes, bool out) {
-        const Range r = rng(p, bytes);
-        if (r.lo != r.hi) spans.push_back({r.lo, r.hi, out});
-    };
-    for (int64_t i = 0; i < count; ++i) {
-        const mla_adamw_tensor& t = tensors[i];
-        add(t.grad, t.n * gs, false);
-        add(t.param, t.n * ps, true);
-        add(t.exp_avg, t.n * ss, true);
-        add(t.exp_avg_sq, t.n * ss, true);
-        add(t.exp_avg_scales, (t.n + 31) / 32, true);
-        add(t.exp_avg_sq_scales, (t.n + 31) / 32, true);
-        add(t.master, t.n * 4, true);
-    }
-    if (spans_alias(spans)) return MLA_ERR_ALIAS;
+    const int alias = written_overlap(tensors, count, ps, gs, ss);
+    if (alias != MLA_OK) return alias;
 
     PlanHeader h{};
     h.magic = kMagic;

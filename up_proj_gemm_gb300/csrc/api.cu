@@ -172,6 +172,7 @@ MLAQ_API const char* mla_status_string(int status) {
         case MLA_ERR_TIMEOUT: return "MLA_ERR_TIMEOUT";
         case MLA_ERR_POS_RANGE: return "MLA_ERR_POS_RANGE";
         case MLA_ERR_WORKSPACE: return "MLA_ERR_WORKSPACE";
+        case MLA_ERR_MEMORY: return "MLA_ERR_MEMORY";
         default: return "MLA_ERR_UNKNOWN";
     }
 }
