@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) adamw_f32_kernel(const StepParams q)
     grid_wait_previous();
     const PlanChunk c = q.chunks[blockIdx.x];
     const PlanTensor T = q.tensors[c.tensor];
-    const float gs = q.grad_scale ? __ldg(q.grad_scale) : 1.f;
+    const float gs = q.grad_scale ? *q.grad_scale : 1.f;
     const int64_t base = (int64_t)c.number * q.chunk;
     const int64_t left = T.t.n - base;
     const int n = left < q.chunk ? (int)left : q.chunk;
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_mx_kernel(const StepParams 
     grid_wait_previous();
     const PlanChunk c = q.chunks[blockIdx.x];
     const PlanTensor& T = q.tensors[c.tensor];
-    const float gs = q.grad_scale ? __ldg(q.grad_scale) : 1.f;
+    const float gs = q.grad_scale ? *q.grad_scale : 1.f;
     const int64_t base = (int64_t)c.number * q.chunk;
     const int64_t left = T.t.n - base;
     const int n = left < q.chunk ? (int)left : q.chunk;

@@ -828,7 +828,7 @@ __device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 __device__ __forceinline__ void load4(const uint16_t* p, float (&v)[4]) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
     v[0] = bf16lo_to_f32(w.x);
     v[1] = bf16hi_to_f32(w.x);
     v[2] = bf16lo_to_f32(w.y);

@@ -6,6 +6,9 @@
 // that reads something before its wait (a later product of a feed-forward
 // call, its weights) relies on the grid before it to have waited first; one that
 // needs nothing of the grid before it may wait at its end instead.
+// Such a kernel runs while the grid before it still writes, so it reads by plain
+// loads: __ldg and restricted pointers are for memory that nobody writes while
+// the kernel runs, and a compiler may move them above the wait.
 #pragma once
 #include <cuda_runtime.h>
 

@@ -58,10 +58,10 @@ struct Raw {
 
     __device__ __forceinline__ void load(const E* p) {
         if constexpr (VE == 1) {
-            if constexpr (sizeof(E) == 2) u[0] = __ldg(p);
-            else u[0] = __float_as_uint(__ldg(p));
+            if constexpr (sizeof(E) == 2) u[0] = *p;
+            else u[0] = __float_as_uint(*p);
         } else {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+            const uint4 w = *reinterpret_cast<const uint4*>(p);
             u[0] = w.x;
             u[1] = w.y;
             u[2] = w.z;
@@ -96,7 +96,7 @@ struct Raw {
 // The position of token t on the axis of rope channel j (j < Dr).
 __device__ __forceinline__ int64_t position(const RopeParams& p, int j, int64_t t) {
     const int half = p.Dr / 2;
-    return __ldg(p.pos + p.axis[j < half ? j : j - half] * p.T + t);
+    return p.pos[p.axis[j < half ? j : j - half] * p.T + t];
 }
 __device__ __forceinline__ bool in_table(const RopeParams& p, int64_t row) { return row >= 0 && row < p.cs_rows; }
 
@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) rope_axes_kernel(const _
                     for (int q = 0; q < kFill; ++q) {
                         const int i = i0f + q * kThreads, j = i % p.Dr;
                         const bool ok = i < n && in_table(p, row[q]);
-                        cv[q] = ok ? __ldg(p.cos_tab + row[q] * p.cs_width + j) : 0.f;
-                        sv[q] = ok ? __ldg(p.sin_tab + row[q] * p.cs_width + j) : 0.f;
+                        cv[q] = ok ? p.cos_tab[row[q] * p.cs_width + j] : 0.f;
+                        sv[q] = ok ? p.sin_tab[row[q] * p.cs_width + j] : 0.f;
                     }
 #pragma unroll
                     for (int q = 0; q < kFill; ++q) {
@@ -268,17 +268,19 @@ __global__ void __launch_bounds__(kThreads) rope_few_kernel(const __grid_constan
 #pragma unroll
         for (int k = 0; k < VE; ++k) row[k] = position(p, i0 + k, t);
         float v[VE], w[VE];
+        bool ok = true;  // reported behind the loads: none of them may pass the report
 #pragma unroll
         for (int k = 0; k < VE; ++k) {
-            const bool ok = in_table(p, row[k]);
-            if (!ok) record_status(p.status, MLA_ERR_POS_RANGE);
-            const int64_t at = (ok ? row[k] : 0) * p.cs_width + i0 + k;
-            const float c0 = __ldg(p.cos_tab + at), c1 = __ldg(p.cos_tab + at + half);
-            const float s0 = __ldg(p.sin_tab + at), s1 = __ldg(p.sin_tab + at + half);
+            const bool in = in_table(p, row[k]);
+            ok &= in;
+            const int64_t at = (in ? row[k] : 0) * p.cs_width + i0 + k;
+            const float c0 = p.cos_tab[at], c1 = p.cos_tab[at + half];
+            const float s0 = p.sin_tab[at], s1 = p.sin_tab[at + half];
             const float u = a.get(k), y = b.get(k);
             v[k] = p.inverse ? u * c0 + y * s1 : u * c0 - y * s0;
             w[k] = p.inverse ? y * c1 - u * s0 : y * c1 + u * s1;
         }
+        if (!ok) record_status(p.status, MLA_ERR_POS_RANGE);
         a.set(v);
         b.set(w);
     }
@@ -365,10 +367,10 @@ __global__ void __launch_bounds__(kSumThreads, 10) rope_sum_kernel(const __grid_
                 const bool in = in_table(p, row[k]);
                 ok &= in;
                 const int64_t at = (in ? row[k] : 0) * p.cs_width + i0 + k;
-                c0[k] = __ldg(p.cos_tab + at);
-                c1[k] = __ldg(p.cos_tab + at + half);
-                n0[k] = __ldg(p.sin_tab + at);
-                n1[k] = __ldg(p.sin_tab + at + half);
+                c0[k] = p.cos_tab[at];
+                c1[k] = p.cos_tab[at + half];
+                n0[k] = p.sin_tab[at];
+                n1[k] = p.sin_tab[at + half];
             }
             if (!ok) record_status(p.status, MLA_ERR_POS_RANGE);
 #pragma unroll
@@ -396,8 +398,7 @@ __global__ void __launch_bounds__(kSumThreads, 10) rope_sum_kernel(const __grid_
 // 6.0, 5.3, 6.6. T = 100: 2.9; 2.1, 2.7, 3.6. T = 131072, Dr = 128: 99; 109, 64, 51.)
 template <int N, int U>
 __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_constant__ RopeParams p,
-                                                              float* __restrict__ cos_out,
-                                                              float* __restrict__ sin_out) {
+                                                              float* cos_out, float* sin_out) {
     grid_launch_next();
     grid_wait_previous();
     const int half = p.Dr / 2;
@@ -425,19 +426,18 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_const
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             ok[u][k] = in_table(p, at[u][k]);
-            if (!ok[u][k]) record_status(p.status, MLA_ERR_POS_RANGE);
             at[u][k] = (ok[u][k] ? at[u][k] : 0) * p.cs_width + c;
         }
         if (N == 4 && same) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(p.cos_tab + at[u][0]));
-            const float4 b = __ldg(reinterpret_cast<const float4*>(p.sin_tab + at[u][0]));
+            const float4 a = *reinterpret_cast<const float4*>(p.cos_tab + at[u][0]);
+            const float4 b = *reinterpret_cast<const float4*>(p.sin_tab + at[u][0]);
             cv[u][0] = a.x, cv[u][1 % N] = a.y, cv[u][2 % N] = a.z, cv[u][3 % N] = a.w;
             sv[u][0] = b.x, sv[u][1 % N] = b.y, sv[u][2 % N] = b.z, sv[u][3 % N] = b.w;
         } else {
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                cv[u][k] = __ldg(p.cos_tab + at[u][k] + k);
-                sv[u][k] = __ldg(p.sin_tab + at[u][k] + k);
+                cv[u][k] = p.cos_tab[at[u][k] + k];
+                sv[u][k] = p.sin_tab[at[u][k] + k];
             }
         }
     }
@@ -447,7 +447,10 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_const
         if (t >= p.T) break;
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            if (!ok[u][k]) cv[u][k] = sv[u][k] = 0.f;
+            if (!ok[u][k]) {  // reported behind the loads: none of them may pass the report
+                record_status(p.status, MLA_ERR_POS_RANGE);
+                cv[u][k] = sv[u][k] = 0.f;
+            }
         float* co = cos_out + t * p.Dr + c;
         float* so = sin_out + t * p.Dr + c;
         if constexpr (N == 4) {
