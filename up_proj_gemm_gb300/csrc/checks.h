@@ -36,6 +36,12 @@ bool any_alias(const Range (&outs)[NO], const Range (&ins)[NI]) {
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether n rows `stride` elements apart stay below 2^58 elements, so that a
+// sum of two such spans is a number of bytes in int64.
+inline bool inside(int64_t n, int64_t stride) {
+    return stride >= 0 && (n <= 1 || stride <= ((int64_t)1 << 58) / (n - 1));
+}
+
 constexpr int64_t kI32Max = 0x7fffffffLL;
 
 }  // namespace mlaq

@@ -1264,7 +1264,8 @@ int check_ffn(const mla_ffn_shape* s) {
     if (s->T < 0 || s->K <= 0 || s->F <= 0 || s->ld_x < 0 || s->reserved != 0) return MLA_ERR_INVALID_ARG;
     if (s->act < MLA_ACT_SILU || s->act > MLA_ACT_GELU_TANH) return MLA_ERR_INVALID_ARG;
     if (s->T > kI32Max - 512 || s->K > kI32Max / 2 - 512 || s->F > kI32Max / 2 - 512) return MLA_ERR_INVALID_ARG;
-    if (s->ld_x != 0 && (s->ld_x < s->K || s->ld_x > ((int64_t)1 << 36))) return MLA_ERR_INVALID_ARG;
+    if (s->ld_x != 0 && (s->ld_x < s->K || s->ld_x > ((int64_t)1 << 36) || !inside(s->T, s->ld_x)))
+        return MLA_ERR_INVALID_ARG;
     if (s->K % 8 || s->F % 8 || s->ld_x % 8) return MLA_ERR_ALIGNMENT;
     return MLA_OK;
 }

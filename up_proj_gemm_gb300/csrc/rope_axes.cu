@@ -551,10 +551,9 @@ MLAQ_API int mla_rope_axes(const mla_rope_axes_shape* shape, int dtype, int mode
         return MLA_ERR_INVALID_ARG;
     if (s.T > 0 && (!in || !out)) return MLA_ERR_INVALID_ARG;
     const int64_t D = (int64_t)s.Dn + s.Dr;
-    const int64_t lim = (int64_t)1 << 40;  // keeps every extent inside int64
-    for (int64_t v : {s.in_t, s.in_h, s.out_t, s.out_h})
-        if (v < 0 || v > lim) return MLA_ERR_INVALID_ARG;
     const int64_t Ho = sum ? 1 : s.H;
+    if (!inside(s.T, s.in_t) || !inside(s.H, s.in_h) || !inside(s.T, s.out_t) || !inside(Ho, s.out_h))
+        return MLA_ERR_INVALID_ARG;
     // no two output rows share an element: heads inside a token, or tokens inside a head
     const bool heads_in = (Ho == 1 || s.out_h >= D) && (s.T <= 1 || s.out_t >= (Ho - 1) * s.out_h + D);
     const bool tokens_in = (s.T <= 1 || s.out_t >= D) && (Ho == 1 || s.out_h >= (s.T - 1) * s.out_t + D);
