@@ -44,7 +44,6 @@ struct RopeParams {
     const float* cos_tab;
     const float* sin_tab;
     int64_t cs_rows, cs_width;
-    int cs_vec;                   // tables read by float4
     const int32_t* pos;           // [axes][T]
     int* status;
     int rows_per_block;
@@ -580,7 +579,6 @@ MLAQ_API int mla_rope_axes(const mla_rope_axes_shape* shape, int dtype, int mode
     // 16-byte accesses: every row and both halves of every pair start on 16 bytes
     const bool vec = aligned(in, 16) && aligned(out, 16) && s.in_t % ve == 0 && s.in_h % ve == 0 &&
                      s.out_t % ve == 0 && s.out_h % ve == 0 && s.Dn % ve == 0 && s.Dr / 2 % ve == 0;
-    p.cs_vec = aligned(cos_tab, 16) && aligned(sin_tab, 16) && s.cs_width % 4 == 0 && s.Dr / 2 % 4 == 0;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (dtype == MLA_IN_F32)
         return vec ? launch_rows<float, 4>(p, sum, di.num_sms, cs) : launch_rows<float, 1>(p, sum, di.num_sms, cs);
@@ -604,18 +602,19 @@ MLAQ_API int mla_rope_axes_table(const mla_rope_axes_shape* shape, const float* 
     DeviceInfo di;
     const int ds = current_device_info(&di);
     if (ds != MLA_OK) return ds;
-    p.cs_vec = aligned(cos_tab, 16) && aligned(sin_tab, 16) && s.cs_width % 4 == 0 && s.Dr / 2 % 4 == 0;
-    const int cols = p.cs_vec ? s.Dr / 4 : s.Dr;
+    // tables read and written by float4
+    const bool cs_vec = aligned(cos_tab, 16) && aligned(sin_tab, 16) && s.cs_width % 4 == 0 && s.Dr / 2 % 4 == 0;
+    const int cols = cs_vec ? s.Dr / 4 : s.Dr;
     // tokens of a thread: one while that leaves SMs room, four once they come in several waves (see the kernel)
     const int64_t threads = s.T * cols;
     const int u = threads <= (int64_t)di.num_sms * 512 ? 1 : threads <= (int64_t)di.num_sms * 8192 ? 2 : 4;
     const int64_t run = (int64_t)(kThreads / cols) * u;
-    const auto kernel = p.cs_vec ? (u == 1   ? rope_table_kernel<4, 1>
-                                    : u == 2 ? rope_table_kernel<4, 2>
-                                             : rope_table_kernel<4, 4>)
-                                 : (u == 1   ? rope_table_kernel<1, 1>
-                                    : u == 2 ? rope_table_kernel<1, 2>
-                                             : rope_table_kernel<1, 4>);
+    const auto kernel = cs_vec ? (u == 1   ? rope_table_kernel<4, 1>
+                                  : u == 2 ? rope_table_kernel<4, 2>
+                                           : rope_table_kernel<4, 4>)
+                               : (u == 1   ? rope_table_kernel<1, 1>
+                                  : u == 2 ? rope_table_kernel<1, 2>
+                                           : rope_table_kernel<1, 4>);
     return launch_overlapped(kernel, (unsigned)((s.T + run - 1) / run), kThreads, 0, 0, static_cast<cudaStream_t>(stream),
                              p, cos_out, sin_out);
 }
