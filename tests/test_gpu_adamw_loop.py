@@ -136,3 +136,35 @@ def test_an_overflowing_second_moment_stops_its_element(cuda_device, bits):
     assert ((p[32:].double() - 0.75).abs() <= 20 * 2.0 ** -24).all()
     if bits == 8:
         assert 255 not in opt.exp_avg_sq_scales[0].tolist()
+
+
+@pytest.mark.parametrize("compiled", [True, False])
+def test_gradients_of_another_stream(cuda_device, monkeypatch, compiled):
+    """Steps on a busy side stream, by its context or by name, with gradients of the main stream that are dropped right
+    away: what the main stream allocates and fills then is not what the steps read."""
+    mlaq.lib()
+    if not compiled:
+        monkeypatch.setattr(mlaq, "_calls", None)
+    elif mlaq._calls is None:
+        pytest.skip("calls.cpp was not built here")
+    n = 1 << 20
+    p = torch.nn.Parameter(torch.ones(n, device=cuda_device))
+    opt = mlaq.AdamW([p], lr=0.125, betas=(0.0, 0.0), weight_decay=0.0)  # a step is lr times the gradient's sign
+    side, main = torch.cuda.Stream(cuda_device), torch.cuda.current_stream(cuda_device)
+    busy = torch.randn((2048, 2048), device=cuda_device)
+    for i in range(4):
+        p.grad = torch.ones_like(p)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                busy = busy @ busy
+                busy = busy / busy.norm()
+            if i % 2:
+                opt.step()
+        if i % 2 == 0:
+            opt.step(stream=side)
+        p.grad = None
+        fill = [torch.full((n,), -1.0, device=cuda_device) for _ in range(4)]
+        main.wait_stream(side)
+        assert ((p.detach().double() - (1 - 0.125 * (i + 1))).abs() <= 40 * (i + 1) * 2.0 ** -24).all()
+        del fill

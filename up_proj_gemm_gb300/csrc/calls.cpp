@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
@@ -255,6 +256,21 @@ PyObject* adamw_places(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// adamw_keep(list of gradients): their memory stays until the current stream has read them, whichever stream they are
+// of (nothing to do where it is this one). True, or None when something else is listed.
+PyObject* adamw_keep(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 1 || !PyList_Check(a[0])) Py_RETURN_NONE;
+    for (Py_ssize_t k = 0; k < PyList_GET_SIZE(a[0]); ++k) {
+        const at::Tensor* t = tensor(PyList_GET_ITEM(a[0], k));
+        if (!t || !t->is_cuda()) Py_RETURN_NONE;
+        c10::cuda::CUDACachingAllocator::recordStream(t->storage().data_ptr(),
+                                                      c10::cuda::getCurrentCUDAStream(t->device().index()));
+    }
+    Py_RETURN_TRUE;
+    END_HANDLE_TH_ERRORS
+}
+
 PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
 }
@@ -267,6 +283,7 @@ PyMethodDef methods[] = {
     {"ffn_bwd", fast(ffn_bwd), METH_FASTCALL, nullptr},
     {"adamw_step", fast(adamw_step), METH_FASTCALL, nullptr},
     {"adamw_places", fast(adamw_places), METH_FASTCALL, nullptr},
+    {"adamw_keep", fast(adamw_keep), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
