@@ -743,6 +743,153 @@ MLAQ_API int mla_gated_ffn_bwd(const mla_ffn_shape *shape, const void *dy, const
                                const void *w_down, const void *gate_up, const void *h, void *dgate_up, void *dx,
                                void *dw_gate_up, void *dw_down, int *dev_status, void *stream);
 
+/* ---- RMS norm -----------------------------------------------------------
+ * The norm in front of the projections (an addition of this library: the
+ * pages start at its result). T rows of K channels:
+ *   h = x + r,  rstd[t] = (mean_k h[t, k]^2 + eps)^(-1/2),  y = h rstd w
+ *   dtype, w_dtype   MLA_IN_F32 or MLA_IN_BF16: of x, residual, h, y, dy, dh
+ *                    and dx, and of weight and dw
+ *   ld_x, ld_res, ld_dy  row pitches in elements of x (backward: h), residual
+ *                    (backward: dh) and dy (0: dense, else >= K); h, y, dx are dense
+ *   out_mode         y as MLA_NORM_OUT_SAME: the type of x; _MXFP8: E4M3 codes
+ *                    [T, K] with y_scales [T, K/32]; _MXFP8_TILED: the codes
+ *                    with y_scales in the order of mxfp8_quantize_rows_tiled,
+ *                    group 128, padding zero-filled (what the forward takes as
+ *                    MLA_WEIGHT_MXFP8_TILED). MXFP8 needs K % 32 == 0, else
+ *                    MLA_ERR_UNSUPPORTED; a block holding NaN or Inf gets
+ *                    scale 0xFF and NaN codes.
+ * K above 32768: MLA_ERR_UNSUPPORTED. Sums are fp32, y is made of the
+ * unrounded x + r; NaN and Inf stay in their row. */
+enum { MLA_NORM_OUT_SAME = 0, MLA_NORM_OUT_MXFP8 = 1, MLA_NORM_OUT_MXFP8_TILED = 2 };
+typedef struct {
+    int64_t T;
+    int64_t K;
+    int64_t ld_x;
+    int64_t ld_res;
+    int64_t ld_dy;
+    int32_t dtype;
+    int32_t w_dtype;
+    int32_t out_mode;
+    float eps; /* >= 0, finite */
+    int64_t reserved; /* set to 0 */
+} mla_norm_shape;
+
+/*
+ * Forward. residual and h go together (both NULL: h = x), y_scales with an
+ * MXFP8 out_mode; rstd [T] fp32 or NULL. Pointers aligned to their elements
+ * (MXFP8 codes to 8 bytes); rows that all start on 16 bytes go faster.
+ */
+MLAQ_API int mla_rms_norm_fwd(const mla_norm_shape *shape, const void *x, const void *residual, const void *weight,
+                              void *h, void *y, uint8_t *y_scales, float *rstd, void *stream);
+
+/*
+ * Backward, from dy, the forward's h (x where there was no residual) and
+ * rstd: dx = rstd (dy w - n mean_k(dy w n)) + dh with n = h rstd, the gradient
+ * of both x and residual; dw = sum_t dy n. dh (the gradient that reaches h
+ * itself), dx and dw may be NULL, not both of the last two. dw needs a
+ * workspace of mla_rms_norm_bwd_workspace_size bytes (0 for an invalid shape),
+ * 16-byte aligned; its sum's order depends on T, K and the device alone.
+ */
+MLAQ_API size_t mla_rms_norm_bwd_workspace_size(const mla_norm_shape *shape);
+MLAQ_API int mla_rms_norm_bwd(const mla_norm_shape *shape, const void *dy, const void *h, const void *weight,
+                              const float *rstd, const void *dh, void *dx, void *dw, void *workspace, size_t ws_bytes,
+                              void *stream);
+
+/* ---- 8-bit cache of keys and values -------------------------------------
+ * Where the keys and values of mla_kv_uproj_fwd (or the latents and rotary
+ * keys they come from) stay between calls, and the attention that reads them
+ * (additions of this library). A cache has `pages` pages of `page` tokens (a
+ * power of two, 16 to 1024):
+ *   k        [pages, H, page, Dk] E4M3 codes, k_scales [pages, H, page/block]
+ *            E8M0 bytes, one for each block of `block` tokens (a power of two,
+ *            1 to page) of a head: value = e4m3(code) * 2^(scale - 127)
+ *   v        [pages, H, page, Dv] and v_scales alike; both NULL: the values are
+ *            the first Dv channels of the keys (Dv <= Dk)
+ * Dk and Dv are multiples of 16 (else MLA_ERR_UNSUPPORTED), k and v start on 16
+ * bytes. Position t of sequence b lies in page table[b * table_width +
+ * t / page] at place t % page (int32; entries that no position needs are not
+ * read).
+ *
+ * Every call has B sequences with n_b new tokens each, T rows on the dense
+ * side: sequence b's are rows cu[b] to cu[b + 1] - 1 (cu int32 [B + 1], from
+ * 0, never falling; NULL: one row each, T == B). Rows from cu[B] on are
+ * neither read nor written. A page outside the cache, a position outside the
+ * table or a cu outside 0..T skips what it concerns (attention reads zeros there)
+ * and sets *dev_status to MLA_ERR_POS_RANGE or MLA_ERR_INVALID_ARG.
+ */
+typedef struct {
+    int64_t pages;
+    int32_t page;
+    int32_t block;
+    int32_t H;
+    int32_t Dk;
+    int32_t Dv;
+    int32_t reserved; /* set to 0 */
+    uint8_t *k;
+    uint8_t *k_scales;
+    uint8_t *v;
+    uint8_t *v_scales;
+} mla_kv_cache;
+
+/*
+ * Quantizes k [T, H, Dk] and v [T, H, Dv] (bf16, strides k_t, k_h, v_t, v_h in
+ * elements, unit inner stride; v NULL with a cache that has none) into
+ * positions start[b], start[b] + 1, ... of every sequence. A block's exponent is
+ * the smallest with amax <= 448 * 2^e (clamped to [-127, 127]) over its finite
+ * elements; a block that already holds tokens before start[b] keeps its exponent
+ * or raises it, and then those tokens' codes are rounded again at the new one
+ * (to nearest even). What a block held behind the new tokens is no longer
+ * valid. Elements that are NaN or Inf get NaN codes. A page that is written must
+ * belong to one sequence of the call.
+ */
+MLAQ_API int mla_kv_cache_write(const mla_kv_cache *cache, const void *k, int64_t k_t, int64_t k_h, const void *v,
+                                int64_t v_t, int64_t v_h, int64_t T, int64_t B, const int32_t *table,
+                                int64_t table_width, const int32_t *start, const int32_t *cu, int *dev_status,
+                                void *stream);
+
+/*
+ * The other way: positions start[b] ... of every sequence as dense k [T, H, Dk]
+ * and v [T, H, Dv] (NULL without values of their own), dtype MLA_IN_BF16 or
+ * MLA_IN_F32 (both hold a code times its scale exactly unless that is below
+ * their smallest normal), 16-byte aligned. A scale of 0xFF reads as NaN.
+ */
+MLAQ_API int mla_kv_cache_read(const mla_kv_cache *cache, void *k, void *v, int dtype, int64_t T, int64_t B,
+                               const int32_t *table, int64_t table_width, const int32_t *start, const int32_t *cu,
+                               int *dev_status, void *stream);
+
+/*
+ * Attention over the cache. Sequence b has length[b] positions (int32), the
+ * last n_b of them its new tokens; new token i (row cu[b] + i) sees the
+ * positions up to length[b] - n_b + i. With Hq query heads, Hq / H to each head of
+ * the cache (query head h reads head h / (Hq / H)):
+ *   s_j = scale q . k_j,  p = softmax(s),  out = sum_j p_j v_j,
+ *   lse = log sum_j exp(s_j)
+ *   q [T, Hq, Dk] bf16, strides q_t and q_h in elements, unit inner stride;
+ *   out [T, Hq, Dv] bf16, lse [T, Hq] fp32 or NULL, both dense.
+ * A row that sees nothing gives zeros and -inf. A NaN reaches the rows that
+ * see it only; a query row with NaN or Inf gives NaN. Scores, statistics and
+ * sums are fp32; probabilities enter the second product with eight bits.
+ * Sizes: Dk and Dv up to 256, or, with the values in the keys, Dk up to 640
+ * and Dv up to 512; T * Hq up to INT32_MAX; else MLA_ERR_UNSUPPORTED. The
+ * workspace (mla_cache_attn_workspace_size bytes, 16-byte aligned, 0 for an
+ * invalid shape) needs no particular contents. Results do not depend on it, and
+ * equal calls give equal bytes on one device type.
+ */
+typedef struct {
+    int64_t T;
+    int64_t B;
+    int64_t q_t;
+    int64_t q_h;
+    int64_t table_width;
+    int32_t Hq;
+    float scale; /* finite */
+    int64_t reserved; /* set to 0 */
+} mla_attn_shape;
+MLAQ_API size_t mla_cache_attn_workspace_size(const mla_attn_shape *shape, const mla_kv_cache *cache);
+MLAQ_API int mla_cache_attn(const mla_attn_shape *shape, const mla_kv_cache *cache, const void *q,
+                            const int32_t *table, const int32_t *length, const int32_t *cu, void *out, float *lse,
+                            void *workspace, size_t ws_bytes, int *dev_status, void *stream);
+
 /* Static, human-readable name of a status code. */
 MLAQ_API const char *mla_status_string(int status);
 

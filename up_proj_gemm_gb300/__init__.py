@@ -652,3 +652,9 @@ __all__ += ["AdamW", "AdamwPlan", "adamw_plan", "adamw_step"]
 from .ffn import ACTIVATIONS, FfnShape, gated_ffn_bwd, gated_ffn_fwd  # noqa: E402
 
 __all__ += ["ACTIVATIONS", "FfnShape", "gated_ffn_bwd", "gated_ffn_fwd"]
+from .norm import NORM_OUTS, NormShape, rms_norm_bwd, rms_norm_fwd  # noqa: E402
+
+__all__ += ["NORM_OUTS", "NormShape", "rms_norm_bwd", "rms_norm_fwd"]
+from .cache import AttnShape, KvCache, KvCacheShape, cache_attn, kv_cache_read, kv_cache_write  # noqa: E402
+
+__all__ += ["AttnShape", "KvCache", "KvCacheShape", "cache_attn", "kv_cache_read", "kv_cache_write"]

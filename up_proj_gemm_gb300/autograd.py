@@ -30,6 +30,9 @@ gradient is the inverse rotation of the heads' sum.
 
 ``gated_ffn(x, w_gate_up, w_down, act)`` is the gated feed-forward block; it
 keeps x, the gate and up products and the hidden activations for its backward.
+
+``rms_norm(x, weight, eps, residual)`` is the norm of x, or of x + residual,
+which it then gives too; it keeps that sum and a number per row.
 """
 from __future__ import annotations
 
@@ -40,11 +43,12 @@ from torch.autograd.function import once_differentiable
 
 from . import bwd_dgrad, bwd_wgrad, fwd
 from . import gated_ffn_bwd, gated_ffn_fwd
+from . import rms_norm_bwd, rms_norm_fwd
 from . import rope_axes as _rope_axes
 from .rotary import _axes
 
 __all__ = ["QUpProj", "q_up_proj", "Mxfp8Query", "q_up_proj_mxfp8", "RopeAxes", "rope_axes", "GatedFfn",
-           "gated_ffn"]
+           "gated_ffn", "RmsNorm", "rms_norm"]
 
 
 def _dense(g):
@@ -209,3 +213,40 @@ def gated_ffn(x, w_gate_up, w_down, act="silu"):
     if not torch.is_grad_enabled():  # nothing to keep for a backward; a Function sees the inputs' flags only
         return gated_ffn_fwd(x, w_gate_up, w_down, act=act)
     return GatedFfn.apply(x, w_gate_up, w_down, act)
+
+
+def _plain_rows(g):
+    """An upstream gradient with unit inner stride and rows that do not overlap (an expanded one is copied)."""
+    return g if g.stride(1) == 1 and (g.shape[0] <= 1 or g.stride(0) >= g.shape[1]) else g.contiguous()
+
+
+class RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        ctx.set_materialize_grads(False)
+        if not any(ctx.needs_input_grad):
+            return rms_norm_fwd(x, weight, eps=eps, residual=residual)
+        r = rms_norm_fwd(x, weight, eps=eps, residual=residual, save=True)
+        ctx.save_for_backward(x if residual is None else r[1], weight, r[-1])
+        return r[0] if residual is None else (r[0], r[1])
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, weight, rstd = ctx.saved_tensors
+        need_x, need_w, need_r = ctx.needs_input_grad[:3]
+        if dy is None:  # h alone was used
+            return dh if need_x else None, torch.zeros_like(weight) if need_w else None, dh if need_r else None, None
+        need = need_x or need_r
+        dx, dw = rms_norm_bwd(_plain_rows(dy), h, weight, rstd, dres=None if dh is None or not need else _plain_rows(dh),
+                              dx=need, dw=need_w)
+        return dx if need_x else None, dw, dx if need_r else None, None
+
+
+def rms_norm(x, weight, eps=1e-6, residual=None):
+    """The RMS norm of x [T, K], differentiable in x and weight; with a
+    residual (y, h): the norm of h = x + residual, and h for the next block,
+    differentiable in the residual too."""
+    if not torch.is_grad_enabled():
+        return rms_norm_fwd(x, weight, eps=eps, residual=residual)
+    return RmsNorm.apply(x, weight, residual, eps)

@@ -96,6 +96,30 @@ int make_tmap_3d(void* tmap_out, const void* base, uint64_t d0, uint64_t d1, uin
     return r == CUDA_SUCCESS ? MLA_OK : MLA_ERR_CUDA;
 }
 
+int make_tmap_pages(void* tmap_out, const void* base, uint64_t D, uint64_t page, uint64_t H, uint64_t pages,
+                    uint32_t box_rows) {
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    std::call_once(once, [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    });
+    if (!encode) return MLA_ERR_CUDA;
+    const cuuint64_t dims[4] = {D, page, H, pages};
+    const cuuint64_t strides[3] = {D, page * D, H * page * D};
+    const cuuint32_t box[4] = {128, box_rows, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = encode(reinterpret_cast<CUtensorMap*>(tmap_out), CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+                        const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MLA_OK : MLA_ERR_CUDA;
+}
+
 int make_tmap_chunks(void* tmap_out, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows,
                      uint32_t box_chunks) {
     static std::once_flag once;

@@ -1,0 +1,1067 @@
+// Attention over the 8-bit cache: out = softmax(scale q k^T) v with keys and
+// values as E4M3 codes and one power-of-two scale per block of tokens.
+//
+// The codes go to the tensor cores as they are. The query is split into two
+// E4M3 numbers instead: with a row scaled to amax < 256, hi = e4m3(q) leaves a
+// residual of at most four bits of a bf16 q, so lo = e4m3(32 (q - hi)) holds the
+// rest and q = hi + lo / 32 exactly (down to 2^-14 of the row's largest; below
+// that to 2^-22 of it). Probabilities, as f32, are split the same way and enter
+// the second product with eight bits, the precision of bf16. So no cached byte
+// is ever converted, and both products run at the 8-bit rate.
+//
+// Both products have the cached tokens as their 128 rows:
+//   S^T [128 tokens, 2R] = K [128, Dk] x [q_hi | q_lo]^T   (R query rows)
+//   O^T [128 channels, 2R] += V^T [128, 128 tokens] x [p_hi | p_lo]^T
+// A query tile is R = 8 to 64 rows, the heads of a group times the new tokens, so
+// one token of a few heads costs an N of 16, not an M of 128; a thread owns a
+// token: its scales are two registers. V^T is read from the same [token][channel]
+// tiles as an MN-major operand; with values in the keys (latents) the keys' tile
+// serves both. The scale of K multiplies the score in the thread that owns the
+// token, that of V the probability (p 2^(e - E), E the largest exponent seen).
+//
+// The running maximum is a reference that a row's scores may pass by 2^4: one
+// vote per tile, and only a tile that passes it pays for reductions and for
+// rescaling O in tensor memory. (The factor 2^4 and E4M3's range leave the
+// weights 14 binades of full precision below the reference.)
+//
+// Work is tiles of 128 tokens of all (head, query tile) pairs in one line, cut into
+// equal shares, one per SM: lengths live on the device, and a ragged batch or one
+// long sequence fills every SM alike. A share's first and last pair may be
+// parts; their O, maximum and sum go to the workspace and a second kernel adds
+// the parts in the order of the shares.
+#include <cuda.h>
+
+#include "cache.cuh"
+#include "internal.h"
+#include "launch.cuh"
+
+namespace mlaq {
+namespace {
+
+constexpr int kTokens = 128;           // tokens of a tile
+constexpr uint32_t kChunk = 16384;     // 128 tokens x 128 channels
+constexpr int kSoftmax = 128;          // threads of the softmax warps (0-3); warp 4 loads, warp 5 issues the products
+constexpr int kThreads = 192;
+constexpr float kPass = 4.f;           // log2 of how far scores may pass the reference
+constexpr float kNothing = -3.0e38f;   // the reference of a row that has seen nothing
+constexpr int kNoScale = -1000;
+constexpr int kHeldSeqs = 512;         // sequences whose lengths fit into shared memory
+constexpr int kMaxQueryChunks = 5;
+constexpr int kCombineThreads = 256;
+
+// The parts of a share: place 0 of the workspace has the one that begins inside
+// its pair of slot and head (it may go on into the next share), place 1 the one
+// that begins with its pair and does not end it.
+enum { kNoPart = 0, kOpens = 1, kGoesOn = 2, kEnds = 3 };
+
+struct AttnParams {
+    const uint16_t* q;
+    uint16_t* out;
+    float* lse;
+    const int32_t *table, *length, *cu;
+    const uint8_t *k_scales, *v_scales;
+    float* part_o;    // [2 * shares][R][Dv]
+    float2* part_ml;  // [2 * shares][R]
+    int4* meta;       // [shares][2]
+    int64_t q_t, q_h, T, pages, slots;
+    int B, width, page_shift, page, block_shift, marks, H, Hq, group, per_seq, Dk, Dv, nk, nv, ring, tmem_cols;
+    int q_vec;
+    float scale_log2;
+    int* status;
+};
+
+// ------------------------------------------------------------- pieces of PTX
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// kind::f8f6f4, E4M3 x E4M3, f32 sums (the fields of idesc_bf16, formats 0)
+__host__ __device__ constexpr uint32_t idesc_f8(uint32_t M, uint32_t N, uint32_t a_mn_major) {
+    return (1u << 4) | (a_mn_major << 15) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const void* map, int c, int place, int h, int page,
+                                              uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(c), "r"(place), "r"(h), "r"(page), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+__device__ __forceinline__ float warp_add(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+__device__ __forceinline__ void sts_b8(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.b8 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
+}
+__device__ __forceinline__ void sts_v2(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
+// ------------------------------------------------------------ work in a line
+// A slot is a tile of R query rows of one sequence (row = token * group + head in
+// the group); slots of sequence b start at first(b) = cu[b] * group / R + b.
+struct Slot {
+    int64_t lo;  // the sequence's first row of q
+    int b, n, len, rho0, rows, tiles;
+};
+
+struct Lengths {  // in shared memory when they fit
+    const int32_t *length, *cu;
+};
+
+template <int R>
+__device__ __forceinline__ int64_t first_slot(const AttnParams& p, const Lengths& s, int b) {
+    return (int64_t)s.cu[b] * p.group / R + b;
+}
+
+// What slot holds; b: a sequence at or before the slot's.
+template <int R>
+__device__ __forceinline__ Slot read_slot(const AttnParams& p, const Lengths& s, int64_t slot, int b) {
+    Slot x;
+    int64_t j;
+    if (p.cu) {
+        while (b + 1 < p.B && first_slot<R>(p, s, b + 1) <= slot) ++b;
+        x.lo = s.cu[b];
+        const int64_t n = (int64_t)s.cu[b + 1] - x.lo;
+        const bool fine = x.lo >= 0 && n >= 0 && x.lo + n <= p.T;
+        if (!fine) record_status(p.status, MLA_ERR_INVALID_ARG);
+        x.n = fine ? (int)n : 0;
+        j = slot - first_slot<R>(p, s, b);
+    } else {
+        b = (int)(slot / p.per_seq);
+        j = slot - (int64_t)b * p.per_seq;
+        x.lo = b;
+        x.n = 1;
+    }
+    x.b = b;
+    const int64_t total = (int64_t)x.n * p.group, left = total - j * R;
+    x.rho0 = (int)(j * R);
+    x.rows = j < 0 || left <= 0 ? 0 : left < R ? (int)left : R;
+    const int64_t room = (int64_t)p.width << p.page_shift;
+    const int len = s.length[b];
+    x.len = len < 0 ? 0 : len > room ? (int)room : len;
+    if (x.rows > 0 && x.len != len) record_status(p.status, MLA_ERR_POS_RANGE);
+    int limit = x.len - x.n + (x.rho0 + x.rows - 1) / p.group + 1;
+    limit = limit < 0 ? 0 : limit > x.len ? x.len : limit;
+    x.tiles = x.rows == 0 ? 0 : limit == 0 ? 1 : (limit + kTokens - 1) / kTokens;
+    return x;
+}
+
+// The pieces of a share, in order: tiles [t0, t1) of one slot and head. Every
+// role of the block walks the same pieces.
+template <int R>
+struct Walk {
+    Slot x;
+    int64_t slot;
+    int h, t0, t1, left;
+
+    __device__ __forceinline__ bool next(const AttnParams& p, const Lengths& s) {
+        if (left <= 0) return false;
+        if (t1 > 0) {  // not the first: to the next slot that has work
+            t1 = 0;
+            t0 = 0;
+            do {
+                if (++slot == p.slots) {
+                    slot = 0;
+                    x.b = 0;
+                    ++h;
+                }
+                x = read_slot<R>(p, s, slot, x.b);
+            } while (x.tiles == 0 && h < p.H);
+        }
+        const int n = x.tiles - t0;
+        t1 = t0 + (n < left ? n : left);
+        left -= t1 - t0;
+        return h < p.H && t1 > t0;
+    }
+};
+
+// A ring slot and its phase, advanced chunk by chunk.
+struct Ring {
+    int i = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step(int n) {
+        if (++i == n) {
+            i = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+template <int R>
+struct Shared {  // behind the ring, the queries and the probabilities
+    uint64_t full[14], empty[14];
+    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, drain;
+    int64_t row_at[2][R];       // row of out, by the piece's parity
+    float2 row[2][R];           // (2^-exponent of the query row, reference)
+    int limit[2][R];            // the last position that a row sees
+    float factor[R];
+    float warp_row[4][R];
+    int warp_e[4];
+    int vote[3];
+    int top_e, nan_seen;
+    uint32_t tmem;
+    volatile int abort;
+    int64_t scan[8];
+    int64_t start_slot;
+    int start_b, start_off;
+    int nan_at[512];            // by channel: the first position with a NaN that not every row sees
+    int32_t length[kHeldSeqs], cu[kHeldSeqs + 1];
+};
+
+template <int R, bool SHARED>
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                      const __grid_constant__ AttnParams p) {
+    constexpr int N2 = 2 * R;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t q_base = base + p.ring * kChunk;
+    const uint32_t p_base = q_base + p.nk * (N2 * 128);
+    Shared<R>& sh = *reinterpret_cast<Shared<R>*>(smem_raw + (p_base - raw) + 2 * N2 * 128);
+    const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
+    const uint32_t s_full = smem_u32(&sh.s_full[0]), s_empty = smem_u32(&sh.s_empty[0]);
+    const uint32_t p_full = smem_u32(&sh.p_full[0]), p_empty = smem_u32(&sh.p_empty[0]);
+    const uint32_t q_full = smem_u32(&sh.q_full), drain = smem_u32(&sh.drain);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int* abort_flag = &sh.abort;
+
+    if (tid == 0) {
+        for (int i = 0; i < p.ring; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(s_empty + 8 * i, 4);
+            mbar_init(p_full + 8 * i, 4);
+            mbar_init(p_empty + 8 * i, 1);
+        }
+        mbar_init(q_full, 4);
+        mbar_init(drain, 1);
+        sh.abort = 0;
+        sh.vote[0] = sh.vote[1] = sh.vote[2] = 0;
+        sh.nan_seen = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&k_map);
+        if (!SHARED) tma_prefetch_desc(&v_map);
+    }
+    __syncwarp();
+    if (warp == 5) {
+        tmem_alloc(smem_u32(&sh.tmem), p.tmem_cols);
+        tmem_relinquish();
+    }
+    // columns of the queries past Dk meet zeros of the cache: they have to be numbers
+    for (uint32_t i = tid * 16; i < (uint32_t)p.nk * N2 * 128; i += kThreads * 16) sts_v4(q_base + i, 0, 0, 0, 0);
+    for (int i = tid; i < 512; i += kThreads) sh.nan_at[i] = 0x7FFFFFFF;
+    grid_launch_next();
+    grid_wait_previous();
+
+    // ------------------------------------------------------------ the share
+    Lengths seqs{p.length, p.cu};
+    if (p.B <= kHeldSeqs) {
+        for (int i = tid; i < p.B; i += kThreads) sh.length[i] = p.length[i];
+        if (p.cu)
+            for (int i = tid; i <= p.B; i += kThreads) sh.cu[i] = p.cu[i];
+        seqs = {sh.length, sh.cu};
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const int64_t per_thread = (p.slots + kThreads - 1) / kThreads;
+    const int64_t my_slot = per_thread * tid;
+    int64_t mine = 0;
+    int my_b = 0;
+    if (my_slot < p.slots) {
+        if (p.cu) {  // the last b with first(b) <= my_slot
+            int hi = p.B;
+            while (hi - my_b > 1) {
+                const int mid = (my_b + hi) / 2;
+                if (first_slot<R>(p, seqs, mid) <= my_slot) my_b = mid;
+                else hi = mid;
+            }
+        }
+        int b = my_b;
+        for (int64_t i = my_slot; i < my_slot + per_thread && i < p.slots; ++i) {
+            const Slot x = read_slot<R>(p, seqs, i, b);
+            b = x.b;
+            mine += x.tiles;
+        }
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) sh.scan[warp] = upto;
+    __syncthreads();
+    int64_t line = 0;  // tiles of one head
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) upto += sh.scan[w];
+        line += sh.scan[w];
+    }
+    const int64_t all = line * p.H;
+    const int64_t shares = all < (int64_t)gridDim.x ? all : (int64_t)gridDim.x;
+    const int64_t c = blockIdx.x;
+    const int64_t w0 = c < shares ? all * c / shares : 0, w1 = c < shares ? all * (c + 1) / shares : 0;
+    if (w1 > w0) {
+        const int64_t at = w0 % line;
+        if (at >= upto - mine && at < upto) {  // one thread's
+            int64_t before = upto - mine, i = my_slot;
+            int b = my_b;
+            for (;; ++i) {
+                const Slot x = read_slot<R>(p, seqs, i, b);
+                b = x.b;
+                if (at < before + x.tiles) break;
+                before += x.tiles;
+            }
+            sh.start_slot = i;
+            sh.start_b = b;
+            sh.start_off = (int)(at - before);
+        }
+    }
+    __syncthreads();
+    const uint32_t tmem = sh.tmem;
+    const int tiles = (int)(w1 - w0);
+    Walk<R> walk;
+    walk.left = tiles;
+    walk.t1 = 0;
+    if (tiles > 0) {
+        walk.slot = sh.start_slot;
+        walk.h = (int)(w0 / line);
+        walk.t0 = sh.start_off;
+        walk.x = read_slot<R>(p, seqs, walk.slot, sh.start_b);
+    }
+    int parts = 0;  // thread 0: which of the share's two places in the workspace it has filled
+    const uint32_t s_tmem = tmem, o_tmem = tmem + 2 * N2;
+
+    if (warp == 4) {
+        // ---------------------------------------------------------- producer
+        // tile t's keys, then tile t - 1's values: the order in which they are used
+        Ring ring;
+        int filled = 0;
+        bool ok = true;
+        const int box = p.page < kTokens ? p.page : kTokens, boxes = kTokens / box;
+        auto load = [&](const CUtensorMap* map, const Slot& x, int h, int tile, int chunks) {
+            const int at = tile * kTokens + lane * box;
+            const bool have = lane < boxes && at < x.len;
+            int page = 0;
+            if (have) {
+                page = p.table[(int64_t)x.b * p.width + (at >> p.page_shift)];
+                if (page < 0 || page >= p.pages) {
+                    record_status(p.status, MLA_ERR_POS_RANGE);
+                    page = (int)p.pages;  // reads as zeros
+                }
+            }
+            const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, have)) * box * 128;
+            for (int j = 0; j < chunks && ok; ++j) {
+                bool got = true;
+                if (lane == 0) got = filled < p.ring || mbar_wait(empty0 + 8 * ring.i, ring.phase ^ 1u, abort_flag);
+                ok = __shfl_sync(0xFFFFFFFFu, got, 0);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * ring.i, bytes);
+                __syncwarp();
+                if (have)
+                    tma_load_page(base + ring.i * kChunk + lane * box * 128, map, j * 128, at & (p.page - 1), h, page,
+                                  full0 + 8 * ring.i);
+                ring.step(p.ring);
+                ++filled;
+            }
+        };
+        if (tiles > 0) {
+            Walk<R> keys = walk, values = walk;
+            keys.next(p, seqs);
+            if (!SHARED) values.next(p, seqs);
+            int tk = keys.t0, tv = values.t0;
+            for (int t = 0; t <= tiles && ok; ++t) {
+                if (t < tiles) {
+                    load(&k_map, keys.x, keys.h, tk, p.nk);
+                    if (++tk == keys.t1 && keys.next(p, seqs)) tk = keys.t0;
+                }
+                if (!SHARED && t > 0 && ok) {
+                    load(&v_map, values.x, values.h, tv, p.nv);
+                    if (++tv == values.t1 && values.next(p, seqs)) tv = values.t0;
+                }
+            }
+            if (!ok && lane == 0) {  // copies in flight land before the block leaves
+                for (int j = filled > p.ring ? filled - p.ring : 0; j < filled; ++j)
+                    mbar_wait(full0 + 8 * (j % p.ring), (uint32_t)(j / p.ring) & 1u, nullptr, 200000000ull);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        // -------------------------------------------------------- MMA issuer
+        if (lane == 0 && tiles > 0) {
+            const uint32_t i_s = idesc_f8(128, N2, 0), i_o = idesc_f8(128, N2, 1);
+            Ring ring;              // next chunk in the order of use
+            int tile_slot = 0;      // SHARED: ring slot of tile t - 1's first chunk
+            bool ok = true, first = true, first_before = false;
+            Walk<R> w = walk;
+            w.next(p, seqs);
+            int tw = w.t0;
+            uint32_t q_phase = 0;
+            for (int t = 0; t <= tiles && ok; ++t) {
+                const int this_slot = ring.i;
+                if (t < tiles) {
+                    if (first) {
+                        ok = mbar_wait(q_full, q_phase, abort_flag);
+                        q_phase ^= 1u;
+                    }
+                    ok = ok && (t < 2 || mbar_wait(s_empty + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1u, abort_flag));
+                    for (int j = 0; j < p.nk && ok; ++j) {
+                        ok = mbar_wait(full0 + 8 * ring.i, ring.phase, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const int left = p.Dk - j * 128, steps = left >= 128 ? 4 : (left + 31) / 32;
+                        for (int s = 0; s < steps; ++s)
+                            mma_f8(s_tmem + (t & 1) * N2, desc_kmajor_sw128(base + ring.i * kChunk + s * 32),
+                                   desc_kmajor_sw128(q_base + j * (N2 * 128) + s * 32), i_s, (j | s) != 0);
+                        if (!SHARED) mma_commit(empty0 + 8 * ring.i);
+                        ring.step(p.ring);
+                    }
+                    if (!ok) break;
+                    mma_commit(s_full + 8 * (t & 1));
+                }
+                if (t > 0) {
+                    const int u = t - 1;
+                    ok = mbar_wait(p_full + 8 * (u & 1), (uint32_t)(u >> 1) & 1u, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t probs = p_base + (u & 1) * (N2 * 128);
+                    for (int j = 0; j < p.nv && ok; ++j) {
+                        int at = ring.i;
+                        if (SHARED) {
+                            at = tile_slot + j;
+                            if (at >= p.ring) at -= p.ring;
+                        } else {
+                            ok = mbar_wait(full0 + 8 * ring.i, ring.phase, abort_flag);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            mma_f8(o_tmem + j * N2, desc_mnmajor_sw128(base + at * kChunk + s * 4096, kChunk),
+                                   desc_kmajor_sw128(probs + s * 32), i_o, !first_before || s != 0);
+                        if (!SHARED) {
+                            mma_commit(empty0 + 8 * ring.i);
+                            ring.step(p.ring);
+                        }
+                    }
+                    if (!ok) break;
+                    if (SHARED)
+                        for (int j = 0; j < p.nk; ++j) mma_commit(empty0 + 8 * ((tile_slot + j) % p.ring));
+                    mma_commit(p_empty + 8 * (u & 1));
+                }
+                tile_slot = this_slot;
+                first_before = first;
+                if (t < tiles) {
+                    first = false;
+                    if (++tw == w.t1) {
+                        first = true;
+                        if (w.next(p, seqs)) tw = w.t0;
+                    }
+                }
+            }
+            if (!ok) {
+                mma_commit(drain);
+                mbar_wait(drain, 0, nullptr, 200000000ull);
+            }
+        }
+        __syncwarp();
+    } else if (tiles > 0) {
+        // ------------------------------------------------------------ softmax
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;  // this warp's lanes of tensor memory
+        // the query rows of a piece as two E4M3 numbers each, row r at r and R + r; a warp takes every fourth row
+        auto load_q = [&](const Walk<R>& w, int par) {
+            const int gran = p.Dk / 8;
+            for (int r0 = 0; r0 < R; r0 += 16) {
+                constexpr int kG = (kMaxQueryChunks * 128 / 8 + 31) / 32;
+                uint4 g[4][kG];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = r0 + i * 4 + warp, rho = w.x.rho0 + r, tok = rho / p.group;
+                    const bool have = r < R && r < w.x.rows;
+                    const uint16_t* src = p.q + (w.x.lo + tok) * p.q_t + (int64_t)(w.h * p.group + rho - tok * p.group) * p.q_h;
+#pragma unroll
+                    for (int k = 0; k < kG; ++k) {
+                        const int at = k * 32 + lane;
+                        g[i][k] = make_uint4(0, 0, 0, 0);
+                        if (have && at < gran) {
+                            const uint16_t* q = src + at * 8;
+                            if (p.q_vec) {
+                                g[i][k] = *reinterpret_cast<const uint4*>(q);
+                            } else {
+                                g[i][k].x = q[0] | ((uint32_t)q[1] << 16);
+                                g[i][k].y = q[2] | ((uint32_t)q[3] << 16);
+                                g[i][k].z = q[4] | ((uint32_t)q[5] << 16);
+                                g[i][k].w = q[6] | ((uint32_t)q[7] << 16);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = r0 + i * 4 + warp;
+                    if (r >= R) continue;
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int k = 0; k < kG; ++k) {
+                        const uint32_t u[4] = {g[i][k].x, g[i][k].y, g[i][k].z, g[i][k].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) m = max(m, max((u[e] << 16) & 0x7FFFFFFFu, u[e] & 0x7FFF0000u));
+                    }
+                    m = __reduce_max_sync(0xFFFFFFFFu, m);
+                    // a factor 2^x that brings the row's largest into [128, 256); NaN and Inf make the row's scale NaN
+                    int x = 134 - (int)(m >> 23);
+                    x = m == 0 ? 0 : x > 120 ? 120 : x;
+                    const bool bad = m >= 0x7F800000u;
+                    const float up = bad ? 0.f : __uint_as_float((uint32_t)(127 + x) << 23);
+#pragma unroll
+                    for (int k = 0; k < kG; ++k) {
+                        const int at = k * 32 + lane;
+                        if (at >= gran) continue;
+                        const uint32_t u[4] = {g[i][k].x, g[i][k].y, g[i][k].z, g[i][k].w};
+                        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = bad ? 0.f : bf16lo_to_f32(u[e]) * up, b = bad ? 0.f : bf16hi_to_f32(u[e]) * up;
+                            const uint32_t h2 = cvt_e4m3x2(a, b);
+                            float ha, hb;
+                            e4m3x2_to_f32(h2, ha, hb);
+                            hi[e / 2] |= h2 << (16 * (e & 1));
+                            lo[e / 2] |= cvt_e4m3x2((a - ha) * 32.f, (b - hb) * 32.f) << (16 * (e & 1));
+                        }
+                        const uint32_t chunk = q_base + (at >> 4) * (N2 * 128);
+                        const uint32_t unit = (at & 15) >> 1, half = (at & 1) * 8;
+                        sts_v2(chunk + r * 128 + ((unit ^ (r & 7)) << 4) + half, hi[0], hi[1]);
+                        sts_v2(chunk + (R + r) * 128 + ((unit ^ (r & 7)) << 4) + half, lo[0], lo[1]);
+                    }
+                    if (lane == 0) {
+                        const int rr = r < w.x.rows ? r : w.x.rows - 1, rho = w.x.rho0 + rr, tok = rho / p.group;
+                        sh.row[par][r] = make_float2(bad ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 - x) << 23), kNothing);
+                        sh.limit[par][r] = w.x.len - w.x.n + tok;
+                        sh.row_at[par][r] = (w.x.lo + tok) * p.Hq + (int64_t)w.h * p.group + rho - tok * p.group;
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            named_bar_sync(1, kSoftmax);
+        };
+        // the scale bytes of this thread's token: keys in bits 0-7, values in 8-15
+        auto load_scales = [&](const Walk<R>& w, int tile) -> uint32_t {
+            const int pos = tile * kTokens + tid;
+            if (pos >= w.x.len) return 0;
+            const int page = p.table[(int64_t)w.x.b * p.width + (pos >> p.page_shift)];
+            if (page < 0 || page >= p.pages) return 0;  // recorded by the producer
+            const int64_t at = ((int64_t)page * p.H + w.h) * p.marks + ((pos & (p.page - 1)) >> p.block_shift);
+            const uint32_t k = p.k_scales[at];
+            return k | (SHARED ? k << 8 : (uint32_t)p.v_scales[at] << 8);
+        };
+
+        uint32_t p_off[8];  // this token's byte in the first eight rows of the probabilities (128-byte swizzle)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p_off[i] = i * 128 + (((uint32_t)(tid >> 4) ^ i) << 4) + (tid & 15);
+
+        Walk<R> w = walk;
+        bool more = w.next(p, seqs);
+        int par = 0, t = 0;
+        // A wait that gave up is reported with the next vote, so that all four warps leave together: until then a
+        // thread that saw it goes on, through every barrier.
+        bool failed = false, leave = false;
+        if (more) load_q(w, 0);
+        uint32_t marks = more ? load_scales(w, w.t0) : 0;
+        while (more) {
+            const float2* row = sh.row[par];
+            const int* limit = sh.limit[par];
+            float l[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) l[r] = 0.f;
+            int top_e = kNoScale;
+            const int least = w.x.len - w.x.n + w.x.rho0 / p.group;  // the last position that every row sees
+            for (int tile = w.t0; tile < w.t1; ++tile, ++t) {
+                const int buf = t & 1, pos = tile * kTokens + tid;
+                const bool masked = (tile + 1) * kTokens - 1 > least;
+                const bool valid = pos < w.x.len;
+                const float ks = e8m0_to_f32(marks & 0xFFu) * p.scale_log2;
+                const int ve = (int)(marks >> 8);
+                if (tile + 1 < w.t1) marks = load_scales(w, tile + 1);  // under this tile
+                failed |= !mbar_wait(s_full + 8 * buf, (uint32_t)(t >> 1) & 1u, abort_flag);
+                __syncwarp();
+                tc_fence_after();
+                float s[R];
+                const uint32_t from = s_tmem + lanes + buf * N2;
+                if constexpr (R == 8) {
+                    uint32_t v[16];
+                    tmem_ld16(from, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) s[r] = fmaf(__uint_as_float(v[8 + r]), 0.03125f, __uint_as_float(v[r]));
+                } else {
+#pragma unroll
+                    for (int r0 = 0; r0 < R; r0 += 16) {
+                        uint32_t v[16], u[16];
+                        tmem_ld16(from + r0, v);
+                        tmem_ld16(from + R + r0, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            s[r0 + r] = fmaf(__uint_as_float(u[r]), 0.03125f, __uint_as_float(v[r]));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_empty + 8 * buf);
+                float over = kNothing;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float2 q = row[r];
+                    s[r] = s[r] * ks * q.x;
+                    if (masked) s[r] = pos <= limit[r] ? s[r] : -INFINITY;
+                    over = fmaxf(over, s[r] - q.y);
+                }
+                const bool grow = valid && (over > kPass || (ve > top_e && ve != 255));
+                const int bits = (__any_sync(0xFFFFFFFFu, grow) ? 1 : 0) | (__any_sync(0xFFFFFFFFu, failed) ? 2 : 0);
+                if (lane == 0 && bits) atomicOr(&sh.vote[t % 3], bits);
+                named_bar_sync(1, kSoftmax);
+                const int vote = *(volatile int*)&sh.vote[t % 3];
+                if (tid == 0) sh.vote[(t + 2) % 3] = 0;
+                if (vote & 2) {
+                    leave = true;
+                    break;
+                }
+                if (vote) {
+                    // a new reference for every row: the largest score so far; and the largest scale of V
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const float m = warp_max(valid ? s[r] : -INFINITY);
+                        if (lane == (r & 31)) sh.warp_row[warp][r] = m;
+                    }
+                    const int e = __reduce_max_sync(0xFFFFFFFFu, valid && ve != 255 ? ve : kNoScale);
+                    if (lane == 0) sh.warp_e[warp] = e;
+                    named_bar_sync(1, kSoftmax);
+                    if (tid < R) {
+                        const float old = sh.row[par][tid].y;
+                        float m = old;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) m = fmaxf(m, sh.warp_row[i][tid]);
+                        sh.row[par][tid].y = m;
+                        sh.factor[tid] = exp2_fast(old - m);
+                    }
+                    const int old_e = top_e;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top_e = max(top_e, sh.warp_e[i]);
+                    named_bar_sync(1, kSoftmax);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) l[r] *= sh.factor[r];
+                    if (tile > w.t0) {
+                        const float down = old_e == top_e ? 1.f : old_e < top_e - 126 ? 0.f : __uint_as_float((uint32_t)(127 + old_e - top_e) << 23);
+                        failed |= !mbar_wait(p_empty + 8 * (buf ^ 1), (uint32_t)((t - 1) >> 1) & 1u, abort_flag);
+                        __syncwarp();
+                        tc_fence_after();
+                        for (int j = 0; j < p.nv; ++j)
+#pragma unroll
+                            for (int r0 = 0; r0 < N2; r0 += 16) {
+                                uint32_t v[16];
+                                const uint32_t at = o_tmem + lanes + j * N2 + r0;
+                                tmem_ld16(at, v);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    v[i] = __float_as_uint(__uint_as_float(v[i]) * sh.factor[(r0 + i) % R] * down);
+                                tmem_st16(at, v);
+                            }
+                        tmem_st_wait();
+                    }
+                }
+                // the probabilities, times the value's scale, as two E4M3 numbers
+                if (t >= 2) failed |= !mbar_wait(p_empty + 8 * buf, (uint32_t)((t >> 1) - 1) & 1u, abort_flag);
+                const int fe = ve - top_e + 4 + 127;
+                float f = fe <= 0 ? 0.f : __uint_as_float((uint32_t)fe << 23);
+                if (ve == 255) f = __uint_as_float(0x7FC00000u);
+                if (!valid) f = 0.f;
+                const uint32_t to = p_base + buf * (N2 * 128);
+#pragma unroll
+                for (int r = 0; r < R; r += 2) {
+                    const float a = exp2_fast(s[r] - row[r].y), b = exp2_fast(s[r + 1] - row[r + 1].y);
+                    float x = a * f, y = b * f;
+                    if (masked) {
+                        const bool ina = valid && pos <= limit[r], inb = valid && pos <= limit[r + 1];
+                        l[r] += ina ? a : 0.f;
+                        l[r + 1] += inb ? b : 0.f;
+                        x = ina ? x : 0.f;
+                        y = inb ? y : 0.f;
+                    } else {
+                        l[r] += a;
+                        l[r + 1] += b;
+                    }
+                    const uint32_t hi = cvt_e4m3x2(x, y);
+                    float ha, hb;
+                    e4m3x2_to_f32(hi, ha, hb);
+                    const uint32_t lo = cvt_e4m3x2((x - ha) * 32.f, (y - hb) * 32.f);
+                    const uint32_t at = to + (r >> 3) * 1024;
+                    sts_b8(at + p_off[r & 7], hi & 0xFFu);
+                    sts_b8(at + p_off[(r + 1) & 7], hi >> 8);
+                    sts_b8(at + R * 128 + p_off[r & 7], lo & 0xFFu);
+                    sts_b8(at + R * 128 + p_off[(r + 1) & 7], lo >> 8);
+                }
+                if ((tile + 1) * kTokens > w.x.len || (masked && w.x.n > 1)) {
+                    // What lies behind the last position may be anything, also NaN: zeros. And a NaN that some rows see
+                    // and others do not must not meet their zero probability: it is noted and put into the result.
+                    int64_t chunk;
+                    if (SHARED) chunk = (int64_t)t * p.nk;
+                    else chunk = (int64_t)(t + 2 < tiles ? t + 2 : tiles) * p.nk + (int64_t)t * p.nv;
+                    for (int j = 0; j < p.nv; ++j, ++chunk) {
+                        const int at = (int)(chunk % p.ring);
+                        failed |= !mbar_wait(full0 + 8 * at, (uint32_t)(chunk / p.ring) & 1u, abort_flag);
+                        const uint32_t mem = base + at * kChunk + tid * 128;
+                        if (!valid) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) sts_v4(mem + i * 16, 0, 0, 0, 0);
+                        } else if (pos > least) {
+                            for (int i = 0; i < 8; ++i) {
+                                const uint4 v = lds_v4(mem + ((i ^ (tid & 7)) << 4));
+                                uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                                bool any = false;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        if (((u[k] >> (8 * e)) & 0x7Fu) == 0x7Fu) {
+                                            any = true;
+                                            atomicMin(&sh.nan_at[(j * 128 + i * 16 + k * 4 + e) & 511], pos);
+                                            u[k] &= ~(0xFFu << (8 * e));
+                                        }
+                                if (any) {
+                                    sts_v4(mem + ((i ^ (tid & 7)) << 4), u[0], u[1], u[2], u[3]);
+                                    sh.nan_seen = 1;
+                                }
+                            }
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * buf);
+            }
+            if (leave) break;
+            const Walk<R> done = w;
+            const int last = t - 1;
+            more = w.next(p, seqs);
+            if (more) {
+                load_q(w, par ^ 1);  // every product of this piece's queries is done: its last scores were read
+                marks = load_scales(w, w.t0);
+            }
+            // ------------------------------------------------ the piece's result
+            const bool whole = done.t0 == 0 && done.t1 == done.x.tiles;
+            const int part = 2 * (int)c + (done.t0 == 0 ? 1 : 0);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float v = warp_add(l[r]);
+                if (lane == (r & 31)) sh.warp_row[warp][r] = v;
+            }
+            named_bar_sync(1, kSoftmax);
+            if (tid < R) {
+                const float sum = (sh.warp_row[0][tid] + sh.warp_row[1][tid]) + (sh.warp_row[2][tid] + sh.warp_row[3][tid]);
+                const float m = row[tid].y;
+                const float f = ldexpf(1.f, top_e < 0 ? -131 : top_e - 131);
+                if (whole) {
+                    sh.factor[tid] = sum == 0.f ? 0.f : f / sum;
+                    if (p.lse && tid < done.x.rows)
+                        p.lse[sh.row_at[par][tid]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945309f;
+                } else {
+                    sh.factor[tid] = f;
+                    p.part_ml[(int64_t)part * R + tid] = make_float2(m, sum);
+                }
+            }
+            named_bar_sync(1, kSoftmax);
+            failed |= !mbar_wait(p_empty + 8 * (last & 1), (uint32_t)(last >> 1) & 1u, abort_flag);
+            __syncwarp();
+            tc_fence_after();
+            const bool nans = *(volatile int*)&sh.nan_seen != 0;
+            for (int j = 0; j < p.nv; ++j) {
+                const int ch = j * 128 + tid;
+                const int nan_at = nans ? sh.nan_at[ch & 511] : 0x7FFFFFFF;
+                constexpr int kStep = R < 16 ? R : 16;
+#pragma unroll
+                for (int r0 = 0; r0 < R; r0 += kStep) {
+                    uint32_t v[16], u[16];
+                    __syncwarp();
+                    tmem_ld16(o_tmem + lanes + j * N2 + r0, v);
+                    if constexpr (R >= 16) tmem_ld16(o_tmem + lanes + j * N2 + R + r0, u);
+                    tmem_ld_wait();
+                    if (ch >= p.Dv) continue;
+#pragma unroll
+                    for (int i = 0; i < kStep; ++i) {
+                        const int r = r0 + i;
+                        if (r >= done.x.rows) break;
+                        const float lo = __uint_as_float(R >= 16 ? u[i] : v[8 + (i & 7)]);
+                        float o = fmaf(lo, 0.03125f, __uint_as_float(v[i])) * sh.factor[r];
+                        if (nan_at <= limit[r]) o = __uint_as_float(0x7FC00000u);
+                        if (whole) p.out[sh.row_at[par][r] * p.Dv + ch] = (uint16_t)pack_bf16x2(o, 0.f);
+                        else p.part_o[((int64_t)part * R + r) * p.Dv + ch] = o;
+                    }
+                }
+            }
+            tc_fence_before();
+            if (nans) {  // uniform: set before the last barriers
+                named_bar_sync(1, kSoftmax);
+                for (int i = tid; i < 512; i += kSoftmax) sh.nan_at[i] = 0x7FFFFFFF;
+                if (tid == 0) sh.nan_seen = 0;
+            }
+            named_bar_sync(1, kSoftmax);
+            if (tid == 0 && !whole) {
+                p.meta[part] = make_int4(done.t0 == 0 ? kOpens : done.t1 == done.x.tiles ? kEnds : kGoesOn, done.x.rho0,
+                                         done.x.rows, (int)done.x.lo * p.H + done.h);
+                parts |= 1 << (part & 1);
+            }
+            par ^= 1;
+        }
+    }
+    if (tid == 0)
+        for (int i = 0; i < 2; ++i)
+            if (!(parts >> i & 1)) p.meta[2 * c + i] = make_int4(kNoPart, 0, 0, 0);
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && *abort_flag) record_status(p.status, MLA_ERR_TIMEOUT);
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, p.tmem_cols);
+    }
+}
+
+// Adds the parts of the pair that share blockIdx.x opens: one query row to a block.
+template <int R>
+__global__ void __launch_bounds__(kCombineThreads) cache_attn_combine_kernel(const __grid_constant__ AttnParams p, int shares) {
+    __shared__ float weight[kCombineThreads];
+    __shared__ float sums[kCombineThreads];
+    __shared__ int ends;
+    __shared__ float total;
+    grid_launch_next();
+    grid_wait_previous();
+    const int c = blockIdx.x / R, r = blockIdx.x % R, tid = threadIdx.x;
+    const int4 m = p.meta[2 * c + 1];
+    if (m.x != kOpens || r >= m.z) return;
+    // the shares behind go on with the pair until one ends it
+    if (tid == 0) ends = shares;
+    __syncthreads();
+    for (int i = c + 1 + tid; i < shares; i += kCombineThreads)
+        if (p.meta[2 * i].x == kEnds) atomicMin(&ends, i);
+    __syncthreads();
+    const int n = (ends < shares ? ends : shares - 1) - c + 1;  // parts; at most one per thread (shares <= kCombineThreads)
+    auto place = [&](int i) { return (int64_t)(2 * (c + i) + (i == 0)) * R + r; };
+    float2 ml = make_float2(kNothing, 0.f);
+    if (tid < n) ml = p.part_ml[place(tid)];
+    weight[tid] = ml.x;
+    __syncthreads();
+    float top = kNothing;
+    for (int i = 0; i < n; ++i) top = fmaxf(top, weight[i]);
+    __syncthreads();
+    const float f = tid < n ? exp2_fast(ml.x - top) : 0.f;
+    weight[tid] = f;
+    sums[tid] = f * ml.y;
+    __syncthreads();
+    if (tid == 0) {
+        float l = 0.f;
+        for (int i = 0; i < n; ++i) l += sums[i];
+        total = l;
+    }
+    __syncthreads();
+    const float l = total, inv = l == 0.f ? 0.f : 1.f / l;
+    const int rho = m.y + r, tok = rho / p.group;
+    const int64_t row = (int64_t)(m.w / p.H + tok) * p.Hq + (int64_t)(m.w % p.H) * p.group + rho - tok * p.group;
+    if (tid == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.693147180559945309f;
+    // half of the block takes the even parts, half the odd ones
+    constexpr int kHalf = kCombineThreads / 2;
+    const int half = tid / kHalf;
+    for (int c0 = 0; c0 < p.Dv; c0 += kHalf) {
+        const int ch = c0 + tid % kHalf;
+        float o = 0.f;
+        if (ch < p.Dv) {
+#pragma unroll 8
+            for (int i = half; i < n; i += 2) o = fmaf(weight[i], p.part_o[place(i) * p.Dv + ch], o);
+        }
+        __syncthreads();
+        sums[tid] = o;
+        __syncthreads();
+        if (half == 0 && ch < p.Dv) p.out[row * p.Dv + ch] = (uint16_t)pack_bf16x2((sums[tid] + sums[tid + kHalf]) * inv, 0.f);
+    }
+}
+
+// -------------------------------------------------------------------- host
+struct AttnPlan {
+    int R, nk, nv, ring, tmem_cols;
+    size_t smem;
+};
+
+// Query rows of a tile: as many as a head of the cache has for a sequence (the
+// group times the new tokens, on average), up to 64; with more than two value
+// tiles up to 32, for tensor memory's sake: 2 score buffers and nv sums of 2R
+// columns each, 512 in all.
+template <int R>
+size_t shared_bytes() { return sizeof(Shared<R>); }
+
+bool attn_plan(const mla_attn_shape& s, const mla_kv_cache& c, int max_smem, AttnPlan* out) {
+    const bool shared = !c.v;
+    if (shared ? (c.Dk > 128 * kMaxQueryChunks || c.Dv > 512) : (c.Dk > 256 || c.Dv > 256)) return false;
+    AttnPlan a{};
+    a.nk = (c.Dk + 127) / 128;
+    a.nv = (c.Dv + 127) / 128;
+    const int64_t group = s.Hq / c.H, rows = group * (s.B > 0 ? (s.T + s.B - 1) / s.B : 1);
+    a.R = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || a.nv > 2 ? 32 : 64;
+    const size_t tail = a.R == 8 ? shared_bytes<8>() : a.R == 16 ? shared_bytes<16>() : a.R == 32 ? shared_bytes<32>() : shared_bytes<64>();
+    const size_t fixed = 1024 + (size_t)a.nk * 2 * a.R * 128 + 2 * 2 * a.R * 128 + tail;
+    const int64_t room = ((int64_t)max_smem - (int64_t)fixed) / kChunk;
+    a.ring = (int)(room > 14 ? 14 : room);
+    if (a.ring < (shared ? 2 * a.nk : a.nk + a.nv)) return false;
+    a.smem = fixed + (size_t)a.ring * kChunk;
+    const int cols = (2 + a.nv) * 2 * a.R;
+    a.tmem_cols = 32;
+    while (a.tmem_cols < cols) a.tmem_cols *= 2;
+    if (a.tmem_cols > 512) return false;
+    *out = a;
+    return true;
+}
+
+int check_attn(const mla_attn_shape* s, const mla_kv_cache* c, const int32_t* table, CacheBytes* n) {
+    if (!s) return MLA_ERR_INVALID_ARG;
+    const int st = check_cache(c, s->B, table, s->table_width, n);
+    if (st != MLA_OK && st != MLA_ERR_UNSUPPORTED && st != MLA_ERR_ALIGNMENT) return st;
+    if (s->T < 0 || s->T > kI32Max || s->Hq <= 0 || s->Hq % c->H != 0 || s->reserved != 0 || (s->T > 0 && s->B == 0))
+        return MLA_ERR_INVALID_ARG;
+    if (!(s->scale >= -3.402823466e38f && s->scale <= 3.402823466e38f)) return MLA_ERR_INVALID_ARG;
+    const int64_t most = s->T > s->Hq ? s->T : s->Hq;
+    if (!inside(most, s->q_t) || !inside(most, s->q_h)) return MLA_ERR_INVALID_ARG;
+    if (st != MLA_OK) return st;
+    if (s->T * s->Hq > kI32Max) return MLA_ERR_UNSUPPORTED;
+    return MLA_OK;
+}
+
+size_t workspace_bytes(int R, int Dv, int shares) {
+    return (size_t)shares * 2 * (R * ((size_t)Dv * 4 + 8) + 16);
+}
+
+template <int R, bool SHARED>
+int launch_attn(const AttnParams& p, const AttnPlan& a, const CUtensorMap& k, const CUtensorMap& v, int shares,
+                cudaStream_t s) {
+    if (cudaFuncSetAttribute(cache_attn_kernel<R, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)a.smem) != cudaSuccess)
+        return MLA_ERR_CUDA;
+    const int st = launch_overlapped(cache_attn_kernel<R, SHARED>, (unsigned)shares, kThreads, a.smem, 0, s, k, v, p);
+    if (st != MLA_OK) return st;
+    return launch_overlapped(cache_attn_combine_kernel<R>, (unsigned)(shares * R), kCombineThreads, 0, 0, s, p, shares);
+}
+
+}  // namespace
+}  // namespace mlaq
+
+using namespace mlaq;
+
+extern "C" {
+
+MLAQ_API size_t mla_cache_attn_workspace_size(const mla_attn_shape* shape, const mla_kv_cache* cache) {
+    CacheBytes n;
+    DeviceInfo di;
+    AttnPlan a;
+    static const int32_t some = 0;  // the table is not looked at
+    if (check_attn(shape, cache, &some, &n) != MLA_OK || current_device_info(&di) != MLA_OK ||
+        !attn_plan(*shape, *cache, di.max_smem_optin, &a))
+        return 0;
+    return workspace_bytes(a.R, cache->Dv, di.num_sms);
+}
+
+MLAQ_API int mla_cache_attn(const mla_attn_shape* shape, const mla_kv_cache* cache, const void* q,
+                            const int32_t* table, const int32_t* length, const int32_t* cu, void* out, float* lse,
+                            void* workspace, size_t ws_bytes, int* dev_status, void* stream) {
+    CacheBytes n;
+    const int st = check_attn(shape, cache, table, &n);
+    if (st != MLA_OK && st != MLA_ERR_UNSUPPORTED && st != MLA_ERR_ALIGNMENT) return st;
+    const mla_attn_shape& s = *shape;
+    const mla_kv_cache& c = *cache;
+    if ((!cu && s.T != s.B) || (s.T > 0 && (!q || !out || !length || c.pages == 0 || s.table_width == 0)))
+        return MLA_ERR_INVALID_ARG;
+    if (st != MLA_OK) return st;
+    const bool shared = !c.v;
+    if (shared ? (c.Dk > 128 * kMaxQueryChunks || c.Dv > 512) : (c.Dk > 256 || c.Dv > 256)) return MLA_ERR_UNSUPPORTED;
+    if (!aligned(q, 2) || !aligned(out, 2) || !aligned(lse, 4) || !aligned(length, 4) || !aligned(cu, 4) ||
+        !aligned(dev_status, 4) || !aligned(workspace, 16))
+        return MLA_ERR_ALIGNMENT;
+    const int64_t q_bytes = s.T > 0 ? ((s.T - 1) * s.q_t + (s.Hq - 1) * s.q_h + c.Dk) * 2 : 0;
+    const Range outs[] = {rng(out, s.T * s.Hq * c.Dv * 2), rng(lse, s.T * s.Hq * 4), rng(workspace, (int64_t)ws_bytes),
+                          rng(dev_status, 4)};
+    const Range ins[] = {rng(q, q_bytes), rng(c.k, n.k), rng(c.k_scales, n.k_scales), rng(c.v, n.v),
+                         rng(c.v_scales, n.v_scales), rng(table, s.B * s.table_width * 4), rng(length, s.B * 4),
+                         rng(cu, (s.B + 1) * 4)};
+    if (any_alias(outs, ins)) return MLA_ERR_ALIAS;
+    if (s.T == 0) return MLA_OK;
+    DeviceInfo di;
+    const int ds = current_device_info(&di);
+    if (ds != MLA_OK) return ds;
+    AttnPlan a;
+    if (!attn_plan(s, c, di.max_smem_optin, &a)) return MLA_ERR_UNSUPPORTED;
+    const int shares = di.num_sms < kCombineThreads ? di.num_sms : kCombineThreads;
+    if (!workspace || ws_bytes < workspace_bytes(a.R, c.Dv, di.num_sms)) return MLA_ERR_WORKSPACE;
+
+    AttnParams p{};
+    p.q = static_cast<const uint16_t*>(q), p.out = static_cast<uint16_t*>(out), p.lse = lse;
+    p.table = table, p.length = length, p.cu = cu, p.k_scales = c.k_scales, p.v_scales = c.v_scales;
+    p.meta = static_cast<int4*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.meta + 2 * shares);
+    p.part_o = reinterpret_cast<float*>(p.part_ml + 2 * (size_t)shares * a.R);
+    p.q_t = s.q_t, p.q_h = s.q_h, p.T = s.T, p.pages = c.pages;
+    p.B = (int)s.B, p.width = (int)s.table_width, p.page = c.page, p.page_shift = __builtin_ctz(c.page);
+    p.block_shift = __builtin_ctz(c.block), p.marks = c.page / c.block, p.H = c.H, p.Hq = s.Hq, p.group = s.Hq / c.H;
+    p.per_seq = (p.group + a.R - 1) / a.R;
+    p.slots = cu ? s.T * p.group / a.R + s.B : s.B * p.per_seq;
+    p.Dk = c.Dk, p.Dv = c.Dv, p.nk = a.nk, p.nv = a.nv, p.ring = a.ring, p.tmem_cols = a.tmem_cols;
+    p.q_vec = aligned(q, 16) && s.q_t % 8 == 0 && s.q_h % 8 == 0;
+    p.scale_log2 = s.scale * 1.44269504088896341f;
+    p.status = dev_status;
+    const uint32_t box = c.page < kTokens ? c.page : kTokens;
+    CUtensorMap km, vm;
+    int ms = make_tmap_pages(&km, c.k, c.Dk, c.page, c.H, c.pages, box);
+    if (ms != MLA_OK) return ms;
+    vm = km;
+    if (!shared) ms = make_tmap_pages(&vm, c.v, c.Dv, c.page, c.H, c.pages, box);
+    if (ms != MLA_OK) return ms;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (shared)
+        return a.R == 8    ? launch_attn<8, true>(p, a, km, vm, shares, cs)
+               : a.R == 16 ? launch_attn<16, true>(p, a, km, vm, shares, cs)
+               : a.R == 32 ? launch_attn<32, true>(p, a, km, vm, shares, cs)
+                           : launch_attn<64, true>(p, a, km, vm, shares, cs);
+    return a.R == 8    ? launch_attn<8, false>(p, a, km, vm, shares, cs)
+           : a.R == 16 ? launch_attn<16, false>(p, a, km, vm, shares, cs)
+           : a.R == 32 ? launch_attn<32, false>(p, a, km, vm, shares, cs)
+                       : launch_attn<64, false>(p, a, km, vm, shares, cs);
+}
+
+}  // extern "C"

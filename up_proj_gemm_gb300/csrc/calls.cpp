@@ -17,6 +17,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdint>
 #include <vector>
 
@@ -29,6 +30,13 @@ decltype(&mla_rope_axes_table) rope_axes_table_fn;
 decltype(&mla_gated_ffn_fwd) ffn_fwd_fn;
 decltype(&mla_gated_ffn_bwd) ffn_bwd_fn;
 decltype(&mla_adamw_step) adamw_step_fn;
+decltype(&mla_rms_norm_fwd) norm_fwd_fn;
+decltype(&mla_rms_norm_bwd) norm_bwd_fn;
+decltype(&mla_rms_norm_bwd_workspace_size) norm_bwd_size_fn;
+decltype(&mla_kv_cache_write) cache_write_fn;
+decltype(&mla_kv_cache_read) cache_read_fn;
+decltype(&mla_cache_attn) attn_fn;
+decltype(&mla_cache_attn_workspace_size) attn_size_fn;
 
 // load(path): the library whose entry points are called.
 PyObject* load(PyObject*, PyObject* path) {
@@ -42,7 +50,10 @@ PyObject* load(PyObject*, PyObject* path) {
     };
     if (!get(rope_axes_fn, "mla_rope_axes") || !get(rope_axes_table_fn, "mla_rope_axes_table") ||
         !get(ffn_fwd_fn, "mla_gated_ffn_fwd") || !get(ffn_bwd_fn, "mla_gated_ffn_bwd") ||
-        !get(adamw_step_fn, "mla_adamw_step"))
+        !get(adamw_step_fn, "mla_adamw_step") || !get(norm_fwd_fn, "mla_rms_norm_fwd") ||
+        !get(norm_bwd_fn, "mla_rms_norm_bwd") || !get(norm_bwd_size_fn, "mla_rms_norm_bwd_workspace_size") ||
+        !get(cache_write_fn, "mla_kv_cache_write") || !get(cache_read_fn, "mla_kv_cache_read") ||
+        !get(attn_fn, "mla_cache_attn") || !get(attn_size_fn, "mla_cache_attn_workspace_size"))
         return PyErr_Format(PyExc_RuntimeError, "%s lacks an entry point", p);
     Py_RETURN_NONE;
 }
@@ -271,6 +282,209 @@ PyObject* adamw_keep(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// The tensors as a tuple (one: itself); they are given up.
+PyObject* wrapped(std::vector<at::Tensor> v) {
+    if (v.size() == 1) return THPVariable_Wrap(std::move(v[0]));
+    PyObject* r = PyTuple_New((Py_ssize_t)v.size());
+    for (size_t i = 0; r && i < v.size(); ++i) {
+        PyObject* o = nullptr;
+        if (v[i].defined()) o = THPVariable_Wrap(std::move(v[i]));
+        else Py_INCREF(o = Py_None);
+        if (!o) {
+            Py_DECREF(r);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(r, (Py_ssize_t)i, o);
+    }
+    return r;
+}
+
+// An optional tensor: false when o is neither one nor None.
+bool optional(PyObject* o, const at::Tensor*& t) {
+    t = o == Py_None ? nullptr : tensor(o);
+    return t || o == Py_None;
+}
+
+bool float_type(const at::Tensor* t) { return t->scalar_type() == at::kFloat || t->scalar_type() == at::kBFloat16; }
+int in_type(const at::Tensor* t) { return t->scalar_type() == at::kFloat ? MLA_IN_F32 : MLA_IN_BF16; }
+
+// The row pitch of a matrix like `like` (itself: null) whose rows are contiguous and do not overlap, else -1.
+int64_t norm_pitch(const at::Tensor* t, const at::Tensor* like) {
+    if (!t || !t->is_cuda() || t->dim() != 2 || !float_type(t)) return -1;
+    if (like && (t->scalar_type() != like->scalar_type() || t->sizes() != like->sizes() || t->device() != like->device()))
+        return -1;
+    const int64_t T = t->size(0), K = t->size(1);
+    if (K > 1 && t->stride(1) != 1) return -1;
+    if (T <= 1) return K;
+    return t->stride(0) >= K ? t->stride(0) : -1;
+}
+bool norm_weight(const at::Tensor* w, const at::Tensor* x) {
+    return w && float_type(w) && dense(w, w->scalar_type(), 1, x) && w->size(0) == x->size(1);
+}
+
+// rms_norm_fwd(x, weight, eps, residual, out mode, save): y, then scales, h and rstd where there are any
+PyObject* rms_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 6) Py_RETURN_NONE;
+    const at::Tensor *x = tensor(a[0]), *w = tensor(a[1]), *res;
+    const double eps = PyFloat_AsDouble(a[2]);
+    const int mode = (int)PyLong_AsLong(a[4]), save = PyObject_IsTrue(a[5]);
+    if (PyErr_Occurred()) return nullptr;
+    const int64_t ld_x = norm_pitch(x, nullptr);
+    if (ld_x < 0 || !here(*x) || !norm_weight(w, x) || !optional(a[3], res)) Py_RETURN_NONE;
+    const int64_t T = x->size(0), K = x->size(1), ld_res = res ? norm_pitch(res, x) : 0;
+    if (ld_res < 0) Py_RETURN_NONE;
+    const bool mx = mode != MLA_NORM_OUT_SAME;
+    if (mx && K % 32 != 0) Py_RETURN_NONE;
+    std::vector<at::Tensor> v;
+    const auto bytes = x->options().dtype(at::kByte);
+    v.push_back(at::empty({T, K}, mx ? bytes : x->options()));
+    if (mode == MLA_NORM_OUT_MXFP8) v.push_back(at::empty({T, K / 32}, bytes));
+    if (mode == MLA_NORM_OUT_MXFP8_TILED) v.push_back(at::empty({(T + 127) / 128 * ((K / 32 + 3) / 4) * 512}, bytes));
+    void *scales = mx ? v[1].data_ptr() : nullptr, *h = nullptr;
+    float* rstd = nullptr;
+    if (res) {
+        v.push_back(at::empty({T, K}, x->options()));
+        h = v.back().data_ptr();
+    }
+    if (save) {
+        v.push_back(at::empty({T}, x->options().dtype(at::kFloat)));
+        rstd = v.back().data_ptr<float>();
+    }
+    const mla_norm_shape s{T, K, ld_x, ld_res, 0, in_type(x), in_type(w), mode, (float)eps, 0};
+    if (norm_fwd_fn(&s, x->data_ptr(), res ? res->data_ptr() : nullptr, w->data_ptr(), h, v[0].data_ptr(),
+                    static_cast<uint8_t*>(scales), rstd, stream_of(*x)) != MLA_OK)
+        Py_RETURN_NONE;
+    return wrapped(std::move(v));
+    END_HANDLE_TH_ERRORS
+}
+
+// rms_norm_bwd(dy, h, weight, rstd, dres): both gradients
+PyObject* rms_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 5) Py_RETURN_NONE;
+    const at::Tensor *dy = tensor(a[0]), *h = tensor(a[1]), *w = tensor(a[2]), *rstd = tensor(a[3]), *dres;
+    const int64_t ld_x = norm_pitch(h, nullptr);
+    if (ld_x < 0 || !here(*h) || !norm_weight(w, h) || !dense(rstd, at::kFloat, 1, h) || !optional(a[4], dres))
+        Py_RETURN_NONE;
+    const int64_t T = h->size(0), K = h->size(1), ld_dy = norm_pitch(dy, h), ld_res = dres ? norm_pitch(dres, h) : 0;
+    if (ld_dy < 0 || ld_res < 0 || rstd->size(0) != T) Py_RETURN_NONE;
+    const mla_norm_shape s{T, K, ld_x, ld_res, ld_dy, in_type(h), in_type(w), MLA_NORM_OUT_SAME, 0.f, 0};
+    const int64_t size = (int64_t)norm_bwd_size_fn(&s);
+    at::Tensor dx = at::empty({T, K}, h->options()), dw = at::empty({K}, w->options()),
+               ws = at::empty({size}, h->options().dtype(at::kByte));
+    if (norm_bwd_fn(&s, dy->data_ptr(), h->data_ptr(), w->data_ptr(), rstd->data_ptr<float>(),
+                    dres ? dres->data_ptr() : nullptr, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), (size_t)size,
+                    stream_of(*h)) != MLA_OK)
+        Py_RETURN_NONE;
+    return wrapped({dx, dw});
+    END_HANDLE_TH_ERRORS
+}
+
+// The cache of a[0..4]: k, k_scales, v, v_scales, Dv. False when it is not one on the current device.
+bool cache_args(PyObject* const* a, mla_kv_cache& c, const at::Tensor*& k) {
+    const at::Tensor *ks = tensor(a[1]), *v, *vs;
+    k = tensor(a[0]);
+    if (!dense(k, at::kByte, 4, nullptr) || !here(*k) || !dense(ks, at::kByte, 3, k) || !optional(a[2], v) ||
+        !optional(a[3], vs) || !v != !vs)
+        return false;
+    const int64_t pages = k->size(0), H = k->size(1), page = k->size(2), Dk = k->size(3), per = ks->size(2);
+    const int64_t Dv = PyLong_AsLongLong(a[4]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return false;
+    }
+    if (ks->size(0) != pages || ks->size(1) != H || per < 1 || page < 16 || page > 1024 || page % per != 0 || H > 65535 ||
+        Dk > 4096 || Dv < 1 || Dv > 4096)
+        return false;
+    if (v && (!dense(v, at::kByte, 4, k) || v->size(0) != pages || v->size(1) != H || v->size(2) != page ||
+              v->size(3) != Dv || !dense(vs, at::kByte, 3, k) || vs->sizes() != ks->sizes()))
+        return false;
+    c = {pages, (int32_t)page, (int32_t)(page / per), (int32_t)H, (int32_t)Dk, (int32_t)Dv, 0,
+         static_cast<uint8_t*>(k->data_ptr()), static_cast<uint8_t*>(ks->data_ptr()),
+         v ? static_cast<uint8_t*>(v->data_ptr()) : nullptr, vs ? static_cast<uint8_t*>(vs->data_ptr()) : nullptr};
+    return true;
+}
+
+// table [B, width], positions [B], cu [B + 1] or None, for T rows.
+bool sequence_args(const at::Tensor* table, const at::Tensor* at, const at::Tensor* cu, int64_t T, const at::Tensor* like) {
+    return dense(table, at::kInt, 2, like) && dense(at, at::kInt, 1, like) && at->size(0) == table->size(0) &&
+           (cu ? dense(cu, at::kInt, 1, like) && cu->size(0) == table->size(0) + 1 : T == table->size(0));
+}
+
+// bf16 rows [T, H, D] with unit inner stride
+bool rows3(const at::Tensor* t, int64_t H, int64_t D, const at::Tensor* like) {
+    return t && t->scalar_type() == at::kBFloat16 && t->dim() == 3 && t->size(1) == H && t->size(2) == D && t->is_cuda() &&
+           t->device() == like->device() && (D <= 1 || t->stride(2) == 1);
+}
+int64_t token_stride(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : 0; }
+int64_t head_stride(const at::Tensor& t) { return t.size(1) > 1 ? t.stride(1) : 0; }
+const int32_t* ints(const at::Tensor* t) { return t ? t->data_ptr<int32_t>() : nullptr; }
+
+// kv_cache_write(the cache's five, k, v, table, start, cu): True
+PyObject* kv_cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 10) Py_RETURN_NONE;
+    mla_kv_cache c;
+    const at::Tensor *ck, *k = tensor(a[5]), *v, *table = tensor(a[7]), *start = tensor(a[8]), *cu;
+    if (!cache_args(a, c, ck) || !rows3(k, c.H, c.Dk, ck) || !optional(a[6], v) || !optional(a[9], cu) || !v != !c.v)
+        Py_RETURN_NONE;
+    const int64_t T = k->size(0);
+    if ((v && (!rows3(v, c.H, c.Dv, ck) || v->size(0) != T)) || !sequence_args(table, start, cu, T, ck)) Py_RETURN_NONE;
+    if (cache_write_fn(&c, k->data_ptr(), token_stride(*k), head_stride(*k), v ? v->data_ptr() : nullptr,
+                       v ? token_stride(*v) : 0, v ? head_stride(*v) : 0, T, table->size(0), ints(table), table->size(1),
+                       ints(start), ints(cu), nullptr, stream_of(*ck)) != MLA_OK)
+        Py_RETURN_NONE;
+    Py_RETURN_TRUE;
+    END_HANDLE_TH_ERRORS
+}
+
+// kv_cache_read(the cache's five, table, start, tokens, cu, dtype): (k, v or None)
+PyObject* kv_cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 10) Py_RETURN_NONE;
+    mla_kv_cache c;
+    const at::Tensor *ck, *table = tensor(a[5]), *start = tensor(a[6]), *cu;
+    const int64_t T = PyLong_AsLongLong(a[7]);
+    const int dtype = (int)PyLong_AsLong(a[9]);
+    if (PyErr_Occurred()) return nullptr;
+    if (!cache_args(a, c, ck) || !optional(a[8], cu) || T < 0 || !sequence_args(table, start, cu, T, ck)) Py_RETURN_NONE;
+    const auto o = ck->options().dtype(dtype == MLA_IN_F32 ? at::kFloat : at::kBFloat16);
+    at::Tensor k = at::empty({T, c.H, c.Dk}, o), v;
+    if (c.v) v = at::empty({T, c.H, c.Dv}, o);
+    if (cache_read_fn(&c, k.data_ptr(), c.v ? v.data_ptr() : nullptr, dtype, T, table->size(0), ints(table),
+                      table->size(1), ints(start), ints(cu), nullptr, stream_of(*ck)) != MLA_OK)
+        Py_RETURN_NONE;
+    return wrapped({k, v});
+    END_HANDLE_TH_ERRORS
+}
+
+// cache_attn(q, the cache's five, table, length, cu, scale (NaN: Dk^-1/2), lse): out or (out, lse)
+PyObject* cache_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 11) Py_RETURN_NONE;
+    mla_kv_cache c;
+    const at::Tensor *q = tensor(a[0]), *ck, *table = tensor(a[6]), *length = tensor(a[7]), *cu;
+    double scale = PyFloat_AsDouble(a[9]);
+    const int want = PyObject_IsTrue(a[10]);
+    if (PyErr_Occurred()) return nullptr;
+    if (!cache_args(a + 1, c, ck) || !optional(a[8], cu) || !q || q->dim() != 3 || !rows3(q, q->size(1), c.Dk, ck) ||
+        q->size(1) < 1 || q->size(1) > INT32_MAX || !sequence_args(table, length, cu, q->size(0), ck))
+        Py_RETURN_NONE;
+    if (scale != scale) scale = 1.0 / std::sqrt((double)c.Dk);
+    const int64_t T = q->size(0), Hq = q->size(1);
+    const mla_attn_shape s{T, table->size(0), token_stride(*q), head_stride(*q), table->size(1), (int32_t)Hq, (float)scale, 0};
+    const int64_t size = (int64_t)attn_size_fn(&s, &c);
+    at::Tensor out = at::empty({T, Hq, c.Dv}, q->options()), lse, ws = at::empty({size}, ck->options());
+    if (want) lse = at::empty({T, Hq}, q->options().dtype(at::kFloat));
+    if (attn_fn(&s, &c, q->data_ptr(), ints(table), ints(length), ints(cu), out.data_ptr(),
+                want ? lse.data_ptr<float>() : nullptr, ws.data_ptr(), (size_t)size, nullptr, stream_of(*ck)) != MLA_OK)
+        Py_RETURN_NONE;
+    if (!want) return wrapped({out});
+    return wrapped({out, lse});
+    END_HANDLE_TH_ERRORS
+}
+
 PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
 }
@@ -284,6 +498,11 @@ PyMethodDef methods[] = {
     {"adamw_step", fast(adamw_step), METH_FASTCALL, nullptr},
     {"adamw_places", fast(adamw_places), METH_FASTCALL, nullptr},
     {"adamw_keep", fast(adamw_keep), METH_FASTCALL, nullptr},
+    {"rms_norm_fwd", fast(rms_norm_fwd), METH_FASTCALL, nullptr},
+    {"rms_norm_bwd", fast(rms_norm_bwd), METH_FASTCALL, nullptr},
+    {"kv_cache_write", fast(kv_cache_write), METH_FASTCALL, nullptr},
+    {"kv_cache_read", fast(kv_cache_read), METH_FASTCALL, nullptr},
+    {"cache_attn", fast(cache_attn), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -39,6 +39,12 @@ int make_tmap_chunks(void* tmap_out, const void* base, uint64_t rows, uint64_t c
 int make_tmap_3d(void* tmap_out, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
                  uint64_t stride2, uint32_t b0, uint32_t b1, uint32_t b2, bool swizzle64 = false);
 
+// 4-D view of a cache's codes [pages, H, page, D] (bytes): dims {D, page, H,
+// pages}, box {128, box_rows, 1, 1}, 128-byte swizzle; channels and pages past
+// the tensor read as zeros.
+int make_tmap_pages(void* tmap_out, const void* base, uint64_t D, uint64_t page, uint64_t H, uint64_t pages,
+                    uint32_t box_rows);
+
 // ------------------------------------------------------------- launchers
 // All launchers assume arguments were validated by the API layer.
 int launch_mxfp8_swizzle(int64_t rows, int64_t cols, int64_t group, const uint8_t* in, int64_t ld, uint8_t* out,

@@ -1,0 +1,526 @@
+// RMS norm of token rows, with the residual's addition in front of it and an
+// MXFP8 result for the block-scaled projections behind it:
+//   h = x + r,  rstd = (mean_k h_k^2 + eps)^(-1/2),  y_k = h_k rstd w_k
+// and its gradient, with g = dy w and the normed row n = h rstd,
+//   dx = rstd (g - n mean_k(g_k n_k)) + dh,   dw = sum_t dy n.
+// Sums are float32; y is made of the unrounded sum x + r, and each result is
+// rounded once, at its store.
+//
+// All of it is bound by HBM: a row is read once and stays in registers, eight
+// channels to a granule, granule j of thread i at (j * threads + i) * 8. A row
+// belongs to a warp (no barrier; several rows in flight per block) or to a
+// block; a thread's weights stay in its registers for all of its rows.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "checks.h"
+#include "internal.h"
+#include "launch.cuh"
+#include "mx.cuh"
+#include "ptx.cuh"
+
+namespace mlaq {
+namespace {
+
+constexpr int kG = 8;                // channels of a granule
+constexpr int64_t kMaxK = 32768;     // 512 threads of eight granules
+constexpr int kWarpRows = 8;         // rows (warps) of a block that gives each row a warp
+
+struct NormParams {
+    const void *x, *res, *w;         // backward: h, dh, weight
+    const void* dy;
+    void *h, *y;                     // backward: y is dx
+    uint8_t* scales;
+    float* rstd;
+    float* partials;                 // backward: [blocks][K]
+    int64_t T, ld_x, ld_res, ld_dy;
+    int K;
+    int x_bf16, w_bf16, tiled, vec;
+    float eps, inv_k;
+};
+
+// Eight channels as they lie in memory: 16 bytes of bf16 or 32 of float32,
+// read and written whole where the rows start on 16 bytes (VEC), else one by one,
+// up to n of them.
+template <typename E, bool VEC>
+struct Granule {
+    uint32_t u[sizeof(E) == 2 ? 4 : 8];
+
+    __device__ __forceinline__ void load(const E* p, int n) {
+        if constexpr (VEC) {
+            const uint4 a = *reinterpret_cast<const uint4*>(p);
+            u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w;
+            if constexpr (sizeof(E) == 4) {
+                const uint4 b = *reinterpret_cast<const uint4*>(p + 4);
+                u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
+            }
+        } else if constexpr (sizeof(E) == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = 2 * i < n ? (uint32_t)p[2 * i] : 0u;
+                const uint32_t hi = 2 * i + 1 < n ? (uint32_t)p[2 * i + 1] : 0u;
+                u[i] = lo | (hi << 16);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = i < n ? __float_as_uint(p[i]) : 0u;
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (sizeof(E) == 2 ? 4 : 8); ++i) u[i] = 0u;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(E) == 4) return __uint_as_float(u[i]);
+        else return i & 1 ? bf16hi_to_f32(u[i / 2]) : bf16lo_to_f32(u[i / 2]);
+    }
+    __device__ __forceinline__ void set(const float (&v)[kG]) {
+#pragma unroll
+        for (int i = 0; i < (sizeof(E) == 2 ? 4 : 8); ++i)
+            u[i] = sizeof(E) == 2 ? pack_bf16x2(v[2 * i % kG], v[(2 * i + 1) % kG]) : __float_as_uint(v[i % kG]);
+    }
+    __device__ __forceinline__ void store(E* p, int n) const {
+        if constexpr (VEC) {
+            st_global_v4(p, u[0], u[1], u[2], u[3]);
+            if constexpr (sizeof(E) == 4) st_global_v4(p + 4, u[4], u[5], u[6], u[7]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kG; ++i)
+                if (i < n) {
+                    if constexpr (sizeof(E) == 2) p[i] = (uint16_t)(i & 1 ? u[i / 2] >> 16 : u[i / 2] & 0xFFFFu);
+                    else p[i] = __uint_as_float(u[i]);
+                }
+        }
+    }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// The sum over the threads of a row: a warp's, or (WARP false) the block's,
+// through a buffer that alternates with the row so that one barrier is enough.
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float v, float* buf, int turn) {
+    v = warp_sum(v);
+    if constexpr (WARP) return v;
+    float* b = buf + (turn & 1) * 32;
+    const int warps = blockDim.x / 32;
+    if (threadIdx.x % 32 == 0) b[threadIdx.x / 32] = v;
+    __syncthreads();
+    const int lane = threadIdx.x % 32;
+    return warp_sum(lane < warps ? b[lane] : 0.f);  // every warp the same sum, in the same order
+}
+
+// The weights of a granule, as 32-bit values (read once per thread).
+template <bool VEC>
+__device__ __forceinline__ void load_weights(const NormParams& p, int c, int n, float (&w)[kG]) {
+    if (p.w_bf16) {
+        Granule<uint16_t, VEC> g;
+        g.load(static_cast<const uint16_t*>(p.w) + c, n);
+#pragma unroll
+        for (int i = 0; i < kG; ++i) w[i] = g.get(i);
+    } else {
+        Granule<float, VEC> g;
+        g.load(static_cast<const float*>(p.w) + c, n);
+#pragma unroll
+        for (int i = 0; i < kG; ++i) w[i] = g.get(i);
+    }
+}
+
+// Threads of a block at most: with more than one granule each, half as many and twice the registers.
+template <bool WARP, int GPT>
+constexpr int kMaxThreads = WARP ? 32 * kWarpRows : GPT == 1 ? 1024 : 512;
+
+// E: x, r, h and y (bf16 as uint16_t, or float). GPT granules per thread. MX:
+// y as E4M3 codes with a scale for each 32 channels, four granules that lie
+// side by side in four lanes.
+template <typename E, int GPT, bool MX, bool VEC, bool WARP>
+__global__ void __launch_bounds__(kMaxThreads<WARP, GPT>) rms_norm_kernel(const __grid_constant__ NormParams p) {
+    __shared__ float buf[64];
+    grid_launch_next();
+    grid_wait_previous();
+    const int lanes = WARP ? 32 : (int)blockDim.x;
+    const int lane = WARP ? (int)threadIdx.x % 32 : (int)threadIdx.x;
+    const int rows = WARP ? kWarpRows : 1;
+    const int64_t step = (int64_t)gridDim.x * rows;
+    const E* x = static_cast<const E*>(p.x);
+    const E* res = static_cast<const E*>(p.res);
+    float w[GPT][kG];
+#pragma unroll
+    for (int j = 0; j < GPT; ++j) {
+        const int c = (j * lanes + lane) * kG;
+        if (c < p.K) load_weights<VEC>(p, c, p.K - c, w[j]);
+    }
+    // tiled scales: the last 128-row tile's missing rows get scale bytes of zero
+    const int64_t end = MX && p.tiled ? (p.T + 127) / 128 * 128 : p.T;
+    const int64_t nkt = (p.K / 32 + 3) / 4;
+    int turn = 0;
+    for (int64_t t = (int64_t)blockIdx.x * rows + (WARP ? threadIdx.x / 32 : 0); t < end; t += step, ++turn) {
+        if (MX && t >= p.T) {  // uniform over the row's threads
+            for (int c = lane; c < nkt * 4; c += lanes) p.scales[sf_tiled_offset(t, c, 128, nkt)] = 0;
+            continue;
+        }
+        Granule<E, VEC> raw[GPT], add[GPT];
+#pragma unroll
+        for (int j = 0; j < GPT; ++j) {
+            const int c = (j * lanes + lane) * kG;
+            raw[j].zero();
+            if (c < p.K) raw[j].load(x + t * p.ld_x + c, p.K - c);
+        }
+        if (res) {
+#pragma unroll
+            for (int j = 0; j < GPT; ++j) {
+                const int c = (j * lanes + lane) * kG;
+                add[j].zero();
+                if (c < p.K) add[j].load(res + t * p.ld_res + c, p.K - c);
+            }
+        }
+        float v[GPT][kG], sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < GPT; ++j) {
+            const int c = (j * lanes + lane) * kG;
+#pragma unroll
+            for (int i = 0; i < kG; ++i) {
+                v[j][i] = raw[j].get(i) + (res ? add[j].get(i) : 0.f);
+                sum = fmaf(v[j][i], v[j][i], sum);
+            }
+            if (res && c < p.K) {
+                raw[j].set(v[j]);
+                raw[j].store(static_cast<E*>(p.h) + t * p.K + c, p.K - c);
+            }
+        }
+        const float rstd = __frsqrt_rn(fmaf(row_sum<WARP>(sum, buf, turn), p.inv_k, p.eps));
+        if (p.rstd && lane == 0) p.rstd[t] = rstd;
+#pragma unroll
+        for (int j = 0; j < GPT; ++j) {
+            const int c = (j * lanes + lane) * kG;
+            const bool in = c < p.K;
+#pragma unroll
+            for (int i = 0; i < kG; ++i) v[j][i] = in ? v[j][i] * rstd * w[j][i] : 0.f;
+            if constexpr (MX) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < kG; ++i) m = max(m, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+                uint32_t codes[2];
+                const uint32_t s = quantize8_block_scale(v[j], m, codes);
+                if (in) {
+                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + t * p.K + c) = make_uint2(codes[0], codes[1]);
+                    if (lane % 4 == 0) {
+                        if (p.tiled) p.scales[sf_tiled_offset(t, c / 32, 128, nkt)] = (uint8_t)s;
+                        else p.scales[t * (p.K / 32) + c / 32] = (uint8_t)s;
+                    }
+                }
+            } else if (in) {
+                Granule<E, VEC> o;
+                o.set(v[j]);
+                o.store(static_cast<E*>(p.y) + t * p.K + c, p.K - c);
+            }
+        }
+        if (MX && p.tiled)  // and so the last tile's missing columns
+            for (int c = p.K / 32 + lane; c < nkt * 4; c += lanes) p.scales[sf_tiled_offset(t, c, 128, nkt)] = 0;
+    }
+}
+
+// The gradient. dw's sum over the rows stays in the threads' registers; each
+// block adds its rows' in a fixed order and leaves one partial row.
+template <typename E, int GPT, bool VEC, bool WARP>
+__global__ void __launch_bounds__(kMaxThreads<WARP, GPT>) rms_norm_bwd_kernel(const __grid_constant__ NormParams p) {
+    extern __shared__ float4 dyn[];
+    __shared__ float buf[64];
+    grid_launch_next();
+    grid_wait_previous();
+    const int lanes = WARP ? 32 : (int)blockDim.x;
+    const int lane = WARP ? (int)threadIdx.x % 32 : (int)threadIdx.x;
+    const int rows = WARP ? kWarpRows : 1;
+    const int64_t step = (int64_t)gridDim.x * rows;
+    const E* h = static_cast<const E*>(p.x);
+    const E* dh = static_cast<const E*>(p.res);
+    const E* dy = static_cast<const E*>(p.dy);
+    float w[GPT][kG], dw[GPT][kG];
+#pragma unroll
+    for (int j = 0; j < GPT; ++j) {
+        const int c = (j * lanes + lane) * kG;
+#pragma unroll
+        for (int i = 0; i < kG; ++i) w[j][i] = dw[j][i] = 0.f;
+        if (c < p.K) load_weights<VEC>(p, c, p.K - c, w[j]);
+    }
+    int turn = 0;
+    for (int64_t t = (int64_t)blockIdx.x * rows + (WARP ? threadIdx.x / 32 : 0); t < p.T; t += step, ++turn) {
+        Granule<E, VEC> a[GPT], b[GPT], d[GPT];
+#pragma unroll
+        for (int j = 0; j < GPT; ++j) {
+            const int c = (j * lanes + lane) * kG;
+            a[j].zero();
+            b[j].zero();
+            if (c < p.K) {
+                a[j].load(dy + t * p.ld_dy + c, p.K - c);
+                b[j].load(h + t * p.ld_x + c, p.K - c);
+            }
+        }
+        if (dh) {
+#pragma unroll
+            for (int j = 0; j < GPT; ++j) {
+                const int c = (j * lanes + lane) * kG;
+                d[j].zero();
+                if (c < p.K) d[j].load(dh + t * p.ld_res + c, p.K - c);
+            }
+        }
+        const float rstd = p.rstd[t];
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < GPT; ++j)
+#pragma unroll
+            for (int i = 0; i < kG; ++i) {
+                const float n = b[j].get(i) * rstd, e = a[j].get(i);
+                sum = fmaf(e * w[j][i], n, sum);
+                dw[j][i] = fmaf(e, n, dw[j][i]);
+            }
+        if (!p.y) continue;
+        const float mean = row_sum<WARP>(sum, buf, turn) * p.inv_k;
+#pragma unroll
+        for (int j = 0; j < GPT; ++j) {
+            const int c = (j * lanes + lane) * kG;
+            if (c >= p.K) continue;
+            float o[kG];
+#pragma unroll
+            for (int i = 0; i < kG; ++i) {
+                const float n = b[j].get(i) * rstd;
+                o[i] = rstd * fmaf(-n, mean, a[j].get(i) * w[j][i]) + (dh ? d[j].get(i) : 0.f);
+            }
+            a[j].set(o);
+            a[j].store(static_cast<E*>(p.y) + t * p.K + c, p.K - c);
+        }
+    }
+    if (!p.partials) return;
+    float* out = p.partials + (int64_t)blockIdx.x * p.K;
+    if constexpr (WARP) {  // the warps' sums through shared memory, [warp][K]
+        float* part = reinterpret_cast<float*>(dyn);
+#pragma unroll
+        for (int j = 0; j < GPT; ++j)
+#pragma unroll
+            for (int i = 0; i < kG; ++i) {
+                const int c = (j * lanes + lane) * kG + i;
+                if (c < p.K) part[(threadIdx.x / 32) * p.K + c] = dw[j][i];
+            }
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.K; c += blockDim.x) {
+            float s = 0.f;
+#pragma unroll
+            for (int r = 0; r < kWarpRows; ++r) s += part[r * p.K + c];
+            out[c] = s;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < GPT; ++j)
+#pragma unroll
+            for (int i = 0; i < kG; ++i) {
+                const int c = (j * lanes + lane) * kG + i;
+                if (c < p.K) out[c] = dw[j][i];
+            }
+    }
+}
+
+// dw from the blocks' partial rows: 32 columns to a block, eight threads to a
+// column, each a fixed share of the rows.
+__global__ void __launch_bounds__(256) rms_norm_dw_kernel(const float* partials, int parts, int K, int w_bf16, void* dw) {
+    __shared__ float sums[8][32];
+    grid_launch_next();
+    grid_wait_previous();
+    const int c = blockIdx.x * 32 + threadIdx.x % 32, r = threadIdx.x / 32;
+    float s = 0.f;
+    if (c < K) {
+#pragma unroll 8
+        for (int i = r; i < parts; i += 8) s += partials[(int64_t)i * K + c];
+    }
+    sums[r][threadIdx.x % 32] = s;
+    __syncthreads();
+    if (r == 0 && c < K) {
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += sums[i][threadIdx.x];
+        if (w_bf16) static_cast<uint16_t*>(dw)[c] = (uint16_t)pack_bf16x2(s, 0.f);
+        else static_cast<float*>(dw)[c] = s;
+    }
+}
+
+struct NormGrid {
+    bool warp;      // a warp to a row
+    int gpt;        // granules per thread
+    unsigned threads, blocks;
+};
+
+// How rows are shared out. Few channels: a warp to a row, as many granules per
+// lane as it takes. Else a block to a row, of one granule per thread while the rows
+// are few (latency), of two or more when they are many.
+NormGrid norm_grid(int64_t T, int64_t K, int num_sms, bool bwd) {
+    const int64_t granules = (K + kG - 1) / kG;
+    NormGrid g{};
+    const int most = bwd ? 4 : 8;
+    if (granules <= 32 || (granules <= 32 * most && T >= (int64_t)num_sms * kWarpRows)) {
+        g.warp = true;
+        g.gpt = granules <= 32 ? 1 : granules <= 64 ? 2 : granules <= 128 ? 4 : 8;
+        g.threads = 32 * kWarpRows;
+        const int64_t need = (T + kWarpRows - 1) / kWarpRows, room = (int64_t)num_sms * (bwd ? 2 : 4);
+        g.blocks = (unsigned)(need < room ? need : room);
+        return g;
+    }
+    g.gpt = granules <= 1024 && (T < 2 * num_sms || granules <= 256) ? 1 : granules <= 1024 ? 2 : granules <= 2048 ? 4 : 8;
+    g.threads = (unsigned)((granules + 32 * g.gpt - 1) / (32 * g.gpt) * 32);
+    const int per = (int)(2048 / g.threads) < 1 ? 1 : (int)(2048 / g.threads);
+    const int64_t room = (int64_t)num_sms * (bwd ? (per > 2 ? 2 : per) : (per > 8 ? 8 : per));
+    g.blocks = (unsigned)(T < room ? T : room);
+    return g;
+}
+
+template <typename E, bool MX, bool VEC>
+int launch_fwd_rows(const NormParams& p, const NormGrid& g, cudaStream_t s) {
+    const auto kernel = g.warp ? (g.gpt == 1   ? rms_norm_kernel<E, 1, MX, VEC, true>
+                                  : g.gpt == 2 ? rms_norm_kernel<E, 2, MX, VEC, true>
+                                  : g.gpt == 4 ? rms_norm_kernel<E, 4, MX, VEC, true>
+                                               : rms_norm_kernel<E, 8, MX, VEC, true>)
+                               : (g.gpt == 1   ? rms_norm_kernel<E, 1, MX, VEC, false>
+                                  : g.gpt == 2 ? rms_norm_kernel<E, 2, MX, VEC, false>
+                                  : g.gpt == 4 ? rms_norm_kernel<E, 4, MX, VEC, false>
+                                               : rms_norm_kernel<E, 8, MX, VEC, false>);
+    return launch_overlapped(kernel, g.blocks, g.threads, 0, 0, s, p);
+}
+
+template <typename E, bool VEC>
+int launch_bwd_rows(const NormParams& p, const NormGrid& g, cudaStream_t s) {
+    const auto kernel = g.warp ? (g.gpt == 1   ? rms_norm_bwd_kernel<E, 1, VEC, true>
+                                  : g.gpt == 2 ? rms_norm_bwd_kernel<E, 2, VEC, true>
+                                               : rms_norm_bwd_kernel<E, 4, VEC, true>)
+                               : (g.gpt == 1   ? rms_norm_bwd_kernel<E, 1, VEC, false>
+                                  : g.gpt == 2 ? rms_norm_bwd_kernel<E, 2, VEC, false>
+                                  : g.gpt == 4 ? rms_norm_bwd_kernel<E, 4, VEC, false>
+                                               : rms_norm_bwd_kernel<E, 8, VEC, false>);
+    const size_t smem = g.warp && p.partials ? (size_t)kWarpRows * p.K * sizeof(float) : 0;
+    return launch_overlapped(kernel, g.blocks, g.threads, smem, 0, s, p);
+}
+
+// What forward and backward check alike; *p gets the sizes.
+int check_norm(const mla_norm_shape* s, NormParams* p) {
+    if (!s) return MLA_ERR_INVALID_ARG;
+    if (s->T < 0 || s->K <= 0 || s->T > kI32Max || s->K > kI32Max || s->reserved != 0) return MLA_ERR_INVALID_ARG;
+    if ((s->dtype != MLA_IN_F32 && s->dtype != MLA_IN_BF16) || (s->w_dtype != MLA_IN_F32 && s->w_dtype != MLA_IN_BF16))
+        return MLA_ERR_INVALID_ARG;
+    if (!(s->eps >= 0.f) || s->eps > 3.402823466e38f) return MLA_ERR_INVALID_ARG;
+    for (const int64_t ld : {s->ld_x, s->ld_res, s->ld_dy})
+        if (ld != 0 && (ld < s->K || !inside(s->T, ld))) return MLA_ERR_INVALID_ARG;
+    p->T = s->T;
+    p->K = (int)s->K;
+    p->ld_x = s->ld_x ? s->ld_x : s->K;
+    p->ld_res = s->ld_res ? s->ld_res : s->K;
+    p->ld_dy = s->ld_dy ? s->ld_dy : s->K;
+    p->x_bf16 = s->dtype == MLA_IN_BF16;
+    p->w_bf16 = s->w_dtype == MLA_IN_BF16;
+    p->eps = s->eps;
+    p->inv_k = 1.f / (float)s->K;
+    if (s->K > kMaxK) return MLA_ERR_UNSUPPORTED;
+    return MLA_OK;
+}
+
+int64_t span(int64_t T, int64_t ld, int64_t K, int64_t size) { return T > 0 ? ((T - 1) * ld + K) * size : 0; }
+
+}  // namespace
+}  // namespace mlaq
+
+using namespace mlaq;
+
+extern "C" {
+
+MLAQ_API int mla_rms_norm_fwd(const mla_norm_shape* shape, const void* x, const void* residual, const void* weight,
+                              void* h, void* y, uint8_t* y_scales, float* rstd, void* stream) {
+    NormParams p{};
+    const int st = check_norm(shape, &p);
+    if (st != MLA_OK && st != MLA_ERR_UNSUPPORTED) return st;
+    const mla_norm_shape& s = *shape;
+    if (s.out_mode < MLA_NORM_OUT_SAME || s.out_mode > MLA_NORM_OUT_MXFP8_TILED) return MLA_ERR_INVALID_ARG;
+    const bool mx = s.out_mode != MLA_NORM_OUT_SAME;
+    if ((residual != nullptr) != (h != nullptr) || mx != (y_scales != nullptr) || !weight) {
+        if (s.T > 0 || !weight) return MLA_ERR_INVALID_ARG;
+    }
+    if (s.T > 0 && (!x || !y)) return MLA_ERR_INVALID_ARG;
+    if (mx && s.K % 32 != 0) return MLA_ERR_UNSUPPORTED;
+    if (st != MLA_OK) return st;
+    const int64_t size = p.x_bf16 ? 2 : 4, wsize = p.w_bf16 ? 2 : 4, n = s.T * s.K;
+    if (!aligned(x, size) || !aligned(residual, size) || !aligned(h, size) || !aligned(weight, wsize) ||
+        !aligned(rstd, 4) || !aligned(y, mx ? 8 : size))
+        return MLA_ERR_ALIGNMENT;
+    const bool tiled = s.out_mode == MLA_NORM_OUT_MXFP8_TILED;
+    const int64_t marks = tiled ? sf_tiled_bytes(s.T, s.K / 32, 128) : n / 32;
+    const Range outs[] = {rng(h, n * size), rng(y, mx ? n : n * size), rng(y_scales, marks), rng(rstd, s.T * 4)};
+    const Range ins[] = {rng(x, span(s.T, p.ld_x, s.K, size)), rng(residual, span(s.T, p.ld_res, s.K, size)),
+                         rng(weight, s.K * wsize)};
+    if (any_alias(outs, ins)) return MLA_ERR_ALIAS;
+    if (s.T == 0) return MLA_OK;
+    DeviceInfo di;
+    const int ds = current_device_info(&di);
+    if (ds != MLA_OK) return ds;
+    p.x = x, p.res = residual, p.w = weight, p.h = h, p.y = y, p.scales = y_scales, p.rstd = rstd, p.tiled = tiled;
+    const int64_t ve = 16 / size;
+    const bool vec = s.K % kG == 0 && aligned(x, 16) && aligned(residual, 16) && aligned(weight, 16) &&
+                     aligned(h, 16) && (mx || aligned(y, 16)) && p.ld_x % ve == 0 && p.ld_res % ve == 0;
+    const NormGrid g = norm_grid(s.T, s.K, di.num_sms, false);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (p.x_bf16)
+        return mx ? (vec ? launch_fwd_rows<uint16_t, true, true>(p, g, cs) : launch_fwd_rows<uint16_t, true, false>(p, g, cs))
+                  : (vec ? launch_fwd_rows<uint16_t, false, true>(p, g, cs) : launch_fwd_rows<uint16_t, false, false>(p, g, cs));
+    return mx ? (vec ? launch_fwd_rows<float, true, true>(p, g, cs) : launch_fwd_rows<float, true, false>(p, g, cs))
+              : (vec ? launch_fwd_rows<float, false, true>(p, g, cs) : launch_fwd_rows<float, false, false>(p, g, cs));
+}
+
+MLAQ_API size_t mla_rms_norm_bwd_workspace_size(const mla_norm_shape* shape) {
+    NormParams p{};
+    DeviceInfo di;
+    if (check_norm(shape, &p) != MLA_OK || current_device_info(&di) != MLA_OK) return 0;
+    return (size_t)norm_grid(p.T, p.K, di.num_sms, true).blocks * p.K * sizeof(float);
+}
+
+MLAQ_API int mla_rms_norm_bwd(const mla_norm_shape* shape, const void* dy, const void* h, const void* weight,
+                              const float* rstd, const void* dh, void* dx, void* dw, void* workspace, size_t ws_bytes,
+                              void* stream) {
+    NormParams p{};
+    const int st = check_norm(shape, &p);
+    if (st != MLA_OK && st != MLA_ERR_UNSUPPORTED) return st;
+    const mla_norm_shape& s = *shape;
+    if (s.out_mode != MLA_NORM_OUT_SAME || (!dx && !dw) || !weight || (dh && !dx)) return MLA_ERR_INVALID_ARG;
+    if (s.T > 0 && (!dy || !h || !rstd)) return MLA_ERR_INVALID_ARG;
+    if (st != MLA_OK) return st;
+    const int64_t size = p.x_bf16 ? 2 : 4, wsize = p.w_bf16 ? 2 : 4, n = s.T * s.K;
+    if (!aligned(dy, size) || !aligned(h, size) || !aligned(dh, size) || !aligned(dx, size) || !aligned(weight, wsize) ||
+        !aligned(dw, wsize) || !aligned(rstd, 4) || !aligned(workspace, 16))
+        return MLA_ERR_ALIGNMENT;
+    const Range outs[] = {rng(dx, n * size), rng(dw, s.K * wsize), rng(workspace, (int64_t)ws_bytes)};
+    const Range ins[] = {rng(dy, span(s.T, p.ld_dy, s.K, size)), rng(h, span(s.T, p.ld_x, s.K, size)),
+                         rng(dh, span(s.T, p.ld_res, s.K, size)), rng(weight, s.K * wsize), rng(rstd, s.T * 4)};
+    if (any_alias(outs, ins)) return MLA_ERR_ALIAS;
+    if (s.T == 0 && !dw) return MLA_OK;
+    DeviceInfo di;
+    const int ds = current_device_info(&di);
+    if (ds != MLA_OK) return ds;
+    const NormGrid g = norm_grid(s.T, s.K, di.num_sms, true);
+    if (dw && (ws_bytes < (size_t)g.blocks * s.K * sizeof(float) || (g.blocks > 0 && !workspace))) return MLA_ERR_WORKSPACE;
+    p.x = h, p.res = dh, p.w = weight, p.dy = dy, p.y = dx, p.rstd = const_cast<float*>(rstd);
+    p.partials = dw ? static_cast<float*>(workspace) : nullptr;
+    const int64_t ve = 16 / size;
+    const bool vec = s.K % kG == 0 && aligned(dy, 16) && aligned(h, 16) && aligned(dh, 16) && aligned(weight, 16) &&
+                     aligned(dx, 16) && p.ld_x % ve == 0 && p.ld_res % ve == 0 && p.ld_dy % ve == 0;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (s.T > 0) {
+        const int r = p.x_bf16 ? (vec ? launch_bwd_rows<uint16_t, true>(p, g, cs) : launch_bwd_rows<uint16_t, false>(p, g, cs))
+                               : (vec ? launch_bwd_rows<float, true>(p, g, cs) : launch_bwd_rows<float, false>(p, g, cs));
+        if (r != MLA_OK) return r;
+    }
+    if (!dw) return MLA_OK;
+    return launch_overlapped(rms_norm_dw_kernel, (unsigned)((s.K + 31) / 32), 256, 0, 0, cs, p.partials, (int)g.blocks,
+                             p.K, p.w_bf16, dw);
+}
+
+}  // extern "C"
