@@ -31,6 +31,8 @@
 // the parts in the order of the shares.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "cache.cuh"
 #include "internal.h"
 #include "launch.cuh"
@@ -40,12 +42,20 @@ namespace {
 
 constexpr int kTokens = 128;           // tokens of a tile
 constexpr uint32_t kChunk = 16384;     // 128 tokens x 128 channels
-constexpr int kSoftmax = 128;          // threads of the softmax warps (0-3); warp 4 loads, warp 5 issues the products
-constexpr int kThreads = 192;
+constexpr int kSoftWarps = 8;          // softmax warps; behind them one that loads codes, one that issues the products
+constexpr int kLoader = 8, kIssuer = 9, kMarker = 10;  // and one that loads scales
+constexpr int kSoftmax = 32 * kSoftWarps, kThreads = kSoftmax + 96;
+constexpr int kMarkTiles = 8;          // tiles whose scales are in shared memory
+// Four softmax warps hold a tile's tokens, a token to a thread. With few query rows
+// a tile is a chain of waits, and the two fours take turns (two streams, each with
+// its own references, sums and O, joined in the end); with many it is arithmetic,
+// and they halve the rows.
+template <int R>
+constexpr int kStreams = R <= 16 ? 2 : 1;
 constexpr float kPass = 4.f;           // log2 of how far scores may pass the reference
 constexpr float kNothing = -3.0e38f;   // the reference of a row that has seen nothing
 constexpr int kNoScale = -1000;
-constexpr int kHeldSeqs = 512;         // sequences whose lengths fit into shared memory
+constexpr int kHeldSeqs = 256;         // sequences whose lengths are held in shared memory
 constexpr int kMaxQueryChunks = 5;
 constexpr int kCombineThreads = 256;
 
@@ -80,8 +90,21 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
 }
 // kind::f8f6f4, E4M3 x E4M3, f32 sums (the fields of idesc_bf16, formats 0)
-__host__ __device__ constexpr uint32_t idesc_f8(uint32_t M, uint32_t N, uint32_t a_mn_major) {
-    return (1u << 4) | (a_mn_major << 15) | ((N >> 3) << 17) | ((M >> 4) << 24);
+__host__ __device__ constexpr uint32_t idesc_f8(uint32_t M, uint32_t N, uint32_t mn_major) {
+    return (1u << 4) | (mn_major << 15) | (mn_major << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+// The probabilities: MN-major without swizzle, [16 query rows of one block][token] of 16 bytes: 8 tokens are a core
+// matrix of 128 bytes, the next 8 the next; blocks are 128 tokens apart. A thread stores its token's bytes whole.
+__device__ __forceinline__ uint64_t desc_weights(uint32_t saddr) { return smem_desc(saddr, 128, 2048, kLayoutNone); }
+// A descriptor `bytes` further on. They are built once and added to: an MMA whose descriptors were built in front of it
+// took the issuing thread 170 clocks, so 48 (N <= 64) to 68 (N = 128).
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
+    return (desc & 0xFFFFFFFF00000000ull) | (uint32_t)((uint32_t)desc + (bytes >> 4));
+}
+// mbar_wait with its long way out of line: some thirty waits share the instruction cache with the loop over the tiles.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort) { return mbar_wait(bar, parity, abort); }
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort);
 }
 __device__ __forceinline__ void tma_load_page(uint32_t dst, const void* map, int c, int place, int h, int page,
                                               uint32_t bar) {
@@ -105,18 +128,57 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// The largest of the warp's values (NaN counts for nothing).
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// Two f32 operations in one instruction.
+__device__ __forceinline__ void fma2(float& r0, float& r1, float a0, float a1, float b0, float b1, float c0, float c1) {
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r0), "=f"(r1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mul2(float& r0, float& r1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r0), "=f"(r1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void add2(float& r0, float& r1, float a0, float a1) {
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(r0), "+f"(r1)
+        : "f"(a0), "f"(a1));
+}
+// Two weights (up to 256) as two E4M3 numbers each: hi, and 32 times what it leaves, by way of f16 (eleven bits, of
+// which the two keep eight). The first in bits 0-7.
+__device__ __forceinline__ void split_weights(float x, float y, uint32_t& hi, uint32_t& lo) {
+    uint16_t a, b;
+    asm("{\n\t.reg .b32 w, h, d, k;\n\t"
+        "cvt.rn.f16x2.f32 w, %3, %2;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 %0, w;\n\t"
+        "cvt.rn.f16x2.e4m3x2 h, %0;\n\t"
+        "sub.rn.f16x2 d, w, h;\n\t"
+        "mov.b32 k, 0x50005000;\n\t"  // 32, 32
+        "mul.rn.f16x2 d, d, k;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 %1, d;\n\t}"
+        : "=&h"(a), "=h"(b)
+        : "f"(x), "f"(y));
+    hi = a;
+    lo = b;
 }
 __device__ __forceinline__ float warp_add(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
-}
-__device__ __forceinline__ void sts_b8(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared.b8 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
 }
 __device__ __forceinline__ void sts_v2(uint32_t addr, uint32_t a, uint32_t b) {
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
@@ -216,29 +278,35 @@ struct Ring {
 template <int R>
 struct Shared {  // behind the ring, the queries and the probabilities
     uint64_t full[14], empty[14];
-    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, drain;
-    int64_t row_at[2][R];       // row of out, by the piece's parity
-    float2 row[2][R];           // (2^-exponent of the query row, reference)
-    int limit[2][R];            // the last position that a row sees
-    float factor[R];
-    float warp_row[4][R];
-    int warp_e[4];
-    int vote[3];
-    int top_e, nan_seen;
+    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], m_full[kMarkTiles], m_empty[kMarkTiles], q_full, drain;
+    uint32_t marks[kMarkTiles][kTokens / 4][2];  // scale bytes of four tokens: keys', values'
+    // query rows, by the piece's parity
+    int64_t row_at[2][R];                        // row of out
+    alignas(16) float unit[2][R];                // 2^-exponent of the row
+    int limit[2][R];                             // the last position that it sees
+    // by stream
+    alignas(16) float ref[2][kStreams<R>][R];    // reference of the row's scores (and the piece's parity)
+    float factor[kStreams<R>][R];
+    float warp_row[kStreams<R>][4][R];
+    int warp_e[kStreams<R>][4];
+    int top_e[kStreams<R>];
+    int vote[kStreams<R>][3];
+    int nan_seen, leave;
     uint32_t tmem;
     volatile int abort;
-    int64_t scan[8];
+    int64_t scan[kThreads / 32 + 1];
     int64_t start_slot;
     int start_b, start_off;
-    int nan_at[512];            // by channel: the first position with a NaN that not every row sees
+    int nan_at[512];                             // by channel: the first position with a NaN that not every row sees
     int32_t length[kHeldSeqs], cu[kHeldSeqs + 1];
 };
+static_assert(sizeof(Shared<32>) <= 10240, "latents of five chunks: two tiles, the queries and the rest fill shared memory");
 
 template <int R, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                       const __grid_constant__ AttnParams p) {
-    constexpr int N2 = 2 * R;
+    constexpr int N2 = 2 * R, kStreams = mlaq::kStreams<R>, kFour = kSoftWarps / kStreams;  // kFour: warps of a stream
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -248,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
     const uint32_t s_full = smem_u32(&sh.s_full[0]), s_empty = smem_u32(&sh.s_empty[0]);
     const uint32_t p_full = smem_u32(&sh.p_full[0]), p_empty = smem_u32(&sh.p_empty[0]);
+    const uint32_t m_full = smem_u32(&sh.m_full[0]), m_empty = smem_u32(&sh.m_empty[0]);
     const uint32_t q_full = smem_u32(&sh.q_full), drain = smem_u32(&sh.drain);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort_flag = &sh.abort;
@@ -259,21 +328,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(s_empty + 8 * i, 4);
-            mbar_init(p_full + 8 * i, 4);
+            mbar_init(s_empty + 8 * i, kFour);
+            mbar_init(p_full + 8 * i, kFour);
             mbar_init(p_empty + 8 * i, 1);
         }
-        mbar_init(q_full, 4);
+        for (int i = 0; i < kMarkTiles; ++i) {
+            mbar_init(m_full + 8 * i, 32);
+            mbar_init(m_empty + 8 * i, kFour);
+        }
+        mbar_init(q_full, kSoftWarps);
         mbar_init(drain, 1);
         sh.abort = 0;
-        sh.vote[0] = sh.vote[1] = sh.vote[2] = 0;
-        sh.nan_seen = 0;
+        for (int i = 0; i < kStreams; ++i) sh.vote[i][0] = sh.vote[i][1] = sh.vote[i][2] = 0;
+        sh.nan_seen = sh.leave = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&k_map);
         if (!SHARED) tma_prefetch_desc(&v_map);
     }
     __syncwarp();
-    if (warp == 5) {
+    if (warp == kIssuer) {
         tmem_alloc(smem_u32(&sh.tmem), p.tmem_cols);
         tmem_relinquish();
     }
@@ -362,53 +435,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     int parts = 0;  // thread 0: which of the share's two places in the workspace it has filled
     const uint32_t s_tmem = tmem, o_tmem = tmem + 2 * N2;
 
-    if (warp == 4) {
+    if (warp == kLoader) {
         // ---------------------------------------------------------- producer
         // tile t's keys, then tile t - 1's values: the order in which they are used
         Ring ring;
         int filled = 0;
         bool ok = true;
         const int box = p.page < kTokens ? p.page : kTokens, boxes = kTokens / box;
-        auto load = [&](const CUtensorMap* map, const Slot& x, int h, int tile, int chunks) {
+        struct Tile {  // this lane's box of a tile: its page's entry of the table; the tile's first place in its page
+            int entry, place, h;
+            bool have;
+        };
+        auto look_up = [&](const Slot& x, int h, int tile) {
             const int at = tile * kTokens + lane * box;
-            const bool have = lane < boxes && at < x.len;
-            int page = 0;
-            if (have) {
-                page = p.table[(int64_t)x.b * p.width + (at >> p.page_shift)];
-                if (page < 0 || page >= p.pages) {
-                    record_status(p.status, MLA_ERR_POS_RANGE);
-                    page = (int)p.pages;  // reads as zeros
-                }
+            Tile k;
+            k.have = lane < boxes && at < x.len;
+            k.entry = k.have ? p.table[(int64_t)x.b * p.width + (at >> p.page_shift)] : 0;
+            k.place = (tile * kTokens) & (p.page - 1);
+            k.h = h;
+            return k;
+        };
+        auto load = [&](const CUtensorMap* map, const Tile& k, int chunks) {
+            int page = k.entry;
+            if (page < 0 || page >= p.pages) {
+                record_status(p.status, MLA_ERR_POS_RANGE);
+                page = (int)p.pages;  // reads as zeros
             }
-            const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, have)) * box * 128;
+            const int count = __popc(__ballot_sync(0xFFFFFFFFu, k.have));
             for (int j = 0; j < chunks && ok; ++j) {
                 bool got = true;
-                if (lane == 0) got = filled < p.ring || mbar_wait(empty0 + 8 * ring.i, ring.phase ^ 1u, abort_flag);
+                if (lane == 0) {
+                    const uint32_t full = full0 + 8 * ring.i;
+                    got = filled < p.ring || wait(empty0 + 8 * ring.i, ring.phase ^ 1u, abort_flag);
+                    if (got) {
+                        mbar_arrive_expect_tx(full, count * box * 128);
+                        if (boxes == 1 && count == 1)
+                            tma_load_page(base + ring.i * kChunk, map, j * 128, k.place, k.h, page, full);
+                    }
+                }
+                if (boxes > 1) {
+                    for (int i = 0; i < count; ++i) {
+                        const int from = __shfl_sync(0xFFFFFFFFu, page, i);
+                        if (lane == 0 && got)
+                            tma_load_page(base + ring.i * kChunk + i * box * 128, map, j * 128, 0, k.h, from, full0 + 8 * ring.i);
+                    }
+                }
                 ok = __shfl_sync(0xFFFFFFFFu, got, 0);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * ring.i, bytes);
-                __syncwarp();
-                if (have)
-                    tma_load_page(base + ring.i * kChunk + lane * box * 128, map, j * 128, at & (p.page - 1), h, page,
-                                  full0 + 8 * ring.i);
                 ring.step(p.ring);
                 ++filled;
             }
         };
         if (tiles > 0) {
-            Walk<R> keys = walk, values = walk;
-            keys.next(p, seqs);
-            if (!SHARED) values.next(p, seqs);
-            int tk = keys.t0, tv = values.t0;
+            Walk<R> w = walk;
+            w.next(p, seqs);
+            int tile = w.t0;
+            Tile now = look_up(w.x, w.h, tile), before = now, next = now;
             for (int t = 0; t <= tiles && ok; ++t) {
-                if (t < tiles) {
-                    load(&k_map, keys.x, keys.h, tk, p.nk);
-                    if (++tk == keys.t1 && keys.next(p, seqs)) tk = keys.t0;
+                if (t + 1 < tiles) {  // the next tile's entry is on its way while this one waits for room
+                    if (++tile == w.t1) {
+                        w.next(p, seqs);
+                        tile = w.t0;
+                    }
+                    next = look_up(w.x, w.h, tile);
                 }
-                if (!SHARED && t > 0 && ok) {
-                    load(&v_map, values.x, values.h, tv, p.nv);
-                    if (++tv == values.t1 && values.next(p, seqs)) tv = values.t0;
-                }
+                if (t < tiles) load(&k_map, now, p.nk);
+                if (!SHARED && t > 0 && ok) load(&v_map, before, p.nv);
+                before = now;
+                now = next;
             }
             if (!ok && lane == 0) {  // copies in flight land before the block leaves
                 for (int j = filled > p.ring ? filled - p.ring : 0; j < filled; ++j)
@@ -416,59 +510,73 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == kIssuer) {
         // -------------------------------------------------------- MMA issuer
         if (lane == 0 && tiles > 0) {
             const uint32_t i_s = idesc_f8(128, N2, 0), i_o = idesc_f8(128, N2, 1);
+            const uint64_t dk = desc_kmajor_sw128(base), dv = desc_mnmajor_sw128(base, kChunk);
+            const uint64_t dq = desc_kmajor_sw128(q_base), dw = desc_weights(p_base);
+            const int last_steps = (p.Dk - (p.nk - 1) * 128 + 31) / 32;  // of the last chunk of the keys
             Ring ring;              // next chunk in the order of use
             int tile_slot = 0;      // SHARED: ring slot of tile t - 1's first chunk
-            bool ok = true, first = true, first_before = false;
+            bool ok = true;
+            int in_piece = 0, in_piece_before = 0;  // tiles of the piece in front of this one
             Walk<R> w = walk;
             w.next(p, seqs);
-            int tw = w.t0;
             uint32_t q_phase = 0;
             for (int t = 0; t <= tiles && ok; ++t) {
                 const int this_slot = ring.i;
+                const uint32_t buf = t & 1;
                 if (t < tiles) {
-                    if (first) {
-                        ok = mbar_wait(q_full, q_phase, abort_flag);
+                    if (in_piece == 0) {
+                        ok = wait(q_full, q_phase, abort_flag);
                         q_phase ^= 1u;
                     }
-                    ok = ok && (t < 2 || mbar_wait(s_empty + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1u, abort_flag));
+                    ok = ok && (t < 2 || wait(s_empty + 8 * buf, (uint32_t)((t >> 1) - 1) & 1u, abort_flag));
+                    const uint32_t d = s_tmem + buf * N2;
                     for (int j = 0; j < p.nk && ok; ++j) {
-                        ok = mbar_wait(full0 + 8 * ring.i, ring.phase, abort_flag);
+                        ok = wait(full0 + 8 * ring.i, ring.phase, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
-                        const int left = p.Dk - j * 128, steps = left >= 128 ? 4 : (left + 31) / 32;
-                        for (int s = 0; s < steps; ++s)
-                            mma_f8(s_tmem + (t & 1) * N2, desc_kmajor_sw128(base + ring.i * kChunk + s * 32),
-                                   desc_kmajor_sw128(q_base + j * (N2 * 128) + s * 32), i_s, (j | s) != 0);
+                        const uint32_t at = ring.i * kChunk, qt = j * (N2 * 128);
+                        if (j < p.nk - 1 || last_steps == 4) {
+#pragma unroll
+                            for (int s = 0; s < 4; ++s)
+                                mma_f8(d, desc_at(dk, at + 32 * s), desc_at(dq, qt + 32 * s), i_s, (j | s) != 0);
+                        } else {
+#pragma unroll
+                            for (int s = 0; s < 3; ++s)
+                                if (s < last_steps)
+                                    mma_f8(d, desc_at(dk, at + 32 * s), desc_at(dq, qt + 32 * s), i_s, (j | s) != 0);
+                        }
                         if (!SHARED) mma_commit(empty0 + 8 * ring.i);
                         ring.step(p.ring);
                     }
                     if (!ok) break;
-                    mma_commit(s_full + 8 * (t & 1));
+                    mma_commit(s_full + 8 * buf);
                 }
                 if (t > 0) {
                     const int u = t - 1;
-                    ok = mbar_wait(p_full + 8 * (u & 1), (uint32_t)(u >> 1) & 1u, abort_flag);
+                    const uint32_t ub = u & 1;
+                    ok = wait(p_full + 8 * ub, (uint32_t)(u >> 1) & 1u, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t probs = p_base + (u & 1) * (N2 * 128);
+                    const uint32_t pt = ub * (N2 * 128), d = o_tmem + (kStreams == 2 ? ub * p.nv * N2 : 0);
+                    const bool fresh = in_piece_before < kStreams;  // the stream's first tile of the piece
                     for (int j = 0; j < p.nv && ok; ++j) {
-                        int at = ring.i;
+                        int slot = ring.i;
                         if (SHARED) {
-                            at = tile_slot + j;
-                            if (at >= p.ring) at -= p.ring;
+                            slot = tile_slot + j;
+                            if (slot >= p.ring) slot -= p.ring;
                         } else {
-                            ok = mbar_wait(full0 + 8 * ring.i, ring.phase, abort_flag);
+                            ok = wait(full0 + 8 * ring.i, ring.phase, abort_flag);
                             if (!ok) break;
                             tc_fence_after();
                         }
+                        const uint32_t at = slot * kChunk;
 #pragma unroll
                         for (int s = 0; s < 4; ++s)
-                            mma_f8(o_tmem + j * N2, desc_mnmajor_sw128(base + at * kChunk + s * 4096, kChunk),
-                                   desc_kmajor_sw128(probs + s * 32), i_o, !first_before || s != 0);
+                            mma_f8(d + j * N2, desc_at(dv, at + 4096 * s), desc_at(dw, pt + 512 * s), i_o, !fresh || s != 0);
                         if (!SHARED) {
                             mma_commit(empty0 + 8 * ring.i);
                             ring.step(p.ring);
@@ -476,17 +584,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (!ok) break;
                     if (SHARED)
-                        for (int j = 0; j < p.nk; ++j) mma_commit(empty0 + 8 * ((tile_slot + j) % p.ring));
-                    mma_commit(p_empty + 8 * (u & 1));
+                        for (int j = 0; j < p.nk; ++j) {
+                            const int slot = tile_slot + j;
+                            mma_commit(empty0 + 8 * (slot >= p.ring ? slot - p.ring : slot));
+                        }
+                    mma_commit(p_empty + 8 * ub);
                 }
                 tile_slot = this_slot;
-                first_before = first;
-                if (t < tiles) {
-                    first = false;
-                    if (++tw == w.t1) {
-                        first = true;
-                        if (w.next(p, seqs)) tw = w.t0;
-                    }
+                in_piece_before = in_piece;
+                if (t < tiles && ++in_piece == w.t1 - w.t0) {
+                    in_piece = 0;
+                    w.next(p, seqs);
                 }
             }
             if (!ok) {
@@ -495,25 +603,91 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
+    } else if (warp == kMarker) {
+        // ------------------------------------------------------------- scales
+        // By plain loads, four tokens to a lane (of one page: its size is a multiple of four), half of the tiles that
+        // shared memory holds in flight. (A softmax thread that fetched its own token's waited for memory at every tile.)
+        constexpr int kFlight = kMarkTiles / 2;
+        if (tiles > 0) {
+            Walk<R> w = walk;
+            w.next(p, seqs);
+            int tile = w.t0;
+            bool ok = true;
+            for (int t0 = 0; t0 < tiles && ok; t0 += kFlight) {
+                int64_t at[kFlight];
+                int place[kFlight], page[kFlight];
+#pragma unroll
+                for (int i = 0; i < kFlight; ++i) {
+                    page[i] = -1;
+                    place[i] = 0;
+                    at[i] = 0;
+                    if (t0 + i >= tiles) continue;
+                    const int pos = tile * kTokens + lane * 4;
+                    if (pos < w.x.len) {
+                        place[i] = pos & (p.page - 1);
+                        page[i] = p.table[(int64_t)w.x.b * p.width + (pos >> p.page_shift)];
+                        at[i] = w.h;
+                    }
+                    if (++tile == w.t1) {
+                        w.next(p, seqs);
+                        tile = w.t0;
+                    }
+                }
+                const bool one = p.block_shift >= 2;  // one scale for the lane's four tokens
+                uint32_t k[kFlight][4], v[kFlight][4];
+#pragma unroll
+                for (int i = 0; i < kFlight; ++i) {
+                    // a bad page is recorded by the producer and reads as zeros; so do its scales
+                    const bool have = page[i] >= 0 && page[i] < p.pages;
+                    const int64_t m = ((int64_t)page[i] * p.H + at[i]) * p.marks;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        k[i][j] = v[i][j] = 0;
+                        if (have && (j == 0 || !one)) {
+                            k[i][j] = p.k_scales[m + ((place[i] + j) >> p.block_shift)];
+                            if (!SHARED) v[i][j] = p.v_scales[m + ((place[i] + j) >> p.block_shift)];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kFlight; ++i) {
+                    const int t = t0 + i, s = t % kMarkTiles;
+                    if (t >= tiles || !ok) continue;
+                    if (t >= kMarkTiles) ok = wait(m_empty + 8 * s, (uint32_t)(t / kMarkTiles - 1) & 1u, abort_flag);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    const uint32_t kw = one ? k[i][0] * 0x01010101u : k[i][0] | k[i][1] << 8 | k[i][2] << 16 | k[i][3] << 24;
+                    const uint32_t vw = SHARED ? kw : one ? v[i][0] * 0x01010101u : v[i][0] | v[i][1] << 8 | v[i][2] << 16 | v[i][3] << 24;
+                    sh.marks[s][lane][0] = kw;
+                    sh.marks[s][lane][1] = vw;
+                    mbar_arrive(m_full + 8 * s);
+                }
+            }
+        }
+        __syncwarp();
     } else if (tiles > 0) {
         // ------------------------------------------------------------ softmax
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;  // this warp's lanes of tensor memory
-        // the query rows of a piece as two E4M3 numbers each, row r at r and R + r; a warp takes every fourth row
+        constexpr int kFours = kFour / 4, RT = R / kFours;  // rows of a thread
+        const int tok = tid & 127, quad = warp & 3, stream = kStreams == 2 ? warp >> 2 : 0;
+        const int r_lo = kStreams == 2 ? 0 : (warp >> 2) * RT;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;  // this warp's lanes of tensor memory
+        const uint32_t my_bar = 1 + stream, all_bar = 3;
+        const uint32_t o_mine = o_tmem + lanes + stream * p.nv * N2;
+        // the query rows of a piece as two E4M3 numbers each, row r at r and R + r; a warp takes every kSoftWarps-th row
         auto load_q = [&](const Walk<R>& w, int par) {
             const int gran = p.Dk / 8;
-            for (int r0 = 0; r0 < R; r0 += 16) {
-                constexpr int kG = (kMaxQueryChunks * 128 / 8 + 31) / 32;
-                uint4 g[4][kG];
+            constexpr int kBatch = R / kSoftWarps < 4 ? R / kSoftWarps : 4;
+            constexpr int kG = (kMaxQueryChunks * 128 / 8 + 31) / 32;
+            for (int r0 = warp; r0 < R; r0 += kBatch * kSoftWarps) {
+                uint4 g[kBatch][kG];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = r0 + i * 4 + warp, rho = w.x.rho0 + r, tok = rho / p.group;
-                    const bool have = r < R && r < w.x.rows;
-                    const uint16_t* src = p.q + (w.x.lo + tok) * p.q_t + (int64_t)(w.h * p.group + rho - tok * p.group) * p.q_h;
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = r0 + i * kSoftWarps, rho = w.x.rho0 + r, at_tok = rho / p.group;
+                    const uint16_t* src = p.q + (w.x.lo + at_tok) * p.q_t + (int64_t)(w.h * p.group + rho - at_tok * p.group) * p.q_h;
 #pragma unroll
                     for (int k = 0; k < kG; ++k) {
                         const int at = k * 32 + lane;
                         g[i][k] = make_uint4(0, 0, 0, 0);
-                        if (have && at < gran) {
+                        if (r < w.x.rows && at < gran) {
                             const uint16_t* q = src + at * 8;
                             if (p.q_vec) {
                                 g[i][k] = *reinterpret_cast<const uint4*>(q);
@@ -527,9 +701,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = r0 + i * 4 + warp;
-                    if (r >= R) continue;
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = r0 + i * kSoftWarps;
                     uint32_t m = 0;
 #pragma unroll
                     for (int k = 0; k < kG; ++k) {
@@ -564,176 +737,196 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sts_v2(chunk + (R + r) * 128 + ((unit ^ (r & 7)) << 4) + half, lo[0], lo[1]);
                     }
                     if (lane == 0) {
-                        const int rr = r < w.x.rows ? r : w.x.rows - 1, rho = w.x.rho0 + rr, tok = rho / p.group;
-                        sh.row[par][r] = make_float2(bad ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 - x) << 23), kNothing);
-                        sh.limit[par][r] = w.x.len - w.x.n + tok;
-                        sh.row_at[par][r] = (w.x.lo + tok) * p.Hq + (int64_t)w.h * p.group + rho - tok * p.group;
+                        const int rr = r < w.x.rows ? r : w.x.rows - 1, rho = w.x.rho0 + rr, at_tok = rho / p.group;
+                        sh.unit[par][r] = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 - x) << 23);
+                        for (int k = 0; k < kStreams; ++k) sh.ref[par][k][r] = kNothing;
+                        sh.limit[par][r] = w.x.len - w.x.n + at_tok;
+                        sh.row_at[par][r] = (w.x.lo + at_tok) * p.Hq + (int64_t)w.h * p.group + rho - at_tok * p.group;
                     }
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
-            named_bar_sync(1, kSoftmax);
+            named_bar_sync(all_bar, kSoftmax);
         };
-        // the scale bytes of this thread's token: keys in bits 0-7, values in 8-15
-        auto load_scales = [&](const Walk<R>& w, int tile) -> uint32_t {
-            const int pos = tile * kTokens + tid;
-            if (pos >= w.x.len) return 0;
-            const int page = p.table[(int64_t)w.x.b * p.width + (pos >> p.page_shift)];
-            if (page < 0 || page >= p.pages) return 0;  // recorded by the producer
-            const int64_t at = ((int64_t)page * p.H + w.h) * p.marks + ((pos & (p.page - 1)) >> p.block_shift);
-            const uint32_t k = p.k_scales[at];
-            return k | (SHARED ? k << 8 : (uint32_t)p.v_scales[at] << 8);
-        };
-
-        uint32_t p_off[8];  // this token's byte in the first eight rows of the probabilities (128-byte swizzle)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p_off[i] = i * 128 + (((uint32_t)(tid >> 4) ^ i) << 4) + (tid & 15);
 
         Walk<R> w = walk;
         bool more = w.next(p, seqs);
-        int par = 0, t = 0;
-        // A wait that gave up is reported with the next vote, so that all four warps leave together: until then a
-        // thread that saw it goes on, through every barrier.
-        bool failed = false, leave = false;
+        int par = 0, t = 0, turn = 0;  // t: tiles of the share so far; turn: this stream's
+        // A wait that gave up is reported with the stream's next vote, and the stream's with the end of the piece, so that
+        // all warps leave together: until then a thread that saw it goes on, through every barrier.
+        bool failed = false;
         if (more) load_q(w, 0);
-        uint32_t marks = more ? load_scales(w, w.t0) : 0;
         while (more) {
-            const float2* row = sh.row[par];
-            const int* limit = sh.limit[par];
-            float l[R];
+            const float *unit = &sh.unit[par][r_lo], *ref = &sh.ref[par][stream][r_lo];
+            const int* limit = &sh.limit[par][r_lo];
+            float l[RT];
 #pragma unroll
-            for (int r = 0; r < R; ++r) l[r] = 0.f;
+            for (int r = 0; r < RT; ++r) l[r] = 0.f;
             int top_e = kNoScale;
+            bool any = false;  // the stream has had a tile of the piece
             const int least = w.x.len - w.x.n + w.x.rho0 / p.group;  // the last position that every row sees
-            for (int tile = w.t0; tile < w.t1; ++tile, ++t) {
-                const int buf = t & 1, pos = tile * kTokens + tid;
+            const int t_piece = t;
+            for (; t - t_piece < w.t1 - w.t0; ++t) {
+                if (kStreams == 2 && (t & 1) != stream) continue;
+                const int tile = w.t0 + t - t_piece, buf = t & 1, pos = tile * kTokens + tok, slot = t % kMarkTiles;
                 const bool masked = (tile + 1) * kTokens - 1 > least;
                 const bool valid = pos < w.x.len;
-                const float ks = e8m0_to_f32(marks & 0xFFu) * p.scale_log2;
-                const int ve = (int)(marks >> 8);
-                if (tile + 1 < w.t1) marks = load_scales(w, tile + 1);  // under this tile
-                failed |= !mbar_wait(s_full + 8 * buf, (uint32_t)(t >> 1) & 1u, abort_flag);
+                failed |= !wait(m_full + 8 * slot, (uint32_t)(t / kMarkTiles) & 1u, abort_flag);
+                const uint8_t* mark = reinterpret_cast<const uint8_t*>(&sh.marks[slot][tok / 4][0]) + tok % 4;
+                const int ve = mark[4];
+                // a value's scale of NaN makes the scores NaN of those who see it
+                const float ks = e8m0_to_f32(ve == 255 ? 255u : mark[0]) * p.scale_log2;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(m_empty + 8 * slot);
+                failed |= !wait(s_full + 8 * buf, (uint32_t)(t >> 1) & 1u, abort_flag);
                 __syncwarp();
                 tc_fence_after();
-                float s[R];
-                const uint32_t from = s_tmem + lanes + buf * N2;
-                if constexpr (R == 8) {
-                    uint32_t v[16];
-                    tmem_ld16(from, v);
-                    tmem_ld_wait();
+                // x = the rows' scores, less their references; -inf where a row does not see the token
+                float x[RT];
+                auto scores = [&](auto less) {
+                    const uint32_t from = s_tmem + lanes + buf * N2 + r_lo;
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) s[r] = fmaf(__uint_as_float(v[8 + r]), 0.03125f, __uint_as_float(v[r]));
-                } else {
-#pragma unroll
-                    for (int r0 = 0; r0 < R; r0 += 16) {
+                    for (int r0 = 0; r0 < RT; r0 += 16) {
                         uint32_t v[16], u[16];
                         tmem_ld16(from + r0, v);
-                        tmem_ld16(from + R + r0, u);
+                        if constexpr (R > 8) tmem_ld16(from + R + r0, u);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            s[r0 + r] = fmaf(__uint_as_float(u[r]), 0.03125f, __uint_as_float(v[r]));
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(s_empty + 8 * buf);
-                float over = kNothing;
+                        for (int r = 0; r < (RT < 16 ? RT : 16); r += 4) {
+                            const float4 q = *reinterpret_cast<const float4*>(unit + r0 + r);
+                            const float4 m = *reinterpret_cast<const float4*>(ref + r0 + r);
+                            const float qs[4] = {q.x, q.y, q.z, q.w}, ms[4] = {-m.x, -m.y, -m.z, -m.w};
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float2 q = row[r];
-                    s[r] = s[r] * ks * q.x;
-                    if (masked) s[r] = pos <= limit[r] ? s[r] : -INFINITY;
-                    over = fmaxf(over, s[r] - q.y);
+                            for (int i = 0; i < 4; i += 2) {
+                                const uint32_t *h = &v[r + i], *o = R > 8 ? &u[r + i] : &v[(8 + r + i) & 15];
+                                float &x0 = x[r0 + r + i], &x1 = x[r0 + r + i + 1];
+                                float k0, k1;
+                                mul2(k0, k1, qs[i], qs[i + 1], ks, ks);
+                                fma2(x0, x1, __uint_as_float(o[0]), __uint_as_float(o[1]), 0.03125f, 0.03125f,
+                                     __uint_as_float(h[0]), __uint_as_float(h[1]));
+                                if constexpr (decltype(less)::value) fma2(x0, x1, x0, x1, k0, k1, ms[i], ms[i + 1]);
+                                else mul2(x0, x1, x0, x1, k0, k1);
+                            }
+                        }
+                    }
+                    if (masked && w.x.n > 1) {
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) x[r] = pos <= limit[r] ? x[r] : -INFINITY;
+                    }
+                };
+                scores(std::true_type{});
+                float over = max3(x[0], x[1], x[2]), over2 = max3(x[3], x[4], x[5]);
+#pragma unroll
+                for (int r = 6; r + 3 < RT; r += 4) {
+                    over = max3(over, x[r], x[r + 1]);
+                    over2 = max3(over2, x[r + 2], x[r + 3]);
                 }
+                over = max3(max3(over, over2, kNothing), x[RT - 2], x[RT - 1]);
                 const bool grow = valid && (over > kPass || (ve > top_e && ve != 255));
                 const int bits = (__any_sync(0xFFFFFFFFu, grow) ? 1 : 0) | (__any_sync(0xFFFFFFFFu, failed) ? 2 : 0);
-                if (lane == 0 && bits) atomicOr(&sh.vote[t % 3], bits);
-                named_bar_sync(1, kSoftmax);
-                const int vote = *(volatile int*)&sh.vote[t % 3];
-                if (tid == 0) sh.vote[(t + 2) % 3] = 0;
+                if (lane == 0 && bits) atomicOr(&sh.vote[stream][turn], bits);
+                named_bar_sync(my_bar, kFour * 32);
+                const int vote = *(volatile int*)&sh.vote[stream][turn];
+                turn = turn == 2 ? 0 : turn + 1;
+                // the place two turns on was read by all before this barrier and is written by none before the next
+                if (tid == stream * 128) sh.vote[stream][turn == 2 ? 0 : turn + 1] = 0;
                 if (vote & 2) {
-                    leave = true;
+                    sh.leave = 1;
+                    t = t_piece + w.t1 - w.t0;
                     break;
                 }
                 if (vote) {
-                    // a new reference for every row: the largest score so far; and the largest scale of V
+                    // a new reference for every row, the largest score so far, and the largest scale of V
+                    scores(std::false_type{});
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const float m = warp_max(valid ? s[r] : -INFINITY);
-                        if (lane == (r & 31)) sh.warp_row[warp][r] = m;
+                    for (int r = 0; r < RT; ++r) {
+                        const float m = warp_max(valid ? x[r] : -INFINITY);
+                        if (lane == (r & 31)) sh.warp_row[stream][quad][r_lo + r] = m;
                     }
                     const int e = __reduce_max_sync(0xFFFFFFFFu, valid && ve != 255 ? ve : kNoScale);
-                    if (lane == 0) sh.warp_e[warp] = e;
-                    named_bar_sync(1, kSoftmax);
-                    if (tid < R) {
-                        const float old = sh.row[par][tid].y;
+                    if (lane == 0) sh.warp_e[stream][quad] = e;
+                    named_bar_sync(my_bar, kFour * 32);
+                    const int r = tid - stream * 128;
+                    if (r < R) {
+                        const float old = sh.ref[par][stream][r];
                         float m = old;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) m = fmaxf(m, sh.warp_row[i][tid]);
-                        sh.row[par][tid].y = m;
-                        sh.factor[tid] = exp2_fast(old - m);
+                        for (int i = 0; i < 4; ++i) m = fmaxf(m, sh.warp_row[stream][i][r]);
+                        sh.ref[par][stream][r] = m;
+                        sh.factor[stream][r] = exp2_fast(old - m);
                     }
                     const int old_e = top_e;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) top_e = max(top_e, sh.warp_e[i]);
-                    named_bar_sync(1, kSoftmax);
+                    for (int i = 0; i < 4; ++i) top_e = max(top_e, sh.warp_e[stream][i]);
+                    named_bar_sync(my_bar, kFour * 32);
 #pragma unroll
-                    for (int r = 0; r < R; ++r) l[r] *= sh.factor[r];
-                    if (tile > w.t0) {
+                    for (int i = 0; i < RT; ++i) {
+                        l[i] *= sh.factor[stream][r_lo + i];
+                        x[i] -= ref[i];
+                    }
+                    if (any) {
                         const float down = old_e == top_e ? 1.f : old_e < top_e - 126 ? 0.f : __uint_as_float((uint32_t)(127 + old_e - top_e) << 23);
-                        failed |= !mbar_wait(p_empty + 8 * (buf ^ 1), (uint32_t)((t - 1) >> 1) & 1u, abort_flag);
+                        const int u = t - kStreams;  // the stream's tile before
+                        failed |= !wait(p_empty + 8 * (u & 1), (uint32_t)(u >> 1) & 1u, abort_flag);
                         __syncwarp();
                         tc_fence_after();
                         for (int j = 0; j < p.nv; ++j)
 #pragma unroll
-                            for (int r0 = 0; r0 < N2; r0 += 16) {
+                            for (int r0 = 0; r0 < 2 * RT; r0 += 16) {
                                 uint32_t v[16];
-                                const uint32_t at = o_tmem + lanes + j * N2 + r0;
+                                const int col = R == 8 ? 0 : r_lo + (r0 < RT ? r0 : R + r0 - RT);
+                                const uint32_t at = o_mine + j * N2 + col;
                                 tmem_ld16(at, v);
                                 tmem_ld_wait();
 #pragma unroll
                                 for (int i = 0; i < 16; ++i)
-                                    v[i] = __float_as_uint(__uint_as_float(v[i]) * sh.factor[(r0 + i) % R] * down);
+                                    v[i] = __float_as_uint(__uint_as_float(v[i]) * sh.factor[stream][(col + i) % R] * down);
                                 tmem_st16(at, v);
                             }
                         tmem_st_wait();
                     }
                 }
-                // the probabilities, times the value's scale, as two E4M3 numbers
-                if (t >= 2) failed |= !mbar_wait(p_empty + 8 * buf, (uint32_t)((t >> 1) - 1) & 1u, abort_flag);
-                const int fe = ve - top_e + 4 + 127;
-                float f = fe <= 0 ? 0.f : __uint_as_float((uint32_t)fe << 23);
-                if (ve == 255) f = __uint_as_float(0x7FC00000u);
-                if (!valid) f = 0.f;
-                const uint32_t to = p_base + buf * (N2 * 128);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_empty + 8 * buf);
+                any = true;
+                // the probabilities, times the value's scale, as two E4M3 numbers; nothing behind the last position
+                uint32_t hi[RT / 4], lo[RT / 4];
+                if (valid) {
+                    const int fe = ve - top_e + 4 + 127;
+                    const float f = fe <= 0 || ve == 255 ? 0.f : __uint_as_float((uint32_t)fe << 23);
 #pragma unroll
-                for (int r = 0; r < R; r += 2) {
-                    const float a = exp2_fast(s[r] - row[r].y), b = exp2_fast(s[r + 1] - row[r + 1].y);
-                    float x = a * f, y = b * f;
-                    if (masked) {
-                        const bool ina = valid && pos <= limit[r], inb = valid && pos <= limit[r + 1];
-                        l[r] += ina ? a : 0.f;
-                        l[r + 1] += inb ? b : 0.f;
-                        x = ina ? x : 0.f;
-                        y = inb ? y : 0.f;
-                    } else {
-                        l[r] += a;
-                        l[r + 1] += b;
+                    for (int r = 0; r < RT; r += 4) {
+                        uint32_t h[2], o[2];
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2) {
+                            const float a = exp2_fast(x[r + i]), b = exp2_fast(x[r + i + 1]);
+                            add2(l[r + i], l[r + i + 1], a, b);
+                            float y, z;
+                            mul2(y, z, a, b, f, f);
+                            split_weights(y, z, h[i / 2], o[i / 2]);
+                        }
+                        hi[r / 4] = __byte_perm(h[0], h[1], 0x5410);
+                        lo[r / 4] = __byte_perm(o[0], o[1], 0x5410);
                     }
-                    const uint32_t hi = cvt_e4m3x2(x, y);
-                    float ha, hb;
-                    e4m3x2_to_f32(hi, ha, hb);
-                    const uint32_t lo = cvt_e4m3x2((x - ha) * 32.f, (y - hb) * 32.f);
-                    const uint32_t at = to + (r >> 3) * 1024;
-                    sts_b8(at + p_off[r & 7], hi & 0xFFu);
-                    sts_b8(at + p_off[(r + 1) & 7], hi >> 8);
-                    sts_b8(at + R * 128 + p_off[r & 7], lo & 0xFFu);
-                    sts_b8(at + R * 128 + p_off[(r + 1) & 7], lo >> 8);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < RT / 4; ++i) hi[i] = lo[i] = 0;
                 }
-                if ((tile + 1) * kTokens > w.x.len || (masked && w.x.n > 1)) {
+                if (t >= 2) failed |= !wait(p_empty + 8 * buf, (uint32_t)((t >> 1) - 1) & 1u, abort_flag);
+                const uint32_t to = p_base + buf * (N2 * 128) + tok * 16;
+                if constexpr (R == 8) {
+                    sts_v4(to, hi[0], hi[1], lo[0], lo[1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < RT / 16; ++i) {
+                        sts_v4(to + (r_lo / 16 + i) * 2048, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+                        sts_v4(to + ((R + r_lo) / 16 + i) * 2048, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+                    }
+                }
+                if (r_lo == 0 && ((tile + 1) * kTokens > w.x.len || (masked && w.x.n > 1))) {
                     // What lies behind the last position may be anything, also NaN: zeros. And a NaN that some rows see
                     // and others do not must not meet their zero probability: it is noted and put into the result.
                     int64_t chunk;
@@ -741,29 +934,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else chunk = (int64_t)(t + 2 < tiles ? t + 2 : tiles) * p.nk + (int64_t)t * p.nv;
                     for (int j = 0; j < p.nv; ++j, ++chunk) {
                         const int at = (int)(chunk % p.ring);
-                        failed |= !mbar_wait(full0 + 8 * at, (uint32_t)(chunk / p.ring) & 1u, abort_flag);
-                        const uint32_t mem = base + at * kChunk + tid * 128;
+                        failed |= !wait(full0 + 8 * at, (uint32_t)(chunk / p.ring) & 1u, abort_flag);
+                        const uint32_t mem = base + at * kChunk + tok * 128;
                         if (!valid) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i) sts_v4(mem + i * 16, 0, 0, 0, 0);
                         } else if (pos > least) {
                             for (int i = 0; i < 8; ++i) {
-                                const uint4 v = lds_v4(mem + ((i ^ (tid & 7)) << 4));
+                                const uint4 v = lds_v4(mem + ((i ^ (tok & 7)) << 4));
                                 uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                                bool any = false;
+                                bool found = false;
+                                for (int k = 0; k < 4; ++k) found |= __vcmpeq4(u[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+                                if (!found) continue;
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
 #pragma unroll
                                     for (int e = 0; e < 4; ++e)
                                         if (((u[k] >> (8 * e)) & 0x7Fu) == 0x7Fu) {
-                                            any = true;
                                             atomicMin(&sh.nan_at[(j * 128 + i * 16 + k * 4 + e) & 511], pos);
                                             u[k] &= ~(0xFFu << (8 * e));
                                         }
-                                if (any) {
-                                    sts_v4(mem + ((i ^ (tid & 7)) << 4), u[0], u[1], u[2], u[3]);
-                                    sh.nan_seen = 1;
-                                }
+                                sts_v4(mem + ((i ^ (tok & 7)) << 4), u[0], u[1], u[2], u[3]);
+                                sh.nan_seen = 1;
                             }
                         }
                     }
@@ -773,72 +965,95 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * buf);
             }
-            if (leave) break;
             const Walk<R> done = w;
-            const int last = t - 1;
             more = w.next(p, seqs);
+            const int last = t - 1;
             if (more) {
-                load_q(w, par ^ 1);  // every product of this piece's queries is done: its last scores were read
-                marks = load_scales(w, w.t0);
+                // the products of this piece's queries are done once its last scores are there (the other stream's, maybe)
+                failed |= !wait(s_full + 8 * (last & 1), (uint32_t)(last >> 1) & 1u, abort_flag);
+                load_q(w, par ^ 1);
             }
             // ------------------------------------------------ the piece's result
             const bool whole = done.t0 == 0 && done.t1 == done.x.tiles;
             const int part = 2 * (int)c + (done.t0 == 0 ? 1 : 0);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
+            for (int r = 0; r < RT; ++r) {
                 const float v = warp_add(l[r]);
-                if (lane == (r & 31)) sh.warp_row[warp][r] = v;
+                if (lane == (r & 31)) sh.warp_row[stream][quad][r_lo + r] = v;
             }
-            named_bar_sync(1, kSoftmax);
+            if (tok == 0 && r_lo == 0) sh.top_e[stream] = any ? top_e : 2 * kNoScale;
+            named_bar_sync(all_bar, kSoftmax);
+            if (*(volatile int*)&sh.leave) break;
             if (tid < R) {
-                const float sum = (sh.warp_row[0][tid] + sh.warp_row[1][tid]) + (sh.warp_row[2][tid] + sh.warp_row[3][tid]);
-                const float m = row[tid].y;
-                const float f = ldexpf(1.f, top_e < 0 ? -131 : top_e - 131);
-                if (whole) {
-                    sh.factor[tid] = sum == 0.f ? 0.f : f / sum;
-                    if (p.lse && tid < done.x.rows)
-                        p.lse[sh.row_at[par][tid]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945309f;
-                } else {
-                    sh.factor[tid] = f;
-                    p.part_ml[(int64_t)part * R + tid] = make_float2(m, sum);
+                float m = kNothing, sum = 0.f, part_f[kStreams];
+                for (int k = 0; k < kStreams; ++k) m = fmaxf(m, sh.ref[par][k][tid]);
+#pragma unroll
+                for (int k = 0; k < kStreams; ++k) {
+                    const float (&row)[4][R] = sh.warp_row[k];
+                    const float up = exp2_fast(sh.ref[par][k][tid] - m);
+                    sum = fmaf(up, (row[0][tid] + row[1][tid]) + (row[2][tid] + row[3][tid]), sum);
+                    part_f[k] = ldexpf(up, sh.top_e[k] < 0 ? -131 : sh.top_e[k] - 131);
                 }
+                const float over = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+                for (int k = 0; k < kStreams; ++k) sh.factor[k][tid] = part_f[k] * over;
+                if (!whole) p.part_ml[(int64_t)part * R + tid] = make_float2(m, sum);
+                else if (p.lse && tid < done.x.rows)
+                    p.lse[sh.row_at[par][tid]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945309f;
             }
-            named_bar_sync(1, kSoftmax);
-            failed |= !mbar_wait(p_empty + 8 * (last & 1), (uint32_t)(last >> 1) & 1u, abort_flag);
-            __syncwarp();
+            named_bar_sync(all_bar, kSoftmax);
+            failed |= !wait(p_empty + 8 * (last & 1), (uint32_t)(last >> 1) & 1u, abort_flag);
+            if (kStreams == 2 && last > t_piece) failed |= !wait(p_empty + 8 * ((last - 1) & 1), (uint32_t)((last - 1) >> 1) & 1u, abort_flag);
             tc_fence_after();
             const bool nans = *(volatile int*)&sh.nan_seen != 0;
+            // a channel to a thread; the rows halved between the two fours
+            constexpr int RE = R / 2, kStep = RE < 16 ? RE : 16;
+            const int e_lo = (warp >> 2) * RE;
             for (int j = 0; j < p.nv; ++j) {
-                const int ch = j * 128 + tid;
+                const int ch = j * 128 + tok;
                 const int nan_at = nans ? sh.nan_at[ch & 511] : 0x7FFFFFFF;
-                constexpr int kStep = R < 16 ? R : 16;
 #pragma unroll
-                for (int r0 = 0; r0 < R; r0 += kStep) {
-                    uint32_t v[16], u[16];
-                    __syncwarp();
-                    tmem_ld16(o_tmem + lanes + j * N2 + r0, v);
-                    if constexpr (R >= 16) tmem_ld16(o_tmem + lanes + j * N2 + R + r0, u);
-                    tmem_ld_wait();
+                for (int r0 = 0; r0 < RE; r0 += kStep) {
+                    float o[kStep];
+#pragma unroll
+                    for (int i = 0; i < kStep; ++i) o[i] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kStreams; ++k) {
+                        if (sh.top_e[k] == 2 * kNoScale) continue;  // the same in every thread: a stream without a tile
+                        uint32_t v[16], u[16];
+                        const uint32_t from = o_tmem + lanes + (k * p.nv + j) * N2;
+                        __syncwarp();
+                        tmem_ld16(from + (R <= 16 ? 0 : e_lo + r0), v);
+                        if constexpr (R > 8) tmem_ld16(from + R + (R <= 16 ? 0 : e_lo + r0), u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < kStep; ++i) {
+                            // R = 8: rows and rests in one load; R <= 16: both halves' rows are in it
+                            const bool up = R <= 16 && e_lo != 0;
+                            const uint32_t a = up ? v[(RE + i) & 15] : v[i];
+                            const uint32_t b = R == 8 ? (up ? v[(8 + RE + i) & 15] : v[(8 + i) & 15]) : up ? u[(RE + i) & 15] : u[i];
+                            o[i] = fmaf(fmaf(__uint_as_float(b), 0.03125f, __uint_as_float(a)), sh.factor[k][e_lo + r0 + i], o[i]);
+                        }
+                    }
                     if (ch >= p.Dv) continue;
 #pragma unroll
                     for (int i = 0; i < kStep; ++i) {
-                        const int r = r0 + i;
+                        const int r = e_lo + r0 + i;
                         if (r >= done.x.rows) break;
-                        const float lo = __uint_as_float(R >= 16 ? u[i] : v[8 + (i & 7)]);
-                        float o = fmaf(lo, 0.03125f, __uint_as_float(v[i])) * sh.factor[r];
-                        if (nan_at <= limit[r]) o = __uint_as_float(0x7FC00000u);
-                        if (whole) p.out[sh.row_at[par][r] * p.Dv + ch] = (uint16_t)pack_bf16x2(o, 0.f);
-                        else p.part_o[((int64_t)part * R + r) * p.Dv + ch] = o;
+                        if (nan_at <= sh.limit[par][r]) o[i] = __uint_as_float(0x7FC00000u);
+                        if (whole) p.out[sh.row_at[par][r] * p.Dv + ch] = (uint16_t)pack_bf16x2(o[i], 0.f);
+                        else p.part_o[((int64_t)part * R + r) * p.Dv + ch] = o[i];
                     }
                 }
             }
+            __syncwarp();
             tc_fence_before();
-            if (nans) {  // uniform: set before the last barriers
-                named_bar_sync(1, kSoftmax);
+            if (nans) {  // the same in every thread: set before the last barriers
+                named_bar_sync(all_bar, kSoftmax);
                 for (int i = tid; i < 512; i += kSoftmax) sh.nan_at[i] = 0x7FFFFFFF;
                 if (tid == 0) sh.nan_seen = 0;
             }
-            named_bar_sync(1, kSoftmax);
+            named_bar_sync(all_bar, kSoftmax);
             if (tid == 0 && !whole) {
                 p.meta[part] = make_int4(done.t0 == 0 ? kOpens : done.t1 == done.x.tiles ? kEnds : kGoesOn, done.x.rho0,
                                          done.x.rows, (int)done.x.lo * p.H + done.h);
@@ -853,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && *abort_flag) record_status(p.status, MLA_ERR_TIMEOUT);
-    if (warp == 5) {
+    if (warp == kIssuer) {
         tc_fence_after();
         tmem_dealloc(tmem, p.tmem_cols);
     }
@@ -944,7 +1159,7 @@ bool attn_plan(const mla_attn_shape& s, const mla_kv_cache& c, int max_smem, Att
     a.ring = (int)(room > 14 ? 14 : room);
     if (a.ring < (shared ? 2 * a.nk : a.nk + a.nv)) return false;
     a.smem = fixed + (size_t)a.ring * kChunk;
-    const int cols = (2 + a.nv) * 2 * a.R;
+    const int cols = (2 + a.nv * (a.R <= 16 ? 2 : 1)) * 2 * a.R;
     a.tmem_cols = 32;
     while (a.tmem_cols < cols) a.tmem_cols *= 2;
     if (a.tmem_cols > 512) return false;
