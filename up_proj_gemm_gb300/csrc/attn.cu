@@ -42,10 +42,15 @@ namespace {
 
 constexpr int kTokens = 128;           // tokens of a tile
 constexpr uint32_t kChunk = 16384;     // 128 tokens x 128 channels
-constexpr int kSoftWarps = 8;          // softmax warps; behind them one that loads codes, one that issues the products
-constexpr int kLoader = 8, kIssuer = 9, kMarker = 10;  // and one that loads scales
-constexpr int kSoftmax = 32 * kSoftWarps, kThreads = kSoftmax + 96;
+// Sixteen warps: eight for the softmax, one that loads codes, one that issues the
+// products, one that loads scales, one that deals out the pieces of work, and four
+// that bring a piece's queries in and its result out, beside the tiles of the pieces
+// after and before.
+constexpr int kSoftWarps = 8, kLoader = 8, kIssuer = 9, kMarker = 10, kDealer = 11, kHelper = 12;
+constexpr int kThreads = 512, kHelpers = 128;
 constexpr int kMarkTiles = 8;          // tiles whose scales are in shared memory
+constexpr int kPieces = 4;             // pieces that are dealt out ahead
+constexpr int kPieceReaders = kSoftWarps + 3 + 4;
 // Four softmax warps hold a tile's tokens, a token to a thread. With few query rows
 // a tile is a chain of waits, and the two fours take turns (two streams, each with
 // its own references, sums and O, joined in the end); with many it is arithmetic,
@@ -55,7 +60,6 @@ constexpr int kStreams = R <= 16 ? 2 : 1;
 constexpr float kPass = 4.f;           // log2 of how far scores may pass the reference
 constexpr float kNothing = -3.0e38f;   // the reference of a row that has seen nothing
 constexpr int kNoScale = -1000;
-constexpr int kHeldSeqs = 256;         // sequences whose lengths are held in shared memory
 constexpr int kMaxQueryChunks = 5;
 constexpr int kCombineThreads = 256;
 
@@ -73,8 +77,10 @@ struct AttnParams {
     float* part_o;    // [2 * shares][R][Dv]
     float2* part_ml;  // [2 * shares][R]
     int4* meta;       // [shares][2]
-    int64_t q_t, q_h, T, pages, slots;
-    int B, width, page_shift, page, block_shift, marks, H, Hq, group, per_seq, Dk, Dv, nk, nv, ring, tmem_cols;
+    int64_t q_t, q_h, T, pages;
+    int slots;
+    int B, width, page_shift, page, block_shift, marks, H, Hq, group, per_seq, Dk, Dv, nk, nv;
+    int ring, q_bufs, o_bufs, tmem_cols;  // buffers of chunks, of queries, of O
     int q_vec;
     float scale_log2;
     int* status;
@@ -188,44 +194,40 @@ __device__ __forceinline__ void sts_v2(uint32_t addr, uint32_t a, uint32_t b) {
 // A slot is a tile of R query rows of one sequence (row = token * group + head in
 // the group); slots of sequence b start at first(b) = cu[b] * group / R + b.
 struct Slot {
-    int64_t lo;  // the sequence's first row of q
+    int lo;  // the sequence's first row of q
     int b, n, len, rho0, rows, tiles;
 };
 
-struct Lengths {  // in shared memory when they fit
-    const int32_t *length, *cu;
-};
-
 template <int R>
-__device__ __forceinline__ int64_t first_slot(const AttnParams& p, const Lengths& s, int b) {
-    return (int64_t)s.cu[b] * p.group / R + b;
+__device__ __forceinline__ int first_slot(const AttnParams& p, int b) {
+    return (int)((int64_t)p.cu[b] * p.group / R) + b;
 }
 
 // What slot holds; b: a sequence at or before the slot's.
 template <int R>
-__device__ __forceinline__ Slot read_slot(const AttnParams& p, const Lengths& s, int64_t slot, int b) {
+__device__ __forceinline__ Slot read_slot(const AttnParams& p, int slot, int b) {
     Slot x;
-    int64_t j;
+    int j;
     if (p.cu) {
-        while (b + 1 < p.B && first_slot<R>(p, s, b + 1) <= slot) ++b;
-        x.lo = s.cu[b];
-        const int64_t n = (int64_t)s.cu[b + 1] - x.lo;
+        while (b + 1 < p.B && first_slot<R>(p, b + 1) <= slot) ++b;
+        x.lo = p.cu[b];
+        const int64_t n = (int64_t)p.cu[b + 1] - x.lo;
         const bool fine = x.lo >= 0 && n >= 0 && x.lo + n <= p.T;
         if (!fine) record_status(p.status, MLA_ERR_INVALID_ARG);
         x.n = fine ? (int)n : 0;
-        j = slot - first_slot<R>(p, s, b);
+        j = fine ? slot - first_slot<R>(p, b) : 0;
     } else {
-        b = (int)(slot / p.per_seq);
-        j = slot - (int64_t)b * p.per_seq;
+        b = slot / p.per_seq;
+        j = slot - b * p.per_seq;
         x.lo = b;
         x.n = 1;
     }
     x.b = b;
-    const int64_t total = (int64_t)x.n * p.group, left = total - j * R;
-    x.rho0 = (int)(j * R);
+    const int64_t left = (int64_t)x.n * p.group - (int64_t)j * R;
+    x.rho0 = j * R;
     x.rows = j < 0 || left <= 0 ? 0 : left < R ? (int)left : R;
     const int64_t room = (int64_t)p.width << p.page_shift;
-    const int len = s.length[b];
+    const int len = p.length[b];
     x.len = len < 0 ? 0 : len > room ? (int)room : len;
     if (x.rows > 0 && x.len != len) record_status(p.status, MLA_ERR_POS_RANGE);
     int limit = x.len - x.n + (x.rho0 + x.rows - 1) / p.group + 1;
@@ -234,33 +236,10 @@ __device__ __forceinline__ Slot read_slot(const AttnParams& p, const Lengths& s,
     return x;
 }
 
-// The pieces of a share, in order: tiles [t0, t1) of one slot and head. Every
-// role of the block walks the same pieces.
-template <int R>
-struct Walk {
+// A piece of a share: tiles [t0, t1) of a slot and head. t1 == 0: no more.
+struct Piece {
     Slot x;
-    int64_t slot;
-    int h, t0, t1, left;
-
-    __device__ __forceinline__ bool next(const AttnParams& p, const Lengths& s) {
-        if (left <= 0) return false;
-        if (t1 > 0) {  // not the first: to the next slot that has work
-            t1 = 0;
-            t0 = 0;
-            do {
-                if (++slot == p.slots) {
-                    slot = 0;
-                    x.b = 0;
-                    ++h;
-                }
-                x = read_slot<R>(p, s, slot, x.b);
-            } while (x.tiles == 0 && h < p.H);
-        }
-        const int n = x.tiles - t0;
-        t1 = t0 + (n < left ? n : left);
-        left -= t1 - t0;
-        return h < p.H && t1 > t0;
-    }
+    int h, t0, t1;
 };
 
 // A ring slot and its phase, advanced chunk by chunk.
@@ -278,27 +257,31 @@ struct Ring {
 template <int R>
 struct Shared {  // behind the ring, the queries and the probabilities
     uint64_t full[14], empty[14];
-    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], m_full[kMarkTiles], m_empty[kMarkTiles], q_full, drain;
+    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], m_full[kMarkTiles], m_empty[kMarkTiles];
+    // by piece: dealt out; its queries; the rows' numbers below; its sums; its O
+    uint64_t piece_full[kPieces], piece_empty[kPieces], q_full[2], q_empty[2], rows_full[2], sums_full[2], sums_empty[2];
+    uint64_t o_full[2], o_empty[2], drain;
+    Piece piece[kPieces];
     uint32_t marks[kMarkTiles][kTokens / 4][2];  // scale bytes of four tokens: keys', values'
     // query rows, by the piece's parity
-    int64_t row_at[2][R];                        // row of out
+    int row_at[2][R];                            // row of out
     alignas(16) float unit[2][R];                // 2^-exponent of the row
     int limit[2][R];                             // the last position that it sees
+    alignas(16) float ref[2][kStreams<R>][R];    // minus the reference of the row's scores
+    float sums[2][kStreams<R>][4][R];            // of probabilities, by the four warps
+    int top_e[2][kStreams<R>];
+    int nan_at[2][512];                          // by channel: the first position with a NaN that not every row sees
+    int nan_seen[2];
+    float out_factor[kStreams<R>][R];
     // by stream
-    alignas(16) float ref[2][kStreams<R>][R];    // reference of the row's scores (and the piece's parity)
     float factor[kStreams<R>][R];
     float warp_row[kStreams<R>][4][R];
     int warp_e[kStreams<R>][4];
-    int top_e[kStreams<R>];
     int vote[kStreams<R>][3];
-    int nan_seen, leave;
     uint32_t tmem;
     volatile int abort;
-    int64_t scan[kThreads / 32 + 1];
-    int64_t start_slot;
-    int start_b, start_off;
-    int nan_at[512];                             // by channel: the first position with a NaN that not every row sees
-    int32_t length[kHeldSeqs], cu[kHeldSeqs + 1];
+    int64_t scan[kThreads / 32];
+    int start_slot, start_b, start_off;
 };
 static_assert(sizeof(Shared<32>) <= 10240, "latents of five chunks: two tiles, the queries and the rest fill shared memory");
 
@@ -310,14 +293,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    const uint32_t q_base = base + p.ring * kChunk;
-    const uint32_t p_base = q_base + p.nk * (N2 * 128);
+    const uint32_t q_base = base + p.ring * kChunk, q_bytes = p.nk * (N2 * 128);
+    const uint32_t p_base = q_base + p.q_bufs * q_bytes;
     Shared<R>& sh = *reinterpret_cast<Shared<R>*>(smem_raw + (p_base - raw) + 2 * N2 * 128);
     const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
     const uint32_t s_full = smem_u32(&sh.s_full[0]), s_empty = smem_u32(&sh.s_empty[0]);
     const uint32_t p_full = smem_u32(&sh.p_full[0]), p_empty = smem_u32(&sh.p_empty[0]);
     const uint32_t m_full = smem_u32(&sh.m_full[0]), m_empty = smem_u32(&sh.m_empty[0]);
-    const uint32_t q_full = smem_u32(&sh.q_full), drain = smem_u32(&sh.drain);
+    const uint32_t piece_full = smem_u32(&sh.piece_full[0]), piece_empty = smem_u32(&sh.piece_empty[0]);
+    const uint32_t q_full = smem_u32(&sh.q_full[0]), q_empty = smem_u32(&sh.q_empty[0]);
+    const uint32_t rows_full = smem_u32(&sh.rows_full[0]);
+    const uint32_t sums_full = smem_u32(&sh.sums_full[0]), sums_empty = smem_u32(&sh.sums_empty[0]);
+    const uint32_t o_full = smem_u32(&sh.o_full[0]), o_empty = smem_u32(&sh.o_empty[0]);
+    const uint32_t drain = smem_u32(&sh.drain);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort_flag = &sh.abort;
 
@@ -326,49 +314,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(full0 + 8 * i, 1);
             mbar_init(empty0 + 8 * i, 1);
         }
+        for (int i = 0; i < kMarkTiles; ++i) {
+            mbar_init(m_full + 8 * i, 32);
+            mbar_init(m_empty + 8 * i, kFour);
+        }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(piece_full + 8 * i, 1);
+            mbar_init(piece_empty + 8 * i, kPieceReaders);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + 8 * i, 1);
             mbar_init(s_empty + 8 * i, kFour);
             mbar_init(p_full + 8 * i, kFour);
             mbar_init(p_empty + 8 * i, 1);
+            mbar_init(q_full + 8 * i, 4);
+            mbar_init(q_empty + 8 * i, 1);
+            mbar_init(rows_full + 8 * i, 4);
+            mbar_init(sums_full + 8 * i, kSoftWarps);
+            mbar_init(sums_empty + 8 * i, 4);
+            mbar_init(o_full + 8 * i, 1);
+            mbar_init(o_empty + 8 * i, 4);
+            sh.nan_seen[i] = 0;
         }
-        for (int i = 0; i < kMarkTiles; ++i) {
-            mbar_init(m_full + 8 * i, 32);
-            mbar_init(m_empty + 8 * i, kFour);
-        }
-        mbar_init(q_full, kSoftWarps);
         mbar_init(drain, 1);
         sh.abort = 0;
         for (int i = 0; i < kStreams; ++i) sh.vote[i][0] = sh.vote[i][1] = sh.vote[i][2] = 0;
-        sh.nan_seen = sh.leave = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&k_map);
         if (!SHARED) tma_prefetch_desc(&v_map);
     }
-    __syncwarp();
     if (warp == kIssuer) {
         tmem_alloc(smem_u32(&sh.tmem), p.tmem_cols);
         tmem_relinquish();
     }
     // columns of the queries past Dk meet zeros of the cache: they have to be numbers
-    for (uint32_t i = tid * 16; i < (uint32_t)p.nk * N2 * 128; i += kThreads * 16) sts_v4(q_base + i, 0, 0, 0, 0);
-    for (int i = tid; i < 512; i += kThreads) sh.nan_at[i] = 0x7FFFFFFF;
+    for (uint32_t i = tid * 16; i < p.q_bufs * q_bytes; i += kThreads * 16) sts_v4(q_base + i, 0, 0, 0, 0);
+    for (int i = tid; i < 1024; i += kThreads) (&sh.nan_at[0][0])[i] = 0x7FFFFFFF;
     grid_launch_next();
     grid_wait_previous();
 
     // ------------------------------------------------------------ the share
-    Lengths seqs{p.length, p.cu};
-    if (p.B <= kHeldSeqs) {
-        for (int i = tid; i < p.B; i += kThreads) sh.length[i] = p.length[i];
-        if (p.cu)
-            for (int i = tid; i <= p.B; i += kThreads) sh.cu[i] = p.cu[i];
-        seqs = {sh.length, sh.cu};
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const int64_t per_thread = (p.slots + kThreads - 1) / kThreads;
-    const int64_t my_slot = per_thread * tid;
+    const int per_thread = (p.slots + kThreads - 1) / kThreads, my_slot = per_thread * tid;
     int64_t mine = 0;
     int my_b = 0;
     if (my_slot < p.slots) {
@@ -376,13 +362,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             int hi = p.B;
             while (hi - my_b > 1) {
                 const int mid = (my_b + hi) / 2;
-                if (first_slot<R>(p, seqs, mid) <= my_slot) my_b = mid;
+                if (first_slot<R>(p, mid) <= my_slot) my_b = mid;
                 else hi = mid;
             }
         }
         int b = my_b;
-        for (int64_t i = my_slot; i < my_slot + per_thread && i < p.slots; ++i) {
-            const Slot x = read_slot<R>(p, seqs, i, b);
+        for (int i = my_slot; i < my_slot + per_thread && i < p.slots; ++i) {
+            const Slot x = read_slot<R>(p, i, b);
             b = x.b;
             mine += x.tiles;
         }
@@ -394,48 +380,103 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane >= o) upto += v;
     }
     if (lane == 31) sh.scan[warp] = upto;
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
     int64_t line = 0;  // tiles of one head
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) upto += sh.scan[w];
         line += sh.scan[w];
     }
+    // equal shares, the first `all % shares` one tile longer
     const int64_t all = line * p.H;
     const int64_t shares = all < (int64_t)gridDim.x ? all : (int64_t)gridDim.x;
-    const int64_t c = blockIdx.x;
-    const int64_t w0 = c < shares ? all * c / shares : 0, w1 = c < shares ? all * (c + 1) / shares : 0;
-    if (w1 > w0) {
-        const int64_t at = w0 % line;
+    const int c = blockIdx.x;
+    int tiles = 0, h0 = 0;
+    if (c < shares) {
+        int64_t each, w0;
+        if (all < kI32Max) {
+            each = (uint32_t)all / (uint32_t)shares;
+            const int more = (int)(all - each * shares);
+            w0 = c * each + (c < more ? c : more);
+            tiles = (int)each + (c < more);
+            h0 = (int)((uint32_t)w0 / (uint32_t)line);
+        } else {
+            each = all / shares;
+            const int64_t more = all - each * shares;
+            w0 = c * each + (c < more ? c : more);
+            tiles = (int)(each + (c < more));
+            h0 = (int)(w0 / line);
+        }
+        const int64_t at = w0 - h0 * line;
         if (at >= upto - mine && at < upto) {  // one thread's
-            int64_t before = upto - mine, i = my_slot;
+            int64_t before = upto - mine;
             int b = my_b;
-            for (;; ++i) {
-                const Slot x = read_slot<R>(p, seqs, i, b);
+            for (int i = my_slot;; ++i) {
+                const Slot x = read_slot<R>(p, i, b);
                 b = x.b;
-                if (at < before + x.tiles) break;
+                if (at < before + x.tiles) {
+                    sh.start_slot = i;
+                    sh.start_b = b;
+                    sh.start_off = (int)(at - before);
+                    break;
+                }
                 before += x.tiles;
             }
-            sh.start_slot = i;
-            sh.start_b = b;
-            sh.start_off = (int)(at - before);
         }
     }
     __syncthreads();
     const uint32_t tmem = sh.tmem;
-    const int tiles = (int)(w1 - w0);
-    Walk<R> walk;
-    walk.left = tiles;
-    walk.t1 = 0;
-    if (tiles > 0) {
-        walk.slot = sh.start_slot;
-        walk.h = (int)(w0 / line);
-        walk.t0 = sh.start_off;
-        walk.x = read_slot<R>(p, seqs, walk.slot, sh.start_b);
-    }
-    int parts = 0;  // thread 0: which of the share's two places in the workspace it has filled
-    const uint32_t s_tmem = tmem, o_tmem = tmem + 2 * N2;
+    const uint32_t s_tmem = tmem, o_tmem = tmem + 2 * N2, o_cols = kStreams * p.nv * N2;  // o_cols: of one O buffer
+    // Piece i as its readers get it; each says once per warp that it has read it.
+    auto get_piece = [&](int i, Piece& x) {
+        const bool ok = wait(piece_full + 8 * (i % kPieces), (uint32_t)(i / kPieces) & 1u, abort_flag);
+        x = sh.piece[i % kPieces];
+        if (!ok) x.t0 = x.t1 = 0;
+        return ok;
+    };
 
-    if (warp == kLoader) {
+    if (warp == kDealer) {
+        if (lane == 0) {
+            int left = tiles, i = 0;
+            Piece x;
+            bool ok = true;
+            if (left > 0) {
+                int slot = sh.start_slot;
+                x.x = read_slot<R>(p, slot, sh.start_b);
+                x.h = h0;
+                x.t0 = sh.start_off;
+                for (;; ++i) {
+                    const int n = x.x.tiles - x.t0;
+                    x.t1 = x.t0 + (n < left ? n : left);
+                    left -= x.t1 - x.t0;
+                    if (i >= kPieces) ok = wait(piece_empty + 8 * (i % kPieces), (uint32_t)(i / kPieces - 1) & 1u, abort_flag);
+                    if (!ok) break;
+                    sh.piece[i % kPieces] = x;
+                    mbar_arrive(piece_full + 8 * (i % kPieces));
+                    if (left <= 0) {
+                        ++i;
+                        break;
+                    }
+                    x.t0 = 0;
+                    do {
+                        if (++slot == p.slots) {
+                            slot = 0;
+                            x.x.b = 0;
+                            ++x.h;
+                        }
+                        x.x = read_slot<R>(p, slot, x.x.b);
+                    } while (x.x.tiles == 0);
+                }
+            }
+            if (ok && i >= kPieces) ok = wait(piece_empty + 8 * (i % kPieces), (uint32_t)(i / kPieces - 1) & 1u, abort_flag);
+            if (ok) {
+                sh.piece[i % kPieces].t0 = sh.piece[i % kPieces].t1 = 0;
+                mbar_arrive(piece_full + 8 * (i % kPieces));
+            }
+        }
+        __syncwarp();
+    } else if (warp == kLoader) {
         // ---------------------------------------------------------- producer
         // tile t's keys, then tile t - 1's values: the order in which they are used
         Ring ring;
@@ -446,13 +487,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             int entry, place, h;
             bool have;
         };
-        auto look_up = [&](const Slot& x, int h, int tile) {
+        auto look_up = [&](const Piece& x, int tile) {
             const int at = tile * kTokens + lane * box;
             Tile k;
-            k.have = lane < boxes && at < x.len;
-            k.entry = k.have ? p.table[(int64_t)x.b * p.width + (at >> p.page_shift)] : 0;
+            k.have = lane < boxes && at < x.x.len;
+            k.entry = k.have ? p.table[(int64_t)x.x.b * p.width + (at >> p.page_shift)] : 0;
             k.place = (tile * kTokens) & (p.page - 1);
-            k.h = h;
+            k.h = x.h;
             return k;
         };
         auto load = [&](const CUtensorMap* map, const Tile& k, int chunks) {
@@ -462,22 +503,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 page = (int)p.pages;  // reads as zeros
             }
             const int count = __popc(__ballot_sync(0xFFFFFFFFu, k.have));
+#pragma unroll 1
             for (int j = 0; j < chunks && ok; ++j) {
                 bool got = true;
+                const uint32_t full = full0 + 8 * ring.i, to = base + ring.i * kChunk;
                 if (lane == 0) {
-                    const uint32_t full = full0 + 8 * ring.i;
                     got = filled < p.ring || wait(empty0 + 8 * ring.i, ring.phase ^ 1u, abort_flag);
-                    if (got) {
-                        mbar_arrive_expect_tx(full, count * box * 128);
-                        if (boxes == 1 && count == 1)
-                            tma_load_page(base + ring.i * kChunk, map, j * 128, k.place, k.h, page, full);
-                    }
+                    if (got) mbar_arrive_expect_tx(full, count * box * 128);
                 }
-                if (boxes > 1) {
+                if (boxes == 1) {
+                    if (lane == 0 && got && count) tma_load_page(to, map, j * 128, k.place, k.h, page, full);
+                } else {
+#pragma unroll 1
                     for (int i = 0; i < count; ++i) {
                         const int from = __shfl_sync(0xFFFFFFFFu, page, i);
-                        if (lane == 0 && got)
-                            tma_load_page(base + ring.i * kChunk + i * box * 128, map, j * 128, 0, k.h, from, full0 + 8 * ring.i);
+                        if (lane == 0 && got) tma_load_page(to + i * box * 128, map, j * 128, 0, k.h, from, full);
                     }
                 }
                 ok = __shfl_sync(0xFFFFFFFFu, got, 0);
@@ -486,28 +526,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++filled;
             }
         };
-        if (tiles > 0) {
-            Walk<R> w = walk;
-            w.next(p, seqs);
-            int tile = w.t0;
-            Tile now = look_up(w.x, w.h, tile), before = now, next = now;
+        Piece x;
+        int i = 0;
+        auto next_piece = [&]() {
+            ok = get_piece(i, x);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (lane == 0) mbar_arrive(piece_empty + 8 * (i % kPieces));
+            ++i;
+        };
+        next_piece();
+        if (ok && x.t1 > 0) {
+            int tile = x.t0;
+            Tile now = look_up(x, tile), before = now, next = now;
             for (int t = 0; t <= tiles && ok; ++t) {
                 if (t + 1 < tiles) {  // the next tile's entry is on its way while this one waits for room
-                    if (++tile == w.t1) {
-                        w.next(p, seqs);
-                        tile = w.t0;
+                    if (++tile == x.t1) {
+                        next_piece();
+                        tile = x.t0;
                     }
-                    next = look_up(w.x, w.h, tile);
+                    if (ok) next = look_up(x, tile);
                 }
-                if (t < tiles) load(&k_map, now, p.nk);
+                if (t < tiles && ok) load(&k_map, now, p.nk);
                 if (!SHARED && t > 0 && ok) load(&v_map, before, p.nv);
                 before = now;
                 now = next;
             }
-            if (!ok && lane == 0) {  // copies in flight land before the block leaves
-                for (int j = filled > p.ring ? filled - p.ring : 0; j < filled; ++j)
-                    mbar_wait(full0 + 8 * (j % p.ring), (uint32_t)(j / p.ring) & 1u, nullptr, 200000000ull);
-            }
+        }
+        if (!ok && lane == 0) {  // copies in flight land before the block leaves
+            for (int j = filled > p.ring ? filled - p.ring : 0; j < filled; ++j)
+                mbar_wait(full0 + 8 * (j % p.ring), (uint32_t)(j / p.ring) & 1u, nullptr, 200000000ull);
         }
         __syncwarp();
     } else if (warp == kIssuer) {
@@ -517,28 +564,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t dk = desc_kmajor_sw128(base), dv = desc_mnmajor_sw128(base, kChunk);
             const uint64_t dq = desc_kmajor_sw128(q_base), dw = desc_weights(p_base);
             const int last_steps = (p.Dk - (p.nk - 1) * 128 + 31) / 32;  // of the last chunk of the keys
-            Ring ring;              // next chunk in the order of use
-            int tile_slot = 0;      // SHARED: ring slot of tile t - 1's first chunk
+            Ring ring;                 // next chunk in the order of use
+            int tile_slot = 0;         // SHARED: ring slot of tile t - 1's first chunk
+            int i = -1, left = 0;      // the keys' piece and its tiles that are left
+            int vi = 0, v_at = 0;      // the values' (tile t - 1's) piece, and its tiles so far
+            int v_len = 0, len = 0;
             bool ok = true;
-            int in_piece = 0, in_piece_before = 0;  // tiles of the piece in front of this one
-            Walk<R> w = walk;
-            w.next(p, seqs);
-            uint32_t q_phase = 0;
             for (int t = 0; t <= tiles && ok; ++t) {
                 const int this_slot = ring.i;
                 const uint32_t buf = t & 1;
+                const int len_before = len;
                 if (t < tiles) {
-                    if (in_piece == 0) {
-                        ok = wait(q_full, q_phase, abort_flag);
-                        q_phase ^= 1u;
+                    if (left == 0) {
+                        Piece x;
+                        ++i;
+                        ok = get_piece(i, x);
+                        mbar_arrive(piece_empty + 8 * (i % kPieces));
+                        len = left = x.t1 - x.t0;
+                        const int use = p.q_bufs == 2 ? i >> 1 : i;
+                        ok = ok && wait(q_full + 8 * (p.q_bufs == 2 ? i & 1 : 0), (uint32_t)use & 1u, abort_flag);
                     }
                     ok = ok && (t < 2 || wait(s_empty + 8 * buf, (uint32_t)((t >> 1) - 1) & 1u, abort_flag));
-                    const uint32_t d = s_tmem + buf * N2;
+                    const uint32_t d = s_tmem + buf * N2, qb = p.q_bufs == 2 ? (i & 1) : 0;
+                    uint32_t qt = qb * q_bytes;
+#pragma unroll 1
                     for (int j = 0; j < p.nk && ok; ++j) {
                         ok = wait(full0 + 8 * ring.i, ring.phase, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t at = ring.i * kChunk, qt = j * (N2 * 128);
+                        const uint32_t at = ring.i * kChunk;
                         if (j < p.nk - 1 || last_steps == 4) {
 #pragma unroll
                             for (int s = 0; s < 4; ++s)
@@ -551,18 +605,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (!SHARED) mma_commit(empty0 + 8 * ring.i);
                         ring.step(p.ring);
+                        qt += N2 * 128;
                     }
                     if (!ok) break;
                     mma_commit(s_full + 8 * buf);
+                    if (--left == 0) mma_commit(q_empty + 8 * qb);
                 }
                 if (t > 0) {
                     const int u = t - 1;
-                    const uint32_t ub = u & 1;
-                    ok = wait(p_full + 8 * ub, (uint32_t)(u >> 1) & 1u, abort_flag);
+                    const uint32_t ub = u & 1, ob = p.o_bufs == 2 ? (vi & 1) : 0;
+                    const int use = p.o_bufs == 2 ? vi >> 1 : vi;
+                    if (v_at == 0) {
+                        v_len = len_before;
+                        ok = use == 0 || wait(o_empty + 8 * ob, (uint32_t)(use - 1) & 1u, abort_flag);
+                    }
+                    ok = ok && wait(p_full + 8 * ub, (uint32_t)(u >> 1) & 1u, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t pt = ub * (N2 * 128), d = o_tmem + (kStreams == 2 ? ub * p.nv * N2 : 0);
-                    const bool fresh = in_piece_before < kStreams;  // the stream's first tile of the piece
+                    const uint32_t pt = ub * (N2 * 128);
+                    uint32_t d = o_tmem + ob * o_cols + (kStreams == 2 ? ub * p.nv * N2 : 0);
+                    const bool fresh = v_at < kStreams;  // the stream's first tile of the piece
+#pragma unroll 1
                     for (int j = 0; j < p.nv && ok; ++j) {
                         int slot = ring.i;
                         if (SHARED) {
@@ -576,26 +639,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t at = slot * kChunk;
 #pragma unroll
                         for (int s = 0; s < 4; ++s)
-                            mma_f8(d + j * N2, desc_at(dv, at + 4096 * s), desc_at(dw, pt + 512 * s), i_o, !fresh || s != 0);
+                            mma_f8(d, desc_at(dv, at + 4096 * s), desc_at(dw, pt + 512 * s), i_o, !fresh || s != 0);
+                        d += N2;
                         if (!SHARED) {
                             mma_commit(empty0 + 8 * ring.i);
                             ring.step(p.ring);
                         }
                     }
                     if (!ok) break;
-                    if (SHARED)
+                    if (SHARED) {
+#pragma unroll 1
                         for (int j = 0; j < p.nk; ++j) {
                             const int slot = tile_slot + j;
                             mma_commit(empty0 + 8 * (slot >= p.ring ? slot - p.ring : slot));
                         }
+                    }
                     mma_commit(p_empty + 8 * ub);
+                    if (++v_at == v_len) {
+                        mma_commit(o_full + 8 * ob);
+                        v_at = 0;
+                        ++vi;
+                    }
                 }
                 tile_slot = this_slot;
-                in_piece_before = in_piece;
-                if (t < tiles && ++in_piece == w.t1 - w.t0) {
-                    in_piece = 0;
-                    w.next(p, seqs);
-                }
             }
             if (!ok) {
                 mma_commit(drain);
@@ -608,119 +674,133 @@ __global__ void __launch_bounds__(kThreads, 1)
         // By plain loads, four tokens to a lane (of one page: its size is a multiple of four), half of the tiles that
         // shared memory holds in flight. (A softmax thread that fetched its own token's waited for memory at every tile.)
         constexpr int kFlight = kMarkTiles / 2;
-        if (tiles > 0) {
-            Walk<R> w = walk;
-            w.next(p, seqs);
-            int tile = w.t0;
-            bool ok = true;
-            for (int t0 = 0; t0 < tiles && ok; t0 += kFlight) {
-                int64_t at[kFlight];
-                int place[kFlight], page[kFlight];
+        Piece x;
+        int i = 0, tile = 0;
+        x.t1 = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int t0 = 0; t0 < tiles && ok; t0 += kFlight) {
+            int place[kFlight], page[kFlight], head[kFlight];
 #pragma unroll
-                for (int i = 0; i < kFlight; ++i) {
-                    page[i] = -1;
-                    place[i] = 0;
-                    at[i] = 0;
-                    if (t0 + i >= tiles) continue;
-                    const int pos = tile * kTokens + lane * 4;
-                    if (pos < w.x.len) {
-                        place[i] = pos & (p.page - 1);
-                        page[i] = p.table[(int64_t)w.x.b * p.width + (pos >> p.page_shift)];
-                        at[i] = w.h;
-                    }
-                    if (++tile == w.t1) {
-                        w.next(p, seqs);
-                        tile = w.t0;
+            for (int f = 0; f < kFlight; ++f) {
+                page[f] = -1;
+                place[f] = head[f] = 0;
+                if (t0 + f >= tiles || !ok) continue;
+                if (tile == x.t1) {
+                    ok = get_piece(i, x);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (lane == 0) mbar_arrive(piece_empty + 8 * (i % kPieces));
+                    ++i;
+                    if (!ok) continue;
+                    tile = x.t0;
+                }
+                const int pos = tile * kTokens + lane * 4;
+                if (pos < x.x.len) {
+                    place[f] = pos & (p.page - 1);
+                    page[f] = p.table[(int64_t)x.x.b * p.width + (pos >> p.page_shift)];
+                    head[f] = x.h;
+                }
+                ++tile;
+            }
+            const bool one = p.block_shift >= 2;  // one scale for the lane's four tokens
+            uint32_t k[kFlight], v[kFlight];
+            if (one) {
+#pragma unroll
+                for (int f = 0; f < kFlight; ++f) {
+                    // a bad page is recorded by the producer and reads as zeros; so do its scales
+                    k[f] = v[f] = 0;
+                    if (page[f] >= 0 && page[f] < p.pages) {
+                        const int64_t m = ((int64_t)page[f] * p.H + head[f]) * p.marks + (place[f] >> p.block_shift);
+                        k[f] = p.k_scales[m];
+                        if (!SHARED) v[f] = p.v_scales[m];
                     }
                 }
-                const bool one = p.block_shift >= 2;  // one scale for the lane's four tokens
-                uint32_t k[kFlight][4], v[kFlight][4];
+            } else {
 #pragma unroll
-                for (int i = 0; i < kFlight; ++i) {
-                    // a bad page is recorded by the producer and reads as zeros; so do its scales
-                    const bool have = page[i] >= 0 && page[i] < p.pages;
-                    const int64_t m = ((int64_t)page[i] * p.H + at[i]) * p.marks;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        k[i][j] = v[i][j] = 0;
-                        if (have && (j == 0 || !one)) {
-                            k[i][j] = p.k_scales[m + ((place[i] + j) >> p.block_shift)];
-                            if (!SHARED) v[i][j] = p.v_scales[m + ((place[i] + j) >> p.block_shift)];
+                for (int f = 0; f < kFlight; ++f) {
+                    k[f] = v[f] = 0;
+                    if (page[f] >= 0 && page[f] < p.pages) {
+                        const int64_t m = ((int64_t)page[f] * p.H + head[f]) * p.marks;
+#pragma unroll 1
+                        for (int j = 3; j >= 0; --j) {
+                            k[f] = k[f] << 8 | p.k_scales[m + ((place[f] + j) >> p.block_shift)];
+                            if (!SHARED) v[f] = v[f] << 8 | p.v_scales[m + ((place[f] + j) >> p.block_shift)];
                         }
                     }
                 }
+            }
 #pragma unroll
-                for (int i = 0; i < kFlight; ++i) {
-                    const int t = t0 + i, s = t % kMarkTiles;
-                    if (t >= tiles || !ok) continue;
-                    if (t >= kMarkTiles) ok = wait(m_empty + 8 * s, (uint32_t)(t / kMarkTiles - 1) & 1u, abort_flag);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    const uint32_t kw = one ? k[i][0] * 0x01010101u : k[i][0] | k[i][1] << 8 | k[i][2] << 16 | k[i][3] << 24;
-                    const uint32_t vw = SHARED ? kw : one ? v[i][0] * 0x01010101u : v[i][0] | v[i][1] << 8 | v[i][2] << 16 | v[i][3] << 24;
-                    sh.marks[s][lane][0] = kw;
-                    sh.marks[s][lane][1] = vw;
-                    mbar_arrive(m_full + 8 * s);
-                }
+            for (int f = 0; f < kFlight; ++f) {
+                const int t = t0 + f, s = t % kMarkTiles;
+                if (t >= tiles || !ok) continue;
+                if (t >= kMarkTiles) ok = wait(m_empty + 8 * s, (uint32_t)(t / kMarkTiles - 1) & 1u, abort_flag);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                const uint32_t kw = one ? k[f] * 0x01010101u : k[f], vw = one ? v[f] * 0x01010101u : v[f];
+                sh.marks[s][lane][0] = kw;
+                sh.marks[s][lane][1] = SHARED ? kw : vw;
+                mbar_arrive(m_full + 8 * s);
             }
         }
         __syncwarp();
-    } else if (tiles > 0) {
-        // ------------------------------------------------------------ softmax
-        constexpr int kFours = kFour / 4, RT = R / kFours;  // rows of a thread
-        const int tok = tid & 127, quad = warp & 3, stream = kStreams == 2 ? warp >> 2 : 0;
-        const int r_lo = kStreams == 2 ? 0 : (warp >> 2) * RT;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;  // this warp's lanes of tensor memory
-        const uint32_t my_bar = 1 + stream, all_bar = 3;
-        const uint32_t o_mine = o_tmem + lanes + stream * p.nv * N2;
-        // the query rows of a piece as two E4M3 numbers each, row r at r and R + r; a warp takes every kSoftWarps-th row
-        auto load_q = [&](const Walk<R>& w, int par) {
-            const int gran = p.Dk / 8;
-            constexpr int kBatch = R / kSoftWarps < 4 ? R / kSoftWarps : 4;
-            constexpr int kG = (kMaxQueryChunks * 128 / 8 + 31) / 32;
-            for (int r0 = warp; r0 < R; r0 += kBatch * kSoftWarps) {
-                uint4 g[kBatch][kG];
+    } else if (warp >= kHelper) {
+        // ------------------------------------------- queries in, results out
+        const int quad = warp & 3, htid = tid - 32 * kHelper;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        bool failed = false;
+        int parts = 0;  // which of the share's two places in the workspace it has filled
+        constexpr int kG = (kMaxQueryChunks * 128 / 8 + 31) / 32;
+        const int gran = p.Dk / 8;
+        // eight bf16 at a time of a piece's query row r, as many as a lane has
+        auto fetch = [&](const Piece& x, int r, uint4 (&g)[kG]) {
+            const int rho = x.x.rho0 + r, tok = rho / p.group;
+            const uint16_t* src = p.q + (int64_t)(x.x.lo + tok) * p.q_t + (int64_t)(x.h * p.group + rho - tok * p.group) * p.q_h;
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int r = r0 + i * kSoftWarps, rho = w.x.rho0 + r, at_tok = rho / p.group;
-                    const uint16_t* src = p.q + (w.x.lo + at_tok) * p.q_t + (int64_t)(w.h * p.group + rho - at_tok * p.group) * p.q_h;
-#pragma unroll
-                    for (int k = 0; k < kG; ++k) {
-                        const int at = k * 32 + lane;
-                        g[i][k] = make_uint4(0, 0, 0, 0);
-                        if (r < w.x.rows && at < gran) {
-                            const uint16_t* q = src + at * 8;
-                            if (p.q_vec) {
-                                g[i][k] = *reinterpret_cast<const uint4*>(q);
-                            } else {
-                                g[i][k].x = q[0] | ((uint32_t)q[1] << 16);
-                                g[i][k].y = q[2] | ((uint32_t)q[3] << 16);
-                                g[i][k].z = q[4] | ((uint32_t)q[5] << 16);
-                                g[i][k].w = q[6] | ((uint32_t)q[7] << 16);
-                            }
-                        }
+            for (int k = 0; k < kG; ++k) {
+                const int at = k * 32 + lane;
+                g[k] = make_uint4(0, 0, 0, 0);
+                if (r < x.x.rows && at < gran) {
+                    const uint16_t* q = src + at * 8;
+                    if (p.q_vec) {
+                        g[k] = *reinterpret_cast<const uint4*>(q);
+                    } else {
+                        g[k].x = q[0] | ((uint32_t)q[1] << 16);
+                        g[k].y = q[2] | ((uint32_t)q[3] << 16);
+                        g[k].z = q[4] | ((uint32_t)q[5] << 16);
+                        g[k].w = q[6] | ((uint32_t)q[7] << 16);
                     }
                 }
+            }
+        };
+        // Piece i's query rows as two E4M3 numbers each, row r at r and R + r; a warp takes every fourth, the next one's
+        // memory on its way.
+        auto load_q = [&](const Piece& x, int i) {
+            const int par = i & 1;
+            const uint32_t qb = p.q_bufs == 2 ? par : 0;
+            uint4 g[kG], g2[kG];
+            fetch(x, quad, g);
+            const int use = p.q_bufs == 2 ? i >> 1 : i;
+            if (use > 0) failed |= !wait(q_empty + 8 * qb, (uint32_t)(use - 1) & 1u, abort_flag);
+#pragma unroll 1
+            for (int r = quad; r < R; r += 4) {
+                if (r + 4 < R) fetch(x, r + 4, g2);
+                uint32_t m = 0;
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int r = r0 + i * kSoftWarps;
-                    uint32_t m = 0;
+                for (int k = 0; k < kG; ++k) {
+                    const uint32_t u[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
 #pragma unroll
-                    for (int k = 0; k < kG; ++k) {
-                        const uint32_t u[4] = {g[i][k].x, g[i][k].y, g[i][k].z, g[i][k].w};
+                    for (int e = 0; e < 4; ++e) m = max(m, max((u[e] << 16) & 0x7FFFFFFFu, u[e] & 0x7FFF0000u));
+                }
+                m = __reduce_max_sync(0xFFFFFFFFu, m);
+                // a factor 2^f that brings the row's largest into [128, 256); NaN and Inf make the row's scale NaN
+                int f = 134 - (int)(m >> 23);
+                f = m == 0 ? 0 : f > 120 ? 120 : f;
+                const bool bad = m >= 0x7F800000u;
+                const float up = bad ? 0.f : __uint_as_float((uint32_t)(127 + f) << 23);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) m = max(m, max((u[e] << 16) & 0x7FFFFFFFu, u[e] & 0x7FFF0000u));
-                    }
-                    m = __reduce_max_sync(0xFFFFFFFFu, m);
-                    // a factor 2^x that brings the row's largest into [128, 256); NaN and Inf make the row's scale NaN
-                    int x = 134 - (int)(m >> 23);
-                    x = m == 0 ? 0 : x > 120 ? 120 : x;
-                    const bool bad = m >= 0x7F800000u;
-                    const float up = bad ? 0.f : __uint_as_float((uint32_t)(127 + x) << 23);
-#pragma unroll
-                    for (int k = 0; k < kG; ++k) {
-                        const int at = k * 32 + lane;
-                        if (at >= gran) continue;
-                        const uint32_t u[4] = {g[i][k].x, g[i][k].y, g[i][k].z, g[i][k].w};
+                for (int k = 0; k < kG; ++k) {
+                    const int at = k * 32 + lane;
+                    if (at < gran) {
+                        const uint32_t u[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
                         uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -731,46 +811,162 @@ __global__ void __launch_bounds__(kThreads, 1)
                             hi[e / 2] |= h2 << (16 * (e & 1));
                             lo[e / 2] |= cvt_e4m3x2((a - ha) * 32.f, (b - hb) * 32.f) << (16 * (e & 1));
                         }
-                        const uint32_t chunk = q_base + (at >> 4) * (N2 * 128);
-                        const uint32_t unit = (at & 15) >> 1, half = (at & 1) * 8;
-                        sts_v2(chunk + r * 128 + ((unit ^ (r & 7)) << 4) + half, hi[0], hi[1]);
-                        sts_v2(chunk + (R + r) * 128 + ((unit ^ (r & 7)) << 4) + half, lo[0], lo[1]);
+                        const uint32_t to = q_base + qb * q_bytes + (at >> 4) * (N2 * 128) + (((at & 15) >> 1 ^ (r & 7)) << 4) + (at & 1) * 8;
+                        sts_v2(to + r * 128, hi[0], hi[1]);
+                        sts_v2(to + (R + r) * 128, lo[0], lo[1]);
                     }
-                    if (lane == 0) {
-                        const int rr = r < w.x.rows ? r : w.x.rows - 1, rho = w.x.rho0 + rr, at_tok = rho / p.group;
-                        sh.unit[par][r] = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 - x) << 23);
-                        for (int k = 0; k < kStreams; ++k) sh.ref[par][k][r] = kNothing;
-                        sh.limit[par][r] = w.x.len - w.x.n + at_tok;
-                        sh.row_at[par][r] = (w.x.lo + at_tok) * p.Hq + (int64_t)w.h * p.group + rho - at_tok * p.group;
-                    }
+                    g[k] = g2[k];
+                }
+                if (lane == 0) {
+                    const int rr = r < x.x.rows ? r : x.x.rows - 1, rho = x.x.rho0 + rr, tok = rho / p.group;
+                    sh.unit[par][r] = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 - f) << 23);
+                    for (int k = 0; k < kStreams; ++k) sh.ref[par][k][r] = -kNothing;
+                    sh.limit[par][r] = x.x.len - x.x.n + tok;
+                    sh.row_at[par][r] = (x.x.lo + tok) * p.Hq + x.h * p.group + rho - tok * p.group;
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
-            named_bar_sync(all_bar, kSoftmax);
+            if (lane == 0) {
+                mbar_arrive(q_full + 8 * qb);
+                mbar_arrive(rows_full + 8 * par);
+            }
         };
-
-        Walk<R> w = walk;
-        bool more = w.next(p, seqs);
-        int par = 0, t = 0, turn = 0;  // t: tiles of the share so far; turn: this stream's
-        // A wait that gave up is reported with the stream's next vote, and the stream's with the end of the piece, so that
-        // all warps leave together: until then a thread that saw it goes on, through every barrier.
-        bool failed = false;
-        if (more) load_q(w, 0);
-        while (more) {
+        Piece now, next;
+        int i = 0;
+        auto read_piece = [&](int k, Piece& x) {
+            failed |= !get_piece(k, x);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(piece_empty + 8 * (k % kPieces));
+        };
+        read_piece(0, now);
+        const bool begin = named_bar_and(3, kHelpers, !failed) && now.t1 > 0;
+        if (begin) load_q(now, 0);
+        while (begin && now.t1 > 0) {
+            read_piece(i + 1, next);
+            if (next.t1 > 0) load_q(next, i + 1);
+            const int par = i & 1;
+            const uint32_t ob = p.o_bufs == 2 ? par : 0;
+            const int use = p.o_bufs == 2 ? i >> 1 : i;
+            failed |= !wait(sums_full + 8 * par, (uint32_t)(i >> 1) & 1u, abort_flag);
+            const bool whole = now.t0 == 0 && now.t1 == now.x.tiles;
+            const int part = 2 * c + (now.t0 == 0 ? 1 : 0);
+            if (htid < R) {
+                float m = kNothing, sum = 0.f, f[kStreams];
+                for (int k = 0; k < kStreams; ++k) m = fmaxf(m, -sh.ref[par][k][htid]);
+#pragma unroll
+                for (int k = 0; k < kStreams; ++k) {
+                    const float(&row)[4][R] = sh.sums[par][k];
+                    const float up = exp2_fast(-sh.ref[par][k][htid] - m);
+                    sum = fmaf(up, (row[0][htid] + row[1][htid]) + (row[2][htid] + row[3][htid]), sum);
+                    f[k] = ldexpf(up, sh.top_e[par][k] < 0 ? -131 : sh.top_e[par][k] - 131);
+                }
+                const float over = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+                for (int k = 0; k < kStreams; ++k) sh.out_factor[k][htid] = f[k] * over;
+                if (!whole) p.part_ml[(int64_t)part * R + htid] = make_float2(m, sum);
+                else if (p.lse && htid < now.x.rows)
+                    p.lse[sh.row_at[par][htid]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945309f;
+            }
+            failed |= !wait(o_full + 8 * ob, (uint32_t)use & 1u, abort_flag);
+            // every warp leaves with the others
+            if (!named_bar_and(3, kHelpers, !failed)) break;
+            tc_fence_after();
+            const bool nans = *(volatile int*)&sh.nan_seen[par] != 0;
+            constexpr int kStep = R < 16 ? R : 16;
+            const uint32_t from0 = o_tmem + ob * o_cols + lanes;
+#pragma unroll 1
+            for (int j = 0; j < p.nv; ++j) {
+                const int ch = j * 128 + quad * 32 + lane;
+                const int nan_at = nans ? sh.nan_at[par][ch & 511] : 0x7FFFFFFF;
+#pragma unroll 1
+                for (int r0 = 0; r0 < now.x.rows; r0 += kStep) {
+                    float o[kStep];
+#pragma unroll
+                    for (int k = 0; k < kStep; ++k) o[k] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kStreams; ++k) {
+                        if (sh.top_e[par][k] == 2 * kNoScale) continue;  // the same in every thread: a stream without a tile
+                        uint32_t v[16], u[16];
+                        const uint32_t from = from0 + (k * p.nv + j) * N2 + r0;
+                        __syncwarp();
+                        tmem_ld16(from, v);
+                        if constexpr (R > 8) tmem_ld16(from + R, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < kStep; ++e)
+                            o[e] = fmaf(fmaf(__uint_as_float(R > 8 ? u[e] : v[(8 + e) & 15]), 0.03125f, __uint_as_float(v[e])),
+                                        sh.out_factor[k][r0 + e], o[e]);
+                    }
+                    if (ch < p.Dv) {
+#pragma unroll
+                        for (int e = 0; e < kStep; ++e) {
+                            const int r = r0 + e;
+                            if (r < now.x.rows) {
+                                if (nan_at <= sh.limit[par][r]) o[e] = __uint_as_float(0x7FC00000u);
+                                if (whole) p.out[(int64_t)sh.row_at[par][r] * p.Dv + ch] = (uint16_t)pack_bf16x2(o[e], 0.f);
+                                else p.part_o[((int64_t)part * R + r) * p.Dv + ch] = o[e];
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            tc_fence_before();
+            if (nans) {  // the same in every thread: set before its sums were
+                named_bar_sync(3, kHelpers);
+                for (int k = htid; k < 512; k += kHelpers) sh.nan_at[par][k] = 0x7FFFFFFF;
+                if (htid == 0) sh.nan_seen[par] = 0;
+            }
+            named_bar_sync(3, kHelpers);  // out_factor and the rows are read
+            if (lane == 0) {
+                mbar_arrive(o_empty + 8 * ob);
+                mbar_arrive(sums_empty + 8 * par);
+            }
+            if (htid == 0 && !whole) {
+                p.meta[part] = make_int4(now.t0 == 0 ? kOpens : now.t1 == now.x.tiles ? kEnds : kGoesOn, now.x.rho0,
+                                         now.x.rows, now.x.lo * p.H + now.h);
+                parts |= 1 << (part & 1);
+            }
+            now = next;
+            ++i;
+        }
+        if (htid == 0)
+            for (int k = 0; k < 2; ++k)
+                if (!(parts >> k & 1)) p.meta[2 * c + k] = make_int4(kNoPart, 0, 0, 0);
+    } else {
+        // ------------------------------------------------------------ softmax
+        constexpr int kFours = kFour / 4, RT = R / kFours;  // rows of a thread
+        const int tok = tid & 127, quad = warp & 3, stream = kStreams == 2 ? warp >> 2 : 0;
+        const int r_lo = kStreams == 2 ? 0 : (warp >> 2) * RT;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;  // this warp's lanes of tensor memory
+        const uint32_t my_bar = 1 + stream;
+        int t = 0, turn = 0;  // t: tiles of the share so far; turn: of this stream's votes
+        // A wait that gave up is reported with the stream's next vote, so that its warps leave together: until then a
+        // thread that saw it goes on, through every barrier.
+        bool failed = false, leave = false;
+#pragma unroll 1
+        for (int i = 0; !leave; ++i) {
+            Piece w;
+            if (!named_bar_and(my_bar, kFour * 32, get_piece(i, w))) break;
+            if (lane == 0) mbar_arrive(piece_empty + 8 * (i % kPieces));
+            if (w.t1 == 0) break;
+            const int par = i & 1;
+            failed |= !wait(rows_full + 8 * par, (uint32_t)(i >> 1) & 1u, abort_flag);
             const float *unit = &sh.unit[par][r_lo], *ref = &sh.ref[par][stream][r_lo];
             const int* limit = &sh.limit[par][r_lo];
+            const uint32_t o_mine = o_tmem + lanes + (p.o_bufs == 2 ? par : 0) * o_cols + stream * p.nv * N2;
             float l[RT];
 #pragma unroll
             for (int r = 0; r < RT; ++r) l[r] = 0.f;
             int top_e = kNoScale;
             bool any = false;  // the stream has had a tile of the piece
             const int least = w.x.len - w.x.n + w.x.rho0 / p.group;  // the last position that every row sees
-            const int t_piece = t;
-            for (; t - t_piece < w.t1 - w.t0; ++t) {
+            const int t_end = t + w.t1 - w.t0, to_tile = w.t0 - t;
+#pragma unroll 1
+            for (; t < t_end; ++t) {
                 if (kStreams == 2 && (t & 1) != stream) continue;
-                const int tile = w.t0 + t - t_piece, buf = t & 1, pos = tile * kTokens + tok, slot = t % kMarkTiles;
+                const int tile = to_tile + t, buf = t & 1, pos = tile * kTokens + tok, slot = t % kMarkTiles;
                 const bool masked = (tile + 1) * kTokens - 1 > least;
                 const bool valid = pos < w.x.len;
                 failed |= !wait(m_full + 8 * slot, (uint32_t)(t / kMarkTiles) & 1u, abort_flag);
@@ -797,16 +993,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int r = 0; r < (RT < 16 ? RT : 16); r += 4) {
                             const float4 q = *reinterpret_cast<const float4*>(unit + r0 + r);
                             const float4 m = *reinterpret_cast<const float4*>(ref + r0 + r);
-                            const float qs[4] = {q.x, q.y, q.z, q.w}, ms[4] = {-m.x, -m.y, -m.z, -m.w};
+                            const float qs[4] = {q.x, q.y, q.z, q.w}, ms[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
-                            for (int i = 0; i < 4; i += 2) {
-                                const uint32_t *h = &v[r + i], *o = R > 8 ? &u[r + i] : &v[(8 + r + i) & 15];
-                                float &x0 = x[r0 + r + i], &x1 = x[r0 + r + i + 1];
+                            for (int e = 0; e < 4; e += 2) {
+                                const uint32_t *h = &v[r + e], *o = R > 8 ? &u[r + e] : &v[(8 + r + e) & 15];
+                                float &x0 = x[r0 + r + e], &x1 = x[r0 + r + e + 1];
                                 float k0, k1;
-                                mul2(k0, k1, qs[i], qs[i + 1], ks, ks);
+                                mul2(k0, k1, qs[e], qs[e + 1], ks, ks);
                                 fma2(x0, x1, __uint_as_float(o[0]), __uint_as_float(o[1]), 0.03125f, 0.03125f,
                                      __uint_as_float(h[0]), __uint_as_float(h[1]));
-                                if constexpr (decltype(less)::value) fma2(x0, x1, x0, x1, k0, k1, ms[i], ms[i + 1]);
+                                if constexpr (decltype(less)::value) fma2(x0, x1, x0, x1, k0, k1, ms[e], ms[e + 1]);
                                 else mul2(x0, x1, x0, x1, k0, k1);
                             }
                         }
@@ -833,8 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the place two turns on was read by all before this barrier and is written by none before the next
                 if (tid == stream * 128) sh.vote[stream][turn == 2 ? 0 : turn + 1] = 0;
                 if (vote & 2) {
-                    sh.leave = 1;
-                    t = t_piece + w.t1 - w.t0;
+                    leave = true;
                     break;
                 }
                 if (vote) {
@@ -850,21 +1045,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     named_bar_sync(my_bar, kFour * 32);
                     const int r = tid - stream * 128;
                     if (r < R) {
-                        const float old = sh.ref[par][stream][r];
+                        const float old = -sh.ref[par][stream][r];
                         float m = old;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) m = fmaxf(m, sh.warp_row[stream][i][r]);
-                        sh.ref[par][stream][r] = m;
+                        for (int k = 0; k < 4; ++k) m = fmaxf(m, sh.warp_row[stream][k][r]);
+                        sh.ref[par][stream][r] = -m;
                         sh.factor[stream][r] = exp2_fast(old - m);
                     }
                     const int old_e = top_e;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) top_e = max(top_e, sh.warp_e[stream][i]);
+                    for (int k = 0; k < 4; ++k) top_e = max(top_e, sh.warp_e[stream][k]);
                     named_bar_sync(my_bar, kFour * 32);
 #pragma unroll
-                    for (int i = 0; i < RT; ++i) {
-                        l[i] *= sh.factor[stream][r_lo + i];
-                        x[i] -= ref[i];
+                    for (int k = 0; k < RT; ++k) {
+                        l[k] *= sh.factor[stream][r_lo + k];
+                        x[k] += ref[k];
                     }
                     if (any) {
                         const float down = old_e == top_e ? 1.f : old_e < top_e - 126 ? 0.f : __uint_as_float((uint32_t)(127 + old_e - top_e) << 23);
@@ -872,17 +1067,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         failed |= !wait(p_empty + 8 * (u & 1), (uint32_t)(u >> 1) & 1u, abort_flag);
                         __syncwarp();
                         tc_fence_after();
+#pragma unroll 1
                         for (int j = 0; j < p.nv; ++j)
-#pragma unroll
+#pragma unroll 1
                             for (int r0 = 0; r0 < 2 * RT; r0 += 16) {
                                 uint32_t v[16];
-                                const int col = R == 8 ? 0 : r_lo + (r0 < RT ? r0 : R + r0 - RT);
+                                const int col = R == 8 ? 0 : r_lo + (r0 < RT ? r0 : R + r0 - RT), row = col < R ? col : col - R;
                                 const uint32_t at = o_mine + j * N2 + col;
                                 tmem_ld16(at, v);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    v[i] = __float_as_uint(__uint_as_float(v[i]) * sh.factor[stream][(col + i) % R] * down);
+                                for (int k = 0; k < 16; ++k)
+                                    v[k] = __float_as_uint(__uint_as_float(v[k]) * sh.factor[stream][R == 8 ? k % 8 : row + k] * down);
                                 tmem_st16(at, v);
                             }
                         tmem_st_wait();
@@ -901,19 +1097,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int r = 0; r < RT; r += 4) {
                         uint32_t h[2], o[2];
 #pragma unroll
-                        for (int i = 0; i < 4; i += 2) {
-                            const float a = exp2_fast(x[r + i]), b = exp2_fast(x[r + i + 1]);
-                            add2(l[r + i], l[r + i + 1], a, b);
+                        for (int k = 0; k < 4; k += 2) {
+                            const float a = exp2_fast(x[r + k]), b = exp2_fast(x[r + k + 1]);
+                            add2(l[r + k], l[r + k + 1], a, b);
                             float y, z;
                             mul2(y, z, a, b, f, f);
-                            split_weights(y, z, h[i / 2], o[i / 2]);
+                            split_weights(y, z, h[k / 2], o[k / 2]);
                         }
                         hi[r / 4] = __byte_perm(h[0], h[1], 0x5410);
                         lo[r / 4] = __byte_perm(o[0], o[1], 0x5410);
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < RT / 4; ++i) hi[i] = lo[i] = 0;
+                    for (int k = 0; k < RT / 4; ++k) hi[k] = lo[k] = 0;
                 }
                 if (t >= 2) failed |= !wait(p_empty + 8 * buf, (uint32_t)((t >> 1) - 1) & 1u, abort_flag);
                 const uint32_t to = p_base + buf * (N2 * 128) + tok * 16;
@@ -921,9 +1117,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sts_v4(to, hi[0], hi[1], lo[0], lo[1]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < RT / 16; ++i) {
-                        sts_v4(to + (r_lo / 16 + i) * 2048, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-                        sts_v4(to + ((R + r_lo) / 16 + i) * 2048, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+                    for (int k = 0; k < RT / 16; ++k) {
+                        sts_v4(to + (r_lo / 16 + k) * 2048, hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+                        sts_v4(to + ((R + r_lo) / 16 + k) * 2048, lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
                     }
                 }
                 if (r_lo == 0 && ((tile + 1) * kTokens > w.x.len || (masked && w.x.n > 1))) {
@@ -932,30 +1128,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     int64_t chunk;
                     if (SHARED) chunk = (int64_t)t * p.nk;
                     else chunk = (int64_t)(t + 2 < tiles ? t + 2 : tiles) * p.nk + (int64_t)t * p.nv;
+#pragma unroll 1
                     for (int j = 0; j < p.nv; ++j, ++chunk) {
                         const int at = (int)(chunk % p.ring);
                         failed |= !wait(full0 + 8 * at, (uint32_t)(chunk / p.ring) & 1u, abort_flag);
                         const uint32_t mem = base + at * kChunk + tok * 128;
                         if (!valid) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) sts_v4(mem + i * 16, 0, 0, 0, 0);
+                            for (int k = 0; k < 8; ++k) sts_v4(mem + k * 16, 0, 0, 0, 0);
                         } else if (pos > least) {
-                            for (int i = 0; i < 8; ++i) {
-                                const uint4 v = lds_v4(mem + ((i ^ (tok & 7)) << 4));
+#pragma unroll 1
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t place = mem + ((k ^ (tok & 7)) << 4);
+                                const uint4 v = lds_v4(place);
                                 uint32_t u[4] = {v.x, v.y, v.z, v.w};
                                 bool found = false;
-                                for (int k = 0; k < 4; ++k) found |= __vcmpeq4(u[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) found |= __vcmpeq4(u[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
                                 if (!found) continue;
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        if (((u[k] >> (8 * e)) & 0x7Fu) == 0x7Fu) {
-                                            atomicMin(&sh.nan_at[(j * 128 + i * 16 + k * 4 + e) & 511], pos);
-                                            u[k] &= ~(0xFFu << (8 * e));
-                                        }
-                                sts_v4(mem + ((i ^ (tok & 7)) << 4), u[0], u[1], u[2], u[3]);
-                                sh.nan_seen = 1;
+                                for (int e = 0; e < 16; ++e)
+                                    if (((u[e / 4] >> (8 * (e & 3))) & 0x7Fu) == 0x7Fu) {
+                                        atomicMin(&sh.nan_at[par][(j * 128 + k * 16 + e) & 511], pos);
+                                        u[e / 4] &= ~(0xFFu << (8 * (e & 3)));
+                                    }
+                                sts_v4(place, u[0], u[1], u[2], u[3]);
+                                sh.nan_seen[par] = 1;
                             }
                         }
                     }
@@ -965,106 +1162,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * buf);
             }
-            const Walk<R> done = w;
-            more = w.next(p, seqs);
-            const int last = t - 1;
-            if (more) {
-                // the products of this piece's queries are done once its last scores are there (the other stream's, maybe)
-                failed |= !wait(s_full + 8 * (last & 1), (uint32_t)(last >> 1) & 1u, abort_flag);
-                load_q(w, par ^ 1);
-            }
-            // ------------------------------------------------ the piece's result
-            const bool whole = done.t0 == 0 && done.t1 == done.x.tiles;
-            const int part = 2 * (int)c + (done.t0 == 0 ? 1 : 0);
+            if (leave) break;
+            // the piece's sums
+            if (i >= 2) failed |= !wait(sums_empty + 8 * par, (uint32_t)((i >> 1) - 1) & 1u, abort_flag);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 const float v = warp_add(l[r]);
-                if (lane == (r & 31)) sh.warp_row[stream][quad][r_lo + r] = v;
+                if (lane == (r & 31)) sh.sums[par][stream][quad][r_lo + r] = v;
             }
-            if (tok == 0 && r_lo == 0) sh.top_e[stream] = any ? top_e : 2 * kNoScale;
-            named_bar_sync(all_bar, kSoftmax);
-            if (*(volatile int*)&sh.leave) break;
-            if (tid < R) {
-                float m = kNothing, sum = 0.f, part_f[kStreams];
-                for (int k = 0; k < kStreams; ++k) m = fmaxf(m, sh.ref[par][k][tid]);
-#pragma unroll
-                for (int k = 0; k < kStreams; ++k) {
-                    const float (&row)[4][R] = sh.warp_row[k];
-                    const float up = exp2_fast(sh.ref[par][k][tid] - m);
-                    sum = fmaf(up, (row[0][tid] + row[1][tid]) + (row[2][tid] + row[3][tid]), sum);
-                    part_f[k] = ldexpf(up, sh.top_e[k] < 0 ? -131 : sh.top_e[k] - 131);
-                }
-                const float over = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-                for (int k = 0; k < kStreams; ++k) sh.factor[k][tid] = part_f[k] * over;
-                if (!whole) p.part_ml[(int64_t)part * R + tid] = make_float2(m, sum);
-                else if (p.lse && tid < done.x.rows)
-                    p.lse[sh.row_at[par][tid]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945309f;
-            }
-            named_bar_sync(all_bar, kSoftmax);
-            failed |= !wait(p_empty + 8 * (last & 1), (uint32_t)(last >> 1) & 1u, abort_flag);
-            if (kStreams == 2 && last > t_piece) failed |= !wait(p_empty + 8 * ((last - 1) & 1), (uint32_t)((last - 1) >> 1) & 1u, abort_flag);
-            tc_fence_after();
-            const bool nans = *(volatile int*)&sh.nan_seen != 0;
-            // a channel to a thread; the rows halved between the two fours
-            constexpr int RE = R / 2, kStep = RE < 16 ? RE : 16;
-            const int e_lo = (warp >> 2) * RE;
-            for (int j = 0; j < p.nv; ++j) {
-                const int ch = j * 128 + tok;
-                const int nan_at = nans ? sh.nan_at[ch & 511] : 0x7FFFFFFF;
-#pragma unroll
-                for (int r0 = 0; r0 < RE; r0 += kStep) {
-                    float o[kStep];
-#pragma unroll
-                    for (int i = 0; i < kStep; ++i) o[i] = 0.f;
-#pragma unroll
-                    for (int k = 0; k < kStreams; ++k) {
-                        if (sh.top_e[k] == 2 * kNoScale) continue;  // the same in every thread: a stream without a tile
-                        uint32_t v[16], u[16];
-                        const uint32_t from = o_tmem + lanes + (k * p.nv + j) * N2;
-                        __syncwarp();
-                        tmem_ld16(from + (R <= 16 ? 0 : e_lo + r0), v);
-                        if constexpr (R > 8) tmem_ld16(from + R + (R <= 16 ? 0 : e_lo + r0), u);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < kStep; ++i) {
-                            // R = 8: rows and rests in one load; R <= 16: both halves' rows are in it
-                            const bool up = R <= 16 && e_lo != 0;
-                            const uint32_t a = up ? v[(RE + i) & 15] : v[i];
-                            const uint32_t b = R == 8 ? (up ? v[(8 + RE + i) & 15] : v[(8 + i) & 15]) : up ? u[(RE + i) & 15] : u[i];
-                            o[i] = fmaf(fmaf(__uint_as_float(b), 0.03125f, __uint_as_float(a)), sh.factor[k][e_lo + r0 + i], o[i]);
-                        }
-                    }
-                    if (ch >= p.Dv) continue;
-#pragma unroll
-                    for (int i = 0; i < kStep; ++i) {
-                        const int r = e_lo + r0 + i;
-                        if (r >= done.x.rows) break;
-                        if (nan_at <= sh.limit[par][r]) o[i] = __uint_as_float(0x7FC00000u);
-                        if (whole) p.out[sh.row_at[par][r] * p.Dv + ch] = (uint16_t)pack_bf16x2(o[i], 0.f);
-                        else p.part_o[((int64_t)part * R + r) * p.Dv + ch] = o[i];
-                    }
-                }
-            }
+            if (tok == 0 && r_lo == 0) sh.top_e[par][stream] = any ? top_e : 2 * kNoScale;
             __syncwarp();
-            tc_fence_before();
-            if (nans) {  // the same in every thread: set before the last barriers
-                named_bar_sync(all_bar, kSoftmax);
-                for (int i = tid; i < 512; i += kSoftmax) sh.nan_at[i] = 0x7FFFFFFF;
-                if (tid == 0) sh.nan_seen = 0;
-            }
-            named_bar_sync(all_bar, kSoftmax);
-            if (tid == 0 && !whole) {
-                p.meta[part] = make_int4(done.t0 == 0 ? kOpens : done.t1 == done.x.tiles ? kEnds : kGoesOn, done.x.rho0,
-                                         done.x.rows, (int)done.x.lo * p.H + done.h);
-                parts |= 1 << (part & 1);
-            }
-            par ^= 1;
+            if (lane == 0) mbar_arrive(sums_full + 8 * par);
         }
     }
-    if (tid == 0)
-        for (int i = 0; i < 2; ++i)
-            if (!(parts >> i & 1)) p.meta[2 * c + i] = make_int4(kNoPart, 0, 0, 0);
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && *abort_flag) record_status(p.status, MLA_ERR_TIMEOUT);
@@ -1134,7 +1244,7 @@ __global__ void __launch_bounds__(kCombineThreads) cache_attn_combine_kernel(con
 
 // -------------------------------------------------------------------- host
 struct AttnPlan {
-    int R, nk, nv, ring, tmem_cols;
+    int R, nk, nv, ring, q_bufs, o_bufs, tmem_cols;
     size_t smem;
 };
 
@@ -1154,12 +1264,18 @@ bool attn_plan(const mla_attn_shape& s, const mla_kv_cache& c, int max_smem, Att
     const int64_t group = s.Hq / c.H, rows = group * (s.B > 0 ? (s.T + s.B - 1) / s.B : 1);
     a.R = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || a.nv > 2 ? 32 : 64;
     const size_t tail = a.R == 8 ? shared_bytes<8>() : a.R == 16 ? shared_bytes<16>() : a.R == 32 ? shared_bytes<32>() : shared_bytes<64>();
-    const size_t fixed = 1024 + (size_t)a.nk * 2 * a.R * 128 + 2 * 2 * a.R * 128 + tail;
-    const int64_t room = ((int64_t)max_smem - (int64_t)fixed) / kChunk;
-    a.ring = (int)(room > 14 ? 14 : room);
-    if (a.ring < (shared ? 2 * a.nk : a.nk + a.nv)) return false;
-    a.smem = fixed + (size_t)a.ring * kChunk;
-    const int cols = (2 + a.nv * (a.R <= 16 ? 2 : 1)) * 2 * a.R;
+    const size_t q = (size_t)a.nk * 2 * a.R * 128, fixed = 1024 + 2 * 2 * a.R * 128 + tail;
+    const int least = shared ? 2 * a.nk : a.nk + a.nv;
+    for (a.q_bufs = 2; a.q_bufs > 0; --a.q_bufs) {  // two buffers of queries where a useful ring is left
+        const int64_t room = ((int64_t)max_smem - (int64_t)(fixed + a.q_bufs * q)) / kChunk;
+        a.ring = (int)(room > 14 ? 14 : room);
+        if (a.ring >= (a.q_bufs == 2 && !shared ? least + 2 : least)) break;
+    }
+    if (a.q_bufs == 0) return false;
+    a.smem = fixed + a.q_bufs * q + (size_t)a.ring * kChunk;
+    const int s_cols = 2 * 2 * a.R, o_cols = a.nv * (a.R <= 16 ? 2 : 1) * 2 * a.R;
+    a.o_bufs = s_cols + 2 * o_cols <= 512 ? 2 : 1;
+    const int cols = s_cols + a.o_bufs * o_cols;
     a.tmem_cols = 32;
     while (a.tmem_cols < cols) a.tmem_cols *= 2;
     if (a.tmem_cols > 512) return false;
@@ -1255,8 +1371,11 @@ MLAQ_API int mla_cache_attn(const mla_attn_shape* shape, const mla_kv_cache* cac
     p.B = (int)s.B, p.width = (int)s.table_width, p.page = c.page, p.page_shift = __builtin_ctz(c.page);
     p.block_shift = __builtin_ctz(c.block), p.marks = c.page / c.block, p.H = c.H, p.Hq = s.Hq, p.group = s.Hq / c.H;
     p.per_seq = (p.group + a.R - 1) / a.R;
-    p.slots = cu ? s.T * p.group / a.R + s.B : s.B * p.per_seq;
+    const int64_t slots = cu ? s.T * p.group / a.R + s.B : s.B * p.per_seq;
+    if (slots > kI32Max) return MLA_ERR_UNSUPPORTED;
+    p.slots = (int)slots;
     p.Dk = c.Dk, p.Dv = c.Dv, p.nk = a.nk, p.nv = a.nv, p.ring = a.ring, p.tmem_cols = a.tmem_cols;
+    p.q_bufs = a.q_bufs, p.o_bufs = a.o_bufs;
     p.q_vec = aligned(q, 16) && s.q_t % 8 == 0 && s.q_h % 8 == 0;
     p.scale_log2 = s.scale * 1.44269504088896341f;
     p.status = dev_status;
