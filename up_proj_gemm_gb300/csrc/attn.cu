@@ -48,7 +48,7 @@ constexpr uint32_t kChunk = 16384;     // 128 tokens x 128 channels
 // after and before.
 constexpr int kSoftWarps = 8, kLoader = 8, kIssuer = 9, kMarker = 10, kDealer = 11, kHelper = 12;
 constexpr int kThreads = 512, kHelpers = 128;
-constexpr int kMarkTiles = 8;          // tiles whose scales are in shared memory
+constexpr int kMarkTiles = 16;         // tiles whose scales are in shared memory
 constexpr int kPieces = 4;             // pieces that are dealt out ahead
 constexpr int kPieceReaders = kSoftWarps + 3 + 4;
 // Four softmax warps hold a tile's tokens, a token to a thread. With few query rows
@@ -181,11 +181,6 @@ __device__ __forceinline__ void split_weights(float x, float y, uint32_t& hi, ui
     hi = a;
     lo = b;
 }
-__device__ __forceinline__ float warp_add(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
-}
 __device__ __forceinline__ void sts_v2(uint32_t addr, uint32_t a, uint32_t b) {
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
@@ -203,9 +198,11 @@ __device__ __forceinline__ int first_slot(const AttnParams& p, int b) {
     return (int)((int64_t)p.cu[b] * p.group / R) + b;
 }
 
-// What slot holds; b: a sequence at or before the slot's.
+// What slot holds; b: a sequence at or before the slot's. (Out of line, as all that is not done at every tile is kept
+// small: what sixteen warps do in one tile's time has to fit into the 32 KB of an SM's instruction cache. When it did
+// not, half of all cycles went into fetching instructions.)
 template <int R>
-__device__ __forceinline__ Slot read_slot(const AttnParams& p, int slot, int b) {
+__device__ __noinline__ Slot read_slot(const AttnParams& p, int slot, int b) {
     Slot x;
     int j;
     if (p.cu) {
@@ -254,7 +251,7 @@ struct Ring {
     }
 };
 
-template <int R>
+template <int R, bool SHARED>
 struct Shared {  // behind the ring, the queries and the probabilities
     uint64_t full[14], empty[14];
     uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], m_full[kMarkTiles], m_empty[kMarkTiles];
@@ -262,7 +259,7 @@ struct Shared {  // behind the ring, the queries and the probabilities
     uint64_t piece_full[kPieces], piece_empty[kPieces], q_full[2], q_empty[2], rows_full[2], sums_full[2], sums_empty[2];
     uint64_t o_full[2], o_empty[2], drain;
     Piece piece[kPieces];
-    uint32_t marks[kMarkTiles][kTokens / 4][2];  // scale bytes of four tokens: keys', values'
+    uint8_t marks[kMarkTiles][SHARED ? 1 : 2][kTokens];  // a tile's scale bytes, one for each block: keys', values'
     // query rows, by the piece's parity
     int row_at[2][R];                            // row of out
     alignas(16) float unit[2][R];                // 2^-exponent of the row
@@ -283,7 +280,7 @@ struct Shared {  // behind the ring, the queries and the probabilities
     int64_t scan[kThreads / 32];
     int start_slot, start_b, start_off;
 };
-static_assert(sizeof(Shared<32>) <= 10240, "latents of five chunks: two tiles, the queries and the rest fill shared memory");
+static_assert(sizeof(Shared<32, true>) <= 10240, "latents of five chunks: two tiles, the queries and the rest fill shared memory");
 
 template <int R, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -295,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = (raw + 1023u) & ~1023u;
     const uint32_t q_base = base + p.ring * kChunk, q_bytes = p.nk * (N2 * 128);
     const uint32_t p_base = q_base + p.q_bufs * q_bytes;
-    Shared<R>& sh = *reinterpret_cast<Shared<R>*>(smem_raw + (p_base - raw) + 2 * N2 * 128);
+    Shared<R, SHARED>& sh = *reinterpret_cast<Shared<R, SHARED>*>(smem_raw + (p_base - raw) + 2 * N2 * 128);
     const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
     const uint32_t s_full = smem_u32(&sh.s_full[0]), s_empty = smem_u32(&sh.s_empty[0]);
     const uint32_t p_full = smem_u32(&sh.p_full[0]), p_empty = smem_u32(&sh.p_empty[0]);
@@ -315,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(empty0 + 8 * i, 1);
         }
         for (int i = 0; i < kMarkTiles; ++i) {
-            mbar_init(m_full + 8 * i, 32);
+            mbar_init(m_full + 8 * i, 1);
             mbar_init(m_empty + 8 * i, kFour);
         }
         for (int i = 0; i < kPieces; ++i) {
@@ -487,70 +484,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             int entry, place, h;
             bool have;
         };
-        auto look_up = [&](const Piece& x, int tile) {
-            const int at = tile * kTokens + lane * box;
-            Tile k;
-            k.have = lane < boxes && at < x.x.len;
-            k.entry = k.have ? p.table[(int64_t)x.x.b * p.width + (at >> p.page_shift)] : 0;
-            k.place = (tile * kTokens) & (p.page - 1);
-            k.h = x.h;
-            return k;
-        };
-        auto load = [&](const CUtensorMap* map, const Tile& k, int chunks) {
-            int page = k.entry;
-            if (page < 0 || page >= p.pages) {
-                record_status(p.status, MLA_ERR_POS_RANGE);
-                page = (int)p.pages;  // reads as zeros
-            }
-            const int count = __popc(__ballot_sync(0xFFFFFFFFu, k.have));
-#pragma unroll 1
-            for (int j = 0; j < chunks && ok; ++j) {
-                bool got = true;
-                const uint32_t full = full0 + 8 * ring.i, to = base + ring.i * kChunk;
-                if (lane == 0) {
-                    got = filled < p.ring || wait(empty0 + 8 * ring.i, ring.phase ^ 1u, abort_flag);
-                    if (got) mbar_arrive_expect_tx(full, count * box * 128);
-                }
-                if (boxes == 1) {
-                    if (lane == 0 && got && count) tma_load_page(to, map, j * 128, k.place, k.h, page, full);
-                } else {
-#pragma unroll 1
-                    for (int i = 0; i < count; ++i) {
-                        const int from = __shfl_sync(0xFFFFFFFFu, page, i);
-                        if (lane == 0 && got) tma_load_page(to + i * box * 128, map, j * 128, 0, k.h, from, full);
-                    }
-                }
-                ok = __shfl_sync(0xFFFFFFFFu, got, 0);
-                if (!ok) break;
-                ring.step(p.ring);
-                ++filled;
-            }
-        };
         Piece x;
         int i = 0;
-        auto next_piece = [&]() {
-            ok = get_piece(i, x);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (lane == 0) mbar_arrive(piece_empty + 8 * (i % kPieces));
-            ++i;
-        };
-        next_piece();
-        if (ok && x.t1 > 0) {
-            int tile = x.t0;
-            Tile now = look_up(x, tile), before = now, next = now;
-            for (int t = 0; t <= tiles && ok; ++t) {
-                if (t + 1 < tiles) {  // the next tile's entry is on its way while this one waits for room
-                    if (++tile == x.t1) {
-                        next_piece();
-                        tile = x.t0;
-                    }
-                    if (ok) next = look_up(x, tile);
+        Tile now{}, before{}, next{};
+        x.t1 = 0;
+        int tile = -1;
+#pragma unroll 1
+        for (int t = -1; t <= tiles && ok && tiles > 0; ++t) {
+            if (t + 1 < tiles) {  // the next tile's entry is on its way while this one waits for room
+                if (++tile == x.t1) {
+                    ok = __all_sync(0xFFFFFFFFu, get_piece(i, x));
+                    if (lane == 0) mbar_arrive(piece_empty + 8 * (i % kPieces));
+                    ++i;
+                    tile = x.t0;
                 }
-                if (t < tiles && ok) load(&k_map, now, p.nk);
-                if (!SHARED && t > 0 && ok) load(&v_map, before, p.nv);
-                before = now;
-                now = next;
+                const int at = tile * kTokens + lane * box;
+                next.have = ok && lane < boxes && at < x.x.len;
+                next.entry = next.have ? p.table[(int64_t)x.x.b * p.width + (at >> p.page_shift)] : 0;
+                next.place = (tile * kTokens) & (p.page - 1);
+                next.h = x.h;
             }
+#pragma unroll 1
+            for (int values = 0; values < (SHARED ? 1 : 2); ++values) {
+                if (values ? t < 1 : t < 0 || t == tiles) continue;
+                const CUtensorMap* map = values ? &v_map : &k_map;
+                const Tile& k = values ? before : now;
+                const int chunks = values ? p.nv : p.nk, count = __popc(__ballot_sync(0xFFFFFFFFu, k.have));
+                int page = k.entry;
+                if (page < 0 || page >= p.pages) {
+                    record_status(p.status, MLA_ERR_POS_RANGE);
+                    page = (int)p.pages;  // reads as zeros
+                }
+#pragma unroll 1
+                for (int j = 0; j < chunks && ok; ++j) {
+                    const uint32_t full = full0 + 8 * ring.i, to = base + ring.i * kChunk;
+                    bool got = true;
+                    if (lane == 0) {
+                        got = filled < p.ring || wait(empty0 + 8 * ring.i, ring.phase ^ 1u, abort_flag);
+                        if (got) mbar_arrive_expect_tx(full, count * box * 128);
+                    }
+                    ok = __shfl_sync(0xFFFFFFFFu, got, 0);
+                    if (!ok) break;
+#pragma unroll 1
+                    for (int e = 0; e < count; ++e) {
+                        const int from = __shfl_sync(0xFFFFFFFFu, page, e);
+                        if (lane == 0) tma_load_page(to + e * box * 128, map, j * 128, k.place, k.h, from, full);
+                    }
+                    ring.step(p.ring);
+                    ++filled;
+                }
+            }
+            before = now;
+            now = next;
         }
         if (!ok && lane == 0) {  // copies in flight land before the block leaves
             for (int j = filled > p.ring ? filled - p.ring : 0; j < filled; ++j)
@@ -593,16 +578,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t at = ring.i * kChunk;
-                        if (j < p.nk - 1 || last_steps == 4) {
+                        const int steps = j < p.nk - 1 ? 4 : last_steps;
 #pragma unroll
-                            for (int s = 0; s < 4; ++s)
+                        for (int s = 0; s < 4; ++s)
+                            if (s < steps)
                                 mma_f8(d, desc_at(dk, at + 32 * s), desc_at(dq, qt + 32 * s), i_s, (j | s) != 0);
-                        } else {
-#pragma unroll
-                            for (int s = 0; s < 3; ++s)
-                                if (s < last_steps)
-                                    mma_f8(d, desc_at(dk, at + 32 * s), desc_at(dq, qt + 32 * s), i_s, (j | s) != 0);
-                        }
                         if (!SHARED) mma_commit(empty0 + 8 * ring.i);
                         ring.step(p.ring);
                         qt += N2 * 128;
@@ -671,75 +651,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == kMarker) {
         // ------------------------------------------------------------- scales
-        // By plain loads, four tokens to a lane (of one page: its size is a multiple of four), half of the tiles that
-        // shared memory holds in flight. (A softmax thread that fetched its own token's waited for memory at every tile.)
-        constexpr int kFlight = kMarkTiles / 2;
+        // By plain loads, one byte to a lane, of up to eight tiles at a time, so that memory is waited for once. (A softmax
+        // thread that fetched its own token's waited at every tile.)
+        const int shift = p.block_shift < 7 ? p.block_shift : 7;  // log2 of the tokens of a byte
+        const int m_shift = 7 - shift, rounds = m_shift > 5 ? 1 << (m_shift - 5) : 1;
+        const int most = m_shift >= 5 ? 1 : m_shift < 2 ? 8 : 32 >> m_shift;
         Piece x;
-        int i = 0, tile = 0;
         x.t1 = 0;
+        int i = 0, tile = 0;
         bool ok = true;
 #pragma unroll 1
-        for (int t0 = 0; t0 < tiles && ok; t0 += kFlight) {
-            int place[kFlight], page[kFlight], head[kFlight];
-#pragma unroll
-            for (int f = 0; f < kFlight; ++f) {
-                page[f] = -1;
-                place[f] = head[f] = 0;
-                if (t0 + f >= tiles || !ok) continue;
-                if (tile == x.t1) {
-                    ok = get_piece(i, x);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (lane == 0) mbar_arrive(piece_empty + 8 * (i % kPieces));
-                    ++i;
-                    if (!ok) continue;
-                    tile = x.t0;
-                }
-                const int pos = tile * kTokens + lane * 4;
-                if (pos < x.x.len) {
-                    place[f] = pos & (p.page - 1);
-                    page[f] = p.table[(int64_t)x.x.b * p.width + (pos >> p.page_shift)];
-                    head[f] = x.h;
-                }
-                ++tile;
+        for (int t = 0; t < tiles && ok;) {
+            if (tile == x.t1) {
+                ok = __all_sync(0xFFFFFFFFu, get_piece(i, x));
+                if (lane == 0) mbar_arrive(piece_empty + 8 * (i % kPieces));
+                ++i;
+                if (!ok) break;
+                tile = x.t0;
             }
-            const bool one = p.block_shift >= 2;  // one scale for the lane's four tokens
-            uint32_t k[kFlight], v[kFlight];
-            if (one) {
-#pragma unroll
-                for (int f = 0; f < kFlight; ++f) {
-                    // a bad page is recorded by the producer and reads as zeros; so do its scales
-                    k[f] = v[f] = 0;
-                    if (page[f] >= 0 && page[f] < p.pages) {
-                        const int64_t m = ((int64_t)page[f] * p.H + head[f]) * p.marks + (place[f] >> p.block_shift);
-                        k[f] = p.k_scales[m];
-                        if (!SHARED) v[f] = p.v_scales[m];
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int f = 0; f < kFlight; ++f) {
-                    k[f] = v[f] = 0;
-                    if (page[f] >= 0 && page[f] < p.pages) {
-                        const int64_t m = ((int64_t)page[f] * p.H + head[f]) * p.marks;
+            const int n = x.t1 - tile < most ? x.t1 - tile : most;
 #pragma unroll 1
-                        for (int j = 3; j >= 0; --j) {
-                            k[f] = k[f] << 8 | p.k_scales[m + ((place[f] + j) >> p.block_shift)];
-                            if (!SHARED) v[f] = v[f] << 8 | p.v_scales[m + ((place[f] + j) >> p.block_shift)];
-                        }
+            for (int r = 0; r < rounds; ++r) {
+                const int e = lane + 32 * r, of = e >> m_shift, m = e & ((1 << m_shift) - 1), slot = (t + of) % kMarkTiles;
+                const int pos = (tile + of) * kTokens + (m << shift);
+                uint32_t k = 0, v = 0;
+                if (of < n && pos < x.x.len) {
+                    const int page = p.table[(int64_t)x.x.b * p.width + (pos >> p.page_shift)];
+                    if (page >= 0 && page < p.pages) {  // a bad one is recorded by the producer and reads as zeros
+                        const int64_t at = ((int64_t)page * p.H + x.h) * p.marks + ((pos & (p.page - 1)) >> p.block_shift);
+                        k = p.k_scales[at];
+                        if (!SHARED) v = p.v_scales[at];
                     }
                 }
+                if (of < n) {
+                    if (t + of >= kMarkTiles)
+                        ok = wait(m_empty + 8 * slot, (uint32_t)((t + of) / kMarkTiles - 1) & 1u, abort_flag);
+                    sh.marks[slot][0][m] = (uint8_t)k;
+                    if (!SHARED) sh.marks[slot][SHARED ? 0 : 1][m] = (uint8_t)v;
+                }
             }
-#pragma unroll
-            for (int f = 0; f < kFlight; ++f) {
-                const int t = t0 + f, s = t % kMarkTiles;
-                if (t >= tiles || !ok) continue;
-                if (t >= kMarkTiles) ok = wait(m_empty + 8 * s, (uint32_t)(t / kMarkTiles - 1) & 1u, abort_flag);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                const uint32_t kw = one ? k[f] * 0x01010101u : k[f], vw = one ? v[f] * 0x01010101u : v[f];
-                sh.marks[s][lane][0] = kw;
-                sh.marks[s][lane][1] = SHARED ? kw : vw;
-                mbar_arrive(m_full + 8 * s);
-            }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (lane < n) mbar_arrive(m_full + 8 * ((t + lane) % kMarkTiles));
+            t += n;
+            tile += n;
         }
         __syncwarp();
     } else if (warp >= kHelper) {
@@ -776,13 +730,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto load_q = [&](const Piece& x, int i) {
             const int par = i & 1;
             const uint32_t qb = p.q_bufs == 2 ? par : 0;
-            uint4 g[kG], g2[kG];
-            fetch(x, quad, g);
             const int use = p.q_bufs == 2 ? i >> 1 : i;
-            if (use > 0) failed |= !wait(q_empty + 8 * qb, (uint32_t)(use - 1) & 1u, abort_flag);
+            uint4 g[kG], g2[kG];
 #pragma unroll 1
-            for (int r = quad; r < R; r += 4) {
-                if (r + 4 < R) fetch(x, r + 4, g2);
+            for (int r = quad - 4; r < R; r += 4) {
+                fetch(x, r + 4, g2);
+                if (r < 0) {
+                    if (use > 0) failed |= !wait(q_empty + 8 * qb, (uint32_t)(use - 1) & 1u, abort_flag);
+#pragma unroll
+                    for (int k = 0; k < kG; ++k) g[k] = g2[k];
+                    continue;
+                }
                 uint32_t m = 0;
 #pragma unroll
                 for (int k = 0; k < kG; ++k) {
@@ -833,18 +791,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         Piece now, next;
-        int i = 0;
-        auto read_piece = [&](int k, Piece& x) {
-            failed |= !get_piece(k, x);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(piece_empty + 8 * (k % kPieces));
-        };
-        read_piece(0, now);
-        const bool begin = named_bar_and(3, kHelpers, !failed) && now.t1 > 0;
-        if (begin) load_q(now, 0);
-        while (begin && now.t1 > 0) {
-            read_piece(i + 1, next);
+        next.t1 = 1;
+        // at turn i the queries of piece i, then the result of piece i - 1; every warp leaves with the others
+#pragma unroll 1
+        for (int i = -1; next.t1 > 0; ++i) {
+            now = next;
+            failed |= !get_piece(i + 1, next);
+            if (!named_bar_and(3, kHelpers, !failed)) break;
+            if (lane == 0) mbar_arrive(piece_empty + 8 * ((i + 1) % kPieces));
             if (next.t1 > 0) load_q(next, i + 1);
+            if (i < 0) continue;
             const int par = i & 1;
             const uint32_t ob = p.o_bufs == 2 ? par : 0;
             const int use = p.o_bufs == 2 ? i >> 1 : i;
@@ -869,7 +825,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p.lse[sh.row_at[par][htid]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945309f;
             }
             failed |= !wait(o_full + 8 * ob, (uint32_t)use & 1u, abort_flag);
-            // every warp leaves with the others
             if (!named_bar_and(3, kHelpers, !failed)) break;
             tc_fence_after();
             const bool nans = *(volatile int*)&sh.nan_seen[par] != 0;
@@ -928,8 +883,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          now.x.rows, now.x.lo * p.H + now.h);
                 parts |= 1 << (part & 1);
             }
-            now = next;
-            ++i;
         }
         if (htid == 0)
             for (int k = 0; k < 2; ++k)
@@ -941,6 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r_lo = kStreams == 2 ? 0 : (warp >> 2) * RT;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;  // this warp's lanes of tensor memory
         const uint32_t my_bar = 1 + stream;
+        const int mark = tok >> (p.block_shift < 7 ? p.block_shift : 7);  // of the token's byte among its tile's
         int t = 0, turn = 0;  // t: tiles of the share so far; turn: of this stream's votes
         // A wait that gave up is reported with the stream's next vote, so that its warps leave together: until then a
         // thread that saw it goes on, through every barrier.
@@ -970,10 +924,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool masked = (tile + 1) * kTokens - 1 > least;
                 const bool valid = pos < w.x.len;
                 failed |= !wait(m_full + 8 * slot, (uint32_t)(t / kMarkTiles) & 1u, abort_flag);
-                const uint8_t* mark = reinterpret_cast<const uint8_t*>(&sh.marks[slot][tok / 4][0]) + tok % 4;
-                const int ve = mark[4];
+                const uint32_t ke = sh.marks[slot][0][mark];
+                const int ve = SHARED ? (int)ke : sh.marks[slot][SHARED ? 0 : 1][mark];
                 // a value's scale of NaN makes the scores NaN of those who see it
-                const float ks = e8m0_to_f32(ve == 255 ? 255u : mark[0]) * p.scale_log2;
+                const float ks = e8m0_to_f32(ve == 255 ? 255u : ke) * p.scale_log2;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(m_empty + 8 * slot);
                 failed |= !wait(s_full + 8 * buf, (uint32_t)(t >> 1) & 1u, abort_flag);
@@ -1165,11 +1119,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (leave) break;
             // the piece's sums
             if (i >= 2) failed |= !wait(sums_empty + 8 * par, (uint32_t)((i >> 1) - 1) & 1u, abort_flag);
+            // over the warp: at each step a lane hands half of its rows to its partner and keeps the others' sums
+            int row = 0;
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const float v = warp_add(l[r]);
-                if (lane == (r & 31)) sh.sums[par][stream][quad][r_lo + r] = v;
+            for (int n = RT / 2, o = 16; o > 0; n /= 2, o /= 2) {
+                const bool upper = (lane & o) != 0;
+#pragma unroll
+                for (int r = 0; r < (n > 0 ? n : 1); ++r) {
+                    if (n > 0) l[r] = (upper ? l[r + n] : l[r]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? l[r] : l[r + n], o);
+                    else l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], o);
+                }
+                if (upper) row += n;
             }
+            sh.sums[par][stream][quad][r_lo + row] = l[0];  // a row's lanes the same
             if (tok == 0 && r_lo == 0) sh.top_e[par][stream] = any ? top_e : 2 * kNoScale;
             __syncwarp();
             if (lane == 0) mbar_arrive(sums_full + 8 * par);
@@ -1253,7 +1215,7 @@ struct AttnPlan {
 // tiles up to 32, for tensor memory's sake: 2 score buffers and nv sums of 2R
 // columns each, 512 in all.
 template <int R>
-size_t shared_bytes() { return sizeof(Shared<R>); }
+size_t shared_bytes(bool shared) { return shared ? sizeof(Shared<R, true>) : sizeof(Shared<R, false>); }
 
 bool attn_plan(const mla_attn_shape& s, const mla_kv_cache& c, int max_smem, AttnPlan* out) {
     const bool shared = !c.v;
@@ -1263,7 +1225,10 @@ bool attn_plan(const mla_attn_shape& s, const mla_kv_cache& c, int max_smem, Att
     a.nv = (c.Dv + 127) / 128;
     const int64_t group = s.Hq / c.H, rows = group * (s.B > 0 ? (s.T + s.B - 1) / s.B : 1);
     a.R = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || a.nv > 2 ? 32 : 64;
-    const size_t tail = a.R == 8 ? shared_bytes<8>() : a.R == 16 ? shared_bytes<16>() : a.R == 32 ? shared_bytes<32>() : shared_bytes<64>();
+    const size_t tail = a.R == 8    ? shared_bytes<8>(shared)
+                        : a.R == 16 ? shared_bytes<16>(shared)
+                        : a.R == 32 ? shared_bytes<32>(shared)
+                                    : shared_bytes<64>(shared);
     const size_t q = (size_t)a.nk * 2 * a.R * 128, fixed = 1024 + 2 * 2 * a.R * 128 + tail;
     const int least = shared ? 2 * a.nk : a.nk + a.nv;
     for (a.q_bufs = 2; a.q_bufs > 0; --a.q_bufs) {  // two buffers of queries where a useful ring is left
