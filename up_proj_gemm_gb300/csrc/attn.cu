@@ -107,6 +107,13 @@ __device__ __forceinline__ uint64_t desc_weights(uint32_t saddr) { return smem_d
 __device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
     return (desc & 0xFFFFFFFF00000000ull) | (uint32_t)((uint32_t)desc + (bytes >> 4));
 }
+// One lane of a converged warp, the same each time. Code that it alone runs keeps its operands in uniform registers, as
+// the MMA and TMA instructions want them; behind lane == 0 they were moved there one by one, 100 clocks of an MMA.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 // mbar_wait with its long way out of line: some thirty waits share the instruction cache with the loop over the tiles.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort) { return mbar_wait(bar, parity, abort); }
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort) {
@@ -303,7 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sums_full = smem_u32(&sh.sums_full[0]), sums_empty = smem_u32(&sh.sums_empty[0]);
     const uint32_t o_full = smem_u32(&sh.o_full[0]), o_empty = smem_u32(&sh.o_empty[0]);
     const uint32_t drain = smem_u32(&sh.drain);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // known to be the same in the whole warp
     volatile int* abort_flag = &sh.abort;
 
     if (tid == 0) {
@@ -518,17 +526,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int j = 0; j < chunks && ok; ++j) {
                     const uint32_t full = full0 + 8 * ring.i, to = base + ring.i * kChunk;
-                    bool got = true;
-                    if (lane == 0) {
-                        got = filled < p.ring || wait(empty0 + 8 * ring.i, ring.phase ^ 1u, abort_flag);
-                        if (got) mbar_arrive_expect_tx(full, count * box * 128);
-                    }
-                    ok = __shfl_sync(0xFFFFFFFFu, got, 0);
+                    ok = __all_sync(0xFFFFFFFFu, filled < p.ring || wait(empty0 + 8 * ring.i, ring.phase ^ 1u, abort_flag));
                     if (!ok) break;
+                    if (elect_one()) mbar_arrive_expect_tx(full, count * box * 128);
+                    __syncwarp();
 #pragma unroll 1
                     for (int e = 0; e < count; ++e) {
                         const int from = __shfl_sync(0xFFFFFFFFu, page, e);
-                        if (lane == 0) tma_load_page(to + e * box * 128, map, j * 128, k.place, k.h, from, full);
+                        if (elect_one()) tma_load_page(to + e * box * 128, map, j * 128, k.place, k.h, from, full);
                     }
                     ring.step(p.ring);
                     ++filled;
@@ -544,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == kIssuer) {
         // -------------------------------------------------------- MMA issuer
-        if (lane == 0 && tiles > 0) {
+        if (tiles > 0 && elect_one()) {
             const uint32_t i_s = idesc_f8(128, N2, 0), i_o = idesc_f8(128, N2, 1);
             const uint64_t dk = desc_kmajor_sw128(base), dv = desc_mnmajor_sw128(base, kChunk);
             const uint64_t dq = desc_kmajor_sw128(q_base), dw = desc_weights(p_base);
