@@ -114,10 +114,18 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r != 0;
 }
-// mbar_wait with its long way out of line: some thirty waits share the instruction cache with the loop over the tiles.
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort) { return mbar_wait(bar, parity, abort); }
+// mbar_wait in few instructions: some thirty waits share the instruction cache with the loop over the tiles (a call in
+// place of the loop would put the values that live across it on the stack).
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-    return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort);
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 15) == 0 && (*abort || globaltimer_ns() - t0 > MLAQ_WAIT_NS)) break;
+    }
+    *abort = 1;
+    return false;
 }
 __device__ __forceinline__ void tma_load_page(uint32_t dst, const void* map, int c, int place, int h, int page,
                                               uint32_t bar) {
@@ -1103,13 +1111,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 uint32_t u[4] = {v.x, v.y, v.z, v.w};
                                 bool found = false;
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) found |= __vcmpeq4(u[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+                                for (int e = 0; e < 4; ++e) {
+                                    uint32_t nan = __vcmpeq4(u[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                                    u[e] &= ~nan;
+                                    found |= nan != 0;
+#pragma unroll 1
+                                    for (int f = 0; nan != 0; ++f, nan >>= 8)
+                                        if (nan & 1u) atomicMin(&sh.nan_at[par][(j * 128 + k * 16 + e * 4 + f) & 511], pos);
+                                }
                                 if (!found) continue;
-                                for (int e = 0; e < 16; ++e)
-                                    if (((u[e / 4] >> (8 * (e & 3))) & 0x7Fu) == 0x7Fu) {
-                                        atomicMin(&sh.nan_at[par][(j * 128 + k * 16 + e) & 511], pos);
-                                        u[e / 4] &= ~(0xFFu << (8 * (e & 3)));
-                                    }
                                 sts_v4(place, u[0], u[1], u[2], u[3]);
                                 sh.nan_seen[par] = 1;
                             }
