@@ -179,6 +179,22 @@ __device__ __forceinline__ void add2(float& r0, float& r1, float a0, float a1) {
         : "+f"(r0), "+f"(r1)
         : "f"(a0), "f"(a1));
 }
+// Sums of 2N values a lane over the warp: at each step a lane hands half of its values to its partner and keeps the sums
+// of the others. l[0] becomes the sum of the values whose number is returned.
+template <int N, int O, int M>
+__device__ __forceinline__ int fold_rows(float (&l)[M], int lane) {
+    const bool upper = (lane & O) != 0;
+    if constexpr (N > 0) {
+#pragma unroll
+        for (int r = 0; r < N; ++r)
+            l[r] = (upper ? l[r + N] : l[r]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? l[r] : l[r + N], O);
+    } else {
+        l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], O);
+    }
+    int row = upper ? N : 0;
+    if constexpr (O > 1) row += fold_rows<N / 2, O / 2>(l, lane);
+    return row;
+}
 // Two weights (up to 256) as two E4M3 numbers each: hi, and 32 times what it leaves, by way of f16 (eleven bits, of
 // which the two keep eight). The first in bits 0-7.
 __device__ __forceinline__ void split_weights(float x, float y, uint32_t& hi, uint32_t& lo) {
@@ -1056,37 +1072,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(s_empty + 8 * buf);
                 any = true;
                 // the probabilities, times the value's scale, as two E4M3 numbers; nothing behind the last position
-                uint32_t hi[RT / 4], lo[RT / 4];
-                if (valid) {
-                    const int fe = ve - top_e + 4 + 127;
-                    const float f = fe <= 0 || ve == 255 ? 0.f : __uint_as_float((uint32_t)fe << 23);
-#pragma unroll
-                    for (int r = 0; r < RT; r += 4) {
-                        uint32_t h[2], o[2];
-#pragma unroll
-                        for (int k = 0; k < 4; k += 2) {
-                            const float a = exp2_fast(x[r + k]), b = exp2_fast(x[r + k + 1]);
-                            add2(l[r + k], l[r + k + 1], a, b);
-                            float y, z;
-                            mul2(y, z, a, b, f, f);
-                            split_weights(y, z, h[k / 2], o[k / 2]);
-                        }
-                        hi[r / 4] = __byte_perm(h[0], h[1], 0x5410);
-                        lo[r / 4] = __byte_perm(o[0], o[1], 0x5410);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < RT / 4; ++k) hi[k] = lo[k] = 0;
-                }
                 if (t >= 2) failed |= !wait(p_empty + 8 * buf, (uint32_t)((t >> 1) - 1) & 1u, abort_flag);
                 const uint32_t to = p_base + buf * (N2 * 128) + tok * 16;
-                if constexpr (R == 8) {
-                    sts_v4(to, hi[0], hi[1], lo[0], lo[1]);
-                } else {
+                const int fe = ve - top_e + 4 + 127;
+                const float f = fe <= 0 || ve == 255 ? 0.f : __uint_as_float((uint32_t)fe << 23);
 #pragma unroll
-                    for (int k = 0; k < RT / 16; ++k) {
-                        sts_v4(to + (r_lo / 16 + k) * 2048, hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
-                        sts_v4(to + ((R + r_lo) / 16 + k) * 2048, lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                for (int r0 = 0; r0 < RT; r0 += 16) {
+                    constexpr int kRows = RT < 16 ? RT : 16;
+                    uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+                    if (valid) {
+#pragma unroll
+                        for (int r = 0; r < kRows; r += 4) {
+                            uint32_t h[2], o[2];
+#pragma unroll
+                            for (int k = 0; k < 4; k += 2) {
+                                const float a = exp2_fast(x[r0 + r + k]), b = exp2_fast(x[r0 + r + k + 1]);
+                                add2(l[r0 + r + k], l[r0 + r + k + 1], a, b);
+                                float y, z;
+                                mul2(y, z, a, b, f, f);
+                                split_weights(y, z, h[k / 2], o[k / 2]);
+                            }
+                            hi[r / 4] = __byte_perm(h[0], h[1], 0x5410);
+                            lo[r / 4] = __byte_perm(o[0], o[1], 0x5410);
+                        }
+                    }
+                    if constexpr (R == 8) {
+                        sts_v4(to, hi[0], hi[1], lo[0], lo[1]);
+                    } else {
+                        sts_v4(to + (r_lo + r0) / 16 * 2048, hi[0], hi[1], hi[2], hi[3]);
+                        sts_v4(to + (R + r_lo + r0) / 16 * 2048, lo[0], lo[1], lo[2], lo[3]);
                     }
                 }
                 if (r_lo == 0 && ((tile + 1) * kTokens > w.x.len || (masked && w.x.n > 1))) {
@@ -1134,18 +1148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (leave) break;
             // the piece's sums
             if (i >= 2) failed |= !wait(sums_empty + 8 * par, (uint32_t)((i >> 1) - 1) & 1u, abort_flag);
-            // over the warp: at each step a lane hands half of its rows to its partner and keeps the others' sums
-            int row = 0;
-#pragma unroll
-            for (int n = RT / 2, o = 16; o > 0; n /= 2, o /= 2) {
-                const bool upper = (lane & o) != 0;
-#pragma unroll
-                for (int r = 0; r < (n > 0 ? n : 1); ++r) {
-                    if (n > 0) l[r] = (upper ? l[r + n] : l[r]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? l[r] : l[r + n], o);
-                    else l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], o);
-                }
-                if (upper) row += n;
-            }
+            const int row = fold_rows<RT / 2, 16>(l, lane);
             sh.sums[par][stream][quad][r_lo + row] = l[0];  // a row's lanes the same
             if (tok == 0 && r_lo == 0) sh.top_e[par][stream] = any ? top_e : 2 * kNoScale;
             __syncwarp();
