@@ -54,7 +54,7 @@ constexpr int kPieceReaders = kSoftWarps + 3 + 4;
 // Four softmax warps hold a tile's tokens, a token to a thread. With few query rows
 // a tile is a chain of waits, and the two fours take turns (two streams, each with
 // its own references, sums and O, joined in the end); with many it is arithmetic,
-// and they halve the rows.
+// and they halve the rows, each with its references and at its own pace.
 template <int R>
 constexpr int kStreams = R <= 16 ? 2 : 1;
 constexpr float kPass = 4.f;           // log2 of how far scores may pass the reference
@@ -297,15 +297,14 @@ struct Shared {  // behind the ring, the queries and the probabilities
     int limit[2][R];                             // the last position that it sees
     alignas(16) float ref[2][kStreams<R>][R];    // minus the reference of the row's scores
     float sums[2][kStreams<R>][4][R];            // of probabilities, by the four warps
-    int top_e[2][kStreams<R>];
+    int top_e[2][2];                             // largest exponent of V seen, by the four warps
     int nan_at[2][512];                          // by channel: the first position with a NaN that not every row sees
     int nan_seen[2];
     float out_factor[kStreams<R>][R];
-    // by stream
     float factor[kStreams<R>][R];
     float warp_row[kStreams<R>][4][R];
-    int warp_e[kStreams<R>][4];
-    int vote[kStreams<R>][3];
+    int warp_e[2][4];
+    int vote[2][3];
     uint32_t tmem;
     volatile int abort;
     int64_t scan[kThreads / 32];
@@ -367,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(drain, 1);
         sh.abort = 0;
-        for (int i = 0; i < kStreams; ++i) sh.vote[i][0] = sh.vote[i][1] = sh.vote[i][2] = 0;
+        for (int i = 0; i < 2; ++i) sh.vote[i][0] = sh.vote[i][1] = sh.vote[i][2] = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&k_map);
         if (!SHARED) tma_prefetch_desc(&v_map);
@@ -844,7 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float(&row)[4][R] = sh.sums[par][k];
                     const float up = exp2_fast(-sh.ref[par][k][htid] - m);
                     sum = fmaf(up, (row[0][htid] + row[1][htid]) + (row[2][htid] + row[3][htid]), sum);
-                    f[k] = ldexpf(up, sh.top_e[par][k] < 0 ? -131 : sh.top_e[par][k] - 131);
+                    const int e = sh.top_e[par][kStreams == 2 ? k : htid / (R / 2)];
+                    f[k] = ldexpf(up, e < 0 ? -131 : e - 131);
                 }
                 const float over = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
@@ -919,19 +919,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ------------------------------------------------------------ softmax
         constexpr int kFours = kFour / 4, RT = R / kFours;  // rows of a thread
-        const int tok = tid & 127, quad = warp & 3, stream = kStreams == 2 ? warp >> 2 : 0;
-        const int r_lo = kStreams == 2 ? 0 : (warp >> 2) * RT;
+        const int tok = tid & 127, quad = warp & 3, four = warp >> 2, stream = kStreams == 2 ? four : 0;
+        const int r_lo = kStreams == 2 ? 0 : four * RT;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;  // this warp's lanes of tensor memory
-        const uint32_t my_bar = 1 + stream;
+        const uint32_t my_bar = 1 + four;
         const int mark = tok >> (p.block_shift < 7 ? p.block_shift : 7);  // of the token's byte among its tile's
-        int t = 0, turn = 0;  // t: tiles of the share so far; turn: of this stream's votes
-        // A wait that gave up is reported with the stream's next vote, so that its warps leave together: until then a
+        int t = 0, turn = 0;  // t: tiles of the share so far; turn: of the four warps' votes
+        // A wait that gave up is reported with the next vote, so that the four warps leave together: until then a
         // thread that saw it goes on, through every barrier.
         bool failed = false, leave = false;
 #pragma unroll 1
         for (int i = 0; !leave; ++i) {
             Piece w;
-            if (!named_bar_and(my_bar, kFour * 32, get_piece(i, w))) break;
+            if (!named_bar_and(my_bar, 128, get_piece(i, w))) break;
             if (lane == 0) mbar_arrive(piece_empty + 8 * (i % kPieces));
             if (w.t1 == 0) break;
             const int par = i & 1;
@@ -1005,12 +1005,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 over = max3(max3(over, over2, kNothing), x[RT - 2], x[RT - 1]);
                 const bool grow = valid && (over > kPass || (ve > top_e && ve != 255));
                 const int bits = (__any_sync(0xFFFFFFFFu, grow) ? 1 : 0) | (__any_sync(0xFFFFFFFFu, failed) ? 2 : 0);
-                if (lane == 0 && bits) atomicOr(&sh.vote[stream][turn], bits);
-                named_bar_sync(my_bar, kFour * 32);
-                const int vote = *(volatile int*)&sh.vote[stream][turn];
+                if (lane == 0 && bits) atomicOr(&sh.vote[four][turn], bits);
+                named_bar_sync(my_bar, 128);
+                const int vote = *(volatile int*)&sh.vote[four][turn];
                 turn = turn == 2 ? 0 : turn + 1;
                 // the place two turns on was read by all before this barrier and is written by none before the next
-                if (tid == stream * 128) sh.vote[stream][turn == 2 ? 0 : turn + 1] = 0;
+                if (tok == 0) sh.vote[four][turn == 2 ? 0 : turn + 1] = 0;
                 if (vote & 2) {
                     leave = true;
                     break;
@@ -1024,10 +1024,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane == (r & 31)) sh.warp_row[stream][quad][r_lo + r] = m;
                     }
                     const int e = __reduce_max_sync(0xFFFFFFFFu, valid && ve != 255 ? ve : kNoScale);
-                    if (lane == 0) sh.warp_e[stream][quad] = e;
-                    named_bar_sync(my_bar, kFour * 32);
-                    const int r = tid - stream * 128;
-                    if (r < R) {
+                    if (lane == 0) sh.warp_e[four][quad] = e;
+                    named_bar_sync(my_bar, 128);
+                    const int r = r_lo + tok;
+                    if (tok < RT) {
                         const float old = -sh.ref[par][stream][r];
                         float m = old;
 #pragma unroll
@@ -1037,8 +1037,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const int old_e = top_e;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) top_e = max(top_e, sh.warp_e[stream][k]);
-                    named_bar_sync(my_bar, kFour * 32);
+                    for (int k = 0; k < 4; ++k) top_e = max(top_e, sh.warp_e[four][k]);
+                    named_bar_sync(my_bar, 128);
 #pragma unroll
                     for (int k = 0; k < RT; ++k) {
                         l[k] *= sh.factor[stream][r_lo + k];
@@ -1071,8 +1071,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_empty + 8 * buf);
                 any = true;
-                // the probabilities, times the value's scale, as two E4M3 numbers; nothing behind the last position
-                if (t >= 2) failed |= !wait(p_empty + 8 * buf, (uint32_t)((t >> 1) - 1) & 1u, abort_flag);
+                // The probabilities, times the value's scale, as two E4M3 numbers; nothing behind the last position. (Their
+                // buffer is free: the scores came behind the product that read it, tile t - 2's.)
                 const uint32_t to = p_base + buf * (N2 * 128) + tok * 16;
                 const int fe = ve - top_e + 4 + 127;
                 const float f = fe <= 0 || ve == 255 ? 0.f : __uint_as_float((uint32_t)fe << 23);
@@ -1150,7 +1150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= 2) failed |= !wait(sums_empty + 8 * par, (uint32_t)((i >> 1) - 1) & 1u, abort_flag);
             const int row = fold_rows<RT / 2, 16>(l, lane);
             sh.sums[par][stream][quad][r_lo + row] = l[0];  // a row's lanes the same
-            if (tok == 0 && r_lo == 0) sh.top_e[par][stream] = any ? top_e : 2 * kNoScale;
+            if (tok == 0) sh.top_e[par][four] = any ? top_e : 2 * kNoScale;
             __syncwarp();
             if (lane == 0) mbar_arrive(sums_full + 8 * par);
         }
