@@ -42,15 +42,17 @@ namespace {
 
 constexpr int kTokens = 128;           // tokens of a tile
 constexpr uint32_t kChunk = 16384;     // 128 tokens x 128 channels
-// Sixteen warps: eight for the softmax, one that loads codes, one that issues the
-// products, one that loads scales, one that deals out the pieces of work, and four
-// that bring a piece's queries in and its result out, beside the tiles of the pieces
-// after and before.
-constexpr int kSoftWarps = 8, kLoader = 8, kIssuer = 9, kMarker = 10, kDealer = 11, kHelper = 12;
+// Sixteen warps: eight for the softmax, two that load codes, one that issues the
+// products, one that loads scales and deals out the pieces of work, and four that
+// bring a piece's queries in and its result out, beside the tiles of the pieces after
+// and before. (A copy holds up the warp that issues it, 50 ns and 2.8 ns per 128-byte
+// row: two warps take turns. One alone reads 5.2 TB/s in boxes of 64 rows on all SMs,
+// from L2 or not, two 10 from L2.)
+constexpr int kSoftWarps = 8, kLoader = 8, kIssuer = 9, kMarker = 10, kLoader2 = 11, kHelper = 12;
 constexpr int kThreads = 512, kHelpers = 128;
 constexpr int kMarkTiles = 16;         // tiles whose scales are in shared memory
 constexpr int kPieces = 4;             // pieces that are dealt out ahead
-constexpr int kPieceReaders = kSoftWarps + 3 + 4;
+constexpr int kPieceReaders = kSoftWarps + 3 + 4;  // warps
 // Four softmax warps hold a tile's tokens, a token to a thread. With few query rows
 // a tile is a chain of waits, and the two fours take turns (two streams, each with
 // its own references, sums and O, joined in the end); with many it is arithmetic,
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     const uint32_t tmem = sh.tmem;
     const uint32_t s_tmem = tmem, o_tmem = tmem + 2 * N2, o_cols = kStreams * p.nv * N2;  // o_cols: of one O buffer
-    // Piece i as its readers get it; each says once per warp that it has read it.
+    // Piece i as its readers get it; each warp says that it has read it.
     auto get_piece = [&](int i, Piece& x) {
         const bool ok = wait(piece_full + 8 * (i % kPieces), (uint32_t)(i / kPieces) & 1u, abort_flag);
         x = sh.piece[i % kPieces];
@@ -464,49 +466,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         return ok;
     };
 
-    if (warp == kDealer) {
-        if (lane == 0) {
-            int left = tiles, i = 0;
-            Piece x;
-            bool ok = true;
-            if (left > 0) {
-                int slot = sh.start_slot;
-                x.x = read_slot<R>(p, slot, sh.start_b);
-                x.h = h0;
-                x.t0 = sh.start_off;
-                for (;; ++i) {
-                    const int n = x.x.tiles - x.t0;
-                    x.t1 = x.t0 + (n < left ? n : left);
-                    left -= x.t1 - x.t0;
-                    if (i >= kPieces) ok = wait(piece_empty + 8 * (i % kPieces), (uint32_t)(i / kPieces - 1) & 1u, abort_flag);
-                    if (!ok) break;
-                    sh.piece[i % kPieces] = x;
-                    mbar_arrive(piece_full + 8 * (i % kPieces));
-                    if (left <= 0) {
-                        ++i;
-                        break;
-                    }
-                    x.t0 = 0;
-                    do {
-                        if (++slot == p.slots) {
-                            slot = 0;
-                            x.x.b = 0;
-                            ++x.h;
-                        }
-                        x.x = read_slot<R>(p, slot, x.x.b);
-                    } while (x.x.tiles == 0);
-                }
-            }
-            if (ok && i >= kPieces) ok = wait(piece_empty + 8 * (i % kPieces), (uint32_t)(i / kPieces - 1) & 1u, abort_flag);
-            if (ok) {
-                sh.piece[i % kPieces].t0 = sh.piece[i % kPieces].t1 = 0;
-                mbar_arrive(piece_full + 8 * (i % kPieces));
-            }
-        }
-        __syncwarp();
-    } else if (warp == kLoader) {
-        // ---------------------------------------------------------- producer
-        // tile t's keys, then tile t - 1's values: the order in which they are used
+    if (warp == kLoader || warp == kLoader2) {
+        // --------------------------------------------------------- producers
+        // tile t's keys, then tile t - 1's values: the order in which they are used; each the second of two chunks
+        const int odd = warp == kLoader2;
         Ring ring;
         int filled = 0;
         bool ok = true;
@@ -549,6 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int j = 0; j < chunks && ok; ++j) {
                     const uint32_t full = full0 + 8 * ring.i, to = base + ring.i * kChunk;
+                    if ((filled & 1) != odd) {
+                        ring.step(p.ring);
+                        ++filled;
+                        continue;
+                    }
                     ok = __all_sync(0xFFFFFFFFu, filled < p.ring || wait(empty0 + 8 * ring.i, ring.phase ^ 1u, abort_flag));
                     if (!ok) break;
                     if (elect_one()) mbar_arrive_expect_tx(full, count * box * 128);
@@ -567,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok && lane == 0) {  // copies in flight land before the block leaves
             for (int j = filled > p.ring ? filled - p.ring : 0; j < filled; ++j)
-                mbar_wait(full0 + 8 * (j % p.ring), (uint32_t)(j / p.ring) & 1u, nullptr, 200000000ull);
+                if ((j & 1) == odd) mbar_wait(full0 + 8 * (j % p.ring), (uint32_t)(j / p.ring) & 1u, nullptr, 200000000ull);
         }
         __syncwarp();
     } else if (warp == kIssuer) {
@@ -686,21 +654,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int most = m_shift >= 5 ? 1 : m_shift < 2 ? 8 : 32 >> m_shift;
         Piece x;
         x.t1 = 0;
-        int i = 0, tile = 0;
+        int i = 0, tile = 0, slot = 0;
         bool ok = true;
+        auto deal = [&]() {  // piece i, to all that read it
+            if (i >= kPieces) ok = wait(piece_empty + 8 * (i % kPieces), (uint32_t)(i / kPieces - 1) & 1u, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (ok && lane == 0) {
+                sh.piece[i % kPieces] = x;
+                mbar_arrive(piece_full + 8 * (i % kPieces));
+            }
+            ++i;
+        };
 #pragma unroll 1
-        for (int t = 0; t < tiles && ok;) {
+        for (int t = 0;;) {
             if (tile == x.t1) {
-                ok = __all_sync(0xFFFFFFFFu, get_piece(i, x));
-                if (lane == 0) mbar_arrive(piece_empty + 8 * (i % kPieces));
-                ++i;
-                if (!ok) break;
+                if (t == tiles || !ok) break;
+                if (t == 0) {
+                    slot = sh.start_slot;
+                    x.x = read_slot<R>(p, slot, sh.start_b);
+                    x.h = h0;
+                    x.t0 = sh.start_off;
+                } else {
+                    x.t0 = 0;
+                    do {
+                        if (++slot == p.slots) {
+                            slot = 0;
+                            x.x.b = 0;
+                            ++x.h;
+                        }
+                        x.x = read_slot<R>(p, slot, x.x.b);
+                    } while (x.x.tiles == 0);
+                }
+                const int left = tiles - t, n = x.x.tiles - x.t0;
+                x.t1 = x.t0 + (n < left ? n : left);
                 tile = x.t0;
+                deal();
+                if (!ok) break;
             }
             const int n = x.t1 - tile < most ? x.t1 - tile : most;
 #pragma unroll 1
             for (int r = 0; r < rounds; ++r) {
-                const int e = lane + 32 * r, of = e >> m_shift, m = e & ((1 << m_shift) - 1), slot = (t + of) % kMarkTiles;
+                const int e = lane + 32 * r, of = e >> m_shift, m = e & ((1 << m_shift) - 1), to = (t + of) % kMarkTiles;
                 const int pos = (tile + of) * kTokens + (m << shift);
                 uint32_t k = 0, v = 0;
                 if (of < n && pos < x.x.len) {
@@ -713,16 +707,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (of < n) {
                     if (t + of >= kMarkTiles)
-                        ok = wait(m_empty + 8 * slot, (uint32_t)((t + of) / kMarkTiles - 1) & 1u, abort_flag);
-                    sh.marks[slot][0][m] = (uint8_t)k;
-                    if (!SHARED) sh.marks[slot][SHARED ? 0 : 1][m] = (uint8_t)v;
+                        ok = wait(m_empty + 8 * to, (uint32_t)((t + of) / kMarkTiles - 1) & 1u, abort_flag);
+                    sh.marks[to][0][m] = (uint8_t)k;
+                    if (!SHARED) sh.marks[to][SHARED ? 0 : 1][m] = (uint8_t)v;
                 }
             }
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (lane < n) mbar_arrive(m_full + 8 * ((t + lane) % kMarkTiles));
             t += n;
             tile += n;
+            if (!ok) break;
         }
+        x.t0 = x.t1 = 0;
+        if (ok) deal();  // no more
         __syncwarp();
     } else if (warp >= kHelper) {
         // ------------------------------------------- queries in, results out
