@@ -788,7 +788,8 @@ MLAQ_API int mla_rms_norm_fwd(const mla_norm_shape *shape, const void *x, const 
  * of both x and residual; dw = sum_t dy n. dh (the gradient that reaches h
  * itself), dx and dw may be NULL, not both of the last two. dw needs a
  * workspace of mla_rms_norm_bwd_workspace_size bytes (0 for an invalid shape),
- * 16-byte aligned; its sum's order depends on T, K and the device alone.
+ * 16-byte aligned; the order of its sum depends on T, K, alignment and the
+ * device alone.
  */
 MLAQ_API size_t mla_rms_norm_bwd_workspace_size(const mla_norm_shape *shape);
 MLAQ_API int mla_rms_norm_bwd(const mla_norm_shape *shape, const void *dy, const void *h, const void *weight,

@@ -29,7 +29,7 @@ struct CacheParams {
     void *ek, *ev;               // the dense side
     int64_t k_t, k_h, v_t, v_h;  // its strides in elements
     int64_t pages, T, slots, units;
-    int B, width, page, block, run, H, Dk, Dv, both;
+    int B, width, page, block, run, H, Dk, Dv, both, heads;  // heads: of one unit
     int out_bf16;
     int* status;
 };
@@ -40,16 +40,15 @@ struct Unit {
     int64_t row, cell;  // dense row; code row in the cache (of this head)
     int n, place;       // rows; place of the first in its page
     int64_t marks;      // first scale of this page and head
-    int head;
+    int head;           // the first of the unit's
     bool values;
 };
 
 __device__ __forceinline__ bool find_unit(const CacheParams& p, int64_t unit, Unit& u) {
-    const int64_t per = (int64_t)p.H * p.both;
-    const int64_t slot = unit / per;
-    const int r = (int)(unit - slot * per);
-    u.values = r >= p.H;
-    u.head = u.values ? r - p.H : r;
+    const int groups = (p.H + p.heads - 1) / p.heads, per = groups * p.both;
+    const int slot = (int)unit / per, r = (int)unit - slot * per;
+    u.values = r >= groups;
+    u.head = (u.values ? r - groups : r) * p.heads;
     int64_t b = slot, lo = slot, n = 1, i = 0;
     if (p.cu) {
         b = find_sequence(p.B, slot, [&](int s) { return (int64_t)(p.cu[s] / p.run) + 2 * (int64_t)s; });
@@ -139,10 +138,12 @@ __global__ void __launch_bounds__(256) kv_cache_write_kernel(const __grid_consta
     if (!find_unit(p, unit, u)) return;  // the same in every thread of the unit
     const int D = u.values ? p.Dv : p.Dk, per = D / 8, total = u.n * per;
     const int64_t st = u.values ? p.v_t : p.k_t;
-    const uint16_t* src = static_cast<const uint16_t*>(u.values ? p.ev : p.ek) + u.row * st +
-                          (int64_t)u.head * (u.values ? p.v_h : p.k_h);
+    const int64_t sh = u.values ? p.v_h : p.k_h;
+    const uint16_t* src = static_cast<const uint16_t*>(u.values ? p.ev : p.ek) + u.row * st + (int64_t)u.head * sh;
     uint8_t* codes = (u.values ? p.v : p.k) + u.cell * D;
     uint8_t* mark = (u.values ? p.v_scales : p.k_scales) + u.marks + u.place / p.block;
+    const int heads = p.H - u.head < p.heads ? p.H - u.head : p.heads;
+    for (int head = 0; head < heads; ++head, src += sh, codes += (int64_t)p.page * D, mark += p.page / p.block) {
     uint4 held[kHeld];
     uint32_t m = 0;
 #pragma unroll
@@ -204,6 +205,8 @@ __global__ void __launch_bounds__(256) kv_cache_write_kernel(const __grid_consta
         *reinterpret_cast<uint2*>(codes + g * 8) = encode_granule(load_granule<VEC>(src + row * st + (g - row * per) * 8), s);
     }
     if (lane == 0) *mark = (uint8_t)e;
+    if constexpr (!WARP) __syncthreads();  // top, for the next head
+    }
 }
 
 // A warp per unit: 16 codes to a step, four steps in flight.
@@ -279,6 +282,7 @@ int check_call(const mla_kv_cache* c, int64_t B, const int32_t* table, int64_t w
     p->B = (int)B, p->width = (int)width, p->page = c->page, p->block = c->block, p->run = (int)run;
     p->H = c->H, p->Dk = c->Dk, p->Dv = c->Dv, p->both = c->v ? 2 : 1;
     p->slots = cu ? T / run + 2 * B : B;
+    p->heads = 1;
     p->units = p->slots * p->H * p->both;
     return p->units > kI32Max ? MLA_ERR_UNSUPPORTED : MLA_OK;
 }
@@ -326,6 +330,10 @@ MLAQ_API int mla_kv_cache_write(const mla_kv_cache* cache, const void* k, int64_
     const int D = p.Dk > p.Dv || shared ? p.Dk : p.Dv;
     const int granules = (cu ? p.block : 1) * (D / 8), warps = (granules + 32 * kHeld - 1) / (32 * kHeld);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    // finding a unit's place takes as long as its memory: several heads to a unit once that leaves enough of them
+    const int64_t enough = (int64_t)di.num_sms * (warps == 1 ? 32 : 8);
+    while (p.heads < 8 && p.heads < p.H && p.units / (2 * p.heads) >= enough) p.heads *= 2;
+    p.units = p.slots * ((p.H + p.heads - 1) / p.heads) * p.both;
     if (warps == 1) {
         const unsigned grid = (unsigned)((p.units + kUnits - 1) / kUnits);
         return vec ? launch_overlapped(kv_cache_write_kernel<true, true>, grid, 32 * kUnits, 0, 0, cs, p)
@@ -341,7 +349,11 @@ MLAQ_API int mla_kv_cache_read(const mla_kv_cache* cache, void* k, void* v, int 
                                int* dev_status, void* stream) {
     CacheParams p{};
     CacheBytes n;
-    const int64_t run = 16;  // tokens of a unit: 2 to 9 KB of codes, and units enough for short prompts
+    // tokens of a unit: 16 (2 to 9 KB of codes), fewer while that leaves SMs without work
+    int64_t run = 16;
+    DeviceInfo sms;
+    if (cache && current_device_info(&sms) == MLA_OK)
+        while (run > 2 && T / run * cache->H * (cache->v ? 2 : 1) < (int64_t)sms.num_sms * 32) run /= 2;
     const int st = check_call(cache, B, table, table_width, start, cu, T, dev_status, run, &n, &p);
     if (st != MLA_OK && st != MLA_ERR_UNSUPPORTED && st != MLA_ERR_ALIGNMENT) return st;
     const mla_kv_cache& c = *cache;

@@ -7,7 +7,7 @@
 // rounded once, at its store.
 //
 // All of it is bound by HBM: a row is read once and stays in registers, eight
-// channels to a granule, granule j of thread i at (j * threads + i) * 8. A row
+// channels to a granule (see Layout). A row
 // belongs to a warp (no barrier; several rows in flight per block) or to a
 // block; a thread's weights stay in its registers for all of its rows.
 #include <cuda_runtime.h>
@@ -40,31 +40,52 @@ struct NormParams {
     float eps, inv_k;
 };
 
-// Eight channels as they lie in memory: 16 bytes of bf16 or 32 of float32,
-// read and written whole where the rows start on 16 bytes (VEC), else one by one,
-// up to n of them.
-template <typename E, bool VEC>
+// Which channels are granule j of lane i. kWhole: the eight from (j * lanes + i) * 8,
+// by 16-byte accesses, where rows start on 16 bytes. kSingle: the same, one by one
+// (an MXFP8 block is four lanes' granules). kStrided: j * 8 * lanes + i and every
+// lanes-th behind it, so that single accesses of a warp lie side by side (777 x 1001
+// float32 gradient: 14.0 us with kSingle, so 10.6).
+enum Layout { kWhole, kSingle, kStrided };
+
+struct Lanes {
+    int lane, lanes, K;
+    template <Layout L>
+    __device__ __forceinline__ int channel(int j, int i) const {
+        return L == kStrided ? (j * kG + i) * lanes + lane : (j * lanes + lane) * kG + i;
+    }
+};
+
+// Eight channels in registers, as they lie in memory; zeros behind the row's end.
+template <typename E, Layout L>
 struct Granule {
     uint32_t u[sizeof(E) == 2 ? 4 : 8];
 
-    __device__ __forceinline__ void load(const E* p, int n) {
-        if constexpr (VEC) {
-            const uint4 a = *reinterpret_cast<const uint4*>(p);
+    __device__ __forceinline__ void load(const E* row, const Lanes& l, int j) {
+        if constexpr (L == kWhole) {
+            zero();
+            const int c = l.channel<L>(j, 0);
+            if (c >= l.K) return;
+            const uint4 a = *reinterpret_cast<const uint4*>(row + c);
             u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w;
             if constexpr (sizeof(E) == 4) {
-                const uint4 b = *reinterpret_cast<const uint4*>(p + 4);
+                const uint4 b = *reinterpret_cast<const uint4*>(row + c + 4);
                 u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
             }
         } else if constexpr (sizeof(E) == 2) {
+            uint32_t v[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t lo = 2 * i < n ? (uint32_t)p[2 * i] : 0u;
-                const uint32_t hi = 2 * i + 1 < n ? (uint32_t)p[2 * i + 1] : 0u;
-                u[i] = lo | (hi << 16);
+            for (int i = 0; i < 8; ++i) {
+                const int c = l.channel<L>(j, i);
+                v[i] = c < l.K ? (uint32_t)row[c] : 0u;
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = v[2 * i] | (v[2 * i + 1] << 16);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] = i < n ? __float_as_uint(p[i]) : 0u;
+            for (int i = 0; i < 8; ++i) {
+                const int c = l.channel<L>(j, i);
+                u[i] = c < l.K ? __float_as_uint(row[c]) : 0u;
+            }
         }
     }
     __device__ __forceinline__ void zero() {
@@ -80,17 +101,21 @@ struct Granule {
         for (int i = 0; i < (sizeof(E) == 2 ? 4 : 8); ++i)
             u[i] = sizeof(E) == 2 ? pack_bf16x2(v[2 * i % kG], v[(2 * i + 1) % kG]) : __float_as_uint(v[i % kG]);
     }
-    __device__ __forceinline__ void store(E* p, int n) const {
-        if constexpr (VEC) {
-            st_global_v4(p, u[0], u[1], u[2], u[3]);
-            if constexpr (sizeof(E) == 4) st_global_v4(p + 4, u[4], u[5], u[6], u[7]);
+    __device__ __forceinline__ void store(E* row, const Lanes& l, int j) const {
+        if constexpr (L == kWhole) {
+            const int c = l.channel<L>(j, 0);
+            if (c >= l.K) return;
+            st_global_v4(row + c, u[0], u[1], u[2], u[3]);
+            if constexpr (sizeof(E) == 4) st_global_v4(row + c + 4, u[4], u[5], u[6], u[7]);
         } else {
 #pragma unroll
-            for (int i = 0; i < kG; ++i)
-                if (i < n) {
-                    if constexpr (sizeof(E) == 2) p[i] = (uint16_t)(i & 1 ? u[i / 2] >> 16 : u[i / 2] & 0xFFFFu);
-                    else p[i] = __uint_as_float(u[i]);
+            for (int i = 0; i < kG; ++i) {
+                const int c = l.channel<L>(j, i);
+                if (c < l.K) {
+                    if constexpr (sizeof(E) == 2) row[c] = (uint16_t)(i & 1 ? u[i / 2] >> 16 : u[i / 2] & 0xFFFFu);
+                    else row[c] = __uint_as_float(u[i]);
                 }
+            }
         }
     }
 };
@@ -115,17 +140,17 @@ __device__ __forceinline__ float row_sum(float v, float* buf, int turn) {
     return warp_sum(lane < warps ? b[lane] : 0.f);  // every warp the same sum, in the same order
 }
 
-// The weights of a granule, as 32-bit values (read once per thread).
-template <bool VEC>
-__device__ __forceinline__ void load_weights(const NormParams& p, int c, int n, float (&w)[kG]) {
+// The weights of a granule, as 32-bit values.
+template <Layout L>
+__device__ __forceinline__ void load_weights(const NormParams& p, const Lanes& l, int j, float (&w)[kG]) {
     if (p.w_bf16) {
-        Granule<uint16_t, VEC> g;
-        g.load(static_cast<const uint16_t*>(p.w) + c, n);
+        Granule<uint16_t, L> g;
+        g.load(static_cast<const uint16_t*>(p.w), l, j);
 #pragma unroll
         for (int i = 0; i < kG; ++i) w[i] = g.get(i);
     } else {
-        Granule<float, VEC> g;
-        g.load(static_cast<const float*>(p.w) + c, n);
+        Granule<float, L> g;
+        g.load(static_cast<const float*>(p.w), l, j);
 #pragma unroll
         for (int i = 0; i < kG; ++i) w[i] = g.get(i);
     }
@@ -138,214 +163,296 @@ constexpr int kMaxThreads = WARP ? 32 * kWarpRows : GPT == 1 ? 1024 : 512;
 // E: x, r, h and y (bf16 as uint16_t, or float). GPT granules per thread. MX:
 // y as E4M3 codes with a scale for each 32 channels, four granules that lie
 // side by side in four lanes.
-template <typename E, int GPT, bool MX, bool VEC, bool WARP>
+template <typename E, int GPT, bool MX, Layout L, bool WARP>
 __global__ void __launch_bounds__(kMaxThreads<WARP, GPT>) rms_norm_kernel(const __grid_constant__ NormParams p) {
     __shared__ float buf[64];
     grid_launch_next();
     grid_wait_previous();
-    const int lanes = WARP ? 32 : (int)blockDim.x;
-    const int lane = WARP ? (int)threadIdx.x % 32 : (int)threadIdx.x;
+    const Lanes l{WARP ? (int)threadIdx.x % 32 : (int)threadIdx.x, WARP ? 32 : (int)blockDim.x, p.K};
     const int rows = WARP ? kWarpRows : 1;
     const int64_t step = (int64_t)gridDim.x * rows;
     const E* x = static_cast<const E*>(p.x);
     const E* res = static_cast<const E*>(p.res);
-    float w[GPT][kG];
+    constexpr bool kHold = GPT <= 4;   // weights stay in registers; else each row reads them again
+    constexpr bool kAhead = GPT <= 2;  // the next row is on its way while this one is worked on
+    float w[kHold ? GPT : 1][kG];
+    if constexpr (kHold) {
 #pragma unroll
-    for (int j = 0; j < GPT; ++j) {
-        const int c = (j * lanes + lane) * kG;
-        if (c < p.K) load_weights<VEC>(p, c, p.K - c, w[j]);
+        for (int j = 0; j < GPT; ++j) load_weights<L>(p, l, j, w[j]);
     }
     // tiled scales: the last 128-row tile's missing rows get scale bytes of zero
     const int64_t end = MX && p.tiled ? (p.T + 127) / 128 * 128 : p.T;
     const int64_t nkt = (p.K / 32 + 3) / 4;
-    int turn = 0;
-    for (int64_t t = (int64_t)blockIdx.x * rows + (WARP ? threadIdx.x / 32 : 0); t < end; t += step, ++turn) {
-        if (MX && t >= p.T) {  // uniform over the row's threads
-            for (int c = lane; c < nkt * 4; c += lanes) p.scales[sf_tiled_offset(t, c, 128, nkt)] = 0;
-            continue;
-        }
-        Granule<E, VEC> raw[GPT], add[GPT];
+    Granule<E, L> raw[GPT], add[GPT], raw2[kAhead ? GPT : 1], add2[kAhead ? GPT : 1];
+    int64_t t = (int64_t)blockIdx.x * rows + (WARP ? threadIdx.x / 32 : 0);
+    auto fetch = [&](int64_t t, auto& a, auto& b) {
 #pragma unroll
         for (int j = 0; j < GPT; ++j) {
-            const int c = (j * lanes + lane) * kG;
-            raw[j].zero();
-            if (c < p.K) raw[j].load(x + t * p.ld_x + c, p.K - c);
-        }
-        if (res) {
-#pragma unroll
-            for (int j = 0; j < GPT; ++j) {
-                const int c = (j * lanes + lane) * kG;
-                add[j].zero();
-                if (c < p.K) add[j].load(res + t * p.ld_res + c, p.K - c);
+            a[j].zero();
+            b[j].zero();
+            if (t < p.T) {
+                a[j].load(x + t * p.ld_x, l, j);
+                if (res) b[j].load(res + t * p.ld_res, l, j);
             }
+        }
+    };
+    if constexpr (kAhead) fetch(t, raw2, add2);
+    int turn = 0;
+    for (; t < end; t += step, ++turn) {
+        if (MX && t >= p.T) {  // uniform over the row's threads
+            for (int c = l.lane; c < nkt * 4; c += l.lanes) p.scales[sf_tiled_offset(t, c, 128, nkt)] = 0;
+            continue;
+        }
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int j = 0; j < GPT; ++j) raw[j] = raw2[j], add[j] = add2[j];
+            fetch(t + step, raw2, add2);
+        } else {
+            fetch(t, raw, add);
         }
         float v[GPT][kG], sum = 0.f;
 #pragma unroll
         for (int j = 0; j < GPT; ++j) {
-            const int c = (j * lanes + lane) * kG;
 #pragma unroll
             for (int i = 0; i < kG; ++i) {
                 v[j][i] = raw[j].get(i) + (res ? add[j].get(i) : 0.f);
                 sum = fmaf(v[j][i], v[j][i], sum);
             }
-            if (res && c < p.K) {
+            if (res) {
                 raw[j].set(v[j]);
-                raw[j].store(static_cast<E*>(p.h) + t * p.K + c, p.K - c);
+                raw[j].store(static_cast<E*>(p.h) + t * p.K, l, j);
             }
         }
         const float rstd = __frsqrt_rn(fmaf(row_sum<WARP>(sum, buf, turn), p.inv_k, p.eps));
-        if (p.rstd && lane == 0) p.rstd[t] = rstd;
+        if (p.rstd && l.lane == 0) p.rstd[t] = rstd;
 #pragma unroll
         for (int j = 0; j < GPT; ++j) {
-            const int c = (j * lanes + lane) * kG;
-            const bool in = c < p.K;
+            if constexpr (!kHold) load_weights<L>(p, l, j, w[0]);
 #pragma unroll
-            for (int i = 0; i < kG; ++i) v[j][i] = in ? v[j][i] * rstd * w[j][i] : 0.f;
+            for (int i = 0; i < kG; ++i) v[j][i] = v[j][i] * rstd * w[kHold ? j : 0][i];
             if constexpr (MX) {
+                const int c = l.channel<L>(j, 0);
                 uint32_t m = 0;
 #pragma unroll
-                for (int i = 0; i < kG; ++i) m = max(m, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+                for (int i = 0; i < kG; ++i) {
+                    if (c >= p.K) v[j][i] = 0.f;  // nothing there, and 0 * rstd may be NaN
+                    m = max(m, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+                }
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
                 uint32_t codes[2];
                 const uint32_t s = quantize8_block_scale(v[j], m, codes);
-                if (in) {
+                if (c < p.K) {
                     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + t * p.K + c) = make_uint2(codes[0], codes[1]);
-                    if (lane % 4 == 0) {
+                    if (l.lane % 4 == 0) {
                         if (p.tiled) p.scales[sf_tiled_offset(t, c / 32, 128, nkt)] = (uint8_t)s;
                         else p.scales[t * (p.K / 32) + c / 32] = (uint8_t)s;
                     }
                 }
-            } else if (in) {
-                Granule<E, VEC> o;
+            } else {
+                Granule<E, L> o;
                 o.set(v[j]);
-                o.store(static_cast<E*>(p.y) + t * p.K + c, p.K - c);
+                o.store(static_cast<E*>(p.y) + t * p.K, l, j);
             }
         }
         if (MX && p.tiled)  // and so the last tile's missing columns
-            for (int c = p.K / 32 + lane; c < nkt * 4; c += lanes) p.scales[sf_tiled_offset(t, c, 128, nkt)] = 0;
+            for (int c = p.K / 32 + l.lane; c < nkt * 4; c += l.lanes) p.scales[sf_tiled_offset(t, c, 128, nkt)] = 0;
     }
 }
 
 // The gradient. dw's sum over the rows stays in the threads' registers; each
 // block adds its rows' in a fixed order and leaves one partial row.
-template <typename E, int GPT, bool VEC, bool WARP>
+template <typename E, int GPT, Layout L, bool WARP>
 __global__ void __launch_bounds__(kMaxThreads<WARP, GPT>) rms_norm_bwd_kernel(const __grid_constant__ NormParams p) {
     extern __shared__ float4 dyn[];
     __shared__ float buf[64];
     grid_launch_next();
     grid_wait_previous();
-    const int lanes = WARP ? 32 : (int)blockDim.x;
-    const int lane = WARP ? (int)threadIdx.x % 32 : (int)threadIdx.x;
+    const Lanes l{WARP ? (int)threadIdx.x % 32 : (int)threadIdx.x, WARP ? 32 : (int)blockDim.x, p.K};
     const int rows = WARP ? kWarpRows : 1;
     const int64_t step = (int64_t)gridDim.x * rows;
     const E* h = static_cast<const E*>(p.x);
     const E* dh = static_cast<const E*>(p.res);
     const E* dy = static_cast<const E*>(p.dy);
-    float w[GPT][kG], dw[GPT][kG];
+    constexpr bool kHold = GPT <= 4;
+    float w[kHold ? GPT : 1][kG], dw[GPT][kG];
 #pragma unroll
     for (int j = 0; j < GPT; ++j) {
-        const int c = (j * lanes + lane) * kG;
 #pragma unroll
-        for (int i = 0; i < kG; ++i) w[j][i] = dw[j][i] = 0.f;
-        if (c < p.K) load_weights<VEC>(p, c, p.K - c, w[j]);
+        for (int i = 0; i < kG; ++i) dw[j][i] = 0.f;
+        if constexpr (kHold) load_weights<L>(p, l, j, w[j]);
     }
     int turn = 0;
     for (int64_t t = (int64_t)blockIdx.x * rows + (WARP ? threadIdx.x / 32 : 0); t < p.T; t += step, ++turn) {
-        Granule<E, VEC> a[GPT], b[GPT], d[GPT];
+        Granule<E, L> a[GPT], b[GPT], d[GPT];
 #pragma unroll
         for (int j = 0; j < GPT; ++j) {
-            const int c = (j * lanes + lane) * kG;
-            a[j].zero();
-            b[j].zero();
-            if (c < p.K) {
-                a[j].load(dy + t * p.ld_dy + c, p.K - c);
-                b[j].load(h + t * p.ld_x + c, p.K - c);
-            }
+            a[j].load(dy + t * p.ld_dy, l, j);
+            b[j].load(h + t * p.ld_x, l, j);
         }
         if (dh) {
 #pragma unroll
-            for (int j = 0; j < GPT; ++j) {
-                const int c = (j * lanes + lane) * kG;
-                d[j].zero();
-                if (c < p.K) d[j].load(dh + t * p.ld_res + c, p.K - c);
-            }
+            for (int j = 0; j < GPT; ++j) d[j].load(dh + t * p.ld_res, l, j);
         }
         const float rstd = p.rstd[t];
         float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < GPT; ++j)
+        for (int j = 0; j < GPT; ++j) {
+            if constexpr (!kHold) load_weights<L>(p, l, j, w[0]);
 #pragma unroll
             for (int i = 0; i < kG; ++i) {
                 const float n = b[j].get(i) * rstd, e = a[j].get(i);
-                sum = fmaf(e * w[j][i], n, sum);
+                sum = fmaf(e * w[kHold ? j : 0][i], n, sum);
                 dw[j][i] = fmaf(e, n, dw[j][i]);
             }
+        }
         if (!p.y) continue;
         const float mean = row_sum<WARP>(sum, buf, turn) * p.inv_k;
 #pragma unroll
         for (int j = 0; j < GPT; ++j) {
-            const int c = (j * lanes + lane) * kG;
-            if (c >= p.K) continue;
+            if constexpr (!kHold) load_weights<L>(p, l, j, w[0]);
             float o[kG];
 #pragma unroll
             for (int i = 0; i < kG; ++i) {
                 const float n = b[j].get(i) * rstd;
-                o[i] = rstd * fmaf(-n, mean, a[j].get(i) * w[j][i]) + (dh ? d[j].get(i) : 0.f);
+                o[i] = rstd * fmaf(-n, mean, a[j].get(i) * w[kHold ? j : 0][i]) + (dh ? d[j].get(i) : 0.f);
             }
             a[j].set(o);
-            a[j].store(static_cast<E*>(p.y) + t * p.K + c, p.K - c);
+            a[j].store(static_cast<E*>(p.y) + t * p.K, l, j);
         }
     }
     if (!p.partials) return;
     float* out = p.partials + (int64_t)blockIdx.x * p.K;
+    float* part = WARP ? reinterpret_cast<float*>(dyn) + (threadIdx.x / 32) * p.K : out;
+#pragma unroll
+    for (int j = 0; j < GPT; ++j)
+#pragma unroll
+        for (int i = 0; i < kG; ++i) {
+            const int c = l.channel<L>(j, i);
+            if (c < p.K) part[c] = dw[j][i];
+        }
     if constexpr (WARP) {  // the warps' sums through shared memory, [warp][K]
-        float* part = reinterpret_cast<float*>(dyn);
-#pragma unroll
-        for (int j = 0; j < GPT; ++j)
-#pragma unroll
-            for (int i = 0; i < kG; ++i) {
-                const int c = (j * lanes + lane) * kG + i;
-                if (c < p.K) part[(threadIdx.x / 32) * p.K + c] = dw[j][i];
-            }
         __syncthreads();
+        part = reinterpret_cast<float*>(dyn);
         for (int c = threadIdx.x; c < p.K; c += blockDim.x) {
             float s = 0.f;
 #pragma unroll
             for (int r = 0; r < kWarpRows; ++r) s += part[r * p.K + c];
             out[c] = s;
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < GPT; ++j)
-#pragma unroll
-            for (int i = 0; i < kG; ++i) {
-                const int c = (j * lanes + lane) * kG + i;
-                if (c < p.K) out[c] = dw[j][i];
-            }
     }
 }
 
-// dw from the blocks' partial rows: 32 columns to a block, eight threads to a
+// The gradient of wide rows that start on 16 bytes. Rows come by bulk copies
+// into a ring of shared memory, several ahead of the one that is worked on: with
+// the loads in registers a block had one row in flight and waited for it (8192 x
+// 7168 with dh: 138 us, so 85 us).
+constexpr int kMaxStages = 8;
+template <typename E, int GPT>
+__global__ void __launch_bounds__(512) rms_norm_bwd_ring_kernel(const __grid_constant__ NormParams p, int stages, int pitch) {
+    extern __shared__ __align__(128) uint8_t ring[];  // [stage][dy | h | dh], rows of `pitch` bytes
+    __shared__ float buf[64];
+    __shared__ uint64_t full[kMaxStages];
+    const int tid = threadIdx.x, parts = p.res ? 3 : 2;
+    const uint32_t bytes = (uint32_t)(p.K * sizeof(E)), ring0 = smem_u32(ring), bar0 = smem_u32(full);
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i) mbar_init(bar0 + 8 * i, 1);
+        fence_mbarrier_init();
+    }
+    __syncthreads();
+    grid_launch_next();
+    grid_wait_previous();
+    const int64_t step = gridDim.x;
+    auto load = [&](int64_t t, int s) {
+        const uint32_t to = ring0 + s * parts * pitch;
+        mbar_arrive_expect_tx(bar0 + 8 * s, parts * bytes);
+        bulk_load(to, static_cast<const E*>(p.dy) + t * p.ld_dy, bytes, bar0 + 8 * s);
+        bulk_load(to + pitch, static_cast<const E*>(p.x) + t * p.ld_x, bytes, bar0 + 8 * s);
+        if (p.res) bulk_load(to + 2 * pitch, static_cast<const E*>(p.res) + t * p.ld_res, bytes, bar0 + 8 * s);
+    };
+    if (tid == 0) {
+        int64_t t = blockIdx.x;
+        for (int s = 0; s < stages && t < p.T; ++s, t += step) load(t, s);
+    }
+    const Lanes l{tid, (int)blockDim.x, p.K};
+    float w[GPT][kG], dw[GPT][kG];
+#pragma unroll
+    for (int j = 0; j < GPT; ++j) {
+#pragma unroll
+        for (int i = 0; i < kG; ++i) dw[j][i] = 0.f;
+        load_weights<kWhole>(p, l, j, w[j]);
+    }
+    int turn = 0, s = 0;
+    uint32_t phase = 0;
+    bool ok = true;  // a copy that never came is waited for once
+    for (int64_t t = blockIdx.x; t < p.T; t += step, ++turn) {
+        ok = ok && mbar_wait(bar0 + 8 * s, phase, nullptr);
+        const float rstd = p.rstd[t];
+        const uint8_t* row = ring + s * parts * pitch;
+        Granule<E, kWhole> a[GPT], b[GPT], d[GPT];
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < GPT; ++j) {
+            a[j].load(reinterpret_cast<const E*>(row), l, j);
+            b[j].load(reinterpret_cast<const E*>(row + pitch), l, j);
+            if (p.res) d[j].load(reinterpret_cast<const E*>(row + 2 * pitch), l, j);
+#pragma unroll
+            for (int i = 0; i < kG; ++i) {
+                const float n = b[j].get(i) * rstd, e = a[j].get(i);
+                sum = fmaf(e * w[j][i], n, sum);
+                dw[j][i] = fmaf(e, n, dw[j][i]);
+            }
+        }
+        const float mean = row_sum<false>(sum, buf, turn) * p.inv_k;  // behind its barrier the stage has been read
+        if (tid == 0 && t + stages * step < p.T) load(t + stages * step, s);
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
+        }
+        if (!p.y) continue;
+#pragma unroll
+        for (int j = 0; j < GPT; ++j) {
+            float o[kG];
+#pragma unroll
+            for (int i = 0; i < kG; ++i) {
+                const float n = b[j].get(i) * rstd;
+                o[i] = rstd * fmaf(-n, mean, a[j].get(i) * w[j][i]) + (p.res ? d[j].get(i) : 0.f);
+            }
+            a[j].set(o);
+            a[j].store(static_cast<E*>(p.y) + t * p.K, l, j);
+        }
+    }
+    if (!p.partials) return;
+    float* out = p.partials + (int64_t)blockIdx.x * p.K;
+#pragma unroll
+    for (int j = 0; j < GPT; ++j) {
+        const int c = l.channel<kWhole>(j, 0);
+        if (c >= p.K) continue;
+#pragma unroll
+        for (int i = 0; i < kG; i += 4) *reinterpret_cast<float4*>(out + c + i) = make_float4(dw[j][i], dw[j][i + 1], dw[j][i + 2], dw[j][i + 3]);
+    }
+}
+
+// dw from the blocks' partial rows: 32 columns to a block, 32 threads to a
 // column, each a fixed share of the rows.
-__global__ void __launch_bounds__(256) rms_norm_dw_kernel(const float* partials, int parts, int K, int w_bf16, void* dw) {
-    __shared__ float sums[8][32];
+constexpr int kDwShares = 32;
+__global__ void __launch_bounds__(32 * kDwShares) rms_norm_dw_kernel(const float* partials, int parts, int K, int w_bf16, void* dw) {
+    __shared__ float sums[kDwShares][33];
     grid_launch_next();
     grid_wait_previous();
     const int c = blockIdx.x * 32 + threadIdx.x % 32, r = threadIdx.x / 32;
     float s = 0.f;
     if (c < K) {
 #pragma unroll 8
-        for (int i = r; i < parts; i += 8) s += partials[(int64_t)i * K + c];
+        for (int i = r; i < parts; i += kDwShares) s += partials[(int64_t)i * K + c];
     }
     sums[r][threadIdx.x % 32] = s;
     __syncthreads();
-    if (r == 0 && c < K) {
-        s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += sums[i][threadIdx.x];
-        if (w_bf16) static_cast<uint16_t*>(dw)[c] = (uint16_t)pack_bf16x2(s, 0.f);
-        else static_cast<float*>(dw)[c] = s;
+    s = warp_sum(sums[threadIdx.x % 32][r]);  // column r of the block's, in a fixed order
+    const int k = blockIdx.x * 32 + r;
+    if (threadIdx.x % 32 == 0 && k < K) {
+        if (w_bf16) static_cast<uint16_t*>(dw)[k] = (uint16_t)pack_bf16x2(s, 0.f);
+        else static_cast<float*>(dw)[k] = s;
     }
 }
 
@@ -361,10 +468,9 @@ struct NormGrid {
 NormGrid norm_grid(int64_t T, int64_t K, int num_sms, bool bwd) {
     const int64_t granules = (K + kG - 1) / kG;
     NormGrid g{};
-    const int most = bwd ? 4 : 8;
-    if (granules <= 32 || (granules <= 32 * most && T >= (int64_t)num_sms * kWarpRows)) {
+    if (granules <= 32 || (granules <= 128 && T >= (int64_t)num_sms * kWarpRows)) {
         g.warp = true;
-        g.gpt = granules <= 32 ? 1 : granules <= 64 ? 2 : granules <= 128 ? 4 : 8;
+        g.gpt = granules <= 32 ? 1 : granules <= 64 ? 2 : 4;
         g.threads = 32 * kWarpRows;
         const int64_t need = (T + kWarpRows - 1) / kWarpRows, room = (int64_t)num_sms * (bwd ? 2 : 4);
         g.blocks = (unsigned)(need < room ? need : room);
@@ -373,33 +479,63 @@ NormGrid norm_grid(int64_t T, int64_t K, int num_sms, bool bwd) {
     g.gpt = granules <= 1024 && (T < 2 * num_sms || granules <= 256) ? 1 : granules <= 1024 ? 2 : granules <= 2048 ? 4 : 8;
     g.threads = (unsigned)((granules + 32 * g.gpt - 1) / (32 * g.gpt) * 32);
     const int per = (int)(2048 / g.threads) < 1 ? 1 : (int)(2048 / g.threads);
-    const int64_t room = (int64_t)num_sms * (bwd ? (per > 2 ? 2 : per) : (per > 8 ? 8 : per));
+    const int64_t room = (int64_t)num_sms * (bwd ? (per > 4 ? 4 : per) : per);
     g.blocks = (unsigned)(T < room ? T : room);
     return g;
 }
 
-template <typename E, bool MX, bool VEC>
+template <typename E, bool MX, Layout L>
 int launch_fwd_rows(const NormParams& p, const NormGrid& g, cudaStream_t s) {
-    const auto kernel = g.warp ? (g.gpt == 1   ? rms_norm_kernel<E, 1, MX, VEC, true>
-                                  : g.gpt == 2 ? rms_norm_kernel<E, 2, MX, VEC, true>
-                                  : g.gpt == 4 ? rms_norm_kernel<E, 4, MX, VEC, true>
-                                               : rms_norm_kernel<E, 8, MX, VEC, true>)
-                               : (g.gpt == 1   ? rms_norm_kernel<E, 1, MX, VEC, false>
-                                  : g.gpt == 2 ? rms_norm_kernel<E, 2, MX, VEC, false>
-                                  : g.gpt == 4 ? rms_norm_kernel<E, 4, MX, VEC, false>
-                                               : rms_norm_kernel<E, 8, MX, VEC, false>);
+    const auto kernel = g.warp ? (g.gpt == 1   ? rms_norm_kernel<E, 1, MX, L, true>
+                                  : g.gpt == 2 ? rms_norm_kernel<E, 2, MX, L, true>
+                                               : rms_norm_kernel<E, 4, MX, L, true>)
+                               : (g.gpt == 1   ? rms_norm_kernel<E, 1, MX, L, false>
+                                  : g.gpt == 2 ? rms_norm_kernel<E, 2, MX, L, false>
+                                  : g.gpt == 4 ? rms_norm_kernel<E, 4, MX, L, false>
+                                               : rms_norm_kernel<E, 8, MX, L, false>);
     return launch_overlapped(kernel, g.blocks, g.threads, 0, 0, s, p);
 }
 
-template <typename E, bool VEC>
+// The ring of rows for a block-to-a-row backward of more rows than SMs: as many
+// blocks to an SM as keep it busy (a row of 48 KB, read and written, takes longer
+// to come than to work on; a shorter one wants others beside it), the rest of
+// shared memory for rows ahead.
+struct NormRing {
+    int stages, pitch;  // stages 0: not this way
+    unsigned blocks;
+    size_t smem;
+};
+NormRing norm_ring(const NormParams& p, const NormGrid& g, int64_t size, const DeviceInfo& di) {
+    NormRing r{};
+    const int64_t row = p.K * size, parts = p.res ? 3 : 2;
+    if (g.warp || g.gpt > 2 || g.threads > 512 || p.T < 4 * (int64_t)di.num_sms) return r;
+    const int per = 4 * row >= 48 * 1024 ? 1 : 4 * row >= 24 * 1024 ? 2 : 4;  // with dh or without: dw's sum is the same
+    r.pitch = (int)((row + 127) / 128 * 128);
+    const int64_t room = ((int64_t)di.max_smem_optin / per - 2048) / (parts * r.pitch);
+    if (room < 2) return r;
+    r.stages = (int)(room > kMaxStages ? kMaxStages : room);
+    r.smem = (size_t)r.stages * parts * r.pitch;
+    const int64_t blocks = (int64_t)di.num_sms * per;
+    r.blocks = (unsigned)(blocks < g.blocks ? blocks : g.blocks);  // no more than the workspace is for
+    return r;
+}
+
+template <typename E>
+int launch_bwd_ring(const NormParams& p, const NormGrid& g, const NormRing& r, cudaStream_t s) {
+    const auto kernel = g.gpt == 1 ? rms_norm_bwd_ring_kernel<E, 1> : rms_norm_bwd_ring_kernel<E, 2>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)r.smem) != cudaSuccess) return MLA_ERR_CUDA;
+    return launch_overlapped(kernel, r.blocks, g.threads, r.smem, 0, s, p, r.stages, r.pitch);
+}
+
+template <typename E, Layout L>
 int launch_bwd_rows(const NormParams& p, const NormGrid& g, cudaStream_t s) {
-    const auto kernel = g.warp ? (g.gpt == 1   ? rms_norm_bwd_kernel<E, 1, VEC, true>
-                                  : g.gpt == 2 ? rms_norm_bwd_kernel<E, 2, VEC, true>
-                                               : rms_norm_bwd_kernel<E, 4, VEC, true>)
-                               : (g.gpt == 1   ? rms_norm_bwd_kernel<E, 1, VEC, false>
-                                  : g.gpt == 2 ? rms_norm_bwd_kernel<E, 2, VEC, false>
-                                  : g.gpt == 4 ? rms_norm_bwd_kernel<E, 4, VEC, false>
-                                               : rms_norm_bwd_kernel<E, 8, VEC, false>);
+    const auto kernel = g.warp ? (g.gpt == 1   ? rms_norm_bwd_kernel<E, 1, L, true>
+                                  : g.gpt == 2 ? rms_norm_bwd_kernel<E, 2, L, true>
+                                               : rms_norm_bwd_kernel<E, 4, L, true>)
+                               : (g.gpt == 1   ? rms_norm_bwd_kernel<E, 1, L, false>
+                                  : g.gpt == 2 ? rms_norm_bwd_kernel<E, 2, L, false>
+                                  : g.gpt == 4 ? rms_norm_bwd_kernel<E, 4, L, false>
+                                               : rms_norm_bwd_kernel<E, 8, L, false>);
     const size_t smem = g.warp && p.partials ? (size_t)kWarpRows * p.K * sizeof(float) : 0;
     return launch_overlapped(kernel, g.blocks, g.threads, smem, 0, s, p);
 }
@@ -470,10 +606,10 @@ MLAQ_API int mla_rms_norm_fwd(const mla_norm_shape* shape, const void* x, const 
     const NormGrid g = norm_grid(s.T, s.K, di.num_sms, false);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (p.x_bf16)
-        return mx ? (vec ? launch_fwd_rows<uint16_t, true, true>(p, g, cs) : launch_fwd_rows<uint16_t, true, false>(p, g, cs))
-                  : (vec ? launch_fwd_rows<uint16_t, false, true>(p, g, cs) : launch_fwd_rows<uint16_t, false, false>(p, g, cs));
-    return mx ? (vec ? launch_fwd_rows<float, true, true>(p, g, cs) : launch_fwd_rows<float, true, false>(p, g, cs))
-              : (vec ? launch_fwd_rows<float, false, true>(p, g, cs) : launch_fwd_rows<float, false, false>(p, g, cs));
+        return mx ? (vec ? launch_fwd_rows<uint16_t, true, kWhole>(p, g, cs) : launch_fwd_rows<uint16_t, true, kSingle>(p, g, cs))
+                  : (vec ? launch_fwd_rows<uint16_t, false, kWhole>(p, g, cs) : launch_fwd_rows<uint16_t, false, kStrided>(p, g, cs));
+    return mx ? (vec ? launch_fwd_rows<float, true, kWhole>(p, g, cs) : launch_fwd_rows<float, true, kSingle>(p, g, cs))
+              : (vec ? launch_fwd_rows<float, false, kWhole>(p, g, cs) : launch_fwd_rows<float, false, kStrided>(p, g, cs));
 }
 
 MLAQ_API size_t mla_rms_norm_bwd_workspace_size(const mla_norm_shape* shape) {
@@ -513,13 +649,19 @@ MLAQ_API int mla_rms_norm_bwd(const mla_norm_shape* shape, const void* dy, const
     const bool vec = s.K % kG == 0 && aligned(dy, 16) && aligned(h, 16) && aligned(dh, 16) && aligned(weight, 16) &&
                      aligned(dx, 16) && p.ld_x % ve == 0 && p.ld_res % ve == 0 && p.ld_dy % ve == 0;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (s.T > 0) {
-        const int r = p.x_bf16 ? (vec ? launch_bwd_rows<uint16_t, true>(p, g, cs) : launch_bwd_rows<uint16_t, false>(p, g, cs))
-                               : (vec ? launch_bwd_rows<float, true>(p, g, cs) : launch_bwd_rows<float, false>(p, g, cs));
+    const NormRing ring = vec ? norm_ring(p, g, size, di) : NormRing{};
+    int parts = (int)g.blocks;
+    if (s.T > 0 && ring.stages > 0) {
+        const int r = p.x_bf16 ? launch_bwd_ring<uint16_t>(p, g, ring, cs) : launch_bwd_ring<float>(p, g, ring, cs);
+        if (r != MLA_OK) return r;
+        parts = (int)ring.blocks;
+    } else if (s.T > 0) {
+        const int r = p.x_bf16 ? (vec ? launch_bwd_rows<uint16_t, kWhole>(p, g, cs) : launch_bwd_rows<uint16_t, kStrided>(p, g, cs))
+                               : (vec ? launch_bwd_rows<float, kWhole>(p, g, cs) : launch_bwd_rows<float, kStrided>(p, g, cs));
         if (r != MLA_OK) return r;
     }
     if (!dw) return MLA_OK;
-    return launch_overlapped(rms_norm_dw_kernel, (unsigned)((s.K + 31) / 32), 256, 0, 0, cs, p.partials, (int)g.blocks,
+    return launch_overlapped(rms_norm_dw_kernel, (unsigned)((s.K + 31) / 32), 32 * kDwShares, 0, 0, cs, p.partials, parts,
                              p.K, p.w_bf16, dw);
 }
 
