@@ -266,6 +266,8 @@ __device__ __noinline__ Slot read_slot(const AttnParams& p, int slot, int b) {
     return x;
 }
 
+__device__ __noinline__ int64_t divide(int64_t a, int64_t b) { return a / b; }
+
 // A piece of a share: tiles [t0, t1) of a slot and head. t1 == 0: no more.
 struct Piece {
     Slot x;
@@ -310,7 +312,7 @@ struct Shared {  // behind the ring, the queries and the probabilities
     uint32_t tmem;
     volatile int abort;
     int64_t scan[kThreads / 32];
-    int start_slot, start_b, start_off;
+    int start_slot;
 };
 static_assert(sizeof(Shared<32, true>) <= 10240, "latents of five chunks: two tiles, the queries and the rest fill shared memory");
 
@@ -339,47 +341,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // known to be the same in the whole warp
     volatile int* abort_flag = &sh.abort;
 
-    if (tid == 0) {
-        for (int i = 0; i < p.ring; ++i) {
-            mbar_init(full0 + 8 * i, 1);
-            mbar_init(empty0 + 8 * i, 1);
-        }
-        for (int i = 0; i < kMarkTiles; ++i) {
-            mbar_init(m_full + 8 * i, 1);
-            mbar_init(m_empty + 8 * i, kFour);
-        }
-        for (int i = 0; i < kPieces; ++i) {
-            mbar_init(piece_full + 8 * i, 1);
-            mbar_init(piece_empty + 8 * i, kPieceReaders);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(s_full + 8 * i, 1);
-            mbar_init(s_empty + 8 * i, kFour);
-            mbar_init(p_full + 8 * i, kFour);
-            mbar_init(p_empty + 8 * i, 1);
-            mbar_init(q_full + 8 * i, 4);
-            mbar_init(q_empty + 8 * i, 1);
-            mbar_init(rows_full + 8 * i, 4);
-            mbar_init(sums_full + 8 * i, kSoftWarps);
-            mbar_init(sums_empty + 8 * i, 4);
-            mbar_init(o_full + 8 * i, 1);
-            mbar_init(o_empty + 8 * i, 4);
-            sh.nan_seen[i] = 0;
-        }
+    if (tid < 14) {
+        mbar_init(full0 + 8 * tid, 1);
+        mbar_init(empty0 + 8 * tid, 1);
+    } else if (tid < 14 + kMarkTiles) {
+        mbar_init(m_full + 8 * (tid - 14), 1);
+        mbar_init(m_empty + 8 * (tid - 14), kFour);
+    } else if (tid < 14 + kMarkTiles + kPieces) {
+        mbar_init(piece_full + 8 * (tid - 14 - kMarkTiles), 1);
+        mbar_init(piece_empty + 8 * (tid - 14 - kMarkTiles), kPieceReaders);
+    } else if (tid >= 64 && tid < 66) {
+        const int i = tid - 64;
+        mbar_init(s_full + 8 * i, 1);
+        mbar_init(s_empty + 8 * i, kFour);
+        mbar_init(p_full + 8 * i, kFour);
+        mbar_init(p_empty + 8 * i, 1);
+        mbar_init(q_full + 8 * i, 4);
+        mbar_init(q_empty + 8 * i, 1);
+        mbar_init(rows_full + 8 * i, 4);
+        mbar_init(sums_full + 8 * i, kSoftWarps);
+        mbar_init(sums_empty + 8 * i, 4);
+        mbar_init(o_full + 8 * i, 1);
+        mbar_init(o_empty + 8 * i, 4);
+        sh.nan_seen[i] = 0;
+        sh.vote[i][0] = sh.vote[i][1] = sh.vote[i][2] = 0;
+    } else if (tid == 96) {
         mbar_init(drain, 1);
         sh.abort = 0;
-        for (int i = 0; i < 2; ++i) sh.vote[i][0] = sh.vote[i][1] = sh.vote[i][2] = 0;
-        fence_mbarrier_init();
         tma_prefetch_desc(&k_map);
         if (!SHARED) tma_prefetch_desc(&v_map);
     }
+    fence_mbarrier_init();
     if (warp == kIssuer) {
         tmem_alloc(smem_u32(&sh.tmem), p.tmem_cols);
         tmem_relinquish();
     }
     // columns of the queries past Dk meet zeros of the cache: they have to be numbers
+#pragma unroll 1
     for (uint32_t i = tid * 16; i < p.q_bufs * q_bytes; i += kThreads * 16) sts_v4(q_base + i, 0, 0, 0, 0);
-    for (int i = tid; i < 1024; i += kThreads) (&sh.nan_at[0][0])[i] = 0x7FFFFFFF;
+    sh.nan_at[0][tid] = sh.nan_at[1][tid] = 0x7FFFFFFF;
     grid_launch_next();
     grid_wait_previous();
 
@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         int b = my_b;
+#pragma unroll 1
         for (int i = my_slot; i < my_slot + per_thread && i < p.slots; ++i) {
             const Slot x = read_slot<R>(p, i, b);
             b = x.b;
@@ -413,11 +414,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    int64_t line = 0;  // tiles of one head
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) upto += sh.scan[w];
-        line += sh.scan[w];
+    int64_t line = lane < kThreads / 32 ? sh.scan[lane] : 0;  // tiles of one head
+#pragma unroll
+    for (int o = 1; o < kThreads / 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, line, o);
+        if (lane >= o) line += v;
     }
+    if (warp > 0) upto += __shfl_sync(0xFFFFFFFFu, line, warp - 1);
+    line = __shfl_sync(0xFFFFFFFFu, line, kThreads / 32 - 1);
     // equal shares, the first `all % shares` one tile longer
     const int64_t all = line * p.H;
     const int64_t shares = all < (int64_t)gridDim.x ? all : (int64_t)gridDim.x;
@@ -432,11 +436,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tiles = (int)each + (c < more);
             h0 = (int)((uint32_t)w0 / (uint32_t)line);
         } else {
-            each = all / shares;
+            each = divide(all, shares);
             const int64_t more = all - each * shares;
             w0 = c * each + (c < more ? c : more);
             tiles = (int)(each + (c < more));
-            h0 = (int)(w0 / line);
+            h0 = (int)divide(w0, line);
         }
         const int64_t at = w0 - h0 * line;
         if (at >= upto - mine && at < upto) {  // one thread's
@@ -446,9 +450,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Slot x = read_slot<R>(p, i, b);
                 b = x.b;
                 if (at < before + x.tiles) {
+                    const int t0 = (int)(at - before), n = x.tiles - t0;
                     sh.start_slot = i;
-                    sh.start_b = b;
-                    sh.start_off = (int)(at - before);
+                    sh.piece[0] = Piece{x, h0, t0, t0 + (n < tiles ? n : tiles)};
+                    mbar_arrive(piece_full);
                     break;
                 }
                 before += x.tiles;
@@ -656,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.t1 = 0;
         int i = 0, tile = 0, slot = 0;
         bool ok = true;
-        auto deal = [&]() {  // piece i, to all that read it
+        auto deal = [&]() {  // piece i, to all that read it; the first lies there
             if (i >= kPieces) ok = wait(piece_empty + 8 * (i % kPieces), (uint32_t)(i / kPieces - 1) & 1u, abort_flag);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (ok && lane == 0) {
@@ -671,9 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (t == tiles || !ok) break;
                 if (t == 0) {
                     slot = sh.start_slot;
-                    x.x = read_slot<R>(p, slot, sh.start_b);
-                    x.h = h0;
-                    x.t0 = sh.start_off;
+                    x = sh.piece[0];
+                    tile = x.t0;
+                    ++i;
+                    continue;  // to its scales
                 } else {
                     x.t0 = 0;
                     do {
