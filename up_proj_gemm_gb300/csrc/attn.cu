@@ -83,6 +83,8 @@ struct AttnParams {
     int slots;
     int B, width, page_shift, page, block_shift, marks, H, Hq, group, per_seq, Dk, Dv, nk, nv;
     int ring, q_bufs, o_bufs, tmem_cols;  // buffers of chunks, of queries, of O
+    int ahead;                            // scores of the next tile before this one's second product
+    uint32_t group_mul, group_shift;      // n / group = n * group_mul >> group_shift for n < 2^31
     int q_vec;
     float scale_log2;
     int* status;
@@ -218,6 +220,11 @@ __device__ __forceinline__ void sts_v2(uint32_t addr, uint32_t a, uint32_t b) {
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
+// A query row's token.
+__device__ __forceinline__ int token_of(const AttnParams& p, int rho) {
+    return (int)((uint64_t)(uint32_t)rho * p.group_mul >> p.group_shift);
+}
+
 // ------------------------------------------------------------ work in a line
 // A slot is a tile of R query rows of one sequence (row = token * group + head in
 // the group); slots of sequence b start at first(b) = cu[b] * group / R + b.
@@ -260,7 +267,7 @@ __device__ __noinline__ Slot read_slot(const AttnParams& p, int slot, int b) {
     const int len = p.length[b];
     x.len = len < 0 ? 0 : len > room ? (int)room : len;
     if (x.rows > 0 && x.len != len) record_status(p.status, MLA_ERR_POS_RANGE);
-    int limit = x.len - x.n + (x.rho0 + x.rows - 1) / p.group + 1;
+    int limit = x.len - x.n + token_of(p, x.rho0 + x.rows - 1) + 1;
     limit = limit < 0 ? 0 : limit > x.len ? x.len : limit;
     x.tiles = x.rows == 0 ? 0 : limit == 0 ? 1 : (limit + kTokens - 1) / kTokens;
     return x;
@@ -296,7 +303,7 @@ struct Shared {  // behind the ring, the queries and the probabilities
     Piece piece[kPieces];
     uint8_t marks[kMarkTiles][SHARED ? 1 : 2][kTokens];  // a tile's scale bytes, one for each block: keys', values'
     // query rows, by the piece's parity
-    int row_at[2][R];                            // row of out
+    alignas(16) int row_at[2][R];                // row of out
     alignas(16) float unit[2][R];                // 2^-exponent of the row
     int limit[2][R];                             // the last position that it sees
     alignas(16) float ref[2][kStreams<R>][R];    // minus the reference of the row's scores
@@ -304,7 +311,7 @@ struct Shared {  // behind the ring, the queries and the probabilities
     int top_e[2][2];                             // largest exponent of V seen, by the four warps
     int nan_at[2][512];                          // by channel: the first position with a NaN that not every row sees
     int nan_seen[2];
-    float out_factor[kStreams<R>][R];
+    alignas(16) float out_factor[kStreams<R>][R];
     float factor[kStreams<R>][R];
     float warp_row[kStreams<R>][4][R];
     int warp_e[2][4];
@@ -556,7 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int vi = 0, v_at = 0;      // the values' (tile t - 1's) piece, and its tiles so far
             int v_len = 0, len = 0;
             bool ok = true;
-            for (int t = 0; t <= tiles && ok; ++t) {
+            const int behind = p.ahead ? 1 : 0;  // tiles that the second product is behind the first
+            for (int t = 0; t < tiles + behind && ok; ++t) {
                 const int this_slot = ring.i;
                 const uint32_t buf = t & 1;
                 const int len_before = len;
@@ -584,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int s = 0; s < 4; ++s)
                             if (s < steps)
                                 mma_f8(d, desc_at(dk, at + 32 * s), desc_at(dq, qt + 32 * s), i_s, (j | s) != 0);
-                        if (!SHARED) mma_commit(empty0 + 8 * ring.i);
+                        if (!SHARED || j >= p.nv) mma_commit(empty0 + 8 * ring.i);  // what the second product does not read
                         ring.step(p.ring);
                         qt += N2 * 128;
                     }
@@ -592,12 +600,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_commit(s_full + 8 * buf);
                     if (--left == 0) mma_commit(q_empty + 8 * qb);
                 }
-                if (t > 0) {
-                    const int u = t - 1;
+                if (t >= behind) {
+                    const int u = t - behind;
                     const uint32_t ub = u & 1, ob = p.o_bufs == 2 ? (vi & 1) : 0;
                     const int use = p.o_bufs == 2 ? vi >> 1 : vi;
                     if (v_at == 0) {
-                        v_len = len_before;
+                        v_len = behind ? len_before : len;
                         ok = use == 0 || wait(o_empty + 8 * ob, (uint32_t)(use - 1) & 1u, abort_flag);
                     }
                     ok = ok && wait(p_full + 8 * ub, (uint32_t)(u >> 1) & 1u, abort_flag);
@@ -610,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < p.nv && ok; ++j) {
                         int slot = ring.i;
                         if (SHARED) {
-                            slot = tile_slot + j;
+                            slot = (behind ? tile_slot : this_slot) + j;
                             if (slot >= p.ring) slot -= p.ring;
                         } else {
                             ok = wait(full0 + 8 * ring.i, ring.phase, abort_flag);
@@ -622,19 +630,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int s = 0; s < 4; ++s)
                             mma_f8(d, desc_at(dv, at + 4096 * s), desc_at(dw, pt + 512 * s), i_o, !fresh || s != 0);
                         d += N2;
-                        if (!SHARED) {
-                            mma_commit(empty0 + 8 * ring.i);
-                            ring.step(p.ring);
-                        }
+                        mma_commit(empty0 + 8 * slot);
+                        if (!SHARED) ring.step(p.ring);
                     }
                     if (!ok) break;
-                    if (SHARED) {
-#pragma unroll 1
-                        for (int j = 0; j < p.nk; ++j) {
-                            const int slot = tile_slot + j;
-                            mma_commit(empty0 + 8 * (slot >= p.ring ? slot - p.ring : slot));
-                        }
-                    }
                     mma_commit(p_empty + 8 * ub);
                     if (++v_at == v_len) {
                         mma_commit(o_full + 8 * ob);
@@ -737,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int gran = p.Dk / 8;
         // eight bf16 at a time of a piece's query row r, as many as a lane has
         auto fetch = [&](const Piece& x, int r, uint4 (&g)[kG]) {
-            const int rho = x.x.rho0 + r, tok = rho / p.group;
+            const int rho = x.x.rho0 + r, tok = token_of(p, rho);
             const uint16_t* src = p.q + (int64_t)(x.x.lo + tok) * p.q_t + (int64_t)(x.h * p.group + rho - tok * p.group) * p.q_h;
 #pragma unroll
             for (int k = 0; k < kG; ++k) {
@@ -807,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     g[k] = g2[k];
                 }
                 if (lane == 0) {
-                    const int rr = r < x.x.rows ? r : x.x.rows - 1, rho = x.x.rho0 + rr, tok = rho / p.group;
+                    const int rr = r < x.x.rows ? r : x.x.rows - 1, rho = x.x.rho0 + rr, tok = token_of(p, rho);
                     sh.unit[par][r] = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 - f) << 23);
                     for (int k = 0; k < kStreams; ++k) sh.ref[par][k][r] = -kNothing;
                     sh.limit[par][r] = x.x.len - x.x.n + tok;
@@ -865,12 +864,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int j = 0; j < p.nv; ++j) {
                 const int ch = j * 128 + quad * 32 + lane;
-                const int nan_at = nans ? sh.nan_at[par][ch & 511] : 0x7FFFFFFF;
 #pragma unroll 1
                 for (int r0 = 0; r0 < now.x.rows; r0 += kStep) {
                     float o[kStep];
+                    int at[kStep];
 #pragma unroll
-                    for (int k = 0; k < kStep; ++k) o[k] = 0.f;
+                    for (int e = 0; e < kStep; e += 4) {
+                        const int4 v = *reinterpret_cast<const int4*>(&sh.row_at[par][r0 + e]);
+                        at[e] = v.x, at[e + 1] = v.y, at[e + 2] = v.z, at[e + 3] = v.w;
+                        o[e] = o[e + 1] = o[e + 2] = o[e + 3] = 0.f;
+                    }
 #pragma unroll
                     for (int k = 0; k < kStreams; ++k) {
                         if (sh.top_e[par][k] == 2 * kNoScale) continue;  // the same in every thread: a stream without a tile
@@ -881,19 +884,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if constexpr (R > 8) tmem_ld16(from + R, u);
                         tmem_ld_wait();
 #pragma unroll
+                        for (int e = 0; e < kStep; e += 4) {
+                            const float4 f4 = *reinterpret_cast<const float4*>(&sh.out_factor[k][r0 + e]);
+                            const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                            for (int i2 = 0; i2 < 4; ++i2)
+                                o[e + i2] = fmaf(fmaf(__uint_as_float(R > 8 ? u[e + i2] : v[(8 + e + i2) & 15]), 0.03125f,
+                                                      __uint_as_float(v[e + i2])),
+                                                 f[i2], o[e + i2]);
+                        }
+                    }
+                    if (nans) {
+                        const int nan_at = sh.nan_at[par][ch & 511];
+#pragma unroll
                         for (int e = 0; e < kStep; ++e)
-                            o[e] = fmaf(fmaf(__uint_as_float(R > 8 ? u[e] : v[(8 + e) & 15]), 0.03125f, __uint_as_float(v[e])),
-                                        sh.out_factor[k][r0 + e], o[e]);
+                            if (nan_at <= sh.limit[par][r0 + e]) o[e] = __uint_as_float(0x7FC00000u);
                     }
                     if (ch < p.Dv) {
+                        const int n = now.x.rows - r0;
+                        if (whole) {
+                            uint16_t* out = p.out + ch;
 #pragma unroll
-                        for (int e = 0; e < kStep; ++e) {
-                            const int r = r0 + e;
-                            if (r < now.x.rows) {
-                                if (nan_at <= sh.limit[par][r]) o[e] = __uint_as_float(0x7FC00000u);
-                                if (whole) p.out[(int64_t)sh.row_at[par][r] * p.Dv + ch] = (uint16_t)pack_bf16x2(o[e], 0.f);
-                                else p.part_o[((int64_t)part * R + r) * p.Dv + ch] = o[e];
-                            }
+                            for (int e = 0; e < kStep; ++e)
+                                if (e < n) out[(int64_t)at[e] * p.Dv] = (uint16_t)pack_bf16x2(o[e], 0.f);
+                        } else {
+                            float* out = p.part_o + ((int64_t)part * R + r0) * p.Dv + ch;
+#pragma unroll
+                            for (int e = 0; e < kStep; ++e)
+                                if (e < n) out[e * p.Dv] = o[e];
                         }
                     }
                 }
@@ -947,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int r = 0; r < RT; ++r) l[r] = 0.f;
             int top_e = kNoScale;
             bool any = false;  // the stream has had a tile of the piece
-            const int least = w.x.len - w.x.n + w.x.rho0 / p.group;  // the last position that every row sees
+            const int least = w.x.len - w.x.n + token_of(p, w.x.rho0);  // the last position that every row sees
             const int t_end = t + w.t1 - w.t0, to_tile = w.t0 - t;
 #pragma unroll 1
             for (; t < t_end; ++t) {
@@ -1205,7 +1223,7 @@ __global__ void __launch_bounds__(kCombineThreads) cache_attn_combine_kernel(con
     }
     __syncthreads();
     const float l = total, inv = l == 0.f ? 0.f : 1.f / l;
-    const int rho = m.y + r, tok = rho / p.group;
+    const int rho = m.y + r, tok = token_of(p, rho);
     const int64_t row = (int64_t)(m.w / p.H + tok) * p.Hq + (int64_t)(m.w % p.H) * p.group + rho - tok * p.group;
     if (tid == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.693147180559945309f;
     // half of the block takes the even parts, half the odd ones
@@ -1362,6 +1380,12 @@ MLAQ_API int mla_cache_attn(const mla_attn_shape* shape, const mla_kv_cache* cac
     p.slots = (int)slots;
     p.Dk = c.Dk, p.Dv = c.Dv, p.nk = a.nk, p.nv = a.nv, p.ring = a.ring, p.tmem_cols = a.tmem_cols;
     p.q_bufs = a.q_bufs, p.o_bufs = a.o_bufs;
+    // latents fill shared memory with two tiles: the second loads under the first
+    p.ahead = !shared || a.ring >= 3 * a.nk;
+    int bits = 0;
+    while ((1 << bits) < p.group) ++bits;
+    p.group_shift = 31 + bits;
+    p.group_mul = (uint32_t)((((uint64_t)1 << p.group_shift) + p.group - 1) / p.group);
     p.q_vec = aligned(q, 16) && s.q_t % 8 == 0 && s.q_h % 8 == 0;
     p.scale_log2 = s.scale * 1.44269504088896341f;
     p.status = dev_status;
