@@ -82,7 +82,7 @@ struct AttnParams {
     int64_t q_t, q_h, T, pages;
     int slots;
     int B, width, page_shift, page, block_shift, marks, H, Hq, group, per_seq, Dk, Dv, nk, nv;
-    int ring, q_bufs, o_bufs, tmem_cols;  // buffers of chunks, of queries, of O
+    int k_stages, v_stages, q_bufs, o_bufs, tmem_cols;  // buffers of the keys' tiles, the values', of queries, of O
     int ahead;                            // scores of the next tile before this one's second product
     uint32_t group_mul, group_shift;      // n / group = n * group_mul >> group_shift for n < 2^31
     int q_vec;
@@ -281,7 +281,7 @@ struct Piece {
     int h, t0, t1;
 };
 
-// A ring slot and its phase, advanced chunk by chunk.
+// A buffer of a ring and its phase.
 struct Ring {
     int i = 0;
     uint32_t phase = 0;
@@ -292,10 +292,11 @@ struct Ring {
         }
     }
 };
+constexpr int kMaxStages = 8;
 
 template <int R, bool SHARED>
 struct Shared {  // behind the ring, the queries and the probabilities
-    uint64_t full[14], empty[14];
+    uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
     uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], m_full[kMarkTiles], m_empty[kMarkTiles];
     // by piece: dealt out; its queries; the rows' numbers below; its sums; its O
     uint64_t piece_full[kPieces], piece_empty[kPieces], q_full[2], q_empty[2], rows_full[2], sums_full[2], sums_empty[2];
@@ -331,10 +332,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    const uint32_t q_base = base + p.ring * kChunk, q_bytes = p.nk * (N2 * 128);
+    const uint32_t v_base = base + p.k_stages * p.nk * kChunk;  // the keys' tiles, then the values'
+    const uint32_t q_base = v_base + (SHARED ? 0 : p.v_stages * p.nv * kChunk), q_bytes = p.nk * (N2 * 128);
     const uint32_t p_base = q_base + p.q_bufs * q_bytes;
     Shared<R, SHARED>& sh = *reinterpret_cast<Shared<R, SHARED>*>(smem_raw + (p_base - raw) + 2 * N2 * 128);
-    const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
+    const uint32_t k_full = smem_u32(&sh.k_full[0]), k_empty = smem_u32(&sh.k_empty[0]);
+    const uint32_t v_full = smem_u32(&sh.v_full[0]), v_empty = smem_u32(&sh.v_empty[0]);
     const uint32_t s_full = smem_u32(&sh.s_full[0]), s_empty = smem_u32(&sh.s_empty[0]);
     const uint32_t p_full = smem_u32(&sh.p_full[0]), p_empty = smem_u32(&sh.p_empty[0]);
     const uint32_t m_full = smem_u32(&sh.m_full[0]), m_empty = smem_u32(&sh.m_empty[0]);
@@ -348,15 +351,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // known to be the same in the whole warp
     volatile int* abort_flag = &sh.abort;
 
-    if (tid < 14) {
-        mbar_init(full0 + 8 * tid, 1);
-        mbar_init(empty0 + 8 * tid, 1);
-    } else if (tid < 14 + kMarkTiles) {
-        mbar_init(m_full + 8 * (tid - 14), 1);
-        mbar_init(m_empty + 8 * (tid - 14), kFour);
-    } else if (tid < 14 + kMarkTiles + kPieces) {
-        mbar_init(piece_full + 8 * (tid - 14 - kMarkTiles), 1);
-        mbar_init(piece_empty + 8 * (tid - 14 - kMarkTiles), kPieceReaders);
+    if (tid < kMaxStages) {
+        mbar_init(k_full + 8 * tid, 2);
+        mbar_init(k_empty + 8 * tid, 1);
+        mbar_init(v_full + 8 * tid, 2);
+        mbar_init(v_empty + 8 * tid, 1);
+    } else if (tid < kMaxStages + kMarkTiles) {
+        mbar_init(m_full + 8 * (tid - kMaxStages), 1);
+        mbar_init(m_empty + 8 * (tid - kMaxStages), kFour);
+    } else if (tid < kMaxStages + kMarkTiles + kPieces) {
+        mbar_init(piece_full + 8 * (tid - kMaxStages - kMarkTiles), 1);
+        mbar_init(piece_empty + 8 * (tid - kMaxStages - kMarkTiles), kPieceReaders);
     } else if (tid >= 64 && tid < 66) {
         const int i = tid - 64;
         mbar_init(s_full + 8 * i, 1);
@@ -480,10 +485,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kLoader || warp == kLoader2) {
         // --------------------------------------------------------- producers
-        // tile t's keys, then tile t - 1's values: the order in which they are used; each the second of two chunks
+        // tile t's keys, then tile t - 1's values: the order in which they are used. Each of the two brings every second
+        // chunk of 128 channels and arrives at the tile's barrier with its bytes.
         const int odd = warp == kLoader2;
-        Ring ring;
-        int filled = 0;
+        Ring k_ring, v_ring;
         bool ok = true;
         const int box = p.page < kTokens ? p.page : kTokens, boxes = kTokens / box;
         struct Tile {  // this lane's box of a tile: its page's entry of the table; the tile's first place in its page
@@ -493,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Piece x;
         int i = 0;
         Tile now{}, before{}, next{};
+        int k_filled = 0, v_filled = 0;
         x.t1 = 0;
         int tile = -1;
 #pragma unroll 1
@@ -515,57 +521,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (values ? t < 1 : t < 0 || t == tiles) continue;
                 const CUtensorMap* map = values ? &v_map : &k_map;
                 const Tile& k = values ? before : now;
-                const int chunks = values ? p.nv : p.nk, count = __popc(__ballot_sync(0xFFFFFFFFu, k.have));
+                Ring& ring = values ? v_ring : k_ring;
+                const int stages = values ? p.v_stages : p.k_stages, chunks = values ? p.nv : p.nk, tile_no = values ? t - 1 : t;
+                const uint32_t full = (values ? v_full : k_full) + 8 * ring.i, empty = (values ? v_empty : k_empty) + 8 * ring.i;
+                const int count = __popc(__ballot_sync(0xFFFFFFFFu, k.have));
+                const int first = (values ? p.nk + odd : odd) & 1;  // chunks first, first + 2, ...
                 int page = k.entry;
                 if (page < 0 || page >= p.pages) {
                     record_status(p.status, MLA_ERR_POS_RANGE);
                     page = (int)p.pages;  // reads as zeros
                 }
+                ok = __all_sync(0xFFFFFFFFu, tile_no < stages || wait(empty, ring.phase ^ 1u, abort_flag));
+                if (!ok) break;
+                if (elect_one()) mbar_arrive_expect_tx(full, (chunks - first + 1) / 2 * count * box * 128);
+                __syncwarp();
+                const uint32_t to = (values ? v_base : base) + ring.i * chunks * kChunk;
 #pragma unroll 1
-                for (int j = 0; j < chunks && ok; ++j) {
-                    const uint32_t full = full0 + 8 * ring.i, to = base + ring.i * kChunk;
-                    if ((filled & 1) != odd) {
-                        ring.step(p.ring);
-                        ++filled;
-                        continue;
-                    }
-                    ok = __all_sync(0xFFFFFFFFu, filled < p.ring || wait(empty0 + 8 * ring.i, ring.phase ^ 1u, abort_flag));
-                    if (!ok) break;
-                    if (elect_one()) mbar_arrive_expect_tx(full, count * box * 128);
-                    __syncwarp();
+                for (int j = first; j < chunks; j += 2)
 #pragma unroll 1
                     for (int e = 0; e < count; ++e) {
                         const int from = __shfl_sync(0xFFFFFFFFu, page, e);
-                        if (elect_one()) tma_load_page(to + e * box * 128, map, j * 128, k.place, k.h, from, full);
+                        if (elect_one()) tma_load_page(to + j * kChunk + e * box * 128, map, j * 128, k.place, k.h, from, full);
                     }
-                    ring.step(p.ring);
-                    ++filled;
-                }
+                if (values) ++v_filled;
+                else ++k_filled;
+                ring.step(stages);
             }
             before = now;
             now = next;
         }
         if (!ok && lane == 0) {  // copies in flight land before the block leaves
-            for (int j = filled > p.ring ? filled - p.ring : 0; j < filled; ++j)
-                if ((j & 1) == odd) mbar_wait(full0 + 8 * (j % p.ring), (uint32_t)(j / p.ring) & 1u, nullptr, 200000000ull);
+            for (int j = k_filled > p.k_stages ? k_filled - p.k_stages : 0; j < k_filled; ++j)
+                mbar_wait(k_full + 8 * (j % p.k_stages), (uint32_t)(j / p.k_stages) & 1u, nullptr, 200000000ull);
+            for (int j = v_filled > p.v_stages ? v_filled - p.v_stages : 0; j < v_filled; ++j)
+                mbar_wait(v_full + 8 * (j % p.v_stages), (uint32_t)(j / p.v_stages) & 1u, nullptr, 200000000ull);
         }
         __syncwarp();
     } else if (warp == kIssuer) {
         // -------------------------------------------------------- MMA issuer
         if (tiles > 0 && elect_one()) {
             const uint32_t i_s = idesc_f8(128, N2, 0), i_o = idesc_f8(128, N2, 1);
-            const uint64_t dk = desc_kmajor_sw128(base), dv = desc_mnmajor_sw128(base, kChunk);
+            const uint64_t dk = desc_kmajor_sw128(base), dv = desc_mnmajor_sw128(SHARED ? base : v_base, kChunk);
             const uint64_t dq = desc_kmajor_sw128(q_base), dw = desc_weights(p_base);
-            const int last_steps = (p.Dk - (p.nk - 1) * 128 + 31) / 32;  // of the last chunk of the keys
-            Ring ring;                 // next chunk in the order of use
-            int tile_slot = 0;         // SHARED: ring slot of tile t - 1's first chunk
+            const int whole = p.Dk / 128, rest = (p.Dk % 128 + 31) / 32;  // chunks of 128 channels, steps of 32 behind them
+            Ring k_ring, v_ring;       // the next tiles' buffers
+            int k_slot = 0;            // SHARED: the buffer of tile t - 1
             int i = -1, left = 0;      // the keys' piece and its tiles that are left
             int vi = 0, v_at = 0;      // the values' (tile t - 1's) piece, and its tiles so far
             int v_len = 0, len = 0;
             bool ok = true;
             const int behind = p.ahead ? 1 : 0;  // tiles that the second product is behind the first
             for (int t = 0; t < tiles + behind && ok; ++t) {
-                const int this_slot = ring.i;
+                const int this_slot = k_ring.i;
                 const uint32_t buf = t & 1;
                 const int len_before = len;
                 if (t < tiles) {
@@ -580,23 +587,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     ok = ok && (t < 2 || wait(s_empty + 8 * buf, (uint32_t)((t >> 1) - 1) & 1u, abort_flag));
                     const uint32_t d = s_tmem + buf * N2, qb = p.q_bufs == 2 ? (i & 1) : 0;
-                    uint32_t qt = qb * q_bytes;
+                    ok = ok && wait(k_full + 8 * k_ring.i, k_ring.phase, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint32_t qt = qb * q_bytes, at = k_ring.i * p.nk * kChunk;
+                    uint32_t add = 0;
 #pragma unroll 1
-                    for (int j = 0; j < p.nk && ok; ++j) {
-                        ok = wait(full0 + 8 * ring.i, ring.phase, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t at = ring.i * kChunk;
-                        const int steps = j < p.nk - 1 ? 4 : last_steps;
+                    for (int j = 0; j < whole; ++j) {
 #pragma unroll
                         for (int s = 0; s < 4; ++s)
-                            if (s < steps)
-                                mma_f8(d, desc_at(dk, at + 32 * s), desc_at(dq, qt + 32 * s), i_s, (j | s) != 0);
-                        if (!SHARED || j >= p.nv) mma_commit(empty0 + 8 * ring.i);  // what the second product does not read
-                        ring.step(p.ring);
+                            mma_f8(d, desc_at(dk, at + 32 * s), desc_at(dq, qt + 32 * s), i_s, s == 0 ? add : 1u);
+                        add = 1;
                         qt += N2 * 128;
+                        at += kChunk;
                     }
-                    if (!ok) break;
+#pragma unroll 1
+                    for (int s = 0; s < rest; ++s) {
+                        mma_f8(d, desc_at(dk, at), desc_at(dq, qt), i_s, add);
+                        add = 1;
+                        qt += 32;
+                        at += 32;
+                    }
+                    if (!SHARED) mma_commit(k_empty + 8 * k_ring.i);
+                    k_ring.step(p.k_stages);
                     mma_commit(s_full + 8 * buf);
                     if (--left == 0) mma_commit(q_empty + 8 * qb);
                 }
@@ -609,31 +622,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = use == 0 || wait(o_empty + 8 * ob, (uint32_t)(use - 1) & 1u, abort_flag);
                     }
                     ok = ok && wait(p_full + 8 * ub, (uint32_t)(u >> 1) & 1u, abort_flag);
+                    if (!SHARED) ok = ok && wait(v_full + 8 * v_ring.i, v_ring.phase, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t pt = ub * (N2 * 128);
+                    const uint32_t pt = ub * (N2 * 128), slot = SHARED ? (behind ? k_slot : this_slot) : v_ring.i;
                     uint32_t d = o_tmem + ob * o_cols + (kStreams == 2 ? ub * p.nv * N2 : 0);
-                    const bool fresh = v_at < kStreams;  // the stream's first tile of the piece
+                    uint32_t at = slot * (SHARED ? p.nk : p.nv) * kChunk;
+                    const uint32_t old = v_at < kStreams ? 0u : 1u;  // not the stream's first tile of the piece
 #pragma unroll 1
-                    for (int j = 0; j < p.nv && ok; ++j) {
-                        int slot = ring.i;
-                        if (SHARED) {
-                            slot = (behind ? tile_slot : this_slot) + j;
-                            if (slot >= p.ring) slot -= p.ring;
-                        } else {
-                            ok = wait(full0 + 8 * ring.i, ring.phase, abort_flag);
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
-                        const uint32_t at = slot * kChunk;
+                    for (int j = 0; j < p.nv; ++j) {
 #pragma unroll
                         for (int s = 0; s < 4; ++s)
-                            mma_f8(d, desc_at(dv, at + 4096 * s), desc_at(dw, pt + 512 * s), i_o, !fresh || s != 0);
+                            mma_f8(d, desc_at(dv, at + 4096 * s), desc_at(dw, pt + 512 * s), i_o, s == 0 ? old : 1u);
                         d += N2;
-                        mma_commit(empty0 + 8 * slot);
-                        if (!SHARED) ring.step(p.ring);
+                        at += kChunk;
                     }
-                    if (!ok) break;
+                    mma_commit((SHARED ? k_empty : v_empty) + 8 * slot);
+                    if (!SHARED) v_ring.step(p.v_stages);
                     mma_commit(p_empty + 8 * ub);
                     if (++v_at == v_len) {
                         mma_commit(o_full + 8 * ob);
@@ -641,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ++vi;
                     }
                 }
-                tile_slot = this_slot;
+                k_slot = this_slot;
             }
             if (!ok) {
                 mma_commit(drain);
@@ -1127,14 +1132,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (r_lo == 0 && ((tile + 1) * kTokens > w.x.len || (masked && w.x.n > 1))) {
                     // What lies behind the last position may be anything, also NaN: zeros. And a NaN that some rows see
                     // and others do not must not meet their zero probability: it is noted and put into the result.
-                    int64_t chunk;
-                    if (SHARED) chunk = (int64_t)t * p.nk;
-                    else chunk = (int64_t)(t + 2 < tiles ? t + 2 : tiles) * p.nk + (int64_t)t * p.nv;
+                    const int stages = SHARED ? p.k_stages : p.v_stages, at = t % stages;
+                    failed |= !wait((SHARED ? k_full : v_full) + 8 * at, (uint32_t)(t / stages) & 1u, abort_flag);
+                    uint32_t mem = (SHARED ? base : v_base) + at * (SHARED ? p.nk : p.nv) * kChunk + tok * 128;
 #pragma unroll 1
-                    for (int j = 0; j < p.nv; ++j, ++chunk) {
-                        const int at = (int)(chunk % p.ring);
-                        failed |= !wait(full0 + 8 * at, (uint32_t)(chunk / p.ring) & 1u, abort_flag);
-                        const uint32_t mem = base + at * kChunk + tok * 128;
+                    for (int j = 0; j < p.nv; ++j, mem += kChunk) {
                         if (!valid) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k) sts_v4(mem + k * 16, 0, 0, 0, 0);
@@ -1245,7 +1247,7 @@ __global__ void __launch_bounds__(kCombineThreads) cache_attn_combine_kernel(con
 
 // -------------------------------------------------------------------- host
 struct AttnPlan {
-    int R, nk, nv, ring, q_bufs, o_bufs, tmem_cols;
+    int R, nk, nv, k_stages, v_stages, q_bufs, o_bufs, tmem_cols;
     size_t smem;
 };
 
@@ -1269,14 +1271,18 @@ bool attn_plan(const mla_attn_shape& s, const mla_kv_cache& c, int max_smem, Att
                         : a.R == 32 ? shared_bytes<32>(shared)
                                     : shared_bytes<64>(shared);
     const size_t q = (size_t)a.nk * 2 * a.R * 128, fixed = 1024 + 2 * 2 * a.R * 128 + tail;
-    const int least = shared ? 2 * a.nk : a.nk + a.nv;
-    for (a.q_bufs = 2; a.q_bufs > 0; --a.q_bufs) {  // two buffers of queries where a useful ring is left
-        const int64_t room = ((int64_t)max_smem - (int64_t)(fixed + a.q_bufs * q)) / kChunk;
-        a.ring = (int)(room > 14 ? 14 : room);
-        if (a.ring >= (a.q_bufs == 2 && !shared ? least + 2 : least)) break;
+    const int tile = shared ? a.nk : a.nk + a.nv;
+    // two buffers of queries where three tiles (latents: two) are left, else one beside a tile (two)
+    for (a.q_bufs = 2; a.q_bufs > 0; --a.q_bufs) {
+        const int room = (int)(((int64_t)max_smem - (int64_t)(fixed + a.q_bufs * q)) / kChunk), stages = room / tile;
+        if (stages < (shared ? 2 : a.q_bufs == 2 ? 3 : 1)) continue;
+        a.v_stages = shared ? 0 : stages > kMaxStages ? kMaxStages : stages;
+        a.k_stages = (room - a.v_stages * a.nv) / a.nk;
+        if (a.k_stages > kMaxStages) a.k_stages = kMaxStages;
+        break;
     }
     if (a.q_bufs == 0) return false;
-    a.smem = fixed + a.q_bufs * q + (size_t)a.ring * kChunk;
+    a.smem = fixed + a.q_bufs * q + ((size_t)a.k_stages * a.nk + (size_t)a.v_stages * a.nv) * kChunk;
     const int s_cols = 2 * 2 * a.R, o_cols = a.nv * (a.R <= 16 ? 2 : 1) * 2 * a.R;
     a.o_bufs = s_cols + 2 * o_cols <= 512 ? 2 : 1;
     const int cols = s_cols + a.o_bufs * o_cols;
@@ -1378,10 +1384,10 @@ MLAQ_API int mla_cache_attn(const mla_attn_shape* shape, const mla_kv_cache* cac
     const int64_t slots = cu ? s.T * p.group / a.R + s.B : s.B * p.per_seq;
     if (slots > kI32Max) return MLA_ERR_UNSUPPORTED;
     p.slots = (int)slots;
-    p.Dk = c.Dk, p.Dv = c.Dv, p.nk = a.nk, p.nv = a.nv, p.ring = a.ring, p.tmem_cols = a.tmem_cols;
+    p.Dk = c.Dk, p.Dv = c.Dv, p.nk = a.nk, p.nv = a.nv, p.k_stages = a.k_stages, p.v_stages = a.v_stages, p.tmem_cols = a.tmem_cols;
     p.q_bufs = a.q_bufs, p.o_bufs = a.o_bufs;
     // latents fill shared memory with two tiles: the second loads under the first
-    p.ahead = !shared || a.ring >= 3 * a.nk;
+    p.ahead = !shared || a.k_stages > 2;
     int bits = 0;
     while ((1 << bits) < p.group) ++bits;
     p.group_shift = 31 + bits;
