@@ -63,7 +63,7 @@ constexpr float kPass = 4.f;           // log2 of how far scores may pass the re
 constexpr float kNothing = -3.0e38f;   // the reference of a row that has seen nothing
 constexpr int kNoScale = -1000;
 constexpr int kMaxQueryChunks = 5;
-constexpr int kCombineThreads = 256;
+constexpr int kCombineThreads = 512, kMaxShares = 256;
 
 // The parts of a share: place 0 of the workspace has the one that begins inside
 // its pair of slot and head (it may go on into the next share), place 1 the one
@@ -76,7 +76,7 @@ struct AttnParams {
     float* lse;
     const int32_t *table, *length, *cu;
     const uint8_t *k_scales, *v_scales;
-    float* part_o;    // [2 * shares][R][Dv]
+    float* part_o;    // [2 * shares][R][Dv], on 16 bytes
     float2* part_ml;  // [2 * shares][R]
     int4* meta;       // [shares][2]
     int64_t q_t, q_h, T, pages;
@@ -1187,61 +1187,98 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Adds the parts of the pair that share blockIdx.x opens: one query row to a block.
+// Adds the parts of the pair that share blockIdx.x / (R / 8) opens, eight query
+// rows to a block. (One row to a block were 4864 blocks of latents, 33 us; these
+// are 608, 6 us.)
+constexpr int kCombineRows = 8;
 template <int R>
 __global__ void __launch_bounds__(kCombineThreads) cache_attn_combine_kernel(const __grid_constant__ AttnParams p, int shares) {
-    __shared__ float weight[kCombineThreads];
-    __shared__ float sums[kCombineThreads];
+    __shared__ float weight[kMaxShares][kCombineRows], sums[kMaxShares][kCombineRows];
+    __shared__ float4 halves[kCombineThreads];
+    __shared__ float inv[kCombineRows];
+    __shared__ int64_t row_at[kCombineRows];
     __shared__ int ends;
-    __shared__ float total;
     grid_launch_next();
     grid_wait_previous();
-    const int c = blockIdx.x / R, r = blockIdx.x % R, tid = threadIdx.x;
+    const int c = blockIdx.x / (R / kCombineRows), r0 = blockIdx.x % (R / kCombineRows) * kCombineRows, tid = threadIdx.x;
     const int4 m = p.meta[2 * c + 1];
-    if (m.x != kOpens || r >= m.z) return;
+    const int rows = m.z - r0 < kCombineRows ? m.z - r0 : kCombineRows;
+    if (m.x != kOpens || rows <= 0) return;
     // the shares behind go on with the pair until one ends it
-    if (tid == 0) ends = shares;
+    if (tid == 0) ends = shares - 1;
     __syncthreads();
     for (int i = c + 1 + tid; i < shares; i += kCombineThreads)
         if (p.meta[2 * i].x == kEnds) atomicMin(&ends, i);
     __syncthreads();
-    const int n = (ends < shares ? ends : shares - 1) - c + 1;  // parts; at most one per thread (shares <= kCombineThreads)
-    auto place = [&](int i) { return (int64_t)(2 * (c + i) + (i == 0)) * R + r; };
-    float2 ml = make_float2(kNothing, 0.f);
-    if (tid < n) ml = p.part_ml[place(tid)];
-    weight[tid] = ml.x;
-    __syncthreads();
-    float top = kNothing;
-    for (int i = 0; i < n; ++i) top = fmaxf(top, weight[i]);
-    __syncthreads();
-    const float f = tid < n ? exp2_fast(ml.x - top) : 0.f;
-    weight[tid] = f;
-    sums[tid] = f * ml.y;
-    __syncthreads();
-    if (tid == 0) {
-        float l = 0.f;
-        for (int i = 0; i < n; ++i) l += sums[i];
-        total = l;
+    const int n = ends - c + 1;  // parts
+    auto place = [&](int i) { return (int64_t)(2 * (c + i) + (i == 0)) * R + r0; };
+    for (int e = tid; e < n * kCombineRows; e += kCombineThreads) {
+        const int i = e / kCombineRows, r = e % kCombineRows;
+        const float2 ml = r < rows ? p.part_ml[place(i) + r] : make_float2(kNothing, 0.f);
+        weight[i][r] = ml.x;
+        sums[i][r] = ml.y;
     }
     __syncthreads();
-    const float l = total, inv = l == 0.f ? 0.f : 1.f / l;
-    const int rho = m.y + r, tok = token_of(p, rho);
-    const int64_t row = (int64_t)(m.w / p.H + tok) * p.Hq + (int64_t)(m.w % p.H) * p.group + rho - tok * p.group;
-    if (tid == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.693147180559945309f;
-    // half of the block takes the even parts, half the odd ones
-    constexpr int kHalf = kCombineThreads / 2;
-    const int half = tid / kHalf;
-    for (int c0 = 0; c0 < p.Dv; c0 += kHalf) {
-        const int ch = c0 + tid % kHalf;
-        float o = 0.f;
-        if (ch < p.Dv) {
-#pragma unroll 8
-            for (int i = half; i < n; i += 2) o = fmaf(weight[i], p.part_o[place(i) * p.Dv + ch], o);
+    const int r = tid / 32, lane = tid % 32;
+    if (r < kCombineRows) {  // a warp to a row
+        float top = kNothing, l = 0.f;
+        for (int i = lane; i < n; i += 32) top = fmaxf(top, weight[i][r]);
+        top = warp_max(top);
+        for (int i = lane; i < n; i += 32) {
+            const float w = exp2_fast(weight[i][r] - top);
+            weight[i][r] = w;
+            l = fmaf(w, sums[i][r], l);
         }
-        __syncthreads();
-        sums[tid] = o;
-        __syncthreads();
-        if (half == 0 && ch < p.Dv) p.out[row * p.Dv + ch] = (uint16_t)pack_bf16x2((sums[tid] + sums[tid + kHalf]) * inv, 0.f);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        if (lane == 0) {
+            const int rho = m.y + r0 + r, tok = token_of(p, rho);
+            const int64_t row = (int64_t)(m.w / p.H + tok) * p.Hq + (int64_t)(m.w % p.H) * p.group + rho - tok * p.group;
+            row_at[r] = row;
+            inv[r] = l == 0.f ? 0.f : 1.f / l;
+            if (p.lse && r < rows) p.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.693147180559945309f;
+        }
+    }
+    __syncthreads();
+    // four channels to a thread; where that leaves threads, they share the parts
+    const int per = p.Dv / 4, all = rows * per;
+    int groups = 1;
+    while (groups < 8 && 2 * groups * all <= kCombineThreads) groups *= 2;
+    const int lanes = kCombineThreads / groups, group = tid / lanes;
+    for (int e0 = 0; e0 < all; e0 += lanes) {
+        const int e = e0 + tid % lanes, row = e / per, ch = (e - row * per) * 4;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e < all) {
+#pragma unroll 8
+            for (int i = group; i < n; i += groups) {
+                const float4 v = *reinterpret_cast<const float4*>(p.part_o + (place(i) + row) * p.Dv + ch);
+                const float w = weight[i][row];
+                o.x = fmaf(w, v.x, o.x);
+                o.y = fmaf(w, v.y, o.y);
+                o.z = fmaf(w, v.z, o.z);
+                o.w = fmaf(w, v.w, o.w);
+            }
+        }
+        if (groups > 1) {
+            halves[tid] = o;
+            __syncthreads();
+            for (int g = 1; g < groups && group == 0; ++g) {
+                const float4 v = halves[tid + g * lanes];
+                o.x += v.x;
+                o.y += v.y;
+                o.z += v.z;
+                o.w += v.w;
+            }
+        }
+        if (group == 0 && e < all) {
+            uint16_t* out = p.out + row_at[row] * p.Dv + ch;
+            const float f = inv[row];
+            const uint32_t a = pack_bf16x2(o.x * f, o.y * f), b = pack_bf16x2(o.z * f, o.w * f);
+            out[0] = (uint16_t)a;
+            out[1] = (uint16_t)(a >> 16);
+            out[2] = (uint16_t)b;
+            out[3] = (uint16_t)(b >> 16);
+        }
     }
 }
 
@@ -1318,7 +1355,7 @@ int launch_attn(const AttnParams& p, const AttnPlan& a, const CUtensorMap& k, co
         return MLA_ERR_CUDA;
     const int st = launch_overlapped(cache_attn_kernel<R, SHARED>, (unsigned)shares, kThreads, a.smem, 0, s, k, v, p);
     if (st != MLA_OK) return st;
-    return launch_overlapped(cache_attn_combine_kernel<R>, (unsigned)(shares * R), kCombineThreads, 0, 0, s, p, shares);
+    return launch_overlapped(cache_attn_combine_kernel<R>, (unsigned)(shares * (R / kCombineRows)), kCombineThreads, 0, 0, s, p, shares);
 }
 
 }  // namespace
@@ -1368,7 +1405,7 @@ MLAQ_API int mla_cache_attn(const mla_attn_shape* shape, const mla_kv_cache* cac
     if (ds != MLA_OK) return ds;
     AttnPlan a;
     if (!attn_plan(s, c, di.max_smem_optin, &a)) return MLA_ERR_UNSUPPORTED;
-    const int shares = di.num_sms < kCombineThreads ? di.num_sms : kCombineThreads;
+    const int shares = di.num_sms < kMaxShares ? di.num_sms : kMaxShares;
     if (!workspace || ws_bytes < workspace_bytes(a.R, c.Dv, di.num_sms)) return MLA_ERR_WORKSPACE;
 
     AttnParams p{};

@@ -29,7 +29,7 @@ struct CacheParams {
     void *ek, *ev;               // the dense side
     int64_t k_t, k_h, v_t, v_h;  // its strides in elements
     int64_t pages, T, slots, units;
-    int B, width, page, block, run, H, Dk, Dv, both, heads;  // heads: of one unit
+    int B, width, page, block, block_shift, run, H, Dk, Dv, both, heads;  // heads: of one unit
     int out_bf16;
     int* status;
 };
@@ -50,8 +50,9 @@ __device__ __forceinline__ bool find_unit(const CacheParams& p, int64_t unit, Un
     u.values = r >= groups;
     u.head = (u.values ? r - groups : r) * p.heads;
     int64_t b = slot, lo = slot, n = 1, i = 0;
+    if (p.cu) b = find_sequence(p.B, slot, [&](int s) { return (int64_t)(p.cu[s] / p.run) + 2 * (int64_t)s; });
+    const int64_t start = p.start[b];  // beside cu's entries: one wait for memory
     if (p.cu) {
-        b = find_sequence(p.B, slot, [&](int s) { return (int64_t)(p.cu[s] / p.run) + 2 * (int64_t)s; });
         lo = p.cu[b];
         n = (int64_t)p.cu[b + 1] - lo;
         i = slot - (lo / p.run + 2 * b);
@@ -60,7 +61,6 @@ __device__ __forceinline__ bool find_unit(const CacheParams& p, int64_t unit, Un
             return false;
         }
     }
-    const int64_t start = p.start[b];
     if (n == 0) return false;
     const int64_t first = start / p.run + i;  // the run's number in its sequence
     int64_t a = first * p.run, e = a + p.run;
@@ -96,7 +96,15 @@ __device__ __forceinline__ uint4 load_granule(const uint16_t* q) {
     }
 }
 
-// The magnitude bits of the largest finite element among eight bf16 and m.
+// The largest magnitudes, bit for bit, of the even and the odd elements among eight bf16 and m; NaN or Inf where one is.
+__device__ __forceinline__ uint32_t amax2(const uint4& g, uint32_t m) {
+    const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7FFF7FFFu));
+    return m;
+}
+// The magnitude bits (of f32) of the largest finite element among eight bf16 and m.
 __device__ __forceinline__ uint32_t finite_amax(const uint4& g, uint32_t m) {
     const uint32_t w[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
@@ -108,7 +116,8 @@ __device__ __forceinline__ uint32_t finite_amax(const uint4& g, uint32_t m) {
     return m;
 }
 
-__device__ __forceinline__ uint2 encode_granule(const uint4& g, float s) {
+// Eight values times s as codes; bad: there are NaN or Inf among the unit's.
+__device__ __forceinline__ uint2 encode_granule(const uint4& g, float s, bool bad) {
     const uint32_t w[4] = {g.x, g.y, g.z, g.w};
     uint32_t c[2];
 #pragma unroll
@@ -116,12 +125,30 @@ __device__ __forceinline__ uint2 encode_granule(const uint4& g, float s) {
         const float v[4] = {bf16lo_to_f32(w[2 * i]), bf16hi_to_f32(w[2 * i]), bf16lo_to_f32(w[2 * i + 1]),
                             bf16hi_to_f32(w[2 * i + 1])};
         c[i] = pack_e4m3x4(v[0] * s, v[1] * s, v[2] * s, v[3] * s);
+        if (bad) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if ((__float_as_uint(v[j]) & 0x7FFFFFFFu) >= 0x7F800000u) c[i] = (c[i] & ~(0xFFu << (8 * j))) | (nan_code(v[j]) << (8 * j));
+            for (int j = 0; j < 4; ++j)
+                if ((__float_as_uint(v[j]) & 0x7FFFFFFFu) >= 0x7F800000u)
+                    c[i] = (c[i] & ~(0xFFu << (8 * j))) | (nan_code(v[j]) << (8 * j));
+        }
     }
     return make_uint2(c[0], c[1]);
 }
+
+// Granules lane, lane + lanes, ... of rows of `per`, without a division for each.
+struct Steps {
+    int row, col, rows, cols, per;
+    __device__ __forceinline__ Steps(int lane, int lanes, int per)
+        : row(lane / per), col(lane % per), rows(lanes / per), cols(lanes % per), per(per) {}
+    __device__ __forceinline__ void next() {
+        row += rows;
+        col += cols;
+        if (col >= per) {
+            col -= per;
+            ++row;
+        }
+    }
+};
 
 // A warp (WARP) or a block per unit. First pass: the new rows' amax, the first
 // kHeld granules of each thread staying in registers; second pass: codes.
@@ -145,24 +172,39 @@ __global__ void __launch_bounds__(256) kv_cache_write_kernel(const __grid_consta
     const int heads = p.H - u.head < p.heads ? p.H - u.head : p.heads;
     for (int head = 0; head < heads; ++head, src += sh, codes += (int64_t)p.page * D, mark += p.page / p.block) {
     uint4 held[kHeld];
-    uint32_t m = 0;
+    uint32_t m2 = 0;
+    Steps at(lane, lanes, per);
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) {
-        const int g = j * lanes + lane, row = g / per;
+    for (int j = 0; j < kHeld; ++j, at.next()) {
         held[j] = make_uint4(0, 0, 0, 0);
-        if (g < total) held[j] = load_granule<VEC>(src + row * st + (g - row * per) * 8);
+        if (j * lanes + lane < total) held[j] = load_granule<VEC>(src + at.row * st + at.col * 8);
     }
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) m = finite_amax(held[j], m);
-    for (int g = kHeld * lanes + lane; g < total; g += lanes) {
-        const int row = g / per;
-        m = finite_amax(load_granule<VEC>(src + row * st + (g - row * per) * 8), m);
-    }
+    for (int j = 0; j < kHeld; ++j) m2 = amax2(held[j], m2);
+    const Steps rest = at;
+    for (int g = kHeld * lanes + lane; g < total; g += lanes, at.next()) m2 = amax2(load_granule<VEC>(src + at.row * st + at.col * 8), m2);
+    uint32_t m = max((m2 << 16) & 0x7FFFFFFFu, m2 & 0x7FFF0000u);
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if constexpr (!WARP) {
         if (threadIdx.x % 32 == 0) top[threadIdx.x / 32] = m;
         __syncthreads();
         for (int i = 0; i < (int)blockDim.x / 32; ++i) m = max(m, top[i]);
+    }
+    const bool bad = m >= 0x7F800000u;  // the same in every thread of the unit
+    if (bad) {  // the others' largest
+        m = 0;
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) m = finite_amax(held[j], m);
+        at = rest;
+        for (int g = kHeld * lanes + lane; g < total; g += lanes, at.next())
+            m = finite_amax(load_granule<VEC>(src + at.row * st + at.col * 8), m);
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if constexpr (!WARP) {
+            __syncthreads();
+            if (threadIdx.x % 32 == 0) top[threadIdx.x / 32] = m;
+            __syncthreads();
+            for (int i = 0; i < (int)blockDim.x / 32; ++i) m = max(m, top[i]);
+        }
     }
     int e = e8m0_exponent_f32(__uint_as_float(m)) + 127;
     const int old_rows = u.place % p.block;
@@ -198,12 +240,11 @@ __global__ void __launch_bounds__(256) kv_cache_write_kernel(const __grid_consta
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
         const int g = j * lanes + lane;
-        if (g < total) *reinterpret_cast<uint2*>(codes + g * 8) = encode_granule(held[j], s);
+        if (g < total) *reinterpret_cast<uint2*>(codes + g * 8) = encode_granule(held[j], s, bad);
     }
-    for (int g = kHeld * lanes + lane; g < total; g += lanes) {
-        const int row = g / per;
-        *reinterpret_cast<uint2*>(codes + g * 8) = encode_granule(load_granule<VEC>(src + row * st + (g - row * per) * 8), s);
-    }
+    at = rest;
+    for (int g = kHeld * lanes + lane; g < total; g += lanes, at.next())
+        *reinterpret_cast<uint2*>(codes + g * 8) = encode_granule(load_granule<VEC>(src + at.row * st + at.col * 8), s, bad);
     if (lane == 0) *mark = (uint8_t)e;
     if constexpr (!WARP) __syncthreads();  // top, for the next head
     }
@@ -225,15 +266,19 @@ __global__ void __launch_bounds__(256) kv_cache_read_kernel(const __grid_constan
     const uint8_t* codes = (u.values ? p.v : p.k) + u.cell * D;
     const uint8_t* marks = (u.values ? p.v_scales : p.k_scales) + u.marks;
     constexpr int kFlight = 4;
+    Steps at(lane, 32, per);
     for (int base = lane; base < total; base += 32 * kFlight) {
+        int row[kFlight], col[kFlight];
         uint4 c[kFlight];
         uint32_t e[kFlight];
 #pragma unroll
         for (int j = 0; j < kFlight; ++j) {
             const int g = base + 32 * j;
+            row[j] = at.row, col[j] = at.col;
+            at.next();
             if (g < total) {
                 c[j] = *reinterpret_cast<const uint4*>(codes + (int64_t)g * 16);
-                e[j] = marks[(u.place + g / per) / p.block];
+                e[j] = marks[(u.place + row[j]) >> p.block_shift];
             }
         }
 #pragma unroll
@@ -241,8 +286,7 @@ __global__ void __launch_bounds__(256) kv_cache_read_kernel(const __grid_constan
             const int g = base + 32 * j;
             if (g >= total) break;
             const float s = e8m0_to_f32(e[j]);
-            const int row = g / per;
-            E* q = dst + row * st + (g - row * per) * 16;
+            E* q = dst + row[j] * st + col[j] * 16;
             const uint32_t w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
             if constexpr (sizeof(E) == 2) {
                 uint32_t o[8];
@@ -279,7 +323,7 @@ int check_call(const mla_kv_cache* c, int64_t B, const int32_t* table, int64_t w
     p->k = c->k, p->k_scales = c->k_scales, p->v = c->v, p->v_scales = c->v_scales;
     p->table = table, p->start = start, p->cu = cu, p->status = const_cast<int*>(status);
     p->pages = c->pages, p->T = T;
-    p->B = (int)B, p->width = (int)width, p->page = c->page, p->block = c->block, p->run = (int)run;
+    p->B = (int)B, p->width = (int)width, p->page = c->page, p->block = c->block, p->block_shift = __builtin_ctz(c->block), p->run = (int)run;
     p->H = c->H, p->Dk = c->Dk, p->Dv = c->Dv, p->both = c->v ? 2 : 1;
     p->slots = cu ? T / run + 2 * B : B;
     p->heads = 1;
