@@ -83,7 +83,6 @@ struct AttnParams {
     int slots;
     int B, width, page_shift, page, block_shift, marks, H, Hq, group, per_seq, Dk, Dv, nk, nv;
     int k_stages, v_stages, q_bufs, o_bufs, tmem_cols;  // buffers of the keys' tiles, the values', of queries, of O
-    int ahead;                            // scores of the next tile before this one's second product
     uint32_t group_mul, group_shift;      // n / group = n * group_mul >> group_shift for n < 2^31
     int q_vec;
     float scale_log2;
@@ -164,6 +163,29 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+// Which of two phases completes first (the first where both have): 0 or 1, or -1 when neither does in time.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ int wait_either(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1, volatile int* abort) {
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_test(bar0, parity0)) return 0;
+        if (mbar_test(bar1, parity1)) return 1;
+        if ((it & 63) == 0 && (*abort || globaltimer_ns() - t0 > MLAQ_WAIT_NS)) break;
+    }
+    *abort = 1;
+    return -1;
+}
 // Two f32 operations in one instruction.
 __device__ __forceinline__ void fma2(float& r0, float& r1, float a0, float a1, float b0, float b1, float c0, float c1) {
     asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
@@ -199,9 +221,9 @@ __device__ __forceinline__ int fold_rows(float (&l)[M], int lane) {
     if constexpr (O > 1) row += fold_rows<N / 2, O / 2>(l, lane);
     return row;
 }
-// Two weights (up to 256) as two E4M3 numbers each: hi, and 32 times what it leaves, by way of f16 (eleven bits, of
-// which the two keep eight). The first in bits 0-7.
-__device__ __forceinline__ void split_weights(float x, float y, uint32_t& hi, uint32_t& lo) {
+// Two numbers (up to 256) as two E4M3 numbers each: hi, and 32 times what it leaves, by way of f16 (eleven bits, of
+// which the two keep eight; of a bf16 number from 2^-14 up, all). The first in bits 0-7.
+__device__ __forceinline__ void split8(float x, float y, uint32_t& hi, uint32_t& lo) {
     uint16_t a, b;
     asm("{\n\t.reg .b32 w, h, d, k;\n\t"
         "cvt.rn.f16x2.f32 w, %3, %2;\n\t"
@@ -565,27 +587,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t dq = desc_kmajor_sw128(q_base), dw = desc_weights(p_base);
             const int whole = p.Dk / 128, rest = (p.Dk % 128 + 31) / 32;  // chunks of 128 channels, steps of 32 behind them
             Ring k_ring, v_ring;       // the next tiles' buffers
-            int k_slot = 0;            // SHARED: the buffer of tile t - 1
-            int i = -1, left = 0;      // the keys' piece and its tiles that are left
-            int vi = 0, v_at = 0;      // the values' (tile t - 1's) piece, and its tiles so far
-            int v_len = 0, len = 0;
+            int tq = 0, tp = 0;        // tiles whose first product, and whose second, was issued
+            int i = -1, left = 0, len = 0, len_before = 0;  // the first's piece, its tiles that are left; the piece's length
+            int vi = 0, v_at = 0, v_len = 0;                // the second's piece, its tiles so far
             bool ok = true;
-            const int behind = p.ahead ? 1 : 0;  // tiles that the second product is behind the first
-            for (int t = 0; t < tiles + behind && ok; ++t) {
-                const int this_slot = k_ring.i;
-                const uint32_t buf = t & 1;
-                const int len_before = len;
-                if (t < tiles) {
+            // The first product is up to two tiles ahead. Latents hold both tiles until the second product, so theirs
+            // goes first when its weights are there before the next keys are.
+            while (tp < tiles && ok) {
+                bool scores = tq < tiles && tq - tp < 2;
+                if (SHARED && scores && tq > tp) {
+                    if (left == 0) {
+                        scores = false;  // the next piece's queries may be long in coming
+                    } else {
+                        const int w = wait_either(k_full + 8 * k_ring.i, k_ring.phase, p_full + 8 * (tp & 1), (uint32_t)(tp >> 1) & 1u, abort_flag);
+                        ok = w >= 0;
+                        scores = w == 0;
+                    }
+                    if (!ok) break;
+                }
+                if (scores) {
+                    const uint32_t buf = tq & 1;
                     if (left == 0) {
                         Piece x;
                         ++i;
                         ok = get_piece(i, x);
                         mbar_arrive(piece_empty + 8 * (i % kPieces));
+                        len_before = len;
                         len = left = x.t1 - x.t0;
                         const int use = p.q_bufs == 2 ? i >> 1 : i;
                         ok = ok && wait(q_full + 8 * (p.q_bufs == 2 ? i & 1 : 0), (uint32_t)use & 1u, abort_flag);
                     }
-                    ok = ok && (t < 2 || wait(s_empty + 8 * buf, (uint32_t)((t >> 1) - 1) & 1u, abort_flag));
+                    ok = ok && (tq < 2 || wait(s_empty + 8 * buf, (uint32_t)((tq >> 1) - 1) & 1u, abort_flag));
                     const uint32_t d = s_tmem + buf * N2, qb = p.q_bufs == 2 ? (i & 1) : 0;
                     ok = ok && wait(k_full + 8 * k_ring.i, k_ring.phase, abort_flag);
                     if (!ok) break;
@@ -612,20 +644,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     k_ring.step(p.k_stages);
                     mma_commit(s_full + 8 * buf);
                     if (--left == 0) mma_commit(q_empty + 8 * qb);
-                }
-                if (t >= behind) {
-                    const int u = t - behind;
-                    const uint32_t ub = u & 1, ob = p.o_bufs == 2 ? (vi & 1) : 0;
+                    ++tq;
+                } else {
+                    const uint32_t ub = tp & 1, ob = p.o_bufs == 2 ? (vi & 1) : 0;
                     const int use = p.o_bufs == 2 ? vi >> 1 : vi;
                     if (v_at == 0) {
-                        v_len = behind ? len_before : len;
+                        v_len = i == vi ? len : len_before;
                         ok = use == 0 || wait(o_empty + 8 * ob, (uint32_t)(use - 1) & 1u, abort_flag);
                     }
-                    ok = ok && wait(p_full + 8 * ub, (uint32_t)(u >> 1) & 1u, abort_flag);
+                    ok = ok && wait(p_full + 8 * ub, (uint32_t)(tp >> 1) & 1u, abort_flag);
                     if (!SHARED) ok = ok && wait(v_full + 8 * v_ring.i, v_ring.phase, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t pt = ub * (N2 * 128), slot = SHARED ? (behind ? k_slot : this_slot) : v_ring.i;
+                    const uint32_t pt = ub * (N2 * 128), slot = SHARED ? tp % p.k_stages : v_ring.i;
                     uint32_t d = o_tmem + ob * o_cols + (kStreams == 2 ? ub * p.nv * N2 : 0);
                     uint32_t at = slot * (SHARED ? p.nk : p.nv) * kChunk;
                     const uint32_t old = v_at < kStreams ? 0u : 1u;  // not the stream's first tile of the piece
@@ -645,8 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         v_at = 0;
                         ++vi;
                     }
+                    ++tp;
                 }
-                k_slot = this_slot;
             }
             if (!ok) {
                 mma_commit(drain);
@@ -797,12 +828,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float a = bad ? 0.f : bf16lo_to_f32(u[e]) * up, b = bad ? 0.f : bf16hi_to_f32(u[e]) * up;
-                            const uint32_t h2 = cvt_e4m3x2(a, b);
-                            float ha, hb;
-                            e4m3x2_to_f32(h2, ha, hb);
+                            uint32_t h2, l2;
+                            split8(bad ? 0.f : bf16lo_to_f32(u[e]) * up, bad ? 0.f : bf16hi_to_f32(u[e]) * up, h2, l2);
                             hi[e / 2] |= h2 << (16 * (e & 1));
-                            lo[e / 2] |= cvt_e4m3x2((a - ha) * 32.f, (b - hb) * 32.f) << (16 * (e & 1));
+                            lo[e / 2] |= l2 << (16 * (e & 1));
                         }
                         const uint32_t to = q_base + qb * q_bytes + (at >> 4) * (N2 * 128) + (((at & 15) >> 1 ^ (r & 7)) << 4) + (at & 1) * 8;
                         sts_v2(to + r * 128, hi[0], hi[1]);
@@ -1116,7 +1145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 add2(l[r0 + r + k], l[r0 + r + k + 1], a, b);
                                 float y, z;
                                 mul2(y, z, a, b, f, f);
-                                split_weights(y, z, h[k / 2], o[k / 2]);
+                                split8(y, z, h[k / 2], o[k / 2]);
                             }
                             hi[r / 4] = __byte_perm(h[0], h[1], 0x5410);
                             lo[r / 4] = __byte_perm(o[0], o[1], 0x5410);
@@ -1309,10 +1338,10 @@ bool attn_plan(const mla_attn_shape& s, const mla_kv_cache& c, int max_smem, Att
                                     : shared_bytes<64>(shared);
     const size_t q = (size_t)a.nk * 2 * a.R * 128, fixed = 1024 + 2 * 2 * a.R * 128 + tail;
     const int tile = shared ? a.nk : a.nk + a.nv;
-    // two buffers of queries where three tiles (latents: two) are left, else one beside a tile (two)
+    // two buffers of queries where two tiles are left, else one beside a tile (latents: two)
     for (a.q_bufs = 2; a.q_bufs > 0; --a.q_bufs) {
         const int room = (int)(((int64_t)max_smem - (int64_t)(fixed + a.q_bufs * q)) / kChunk), stages = room / tile;
-        if (stages < (shared ? 2 : a.q_bufs == 2 ? 3 : 1)) continue;
+        if (stages < (shared || a.q_bufs == 2 ? 2 : 1)) continue;
         a.v_stages = shared ? 0 : stages > kMaxStages ? kMaxStages : stages;
         a.k_stages = (room - a.v_stages * a.nv) / a.nk;
         if (a.k_stages > kMaxStages) a.k_stages = kMaxStages;
@@ -1423,8 +1452,6 @@ MLAQ_API int mla_cache_attn(const mla_attn_shape* shape, const mla_kv_cache* cac
     p.slots = (int)slots;
     p.Dk = c.Dk, p.Dv = c.Dv, p.nk = a.nk, p.nv = a.nv, p.k_stages = a.k_stages, p.v_stages = a.v_stages, p.tmem_cols = a.tmem_cols;
     p.q_bufs = a.q_bufs, p.o_bufs = a.o_bufs;
-    // latents fill shared memory with two tiles: the second loads under the first
-    p.ahead = !shared || a.k_stages > 2;
     int bits = 0;
     while ((1 << bits) < p.group) ++bits;
     p.group_shift = 31 + bits;
