@@ -50,8 +50,8 @@ class KvCache:
     v [pages, H, page, Dv] and v_scales alike, or None: the values are then the
     first Dv channels of the keys (a latent cache; Dv defaults to all). page
     is a power of two from 16 to 1024, block one from 1 to page, Dk and Dv
-    multiples of 16. ``KvCache.empty`` allocates one. Pages need no particular
-    contents until they are written."""
+    multiples of 16, and there is a page at least. ``KvCache.empty`` allocates
+    one. Pages need no particular contents until they are written."""
 
     def __init__(self, k, k_scales, v=None, v_scales=None, Dv=None):
         self.k, self.k_scales, self.v, self.v_scales = k, k_scales, v, v_scales
@@ -79,6 +79,8 @@ class KvCache:
         dev = self.k.device
         _need(self.k_scales, "cache.k_scales", _u8, dev, ndim=3)
         per = self.k_scales.shape[2]
+        if pages < 1:
+            raise ValueError("a cache has a page at least")
         if page < 16 or page > 1024 or page & (page - 1):
             raise ValueError(f"a page must hold a power of two of 16 to 1024 tokens, got {page}")
         if per < 1 or page % per or (per & (per - 1)):
@@ -213,8 +215,11 @@ def cache_attn(q, cache, table, length, cu=None, scale=None, lse=False, out=None
     if not isinstance(cache, KvCache):
         raise TypeError("cache must be a KvCache")
     lib()
+    if scale is not None and not math.isfinite(scale):
+        raise ValueError(f"scale must be finite, got {scale}")
     c = _pkg._calls
-    if c is not None and out is None and workspace is None and status is None and stream is None and lse in (True, False):
+    if c is not None and out is None and workspace is None and status is None and stream is None and (
+            lse is True or lse is False):
         r = c.cache_attn(q, cache.k, cache.k_scales, cache.v, cache.v_scales, cache.Dv, table, length, cu,
                          math.nan if scale is None else scale, lse)
         if r is not None:
@@ -230,8 +235,6 @@ def cache_attn(q, cache, table, length, cu=None, scale=None, lse=False, out=None
     B = _sequences(table, length, "length", cu, T, dev)
     _status(status, dev)
     scale = s.Dk ** -0.5 if scale is None else float(scale)
-    if not math.isfinite(scale):
-        raise ValueError(f"scale must be finite, got {scale}")
     if out is None:
         out = _empty((T, Hq, s.Dv), _bf16, dev, stream)
     else:

@@ -50,6 +50,7 @@ constexpr uint32_t kChunk = 16384;     // 128 tokens x 128 channels
 // from L2 or not, two 10 from L2.)
 constexpr int kSoftWarps = 8, kLoader = 8, kIssuer = 9, kMarker = 10, kLoader2 = 11, kHelper = 12;
 constexpr int kThreads = 512, kHelpers = 128;
+constexpr int64_t kMaxLength = 0x7FFFFF80;  // whole tiles within an int
 constexpr int kMarkTiles = 16;         // tiles whose scales are in shared memory
 constexpr int kPieces = 4;             // pieces that are dealt out ahead
 constexpr int kPieceReaders = kSoftWarps + 3 + 4;  // warps
@@ -285,7 +286,7 @@ __device__ __noinline__ Slot read_slot(const AttnParams& p, int slot, int b) {
     const int64_t left = (int64_t)x.n * p.group - (int64_t)j * R;
     x.rho0 = j * R;
     x.rows = j < 0 || left <= 0 ? 0 : left < R ? (int)left : R;
-    const int64_t room = (int64_t)p.width << p.page_shift;
+    const int64_t table = (int64_t)p.width << p.page_shift, room = table < kMaxLength ? table : kMaxLength;
     const int len = p.length[b];
     x.len = len < 0 ? 0 : len > room ? (int)room : len;
     if (x.rows > 0 && x.len != len) record_status(p.status, MLA_ERR_POS_RANGE);
@@ -721,10 +722,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (++slot == p.slots) {
                             slot = 0;
                             x.x.b = 0;
-                            ++x.h;
+                            if (++x.h == p.H) {  // a cu that falls: the slots' tiles are not those that the share was made from
+                                record_status(p.status, MLA_ERR_INVALID_ARG);
+                                *abort_flag = 1;
+                                ok = false;
+                                break;
+                            }
                         }
                         x.x = read_slot<R>(p, slot, x.x.b);
                     } while (x.x.tiles == 0);
+                    if (!ok) break;
                 }
                 const int left = tiles - t, n = x.x.tiles - x.t0;
                 x.t1 = x.t0 + (n < left ? n : left);
