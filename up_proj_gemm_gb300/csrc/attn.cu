@@ -83,6 +83,7 @@ struct AttnParams {
     int64_t q_t, q_h, T, pages;
     int slots;
     int B, width, page_shift, page, block_shift, marks, H, Hq, group, per_seq, Dk, Dv, nk, nv;
+    int pair;                             // blocks that share tiles: 1 or 2
     int k_stages, v_stages, q_bufs, o_bufs, tmem_cols;  // buffers of the keys' tiles, the values', of queries, of O
     uint32_t group_mul, group_shift;      // n / group = n * group_mul >> group_shift for n < 2^31
     int q_vec;
@@ -139,6 +140,23 @@ __device__ __forceinline__ void tma_load_page(uint32_t dst, const void* map, int
         "l"(map), "r"(c), "r"(place), "r"(h), "r"(page), "r"(bar)
         : "memory");
 }
+// The same into both blocks of a pair, and for its barriers: each at its own addresses.
+__device__ __forceinline__ void tma_load_page_pair(uint32_t dst, const void* map, int c, int place, int h, int page,
+                                                   uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+        "l"(map), "r"(c), "r"(place), "r"(h), "r"(page), "r"(bar), "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -347,11 +365,13 @@ struct Shared {  // behind the ring, the queries and the probabilities
 };
 static_assert(sizeof(Shared<32, true>) <= 10240, "latents of five chunks: two tiles, the queries and the rest fill shared memory");
 
-template <int R, bool SHARED>
+// PAIR: blocks that share tiles. With two, a slot has 2R rows, each block has half of them, and a tile is read once for
+// both.
+template <int R, bool SHARED, int PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                       const __grid_constant__ AttnParams p) {
-    constexpr int N2 = 2 * R, kStreams = mlaq::kStreams<R>, kFour = kSoftWarps / kStreams;  // kFour: warps of a stream
+    constexpr int N2 = 2 * R, kSlotRows = R * PAIR, kStreams = mlaq::kStreams<R>, kFour = kSoftWarps / kStreams;  // kFour: warps of a stream
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -376,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid < kMaxStages) {
         mbar_init(k_full + 8 * tid, 2);
-        mbar_init(k_empty + 8 * tid, 1);
+        mbar_init(k_empty + 8 * tid, PAIR);
         mbar_init(v_full + 8 * tid, 2);
         mbar_init(v_empty + 8 * tid, 1);
     } else if (tid < kMaxStages + kMarkTiles) {
@@ -407,6 +427,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!SHARED) tma_prefetch_desc(&v_map);
     }
     fence_mbarrier_init();
+    if constexpr (PAIR > 1) {
+        __syncwarp();
+        cluster_arrive();
+    }
     if (warp == kIssuer) {
         tmem_alloc(smem_u32(&sh.tmem), p.tmem_cols);
         tmem_relinquish();
@@ -427,14 +451,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             int hi = p.B;
             while (hi - my_b > 1) {
                 const int mid = (my_b + hi) / 2;
-                if (first_slot<R>(p, mid) <= my_slot) my_b = mid;
+                if (first_slot<kSlotRows>(p, mid) <= my_slot) my_b = mid;
                 else hi = mid;
             }
         }
         int b = my_b;
 #pragma unroll 1
         for (int i = my_slot; i < my_slot + per_thread && i < p.slots; ++i) {
-            const Slot x = read_slot<R>(p, i, b);
+            const Slot x = read_slot<kSlotRows>(p, i, b);
             b = x.b;
             mine += x.tiles;
         }
@@ -459,8 +483,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     line = __shfl_sync(0xFFFFFFFFu, line, kThreads / 32 - 1);
     // equal shares, the first `all % shares` one tile longer
     const int64_t all = line * p.H;
-    const int64_t shares = all < (int64_t)gridDim.x ? all : (int64_t)gridDim.x;
-    const int c = blockIdx.x;
+    const int64_t most_shares = gridDim.x / PAIR, shares = all < most_shares ? all : most_shares;
+    const int c = blockIdx.x / PAIR, rank = PAIR > 1 ? blockIdx.x % PAIR : 0;
+    // this block's rows of a slot
+    auto own = [&](Piece x) {
+        if constexpr (PAIR > 1) {
+            x.x.rho0 += rank * R;
+            const int left = x.x.rows - rank * R;
+            x.x.rows = left < 0 ? 0 : left < R ? left : R;
+        }
+        return x;
+    };
     int tiles = 0, h0 = 0;
     if (c < shares) {
         int64_t each, w0;
@@ -482,12 +515,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             int64_t before = upto - mine;
             int b = my_b;
             for (int i = my_slot;; ++i) {
-                const Slot x = read_slot<R>(p, i, b);
+                const Slot x = read_slot<kSlotRows>(p, i, b);
                 b = x.b;
                 if (at < before + x.tiles) {
                     const int t0 = (int)(at - before), n = x.tiles - t0;
                     sh.start_slot = i;
-                    sh.piece[0] = Piece{x, h0, t0, t0 + (n < tiles ? n : tiles)};
+                    sh.piece[0] = own(Piece{x, h0, t0, t0 + (n < tiles ? n : tiles)});
                     mbar_arrive(piece_full);
                     break;
                 }
@@ -496,6 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
+    if constexpr (PAIR > 1) cluster_wait();  // the other's barriers are there
     const uint32_t tmem = sh.tmem;
     const uint32_t s_tmem = tmem, o_tmem = tmem + 2 * N2, o_cols = kStreams * p.nv * N2;  // o_cols: of one O buffer
     // Piece i as its readers get it; each warp says that it has read it.
@@ -556,9 +590,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ok = __all_sync(0xFFFFFFFFu, tile_no < stages || wait(empty, ring.phase ^ 1u, abort_flag));
                 if (!ok) break;
-                if (elect_one()) mbar_arrive_expect_tx(full, (chunks - first + 1) / 2 * count * box * 128);
+                const int halves = PAIR > 1 ? chunks : (chunks - first + 1) / 2 * 2;  // of a chunk's bytes, by this warp's arrival
+                if (elect_one()) mbar_arrive_expect_tx(full, halves * count * box * 64);
                 __syncwarp();
                 const uint32_t to = (values ? v_base : base) + ring.i * chunks * kChunk;
+                if constexpr (PAIR > 1) {  // each of the two blocks' two warps has every fourth copy
+                    int turn = 0;
+#pragma unroll 1
+                    for (int j = 0; j < chunks; ++j)
+#pragma unroll 1
+                        for (int e = 0; e < count; ++e, ++turn) {
+                            if ((turn & 3) != 2 * rank + odd) continue;
+                            const int from = __shfl_sync(0xFFFFFFFFu, page, e);
+                            if (elect_one()) tma_load_page_pair(to + j * kChunk + e * box * 128, map, j * 128, k.place, k.h, from, full);
+                        }
+                } else
 #pragma unroll 1
                 for (int j = first; j < chunks; j += 2)
 #pragma unroll 1
@@ -669,7 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         d += N2;
                         at += kChunk;
                     }
-                    mma_commit((SHARED ? k_empty : v_empty) + 8 * slot);
+                    if constexpr (PAIR > 1) mma_commit_pair(k_empty + 8 * slot);
+                    else mma_commit((SHARED ? k_empty : v_empty) + 8 * slot);
                     if (!SHARED) v_ring.step(p.v_stages);
                     mma_commit(p_empty + 8 * ub);
                     if (++v_at == v_len) {
@@ -701,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= kPieces) ok = wait(piece_empty + 8 * (i % kPieces), (uint32_t)(i / kPieces - 1) & 1u, abort_flag);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (ok && lane == 0) {
-                sh.piece[i % kPieces] = x;
+                sh.piece[i % kPieces] = own(x);
                 mbar_arrive(piece_full + 8 * (i % kPieces));
             }
             ++i;
@@ -729,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 break;
                             }
                         }
-                        x.x = read_slot<R>(p, slot, x.x.b);
+                        x.x = read_slot<kSlotRows>(p, slot, x.x.b);
                     } while (x.x.tiles == 0);
                     if (!ok) break;
                 }
@@ -775,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         bool failed = false;
         int parts = 0;  // which of the share's two places in the workspace it has filled
-        constexpr int kG = (kMaxQueryChunks * 128 / 8 + 31) / 32;
+        constexpr int kG = SHARED ? (kMaxQueryChunks * 128 / 8 + 31) / 32 : 1;
         const int gran = p.Dk / 8;
         // eight bf16 at a time of a piece's query row r, as many as a lane has
         auto fetch = [&](const Piece& x, int r, uint4 (&g)[kG]) {
@@ -877,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int use = p.o_bufs == 2 ? i >> 1 : i;
             failed |= !wait(sums_full + 8 * par, (uint32_t)(i >> 1) & 1u, abort_flag);
             const bool whole = now.t0 == 0 && now.t1 == now.x.tiles;
-            const int part = 2 * c + (now.t0 == 0 ? 1 : 0);
+            const int part = 2 * (int)blockIdx.x + (now.t0 == 0 ? 1 : 0);
             if (htid < R) {
                 float m = kNothing, sum = 0.f, f[kStreams];
                 for (int k = 0; k < kStreams; ++k) m = fmaxf(m, -sh.ref[par][k][htid]);
@@ -977,7 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (htid == 0)
             for (int k = 0; k < 2; ++k)
-                if (!(parts >> k & 1)) p.meta[2 * c + k] = make_int4(kNoPart, 0, 0, 0);
+                if (!(parts >> k & 1)) p.meta[2 * blockIdx.x + k] = make_int4(kNoPart, 0, 0, 0);
     } else {
         // ------------------------------------------------------------ softmax
         constexpr int kFours = kFour / 4, RT = R / kFours;  // rows of a thread
@@ -1221,6 +1268,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, p.tmem_cols);
     }
+    if constexpr (PAIR > 1) {  // neither leaves while the other may still write to it
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
 // Adds the parts of the pair that share blockIdx.x / (R / 8) opens, eight query
@@ -1241,13 +1293,14 @@ __global__ void __launch_bounds__(kCombineThreads) cache_attn_combine_kernel(con
     const int rows = m.z - r0 < kCombineRows ? m.z - r0 : kCombineRows;
     if (m.x != kOpens || rows <= 0) return;
     // the shares behind go on with the pair until one ends it
-    if (tid == 0) ends = shares - 1;
+    const int behind = (shares - 1 - c) / p.pair;
+    if (tid == 0) ends = behind;
     __syncthreads();
-    for (int i = c + 1 + tid; i < shares; i += kCombineThreads)
-        if (p.meta[2 * i].x == kEnds) atomicMin(&ends, i);
+    for (int i = 1 + tid; i <= behind; i += kCombineThreads)
+        if (p.meta[2 * (c + i * p.pair)].x == kEnds) atomicMin(&ends, i);
     __syncthreads();
-    const int n = ends - c + 1;  // parts
-    auto place = [&](int i) { return (int64_t)(2 * (c + i) + (i == 0)) * R + r0; };
+    const int n = ends + 1;  // parts
+    auto place = [&](int i) { return (int64_t)(2 * (c + i * p.pair) + (i == 0)) * R + r0; };
     for (int e = tid; e < n * kCombineRows; e += kCombineThreads) {
         const int i = e / kCombineRows, r = e % kCombineRows;
         const float2 ml = r < rows ? p.part_ml[place(i) + r] : make_float2(kNothing, 0.f);
@@ -1320,7 +1373,7 @@ __global__ void __launch_bounds__(kCombineThreads) cache_attn_combine_kernel(con
 
 // -------------------------------------------------------------------- host
 struct AttnPlan {
-    int R, nk, nv, k_stages, v_stages, q_bufs, o_bufs, tmem_cols;
+    int R, pair, nk, nv, k_stages, v_stages, q_bufs, o_bufs, tmem_cols;
     size_t smem;
 };
 
@@ -1339,6 +1392,7 @@ bool attn_plan(const mla_attn_shape& s, const mla_kv_cache& c, int max_smem, Att
     a.nv = (c.Dv + 127) / 128;
     const int64_t group = s.Hq / c.H, rows = group * (s.B > 0 ? (s.T + s.B - 1) / s.B : 1);
     a.R = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || a.nv > 2 ? 32 : 64;
+    a.pair = shared && rows > a.R ? 2 : 1;
     const size_t tail = a.R == 8    ? shared_bytes<8>(shared)
                         : a.R == 16 ? shared_bytes<16>(shared)
                         : a.R == 32 ? shared_bytes<32>(shared)
@@ -1384,12 +1438,12 @@ size_t workspace_bytes(int R, int Dv, int shares) {
     return (size_t)shares * 2 * (R * ((size_t)Dv * 4 + 8) + 16);
 }
 
-template <int R, bool SHARED>
+template <int R, bool SHARED, int PAIR>
 int launch_attn(const AttnParams& p, const AttnPlan& a, const CUtensorMap& k, const CUtensorMap& v, int shares,
                 cudaStream_t s) {
-    if (cudaFuncSetAttribute(cache_attn_kernel<R, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)a.smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(cache_attn_kernel<R, SHARED, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)a.smem) != cudaSuccess)
         return MLA_ERR_CUDA;
-    const int st = launch_overlapped(cache_attn_kernel<R, SHARED>, (unsigned)shares, kThreads, a.smem, 0, s, k, v, p);
+    const int st = launch_overlapped(cache_attn_kernel<R, SHARED, PAIR>, (unsigned)shares, kThreads, a.smem, PAIR > 1 ? PAIR : 0, s, k, v, p);
     if (st != MLA_OK) return st;
     return launch_overlapped(cache_attn_combine_kernel<R>, (unsigned)(shares * (R / kCombineRows)), kCombineThreads, 0, 0, s, p, shares);
 }
@@ -1441,7 +1495,7 @@ MLAQ_API int mla_cache_attn(const mla_attn_shape* shape, const mla_kv_cache* cac
     if (ds != MLA_OK) return ds;
     AttnPlan a;
     if (!attn_plan(s, c, di.max_smem_optin, &a)) return MLA_ERR_UNSUPPORTED;
-    const int shares = di.num_sms < kMaxShares ? di.num_sms : kMaxShares;
+    const int shares = (di.num_sms < kMaxShares ? di.num_sms : kMaxShares) / a.pair * a.pair;
     if (!workspace || ws_bytes < workspace_bytes(a.R, c.Dv, di.num_sms)) return MLA_ERR_WORKSPACE;
 
     AttnParams p{};
@@ -1453,8 +1507,10 @@ MLAQ_API int mla_cache_attn(const mla_attn_shape* shape, const mla_kv_cache* cac
     p.q_t = s.q_t, p.q_h = s.q_h, p.T = s.T, p.pages = c.pages;
     p.B = (int)s.B, p.width = (int)s.table_width, p.page = c.page, p.page_shift = __builtin_ctz(c.page);
     p.block_shift = __builtin_ctz(c.block), p.marks = c.page / c.block, p.H = c.H, p.Hq = s.Hq, p.group = s.Hq / c.H;
-    p.per_seq = (p.group + a.R - 1) / a.R;
-    const int64_t slots = cu ? s.T * p.group / a.R + s.B : s.B * p.per_seq;
+    const int slot_rows = a.R * a.pair;
+    p.pair = a.pair;
+    p.per_seq = (p.group + slot_rows - 1) / slot_rows;
+    const int64_t slots = cu ? s.T * p.group / slot_rows + s.B : s.B * p.per_seq;
     if (slots > kI32Max) return MLA_ERR_UNSUPPORTED;
     p.slots = (int)slots;
     p.Dk = c.Dk, p.Dv = c.Dv, p.nk = a.nk, p.nv = a.nv, p.k_stages = a.k_stages, p.v_stages = a.v_stages, p.tmem_cols = a.tmem_cols;
@@ -1475,14 +1531,16 @@ MLAQ_API int mla_cache_attn(const mla_attn_shape* shape, const mla_kv_cache* cac
     if (ms != MLA_OK) return ms;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (shared)
-        return a.R == 8    ? launch_attn<8, true>(p, a, km, vm, shares, cs)
-               : a.R == 16 ? launch_attn<16, true>(p, a, km, vm, shares, cs)
-               : a.R == 32 ? launch_attn<32, true>(p, a, km, vm, shares, cs)
-                           : launch_attn<64, true>(p, a, km, vm, shares, cs);
-    return a.R == 8    ? launch_attn<8, false>(p, a, km, vm, shares, cs)
-           : a.R == 16 ? launch_attn<16, false>(p, a, km, vm, shares, cs)
-           : a.R == 32 ? launch_attn<32, false>(p, a, km, vm, shares, cs)
-                       : launch_attn<64, false>(p, a, km, vm, shares, cs);
+        return a.R == 8    ? launch_attn<8, true, 1>(p, a, km, vm, shares, cs)
+               : a.R == 16 ? launch_attn<16, true, 1>(p, a, km, vm, shares, cs)
+               : a.R == 32 ? (a.pair == 2 ? launch_attn<32, true, 2>(p, a, km, vm, shares, cs)
+                                          : launch_attn<32, true, 1>(p, a, km, vm, shares, cs))
+                           : (a.pair == 2 ? launch_attn<64, true, 2>(p, a, km, vm, shares, cs)
+                                          : launch_attn<64, true, 1>(p, a, km, vm, shares, cs));
+    return a.R == 8    ? launch_attn<8, false, 1>(p, a, km, vm, shares, cs)
+           : a.R == 16 ? launch_attn<16, false, 1>(p, a, km, vm, shares, cs)
+           : a.R == 32 ? launch_attn<32, false, 1>(p, a, km, vm, shares, cs)
+                       : launch_attn<64, false, 1>(p, a, km, vm, shares, cs);
 }
 
 }  // extern "C"
