@@ -132,6 +132,16 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
     *abort = 1;
     return false;
 }
+// The same with the waiting itself out of line (FAR), for warps that hold few values across it. Which warps' waits are
+// out of line was measured for each R, the softmax's and the loaders' never: the issuer's up to R = 16 (64 sequences of 8192
+// tokens 104.7 -> 103.4 us; at R = 64 slower, 1497 -> 1509), the helpers' at R = 64 (a chunk of 128 heads 1497 -> 1457;
+// at R = 32 nothing).
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort) { return wait(bar, parity, abort); }
+template <bool FAR>
+__device__ __forceinline__ bool wait_by(uint32_t bar, uint32_t parity, volatile int* abort) {
+    if constexpr (FAR) return mbar_try_wait(bar, parity) || wait_on(bar, parity, abort);
+    else return wait(bar, parity, abort);
+}
 __device__ __forceinline__ void tma_load_page(uint32_t dst, const void* map, int c, int place, int h, int page,
                                               uint32_t bar) {
     asm volatile(
@@ -157,6 +167,17 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Columns of a lane, W at a time.
+template <int W>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[W]) {
+    if constexpr (W == 16) {
+        tmem_ld16(taddr, r);
+    } else {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+    }
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -662,11 +683,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         len_before = len;
                         len = left = x.t1 - x.t0;
                         const int use = p.q_bufs == 2 ? i >> 1 : i;
-                        ok = ok && wait(q_full + 8 * (p.q_bufs == 2 ? i & 1 : 0), (uint32_t)use & 1u, abort_flag);
+                        ok = ok && wait_by<(R <= 16)>(q_full + 8 * (p.q_bufs == 2 ? i & 1 : 0), (uint32_t)use & 1u, abort_flag);
                     }
-                    ok = ok && (tq < 2 || wait(s_empty + 8 * buf, (uint32_t)((tq >> 1) - 1) & 1u, abort_flag));
+                    ok = ok && (tq < 2 || wait_by<(R <= 16)>(s_empty + 8 * buf, (uint32_t)((tq >> 1) - 1) & 1u, abort_flag));
                     const uint32_t d = s_tmem + buf * N2, qb = p.q_bufs == 2 ? (i & 1) : 0;
-                    ok = ok && wait(k_full + 8 * k_ring.i, k_ring.phase, abort_flag);
+                    ok = ok && wait_by<(R <= 16)>(k_full + 8 * k_ring.i, k_ring.phase, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
                     uint32_t qt = qb * q_bytes, at = k_ring.i * p.nk * kChunk;
@@ -697,10 +718,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int use = p.o_bufs == 2 ? vi >> 1 : vi;
                     if (v_at == 0) {
                         v_len = i == vi ? len : len_before;
-                        ok = use == 0 || wait(o_empty + 8 * ob, (uint32_t)(use - 1) & 1u, abort_flag);
+                        ok = use == 0 || wait_by<(R <= 16)>(o_empty + 8 * ob, (uint32_t)(use - 1) & 1u, abort_flag);
                     }
-                    ok = ok && wait(p_full + 8 * ub, (uint32_t)(tp >> 1) & 1u, abort_flag);
-                    if (!SHARED) ok = ok && wait(v_full + 8 * v_ring.i, v_ring.phase, abort_flag);
+                    ok = ok && wait_by<(R <= 16)>(p_full + 8 * ub, (uint32_t)(tp >> 1) & 1u, abort_flag);
+                    if (!SHARED) ok = ok && wait_by<(R <= 16)>(v_full + 8 * v_ring.i, v_ring.phase, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t pt = ub * (N2 * 128), slot = SHARED ? tp % p.k_stages : v_ring.i;
@@ -851,12 +872,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int par = i & 1;
             const uint32_t qb = p.q_bufs == 2 ? par : 0;
             const int use = p.q_bufs == 2 ? i >> 1 : i;
+            if constexpr (SHARED) {
+                // all of the rows' lines at once: one by one they queue behind the first tiles of all SMs
+#pragma unroll 1
+                for (int r = quad; r < x.x.rows; r += 4) {
+                    const int rho = x.x.rho0 + r, tok = token_of(p, rho);
+                    const uint16_t* src = p.q + (int64_t)(x.x.lo + tok) * p.q_t + (int64_t)(x.h * p.group + rho - tok * p.group) * p.q_h;
+                    if (lane * 64 < p.Dk) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + lane * 64));
+                }
+            }
             uint4 g[kG], g2[kG];
 #pragma unroll 1
             for (int r = quad - 4; r < R; r += 4) {
                 fetch(x, r + 4, g2);
                 if (r < 0) {
-                    if (use > 0) failed |= !wait(q_empty + 8 * qb, (uint32_t)(use - 1) & 1u, abort_flag);
+                    if (use > 0) failed |= !wait_by<(R == 64)>(q_empty + 8 * qb, (uint32_t)(use - 1) & 1u, abort_flag);
 #pragma unroll
                     for (int k = 0; k < kG; ++k) g[k] = g2[k];
                     continue;
@@ -922,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int par = i & 1;
             const uint32_t ob = p.o_bufs == 2 ? par : 0;
             const int use = p.o_bufs == 2 ? i >> 1 : i;
-            failed |= !wait(sums_full + 8 * par, (uint32_t)(i >> 1) & 1u, abort_flag);
+            failed |= !wait_by<(R == 64)>(sums_full + 8 * par, (uint32_t)(i >> 1) & 1u, abort_flag);
             const bool whole = now.t0 == 0 && now.t1 == now.x.tiles;
             const int part = 2 * (int)blockIdx.x + (now.t0 == 0 ? 1 : 0);
             if (htid < R) {
@@ -943,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else if (p.lse && htid < now.x.rows)
                     p.lse[sh.row_at[par][htid]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945309f;
             }
-            failed |= !wait(o_full + 8 * ob, (uint32_t)use & 1u, abort_flag);
+            failed |= !wait_by<(R == 64)>(o_full + 8 * ob, (uint32_t)use & 1u, abort_flag);
             if (!named_bar_and(3, kHelpers, !failed)) break;
             tc_fence_after();
             const bool nans = *(volatile int*)&sh.nan_seen[par] != 0;
@@ -1028,6 +1058,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ------------------------------------------------------------ softmax
         constexpr int kFours = kFour / 4, RT = R / kFours;  // rows of a thread
+        constexpr int kWide = RT > 16 ? 8 : 16;             // scores read at a time (with sixteen of 32, registers ran out)
         const int tok = tid & 127, quad = warp & 3, four = warp >> 2, stream = kStreams == 2 ? four : 0;
         const int r_lo = kStreams == 2 ? 0 : four * RT;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;  // this warp's lanes of tensor memory
@@ -1076,19 +1107,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto scores = [&](auto less) {
                     const uint32_t from = s_tmem + lanes + buf * N2 + r_lo;
 #pragma unroll
-                    for (int r0 = 0; r0 < RT; r0 += 16) {
-                        uint32_t v[16], u[16];
-                        tmem_ld16(from + r0, v);
-                        if constexpr (R > 8) tmem_ld16(from + R + r0, u);
+                    for (int r0 = 0; r0 < RT; r0 += kWide) {
+                        uint32_t v[kWide], u[kWide];
+                        tmem_ld<kWide>(from + r0, v);
+                        if constexpr (R > 8) tmem_ld<kWide>(from + R + r0, u);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int r = 0; r < (RT < 16 ? RT : 16); r += 4) {
+                        for (int r = 0; r < (RT < kWide ? RT : kWide); r += 4) {
                             const float4 q = *reinterpret_cast<const float4*>(unit + r0 + r);
                             const float4 m = *reinterpret_cast<const float4*>(ref + r0 + r);
                             const float qs[4] = {q.x, q.y, q.z, q.w}, ms[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
                             for (int e = 0; e < 4; e += 2) {
-                                const uint32_t *h = &v[r + e], *o = R > 8 ? &u[r + e] : &v[(8 + r + e) & 15];
+                                const uint32_t *h = &v[r + e], *o = R > 8 ? &u[r + e] : &v[(8 + r + e) % kWide];
                                 float &x0 = x[r0 + r + e], &x1 = x[r0 + r + e + 1];
                                 float k0, k1;
                                 mul2(k0, k1, qs[e], qs[e + 1], ks, ks);
