@@ -2,12 +2,14 @@
 // values as E4M3 codes and one power-of-two scale per block of tokens.
 //
 // The codes go to the tensor cores as they are. The query is split into two
-// E4M3 numbers instead: with a row scaled to amax < 256, hi = e4m3(q) leaves a
-// residual of at most four bits of a bf16 q, so lo = e4m3(32 (q - hi)) holds the
-// rest and q = hi + lo / 32 exactly (down to 2^-14 of the row's largest; below
-// that to 2^-22 of it). Probabilities, as f32, are split the same way and enter
-// the second product with eight bits, the precision of bf16. So no cached byte
-// is ever converted, and both products run at the 8-bit rate.
+// E4M3 numbers instead: with a row scaled to amax in [128, 256), hi = e4m3(q)
+// leaves a residual of at most four bits of a bf16 q, so lo = e4m3(32 (q - hi))
+// holds the rest and q = hi + lo / 32 exactly (down to 2^-14 of the row's
+// largest; below that to 2^-22 of it). Both go by way of f16, whose eleven bits
+// are more than the two keep. Probabilities, as f32, are split the same way and
+// enter the second product with eight bits, the precision of bf16: the rounding
+// of a result to bf16 is as large. So no cached byte is ever converted, and both
+// products run at the 8-bit rate.
 //
 // Both products have the cached tokens as their 128 rows:
 //   S^T [128 tokens, 2R] = K [128, Dk] x [q_hi | q_lo]^T   (R query rows)
@@ -29,6 +31,21 @@
 // long sequence fills every SM alike. A share's first and last pair may be
 // parts; their O, maximum and sum go to the workspace and a second kernel adds
 // the parts in the order of the shares.
+//
+// What bounds it, by calls in a graph:
+// - Tokens over keys and values of their own: HBM. 64 sequences of up to 8192
+//   tokens, 8 heads of 128 + 128 (608 MB): 103.5 us, 5.9 TB/s, 88% of a copy's rate;
+//   in pages of 128 and more 100 us. Pages of 32 and 16 take 113 and 136: a copy's
+//   fixed 50 ns. 512 sequences of 1024: 174 us; a piece of eight tiles is too short
+//   to hide bringing its queries in and its result out.
+// - Latents (576 channels, 512 of them values, 128 query heads): the chain copy (2600
+//   clocks) -> first product (1100) -> softmax (1100) -> second product (1300, and
+//   600 until it starts), with room for two tiles of 80 KB. 48 sequences of up to 4096:
+//   100 us, of which a third is the first queries, the results of parts and
+//   their addition; 256 sequences: 335 us, 0.5 PFLOP/s.
+// - A chunk of 2048 tokens, 128 heads of 192 + 128, over 4096 positions: 1459 us, 589
+//   TFLOP/s. The softmax: 128 x 64 scores are 32 a thread, with four conversions for
+//   each two of them (the 8-bit pairs), at a quarter of the rate of an addition.
 #include <cuda.h>
 
 #include <type_traits>
@@ -57,7 +74,10 @@ constexpr int kPieceReaders = kSoftWarps + 3 + 4;  // warps
 // Four softmax warps hold a tile's tokens, a token to a thread. With few query rows
 // a tile is a chain of waits, and the two fours take turns (two streams, each with
 // its own references, sums and O, joined in the end); with many it is arithmetic,
-// and they halve the rows, each with its references and at its own pace.
+// and they halve the rows, each with its references and at its own pace. (Two streams
+// need O twice, which tensor memory has up to R = 16 for every size. In the version that
+// brought them a decode batch went from 205 to 183 us and a chunk, whose fours halve the
+// rows, from 7.7 to 2.9 ms, with the weights stored whole per token as the rest of it.)
 template <int R>
 constexpr int kStreams = R <= 16 ? 2 : 1;
 constexpr float kPass = 4.f;           // log2 of how far scores may pass the reference
@@ -386,8 +406,10 @@ struct Shared {  // behind the ring, the queries and the probabilities
 };
 static_assert(sizeof(Shared<32, true>) <= 10240, "latents of five chunks: two tiles, the queries and the rest fill shared memory");
 
-// PAIR: blocks that share tiles. With two, a slot has 2R rows, each block has half of them, and a tile is read once for
-// both.
+// PAIR: blocks that share tiles. With two (a cluster), a slot has 2R rows, each block has half of them, and a tile is read
+// from L2 once for both: each brings half of the boxes, for both, once both have let go of the place. Latents only: with
+// R = 32 of 128 heads four blocks read the same tiles, at 4.4 TB/s together (256 sequences of 4096: 387 us, so 343). Keys
+// and values of one head are read by few blocks, and their softmax takes longer than their copies.
 template <int R, bool SHARED, int PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
@@ -1411,7 +1433,9 @@ struct AttnPlan {
 // Query rows of a tile: as many as a head of the cache has for a sequence (the
 // group times the new tokens, on average), up to 64; with more than two value
 // tiles up to 32, for tensor memory's sake: 2 score buffers and nv sums of 2R
-// columns each, 512 in all.
+// columns each, 512 in all. (More rows than there are would only add to both
+// products and the softmax: eight rows over latents take 29 us with R = 8, and 32
+// take 42 with R = 32. Fewer would read the cache again for the others.)
 template <int R>
 size_t shared_bytes(bool shared) { return shared ? sizeof(Shared<R, true>) : sizeof(Shared<R, false>); }
 
