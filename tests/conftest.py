@@ -3,6 +3,7 @@
 Tests marked ``gpu`` need a CUDA device and the in-tree ``libmlaq.so``; the
 rest run on the CPU (oracle pins, host-side argument checks, symbol exports).
 """
+import ctypes
 import os
 import sys
 
@@ -23,3 +24,19 @@ def cuda_device():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
     return torch.device("cuda:0")
+
+
+@pytest.fixture(autouse=True)
+def fresh_small_blocks(request):
+    """Blocks that the C library kept from earlier tests and imports stay away from the optimizer loop's tests, which tell
+    a dropped buffer from a new one by its address: with a full list of kept blocks of one size, a new buffer could
+    get the dropped one's place."""
+    if request.module.__name__ != "test_adamw_loop":
+        yield
+        return
+    libc = ctypes.CDLL(None)
+    libc.malloc.restype, libc.malloc.argtypes, libc.free.argtypes = ctypes.c_void_p, [ctypes.c_size_t], [ctypes.c_void_p]
+    held = [libc.malloc(size) for size in range(24, 1025, 16) for _ in range(64)]
+    yield
+    for block in held:
+        libc.free(block)
