@@ -12,7 +12,8 @@
 // weights stay in its registers for all of its rows. In a graph, bf16 with the
 // residual: 8192 x 7168 75.6 us (6.2 TB/s, 93% of a copy's rate), its gradient with
 // dh 83 to 86 (by box; 5.6 TB/s); short calls are a launch and one row's chain of
-// load, sum and store: 1 x 1536 as MXFP8 2.1 us, 4099 x 1536 9.6.
+// load, sum and store: 1 x 1536 as MXFP8 2.1 us, 4099 x 1536 8.3. (MXFP8 of large
+// calls is bound by instructions: 8192 x 7168 66 us, of 26 for its bytes.)
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -217,10 +218,13 @@ __global__ void __launch_bounds__(kMaxThreads<WARP, GPT>) rms_norm_kernel(const 
 #pragma unroll
         for (int j = 0; j < GPT; ++j) {
 #pragma unroll
-            for (int i = 0; i < kG; ++i) {
-                v[j][i] = raw[j].get(i) + (res ? add[j].get(i) : 0.f);
-                sum = fmaf(v[j][i], v[j][i], sum);
+            for (int i = 0; i < kG; ++i) v[j][i] = raw[j].get(i);
+            if (res) {
+#pragma unroll
+                for (int i = 0; i < kG; ++i) v[j][i] += add[j].get(i);
             }
+#pragma unroll
+            for (int i = 0; i < kG; ++i) sum = fmaf(v[j][i], v[j][i], sum);
             if (res) {
                 raw[j].set(v[j]);
                 raw[j].store(static_cast<E*>(p.h) + t * p.K, l, j);
@@ -228,6 +232,7 @@ __global__ void __launch_bounds__(kMaxThreads<WARP, GPT>) rms_norm_kernel(const 
         }
         const float rstd = __frsqrt_rn(fmaf(row_sum<WARP>(sum, buf, turn), p.inv_k, p.eps));
         if (p.rstd && l.lane == 0) p.rstd[t] = rstd;
+        uint8_t* row_scales = MX && p.tiled ? p.scales + sf_tiled_offset(t, 0, 128, nkt) : nullptr;
 #pragma unroll
         for (int j = 0; j < GPT; ++j) {
             if constexpr (!kHold) load_weights<L>(p, l, j, w[0]);
@@ -238,8 +243,7 @@ __global__ void __launch_bounds__(kMaxThreads<WARP, GPT>) rms_norm_kernel(const 
                 uint32_t m = 0;
 #pragma unroll
                 for (int i = 0; i < kG; ++i) {
-                    if (c >= p.K) v[j][i] = 0.f;  // nothing there, and 0 * rstd may be NaN
-                    m = max(m, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+                    m = max(m, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);  // a block's four lanes are inside K or behind it
                 }
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(kMaxThreads<WARP, GPT>) rms_norm_kernel(const 
                 if (c < p.K) {
                     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + t * p.K + c) = make_uint2(codes[0], codes[1]);
                     if (l.lane % 4 == 0) {
-                        if (p.tiled) p.scales[sf_tiled_offset(t, c / 32, 128, nkt)] = (uint8_t)s;
+                        if (p.tiled) row_scales[(c >> 7) * 512 + ((c >> 5) & 3)] = (uint8_t)s;  // as sf_tiled_offset
                         else p.scales[t * (p.K / 32) + c / 32] = (uint8_t)s;
                     }
                 }
@@ -474,7 +478,7 @@ struct NormGrid {
 // 7168: 2.6 us, with two 3.1), then two (8192 x 7168: 75.6 us, with one 102.6; 8192
 // x 2048: 20.9, with one 24.7; its gradient 27.2, with one 32.0), and four or eight
 // where the block would pass 512 threads.
-NormGrid norm_grid(int64_t T, int64_t K, int num_sms, bool bwd) {
+NormGrid norm_grid(int64_t T, int64_t K, int num_sms, bool bwd, bool mx = false) {
     const int64_t granules = (K + kG - 1) / kG;
     NormGrid g{};
     if (granules <= 32 || (granules <= 128 && (bwd || T >= (int64_t)num_sms * kWarpRows))) {
@@ -487,7 +491,10 @@ NormGrid norm_grid(int64_t T, int64_t K, int num_sms, bool bwd) {
     }
     g.gpt = granules <= 1024 && (T < num_sms || granules <= 128) ? 1 : granules <= 1024 ? 2 : granules <= 2048 ? 4 : 8;
     g.threads = (unsigned)((granules + 32 * g.gpt - 1) / (32 * g.gpt) * 32);
-    const int per = (int)(2048 / g.threads) < 1 ? 1 : (int)(2048 / g.threads);
+    // Blocks to an SM: as its threads allow; MXFP8 with more than one granule as its registers do (88 a thread), so that a
+    // block goes on to its next row, already on its way, instead of others' first ones (8192 x 1536: 14.1 us, else 15.7;
+    // 8192 x 7168: 66.4, else 69.5). Results in x's type want the threads (8192 x 1536: 15.2, with fewer 20.0).
+    const int fill = mx && g.gpt > 1 ? 640 : 2048, per = fill / (int)g.threads < 1 ? 1 : fill / (int)g.threads;
     const int64_t room = (int64_t)num_sms * (bwd ? (per > 4 ? 4 : per) : per);
     g.blocks = (unsigned)(T < room ? T : room);
     return g;
@@ -612,7 +619,7 @@ MLAQ_API int mla_rms_norm_fwd(const mla_norm_shape* shape, const void* x, const 
     const int64_t ve = 16 / size;
     const bool vec = s.K % kG == 0 && aligned(x, 16) && aligned(residual, 16) && aligned(weight, 16) &&
                      aligned(h, 16) && (mx || aligned(y, 16)) && p.ld_x % ve == 0 && p.ld_res % ve == 0;
-    const NormGrid g = norm_grid(s.T, s.K, di.num_sms, false);
+    const NormGrid g = norm_grid(s.T, s.K, di.num_sms, false, mx);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (p.x_bf16)
         return mx ? (vec ? launch_fwd_rows<uint16_t, true, kWhole>(p, g, cs) : launch_fwd_rows<uint16_t, true, kSingle>(p, g, cs))
