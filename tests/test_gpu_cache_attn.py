@@ -118,6 +118,45 @@ def test_several_tokens(cuda_device, c):
     check(out, ref[0], ref[2], "out")
 
 
+PAIRS = [  # latents with more query rows than a block takes: two blocks share their tiles
+    dict(Hq=40, c=dict(H=1, Dk=576, Dv=512, page=16, block=16, start=[300, 0, 127], n=[1, 1, 1], shared=True)),
+    dict(Hq=128, c=dict(H=1, Dk=320, Dv=256, page=128, block=32, start=[1000, 40], n=[1, 1], shared=True)),
+    dict(Hq=200, c=dict(H=2, Dk=144, Dv=96, page=256, block=128, start=[600, 0, 0], n=[1, 0, 1], shared=True)),
+    dict(Hq=33, c=dict(H=1, Dk=640, Dv=512, page=32, block=1, start=[5, 250], n=[9, 4], shared=True)),
+    dict(Hq=3, c=dict(H=1, Dk=512, Dv=512, page=1024, block=64, start=[100, 0, 700], n=[60, 0, 33], shared=True)),
+    dict(Hq=128, c=dict(H=1, Dk=576, Dv=512, page=64, block=64, start=[12000], n=[1], shared=True)),
+]
+
+
+@pytest.mark.parametrize("c", PAIRS)
+def test_latents_of_many_rows(cuda_device, c):
+    s = Case(cuda_device, **c["c"])
+    q, scale, out, lse = attend(cuda_device, s, c["Hq"])
+    ref = reference(s, q, scale)
+    check(lse, ref[1], ref[3], "lse")
+    check(out, ref[0], ref[2], "out")
+    _, _, again, _ = attend(cuda_device, s, c["Hq"])
+    assert torch.equal(out, again)
+
+
+def test_nan_in_latents_of_many_rows(cuda_device):
+    """A NaN in one channel of a cached row: the rows that see it, each in both blocks of a pair, and no others; a bad page."""
+    s = Case(cuda_device, H=1, Dk=320, Dv=256, page=16, block=16, start=[150], n=[20], shared=True)
+    at = 155
+    p = int(s.table[0, at // 16])
+    s.host[0][p, 0, at % 16, 300] = 0x7F  # behind the values: a score of NaN
+    s.cache.k.copy_(s.host[0])
+    q, scale, out, lse = attend(cuda_device, s, 8)
+    ref = reference(s, q, scale)
+    assert out[5:].isnan().all() and lse[5:].isnan().all()
+    check(out[:5], ref[0][:5], ref[2][:5], "out")
+    st = torch.zeros(1, dtype=i32, device=cuda_device)
+    table = s.table_d.clone()
+    table[0, 2] = 2 ** 30
+    o = mlaq.cache_attn(q[:, :, :].to(cuda_device), s.cache, table, s.length_d, cu=s.cu, scale=scale, status=st)
+    assert st.item() == mlaq.STATUS["MLA_ERR_POS_RANGE"] and o[:5].isfinite().all()
+
+
 def test_one_long_sequence_over_every_sm(cuda_device):
     """More tiles than shares: parts that begin and end inside a pair, added in the second kernel."""
     s = Case(cuda_device, H=1, Dk=64, Dv=80, page=128, block=128, start=[40_000], n=[1])
