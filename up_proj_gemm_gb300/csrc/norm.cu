@@ -12,8 +12,10 @@
 // weights stay in its registers for all of its rows. In a graph, bf16 with the
 // residual: 8192 x 7168 75.6 us (6.2 TB/s, 93% of a copy's rate), its gradient with
 // dh 83 to 86 (by box; 5.6 TB/s); short calls are a launch and one row's chain of
-// load, sum and store: 1 x 1536 as MXFP8 2.1 us, 4099 x 1536 8.3. (MXFP8 of large
-// calls is bound by instructions: 8192 x 7168 66 us, of 26 for its bytes.)
+// load, sum and store: 1 x 1536 as MXFP8 2.1 us, 4099 x 1536 8.3. A
+// large MXFP8 call is bound by the rows that an SM's registers hold: 8192 x 7168 66
+// us, of 26 for its bytes, with one block of 448 threads and 88 registers an SM (64
+// registers and two blocks 65, packed products and these 64).
 #include <cuda_runtime.h>
 
 #include <cstdint>
