@@ -41,8 +41,9 @@
 // - Latents (576 channels, 512 of them values, 128 query heads): the chain copy (2600
 //   clocks) -> first product (1100) -> softmax (1100) -> second product (1300, and
 //   600 until it starts), with room for two tiles of 80 KB. 48 sequences of up to 4096:
-//   100 us, of which a third is the first queries, the results of parts and
-//   their addition; 256 sequences: 335 us, 0.5 PFLOP/s.
+//   105 us, of which a third is the first queries, the results of parts and
+//   their addition; 256 sequences: 366 us, 0.45 PFLOP/s, four blocks reading the
+//   same tiles from L2 for 32 rows each.
 // - A chunk of 2048 tokens, 128 heads of 192 + 128, over 4096 positions: 1459 us, 589
 //   TFLOP/s. The softmax: 128 x 64 scores are 32 a thread, with four conversions for
 //   each two of them (the 8-bit pairs), at a quarter of the rate of an addition.
@@ -103,7 +104,6 @@ struct AttnParams {
     int64_t q_t, q_h, T, pages;
     int slots;
     int B, width, page_shift, page, block_shift, marks, H, Hq, group, per_seq, Dk, Dv, nk, nv;
-    int pair;                             // blocks that share tiles: 1 or 2
     int k_stages, v_stages, q_bufs, o_bufs, tmem_cols;  // buffers of the keys' tiles, the values', of queries, of O
     uint32_t group_mul, group_shift;      // n / group = n * group_mul >> group_shift for n < 2^31
     int q_vec;
@@ -170,23 +170,6 @@ __device__ __forceinline__ void tma_load_page(uint32_t dst, const void* map, int
         "l"(map), "r"(c), "r"(place), "r"(h), "r"(page), "r"(bar)
         : "memory");
 }
-// The same into both blocks of a pair, and for its barriers: each at its own addresses.
-__device__ __forceinline__ void tma_load_page_pair(uint32_t dst, const void* map, int c, int place, int h, int page,
-                                                   uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
-        "l"(map), "r"(c), "r"(place), "r"(h), "r"(page), "r"(bar), "h"((uint16_t)3)
-        : "memory");
-}
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Columns of a lane, W at a time.
 template <int W>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[W]) {
@@ -406,15 +389,11 @@ struct Shared {  // behind the ring, the queries and the probabilities
 };
 static_assert(sizeof(Shared<32, true>) <= 10240, "latents of five chunks: two tiles, the queries and the rest fill shared memory");
 
-// PAIR: blocks that share tiles. With two (a cluster), a slot has 2R rows, each block has half of them, and a tile is read
-// from L2 once for both: each brings half of the boxes, for both, once both have let go of the place. Latents only: with
-// R = 32 of 128 heads four blocks read the same tiles, at 4.4 TB/s together (256 sequences of 4096: 387 us, so 343). Keys
-// and values of one head are read by few blocks, and their softmax takes longer than their copies.
-template <int R, bool SHARED, int PAIR>
+template <int R, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                       const __grid_constant__ AttnParams p) {
-    constexpr int N2 = 2 * R, kSlotRows = R * PAIR, kStreams = mlaq::kStreams<R>, kFour = kSoftWarps / kStreams;  // kFour: warps of a stream
+    constexpr int N2 = 2 * R, kStreams = mlaq::kStreams<R>, kFour = kSoftWarps / kStreams;  // kFour: warps of a stream
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -439,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid < kMaxStages) {
         mbar_init(k_full + 8 * tid, 2);
-        mbar_init(k_empty + 8 * tid, PAIR);
+        mbar_init(k_empty + 8 * tid, 1);
         mbar_init(v_full + 8 * tid, 2);
         mbar_init(v_empty + 8 * tid, 1);
     } else if (tid < kMaxStages + kMarkTiles) {
@@ -470,10 +449,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!SHARED) tma_prefetch_desc(&v_map);
     }
     fence_mbarrier_init();
-    if constexpr (PAIR > 1) {
-        __syncwarp();
-        cluster_arrive();
-    }
     if (warp == kIssuer) {
         tmem_alloc(smem_u32(&sh.tmem), p.tmem_cols);
         tmem_relinquish();
@@ -494,14 +469,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             int hi = p.B;
             while (hi - my_b > 1) {
                 const int mid = (my_b + hi) / 2;
-                if (first_slot<kSlotRows>(p, mid) <= my_slot) my_b = mid;
+                if (first_slot<R>(p, mid) <= my_slot) my_b = mid;
                 else hi = mid;
             }
         }
         int b = my_b;
 #pragma unroll 1
         for (int i = my_slot; i < my_slot + per_thread && i < p.slots; ++i) {
-            const Slot x = read_slot<kSlotRows>(p, i, b);
+            const Slot x = read_slot<R>(p, i, b);
             b = x.b;
             mine += x.tiles;
         }
@@ -526,17 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     line = __shfl_sync(0xFFFFFFFFu, line, kThreads / 32 - 1);
     // equal shares, the first `all % shares` one tile longer
     const int64_t all = line * p.H;
-    const int64_t most_shares = gridDim.x / PAIR, shares = all < most_shares ? all : most_shares;
-    const int c = blockIdx.x / PAIR, rank = PAIR > 1 ? blockIdx.x % PAIR : 0;
-    // this block's rows of a slot
-    auto own = [&](Piece x) {
-        if constexpr (PAIR > 1) {
-            x.x.rho0 += rank * R;
-            const int left = x.x.rows - rank * R;
-            x.x.rows = left < 0 ? 0 : left < R ? left : R;
-        }
-        return x;
-    };
+    const int64_t most_shares = gridDim.x, shares = all < most_shares ? all : most_shares;
+    const int c = blockIdx.x;
     int tiles = 0, h0 = 0;
     if (c < shares) {
         int64_t each, w0;
@@ -558,12 +524,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             int64_t before = upto - mine;
             int b = my_b;
             for (int i = my_slot;; ++i) {
-                const Slot x = read_slot<kSlotRows>(p, i, b);
+                const Slot x = read_slot<R>(p, i, b);
                 b = x.b;
                 if (at < before + x.tiles) {
                     const int t0 = (int)(at - before), n = x.tiles - t0;
                     sh.start_slot = i;
-                    sh.piece[0] = own(Piece{x, h0, t0, t0 + (n < tiles ? n : tiles)});
+                    sh.piece[0] = Piece{x, h0, t0, t0 + (n < tiles ? n : tiles)};
                     mbar_arrive(piece_full);
                     break;
                 }
@@ -572,7 +538,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    if constexpr (PAIR > 1) cluster_wait();  // the other's barriers are there
     const uint32_t tmem = sh.tmem;
     const uint32_t s_tmem = tmem, o_tmem = tmem + 2 * N2, o_cols = kStreams * p.nv * N2;  // o_cols: of one O buffer
     // Piece i as its readers get it; each warp says that it has read it.
@@ -633,21 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ok = __all_sync(0xFFFFFFFFu, tile_no < stages || wait(empty, ring.phase ^ 1u, abort_flag));
                 if (!ok) break;
-                const int halves = PAIR > 1 ? chunks : (chunks - first + 1) / 2 * 2;  // of a chunk's bytes, by this warp's arrival
-                if (elect_one()) mbar_arrive_expect_tx(full, halves * count * box * 64);
+                if (elect_one()) mbar_arrive_expect_tx(full, (chunks - first + 1) / 2 * count * box * 128);
                 __syncwarp();
                 const uint32_t to = (values ? v_base : base) + ring.i * chunks * kChunk;
-                if constexpr (PAIR > 1) {  // each of the two blocks' two warps has every fourth copy
-                    int turn = 0;
-#pragma unroll 1
-                    for (int j = 0; j < chunks; ++j)
-#pragma unroll 1
-                        for (int e = 0; e < count; ++e, ++turn) {
-                            if ((turn & 3) != 2 * rank + odd) continue;
-                            const int from = __shfl_sync(0xFFFFFFFFu, page, e);
-                            if (elect_one()) tma_load_page_pair(to + j * kChunk + e * box * 128, map, j * 128, k.place, k.h, from, full);
-                        }
-                } else
 #pragma unroll 1
                 for (int j = first; j < chunks; j += 2)
 #pragma unroll 1
@@ -758,8 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         d += N2;
                         at += kChunk;
                     }
-                    if constexpr (PAIR > 1) mma_commit_pair(k_empty + 8 * slot);
-                    else mma_commit((SHARED ? k_empty : v_empty) + 8 * slot);
+                    mma_commit((SHARED ? k_empty : v_empty) + 8 * slot);
                     if (!SHARED) v_ring.step(p.v_stages);
                     mma_commit(p_empty + 8 * ub);
                     if (++v_at == v_len) {
@@ -791,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= kPieces) ok = wait(piece_empty + 8 * (i % kPieces), (uint32_t)(i / kPieces - 1) & 1u, abort_flag);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (ok && lane == 0) {
-                sh.piece[i % kPieces] = own(x);
+                sh.piece[i % kPieces] = x;
                 mbar_arrive(piece_full + 8 * (i % kPieces));
             }
             ++i;
@@ -819,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 break;
                             }
                         }
-                        x.x = read_slot<kSlotRows>(p, slot, x.x.b);
+                        x.x = read_slot<R>(p, slot, x.x.b);
                     } while (x.x.tiles == 0);
                     if (!ok) break;
                 }
@@ -1321,11 +1273,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, p.tmem_cols);
     }
-    if constexpr (PAIR > 1) {  // neither leaves while the other may still write to it
-        __syncwarp();
-        cluster_arrive();
-        cluster_wait();
-    }
 }
 
 // Adds the parts of the pair that share blockIdx.x / (R / 8) opens, eight query
@@ -1346,14 +1293,14 @@ __global__ void __launch_bounds__(kCombineThreads) cache_attn_combine_kernel(con
     const int rows = m.z - r0 < kCombineRows ? m.z - r0 : kCombineRows;
     if (m.x != kOpens || rows <= 0) return;
     // the shares behind go on with the pair until one ends it
-    const int behind = (shares - 1 - c) / p.pair;
+    const int behind = shares - 1 - c;
     if (tid == 0) ends = behind;
     __syncthreads();
     for (int i = 1 + tid; i <= behind; i += kCombineThreads)
-        if (p.meta[2 * (c + i * p.pair)].x == kEnds) atomicMin(&ends, i);
+        if (p.meta[2 * (c + i)].x == kEnds) atomicMin(&ends, i);
     __syncthreads();
     const int n = ends + 1;  // parts
-    auto place = [&](int i) { return (int64_t)(2 * (c + i * p.pair) + (i == 0)) * R + r0; };
+    auto place = [&](int i) { return (int64_t)(2 * (c + i) + (i == 0)) * R + r0; };
     for (int e = tid; e < n * kCombineRows; e += kCombineThreads) {
         const int i = e / kCombineRows, r = e % kCombineRows;
         const float2 ml = r < rows ? p.part_ml[place(i) + r] : make_float2(kNothing, 0.f);
@@ -1426,7 +1373,7 @@ __global__ void __launch_bounds__(kCombineThreads) cache_attn_combine_kernel(con
 
 // -------------------------------------------------------------------- host
 struct AttnPlan {
-    int R, pair, nk, nv, k_stages, v_stages, q_bufs, o_bufs, tmem_cols;
+    int R, nk, nv, k_stages, v_stages, q_bufs, o_bufs, tmem_cols;
     size_t smem;
 };
 
@@ -1447,7 +1394,6 @@ bool attn_plan(const mla_attn_shape& s, const mla_kv_cache& c, int max_smem, Att
     a.nv = (c.Dv + 127) / 128;
     const int64_t group = s.Hq / c.H, rows = group * (s.B > 0 ? (s.T + s.B - 1) / s.B : 1);
     a.R = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || a.nv > 2 ? 32 : 64;
-    a.pair = shared && rows > a.R ? 2 : 1;
     const size_t tail = a.R == 8    ? shared_bytes<8>(shared)
                         : a.R == 16 ? shared_bytes<16>(shared)
                         : a.R == 32 ? shared_bytes<32>(shared)
@@ -1493,12 +1439,12 @@ size_t workspace_bytes(int R, int Dv, int shares) {
     return (size_t)shares * 2 * (R * ((size_t)Dv * 4 + 8) + 16);
 }
 
-template <int R, bool SHARED, int PAIR>
+template <int R, bool SHARED>
 int launch_attn(const AttnParams& p, const AttnPlan& a, const CUtensorMap& k, const CUtensorMap& v, int shares,
                 cudaStream_t s) {
-    if (cudaFuncSetAttribute(cache_attn_kernel<R, SHARED, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)a.smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(cache_attn_kernel<R, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)a.smem) != cudaSuccess)
         return MLA_ERR_CUDA;
-    const int st = launch_overlapped(cache_attn_kernel<R, SHARED, PAIR>, (unsigned)shares, kThreads, a.smem, PAIR > 1 ? PAIR : 0, s, k, v, p);
+    const int st = launch_overlapped(cache_attn_kernel<R, SHARED>, (unsigned)shares, kThreads, a.smem, 0, s, k, v, p);
     if (st != MLA_OK) return st;
     return launch_overlapped(cache_attn_combine_kernel<R>, (unsigned)(shares * (R / kCombineRows)), kCombineThreads, 0, 0, s, p, shares);
 }
@@ -1550,7 +1496,7 @@ MLAQ_API int mla_cache_attn(const mla_attn_shape* shape, const mla_kv_cache* cac
     if (ds != MLA_OK) return ds;
     AttnPlan a;
     if (!attn_plan(s, c, di.max_smem_optin, &a)) return MLA_ERR_UNSUPPORTED;
-    const int shares = (di.num_sms < kMaxShares ? di.num_sms : kMaxShares) / a.pair * a.pair;
+    const int shares = di.num_sms < kMaxShares ? di.num_sms : kMaxShares;
     if (!workspace || ws_bytes < workspace_bytes(a.R, c.Dv, di.num_sms)) return MLA_ERR_WORKSPACE;
 
     AttnParams p{};
@@ -1562,10 +1508,8 @@ MLAQ_API int mla_cache_attn(const mla_attn_shape* shape, const mla_kv_cache* cac
     p.q_t = s.q_t, p.q_h = s.q_h, p.T = s.T, p.pages = c.pages;
     p.B = (int)s.B, p.width = (int)s.table_width, p.page = c.page, p.page_shift = __builtin_ctz(c.page);
     p.block_shift = __builtin_ctz(c.block), p.marks = c.page / c.block, p.H = c.H, p.Hq = s.Hq, p.group = s.Hq / c.H;
-    const int slot_rows = a.R * a.pair;
-    p.pair = a.pair;
-    p.per_seq = (p.group + slot_rows - 1) / slot_rows;
-    const int64_t slots = cu ? s.T * p.group / slot_rows + s.B : s.B * p.per_seq;
+    p.per_seq = (p.group + a.R - 1) / a.R;
+    const int64_t slots = cu ? s.T * p.group / a.R + s.B : s.B * p.per_seq;
     if (slots > kI32Max) return MLA_ERR_UNSUPPORTED;
     p.slots = (int)slots;
     p.Dk = c.Dk, p.Dv = c.Dv, p.nk = a.nk, p.nv = a.nv, p.k_stages = a.k_stages, p.v_stages = a.v_stages, p.tmem_cols = a.tmem_cols;
@@ -1586,16 +1530,14 @@ MLAQ_API int mla_cache_attn(const mla_attn_shape* shape, const mla_kv_cache* cac
     if (ms != MLA_OK) return ms;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (shared)
-        return a.R == 8    ? launch_attn<8, true, 1>(p, a, km, vm, shares, cs)
-               : a.R == 16 ? launch_attn<16, true, 1>(p, a, km, vm, shares, cs)
-               : a.R == 32 ? (a.pair == 2 ? launch_attn<32, true, 2>(p, a, km, vm, shares, cs)
-                                          : launch_attn<32, true, 1>(p, a, km, vm, shares, cs))
-                           : (a.pair == 2 ? launch_attn<64, true, 2>(p, a, km, vm, shares, cs)
-                                          : launch_attn<64, true, 1>(p, a, km, vm, shares, cs));
-    return a.R == 8    ? launch_attn<8, false, 1>(p, a, km, vm, shares, cs)
-           : a.R == 16 ? launch_attn<16, false, 1>(p, a, km, vm, shares, cs)
-           : a.R == 32 ? launch_attn<32, false, 1>(p, a, km, vm, shares, cs)
-                       : launch_attn<64, false, 1>(p, a, km, vm, shares, cs);
+        return a.R == 8    ? launch_attn<8, true>(p, a, km, vm, shares, cs)
+               : a.R == 16 ? launch_attn<16, true>(p, a, km, vm, shares, cs)
+               : a.R == 32 ? launch_attn<32, true>(p, a, km, vm, shares, cs)
+                           : launch_attn<64, true>(p, a, km, vm, shares, cs);
+    return a.R == 8    ? launch_attn<8, false>(p, a, km, vm, shares, cs)
+           : a.R == 16 ? launch_attn<16, false>(p, a, km, vm, shares, cs)
+           : a.R == 32 ? launch_attn<32, false>(p, a, km, vm, shares, cs)
+                       : launch_attn<64, false>(p, a, km, vm, shares, cs);
 }
 
 }  // extern "C"
