@@ -869,7 +869,10 @@ MLAQ_API int mla_kv_cache_read(const mla_kv_cache *cache, void *k, void *v, int 
  *   out [T, Hq, Dv] bf16, lse [T, Hq] fp32 or NULL, both dense.
  * A row that sees nothing gives zeros and -inf. A NaN reaches the rows that
  * see it only; a query row with NaN or Inf gives NaN. Scores, statistics and
- * sums are fp32; probabilities enter the second product with eight bits.
+ * sums are fp32. A probability times its block's scale of V enters the second
+ * product with eight bits while it is 2^-10 of the row's largest such product or
+ * more, and in steps of 2^-18 of that below (a row whose probability lies on
+ * blocks 2^90 times smaller than those of other rows of its head may lose them).
  * Sizes: Dk and Dv up to 256, or, with the values in the keys, Dk up to 640
  * and Dv up to 512; T * Hq up to INT32_MAX; else MLA_ERR_UNSUPPORTED. The
  * workspace (mla_cache_attn_workspace_size bytes, 16-byte aligned, 0 for an

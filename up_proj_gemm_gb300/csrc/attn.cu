@@ -19,12 +19,21 @@
 // token: its scales are two registers. V^T is read from the same [token][channel]
 // tiles as an MN-major operand; with values in the keys (latents) the keys' tile
 // serves both. The scale of K multiplies the score in the thread that owns the
-// token, that of V the probability (p 2^(e - E), E the largest exponent seen).
+// token, that of V the probability: a weight is p 2^(e - E), E an exponent of the
+// warps that share the token's rows.
 //
-// The running maximum is a reference that a row's scores may pass by 2^4: one
-// vote per tile, and only a tile that passes it pays for reductions and for
-// rescaling O in tensor memory. (The factor 2^4 and E4M3's range leave the
-// weights 14 binades of full precision below the reference.)
+// The reference of a row is its largest s + max(e - E, -90), s the score in powers
+// of two: the largest weight, not the largest probability, since weights are what
+// the two E4M3 numbers hold. (With the largest s, and E the largest e, a row whose
+// probability lies on small values lost them: a block 2^20 larger that it gives no
+// weight, or does not even see, took all of its result.) The floor of -90 keeps the
+// sum of the probabilities, at most 2^94 each, within float32. Weights may pass the
+// reference by 2^4: one vote per tile, and only a tile that passes it pays for
+// reductions and for rescaling O in tensor memory; E then becomes the largest e of
+// the tokens that passed, and references fall by as much. The factor 2^4 and E4M3's
+// range leave the weights ten binades of eight bits below the reference; further
+// down they are held in steps of 2^-18 of it. A row keeps its eight bits while a
+// block to which another row of its tile gives weight is up to 2^90 larger.
 //
 // Work is tiles of 128 tokens of all (head, query tile) pairs in one line, cut into
 // equal shares, one per SM: lengths live on the device, and a ragged batch or one
@@ -84,6 +93,9 @@ constexpr int kStreams = R <= 16 ? 2 : 1;
 constexpr float kPass = 4.f;           // log2 of how far scores may pass the reference
 constexpr float kNothing = -3.0e38f;   // the reference of a row that has seen nothing
 constexpr int kNoScale = -1000;
+constexpr int kFar = -90;              // what a scale counts for that is further below the largest
+constexpr float kMostSum = 100.f;      // log2 of what a thread's sums may become where references fall
+constexpr int kFailed = 1 << 20;       // among the votes: a wait that gave up
 constexpr int kMaxQueryChunks = 5;
 constexpr int kCombineThreads = 512, kMaxShares = 256;
 
@@ -194,6 +206,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+// ln(2^m sum). A sum may be 2^94 with a reference as far below: its exponent goes to m first.
+__device__ __forceinline__ float log_sum(float m, float sum) {
+    const uint32_t u = __float_as_uint(sum);
+    const bool normal = u >= 0x00800000u && u < 0x7F800000u;
+    if (normal) m += (float)((int)(u >> 23) - 127);
+    return (m + log2f(normal ? __uint_as_float((u & 0x7FFFFFu) | 0x3F800000u) : sum)) * 0.693147180559945309f;
 }
 // The largest of the warp's values (NaN counts for nothing).
 __device__ __forceinline__ float warp_max(float v) {
@@ -374,13 +393,13 @@ struct Shared {  // behind the ring, the queries and the probabilities
     int limit[2][R];                             // the last position that it sees
     alignas(16) float ref[2][kStreams<R>][R];    // minus the reference of the row's scores
     float sums[2][kStreams<R>][4][R];            // of probabilities, by the four warps
-    int top_e[2][2];                             // largest exponent of V seen, by the four warps
+    int top_e[2][2];                             // the exponent E, by the four warps
     int nan_at[2][512];                          // by channel: the first position with a NaN that not every row sees
     int nan_seen[2];
     alignas(16) float out_factor[kStreams<R>][R];
     float factor[kStreams<R>][R];
     float warp_row[kStreams<R>][4][R];
-    int warp_e[2][4];
+    float warp_l[2][4];
     int vote[2][3];
     uint32_t tmem;
     volatile int abort;
@@ -945,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < kStreams; ++k) sh.out_factor[k][htid] = f[k] * over;
                 if (!whole) p.part_ml[(int64_t)part * R + htid] = make_float2(m, sum);
                 else if (p.lse && htid < now.x.rows)
-                    p.lse[sh.row_at[par][htid]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945309f;
+                    p.lse[sh.row_at[par][htid]] = sum == 0.f ? -INFINITY : log_sum(m, sum);
             }
             failed |= !wait_by<(R == 64)>(o_full + 8 * ob, (uint32_t)use & 1u, abort_flag);
             if (!named_bar_and(3, kHelpers, !failed)) break;
@@ -1071,6 +1090,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int ve = SHARED ? (int)ke : sh.marks[slot][SHARED ? 0 : 1][mark];
                 // a value's scale of NaN makes the scores NaN of those who see it
                 const float ks = e8m0_to_f32(ve == 255 ? 255u : ke) * p.scale_log2;
+                const int e = valid && ve != 255 ? ve : 0;
+                // what the token's scores may be, less their references, before a vote: kPass less the difference of the
+                // exponents (1.5 2^23 + 4 in the last bits of a float)
+                const float most = valid ? __int_as_float(0x4B400000 + (int)kPass - max(e - top_e, kFar)) - 12582912.f : INFINITY;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(m_empty + 8 * slot);
                 failed |= !wait(s_full + 8 * buf, (uint32_t)(t >> 1) & 1u, abort_flag);
@@ -1117,41 +1140,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                     over2 = max3(over2, x[r + 2], x[r + 3]);
                 }
                 over = max3(max3(over, over2, kNothing), x[RT - 2], x[RT - 1]);
-                const bool grow = valid && (over > kPass || (ve > top_e && ve != 255));
-                const int bits = (__any_sync(0xFFFFFFFFu, grow) ? 1 : 0) | (__any_sync(0xFFFFFFFFu, failed) ? 2 : 0);
-                if (lane == 0 && bits) atomicOr(&sh.vote[four][turn], bits);
+                if (__any_sync(0xFFFFFFFFu, over > most || failed)) {  // a vote: one more than the largest scale among those who pass
+                    const int word = 1 + __reduce_max_sync(0xFFFFFFFFu, failed ? kFailed : over > most ? e : 0);
+                    if (lane == 0) atomicMax(&sh.vote[four][turn], word);
+                }
                 named_bar_sync(my_bar, 128);
                 const int vote = *(volatile int*)&sh.vote[four][turn];
                 turn = turn == 2 ? 0 : turn + 1;
                 // the place two turns on was read by all before this barrier and is written by none before the next
                 if (tok == 0) sh.vote[four][turn == 2 ? 0 : turn + 1] = 0;
-                if (vote & 2) {
+                if (vote > kFailed) {
                     leave = true;
                     break;
                 }
                 if (vote) {
-                    // a new reference for every row, the largest score so far, and the largest scale of V
+                    // a larger exponent for all, and a new reference for every row: its largest weight so far
+                    const int old_e = top_e;
+                    top_e = max(top_e, vote - 1);
+                    const float low = valid ? (float)max(e - top_e, kFar) : -INFINITY;
+                    const bool raised = any && top_e > old_e;
+                    if (raised) {  // how far the references may fall with the larger scale: the sums so far grow as much
+                        float sum = l[0];
+#pragma unroll
+                        for (int r = 1; r < RT; ++r) sum = fmaxf(sum, l[r]);
+                        sum = warp_max(sum);
+                        if (lane == 0) sh.warp_l[four][quad] = __log2f(sum);
+                    }
                     scores(std::false_type{});
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
-                        const float m = warp_max(valid ? x[r] : -INFINITY);
+                        const float m = warp_max(x[r] + low);
                         if (lane == (r & 31)) sh.warp_row[stream][quad][r_lo + r] = m;
                     }
-                    const int e = __reduce_max_sync(0xFFFFFFFFu, valid && ve != 255 ? ve : kNoScale);
-                    if (lane == 0) sh.warp_e[four][quad] = e;
                     named_bar_sync(my_bar, 128);
                     const int r = r_lo + tok;
                     if (tok < RT) {
                         const float old = -sh.ref[par][stream][r];
                         float m = old;
+                        if (raised) {
+                            const float *w = sh.warp_l[four], sum = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+                            m -= fmaxf(fminf((float)(top_e - old_e), kMostSum - sum), 0.f);
+                        }
 #pragma unroll
                         for (int k = 0; k < 4; ++k) m = fmaxf(m, sh.warp_row[stream][k][r]);
                         sh.ref[par][stream][r] = -m;
-                        sh.factor[stream][r] = exp2_fast(old - m);
+                        sh.factor[stream][r] = exp2_fast(old - m);  // above 1, by 2^90 at most, where a larger scale lowers the reference
                     }
-                    const int old_e = top_e;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) top_e = max(top_e, sh.warp_e[four][k]);
                     named_bar_sync(my_bar, 128);
 #pragma unroll
                     for (int k = 0; k < RT; ++k) {
@@ -1175,7 +1209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_ld_wait();
 #pragma unroll
                                 for (int k = 0; k < 16; ++k)
-                                    v[k] = __float_as_uint(__uint_as_float(v[k]) * sh.factor[stream][R == 8 ? k % 8 : row + k] * down);
+                                    v[k] = __float_as_uint(__uint_as_float(v[k]) * (sh.factor[stream][R == 8 ? k % 8 : row + k] * down));
                                 tmem_st16(at, v);
                             }
                         tmem_st_wait();
@@ -1188,8 +1222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The probabilities, times the value's scale, as two E4M3 numbers; nothing behind the last position. (Their
                 // buffer is free: the scores came behind the product that read it, tile t - 2's.)
                 const uint32_t to = p_base + buf * (N2 * 128) + tok * 16;
-                const int fe = ve - top_e + 4 + 127;
-                const float f = fe <= 0 || ve == 255 ? 0.f : __uint_as_float((uint32_t)fe << 23);
+                const float f = __int_as_float(min(max(e - top_e + 4 + 127, 0), 254) << 23);
 #pragma unroll
                 for (int r0 = 0; r0 < RT; r0 += 16) {
                     constexpr int kRows = RT < 16 ? RT : 16;
@@ -1325,7 +1358,7 @@ __global__ void __launch_bounds__(kCombineThreads) cache_attn_combine_kernel(con
             const int64_t row = (int64_t)(m.w / p.H + tok) * p.Hq + (int64_t)(m.w % p.H) * p.group + rho - tok * p.group;
             row_at[r] = row;
             inv[r] = l == 0.f ? 0.f : 1.f / l;
-            if (p.lse && r < rows) p.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.693147180559945309f;
+            if (p.lse && r < rows) p.lse[row] = l == 0.f ? -INFINITY : log_sum(top, l);
         }
     }
     __syncthreads();
