@@ -1426,24 +1426,29 @@ bool attn_plan(const mla_attn_shape& s, const mla_kv_cache& c, int max_smem, Att
     a.nk = (c.Dk + 127) / 128;
     a.nv = (c.Dv + 127) / 128;
     const int64_t group = s.Hq / c.H, rows = group * (s.B > 0 ? (s.T + s.B - 1) / s.B : 1);
-    a.R = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || a.nv > 2 ? 32 : 64;
-    const size_t tail = a.R == 8    ? shared_bytes<8>(shared)
-                        : a.R == 16 ? shared_bytes<16>(shared)
-                        : a.R == 32 ? shared_bytes<32>(shared)
-                                    : shared_bytes<64>(shared);
-    const size_t q = (size_t)a.nk * 2 * a.R * 128, fixed = 1024 + 2 * 2 * a.R * 128 + tail;
-    const int tile = shared ? a.nk : a.nk + a.nv;
-    // two buffers of queries where two tiles are left, else one beside a tile (latents: two)
-    for (a.q_bufs = 2; a.q_bufs > 0; --a.q_bufs) {
-        const int room = (int)(((int64_t)max_smem - (int64_t)(fixed + a.q_bufs * q)) / kChunk), stages = room / tile;
-        if (stages < (shared || a.q_bufs == 2 ? 2 : 1)) continue;
-        a.v_stages = shared ? 0 : stages > kMaxStages ? kMaxStages : stages;
-        a.k_stages = (room - a.v_stages * a.nv) / a.nk;
-        if (a.k_stages > kMaxStages) a.k_stages = kMaxStages;
+    // half as many rows where two tiles find no room beside them (latents of more than 384 channels, up to 256 of them values)
+    for (a.R = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || a.nv > 2 ? 32 : 64; a.R >= 8; a.R /= 2) {
+        const size_t tail = a.R == 8    ? shared_bytes<8>(shared)
+                            : a.R == 16 ? shared_bytes<16>(shared)
+                            : a.R == 32 ? shared_bytes<32>(shared)
+                                        : shared_bytes<64>(shared);
+        const size_t q = (size_t)a.nk * 2 * a.R * 128, fixed = 1024 + 2 * 2 * a.R * 128 + tail;
+        const int tile = shared ? a.nk : a.nk + a.nv;
+        // two buffers of queries where two tiles are left, else one beside a tile (latents: two)
+        for (a.q_bufs = 2; a.q_bufs > 0; --a.q_bufs) {
+            const int64_t left = (int64_t)max_smem - (int64_t)(fixed + a.q_bufs * q);
+            const int room = (int)(left / kChunk), stages = room / tile;
+            if (stages < (shared || a.q_bufs == 2 ? 2 : 1)) continue;
+            a.v_stages = shared ? 0 : stages > kMaxStages ? kMaxStages : stages;
+            a.k_stages = (room - a.v_stages * a.nv) / a.nk;
+            if (a.k_stages > kMaxStages) a.k_stages = kMaxStages;
+            break;
+        }
+        if (a.q_bufs == 0) continue;
+        a.smem = fixed + a.q_bufs * q + ((size_t)a.k_stages * a.nk + (size_t)a.v_stages * a.nv) * kChunk;
         break;
     }
-    if (a.q_bufs == 0) return false;
-    a.smem = fixed + a.q_bufs * q + ((size_t)a.k_stages * a.nk + (size_t)a.v_stages * a.nv) * kChunk;
+    if (a.R < 8) return false;
     const int s_cols = 2 * 2 * a.R, o_cols = a.nv * (a.R <= 16 ? 2 : 1) * 2 * a.R;
     a.o_bufs = s_cols + 2 * o_cols <= 512 ? 2 : 1;
     const int cols = s_cols + a.o_bufs * o_cols;
