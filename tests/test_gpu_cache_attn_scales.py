@@ -186,3 +186,14 @@ def test_parts_of_one_sequence(cuda_device, gap):
     block_of(s, 0, 20_000, -40.0, gap)
     block_of(s, 0, 30_000, 12.0, -gap // 2)
     attend(cuda_device, s, 2)
+
+
+@pytest.mark.parametrize("block", [1, 2, 4, 8, 16, 32, 64, 128, 256])
+def test_scale_bytes_by_the_tile(cuda_device, block):
+    """Every block has scales of its own, for keys and values, over more tiles than shared memory holds bytes for: a tile that
+    got another's, or an older one's, is off by a power of two."""
+    s = scene(cuda_device, H=2, Dk=64, Dv=64, page=256, block=block, start=[5000, 200, 2500], n=[1, 2, 1])
+    g = torch.Generator().manual_seed(block)
+    s.host[1].copy_(torch.randint(112, 121, s.host[1].shape, generator=g, dtype=u8))
+    s.host[3].copy_(torch.randint(123, 132, s.host[3].shape, generator=g, dtype=u8))
+    attend(cuda_device, s, 8)

@@ -590,6 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t + 1 < tiles) {  // the next tile's entry is on its way while this one waits for room
                 if (++tile == x.t1) {
                     ok = __all_sync(0xFFFFFFFFu, get_piece(i, x));
+                    __syncwarp();  // all have read it: a vote orders no memory
                     if (lane == 0) mbar_arrive(piece_empty + 8 * (i % kPieces));
                     ++i;
                     tile = x.t0;
@@ -822,6 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             ok = __all_sync(0xFFFFFFFFu, ok);
+            __syncwarp();  // the lanes' bytes lie there: a vote orders no memory
             if (lane < n) mbar_arrive(m_full + 8 * ((t + lane) % kMarkTiles));
             t += n;
             tile += n;
