@@ -42,7 +42,7 @@ struct NormParams {
     float* partials;                 // backward: [blocks][K]
     int64_t T, ld_x, ld_res, ld_dy;
     int K;
-    int x_bf16, w_bf16, tiled, vec;
+    int x_bf16, w_bf16, tiled;
     float eps, inv_k;
 };
 
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kMaxThreads<WARP, GPT>) rms_norm_bwd_kernel(co
 // x 7168 with dh: 138 us, so 85 us). A thread copies the granules that it reads
 // itself, so it waits for its own copies and for no barrier. (By bulk copies and
 // barriers: 85 us as well, without dh 80 for 75, in float32 5% less.)
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 8, kRingGranules = 2;  // granules of a thread: norm_grid's for a block to a row of more rows than SMs
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
@@ -376,8 +376,9 @@ __device__ __forceinline__ void copies_wait(int n) {
         default: asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
 }
-template <typename E, int GPT>
+template <typename E>
 __global__ void __launch_bounds__(512) rms_norm_bwd_ring_kernel(const __grid_constant__ NormParams p, int stages, int pitch) {
+    constexpr int GPT = kRingGranules;
     extern __shared__ __align__(128) uint8_t ring[];  // [stage][dy | h | dh], rows of `pitch` bytes
     __shared__ float buf[64];
     const int tid = threadIdx.x, parts = p.res ? 3 : 2;
@@ -544,7 +545,7 @@ struct NormRing {
 NormRing norm_ring(const NormParams& p, const NormGrid& g, int64_t size, const DeviceInfo& di) {
     NormRing r{};
     const int64_t row = p.K * size, parts = p.res ? 3 : 2;
-    if (g.warp || g.gpt > 2 || g.threads > 512 || p.T < 4 * (int64_t)di.num_sms) return r;
+    if (g.warp || g.gpt != kRingGranules || g.threads > 512 || p.T < 4 * (int64_t)di.num_sms) return r;
     const int per = 4 * row >= 48 * 1024 ? 1 : 4 * row >= 24 * 1024 ? 2 : 4;  // with dh or without: dw's sum is the same
     r.pitch = (int)((row + 127) / 128 * 128);
     const int64_t room = ((int64_t)di.max_smem_optin / per - 2048) / (parts * r.pitch);
@@ -558,7 +559,7 @@ NormRing norm_ring(const NormParams& p, const NormGrid& g, int64_t size, const D
 
 template <typename E>
 int launch_bwd_ring(const NormParams& p, const NormGrid& g, const NormRing& r, cudaStream_t s) {
-    const auto kernel = g.gpt == 1 ? rms_norm_bwd_ring_kernel<E, 1> : rms_norm_bwd_ring_kernel<E, 2>;
+    const auto kernel = rms_norm_bwd_ring_kernel<E>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)r.smem) != cudaSuccess) return MLA_ERR_CUDA;
     return launch_overlapped(kernel, r.blocks, g.threads, r.smem, 0, s, p, r.stages, r.pitch);
 }
