@@ -1554,10 +1554,8 @@ MLAQ_API int mla_cache_attn(const mla_attn_shape* shape, const mla_kv_cache* cac
     p.slots = (int)slots;
     p.Dk = c.Dk, p.Dv = c.Dv, p.nk = a.nk, p.nv = a.nv, p.k_stages = a.k_stages, p.v_stages = a.v_stages, p.tmem_cols = a.tmem_cols;
     p.q_bufs = a.q_bufs, p.o_bufs = a.o_bufs;
-    int bits = 0;
-    while ((1 << bits) < p.group) ++bits;
-    p.group_shift = 31 + bits;
-    p.group_mul = (uint32_t)((((uint64_t)1 << p.group_shift) + p.group - 1) / p.group);
+    const Divisor by = divisor(p.group);
+    p.group_mul = by.mul, p.group_shift = by.shift;
     p.q_vec = aligned(q, 16) && s.q_t % 8 == 0 && s.q_h % 8 == 0;
     p.scale_log2 = s.scale * 1.44269504088896341f;
     p.status = dev_status;

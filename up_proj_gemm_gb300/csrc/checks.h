@@ -44,4 +44,16 @@ inline bool inside(int64_t n, int64_t stride) {
 
 constexpr int64_t kI32Max = 0x7fffffffLL;
 
+// n / d = n * mul >> shift for 0 <= n < 2^31, d > 0: shift = 31 + the bits of d - 1, so mul is below 2^32 and the product
+// below 2^63, and mul d - 2^shift < d, times n, stays below 2^shift.
+struct Divisor {
+    uint32_t mul, shift;
+};
+inline Divisor divisor(int32_t d) {
+    uint32_t bits = 0;
+    while (((int64_t)1 << bits) < d) ++bits;
+    const uint32_t shift = 31 + bits;
+    return {(uint32_t)((((uint64_t)1 << shift) + (uint64_t)d - 1) / (uint64_t)d), shift};
+}
+
 }  // namespace mlaq
