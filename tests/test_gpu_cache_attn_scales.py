@@ -197,3 +197,13 @@ def test_scale_bytes_by_the_tile(cuda_device, block):
     s.host[1].copy_(torch.randint(112, 121, s.host[1].shape, generator=g, dtype=u8))
     s.host[3].copy_(torch.randint(123, 132, s.host[3].shape, generator=g, dtype=u8))
     attend(cuda_device, s, 8)
+
+
+@pytest.mark.parametrize("Hq", [2, 64])
+def test_the_largest_values(cuda_device, Hq):
+    """Values of 2^126 to 2^127, all of one sign, in parts: their sums are beyond float32, their mean is not."""
+    s = scene(cuda_device, H=1, Dk=64, Dv=64, page=128, block=128, start=[40_000], n=[1])
+    s.host[2] &= 0x7F
+    s.host[3].fill_(254)
+    out, _ = attend(cuda_device, s, Hq)
+    assert out.isfinite().all()

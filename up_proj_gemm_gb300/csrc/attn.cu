@@ -961,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int e = sh.top_e[par][kStreams == 2 ? k : htid / (R / 2)];
                     f[k] = ldexpf(up, e < 0 ? -131 : e - 131);
                 }
-                const float over = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                const float over = sum == 0.f ? 0.f : 1.f / sum;  // of a part too: sums of large values may overflow
 #pragma unroll
                 for (int k = 0; k < kStreams; ++k) sh.out_factor[k][htid] = f[k] * over;
                 if (!whole) p.part_ml[(int64_t)part * R + htid] = make_float2(m, sum);
@@ -1318,7 +1318,6 @@ template <int R>
 __global__ void __launch_bounds__(kCombineThreads) cache_attn_combine_kernel(const __grid_constant__ AttnParams p, int shares) {
     __shared__ float weight[kMaxShares][kCombineRows], sums[kMaxShares][kCombineRows];
     __shared__ float4 halves[kCombineThreads];
-    __shared__ float inv[kCombineRows];
     __shared__ int64_t row_at[kCombineRows];
     __shared__ int ends;
     grid_launch_next();
@@ -1349,17 +1348,18 @@ __global__ void __launch_bounds__(kCombineThreads) cache_attn_combine_kernel(con
         for (int i = lane; i < n; i += 32) top = fmaxf(top, weight[i][r]);
         top = warp_max(top);
         for (int i = lane; i < n; i += 32) {
-            const float w = exp2_fast(weight[i][r] - top);
+            const float w = exp2_fast(weight[i][r] - top) * sums[i][r];
             weight[i][r] = w;
-            l = fmaf(w, sums[i][r], l);
+            l += w;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        for (int i = lane; i < n; i += 32) weight[i][r] *= inv;
         if (lane == 0) {
             const int rho = m.y + r0 + r, tok = token_of(p, rho);
             const int64_t row = (int64_t)(m.w / p.H + tok) * p.Hq + (int64_t)(m.w % p.H) * p.group + rho - tok * p.group;
             row_at[r] = row;
-            inv[r] = l == 0.f ? 0.f : 1.f / l;
             if (p.lse && r < rows) p.lse[row] = l == 0.f ? -INFINITY : log_sum(top, l);
         }
     }
@@ -1396,8 +1396,7 @@ __global__ void __launch_bounds__(kCombineThreads) cache_attn_combine_kernel(con
         }
         if (group == 0 && e < all) {
             uint16_t* out = p.out + row_at[row] * p.Dv + ch;
-            const float f = inv[row];
-            const uint32_t a = pack_bf16x2(o.x * f, o.y * f), b = pack_bf16x2(o.z * f, o.w * f);
+            const uint32_t a = pack_bf16x2(o.x, o.y), b = pack_bf16x2(o.z, o.w);
             out[0] = (uint16_t)a;
             out[1] = (uint16_t)(a >> 16);
             out[2] = (uint16_t)b;
