@@ -207,8 +207,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// ln(2^m sum). A sum may be 2^94 with a reference as far below: its exponent goes to m first.
-__device__ __forceinline__ float log_sum(float m, float sum) {
+// ln(2^m sum). A sum may be 2^94 with a reference as far below: its exponent goes to m first. (Out of line, for the loop's
+// instructions to stay in their cache: a chunk 1498 us with this and the division below inline, so 1467.)
+__device__ __noinline__ float log_sum(float m, float sum) {
     const uint32_t u = __float_as_uint(sum);
     const bool normal = u >= 0x00800000u && u < 0x7F800000u;
     if (normal) m += (float)((int)(u >> 23) - 127);
@@ -961,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int e = sh.top_e[par][kStreams == 2 ? k : htid / (R / 2)];
                     f[k] = ldexpf(up, e < 0 ? -131 : e - 131);
                 }
-                const float over = sum == 0.f ? 0.f : 1.f / sum;  // of a part too: sums of large values may overflow
+                const float over = sum == 0.f ? 0.f : __fdividef(1.f, sum);  // of a part too: sums of large values may overflow; 2 ulp
 #pragma unroll
                 for (int k = 0; k < kStreams; ++k) sh.out_factor[k][htid] = f[k] * over;
                 if (!whole) p.part_ml[(int64_t)part * R + htid] = make_float2(m, sum);
