@@ -815,8 +815,10 @@ MLAQ_API int mla_rms_norm_bwd(const mla_norm_shape *shape, const void *dy, const
  * side: sequence b's are rows cu[b] to cu[b + 1] - 1 (cu int32 [B + 1], from
  * 0, never falling; NULL: one row each, T == B). Rows from cu[B] on are
  * neither read nor written. A page outside the cache, a position outside the
- * table or a cu outside 0..T skips what it concerns (attention reads zeros there)
- * and sets *dev_status to MLA_ERR_POS_RANGE or MLA_ERR_INVALID_ARG.
+ * table or a cu outside 0..T skips what it concerns and sets *dev_status to
+ * MLA_ERR_POS_RANGE or MLA_ERR_INVALID_ARG. (Attention reads zeros in such a
+ * page, takes a length past the table for the table's end, and gives no valid
+ * result at all where a cu falls.)
  */
 typedef struct {
     int64_t pages;

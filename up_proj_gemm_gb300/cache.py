@@ -4,8 +4,10 @@ argument marshalling for ``mla_kv_cache_write``, ``mla_kv_cache_read`` and
 
 ``KvCache`` holds the pages. ``kv_cache_write`` quantizes what ``kv_fwd`` gives
 (or the latents and rotary keys it starts from) as it is appended,
-``kv_cache_read`` gives it back, and ``cache_attn`` takes the query that ``fwd``
-gives over it: single tokens, drafts of a few, or a prompt's chunk.
+``kv_cache_read`` gives it back, and ``cache_attn`` takes a query over it: single
+tokens, drafts of a few, or a prompt's chunk. Over keys and values of the heads
+that is the query that ``fwd`` gives. Over latents the caller multiplies the key
+weights into the query and the value weights into the result.
 """
 from __future__ import annotations
 

@@ -38,14 +38,14 @@
 // Work is tiles of 128 tokens of all (head, query tile) pairs in one line, cut into
 // equal shares, one per SM: lengths live on the device, and a ragged batch or one
 // long sequence fills every SM alike. A share's first and last pair may be
-// parts; their O, maximum and sum go to the workspace and a second kernel adds
-// the parts in the order of the shares.
+// parts; their O (divided by the sum), reference and sum go to the workspace and a
+// second kernel adds the parts in the order of the shares.
 //
 // What bounds it, by calls in a graph:
 // - Tokens over keys and values of their own: HBM. 64 sequences of up to 8192
-//   tokens, 8 heads of 128 + 128 (608 MB): 103.5 us, 5.9 TB/s, 88% of a copy's rate;
-//   in pages of 128 and more 100 us. Pages of 32 and 16 take 113 and 136: a copy's
-//   fixed 50 ns. 512 sequences of 1024: 174 us; a piece of eight tiles is too short
+//   tokens, 8 heads of 128 + 128 (608 MB): 104.5 us, 5.8 TB/s, 87% of a copy's rate;
+//   in pages of 128 and more 100 us. Pages of 32 and 16 take 114 and 136: a copy's
+//   fixed 50 ns. 512 sequences of 1024: 178 us; a piece of eight tiles is too short
 //   to hide bringing its queries in and its result out.
 // - Latents (576 channels, 512 of them values, 128 query heads): the chain copy (2600
 //   clocks) -> first product (1100) -> softmax (1100) -> second product (1300, and
@@ -53,7 +53,7 @@
 //   105 us, of which a third is the first queries, the results of parts and
 //   their addition; 256 sequences: 366 us, 0.45 PFLOP/s, four blocks reading the
 //   same tiles from L2 for 32 rows each.
-// - A chunk of 2048 tokens, 128 heads of 192 + 128, over 4096 positions: 1459 us, 589
+// - A chunk of 2048 tokens, 128 heads of 192 + 128, over 4096 positions: 1465 us, 587
 //   TFLOP/s. The softmax: 128 x 64 scores are 32 a thread, with four conversions for
 //   each two of them (the 8-bit pairs), at a quarter of the rate of an addition.
 #include <cuda.h>
@@ -90,7 +90,7 @@ constexpr int kPieceReaders = kSoftWarps + 3 + 4;  // warps
 // rows, from 7.7 to 2.9 ms, with the weights stored whole per token as the rest of it.)
 template <int R>
 constexpr int kStreams = R <= 16 ? 2 : 1;
-constexpr float kPass = 4.f;           // log2 of how far scores may pass the reference
+constexpr float kPass = 4.f;           // log2 of how far weights may pass the reference
 constexpr float kNothing = -3.0e38f;   // the reference of a row that has seen nothing
 constexpr int kNoScale = -1000;
 constexpr int kFar = -90;              // what a scale counts for that is further below the largest
